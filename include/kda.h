@@ -242,6 +242,126 @@ KDA_API int kda_decode_ex(const void *q, const void *k, const void *v, const voi
                           float lower_bound, int32_t gate_mode, int32_t flags, float norm_eps,
                           kda_stream_t stream);
 
+/*
+ * The operators a hybrid model needs beside KDA layers: linear attention with one decay a
+ * head (kda_linear_prefill, kda_linear_decode), attention of one new token over a paged
+ * key-value cache (kda_attn_decode) and eviction from that cache (kda_cache_evict).
+ */
+
+/*
+ * kda_linear_prefill -- varlen linear attention with a decay for each head. Per head
+ *     S_t = exp(g_t) S_{t-1} + k_t v_t^T,   o_t = scale * S_t^T q_t
+ * with g_t a natural-log decay shared by the head's channels.
+ *   q, k, v      BF16 [total_tokens, num_heads, 128]
+ *   log_decay    FP32; decay_per_token = 0: [num_heads], the same for every token;
+ *                decay_per_token = 1: [total_tokens, num_heads]. Expected <= 0 (-inf clears
+ *                the state); positive values are not checked and make the state grow.
+ *   cu_seqlens, init_state, out, final_state, scale, num_seqs, total_tokens, num_heads
+ *                as for kda_prefill (final_state may equal init_state; bad cu_seqlens are
+ *                clamped and recorded as KDA_ERR_DEVICE_INPUT).
+ *   workspace    NULL: one thread block walks each (sequence, head) chain; otherwise at
+ *                least kda_linear_prefill_workspace_size(..., 0) bytes, 16-byte aligned, or
+ *                KDA_ERR_INVALID_ARG: chains too few to fill the GPU (or its last wave) are
+ *                then cut into windows that run in parallel. Contents on entry do not
+ *                matter; calls sharing one workspace must not overlap on the GPU. Results
+ *                agree up to rounding.
+ * Outputs are rounded once to BF16 from FP32 sums of products whose inner factors (the
+ * decayed scores and the state the queries read) are BF16; the state itself is carried in
+ * FP32 and its update keeps the decayed keys to 16 bits of mantissa.
+ */
+KDA_API int kda_linear_prefill(const void *q, const void *k, const void *v, const float *log_decay,
+                               int32_t decay_per_token, const int32_t *cu_seqlens,
+                               const float *init_state, void *out, float *final_state,
+                               int32_t num_seqs, int32_t total_tokens, int32_t num_heads, float scale,
+                               void *workspace, int64_t workspace_bytes, kda_stream_t stream);
+
+/* kda_linear_prefill_workspace_size -- bytes of workspace kda_linear_prefill uses for this
+ * shape (0: none). sm_count as for kda_prefill_workspace_size. */
+KDA_API int64_t kda_linear_prefill_workspace_size(int32_t num_seqs, int32_t total_tokens,
+                                                  int32_t num_heads, int32_t sm_count);
+
+/*
+ * kda_linear_decode -- one token per row of the same recurrence against a slot-indexed pool.
+ *   q, k, v      BF16 [rows, num_heads, 128]
+ *   log_decay    FP32 [num_heads] (decay_per_row = 0) or [rows, num_heads] (1)
+ *   slot_idx, state_pool, num_slots, state_dtype, out, rows, num_heads, scale
+ *                as for kda_decode (unique slots; a negative slot is a padding row whose
+ *                output is zeros; a slot >= num_slots is also recorded as
+ *                KDA_ERR_DEVICE_INPUT; BF16 states are computed in FP32, the output taken
+ *                from the FP32 values, and stored rounded to nearest even).
+ */
+KDA_API int kda_linear_decode(const void *q, const void *k, const void *v, const float *log_decay,
+                              int32_t decay_per_row, const int32_t *slot_idx, void *state_pool,
+                              int64_t num_slots, int32_t state_dtype, void *out, int32_t rows,
+                              int32_t num_heads, float scale, kda_stream_t stream);
+
+/*
+ * Paged key-value cache. k_cache and v_cache are BF16 [num_pages, num_kv_heads, page_size, 128]
+ * with the pages `k_page_stride` / `v_page_stride` elements apart (a multiple of 8, at least
+ * num_kv_heads * page_size * 128, so both may be views of one [num_pages, 2, ...] tensor);
+ * page_size is a power of two in [8, 1024]. Token j of batch row b lies at offset
+ * j % page_size of page block_table[b][j / page_size] (int32 [batch, max_pages], device).
+ * Offsets are 64-bit. Rows may share pages that are only read. seq_lens (int32 [batch],
+ * device) counts the tokens of each row; a value outside [0, max_pages * page_size] is
+ * clamped and recorded as KDA_ERR_DEVICE_INPUT. A negative page is missing: its tokens are
+ * masked. A page >= num_pages is also recorded as KDA_ERR_DEVICE_INPUT. Cache slots past a
+ * row's length, and tokens of missing pages, are never read (they may hold NaN).
+ */
+
+/*
+ * kda_attn_decode -- attention of one new token per row over its cached tokens:
+ *     x_j = scale * q . k_j,   p = softmax(x),   o = sum_j p_j v_j
+ * (the new token's own key and value are in the cache already, and counted by seq_lens).
+ *   q, out       BF16 [batch, num_q_heads, 128]; query head h reads key head
+ *                h / (num_q_heads / num_kv_heads)
+ *   lse          FP32 [batch, num_q_heads] log(sum_j exp(x_j)), or NULL
+ *   weight       FP32 [batch, num_kv_heads, max_pages * page_size], or NULL. weight[b][h][j]
+ *                grows by p_j summed over the query heads that read key head h, for every
+ *                unmasked token j; other entries are not written.
+ *   workspace    at least kda_attn_decode_workspace_size(...) bytes, 16-byte aligned.
+ *                Contents on entry do not matter; calls sharing one must not overlap.
+ * A row with no unmasked token (or whose every x_j is -inf) gives zeros, and -inf in lse. The
+ * sums run in a fixed order: equal inputs give equal bits.
+ */
+KDA_API int kda_attn_decode(const void *q, const void *k_cache, const void *v_cache,
+                            int64_t k_page_stride, int64_t v_page_stride, int64_t num_pages,
+                            int32_t page_size, const int32_t *block_table, int32_t max_pages,
+                            const int32_t *seq_lens, void *out, float *lse, float *weight,
+                            int32_t batch, int32_t num_q_heads, int32_t num_kv_heads, float scale,
+                            void *workspace, int64_t workspace_bytes, kda_stream_t stream);
+
+/* kda_attn_decode_workspace_size -- bytes of workspace for a call of this shape, with or
+ * without `weight`. sm_count 0 asks the current device; > 0 is pure host arithmetic. */
+KDA_API int64_t kda_attn_decode_workspace_size(int32_t batch, int32_t num_q_heads, int32_t num_kv_heads,
+                                               int32_t max_pages, int32_t page_size,
+                                               int32_t with_weight, int32_t sm_count);
+
+/*
+ * kda_cache_evict -- shortens rows longer than `budget` tokens to `budget`, for each key head
+ * by itself: the first `sink` and the last `recent` tokens stay, and of the others the
+ * budget - sink - recent with the largest weight (equal weights, +0 and -0 among them: the
+ * earlier token; NaN counts as -inf). The kept tokens keep their order and are packed into
+ * positions [0, budget). Rows of at most `budget` tokens keep them all.
+ *   weight       FP32 [batch, num_kv_heads, max_pages * page_size], as kda_attn_decode
+ *                accumulates it
+ *   dst_table    int32 [batch, max_pages] like block_table: the pages the kept tokens are
+ *                packed into, none of which a row of block_table may hold; NULL:
+ *                block_table itself (in place; rows that share pages race).
+ *   dst_weight   the kept tokens' weights, packed alike, in a tensor of weight's shape; may
+ *                equal weight (in place). Entries from the new length to the old one become 0.
+ *   new_lens     int32 [batch]: min(seq_lens, budget). May equal seq_lens.
+ *   kept         int32 [batch, num_kv_heads, budget]: the old positions of the kept tokens,
+ *                ascending, then -1.
+ * A kept token whose source or destination page is missing is not copied, and recorded as
+ * KDA_ERR_DEVICE_INPUT. 0 <= sink, 0 <= recent, sink + recent <= budget, budget >= 1.
+ */
+KDA_API int kda_cache_evict(void *k_cache, void *v_cache, int64_t k_page_stride, int64_t v_page_stride,
+                            int64_t num_pages, int32_t page_size, const int32_t *block_table,
+                            const int32_t *dst_table, int32_t max_pages, const int32_t *seq_lens,
+                            const float *weight, float *dst_weight, int32_t *new_lens, int32_t *kept,
+                            int32_t batch, int32_t num_kv_heads, int32_t budget, int32_t sink,
+                            int32_t recent, kda_stream_t stream);
+
 /* A static, human-readable name for a kda_status value. Never NULL. */
 KDA_API const char *kda_status_string(int status);
 

@@ -12,10 +12,21 @@ Low-level calls mirror the C names and take caller-owned torch tensors:
                gate_mode, stream=None)
     kda_prefill_ex(..., workspace=None, stream=None), kda_prefill_workspace_size(N, T, H, sm_count=0)
     kda_status_string(status), kda_device_status(stream=None)
-Convenience wrappers ``prefill`` / ``decode`` allocate the outputs.
+and, for the other layers of a hybrid model (linear attention with a decay for each head,
+attention over a paged key-value cache):
+    kda_linear_prefill(q, k, v, log_decay, cu_seqlens, init_state, out, final_state, scale,
+                       workspace=None, stream=None)
+    kda_linear_decode(q, k, v, log_decay, slot_idx, state_pool, out, scale, stream=None)
+    kda_attn_decode(q, k_cache, v_cache, block_table, seq_lens, out, scale, workspace, lse=None,
+                    weight=None, stream=None)
+    kda_cache_evict(k_cache, v_cache, block_table, seq_lens, weight, new_lens, kept, budget,
+                    sink=0, recent=0, dst_table=None, dst_weight=None, stream=None)
+Convenience wrappers ``prefill``, ``decode``, ``linear_prefill``, ``linear_decode``,
+``attn_decode`` and ``cache_evict`` allocate the outputs.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
@@ -36,7 +47,9 @@ HEAD_DIM = 128
 CHUNK = 32
 
 EXPORTED_SYMBOLS = ("kda_prefill", "kda_prefill_ex", "kda_prefill_workspace_size", "kda_prefill_noalloc", "kda_decode",
-                    "kda_decode_ex", "kda_status_string", "kda_device_status", "kda_abi_version")
+                    "kda_decode_ex", "kda_linear_prefill", "kda_linear_prefill_workspace_size", "kda_linear_decode",
+                    "kda_attn_decode", "kda_attn_decode_workspace_size", "kda_cache_evict", "kda_status_string",
+                    "kda_device_status", "kda_abi_version")
 KDA_NOALLOC_SCRATCH_BYTES = 32 << 20  # fixed scratch array of kda_prefill_noalloc
 KDA_DECODE_L2NORM_QK = 1
 KDA_DECODE_BETA_LOGITS = 2
@@ -88,6 +101,20 @@ def bind(lib):
     lib.kda_decode_ex.restype = ctypes.c_int
     lib.kda_decode_ex.argtypes = [vp, vp, vp, vp, vp, vp, vp, i64, i32, vp, i32, i32, i32, f32, f32, i32, i32,
                                   f32, vp]
+    lib.kda_linear_prefill.restype = ctypes.c_int
+    lib.kda_linear_prefill.argtypes = [vp, vp, vp, vp, i32, vp, vp, vp, vp, i32, i32, i32, f32, vp, i64, vp]
+    lib.kda_linear_prefill_workspace_size.restype = ctypes.c_int64
+    lib.kda_linear_prefill_workspace_size.argtypes = [i32, i32, i32, i32]
+    lib.kda_linear_decode.restype = ctypes.c_int
+    lib.kda_linear_decode.argtypes = [vp, vp, vp, vp, i32, vp, vp, i64, i32, vp, i32, i32, f32, vp]
+    lib.kda_attn_decode.restype = ctypes.c_int
+    lib.kda_attn_decode.argtypes = [vp, vp, vp, i64, i64, i64, i32, vp, i32, vp, vp, vp, vp, i32, i32, i32, f32, vp,
+                                    i64, vp]
+    lib.kda_attn_decode_workspace_size.restype = ctypes.c_int64
+    lib.kda_attn_decode_workspace_size.argtypes = [i32, i32, i32, i32, i32, i32, i32]
+    lib.kda_cache_evict.restype = ctypes.c_int
+    lib.kda_cache_evict.argtypes = [vp, vp, i64, i64, i64, i32, vp, vp, i32, vp, vp, vp, vp, vp, i32, i32, i32, i32,
+                                    i32, vp]
     lib.kda_status_string.restype = ctypes.c_char_p
     lib.kda_status_string.argtypes = [ctypes.c_int]
     lib.kda_device_status.restype = ctypes.c_int
@@ -328,3 +355,244 @@ def decode(q, k, v, g_raw, beta, slot_idx, state_pool, *, scale, lower_bound=0.0
         kda_decode(q, k, v, g_raw, beta, slot_idx, state_pool, out, scale, lower_bound, gate_mode, stream)
     del torch
     return out
+
+
+def _on(device):
+    """Makes `device` current for the call (nothing to do when it is already)."""
+    import torch
+    if torch.cuda.current_device() == (device.index or 0):
+        return contextlib.nullcontext()
+    return torch.cuda.device(device)
+
+
+def _per_head_or_token(log_decay, rows, H, device):
+    """0 for a decay per head [H], 1 for one per token and head [rows, H]."""
+    import torch
+    if log_decay.dim() == 1:
+        _check(log_decay, "log_decay", torch.float32, (H,), device)
+        return 0
+    _check(log_decay, "log_decay", torch.float32, (rows, H), device)
+    return 1
+
+
+def _workspace_arg(workspace, device):
+    if workspace is None:
+        return None, 0
+    if workspace.device != device or not workspace.is_contiguous():
+        raise ValueError("workspace: must be a contiguous tensor on the inputs' device")
+    return _ptr(workspace), workspace.numel() * workspace.element_size()
+
+
+def kda_linear_prefill(q, k, v, log_decay, cu_seqlens, init_state, out, final_state, scale, workspace=None,
+                       stream=None):
+    """Varlen linear attention with a decay for each head, S_t = exp(g_t) S_{t-1} + k_t v_t^T and
+    o_t = scale S_t^T q_t, into caller-owned ``out`` / ``final_state``. ``log_decay`` is g: FP32
+    [H], or [T, H] for one per token. ``workspace``: see linear_prefill_workspace (or None)."""
+    import torch
+    T, H, d = q.shape
+    N = cu_seqlens.shape[0] - 1
+    dev = q.device
+    for name, t in (("q", q), ("k", k), ("v", v), ("out", out)):
+        _check(t, name, torch.bfloat16, (T, H, HEAD_DIM), dev)
+    per_token = _per_head_or_token(log_decay, T, H, dev)
+    _check(cu_seqlens, "cu_seqlens", torch.int32, (N + 1,), dev)
+    for name, t in (("init_state", init_state), ("final_state", final_state)):
+        if t is not None:
+            _check(t, name, torch.float32, (N, H, d, d), dev)
+    ws, nbytes = _workspace_arg(workspace, dev)
+    _require_cuda(dev)
+    with _on(dev):
+        st = load().kda_linear_prefill(_ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), per_token, _ptr(cu_seqlens),
+                                       _ptr(init_state), _ptr(out), _ptr(final_state), N, T, H, float(scale), ws,
+                                       nbytes, _stream_handle(stream, dev))
+    if st != KDA_OK:
+        raise KdaError(st, "kda_linear_prefill")
+
+
+def kda_linear_prefill_workspace_size(num_seqs, total_tokens, num_heads, sm_count=0) -> int:
+    """Workspace bytes kda_linear_prefill uses for this shape (0: none); sm_count 0 asks the current device."""
+    n = load().kda_linear_prefill_workspace_size(int(num_seqs), int(total_tokens), int(num_heads), int(sm_count))
+    if n < 0:
+        raise KdaError(int(n), "kda_linear_prefill_workspace_size")
+    return int(n)
+
+
+def linear_prefill_workspace(num_seqs, total_tokens, num_heads, device):
+    """A uint8 device tensor sized for kda_linear_prefill on `device` (None when none is used)."""
+    import torch
+    with torch.cuda.device(device):
+        n = kda_linear_prefill_workspace_size(num_seqs, total_tokens, num_heads)
+    return torch.empty(n, dtype=torch.uint8, device=device) if n > 0 else None
+
+
+def kda_linear_decode(q, k, v, log_decay, slot_idx, state_pool, out, scale, stream=None):
+    """One token per row of linear attention with a decay for each head, on ``state_pool``
+    [slots, H, 128, 128] (FP32 or BF16, updated in place) at slots ``slot_idx`` (a negative one
+    is a padding row). ``log_decay``: FP32 [H] or [rows, H]."""
+    import torch
+    R, H, d = q.shape
+    dev = q.device
+    for name, t in (("q", q), ("k", k), ("v", v), ("out", out)):
+        _check(t, name, torch.bfloat16, (R, H, HEAD_DIM), dev)
+    per_row = _per_head_or_token(log_decay, R, H, dev)
+    _check(slot_idx, "slot_idx", torch.int32, (R,), dev)
+    if state_pool.dtype == torch.float32:
+        sdt = STATE_DTYPES["f32"]
+    elif state_pool.dtype == torch.bfloat16:
+        sdt = STATE_DTYPES["bf16"]
+    else:
+        raise TypeError("state_pool must be float32 or bfloat16")
+    _check(state_pool, "state_pool", state_pool.dtype, (state_pool.shape[0], H, d, d), dev)
+    _require_cuda(dev)
+    with _on(dev):
+        st = load().kda_linear_decode(_ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), per_row, _ptr(slot_idx),
+                                      _ptr(state_pool), int(state_pool.shape[0]), sdt, _ptr(out), R, H, float(scale),
+                                      _stream_handle(stream, dev))
+    if st != KDA_OK:
+        raise KdaError(st, "kda_linear_decode")
+
+
+def _check_cache(k_cache, v_cache, block_table, seq_lens, device):
+    """(batch, key heads, page size, pages, table width, page strides) of a paged cache: k_cache and
+    v_cache BF16 [pages, Hkv, page_size, 128], contiguous but for the distance between pages."""
+    import torch
+    if k_cache.dim() != 4:
+        raise ValueError(f"k_cache: expected [pages, heads, page_size, {HEAD_DIM}], got {tuple(k_cache.shape)}")
+    pages, Hkv, ps, d = k_cache.shape
+    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
+        if t.dtype != torch.bfloat16:
+            raise TypeError(f"{name}: expected {torch.bfloat16}, got {t.dtype}")
+        if tuple(t.shape) != (pages, Hkv, ps, HEAD_DIM):
+            raise ValueError(f"{name}: expected shape {(pages, Hkv, ps, HEAD_DIM)}, got {tuple(t.shape)}")
+        if tuple(t.stride()[1:]) != (ps * HEAD_DIM, HEAD_DIM, 1):
+            raise ValueError(f"{name}: a page must be contiguous")
+        if t.device != device:
+            raise ValueError(f"{name}: expected device {device}, got {t.device}")
+    B = seq_lens.shape[0]
+    _check(seq_lens, "seq_lens", torch.int32, (B,), device)
+    if block_table.dim() != 2:
+        raise ValueError(f"block_table: expected [batch, max_pages], got {tuple(block_table.shape)}")
+    P = block_table.shape[1]
+    _check(block_table, "block_table", torch.int32, (B, P), device)
+    return B, Hkv, ps, pages, P, k_cache.stride(0), v_cache.stride(0)
+
+
+def kda_attn_decode(q, k_cache, v_cache, block_table, seq_lens, out, scale, workspace, lse=None, weight=None,
+                    stream=None):
+    """Attention of one new token per row over a paged key-value cache: ``q`` and ``out`` BF16
+    [B, Hq, 128], the caches BF16 [pages, Hkv, page_size, 128], ``block_table`` int32
+    [B, max_pages] (negative: missing page), ``seq_lens`` int32 [B]. Optionally writes ``lse``
+    [B, Hq] and adds each token's attention weight, summed over the query heads of its key head,
+    to ``weight`` FP32 [B, Hkv, max_pages * page_size]. ``workspace``: attn_decode_workspace."""
+    import torch
+    dev = q.device
+    B, Hkv, ps, pages, P, ks, vs = _check_cache(k_cache, v_cache, block_table, seq_lens, dev)
+    Hq = q.shape[1]
+    for name, t in (("q", q), ("out", out)):
+        _check(t, name, torch.bfloat16, (B, Hq, HEAD_DIM), dev)
+    if lse is not None:
+        _check(lse, "lse", torch.float32, (B, Hq), dev)
+    if weight is not None:
+        _check(weight, "weight", torch.float32, (B, Hkv, P * ps), dev)
+    ws, nbytes = _workspace_arg(workspace, dev)
+    _require_cuda(dev)
+    with _on(dev):
+        st = load().kda_attn_decode(_ptr(q), _ptr(k_cache), _ptr(v_cache), ks, vs, pages, ps, _ptr(block_table), P,
+                                    _ptr(seq_lens), _ptr(out), _ptr(lse), _ptr(weight), B, Hq, Hkv, float(scale), ws,
+                                    nbytes, _stream_handle(stream, dev))
+    if st != KDA_OK:
+        raise KdaError(st, "kda_attn_decode")
+
+
+def kda_attn_decode_workspace_size(batch, num_q_heads, num_kv_heads, max_pages, page_size, with_weight=False,
+                                   sm_count=0) -> int:
+    """Workspace bytes of kda_attn_decode for this shape; sm_count 0 asks the current device."""
+    n = load().kda_attn_decode_workspace_size(int(batch), int(num_q_heads), int(num_kv_heads), int(max_pages),
+                                              int(page_size), int(bool(with_weight)), int(sm_count))
+    if n < 0:
+        raise KdaError(int(n), "kda_attn_decode_workspace_size")
+    return int(n)
+
+
+def attn_decode_workspace(batch, num_q_heads, num_kv_heads, max_pages, page_size, with_weight, device):
+    """A uint8 device tensor sized for kda_attn_decode on `device`."""
+    import torch
+    with torch.cuda.device(device):
+        n = kda_attn_decode_workspace_size(batch, num_q_heads, num_kv_heads, max_pages, page_size, with_weight)
+    return torch.empty(max(n, 16), dtype=torch.uint8, device=device)
+
+
+def kda_cache_evict(k_cache, v_cache, block_table, seq_lens, weight, new_lens, kept, budget, sink=0, recent=0,
+                    dst_table=None, dst_weight=None, stream=None):
+    """Shortens rows of a paged cache longer than ``budget`` tokens to ``budget``, per key head:
+    the first ``sink``, the last ``recent`` and the heaviest others by ``weight`` stay, packed in
+    order into the pages of ``dst_table`` (None: in place), their weights into ``dst_weight``
+    (None: in place). Writes ``new_lens`` int32 [B] and ``kept`` int32 [B, Hkv, budget] (old
+    positions, ascending, then -1)."""
+    import torch
+    dev = k_cache.device
+    B, Hkv, ps, pages, P, ks, vs = _check_cache(k_cache, v_cache, block_table, seq_lens, dev)
+    dst_weight = weight if dst_weight is None else dst_weight
+    for name, t in (("weight", weight), ("dst_weight", dst_weight)):
+        _check(t, name, torch.float32, (B, Hkv, P * ps), dev)
+    if dst_table is not None:
+        _check(dst_table, "dst_table", torch.int32, (B, P), dev)
+    _check(new_lens, "new_lens", torch.int32, (B,), dev)
+    _check(kept, "kept", torch.int32, (B, Hkv, int(budget)), dev)
+    _require_cuda(dev)
+    with _on(dev):
+        st = load().kda_cache_evict(_ptr(k_cache), _ptr(v_cache), ks, vs, pages, ps, _ptr(block_table),
+                                    _ptr(dst_table), P, _ptr(seq_lens), _ptr(weight), _ptr(dst_weight),
+                                    _ptr(new_lens), _ptr(kept), B, Hkv, int(budget), int(sink), int(recent),
+                                    _stream_handle(stream, dev))
+    if st != KDA_OK:
+        raise KdaError(st, "kda_cache_evict")
+
+
+def linear_prefill(q, k, v, log_decay, cu_seqlens, init_state=None, *, scale, want_final=True, workspace=None,
+                   stream=None):
+    """Allocates ``out`` (and ``final_state``) and runs ``kda_linear_prefill``; returns (out, final_state)."""
+    import torch
+    T, H, d = q.shape
+    N = cu_seqlens.shape[0] - 1
+    out = torch.empty_like(q)
+    final = torch.empty(N, H, d, d, dtype=torch.float32, device=q.device) if want_final else None
+    kda_linear_prefill(q, k, v, log_decay, cu_seqlens, init_state, out, final, scale, workspace, stream)
+    return out, final
+
+
+def linear_decode(q, k, v, log_decay, slot_idx, state_pool, *, scale, stream=None):
+    """Allocates ``out`` and runs ``kda_linear_decode`` (pool updated in place); returns out."""
+    import torch
+    out = torch.empty_like(q)
+    kda_linear_decode(q, k, v, log_decay, slot_idx, state_pool, out, scale, stream)
+    return out
+
+
+def attn_decode(q, k_cache, v_cache, block_table, seq_lens, *, scale, want_lse=False, weight=None, workspace=None,
+                stream=None):
+    """Allocates ``out`` (and ``lse``, and a workspace when none is given) and runs
+    ``kda_attn_decode``; returns out, or (out, lse)."""
+    import torch
+    B, Hq, _ = q.shape
+    out = torch.empty_like(q)
+    lse = torch.empty(B, Hq, dtype=torch.float32, device=q.device) if want_lse else None
+    _require_cuda(q.device)
+    if workspace is None:
+        workspace = attn_decode_workspace(B, Hq, k_cache.shape[1], block_table.shape[1], k_cache.shape[2],
+                                          weight is not None, q.device)
+        if stream is not None:  # the caching allocator must not hand it out while `stream` uses it
+            workspace.record_stream(stream)
+    kda_attn_decode(q, k_cache, v_cache, block_table, seq_lens, out, scale, workspace, lse, weight, stream)
+    return (out, lse) if want_lse else out
+
+
+def cache_evict(k_cache, v_cache, block_table, seq_lens, weight, *, budget, sink=0, recent=0, dst_table=None,
+                dst_weight=None, stream=None):
+    """Allocates ``new_lens`` and ``kept`` and runs ``kda_cache_evict``; returns (new_lens, kept)."""
+    import torch
+    new_lens = torch.empty_like(seq_lens)
+    kept = torch.empty(seq_lens.shape[0], k_cache.shape[1], int(budget), dtype=torch.int32, device=seq_lens.device)
+    kda_cache_evict(k_cache, v_cache, block_table, seq_lens, weight, new_lens, kept, budget, sink, recent, dst_table,
+                    dst_weight, stream)
+    return new_lens, kept

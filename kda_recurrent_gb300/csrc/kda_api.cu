@@ -42,6 +42,14 @@ cudaError_t device_status_ptr(DeviceStatus **out) {
     return cudaSuccess;
 }
 
+int sm_count_of_current_device(int32_t *sms) {
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return KDA_ERR_CUDA;
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return KDA_ERR_CUDA;
+    *sms = n;
+    return KDA_OK;
+}
+
 }  // namespace kda
 
 using namespace kda;
@@ -64,14 +72,6 @@ const char *kda_status_string(int status) {
 }
 
 namespace {
-
-int sm_count_of_current_device(int32_t *sms) {
-    int dev = 0, n = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return KDA_ERR_CUDA;
-    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return KDA_ERR_CUDA;
-    *sms = n;
-    return KDA_OK;
-}
 
 int prefill_common(const void *q, const void *k, const void *v, const void *g_raw, const float *beta,
                    const int32_t *cu_seqlens, const float *init_state, void *out, float *final_state,

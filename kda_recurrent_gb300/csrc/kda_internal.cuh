@@ -94,6 +94,83 @@ __host__ __device__ constexpr int64_t window_flag_bytes(int64_t chains, int64_t 
     return (chains * wins * 4 + 255) / 256 * 256;
 }
 
+// Linear attention with a decay for each head: prompt form.
+struct LinearPrefillArgs {
+    const __nv_bfloat16 *q, *k, *v;
+    const float *log_decay;      // [H], or [T][H]
+    int64_t decay_token_stride;  // 0, or num_heads
+    const int32_t *cu_seqlens;
+    const float *init_state;
+    __nv_bfloat16 *out;
+    float *final_state;
+    int32_t num_seqs, total_tokens, num_heads;
+    float scale;
+    DeviceStatus *status;
+};
+
+// Linear attention: single-token form on a slot pool.
+struct LinearDecodeArgs {
+    const __nv_bfloat16 *q, *k, *v;
+    const float *log_decay;    // [H], or [rows][H]
+    int64_t decay_row_stride;  // 0, or num_heads
+    const int32_t *slot_idx;
+    void *state_pool;
+    int64_t num_slots;
+    __nv_bfloat16 *out;
+    int32_t rows, num_heads, state_dtype;
+    float scale;
+    DeviceStatus *status;
+};
+
+// Pages of a key-value cache and the rows' tables (kda.h: "Paged key-value cache").
+struct PagedCache {
+    __nv_bfloat16 *k, *v;
+    int64_t k_page_stride, v_page_stride;  // elements
+    int64_t num_pages;
+    const int32_t *block_table;
+    const int32_t *seq_lens;
+    int32_t batch, num_kv_heads, max_pages, page_size, page_shift;
+    int32_t capacity;  // max_pages * page_size
+};
+
+struct AttnDecodeArgs {
+    PagedCache c;
+    const __nv_bfloat16 *q;
+    __nv_bfloat16 *out;
+    float *lse, *weight;
+    int32_t num_q_heads, group;  // group: query heads per key head
+    float scale;
+    void *ws;
+    DeviceStatus *status;
+};
+
+struct CacheEvictArgs {
+    PagedCache c;
+    const int32_t *dst_table;
+    const float *weight;
+    float *dst_weight;
+    int32_t *new_lens, *kept;
+    int32_t budget, sink, recent;
+    DeviceStatus *status;
+};
+
+// Token count of a row, clamped into range; `report` (one caller per row) records a bad value.
+__device__ __forceinline__ int row_length(const PagedCache &c, int b, DeviceStatus *st, bool report) {
+    const int n = c.seq_lens[b];
+    if (n >= 0 && n <= c.capacity) return n;
+    if (report) report_error(st, KDA_ERR_DEVICE_INPUT, b);
+    return n < 0 ? 0 : c.capacity;
+}
+
+cudaError_t launch_linear_prefill(const LinearPrefillArgs &a, cudaStream_t stream);
+cudaError_t launch_linear_decode(const LinearDecodeArgs &a, cudaStream_t stream);
+cudaError_t launch_attn_decode(const AttnDecodeArgs &a, cudaStream_t stream);
+cudaError_t launch_cache_evict(const CacheEvictArgs &a, cudaStream_t stream);
+int64_t linear_prefill_workspace_bytes(int32_t num_seqs, int32_t total_tokens, int32_t num_heads, int32_t sms);
+int64_t attn_decode_workspace_bytes(int32_t batch, int32_t num_q_heads, int32_t num_kv_heads, int64_t capacity,
+                                    bool with_weight, int32_t sms);
+int sm_count_of_current_device(int32_t *sms);  // a kda_status
+
 cudaError_t launch_decode(const DecodeArgs &a, cudaStream_t stream);
 cudaError_t launch_prefill_tc(const PrefillArgs &a, cudaStream_t stream);  // windows when a.wins > 1
 
