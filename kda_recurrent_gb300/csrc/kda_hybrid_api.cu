@@ -89,6 +89,7 @@ int kda_linear_prefill(const void *q, const void *k, const void *v, const float 
     a.total_tokens = total_tokens;
     a.num_heads = num_heads;
     a.scale = scale;
+    a.ws = workspace;
     if (device_status_ptr(&a.status) != cudaSuccess) return KDA_ERR_CUDA;
     return from_cuda(launch_linear_prefill(a, reinterpret_cast<cudaStream_t>(stream)));
 }

@@ -105,6 +105,7 @@ struct LinearPrefillArgs {
     float *final_state;
     int32_t num_seqs, total_tokens, num_heads;
     float scale;
+    void *ws;  // window schedule's workspace, or NULL
     DeviceStatus *status;
 };
 

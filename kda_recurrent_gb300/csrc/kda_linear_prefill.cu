@@ -1,55 +1,766 @@
-// Linear attention with a decay for each head, prompt form (sm_103a).
+// Linear attention with a decay for each head, prompt form (sm_103a, tcgen05 / TMEM / TMA).
 //
 //     S_t = exp(g_t) S_{t-1} + k_t v_t^T,   o_t = scale S_t^T q_t
 //
-// Token by token: one CTA per (sequence, head) chain, thread j holding column j of the
-// 128 x 128 state in registers; k and q of a token are shared through shared memory.
+// Chunks of C = 128 tokens. With G the inclusive prefix sum of g over the chunk and S the state
+// before it, the chunk is four products of 128 x 128 tiles:
+//     A   = Q K^T                                  scores
+//     P   = A . exp(G_i - G_j) for j <= i, else 0
+//     O   = scale (Diag(exp G) (Q S) + P V)
+//     S' = exp(G_last) S + D,   D = (Diag(exp(G_last - G_j)) K)^T V
+// All inputs of the products are BF16 tiles in shared memory (P in tensor memory), accumulators
+// FP32 in tensor memory. What is rounded to BF16 on the way to an output: P, and the copy of S that
+// the queries read; each adds about the error of the output's own rounding. The state must carry
+// more (it is an FP32 output, summed over thousands of tokens): its decayed keys are split into two
+// BF16 terms, hi + lo, 16 bits of mantissa, at the price of a second product (V is exact), and S itself
+// stays FP32 in the registers of the state warps. D does not depend on S, so the only serial work
+// from chunk to chunk is S' = exp(G_last) S + D and its rounding into the next chunk's operand.
+//
+// One CTA per chain (or window of a chain), 20 warps in five roles:
+//   warp 0        TMA: K, Q, V tiles of a chunk (128-byte swizzle) into a ring of five 32 KiB tiles
+//   warp 1        issues every MMA: A, Q S, D (hi then lo), P V
+//   warp 2        the chunk's prefix and suffix sums of g
+//   warps 4-7     A -> P (one row a thread), written over A in tensor memory
+//   warps 8-11    O: both accumulators -> BF16 -> global memory
+//   warps 12-19   state: K -> hi (in place) and lo, S in registers (row dk, 64 columns a thread)
+// The suffix sums G_last - G_j are scanned from the end, not formed as differences, so that a
+// strong decay early in a chunk costs the later tokens' weights no precision. A log decay below
+// -128 counts as -128 (both decay to zero in FP32), which keeps the sums finite.
+//
+// Bound: 1 KiB of HBM traffic a token and head against 164 KFLOP of BF16 products.
+//
+// Few chains leave most SMs idle. A chain is then cut into windows: a first pass computes each
+// window's end state from zero (the update half of the kernel) and its total decay, an
+// elementwise pass chains the windows' start states, S_{w+1} = exp(g_w) S_w + D_w, and the chunk
+// kernel runs every window from its start state. The same is done for the chains of a short last
+// wave, whose windows are launched behind the whole chains.
+//
+// All waits are bounded; on expiry the CTA records KDA_ERR_DEVICE_TIMEOUT, waits for its own
+// copies and MMAs in flight, frees its tensor memory and returns.
+#include <cuda.h>
+
+#include <algorithm>
+
 #include "kda_internal.cuh"
+#include "kda_mma.cuh"
+#include "kda_tc.cuh"
 
 namespace kda {
 namespace {
 
-__global__ void __launch_bounds__(kHeadDim) kda_linear_prefill_kernel(const LinearPrefillArgs a) {
-    __shared__ float s_k[kHeadDim], s_q[kHeadDim];
-    const int h = blockIdx.x % a.num_heads, n = blockIdx.x / a.num_heads, j = threadIdx.x;
-    int bos = a.cu_seqlens[n], eos = a.cu_seqlens[n + 1];
-    if (bos < 0 || eos < bos || eos > a.total_tokens) {
-        if (j == 0 && h == 0) report_error(a.status, KDA_ERR_DEVICE_INPUT, n);
-        bos = min(max(bos, 0), a.total_tokens);
-        eos = min(max(eos, bos), a.total_tokens);
-    }
-    const size_t base = (size_t)blockIdx.x * kHeadDim * kHeadDim + j;
-    float S[kHeadDim];
-#pragma unroll
-    for (int i = 0; i < kHeadDim; ++i) S[i] = a.init_state ? a.init_state[base + i * kHeadDim] : 0.0f;
-    for (int t = bos; t < eos; ++t) {
-        const size_t at = ((size_t)t * a.num_heads + h) * kHeadDim + j;
-        __syncthreads();
-        s_k[j] = __bfloat162float(a.k[at]);
-        s_q[j] = __bfloat162float(a.q[at]);
-        const float v = __bfloat162float(a.v[at]);
-        const float decay = expf(a.log_decay[(size_t)t * a.decay_token_stride + h]);
-        __syncthreads();
-        float o = 0.0f;
-#pragma unroll
-        for (int i = 0; i < kHeadDim; ++i) {
-            S[i] = fmaf(S[i], decay, s_k[i] * v);
-            o = fmaf(s_q[i], S[i], o);
-        }
-        a.out[at] = __float2bfloat16_rn(a.scale * o);
-    }
-    if (a.final_state)
-#pragma unroll
-        for (int i = 0; i < kHeadDim; ++i) a.final_state[base + i * kHeadDim] = S[i];
+constexpr int kC = 128;  // tokens of a chunk
+constexpr int kTile = kC * kHeadDim * 2;
+constexpr int kHalf = kTile / 2;  // a tile is two halves of 64 columns: 128 rows of 128 bytes
+constexpr int kRing = 5;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kMinLogDecay = -128.0f;
+
+constexpr int kWarpMma = 1, kWarpGate = 2, kWarpAlloc = 3, kWarpP = 4, kWarpO = 8, kWarpS = 12;
+constexpr int kStateWarps = 8;
+constexpr int kStateThreads = kStateWarps * 32;
+constexpr int kThreads = (kWarpS + kStateWarps) * 32;
+
+struct Gates {
+    float prefix[kC];  // log2 units: inclusive prefix sums, and sums over the later tokens
+    float suffix[kC];
+    float decay;  // of the whole chunk
+    float pad[3];
+};
+
+struct Bars {
+    uint64_t full[kRing], empty[kRing];  // TMA -> users, users (tcgen05.commit) -> TMA
+    uint64_t scores;   // A done
+    uint64_t p;        // P written (4 warps)
+    uint64_t kp;       // hi and lo written (8 warps)
+    uint64_t d;        // D done
+    uint64_t d_free;   // D read (8 warps)
+    uint64_t s;        // S operand written (8 warps)
+    uint64_t qs;       // Q S done: the S operand is free
+    uint64_t o;        // P V done (and everything before it)
+    uint64_t o_free;   // both output accumulators read (4 warps)
+    uint64_t gate[2], gate_free[2];
+    uint64_t drain;
+    uint32_t tmem;
+    int32_t abort;
+};
+
+// ---- shared memory (bytes); the swizzled tiles need 1024-byte alignment
+constexpr int kLo = kRing * kTile;
+constexpr int kS = kLo + kTile;
+constexpr int kGates = kS + kTile;
+constexpr int kBars = kGates + 2 * (int)sizeof(Gates);
+constexpr int kSmem = kBars + (int)sizeof(Bars);
+static_assert(kSmem <= 227 * 1024, "one CTA per SM");
+
+// ---- tensor memory (columns)
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kColA = 0;  // A (128), then P as BF16 pairs in the first 64
+constexpr uint32_t kColO = 128, kColQS = 256, kColD = 384;
+
+constexpr uint32_t kTransA = 1u << 15, kTransB = 1u << 16;  // MN-major operands
+constexpr uint32_t kIdescQK = instr_desc(1, 128, 128);
+constexpr uint32_t kIdescQS = instr_desc(1, 128, 128) | kTransB;
+constexpr uint32_t kIdescD = instr_desc(1, 128, 128) | kTransA | kTransB;
+constexpr uint32_t kIdescPV = instr_desc(1, 128, 128) | kTransB;
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
 }
+
+// MN-major operand with the 128-byte swizzle: 128-byte rows hold 64 elements along M or N, eight
+// rows (along K) make a 1024-byte group; `lbo` = distance between blocks of 64 along M or N.
+__device__ __forceinline__ uint64_t desc_mn(uint32_t saddr) {
+    uint64_t d = 0;
+    d |= (uint64_t)((saddr >> 4) & 0x3FFFu);
+    d |= (uint64_t)(kHalf >> 4) << 16;
+    d |= (uint64_t)(1024 >> 4) << 32;
+    d |= (uint64_t)1 << 46;
+    d |= (uint64_t)2 << 61;
+    return d;
+}
+
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc)
+        : "memory");
+}
+
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc)
+        : "memory");
+}
+
+__device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap *map, int x, int y, int z, uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+            dst),
+        "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_addr(bar))
+        : "memory");
+}
+
+__device__ __forceinline__ void expect_tx(uint64_t *bar, uint32_t bytes) {
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_addr(bar)), "r"(bytes) : "memory");
+}
+
+// Bounded wait of one thread that also gives up as soon as any thread of the CTA has.
+__device__ __forceinline__ bool wait_one(uint64_t *bar, uint32_t parity, Bars *B, DeviceStatus *st) {
+    const uint32_t addr = smem_addr(bar);
+    uint64_t start = 0;
+    for (;;) {
+        uint32_t done;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(done)
+            : "r"(addr), "r"(parity), "r"(kSuspendHintNs)
+            : "memory");
+        if (done) return true;
+        if (*reinterpret_cast<volatile int32_t *>(&B->abort)) return false;
+        const uint64_t now = global_ns();
+        if (start == 0) {
+            start = now;
+        } else if (now - start > kWaitLimitNs) {
+            *reinterpret_cast<volatile int32_t *>(&B->abort) = 1;
+            report_error(st, KDA_ERR_DEVICE_TIMEOUT, (int)blockIdx.x);
+            return false;
+        }
+    }
+}
+
+// The same for a whole warp, with one decision for all its lanes.
+__device__ __forceinline__ bool wait_warp(uint64_t *bar, uint32_t parity, Bars *B, DeviceStatus *st) {
+    return __all_sync(0xffffffffu, wait_one(bar, parity, B, st));
+}
+
+// One arrival for a warp, after what its lanes did.
+__device__ __forceinline__ void arrive_warp(uint64_t *bar) {
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+}
+
+__device__ __forceinline__ void pdl_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+struct Plan {
+    int32_t wins;        // windows of each windowed chain (1: none)
+    int32_t seq_chains;  // chains before the windowed ones
+};
+
+struct ChunkArgs {
+    LinearPrefillArgs p;
+    Plan plan;
+    float *slots;  // windowed chain lc, window w: the window's own end state, then the start of window w + 1
+    float *decay;  // windowed chain lc, window w: its total decay (log2)
+};
+
+__device__ __forceinline__ float *slot_of(const ChunkArgs &a, int lc, int w) {
+    return a.slots + ((size_t)lc * (a.plan.wins - 1) + w) * (kHeadDim * kHeadDim);
+}
+
+// Chains in order of their sequences' lengths, longest first (ties by index; more than kRanked
+// sequences keep index order): CTAs start in index order, so the longest start first.
+constexpr int kRanked = 256;
+
+__device__ __forceinline__ int seq_of_rank(const LinearPrefillArgs &a, int j, int *scratch) {
+    const int N = a.num_seqs;
+    if (N <= 1 || N > kRanked) return j;
+    int *len = scratch, *pick = scratch + kRanked;
+    for (int i = threadIdx.x; i < N; i += blockDim.x)
+        len[i] = (int)((unsigned)__ldg(a.cu_seqlens + i + 1) - (unsigned)__ldg(a.cu_seqlens + i));
+    __syncthreads();
+    for (int i = threadIdx.x; i < N; i += blockDim.x) {
+        const int li = len[i];
+        int r = 0;
+        for (int m = 0; m < N; ++m) r += (len[m] > li) | ((len[m] == li) & (m < i));
+        if (r == j) *pick = i;
+    }
+    __syncthreads();
+    const int n = *pick;
+    __syncthreads();
+    return n;
+}
+
+struct Span {
+    int bos, eos;  // tokens of the window
+    bool first, last, live;
+};
+
+// Window w (of at most W) of sequence n.
+__device__ __forceinline__ Span span_of(const LinearPrefillArgs &a, int n, int w, int W, bool report) {
+    int sb = a.cu_seqlens[n], se = a.cu_seqlens[n + 1];
+    if (sb < 0 || se < sb || se > a.total_tokens) {
+        if (report && threadIdx.x == 0) report_error(a.status, KDA_ERR_DEVICE_INPUT, n);
+        sb = min(max(sb, 0), a.total_tokens);
+        se = min(max(se, sb), a.total_tokens);
+    }
+    const int chunks = (se - sb + kC - 1) / kC;
+    const int per = max(1, (chunks + W - 1) / W);
+    const int wins = max(1, (chunks + per - 1) / per);
+    Span s;
+    s.live = w < wins;
+    s.first = w == 0;
+    s.last = w >= wins - 1;
+    s.bos = s.live ? sb + kC * per * w : se;
+    s.eos = s.last ? se : s.bos + kC * per;
+    return s;
+}
+
+// kStates: only the state update, from zero, over the windows of the windowed chains but the last.
+template <bool kStates>
+__global__ void __launch_bounds__(kThreads, 1)
+    kda_linear_chunk_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap map_q,
+                            const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v) {
+    extern __shared__ __align__(1024) uint8_t smem[];
+    const LinearPrefillArgs &p = a.p;
+    Bars *B = reinterpret_cast<Bars *>(smem + kBars);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, H = p.num_heads;
+    const int W = a.plan.wins;
+    // the item: a whole chain, or window w of windowed chain lc
+    int pos = blockIdx.x, w = 0, lc = -1;
+    if (kStates || pos >= a.plan.seq_chains) {
+        const int per = kStates ? W - 1 : W;
+        const int i = kStates ? pos : pos - a.plan.seq_chains;
+        lc = i / per;
+        w = i - lc * per;
+        pos = a.plan.seq_chains + lc;
+    }
+    const int h = pos % H;
+    const int n = seq_of_rank(p, pos / H, reinterpret_cast<int *>(smem));
+    const Span sp = span_of(p, n, w, lc >= 0 ? W : 1, h == 0 && w == 0 && !kStates);
+    if (kStates) pdl_launch_dependents();
+    if (!sp.live || (kStates && sp.last)) {
+        if (!kStates) pdl_wait();  // every CTA ends after the launches before: see the last lines
+        return;
+    }
+    const int nchunks = (sp.eos - sp.bos + kC - 1) / kC;
+    const size_t chain = ((size_t)n * H + h) * (kHeadDim * kHeadDim);
+    const float *const start = kStates ? nullptr : lc >= 0 && !sp.first ? slot_of(a, lc, w - 1)
+                                               : p.init_state ? p.init_state + chain : nullptr;
+    float *const end = kStates ? slot_of(a, lc, w) : sp.last && p.final_state ? p.final_state + chain : nullptr;
+    // the last chunk's update is needed only where somebody reads the end state
+    const int updates = end ? nchunks : nchunks - 1;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kRing; ++i) mbar_init(&B->full[i], 1), mbar_init(&B->empty[i], 1);
+        mbar_init(&B->scores, 1);
+        mbar_init(&B->p, 4);
+        mbar_init(&B->kp, kStateWarps);
+        mbar_init(&B->d, 1);
+        mbar_init(&B->d_free, kStateWarps);
+        mbar_init(&B->s, kStateWarps);
+        mbar_init(&B->qs, 1);
+        mbar_init(&B->o, 1);
+        mbar_init(&B->o_free, 4);
+        for (int i = 0; i < 2; ++i) mbar_init(&B->gate[i], 1), mbar_init(&B->gate_free[i], kStates ? kStateWarps : kStateWarps + 8);
+        mbar_init(&B->drain, 1);
+        // the swizzled tiles are laid out for a 1024-byte-aligned base
+        B->abort = (smem_addr(smem) & 1023u) != 0;
+        if (B->abort) report_error(p.status, KDA_ERR_CUDA, 0);
+        fence_mbar_init();
+    }
+    if (warp == kWarpAlloc) {
+        tmem_alloc(&B->tmem, kTmemCols);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    fence_async_smem();  // the ranking's scratch lies where the first tiles go
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = B->tmem;
+    const uint32_t base = smem_addr(smem);
+    constexpr int kPer = kStates ? 2 : 3;  // tiles of a chunk: K, (Q,) V
+    int issued = 0;                        // loads issued (the TMA thread)
+
+    if (B->abort) {
+        // nothing has started
+    } else if (warp == 0) {
+        if (lane == 0) {
+            for (; issued < nchunks * kPer; ++issued) {
+                const int slot = issued % kRing, c = issued / kPer, which = issued - c * kPer;
+                if (issued >= kRing && !wait_one(&B->empty[slot], (issued / kRing - 1) & 1, B, p.status)) break;
+                const CUtensorMap *map = which == 0 ? &map_k : which == kPer - 1 ? &map_v : &map_q;
+                expect_tx(&B->full[slot], kTile);
+                tma_load(base + slot * kTile, map, 0, h, sp.bos + c * kC, &B->full[slot]);
+                tma_load(base + slot * kTile + kHalf, map, 64, h, sp.bos + c * kC, &B->full[slot]);
+            }
+        }
+    } else if (warp == kWarpMma) {
+        if (lane == 0) {
+            for (int c = 0; c < nchunks; ++c) {
+                const int ik = c * kPer, iq = ik + 1, iv = ik + kPer - 1;
+                const uint32_t k = base + (ik % kRing) * kTile, q = base + (iq % kRing) * kTile, v = base + (iv % kRing) * kTile;
+                const int steps = min(kC, sp.eos - sp.bos - c * kC + 15) >> 4;  // of 16 tokens
+                if (!wait_one(&B->full[ik % kRing], (ik / kRing) & 1, B, p.status)) break;
+                if (!kStates) {
+                    if (!wait_one(&B->full[iq % kRing], (iq / kRing) & 1, B, p.status)) break;
+                    if (c > 0 && !wait_one(&B->o, (c - 1) & 1, B, p.status)) break;  // P of the last chunk is read
+#pragma unroll
+                    for (int s = 0; s < 8; ++s) {
+                        const uint32_t off = (s >> 2) * kHalf + (s & 3) * 32;
+                        mma_ss(tmem + kColA, smem_desc_sw128(q + off), smem_desc_sw128(k + off), kIdescQK, s > 0);
+                    }
+                    mma_commit(&B->scores);
+                    if (!wait_one(&B->s, c & 1, B, p.status)) break;
+                    if (c > 0 && !wait_one(&B->o_free, (c - 1) & 1, B, p.status)) break;
+                    tc_fence_after();
+#pragma unroll
+                    for (int s = 0; s < 8; ++s)
+                        mma_ss(tmem + kColQS, smem_desc_sw128(q + (s >> 2) * kHalf + (s & 3) * 32),
+                               desc_mn(base + kS + s * 2048), kIdescQS, s > 0);
+                    mma_commit(&B->qs);
+                    mma_commit(&B->empty[iq % kRing]);
+                }
+                if (!wait_one(&B->kp, c & 1, B, p.status)) break;
+                if (!wait_one(&B->full[iv % kRing], (iv / kRing) & 1, B, p.status)) break;
+                if (c > 0 && c < updates && !wait_one(&B->d_free, (c - 1) & 1, B, p.status)) break;
+                tc_fence_after();
+                if (c < updates) {
+                    for (int s = 0; s < steps; ++s)
+                        mma_ss(tmem + kColD, desc_mn(k + s * 2048), desc_mn(v + s * 2048), kIdescD, s > 0);
+                    for (int s = 0; s < steps; ++s)
+                        mma_ss(tmem + kColD, desc_mn(base + kLo + s * 2048), desc_mn(v + s * 2048), kIdescD, true);
+                    mma_commit(&B->d);
+                }
+                mma_commit(&B->empty[ik % kRing]);
+                if (!kStates) {
+                    if (!wait_one(&B->p, c & 1, B, p.status)) break;
+                    tc_fence_after();
+                    for (int s = 0; s < steps; ++s)
+                        mma_ts(tmem + kColO, tmem + kColA + 8 * s, desc_mn(v + s * 2048), kIdescPV, s > 0);
+                    mma_commit(&B->o);
+                }
+                mma_commit(&B->empty[iv % kRing]);
+            }
+            mma_commit(&B->drain);  // every earlier commit has reached its barrier when this one has
+            mbar_wait(&B->drain, 0);
+        }
+    } else if (warp == kWarpGate) {
+        float run = 0.0f;  // total decay of the window so far
+        for (int c = 0; c < nchunks; ++c) {
+            const int t0 = sp.bos + c * kC, L = min(kC, sp.eos - t0), b = c & 1;
+            float g[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int t = 4 * lane + e;
+                float x = t < L ? p.log_decay[(size_t)(t0 + t) * p.decay_token_stride + h] : 0.0f;
+                g[e] = (x < kMinLogDecay ? kMinLogDecay : x) * kLog2e;
+            }
+            const float mine = (g[0] + g[1]) + (g[2] + g[3]);
+            float up = mine, down = mine;  // inclusive over the lanes before, and after
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const float x = __shfl_up_sync(0xffffffffu, up, o), y = __shfl_down_sync(0xffffffffu, down, o);
+                if (lane >= o) up += x;
+                if (lane + o < 32) down += y;
+            }
+            float before = __shfl_up_sync(0xffffffffu, up, 1), after = __shfl_down_sync(0xffffffffu, down, 1);
+            if (lane == 0) before = 0.0f;
+            if (lane == 31) after = 0.0f;
+            const float total = __shfl_sync(0xffffffffu, down, 0);
+            if (c >= 2 && !wait_warp(&B->gate_free[b], ((c >> 1) - 1) & 1, B, p.status)) break;
+            Gates *G = reinterpret_cast<Gates *>(smem + kGates) + b;
+            const float p0 = before + g[0], p1 = p0 + g[1], p2 = p1 + g[2], p3 = p2 + g[3];
+            *reinterpret_cast<float4 *>(&G->prefix[4 * lane]) = make_float4(p0, p1, p2, p3);
+            const float s2 = after + g[3], s1 = s2 + g[2], s0 = s1 + g[1];
+            *reinterpret_cast<float4 *>(&G->suffix[4 * lane]) = make_float4(s0, s1, s2, after);
+            // exp2f, not the 2^-22 of the hardware's: this error repeats every chunk and adds up over
+            // the chunks that a slowly decaying state remembers
+            if (lane == 0) G->decay = exp2f(total);
+            arrive_warp(&B->gate[b]);
+            run += total;
+        }
+        if (kStates && lane == 0) a.decay[(size_t)lc * W + w] = run;
+    } else if (warp >= kWarpP && warp < kWarpO && !kStates) {
+        const int quad = warp & 3, row = 32 * quad + lane;
+        const uint32_t lanes = tmem + ((uint32_t)(32 * quad) << 16) + kColA;
+        for (int c = 0; c < nchunks; ++c) {
+            const Gates *G = reinterpret_cast<const Gates *>(smem + kGates) + (c & 1);
+            if (!wait_warp(&B->gate[c & 1], (c >> 1) & 1, B, p.status)) break;
+            if (!wait_warp(&B->scores, c & 1, B, p.status)) break;
+            tc_fence_after();
+            const float gi = G->prefix[row];
+            // columns [32 b, 32 b + 32) of A become columns [16 b, 16 b + 16) of P, which lie under
+            // columns of A already read
+#pragma unroll 1
+            for (int b = 0; b < 4; ++b) {
+                uint32_t pk[16];
+                if (b <= quad) {
+                    float s[32];
+                    tmem_ld32(lanes + 32 * b, s);
+                    float e[32];
+#pragma unroll
+                    for (int j = 0; j < 32; j += 4) {
+                        const float4 gj = *reinterpret_cast<const float4 *>(&G->prefix[32 * b + j]);
+                        e[j] = ex2(gi - gj.x), e[j + 1] = ex2(gi - gj.y), e[j + 2] = ex2(gi - gj.z), e[j + 3] = ex2(gi - gj.w);
+                    }
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) s[j] = (b < quad || j <= lane) ? s[j] * e[j] : 0.0f;
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) pk[j] = pack_bf16(s[2 * j], s[2 * j + 1]);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) pk[j] = 0;
+                }
+                float f[16];
+#pragma unroll
+                for (int j = 0; j < 16; ++j) f[j] = __uint_as_float(pk[j]);
+                tmem_st16(lanes + 16 * b, f);
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            arrive_warp(&B->p);
+            if (lane == 0) mbar_arrive(&B->gate_free[c & 1]);
+        }
+    } else if (warp >= kWarpO && warp < kWarpS && !kStates) {
+        const int quad = warp & 3, row = 32 * quad + lane;
+        const uint32_t lanes = tmem + ((uint32_t)(32 * quad) << 16);
+        for (int c = 0; c < nchunks; ++c) {
+            if (!wait_warp(&B->gate[c & 1], (c >> 1) & 1, B, p.status)) break;
+            const float lam = p.scale * ex2((reinterpret_cast<const Gates *>(smem + kGates) + (c & 1))->prefix[row]);
+            arrive_warp(&B->gate_free[c & 1]);
+            if (!wait_warp(&B->o, c & 1, B, p.status)) break;
+            tc_fence_after();
+            const int t = sp.bos + c * kC + row;
+            uint4 *const dst = reinterpret_cast<uint4 *>(p.out + ((size_t)t * H + h) * kHeadDim);
+#pragma unroll 1
+            for (int b = 0; b < 8; ++b) {
+                float o[16], x[16];
+                tmem_ld16(lanes + kColO + 16 * b, o);
+                tmem_ld16(lanes + kColQS + 16 * b, x);
+                tmem_wait_ld();
+                uint32_t pk[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    pk[j] = pack_bf16(fmaf(lam, x[2 * j], p.scale * o[2 * j]), fmaf(lam, x[2 * j + 1], p.scale * o[2 * j + 1]));
+                if (t < sp.eos) {
+                    dst[2 * b] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+                    dst[2 * b + 1] = make_uint4(pk[4], pk[5], pk[6], pk[7]);
+                }
+            }
+            tc_fence_before();
+            arrive_warp(&B->o_free);
+        }
+    } else if (warp >= kWarpS) {
+        const int quad = warp & 3, half = (warp - kWarpS) >> 2, row = 32 * quad + lane;  // row: dk
+        const int tid = threadIdx.x - kWarpS * 32;
+        const uint32_t lanes = tmem + ((uint32_t)(32 * quad) << 16) + kColD + 64 * half;
+        uint8_t *const s_row = smem + kS + half * kHalf + row * 128;
+        float S[64];
+        if (!kStates && lc >= 0 && !sp.first) pdl_wait();  // the slots are written by the launch before
+        if (start) {
+            const float4 *src = reinterpret_cast<const float4 *>(start + (size_t)row * kHeadDim + 64 * half);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const float4 x = src[i];
+                S[4 * i] = x.x, S[4 * i + 1] = x.y, S[4 * i + 2] = x.z, S[4 * i + 3] = x.w;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 64; ++i) S[i] = 0.0f;
+        }
+        auto publish = [&] {  // S as the BF16 operand of Q S
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                *reinterpret_cast<uint4 *>(s_row + ((i ^ (row & 7)) << 4)) =
+                    make_uint4(pack_bf16(S[8 * i], S[8 * i + 1]), pack_bf16(S[8 * i + 2], S[8 * i + 3]),
+                               pack_bf16(S[8 * i + 4], S[8 * i + 5]), pack_bf16(S[8 * i + 6], S[8 * i + 7]));
+            fence_async_smem();
+            arrive_warp(&B->s);
+        };
+        if (!kStates && nchunks > 0) publish();
+        bool ok = true;
+        for (int c = 0; c < nchunks && ok; ++c) {
+            const int ik = c * kPer, iv = ik + kPer - 1;
+            const int L = min(kC, sp.eos - sp.bos - c * kC);
+            const Gates *G = reinterpret_cast<const Gates *>(smem + kGates) + (c & 1);
+            ok = wait_warp(&B->gate[c & 1], (c >> 1) & 1, B, p.status) &&
+                 wait_warp(&B->full[ik % kRing], (ik / kRing) & 1, B, p.status) &&
+                 (kStates || wait_warp(&B->scores, c & 1, B, p.status));  // K has been read as it is
+            if (!ok) break;
+            if (c < updates) {
+                uint8_t *const tile = smem + (ik % kRing) * kTile, *const lo = smem + kLo;
+#pragma unroll 2
+                for (int i = 0; i < 8; ++i) {
+                    const int x = tid + kStateThreads * i, t = (x & 1023) >> 3;
+                    uint4 *const at = reinterpret_cast<uint4 *>(tile + x * 16);
+                    const uint4 in = *at;
+                    const float f = ex2(G->suffix[t]);
+                    const uint32_t u[4] = {in.x, in.y, in.z, in.w};
+                    uint32_t hi[4], rest[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float y0 = __uint_as_float(u[e] << 16) * f, y1 = __uint_as_float(u[e] & 0xffff0000u) * f;
+                        hi[e] = pack_bf16(y0, y1);
+                        rest[e] = pack_bf16(y0 - __uint_as_float(hi[e] << 16), y1 - __uint_as_float(hi[e] & 0xffff0000u));
+                        if (t >= L) hi[e] = rest[e] = 0;  // another sequence's key
+                    }
+                    *at = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                    *reinterpret_cast<uint4 *>(lo + x * 16) = make_uint4(rest[0], rest[1], rest[2], rest[3]);
+                }
+            }
+            if (L & 15) {  // another sequence's values inside the last 16 tokens that the products read
+                ok = wait_warp(&B->full[iv % kRing], (iv / kRing) & 1, B, p.status);
+                if (!ok) break;
+                for (int x = tid; x < 2048; x += kStateThreads)
+                    if (((x & 1023) >> 3) >= L) *reinterpret_cast<uint4 *>(smem + (iv % kRing) * kTile + x * 16) = make_uint4(0, 0, 0, 0);
+            }
+            const float decay = G->decay;
+            fence_async_smem();
+            arrive_warp(&B->kp);
+            if (lane == 0) mbar_arrive(&B->gate_free[c & 1]);
+            if (c < updates) {
+                ok = wait_warp(&B->d, c & 1, B, p.status);
+                if (!ok) break;
+                tc_fence_after();
+#pragma unroll
+                for (int b = 0; b < 4; ++b) {
+                    float d[16];
+                    tmem_ld16(lanes + 16 * b, d);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) S[16 * b + j] = fmaf(S[16 * b + j], decay, d[j]);
+                }
+                tc_fence_before();
+                arrive_warp(&B->d_free);  // (only with an update: an arrival for a chunk without one could complete
+                                          // a second phase before the MMA thread has seen the first)
+            }
+            if (!kStates && c + 1 < nchunks) {
+                ok = wait_warp(&B->qs, c & 1, B, p.status);
+                if (!ok) break;
+                publish();
+            }
+        }
+        pdl_wait();  // an initial state in the same place has been read by the launches before
+        if (ok && end) {
+            float4 *dst = reinterpret_cast<float4 *>(end + (size_t)row * kHeadDim + 64 * half);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) dst[i] = make_float4(S[4 * i], S[4 * i + 1], S[4 * i + 2], S[4 * i + 3]);
+        }
+    }
+    __syncwarp();
+    __syncthreads();
+    if (B->abort) {  // wait (bounded) for what is still in flight before the memory is given back
+        if (threadIdx.x == 0)
+            for (int i = max(0, issued - kRing); i < issued; ++i) mbar_wait(&B->full[i % kRing], (i / kRing) & 1);
+        __syncthreads();
+    }
+    tc_fence_after();
+    if (warp == kWarpAlloc) tmem_dealloc(tmem, kTmemCols);
+    // whatever follows this grid on the stream also follows the launches that it may overlap
+    pdl_wait();
+}
+
+// S_{w+1} = exp2(g_w) S_w + D_w over the windows of a windowed chain, in place in its slots; one
+// float4 of the state a thread, the windows' own states loaded ahead.
+constexpr int kScanThreads = 128;
+constexpr int kScanCtas = kHeadDim * kHeadDim / (4 * kScanThreads);
+
+__global__ void __launch_bounds__(kScanThreads) kda_linear_scan_kernel(const ChunkArgs a) {
+    __shared__ int scratch[kRanked + 1];
+    const int lc = blockIdx.x / kScanCtas, part = blockIdx.x - lc * kScanCtas;
+    const int pos = a.plan.seq_chains + lc, h = pos % a.p.num_heads, W = a.plan.wins;
+    const int n = seq_of_rank(a.p, pos / a.p.num_heads, scratch);
+    pdl_launch_dependents();
+    const size_t off = ((size_t)part * kScanThreads + threadIdx.x) * 4;
+    float4 S = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (a.p.init_state)
+        S = *reinterpret_cast<const float4 *>(a.p.init_state + ((size_t)n * a.p.num_heads + h) * (kHeadDim * kHeadDim) + off);
+    pdl_wait();
+    constexpr int kAhead = 4;
+    for (int w0 = 0; w0 < W - 1; w0 += kAhead) {
+        float4 d[kAhead];
+        float g[kAhead];
+        bool on[kAhead];
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            const int w = w0 + i;
+            const Span sp = span_of(a.p, n, w, W, false);
+            on[i] = w < W - 1 && sp.live && !sp.last;
+            if (on[i]) {
+                d[i] = *reinterpret_cast<const float4 *>(slot_of(a, lc, w) + off);
+                g[i] = exp2f(a.decay[(size_t)lc * W + w]);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            if (!on[i]) continue;
+            S = make_float4(fmaf(S.x, g[i], d[i].x), fmaf(S.y, g[i], d[i].y), fmaf(S.z, g[i], d[i].z), fmaf(S.w, g[i], d[i].w));
+            *reinterpret_cast<float4 *>(slot_of(a, lc, w0 + i) + off) = S;
+        }
+    }
+}
+
+using EncodeTiled = decltype(&cuTensorMapEncodeTiled);
+
+EncodeTiled encode_tiled() {
+    static const EncodeTiled fn = [] {
+        void *p = nullptr;
+        cudaDriverEntryPointQueryResult found = cudaDriverEntryPointSymbolNotFound;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &found) != cudaSuccess ||
+            found != cudaDriverEntryPointSuccess)
+            p = nullptr;
+        return reinterpret_cast<EncodeTiled>(p);
+    }();
+    return fn;
+}
+
+// [T][H][128] BF16, in boxes of 128 tokens x one head x 64 columns; tokens past T read as zeros.
+cudaError_t token_map(CUtensorMap *map, const __nv_bfloat16 *base, int32_t T, int32_t H) {
+    const EncodeTiled encode = encode_tiled();
+    if (!encode) return cudaErrorNotSupported;
+    const cuuint64_t dims[3] = {kHeadDim, (cuuint64_t)H, (cuuint64_t)T};
+    const cuuint64_t strides[2] = {kHeadDim * 2, (cuuint64_t)H * kHeadDim * 2};
+    const cuuint32_t box[3] = {64, 1, kC}, step[3] = {1, 1, 1};
+    const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<__nv_bfloat16 *>(base), dims, strides, box,
+                              step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+template <bool kStates>
+cudaError_t configure_once() {
+    static bool configured[64] = {};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64 || !configured[dev]) {
+        e = cudaFuncSetAttribute(kda_linear_chunk_kernel<kStates>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+        if (e != cudaSuccess) return e;
+        if (dev >= 0 && dev < 64) configured[dev] = true;
+    }
+    return cudaSuccess;
+}
+
+template <typename... P, typename... A>
+cudaError_t launch(void (*kernel)(P...), unsigned grid, unsigned block, size_t smem, cudaStream_t stream, bool dependent,
+                   const A &...args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(block);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = dependent ? 1 : 0;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+// Chains that fill at most a third of the GPU, alone or as a last wave, are cut into windows.
+Plan plan_linear(int32_t num_seqs, int32_t total_tokens, int32_t num_heads, int32_t sms) {
+    const int64_t chains = (int64_t)num_seqs * num_heads;
+    Plan p = {1, (int32_t)chains};
+    if (chains <= 0 || sms <= 0) return p;
+    const int64_t tail = chains % sms;
+    const int64_t most = ((int64_t)total_tokens + kC - 1) / kC;  // chunks of any one sequence
+    if (tail == 0 || tail * 3 > sms) return p;
+    const int64_t wins = std::min<int64_t>(sms / tail, most);
+    if (wins < 3) return p;
+    p.wins = (int32_t)wins;
+    p.seq_chains = (int32_t)(chains - tail);
+    return p;
+}
+
+int64_t slot_bytes(int64_t tail, int64_t wins) { return tail * (wins - 1) * (kHeadDim * kHeadDim * 4LL); }
 
 }  // namespace
 
-int64_t linear_prefill_workspace_bytes(int32_t, int32_t, int32_t, int32_t) { return 0; }
+int64_t linear_prefill_workspace_bytes(int32_t num_seqs, int32_t total_tokens, int32_t num_heads, int32_t sms) {
+    const Plan p = plan_linear(num_seqs, total_tokens, num_heads, sms);
+    if (p.wins == 1) return 0;
+    const int64_t tail = (int64_t)num_seqs * num_heads - p.seq_chains;
+    return slot_bytes(tail, p.wins) + (tail * p.wins * 4 + 255) / 256 * 256;
+}
 
-cudaError_t launch_linear_prefill(const LinearPrefillArgs &a, cudaStream_t stream) {
-    kda_linear_prefill_kernel<<<(unsigned)a.num_seqs * (unsigned)a.num_heads, kHeadDim, 0, stream>>>(a);
-    return cudaGetLastError();
+cudaError_t launch_linear_prefill(const LinearPrefillArgs &args, cudaStream_t stream) {
+    const int64_t chains = (int64_t)args.num_seqs * args.num_heads;
+    if (args.total_tokens == 0) {  // every sequence is empty: final = initial
+        const size_t bytes = (size_t)chains * kHeadDim * kHeadDim * 4;
+        if (!args.init_state) return cudaMemsetAsync(args.final_state, 0, bytes, stream);
+        if (args.init_state == args.final_state) return cudaSuccess;
+        return cudaMemcpyAsync(args.final_state, args.init_state, bytes, cudaMemcpyDeviceToDevice, stream);
+    }
+    ChunkArgs a;
+    a.p = args;
+    a.plan = {1, (int32_t)chains};
+    a.slots = nullptr;
+    a.decay = nullptr;
+    if (args.ws) {
+        int32_t sms = 0;
+        if (sm_count_of_current_device(&sms) != KDA_OK) return cudaErrorInvalidDevice;
+        a.plan = plan_linear(args.num_seqs, args.total_tokens, args.num_heads, sms);
+    }
+    const int64_t tail = chains - a.plan.seq_chains;
+    CUtensorMap mq, mk, mv;
+    cudaError_t e = token_map(&mq, args.q, args.total_tokens, args.num_heads);
+    if (e == cudaSuccess) e = token_map(&mk, args.k, args.total_tokens, args.num_heads);
+    if (e == cudaSuccess) e = token_map(&mv, args.v, args.total_tokens, args.num_heads);
+    if (e == cudaSuccess) e = configure_once<false>();
+    if (e != cudaSuccess) return e;
+    if (tail > 0) {
+        a.slots = static_cast<float *>(args.ws);
+        a.decay = a.slots + slot_bytes(tail, a.plan.wins) / 4;
+        e = configure_once<true>();
+        if (e != cudaSuccess) return e;
+        e = launch(kda_linear_chunk_kernel<true>, (unsigned)(tail * (a.plan.wins - 1)), kThreads, kSmem, stream, false, a, mq, mk, mv);
+        if (e != cudaSuccess) return e;
+        e = launch(kda_linear_scan_kernel, (unsigned)(tail * kScanCtas), kScanThreads, 0, stream, true, a);
+        if (e != cudaSuccess) return e;
+    }
+    return launch(kda_linear_chunk_kernel<false>, (unsigned)(a.plan.seq_chains + tail * a.plan.wins), kThreads, kSmem, stream,
+                  tail > 0, a, mq, mk, mv);
 }
 
 }  // namespace kda
