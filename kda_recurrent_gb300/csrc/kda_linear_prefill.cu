@@ -7,22 +7,23 @@
 //     A   = Q K^T                                  scores
 //     P   = A . exp(G_i - G_j) for j <= i, else 0
 //     O   = scale (Diag(exp G) (Q S) + P V)
-//     S' = exp(G_last) S + D,   D = (Diag(exp(G_last - G_j)) K)^T V
+//     S' = exp(G_last) S + D,   D = K^T (Diag(exp(G_last - G_j)) V)
 // All inputs of the products are BF16 tiles in shared memory (P in tensor memory), accumulators
 // FP32 in tensor memory. What is rounded to BF16 on the way to an output: P, and the copy of S that
 // the queries read; each adds about the error of the output's own rounding. The state must carry
-// more (it is an FP32 output, summed over thousands of tokens): its decayed keys are split into two
-// BF16 terms, hi + lo, 16 bits of mantissa, at the price of a second product (V is exact), and S itself
+// more (it is an FP32 output, summed over thousands of tokens): its decayed values are split into two
+// BF16 terms, hi + lo, 17 bits of mantissa, at the price of a second product (K is exact), and S itself
 // stays FP32 in the registers of the state warps. D does not depend on S, so the only serial work
 // from chunk to chunk is S' = exp(G_last) S + D and its rounding into the next chunk's operand.
 //
 // One CTA per chain (or window of a chain), 20 warps in five roles:
-//   warp 0        TMA: K, Q, V tiles of a chunk (128-byte swizzle) into a ring of five 32 KiB tiles
-//   warp 1        issues every MMA: A, Q S, D (hi then lo), P V
+//   warp 0        TMA: Q, K, V tiles of a chunk (128-byte swizzle) into a ring of five 32 KiB tiles
+//   warp 1        issues every MMA: A, Q S, D by quarters of 32 tokens (hi then lo), P V
 //   warp 2        the chunk's prefix and suffix sums of g
-//   warps 4-7     A -> P (one row a thread), written over A in tensor memory
-//   warps 8-11    O: both accumulators -> BF16 -> global memory
-//   warps 12-19   state: K -> hi (in place) and lo, S in registers (row dk, 64 columns a thread)
+//   warps 4-11    A -> P in place in tensor memory, then O: both accumulators -> BF16 -> global
+//   warps 12-19   V -> hi, lo by quarters into a ring of two; S in registers (row dk, 64 columns a thread)
+// The values are decayed, not the keys, because V is only read by the last product of the chunk: the
+// split runs beside the scores instead of behind them.
 // The suffix sums G_last - G_j are scanned from the end, not formed as differences, so that a
 // strong decay early in a chunk costs the later tokens' weights no precision. A log decay below
 // -128 counts as -128 (both decay to zero in FP32), which keeps the sums finite.
@@ -55,29 +56,30 @@ constexpr int kRing = 5;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kMinLogDecay = -128.0f;
 
-constexpr int kWarpMma = 1, kWarpGate = 2, kWarpAlloc = 3, kWarpP = 4, kWarpO = 8, kWarpS = 12;
-constexpr int kStateWarps = 8;
+constexpr int kWarpMma = 1, kWarpGate = 2, kWarpAlloc = 3, kWarpO = 4, kWarpS = 12;
+constexpr int kOutWarps = 8, kStateWarps = 8;
 constexpr int kStateThreads = kStateWarps * 32;
 constexpr int kThreads = (kWarpS + kStateWarps) * 32;
 
 struct Gates {
     float prefix[kC];  // log2 units: inclusive prefix sums, and sums over the later tokens
-    float suffix[kC];
-    float decay;  // of the whole chunk
+    float suffix[kC];  // (as factors, 2^suffix)
+    float decay;       // of the whole chunk
     float pad[3];
 };
 
 struct Bars {
     uint64_t full[kRing], empty[kRing];  // TMA -> users, users (tcgen05.commit) -> TMA
     uint64_t scores;   // A done
-    uint64_t p;        // P written (4 warps)
-    uint64_t kp;       // hi and lo written (8 warps)
+    uint64_t p;        // P written (8 warps)
+    uint64_t split[2], split_free[2];  // hi and lo of a quarter written (8 warps), and read
+    uint64_t tail;     // rows past the window's last token cleared (8 warps)
     uint64_t d;        // D done
     uint64_t d_free;   // D read (8 warps)
     uint64_t s;        // S operand written (8 warps)
     uint64_t qs;       // Q S done: the S operand is free
     uint64_t o;        // P V done (and everything before it)
-    uint64_t o_free;   // both output accumulators read (4 warps)
+    uint64_t o_free;   // both output accumulators read (8 warps)
     uint64_t gate[2], gate_free[2];
     uint64_t drain;
     uint32_t tmem;
@@ -85,8 +87,11 @@ struct Bars {
 };
 
 // ---- shared memory (bytes); the swizzled tiles need 1024-byte alignment
-constexpr int kLo = kRing * kTile;
-constexpr int kS = kLo + kTile;
+constexpr int kQuarter = 32;                          // tokens
+constexpr int kSplitHalf = kQuarter * 128;            // 64 columns of a quarter
+constexpr int kSplitLo = 2 * kSplitHalf, kSplitStage = 2 * kSplitLo;
+constexpr int kSplit = kRing * kTile;
+constexpr int kS = kSplit + 2 * kSplitStage;
 constexpr int kGates = kS + kTile;
 constexpr int kBars = kGates + 2 * (int)sizeof(Gates);
 constexpr int kSmem = kBars + (int)sizeof(Bars);
@@ -94,7 +99,7 @@ static_assert(kSmem <= 227 * 1024, "one CTA per SM");
 
 // ---- tensor memory (columns)
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kColA = 0;  // A (128), then P as BF16 pairs in the first 64
+constexpr uint32_t kColA = 0;  // A (128); each 32 columns then hold their part of P in the first 16
 constexpr uint32_t kColO = 128, kColQS = 256, kColD = 384;
 
 constexpr uint32_t kTransA = 1u << 15, kTransB = 1u << 16;  // MN-major operands
@@ -111,10 +116,10 @@ __device__ __forceinline__ float ex2(float x) {
 
 // MN-major operand with the 128-byte swizzle: 128-byte rows hold 64 elements along M or N, eight
 // rows (along K) make a 1024-byte group; `lbo` = distance between blocks of 64 along M or N.
-__device__ __forceinline__ uint64_t desc_mn(uint32_t saddr) {
+__device__ __forceinline__ uint64_t desc_mn(uint32_t saddr, uint32_t lbo = kHalf) {
     uint64_t d = 0;
     d |= (uint64_t)((saddr >> 4) & 0x3FFFu);
-    d |= (uint64_t)(kHalf >> 4) << 16;
+    d |= (uint64_t)(lbo >> 4) << 16;
     d |= (uint64_t)(1024 >> 4) << 32;
     d |= (uint64_t)1 << 46;
     d |= (uint64_t)2 << 61;
@@ -137,6 +142,13 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
         "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
         "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc)
         : "memory");
+}
+
+// 32 bytes to a 32-byte-aligned address.
+__device__ __forceinline__ void store_32(void *dst, const uint32_t *x) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(x[0]), "r"(x[1]), "r"(x[2]),
+                 "r"(x[3]), "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7])
+                 : "memory");
 }
 
 __device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap *map, int x, int y, int z, uint64_t *bar) {
@@ -293,15 +305,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (threadIdx.x == 0) {
         for (int i = 0; i < kRing; ++i) mbar_init(&B->full[i], 1), mbar_init(&B->empty[i], 1);
         mbar_init(&B->scores, 1);
-        mbar_init(&B->p, 4);
-        mbar_init(&B->kp, kStateWarps);
+        mbar_init(&B->p, kOutWarps);
+        for (int i = 0; i < 2; ++i) mbar_init(&B->split[i], kStateWarps), mbar_init(&B->split_free[i], 1);
+        mbar_init(&B->tail, kStateWarps);
         mbar_init(&B->d, 1);
         mbar_init(&B->d_free, kStateWarps);
         mbar_init(&B->s, kStateWarps);
         mbar_init(&B->qs, 1);
         mbar_init(&B->o, 1);
-        mbar_init(&B->o_free, 4);
-        for (int i = 0; i < 2; ++i) mbar_init(&B->gate[i], 1), mbar_init(&B->gate_free[i], kStates ? kStateWarps : kStateWarps + 8);
+        mbar_init(&B->o_free, kOutWarps);
+        for (int i = 0; i < 2; ++i) mbar_init(&B->gate[i], 1), mbar_init(&B->gate_free[i], kStates ? kStateWarps : kStateWarps + kOutWarps);
         mbar_init(&B->drain, 1);
         // the swizzled tiles are laid out for a 1024-byte-aligned base
         B->abort = (smem_addr(smem) & 1023u) != 0;
@@ -318,7 +331,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     const uint32_t tmem = B->tmem;
     const uint32_t base = smem_addr(smem);
-    constexpr int kPer = kStates ? 2 : 3;  // tiles of a chunk: K, (Q,) V
+    constexpr int kPer = kStates ? 2 : 3;  // tiles of a chunk: (Q,) K, V
+    const int last_rows = sp.eos - sp.bos - (nchunks - 1) * kC;  // of the last chunk
     int issued = 0;                        // loads issued (the TMA thread)
 
     if (B->abort) {
@@ -328,7 +342,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (; issued < nchunks * kPer; ++issued) {
                 const int slot = issued % kRing, c = issued / kPer, which = issued - c * kPer;
                 if (issued >= kRing && !wait_one(&B->empty[slot], (issued / kRing - 1) & 1, B, p.status)) break;
-                const CUtensorMap *map = which == 0 ? &map_k : which == kPer - 1 ? &map_v : &map_q;
+                const CUtensorMap *map = which == kPer - 1 ? &map_v : which == kPer - 2 ? &map_k : &map_q;
                 expect_tx(&B->full[slot], kTile);
                 tma_load(base + slot * kTile, map, 0, h, sp.bos + c * kC, &B->full[slot]);
                 tma_load(base + slot * kTile + kHalf, map, 64, h, sp.bos + c * kC, &B->full[slot]);
@@ -336,14 +350,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else if (warp == kWarpMma) {
         if (lane == 0) {
+            int quarter = 0;
             for (int c = 0; c < nchunks; ++c) {
-                const int ik = c * kPer, iq = ik + 1, iv = ik + kPer - 1;
+                const int iq = c * kPer, ik = iq + kPer - 2, iv = ik + 1;
                 const uint32_t k = base + (ik % kRing) * kTile, q = base + (iq % kRing) * kTile, v = base + (iv % kRing) * kTile;
-                const int steps = min(kC, sp.eos - sp.bos - c * kC + 15) >> 4;  // of 16 tokens
+                const int L = c + 1 < nchunks ? kC : last_rows;
                 if (!wait_one(&B->full[ik % kRing], (ik / kRing) & 1, B, p.status)) break;
                 if (!kStates) {
                     if (!wait_one(&B->full[iq % kRing], (iq / kRing) & 1, B, p.status)) break;
-                    if (c > 0 && !wait_one(&B->o, (c - 1) & 1, B, p.status)) break;  // P of the last chunk is read
+                    if (c > 0 && !wait_one(&B->o, (c - 1) & 1, B, p.status)) break;  // P of the last chunk has been read
 #pragma unroll
                     for (int s = 0; s < 8; ++s) {
                         const uint32_t off = (s >> 2) * kHalf + (s & 3) * 32;
@@ -360,23 +375,31 @@ __global__ void __launch_bounds__(kThreads, 1)
                     mma_commit(&B->qs);
                     mma_commit(&B->empty[iq % kRing]);
                 }
-                if (!wait_one(&B->kp, c & 1, B, p.status)) break;
-                if (!wait_one(&B->full[iv % kRing], (iv / kRing) & 1, B, p.status)) break;
-                if (c > 0 && c < updates && !wait_one(&B->d_free, (c - 1) & 1, B, p.status)) break;
-                tc_fence_after();
+                if (L < kC && !wait_one(&B->tail, 0, B, p.status)) break;
                 if (c < updates) {
-                    for (int s = 0; s < steps; ++s)
-                        mma_ss(tmem + kColD, desc_mn(k + s * 2048), desc_mn(v + s * 2048), kIdescD, s > 0);
-                    for (int s = 0; s < steps; ++s)
-                        mma_ss(tmem + kColD, desc_mn(base + kLo + s * 2048), desc_mn(v + s * 2048), kIdescD, true);
+                    if (c > 0 && !wait_one(&B->d_free, (c - 1) & 1, B, p.status)) break;
+                    bool lost = false;
+                    for (int t = 0; t < L; t += kQuarter, ++quarter) {
+                        const int st = quarter & 1;
+                        if (lost = !wait_one(&B->split[st], (quarter >> 1) & 1, B, p.status); lost) break;
+                        tc_fence_after();
+                        const uint32_t hi = base + kSplit + st * kSplitStage;
+#pragma unroll
+                        for (int s = 0; s < 4; ++s)  // hi, hi, lo, lo
+                            mma_ss(tmem + kColD, desc_mn(k + (t >> 4) * 2048 + (s & 1) * 2048),
+                                   desc_mn(hi + (s >> 1) * kSplitLo + (s & 1) * 2048, kSplitHalf), kIdescD, t > 0 || s > 0);
+                        mma_commit(&B->split_free[st]);
+                    }
+                    if (lost) break;
                     mma_commit(&B->d);
                 }
                 mma_commit(&B->empty[ik % kRing]);
+                if (!wait_one(&B->full[iv % kRing], (iv / kRing) & 1, B, p.status)) break;
                 if (!kStates) {
                     if (!wait_one(&B->p, c & 1, B, p.status)) break;
                     tc_fence_after();
-                    for (int s = 0; s < steps; ++s)
-                        mma_ts(tmem + kColO, tmem + kColA + 8 * s, desc_mn(v + s * 2048), kIdescPV, s > 0);
+                    for (int s = 0; s * 16 < L; ++s)
+                        mma_ts(tmem + kColO, tmem + kColA + 32 * (s >> 1) + 8 * (s & 1), desc_mn(v + s * 2048), kIdescPV, s > 0);
                     mma_commit(&B->o);
                 }
                 mma_commit(&B->empty[iv % kRing]);
@@ -412,7 +435,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float p0 = before + g[0], p1 = p0 + g[1], p2 = p1 + g[2], p3 = p2 + g[3];
             *reinterpret_cast<float4 *>(&G->prefix[4 * lane]) = make_float4(p0, p1, p2, p3);
             const float s2 = after + g[3], s1 = s2 + g[2], s0 = s1 + g[1];
-            *reinterpret_cast<float4 *>(&G->suffix[4 * lane]) = make_float4(s0, s1, s2, after);
+            *reinterpret_cast<float4 *>(&G->suffix[4 * lane]) = make_float4(ex2(s0), ex2(s1), ex2(s2), ex2(after));
             // exp2f, not the 2^-22 of the hardware's: this error repeats every chunk and adds up over
             // the chunks that a slowly decaying state remembers
             if (lane == 0) G->decay = exp2f(total);
@@ -420,23 +443,24 @@ __global__ void __launch_bounds__(kThreads, 1)
             run += total;
         }
         if (kStates && lane == 0) a.decay[(size_t)lc * W + w] = run;
-    } else if (warp >= kWarpP && warp < kWarpO && !kStates) {
-        const int quad = warp & 3, row = 32 * quad + lane;
-        const uint32_t lanes = tmem + ((uint32_t)(32 * quad) << 16) + kColA;
+    } else if (warp >= kWarpO && warp < kWarpS && !kStates) {
+        const int quad = warp & 3, half = (warp - kWarpO) >> 2, row = 32 * quad + lane;
+        const uint32_t lanes = tmem + ((uint32_t)(32 * quad) << 16);
+        const bool wide = (reinterpret_cast<uintptr_t>(p.out) & 31) == 0;
         for (int c = 0; c < nchunks; ++c) {
             const Gates *G = reinterpret_cast<const Gates *>(smem + kGates) + (c & 1);
             if (!wait_warp(&B->gate[c & 1], (c >> 1) & 1, B, p.status)) break;
+            const float gi = G->prefix[row], lam = p.scale * ex2(gi);
             if (!wait_warp(&B->scores, c & 1, B, p.status)) break;
             tc_fence_after();
-            const float gi = G->prefix[row];
-            // columns [32 b, 32 b + 32) of A become columns [16 b, 16 b + 16) of P, which lie under
-            // columns of A already read
-#pragma unroll 1
-            for (int b = 0; b < 4; ++b) {
-                uint32_t pk[16];
+            // this warp's blocks of 32 columns: every other one
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int b = 2 * i + half;
+                float f[16];
                 if (b <= quad) {
                     float s[32];
-                    tmem_ld32(lanes + 32 * b, s);
+                    tmem_ld32(lanes + kColA + 32 * b, s);
                     float e[32];
 #pragma unroll
                     for (int j = 0; j < 32; j += 4) {
@@ -447,49 +471,45 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int j = 0; j < 32; ++j) s[j] = (b < quad || j <= lane) ? s[j] * e[j] : 0.0f;
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) pk[j] = pack_bf16(s[2 * j], s[2 * j + 1]);
+                    for (int j = 0; j < 16; ++j) f[j] = __uint_as_float(pack_bf16(s[2 * j], s[2 * j + 1]));
                 } else {
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) pk[j] = 0;
+                    for (int j = 0; j < 16; ++j) f[j] = 0.0f;
                 }
-                float f[16];
-#pragma unroll
-                for (int j = 0; j < 16; ++j) f[j] = __uint_as_float(pk[j]);
-                tmem_st16(lanes + 16 * b, f);
+                tmem_st16(lanes + kColA + 32 * b, f);
             }
             tmem_wait_st();
             tc_fence_before();
             arrive_warp(&B->p);
             if (lane == 0) mbar_arrive(&B->gate_free[c & 1]);
-        }
-    } else if (warp >= kWarpO && warp < kWarpS && !kStates) {
-        const int quad = warp & 3, row = 32 * quad + lane;
-        const uint32_t lanes = tmem + ((uint32_t)(32 * quad) << 16);
-        for (int c = 0; c < nchunks; ++c) {
-            if (!wait_warp(&B->gate[c & 1], (c >> 1) & 1, B, p.status)) break;
-            const float lam = p.scale * ex2((reinterpret_cast<const Gates *>(smem + kGates) + (c & 1))->prefix[row]);
-            arrive_warp(&B->gate_free[c & 1]);
             if (!wait_warp(&B->o, c & 1, B, p.status)) break;
             tc_fence_after();
-            const int t = sp.bos + c * kC + row;
-            uint4 *const dst = reinterpret_cast<uint4 *>(p.out + ((size_t)t * H + h) * kHeadDim);
-#pragma unroll 1
-            for (int b = 0; b < 8; ++b) {
+            uint32_t pk[32];
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
                 float o[16], x[16];
-                tmem_ld16(lanes + kColO + 16 * b, o);
-                tmem_ld16(lanes + kColQS + 16 * b, x);
+                tmem_ld16(lanes + kColO + 64 * half + 16 * b, o);
+                tmem_ld16(lanes + kColQS + 64 * half + 16 * b, x);
                 tmem_wait_ld();
-                uint32_t pk[8];
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
-                    pk[j] = pack_bf16(fmaf(lam, x[2 * j], p.scale * o[2 * j]), fmaf(lam, x[2 * j + 1], p.scale * o[2 * j + 1]));
-                if (t < sp.eos) {
-                    dst[2 * b] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
-                    dst[2 * b + 1] = make_uint4(pk[4], pk[5], pk[6], pk[7]);
-                }
+                    pk[8 * b + j] =
+                        pack_bf16(fmaf(lam, x[2 * j], p.scale * o[2 * j]), fmaf(lam, x[2 * j + 1], p.scale * o[2 * j + 1]));
             }
             tc_fence_before();
             arrive_warp(&B->o_free);
+            const int t = sp.bos + c * kC + row;
+            if (t < sp.eos) {
+                __nv_bfloat16 *const dst = p.out + ((size_t)t * H + h) * kHeadDim + 64 * half;
+                if (wide) {
+#pragma unroll
+                    for (int b = 0; b < 4; ++b) store_32(dst + 16 * b, pk + 8 * b);
+                } else {
+#pragma unroll
+                    for (int b = 0; b < 8; ++b)
+                        reinterpret_cast<uint4 *>(dst)[b] = make_uint4(pk[4 * b], pk[4 * b + 1], pk[4 * b + 2], pk[4 * b + 3]);
+                }
+            }
         }
     } else if (warp >= kWarpS) {
         const int quad = warp & 3, half = (warp - kWarpS) >> 2, row = 32 * quad + lane;  // row: dk
@@ -520,44 +540,61 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         if (!kStates && nchunks > 0) publish();
         bool ok = true;
-        for (int c = 0; c < nchunks && ok; ++c) {
-            const int ik = c * kPer, iv = ik + kPer - 1;
-            const int L = min(kC, sp.eos - sp.bos - c * kC);
+        int quarter = 0;
+        for (int c = 0; c < nchunks; ++c) {
+            const int ik = c * kPer + kPer - 2, iv = ik + 1;
+            const int L = c + 1 < nchunks ? kC : last_rows;
             const Gates *G = reinterpret_cast<const Gates *>(smem + kGates) + (c & 1);
+            uint8_t *const tile = smem + (iv % kRing) * kTile;
             ok = wait_warp(&B->gate[c & 1], (c >> 1) & 1, B, p.status) &&
-                 wait_warp(&B->full[ik % kRing], (ik / kRing) & 1, B, p.status) &&
-                 (kStates || wait_warp(&B->scores, c & 1, B, p.status));  // K has been read as it is
+                 wait_warp(&B->full[iv % kRing], (iv / kRing) & 1, B, p.status);
             if (!ok) break;
-            if (c < updates) {
-                uint8_t *const tile = smem + (ik % kRing) * kTile, *const lo = smem + kLo;
-#pragma unroll 2
-                for (int i = 0; i < 8; ++i) {
-                    const int x = tid + kStateThreads * i, t = (x & 1023) >> 3;
-                    uint4 *const at = reinterpret_cast<uint4 *>(tile + x * 16);
-                    const uint4 in = *at;
-                    const float f = ex2(G->suffix[t]);
-                    const uint32_t u[4] = {in.x, in.y, in.z, in.w};
-                    uint32_t hi[4], rest[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float y0 = __uint_as_float(u[e] << 16) * f, y1 = __uint_as_float(u[e] & 0xffff0000u) * f;
-                        hi[e] = pack_bf16(y0, y1);
-                        rest[e] = pack_bf16(y0 - __uint_as_float(hi[e] << 16), y1 - __uint_as_float(hi[e] & 0xffff0000u));
-                        if (t >= L) hi[e] = rest[e] = 0;  // another sequence's key
-                    }
-                    *at = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                    *reinterpret_cast<uint4 *>(lo + x * 16) = make_uint4(rest[0], rest[1], rest[2], rest[3]);
-                }
-            }
-            if (L & 15) {  // another sequence's values inside the last 16 tokens that the products read
-                ok = wait_warp(&B->full[iv % kRing], (iv / kRing) & 1, B, p.status);
+            if (L < kC) {
+                // rows past the last token hold another sequence's keys and values, which a zero in the
+                // other operand does not silence if they are not finite
+                ok = wait_warp(&B->full[ik % kRing], (ik / kRing) & 1, B, p.status);
                 if (!ok) break;
-                for (int x = tid; x < 2048; x += kStateThreads)
-                    if (((x & 1023) >> 3) >= L) *reinterpret_cast<uint4 *>(smem + (iv % kRing) * kTile + x * 16) = make_uint4(0, 0, 0, 0);
+                for (int x = tid; x < 4096; x += kStateThreads)
+                    if (((x & 1023) >> 3) >= L)
+                        *reinterpret_cast<uint4 *>((x < 2048 ? tile : smem + (ik % kRing) * kTile - 32768) + x * 16) = make_uint4(0, 0, 0, 0);
+                fence_async_smem();
+                arrive_warp(&B->tail);
+            }
+            if (c < updates) {
+                for (int t0 = 0; t0 < L; t0 += kQuarter, ++quarter) {
+                    const int st = quarter & 1, t = t0 + (tid >> 3);
+                    const float f = G->suffix[t];
+                    uint8_t *const to = smem + kSplit + st * kSplitStage + tid * 16;
+                    uint4 in[2];
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        in[i] = *reinterpret_cast<const uint4 *>(tile + i * kHalf + t0 * 128 + tid * 16);
+                        if (t >= L) in[i] = make_uint4(0, 0, 0, 0);
+                    }
+                    if (quarter >= 2) {
+                        ok = wait_warp(&B->split_free[st], ((quarter >> 1) - 1) & 1, B, p.status);
+                        if (!ok) break;
+                    }
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const uint32_t u[4] = {in[i].x, in[i].y, in[i].z, in[i].w};
+                        uint32_t hi[4], rest[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float y0 = __uint_as_float(u[e] << 16) * f, y1 = __uint_as_float(u[e] & 0xffff0000u) * f;
+                            hi[e] = pack_bf16(y0, y1);
+                            rest[e] = pack_bf16(y0 - __uint_as_float(hi[e] << 16), y1 - __uint_as_float(hi[e] & 0xffff0000u));
+                        }
+                        *reinterpret_cast<uint4 *>(to + i * kSplitHalf) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                        *reinterpret_cast<uint4 *>(to + kSplitLo + i * kSplitHalf) = make_uint4(rest[0], rest[1], rest[2], rest[3]);
+                    }
+                    fence_async_smem();
+                    arrive_warp(&B->split[st]);
+                }
+                if (!ok) break;
             }
             const float decay = G->decay;
-            fence_async_smem();
-            arrive_warp(&B->kp);
+            __syncwarp();
             if (lane == 0) mbar_arrive(&B->gate_free[c & 1]);
             if (c < updates) {
                 ok = wait_warp(&B->d, c & 1, B, p.status);
