@@ -99,6 +99,7 @@ static_assert(kSmem <= 227 * 1024, "one CTA per SM");
 
 // ---- tensor memory (columns)
 constexpr uint32_t kTmemCols = 512;
+// (all 512 are allocated, so the base is column 0)
 constexpr uint32_t kColA = 0;  // A (128); each 32 columns then hold their part of P in the first 16
 constexpr uint32_t kColO = 128, kColQS = 256, kColD = 384;
 
@@ -114,33 +115,46 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
-// MN-major operand with the 128-byte swizzle: 128-byte rows hold 64 elements along M or N, eight
-// rows (along K) make a 1024-byte group; `lbo` = distance between blocks of 64 along M or N.
-__device__ __forceinline__ uint64_t desc_mn(uint32_t saddr, uint32_t lbo = kHalf) {
-    uint64_t d = 0;
-    d |= (uint64_t)((saddr >> 4) & 0x3FFFu);
-    d |= (uint64_t)(lbo >> 4) << 16;
-    d |= (uint64_t)(1024 >> 4) << 32;
-    d |= (uint64_t)1 << 46;
-    d |= (uint64_t)2 << 61;
-    return d;
+// Operand descriptors: the constant part plus the address in 16-byte units (under 2^14 for any
+// address in shared memory, so an offset adds without carry).
+//   K-major, 128-byte swizzle: smem_desc_sw128.
+//   MN-major, 128-byte swizzle: 128-byte rows hold 64 elements along M or N, eight rows (along K)
+//   make a 1024-byte group; `lbo` = distance between blocks of 64 along M or N.
+__device__ __forceinline__ constexpr uint64_t desc_mn(uint32_t lbo) {
+    return (uint64_t)(lbo >> 4) << 16 | (uint64_t)(1024 >> 4) << 32 | (uint64_t)1 << 46 | (uint64_t)2 << 61;
 }
+constexpr uint64_t kDescK = (uint64_t)1 << 16 | (uint64_t)(1024 >> 4) << 32 | (uint64_t)1 << 46 | (uint64_t)2 << 61;
+constexpr uint64_t kDescMn = desc_mn(kHalf), kDescSplit = desc_mn(kSplitHalf);
 
+__device__ __forceinline__ uint64_t at(uint64_t desc, uint32_t saddr) { return desc | (saddr >> 4); }
+
+// Every lane of the warp calls these with the same operands (which keeps them in uniform
+// registers); one elected lane issues, always the same one, so that its commits follow its MMAs.
 __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
+        "{\n\t.reg .pred p, e;\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
         "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc)
         : "memory");
 }
 
 __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool acc) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
+        "{\n\t.reg .pred p, e;\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
         "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc)
+        : "memory");
+}
+
+__device__ __forceinline__ void commit(uint64_t *bar) {
+    asm volatile(
+        "{\n\t.reg .pred e;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_addr(bar))
         : "memory");
 }
 
@@ -275,7 +289,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     extern __shared__ __align__(1024) uint8_t smem[];
     const LinearPrefillArgs &p = a.p;
     Bars *B = reinterpret_cast<Bars *>(smem + kBars);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, H = p.num_heads;
+    // the shuffle tells the compiler that the role is one for the warp
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31, H = p.num_heads;
     const int W = a.plan.wins;
     // the item: a whole chain, or window w of windowed chain lc
     int pos = blockIdx.x, w = 0, lc = -1;
@@ -329,7 +344,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     fence_async_smem();  // the ranking's scratch lies where the first tiles go
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = B->tmem;
+    constexpr uint32_t tmem = 0;
+    if (threadIdx.x == 0 && B->tmem != 0) {
+        report_error(p.status, KDA_ERR_CUDA, 1);
+        B->abort = 1;
+    }
+    __syncthreads();
     const uint32_t base = smem_addr(smem);
     constexpr int kPer = kStates ? 2 : 3;  // tiles of a chunk: (Q,) K, V
     const int last_rows = sp.eos - sp.bos - (nchunks - 1) * kC;  // of the last chunk
@@ -349,64 +369,71 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
     } else if (warp == kWarpMma) {
-        if (lane == 0) {
-            int quarter = 0;
-            for (int c = 0; c < nchunks; ++c) {
-                const int iq = c * kPer, ik = iq + kPer - 2, iv = ik + 1;
-                const uint32_t k = base + (ik % kRing) * kTile, q = base + (iq % kRing) * kTile, v = base + (iv % kRing) * kTile;
-                const int L = c + 1 < nchunks ? kC : last_rows;
-                if (!wait_one(&B->full[ik % kRing], (ik / kRing) & 1, B, p.status)) break;
-                if (!kStates) {
-                    if (!wait_one(&B->full[iq % kRing], (iq / kRing) & 1, B, p.status)) break;
-                    if (c > 0 && !wait_one(&B->o, (c - 1) & 1, B, p.status)) break;  // P of the last chunk has been read
+        int quarter = 0;
+        for (int c = 0; c < nchunks; ++c) {
+            const int iq = c * kPer, ik = iq + kPer - 2, iv = ik + 1;
+            const uint32_t k = base + (ik % kRing) * kTile, q = base + (iq % kRing) * kTile, v = base + (iv % kRing) * kTile;
+            const int L = c + 1 < nchunks ? kC : last_rows;
+            if (!wait_warp(&B->full[ik % kRing], (ik / kRing) & 1, B, p.status)) break;
+            if (!kStates) {
+                if (!wait_warp(&B->full[iq % kRing], (iq / kRing) & 1, B, p.status)) break;
+                if (c > 0 && !wait_warp(&B->o, (c - 1) & 1, B, p.status)) break;  // P of the last chunk has been read
+                const uint64_t dq = at(kDescK, q), dk = at(kDescK, k);
 #pragma unroll
-                    for (int s = 0; s < 8; ++s) {
-                        const uint32_t off = (s >> 2) * kHalf + (s & 3) * 32;
-                        mma_ss(tmem + kColA, smem_desc_sw128(q + off), smem_desc_sw128(k + off), kIdescQK, s > 0);
-                    }
-                    mma_commit(&B->scores);
-                    if (!wait_one(&B->s, c & 1, B, p.status)) break;
-                    if (c > 0 && !wait_one(&B->o_free, (c - 1) & 1, B, p.status)) break;
+                for (int s = 0; s < 8; ++s) {
+                    const uint32_t off = ((s >> 2) * kHalf + (s & 3) * 32) >> 4;
+                    mma_ss(tmem + kColA, dq + off, dk + off, kIdescQK, s > 0);
+                }
+                commit(&B->scores);
+                if (!wait_warp(&B->s, c & 1, B, p.status)) break;
+                if (c > 0 && !wait_warp(&B->o_free, (c - 1) & 1, B, p.status)) break;
+                tc_fence_after();
+                const uint64_t ds = at(kDescMn, base + kS);
+#pragma unroll
+                for (int s = 0; s < 8; ++s)
+                    mma_ss(tmem + kColQS, dq + (((s >> 2) * kHalf + (s & 3) * 32) >> 4), ds + s * 128, kIdescQS, s > 0);
+                commit(&B->qs);
+                commit(&B->empty[iq % kRing]);
+            }
+            if (L < kC && !wait_warp(&B->tail, 0, B, p.status)) break;
+            if (c < updates) {
+                if (c > 0 && !wait_warp(&B->d_free, (c - 1) & 1, B, p.status)) break;
+                bool lost = false;
+                for (int t = 0; t < L; t += kQuarter, ++quarter) {
+                    const int st = quarter & 1;
+                    lost = !wait_warp(&B->split[st], (quarter >> 1) & 1, B, p.status);
+                    if (lost) break;
                     tc_fence_after();
+                    const uint64_t da = at(kDescMn, k + t * 128), db = at(kDescSplit, base + kSplit + st * kSplitStage);
+#pragma unroll
+                    for (int s = 0; s < 4; ++s)  // hi, hi, lo, lo
+                        mma_ss(tmem + kColD, da + (s & 1) * 128, db + (((s >> 1) * kSplitLo + (s & 1) * 2048) >> 4), kIdescD,
+                               t > 0 || s > 0);
+                    commit(&B->split_free[st]);
+                }
+                if (lost) break;
+                commit(&B->d);
+            }
+            commit(&B->empty[ik % kRing]);
+            if (!wait_warp(&B->full[iv % kRing], (iv / kRing) & 1, B, p.status)) break;
+            if (!kStates) {
+                if (!wait_warp(&B->p, c & 1, B, p.status)) break;
+                tc_fence_after();
+                const uint64_t dv = at(kDescMn, v);
+                if (L == kC) {
 #pragma unroll
                     for (int s = 0; s < 8; ++s)
-                        mma_ss(tmem + kColQS, smem_desc_sw128(q + (s >> 2) * kHalf + (s & 3) * 32),
-                               desc_mn(base + kS + s * 2048), kIdescQS, s > 0);
-                    mma_commit(&B->qs);
-                    mma_commit(&B->empty[iq % kRing]);
-                }
-                if (L < kC && !wait_one(&B->tail, 0, B, p.status)) break;
-                if (c < updates) {
-                    if (c > 0 && !wait_one(&B->d_free, (c - 1) & 1, B, p.status)) break;
-                    bool lost = false;
-                    for (int t = 0; t < L; t += kQuarter, ++quarter) {
-                        const int st = quarter & 1;
-                        if (lost = !wait_one(&B->split[st], (quarter >> 1) & 1, B, p.status); lost) break;
-                        tc_fence_after();
-                        const uint32_t hi = base + kSplit + st * kSplitStage;
-#pragma unroll
-                        for (int s = 0; s < 4; ++s)  // hi, hi, lo, lo
-                            mma_ss(tmem + kColD, desc_mn(k + (t >> 4) * 2048 + (s & 1) * 2048),
-                                   desc_mn(hi + (s >> 1) * kSplitLo + (s & 1) * 2048, kSplitHalf), kIdescD, t > 0 || s > 0);
-                        mma_commit(&B->split_free[st]);
-                    }
-                    if (lost) break;
-                    mma_commit(&B->d);
-                }
-                mma_commit(&B->empty[ik % kRing]);
-                if (!wait_one(&B->full[iv % kRing], (iv / kRing) & 1, B, p.status)) break;
-                if (!kStates) {
-                    if (!wait_one(&B->p, c & 1, B, p.status)) break;
-                    tc_fence_after();
+                        mma_ts(tmem + kColO, tmem + kColA + 32 * (s >> 1) + 8 * (s & 1), dv + s * 128, kIdescPV, s > 0);
+                } else {
                     for (int s = 0; s * 16 < L; ++s)
-                        mma_ts(tmem + kColO, tmem + kColA + 32 * (s >> 1) + 8 * (s & 1), desc_mn(v + s * 2048), kIdescPV, s > 0);
-                    mma_commit(&B->o);
+                        mma_ts(tmem + kColO, tmem + kColA + 32 * (s >> 1) + 8 * (s & 1), dv + s * 128, kIdescPV, s > 0);
                 }
-                mma_commit(&B->empty[iv % kRing]);
+                commit(&B->o);
             }
-            mma_commit(&B->drain);  // every earlier commit has reached its barrier when this one has
-            mbar_wait(&B->drain, 0);
+            commit(&B->empty[iv % kRing]);
         }
+        commit(&B->drain);  // every earlier commit has reached its barrier when this one has
+        mbar_wait(&B->drain, 0);
     } else if (warp == kWarpGate) {
         float run = 0.0f;  // total decay of the window so far
         for (int c = 0; c < nchunks; ++c) {
@@ -633,7 +660,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncthreads();
     }
     tc_fence_after();
-    if (warp == kWarpAlloc) tmem_dealloc(tmem, kTmemCols);
+    if (warp == kWarpAlloc) tmem_dealloc(B->tmem, kTmemCols);
     // whatever follows this grid on the stream also follows the launches that it may overlap
     pdl_wait();
 }
