@@ -17,13 +17,21 @@
 // from chunk to chunk is S' = exp(G_last) S + D and its rounding into the next chunk's operand.
 //
 // One CTA per chain (or window of a chain), 20 warps in five roles:
-//   warp 0        TMA: Q, K, V tiles of a chunk (128-byte swizzle) into a ring of five 32 KiB tiles
+//   warp 0        a chunk's prefix and suffix sums of g, and its TMA loads: Q, K, V tiles (128-byte
+//                 swizzle) into a ring of five 32 KiB tiles
 //   warp 1        issues every MMA: A, Q S, D by quarters of 32 tokens (hi then lo), P V
-//   warp 2        the chunk's prefix and suffix sums of g
-//   warps 4-11    A -> P in place in tensor memory, then O: both accumulators -> BF16 -> global
-//   warps 12-19   V -> hi, lo by quarters into a ring of two; S in registers (row dk, 64 columns a thread)
-// The values are decayed, not the keys, because V is only read by the last product of the chunk: the
-// split runs beside the scores instead of behind them.
+//   warps 4-11    A -> P in place in tensor memory; the second half of V -> hi, lo; O: both accumulators
+//                 -> BF16 -> the tile that held V -> TMA store
+//   warps 12-19   S in registers (row dk, 64 columns a thread): the update and the operand of Q S; the
+//                 first half of the next chunk's V -> hi, lo
+// hi and lo pass through a ring of two quarters. The values are decayed, not the keys, because V is only
+// read by the last product of the chunk, so that the split needs no scores; it is shared out so that
+// each group does its part where it would wait for the tensor core. (All of it on warps 12-19 made their
+// work the longest chain of a chunk, two extra warps took 1.5k cycles a quarter, and four extra warps
+// left too few registers for the state.) O leaves through shared memory because a
+// thread's row-wise 32-byte stores (32 rows an instruction) kept the load/store unit busy for 2k
+// cycles a chunk, during which the MMAs' operand reads took four times their time (2.56 ms at
+// 8 x 16384 x 96 heads).
 // The suffix sums G_last - G_j are scanned from the end, not formed as differences, so that a
 // strong decay early in a chunk costs the later tokens' weights no precision. A log decay below
 // -128 counts as -128 (both decay to zero in FP32), which keeps the sums finite.
@@ -56,9 +64,10 @@ constexpr int kRing = 5;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kMinLogDecay = -128.0f;
 
-constexpr int kWarpMma = 1, kWarpGate = 2, kWarpAlloc = 3, kWarpO = 4, kWarpS = 12;
+constexpr int kWarpMma = 1, kWarpAlloc = 2, kWarpO = 4, kWarpS = 12;
 constexpr int kOutWarps = 8, kStateWarps = 8;
-constexpr int kStateThreads = kStateWarps * 32;
+constexpr int kGroup = 256;  // threads of each of the two groups
+static_assert(kOutWarps * 32 == kGroup && kStateWarps * 32 == kGroup, "both groups split quarters");
 constexpr int kThreads = (kWarpS + kStateWarps) * 32;
 
 struct Gates {
@@ -80,6 +89,7 @@ struct Bars {
     uint64_t qs;       // Q S done: the S operand is free
     uint64_t o;        // P V done (and everything before it)
     uint64_t o_free;   // both output accumulators read (8 warps)
+    uint64_t stored[2];  // the chunk's V tile, reused for O, has been read by the stores (8 warps)
     uint64_t gate[2], gate_free[2];
     uint64_t drain;
     uint32_t tmem;
@@ -158,19 +168,18 @@ __device__ __forceinline__ void commit(uint64_t *bar) {
         : "memory");
 }
 
-// 32 bytes to a 32-byte-aligned address.
-__device__ __forceinline__ void store_32(void *dst, const uint32_t *x) {
-    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(x[0]), "r"(x[1]), "r"(x[2]),
-                 "r"(x[3]), "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7])
-                 : "memory");
-}
-
 __device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap *map, int x, int y, int z, uint64_t *bar) {
     asm volatile(
         "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
             dst),
         "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_addr(bar))
         : "memory");
+}
+
+__device__ __forceinline__ void tma_store(const CUtensorMap *map, uint32_t src, int x, int y, int z) {
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(map), "r"(x),
+                 "r"(y), "r"(z), "r"(src)
+                 : "memory");
 }
 
 __device__ __forceinline__ void expect_tx(uint64_t *bar, uint32_t bytes) {
@@ -281,11 +290,45 @@ __device__ __forceinline__ Span span_of(const LinearPrefillArgs &a, int n, int w
     return s;
 }
 
+// hi and lo of 32 tokens of V, by the 256 threads of a group: row t of the quarter at `tile` (eight
+// threads a row, a thread the same 16 bytes of both halves) times its factor f, rows past the last
+// token as zeros, into the split stage at `to`.
+__device__ __forceinline__ void split_quarter(const uint8_t *tile, uint8_t *to, float f, bool live) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        uint4 in = *reinterpret_cast<const uint4 *>(tile + i * kHalf);
+        if (!live) in = make_uint4(0, 0, 0, 0);
+        const uint32_t u[4] = {in.x, in.y, in.z, in.w};
+        uint32_t hi[4], rest[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float y0 = __uint_as_float(u[e] << 16) * f, y1 = __uint_as_float(u[e] & 0xffff0000u) * f;
+            hi[e] = pack_bf16(y0, y1);
+            rest[e] = pack_bf16(y0 - __uint_as_float(hi[e] << 16), y1 - __uint_as_float(hi[e] & 0xffff0000u));
+        }
+        *reinterpret_cast<uint4 *>(to + i * kSplitHalf) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        *reinterpret_cast<uint4 *>(to + kSplitLo + i * kSplitHalf) = make_uint4(rest[0], rest[1], rest[2], rest[3]);
+    }
+}
+
+// Parity of the release of tile i on its slot: V tiles of the full kernel are released through `stored`,
+// so the slot's `empty` barrier has one phase for each of its other tiles up to i.
+__device__ __forceinline__ uint32_t empty_parity(int i, bool with_v) {
+    const int uses = i / kRing;  // earlier tiles on the slot: i % kRing + kRing u for u < uses
+    if (with_v) return uses & 1;
+    // tile j is a V tile when j % 3 == 2; over three uses of a slot (15 tiles) exactly one is
+    const int first = i % kRing;
+    int vs = uses / 3;
+    for (int u = uses / 3 * 3; u < uses; ++u) vs += (first + kRing * u) % 3 == 2;
+    return (uses - vs) & 1;
+}
+
 // kStates: only the state update, from zero, over the windows of the windowed chains but the last.
 template <bool kStates>
 __global__ void __launch_bounds__(kThreads, 1)
     kda_linear_chunk_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap map_q,
-                            const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v) {
+                            const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
+                            const __grid_constant__ CUtensorMap map_o) {
     extern __shared__ __align__(1024) uint8_t smem[];
     const LinearPrefillArgs &p = a.p;
     Bars *B = reinterpret_cast<Bars *>(smem + kBars);
@@ -321,7 +364,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < kRing; ++i) mbar_init(&B->full[i], 1), mbar_init(&B->empty[i], 1);
         mbar_init(&B->scores, 1);
         mbar_init(&B->p, kOutWarps);
-        for (int i = 0; i < 2; ++i) mbar_init(&B->split[i], kStateWarps), mbar_init(&B->split_free[i], 1);
+        for (int i = 0; i < 2; ++i) mbar_init(&B->split[i], kGroup / 32), mbar_init(&B->split_free[i], 1);
+        for (int i = 0; i < 2; ++i) mbar_init(&B->stored[i], kOutWarps);
         mbar_init(&B->tail, kStateWarps);
         mbar_init(&B->d, 1);
         mbar_init(&B->d_free, kStateWarps);
@@ -329,7 +373,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(&B->qs, 1);
         mbar_init(&B->o, 1);
         mbar_init(&B->o_free, kOutWarps);
-        for (int i = 0; i < 2; ++i) mbar_init(&B->gate[i], 1), mbar_init(&B->gate_free[i], kStates ? kStateWarps : kStateWarps + kOutWarps);
+        for (int i = 0; i < 2; ++i) mbar_init(&B->gate[i], 1), mbar_init(&B->gate_free[i], kStateWarps + kOutWarps);
         mbar_init(&B->drain, 1);
         // the swizzled tiles are laid out for a 1024-byte-aligned base
         B->abort = (smem_addr(smem) & 1023u) != 0;
@@ -353,21 +397,84 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t base = smem_addr(smem);
     constexpr int kPer = kStates ? 2 : 3;  // tiles of a chunk: (Q,) K, V
     const int last_rows = sp.eos - sp.bos - (nchunks - 1) * kC;  // of the last chunk
-    int issued = 0;                        // loads issued (the TMA thread)
+    int issued = 0;                        // loads issued (warp 0)
+    // Quarters [q0, q0 + 2) of chunk c, those that it has, by the 256 threads of a group (thread tid); the
+    // quarters of all chunks count through the ring of two stages (only the last chunk may have fewer
+    // than four).
+    auto split = [&](int c, int q0, int tid) {
+        if (c >= updates) return true;
+        const int L = c + 1 < nchunks ? kC : last_rows;
+        const Gates *G = reinterpret_cast<const Gates *>(smem + kGates) + (c & 1);
+        const uint8_t *const tile = smem + ((c * kPer + kPer - 1) % kRing) * kTile;
+#pragma unroll 1
+        for (int q = q0; q < q0 + 2 && q * kQuarter < L; ++q) {
+            const int use = 4 * c + q, st = use & 1, t = q * kQuarter + (tid >> 3);
+            if (use >= 2 && !wait_warp(&B->split_free[st], ((use >> 1) - 1) & 1, B, p.status)) return false;
+            split_quarter(tile + q * kQuarter * 128 + tid * 16, smem + kSplit + st * kSplitStage + tid * 16, G->suffix[t], t < L);
+            fence_async_smem();
+            arrive_warp(&B->split[st]);
+        }
+        return true;
+    };
 
     if (B->abort) {
         // nothing has started
     } else if (warp == 0) {
-        if (lane == 0) {
-            for (; issued < nchunks * kPer; ++issued) {
-                const int slot = issued % kRing, c = issued / kPer, which = issued - c * kPer;
-                if (issued >= kRing && !wait_one(&B->empty[slot], (issued / kRing - 1) & 1, B, p.status)) break;
-                const CUtensorMap *map = which == kPer - 1 ? &map_v : which == kPer - 2 ? &map_k : &map_q;
-                expect_tx(&B->full[slot], kTile);
-                tma_load(base + slot * kTile, map, 0, h, sp.bos + c * kC, &B->full[slot]);
-                tma_load(base + slot * kTile + kHalf, map, 64, h, sp.bos + c * kC, &B->full[slot]);
+        float run = 0.0f;  // total decay of the window so far
+        for (int c = 0; c < nchunks; ++c) {
+            const int t0 = sp.bos + c * kC, L = min(kC, sp.eos - t0), b = c & 1;
+            float g[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int t = 4 * lane + e;
+                g[e] = t < L ? p.log_decay[(size_t)(t0 + t) * p.decay_token_stride + h] : 0.0f;
             }
+            bool ok = true;
+            for (int which = 0; which < kPer; ++which, ++issued) {
+                const int slot = issued % kRing;
+                if (issued >= kRing) {  // the tile five loads ago has been read
+                    const int before = issued - kRing, cb = before / kPer;
+                    const bool is_v = !kStates && before - cb * kPer == kPer - 1;  // then also as O
+                    ok = is_v ? wait_warp(&B->stored[cb & 1], (cb >> 1) & 1, B, p.status)
+                              : wait_warp(&B->empty[slot], empty_parity(before, kStates), B, p.status);
+                    if (!ok) break;
+                }
+                const CUtensorMap *map = which == kPer - 1 ? &map_v : which == kPer - 2 ? &map_k : &map_q;
+                if (lane == 0) {
+                    expect_tx(&B->full[slot], kTile);
+                    tma_load(base + slot * kTile, map, 0, h, t0, &B->full[slot]);
+                    tma_load(base + slot * kTile + kHalf, map, 64, h, t0, &B->full[slot]);
+                }
+                __syncwarp();
+            }
+            if (!ok) break;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) g[e] = (g[e] < kMinLogDecay ? kMinLogDecay : g[e]) * kLog2e;
+            const float mine = (g[0] + g[1]) + (g[2] + g[3]);
+            float up = mine, down = mine;  // inclusive over the lanes before, and after
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const float x = __shfl_up_sync(0xffffffffu, up, o), y = __shfl_down_sync(0xffffffffu, down, o);
+                if (lane >= o) up += x;
+                if (lane + o < 32) down += y;
+            }
+            float before = __shfl_up_sync(0xffffffffu, up, 1), after = __shfl_down_sync(0xffffffffu, down, 1);
+            if (lane == 0) before = 0.0f;
+            if (lane == 31) after = 0.0f;
+            const float total = __shfl_sync(0xffffffffu, down, 0);
+            if (c >= 2 && !wait_warp(&B->gate_free[b], ((c >> 1) - 1) & 1, B, p.status)) break;
+            Gates *G = reinterpret_cast<Gates *>(smem + kGates) + b;
+            const float p0 = before + g[0], p1 = p0 + g[1], p2 = p1 + g[2], p3 = p2 + g[3];
+            *reinterpret_cast<float4 *>(&G->prefix[4 * lane]) = make_float4(p0, p1, p2, p3);
+            const float s2 = after + g[3], s1 = s2 + g[2], s0 = s1 + g[1];
+            *reinterpret_cast<float4 *>(&G->suffix[4 * lane]) = make_float4(ex2(s0), ex2(s1), ex2(s2), ex2(after));
+            // exp2f, not the 2^-22 of the hardware's: this error repeats every chunk and adds up over
+            // the chunks that a slowly decaying state remembers
+            if (lane == 0) G->decay = exp2f(total);
+            arrive_warp(&B->gate[b]);
+            run += total;
         }
+        if (kStates && lane == 0) a.decay[(size_t)lc * W + w] = run;
     } else if (warp == kWarpMma) {
         int quarter = 0;
         for (int c = 0; c < nchunks; ++c) {
@@ -430,53 +537,25 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 commit(&B->o);
             }
-            commit(&B->empty[iv % kRing]);
+            if (kStates) commit(&B->empty[iv % kRing]);
         }
         commit(&B->drain);  // every earlier commit has reached its barrier when this one has
         mbar_wait(&B->drain, 0);
-    } else if (warp == kWarpGate) {
-        float run = 0.0f;  // total decay of the window so far
-        for (int c = 0; c < nchunks; ++c) {
-            const int t0 = sp.bos + c * kC, L = min(kC, sp.eos - t0), b = c & 1;
-            float g[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int t = 4 * lane + e;
-                float x = t < L ? p.log_decay[(size_t)(t0 + t) * p.decay_token_stride + h] : 0.0f;
-                g[e] = (x < kMinLogDecay ? kMinLogDecay : x) * kLog2e;
-            }
-            const float mine = (g[0] + g[1]) + (g[2] + g[3]);
-            float up = mine, down = mine;  // inclusive over the lanes before, and after
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const float x = __shfl_up_sync(0xffffffffu, up, o), y = __shfl_down_sync(0xffffffffu, down, o);
-                if (lane >= o) up += x;
-                if (lane + o < 32) down += y;
-            }
-            float before = __shfl_up_sync(0xffffffffu, up, 1), after = __shfl_down_sync(0xffffffffu, down, 1);
-            if (lane == 0) before = 0.0f;
-            if (lane == 31) after = 0.0f;
-            const float total = __shfl_sync(0xffffffffu, down, 0);
-            if (c >= 2 && !wait_warp(&B->gate_free[b], ((c >> 1) - 1) & 1, B, p.status)) break;
-            Gates *G = reinterpret_cast<Gates *>(smem + kGates) + b;
-            const float p0 = before + g[0], p1 = p0 + g[1], p2 = p1 + g[2], p3 = p2 + g[3];
-            *reinterpret_cast<float4 *>(&G->prefix[4 * lane]) = make_float4(p0, p1, p2, p3);
-            const float s2 = after + g[3], s1 = s2 + g[2], s0 = s1 + g[1];
-            *reinterpret_cast<float4 *>(&G->suffix[4 * lane]) = make_float4(ex2(s0), ex2(s1), ex2(s2), ex2(after));
-            // exp2f, not the 2^-22 of the hardware's: this error repeats every chunk and adds up over
-            // the chunks that a slowly decaying state remembers
-            if (lane == 0) G->decay = exp2f(total);
-            arrive_warp(&B->gate[b]);
-            run += total;
-        }
-        if (kStates && lane == 0) a.decay[(size_t)lc * W + w] = run;
-    } else if (warp >= kWarpO && warp < kWarpS && !kStates) {
+    } else if (warp < kWarpO) {
+        // idle
+    } else if (warp < kWarpS) {
         const int quad = warp & 3, half = (warp - kWarpO) >> 2, row = 32 * quad + lane;
+        const int tid = threadIdx.x - kWarpO * 32;
         const uint32_t lanes = tmem + ((uint32_t)(32 * quad) << 16);
-        const bool wide = (reinterpret_cast<uintptr_t>(p.out) & 31) == 0;
         for (int c = 0; c < nchunks; ++c) {
             const Gates *G = reinterpret_cast<const Gates *>(smem + kGates) + (c & 1);
+            const int iv = c * kPer + kPer - 1;
             if (!wait_warp(&B->gate[c & 1], (c >> 1) & 1, B, p.status)) break;
+            if (kStates) {
+                if (!wait_warp(&B->full[iv % kRing], (iv / kRing) & 1, B, p.status) || !split(c, 2, tid)) break;
+                arrive_warp(&B->gate_free[c & 1]);
+                continue;
+            }
             const float gi = G->prefix[row], lam = p.scale * ex2(gi);
             if (!wait_warp(&B->scores, c & 1, B, p.status)) break;
             tc_fence_after();
@@ -485,62 +564,77 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int i = 0; i < 2; ++i) {
                 const int b = 2 * i + half;
                 float f[16];
+#pragma unroll
+                for (int j = 0; j < 16; ++j) f[j] = 0.0f;
                 if (b <= quad) {
-                    float s[32];
-                    tmem_ld32(lanes + kColA + 32 * b, s);
-                    float e[32];
 #pragma unroll
-                    for (int j = 0; j < 32; j += 4) {
-                        const float4 gj = *reinterpret_cast<const float4 *>(&G->prefix[32 * b + j]);
-                        e[j] = ex2(gi - gj.x), e[j + 1] = ex2(gi - gj.y), e[j + 2] = ex2(gi - gj.z), e[j + 3] = ex2(gi - gj.w);
+                    for (int u = 0; u < 2; ++u) {
+                        float s[16], e[16];
+                        tmem_ld16(lanes + kColA + 32 * b + 16 * u, s);
+#pragma unroll
+                        for (int j = 0; j < 16; j += 4) {
+                            const float4 gj = *reinterpret_cast<const float4 *>(&G->prefix[32 * b + 16 * u + j]);
+                            e[j] = ex2(gi - gj.x), e[j + 1] = ex2(gi - gj.y), e[j + 2] = ex2(gi - gj.z), e[j + 3] = ex2(gi - gj.w);
+                        }
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) s[j] = (b < quad || 16 * u + j <= lane) ? s[j] * e[j] : 0.0f;
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) f[8 * u + j] = __uint_as_float(pack_bf16(s[2 * j], s[2 * j + 1]));
                     }
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) s[j] = (b < quad || j <= lane) ? s[j] * e[j] : 0.0f;
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) f[j] = __uint_as_float(pack_bf16(s[2 * j], s[2 * j + 1]));
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) f[j] = 0.0f;
                 }
                 tmem_st16(lanes + kColA + 32 * b, f);
             }
             tmem_wait_st();
             tc_fence_before();
             arrive_warp(&B->p);
-            if (lane == 0) mbar_arrive(&B->gate_free[c & 1]);
+            if (c > 0 && lane == 0) {  // by now the last chunk's store has read its tile
+                asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+                mbar_arrive(&B->stored[(c - 1) & 1]);
+            }
+            __syncwarp();
+            if (!wait_warp(&B->full[iv % kRing], (iv / kRing) & 1, B, p.status) || !split(c, 2, tid)) break;
+            arrive_warp(&B->gate_free[c & 1]);
             if (!wait_warp(&B->o, c & 1, B, p.status)) break;
             tc_fence_after();
-            uint32_t pk[32];
+            // rows of 128 bytes into the V tile, which nobody reads any more; a warp whose rows are all
+            // tokens of the window sends them by one TMA store, else its lanes store what is left
+            const int t = sp.bos + c * kC + row;
+            const bool whole = c + 1 < nchunks || 32 * quad + 32 <= last_rows;
+            uint8_t *const rows = smem + (iv % kRing) * kTile + half * kHalf + quad * 4096;
+            uint4 *const dst = reinterpret_cast<uint4 *>(p.out + ((size_t)t * H + h) * kHeadDim + 64 * half);
 #pragma unroll
             for (int b = 0; b < 4; ++b) {
                 float o[16], x[16];
                 tmem_ld16(lanes + kColO + 64 * half + 16 * b, o);
                 tmem_ld16(lanes + kColQS + 64 * half + 16 * b, x);
                 tmem_wait_ld();
+                uint32_t pk[8];
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
-                    pk[8 * b + j] =
-                        pack_bf16(fmaf(lam, x[2 * j], p.scale * o[2 * j]), fmaf(lam, x[2 * j + 1], p.scale * o[2 * j + 1]));
-            }
-            tc_fence_before();
-            arrive_warp(&B->o_free);
-            const int t = sp.bos + c * kC + row;
-            if (t < sp.eos) {
-                __nv_bfloat16 *const dst = p.out + ((size_t)t * H + h) * kHeadDim + 64 * half;
-                if (wide) {
+                    pk[j] = pack_bf16(fmaf(lam, x[2 * j], p.scale * o[2 * j]), fmaf(lam, x[2 * j + 1], p.scale * o[2 * j + 1]));
 #pragma unroll
-                    for (int b = 0; b < 4; ++b) store_32(dst + 16 * b, pk + 8 * b);
-                } else {
-#pragma unroll
-                    for (int b = 0; b < 8; ++b)
-                        reinterpret_cast<uint4 *>(dst)[b] = make_uint4(pk[4 * b], pk[4 * b + 1], pk[4 * b + 2], pk[4 * b + 3]);
+                for (int i = 0; i < 2; ++i) {
+                    const uint4 y = make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
+                    if (whole)
+                        *reinterpret_cast<uint4 *>(rows + lane * 128 + (((2 * b + i) ^ (lane & 7)) << 4)) = y;
+                    else if (t < sp.eos)
+                        dst[2 * b + i] = y;
                 }
             }
+            tc_fence_before();
+            fence_async_smem();
+            arrive_warp(&B->o_free);
+            if (whole && lane == 0) {
+                tma_store(&map_o, smem_addr(rows), 64 * half, h, t);
+                asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+            }
+            __syncwarp();
         }
-    } else if (warp >= kWarpS) {
+        if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+        __syncwarp();
+    } else {
         const int quad = warp & 3, half = (warp - kWarpS) >> 2, row = 32 * quad + lane;  // row: dk
-        const int tid = threadIdx.x - kWarpS * 32;
         const uint32_t lanes = tmem + ((uint32_t)(32 * quad) << 16) + kColD + 64 * half;
         uint8_t *const s_row = smem + kS + half * kHalf + row * 128;
         float S[64];
@@ -566,63 +660,29 @@ __global__ void __launch_bounds__(kThreads, 1)
             arrive_warp(&B->s);
         };
         if (!kStates && nchunks > 0) publish();
-        bool ok = true;
-        int quarter = 0;
-        for (int c = 0; c < nchunks; ++c) {
+        const int tid = threadIdx.x - kWarpS * 32;
+        // Opens chunk c: its gate sums and V are there; in a chunk that is not full, the rows past the last
+        // token are cleared (they hold another sequence's keys and values, which a zero in the other
+        // operand does not silence if they are not finite); then the first half of the split.
+        auto open_chunk = [&](int c) {
             const int ik = c * kPer + kPer - 2, iv = ik + 1;
-            const int L = c + 1 < nchunks ? kC : last_rows;
-            const Gates *G = reinterpret_cast<const Gates *>(smem + kGates) + (c & 1);
-            uint8_t *const tile = smem + (iv % kRing) * kTile;
-            ok = wait_warp(&B->gate[c & 1], (c >> 1) & 1, B, p.status) &&
-                 wait_warp(&B->full[iv % kRing], (iv / kRing) & 1, B, p.status);
-            if (!ok) break;
-            if (L < kC) {
-                // rows past the last token hold another sequence's keys and values, which a zero in the
-                // other operand does not silence if they are not finite
-                ok = wait_warp(&B->full[ik % kRing], (ik / kRing) & 1, B, p.status);
-                if (!ok) break;
-                for (int x = tid; x < 4096; x += kStateThreads)
-                    if (((x & 1023) >> 3) >= L)
-                        *reinterpret_cast<uint4 *>((x < 2048 ? tile : smem + (ik % kRing) * kTile - 32768) + x * 16) = make_uint4(0, 0, 0, 0);
+            if (!wait_warp(&B->gate[c & 1], (c >> 1) & 1, B, p.status)) return false;
+            if (!wait_warp(&B->full[iv % kRing], (iv / kRing) & 1, B, p.status)) return false;
+            if (c + 1 == nchunks && last_rows < kC) {
+                if (!wait_warp(&B->full[ik % kRing], (ik / kRing) & 1, B, p.status)) return false;
+                uint8_t *const keys = smem + (ik % kRing) * kTile, *const values = smem + (iv % kRing) * kTile;
+                for (int x = tid; x < 2048; x += kGroup)
+                    if (((x & 1023) >> 3) >= last_rows)
+                        *reinterpret_cast<uint4 *>(values + x * 16) = *reinterpret_cast<uint4 *>(keys + x * 16) = make_uint4(0, 0, 0, 0);
                 fence_async_smem();
                 arrive_warp(&B->tail);
             }
-            if (c < updates) {
-                for (int t0 = 0; t0 < L; t0 += kQuarter, ++quarter) {
-                    const int st = quarter & 1, t = t0 + (tid >> 3);
-                    const float f = G->suffix[t];
-                    uint8_t *const to = smem + kSplit + st * kSplitStage + tid * 16;
-                    uint4 in[2];
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        in[i] = *reinterpret_cast<const uint4 *>(tile + i * kHalf + t0 * 128 + tid * 16);
-                        if (t >= L) in[i] = make_uint4(0, 0, 0, 0);
-                    }
-                    if (quarter >= 2) {
-                        ok = wait_warp(&B->split_free[st], ((quarter >> 1) - 1) & 1, B, p.status);
-                        if (!ok) break;
-                    }
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const uint32_t u[4] = {in[i].x, in[i].y, in[i].z, in[i].w};
-                        uint32_t hi[4], rest[4];
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const float y0 = __uint_as_float(u[e] << 16) * f, y1 = __uint_as_float(u[e] & 0xffff0000u) * f;
-                            hi[e] = pack_bf16(y0, y1);
-                            rest[e] = pack_bf16(y0 - __uint_as_float(hi[e] << 16), y1 - __uint_as_float(hi[e] & 0xffff0000u));
-                        }
-                        *reinterpret_cast<uint4 *>(to + i * kSplitHalf) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                        *reinterpret_cast<uint4 *>(to + kSplitLo + i * kSplitHalf) = make_uint4(rest[0], rest[1], rest[2], rest[3]);
-                    }
-                    fence_async_smem();
-                    arrive_warp(&B->split[st]);
-                }
-                if (!ok) break;
-            }
-            const float decay = G->decay;
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&B->gate_free[c & 1]);
+            return split(c, 0, tid);
+        };
+        bool ok = nchunks == 0 || open_chunk(0);
+        for (int c = 0; c < nchunks && ok; ++c) {
+            const float decay = (reinterpret_cast<const Gates *>(smem + kGates) + (c & 1))->decay;
+            arrive_warp(&B->gate_free[c & 1]);
             if (c < updates) {
                 ok = wait_warp(&B->d, c & 1, B, p.status);
                 if (!ok) break;
@@ -637,12 +697,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 tc_fence_before();
                 arrive_warp(&B->d_free);  // (only with an update: an arrival for a chunk without one could complete
-                                          // a second phase before the MMA thread has seen the first)
+                                          // a second phase before the MMA warp has seen the first)
             }
-            if (!kStates && c + 1 < nchunks) {
-                ok = wait_warp(&B->qs, c & 1, B, p.status);
-                if (!ok) break;
-                publish();
+            if (c + 1 < nchunks) {
+                if (!kStates) {
+                    ok = wait_warp(&B->qs, c & 1, B, p.status);
+                    if (!ok) break;
+                    publish();
+                }
+                ok = open_chunk(c + 1);
             }
         }
         pdl_wait();  // an initial state in the same place has been read by the launches before
@@ -719,13 +782,13 @@ EncodeTiled encode_tiled() {
     return fn;
 }
 
-// [T][H][128] BF16, in boxes of 128 tokens x one head x 64 columns; tokens past T read as zeros.
-cudaError_t token_map(CUtensorMap *map, const __nv_bfloat16 *base, int32_t T, int32_t H) {
+// [T][H][128] BF16, in boxes of `rows` tokens x one head x 64 columns; tokens past T read as zeros.
+cudaError_t token_map(CUtensorMap *map, const __nv_bfloat16 *base, int32_t T, int32_t H, cuuint32_t rows) {
     const EncodeTiled encode = encode_tiled();
     if (!encode) return cudaErrorNotSupported;
     const cuuint64_t dims[3] = {kHeadDim, (cuuint64_t)H, (cuuint64_t)T};
     const cuuint64_t strides[2] = {kHeadDim * 2, (cuuint64_t)H * kHeadDim * 2};
-    const cuuint32_t box[3] = {64, 1, kC}, step[3] = {1, 1, 1};
+    const cuuint32_t box[3] = {64, 1, rows}, step[3] = {1, 1, 1};
     const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<__nv_bfloat16 *>(base), dims, strides, box,
                               step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
@@ -807,10 +870,11 @@ cudaError_t launch_linear_prefill(const LinearPrefillArgs &args, cudaStream_t st
         a.plan = plan_linear(args.num_seqs, args.total_tokens, args.num_heads, sms);
     }
     const int64_t tail = chains - a.plan.seq_chains;
-    CUtensorMap mq, mk, mv;
-    cudaError_t e = token_map(&mq, args.q, args.total_tokens, args.num_heads);
-    if (e == cudaSuccess) e = token_map(&mk, args.k, args.total_tokens, args.num_heads);
-    if (e == cudaSuccess) e = token_map(&mv, args.v, args.total_tokens, args.num_heads);
+    CUtensorMap mq, mk, mv, mo;
+    cudaError_t e = token_map(&mq, args.q, args.total_tokens, args.num_heads, kC);
+    if (e == cudaSuccess) e = token_map(&mk, args.k, args.total_tokens, args.num_heads, kC);
+    if (e == cudaSuccess) e = token_map(&mv, args.v, args.total_tokens, args.num_heads, kC);
+    if (e == cudaSuccess) e = token_map(&mo, args.out, args.total_tokens, args.num_heads, 32);
     if (e == cudaSuccess) e = configure_once<false>();
     if (e != cudaSuccess) return e;
     if (tail > 0) {
@@ -818,13 +882,13 @@ cudaError_t launch_linear_prefill(const LinearPrefillArgs &args, cudaStream_t st
         a.decay = a.slots + slot_bytes(tail, a.plan.wins) / 4;
         e = configure_once<true>();
         if (e != cudaSuccess) return e;
-        e = launch(kda_linear_chunk_kernel<true>, (unsigned)(tail * (a.plan.wins - 1)), kThreads, kSmem, stream, false, a, mq, mk, mv);
+        e = launch(kda_linear_chunk_kernel<true>, (unsigned)(tail * (a.plan.wins - 1)), kThreads, kSmem, stream, false, a, mq, mk, mv, mo);
         if (e != cudaSuccess) return e;
         e = launch(kda_linear_scan_kernel, (unsigned)(tail * kScanCtas), kScanThreads, 0, stream, true, a);
         if (e != cudaSuccess) return e;
     }
     return launch(kda_linear_chunk_kernel<false>, (unsigned)(a.plan.seq_chains + tail * a.plan.wins), kThreads, kSmem, stream,
-                  tail > 0, a, mq, mk, mv);
+                  tail > 0, a, mq, mk, mv, mo);
 }
 
 }  // namespace kda
