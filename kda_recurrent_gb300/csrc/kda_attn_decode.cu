@@ -2,20 +2,107 @@
 //
 //     x_j = scale q . k_j,  p = softmax(x),  o = sum_j p_j v_j
 //
-// One CTA per (row, query head): its warps take every fourth cached token each, keeping a
-// running maximum m, sum l = sum e^{x - m} and o; the warps' parts are joined at the end. The
-// weights need the final sum, so a second kernel forms them once lse is known.
+// Every cached token is read once (512 bytes a key head) and used by the query heads that share
+// its key head, so the kernel is an HBM stream. An item is a (row, key head, 16 of its query
+// heads); its tokens come in tiles of 16. All items' tiles, laid end to end, are cut into
+// equal shares, one for each warp of the GPU (eight on an SM), so that any mixture of lengths keeps
+// every warp busy to the end. A warp walks its share alone: its own ring of cp.async stages
+// (three tiles, so about 128 KiB are in flight on an SM), no barrier with other warps. It keeps
+// the running maximum m, sum l = sum 2^(x - m) and o of its 16 query rows in registers; the products
+// are m16n8k16 BF16 tensor-core instructions whose 16 rows are the query heads. (Tensor memory and
+// tcgen05 would need 64 or 128 rows; the rows here are 1 to 16, and the tensor work is a few
+// percent of the time.) The probabilities are split into two BF16 terms for P V, which costs
+// nothing here and leaves the output's own rounding as the only one.
+//
+// An item inside one share is finished by its warp. An item cut between shares leaves (m, l, o) of each
+// part in the workspace, and a second kernel joins the parts in order, which makes the result
+// independent of timing. It also writes the rows that have no token. With `weight`, the first kernel
+// stores the scores (4 bytes a query head beside the token's 512) and a third adds
+// 2^(x - lse) to the weights.
+//
+// The order of the 128 channels inside a product is free, so the fragments are laid out for 16-byte
+// shared-memory reads: a lane's 16 bytes of a key row serve two k-steps, and of a value row eight column
+// tiles, which leaves a lane with 16 consecutive output channels. Two swizzles (keys: bit 2 of the
+// chunk with the row's parity; values: bits 1-2 with the row pair) keep the reads free of bank
+// conflicts.
+#include <algorithm>
+
 #include "kda_internal.cuh"
+#include "kda_mma.cuh"
 
 namespace kda {
 namespace {
 
-constexpr int kWarps = 4;
+constexpr int kWarps = 8;
+constexpr int kThreads = kWarps * 32;
+constexpr int kTokens = 16;  // of a tile
+constexpr int kRows = 16;    // query heads of an item
+constexpr int kStages = 3;
+constexpr int kStageBytes = 2 * kTokens * kHeadDim * 2;
+constexpr int kRingBytes = kWarps * kStages * kStageBytes;
+constexpr int kSmem = kRingBytes + kWarps * kStages * 4;
+constexpr int kMinTiles = 2;  // a share holds at least this many tiles, as long as there are shares to spare
 constexpr float kNegInf = -INFINITY;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
-// Page of token j of row b, or -1 (missing). A bad table entry is recorded.
-__device__ __forceinline__ int page_of(const PagedCache &c, int b, int j, DeviceStatus *st) {
-    const int page = c.block_table[(size_t)b * c.max_pages + (j >> c.page_shift)];
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ void pdl_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// A part of an item: (m, l) of its rows, then o.
+struct Part {
+    float m[kRows], l[kRows];
+    float o[kRows][kHeadDim];
+};
+
+struct Workspace {
+    int64_t *first;  // [batch + 1]: tiles of all items of the rows before
+    float *lse2;     // [batch][query heads]: log2(sum 2^x)
+    Part *parts;     // [shares][2]: an item begun in an earlier share, and one begun in this share
+    float *scores;   // [batch][query heads][capacity] (with weights): x in log2 units
+};
+
+__host__ __device__ __forceinline__ int64_t align16(int64_t n) { return (n + 15) / 16 * 16; }
+
+__host__ __device__ __forceinline__ int64_t workspace_layout(Workspace *w, char *base, int64_t batch, int64_t q_heads,
+                                                             int64_t capacity, bool with_weight, int64_t shares) {
+    int64_t at = 0;
+    if (w) w->first = reinterpret_cast<int64_t *>(base + at);
+    at += align16((batch + 1) * 8);
+    if (w) w->lse2 = reinterpret_cast<float *>(base + at);
+    at += align16(batch * q_heads * 4);
+    if (w) w->parts = reinterpret_cast<Part *>(base + at);
+    at += shares * 2 * (int64_t)sizeof(Part);
+    if (w) w->scores = reinterpret_cast<float *>(base + at);
+    if (with_weight) at += align16(batch * q_heads * capacity * 4);
+    return at;
+}
+
+struct Args {
+    AttnDecodeArgs p;
+    Workspace ws;
+    int32_t shares;  // warps of the first kernel
+    int32_t q_tiles;  // items of a key head
+};
+
+// Share s covers tiles [s total / used, (s + 1) total / used) of all items, laid end to end.
+__device__ __forceinline__ int64_t shares_used(int64_t total, int shares) {
+    const int64_t most = (total + kMinTiles - 1) / kMinTiles;
+    return most < 1 ? 1 : most < shares ? most : shares;
+}
+
+__device__ __forceinline__ int64_t share_begin(int64_t s, int64_t total, int64_t used) { return s * total / used; }
+
+// The share that holds tile x.
+__device__ __forceinline__ int64_t share_of(int64_t x, int64_t total, int64_t used) { return ((x + 1) * used - 1) / total; }
+
+__device__ __forceinline__ int page_at(const PagedCache &c, int b, int j, DeviceStatus *st) {
+    const int page = __ldg(c.block_table + (size_t)b * c.max_pages + (j >> c.page_shift));
     if (page >= c.num_pages) {
         report_error(st, KDA_ERR_DEVICE_INPUT, b);
         return -1;
@@ -23,104 +110,420 @@ __device__ __forceinline__ int page_of(const PagedCache &c, int b, int j, Device
     return page;
 }
 
-__device__ __forceinline__ size_t row_offset(const PagedCache &c, int64_t page_stride, int page, int h, int j) {
-    return (size_t)page * page_stride + ((size_t)h * c.page_size + (j & (c.page_size - 1))) * kHeadDim;
+// A place in the sequence of tiles: tile `tile` of the `tiles` of item `item` of row b, which has n
+// tokens.
+struct Place {
+    int b, item, tile, tiles, n;
+};
+
+__device__ __forceinline__ void next_tile(Place &at, const Args &a, int items) {
+    if (++at.tile < at.tiles) return;
+    at.tile = 0;
+    if (++at.item < items) return;
+    at.item = 0;
+    do {  // the next row with a token (there is one: the share holds another tile)
+        ++at.b;
+        at.n = row_length(a.p.c, at.b, a.p.status, false);
+    } while (at.n == 0 && at.b + 1 < a.p.c.batch);
+    at.tiles = (at.n + kTokens - 1) / kTokens;
 }
 
-__device__ __forceinline__ float warp_sum(float x) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-    return x;
-}
-
-__device__ __forceinline__ void load4(const __nv_bfloat16 *p, float (&x)[4]) {
-    const uint2 w = *reinterpret_cast<const uint2 *>(p);
-    x[0] = __uint_as_float(w.x << 16), x[1] = __uint_as_float(w.x & 0xffff0000u);
-    x[2] = __uint_as_float(w.y << 16), x[3] = __uint_as_float(w.y & 0xffff0000u);
-}
-
-__device__ __forceinline__ float score(const AttnDecodeArgs &a, const float (&q)[4], int page, int h, int j, int lane) {
-    float k[4];
-    load4(a.c.k + row_offset(a.c, a.c.k_page_stride, page, h, j) + 4 * lane, k);
-    return a.scale * warp_sum(q[0] * k[0] + q[1] * k[1] + q[2] * k[2] + q[3] * k[3]);
-}
-
-__global__ void __launch_bounds__(kWarps * 32) kda_attn_decode_kernel(const AttnDecodeArgs a, float *lse) {
-    __shared__ float s_m[kWarps], s_l[kWarps], s_o[kWarps][kHeadDim];
-    const int b = blockIdx.x / a.num_q_heads, hq = blockIdx.x - b * a.num_q_heads, h = hq / a.group;
+__global__ void __launch_bounds__(kThreads, 1) kda_attn_decode_kernel(const Args a) {
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ int64_t s_sum[kWarps], s_start[kWarps], s_off[kWarps];
+    __shared__ int s_row[kWarps];
+    const AttnDecodeArgs &p = a.p;
+    const PagedCache &c = p.c;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int n = row_length(a.c, b, a.status, threadIdx.x == 0 && hq == 0);
-    float q[4], o[4] = {0.0f, 0.0f, 0.0f, 0.0f}, m = kNegInf, l = 0.0f;
-    load4(a.q + (size_t)blockIdx.x * kHeadDim + 4 * lane, q);
-    for (int j = warp; j < n; j += kWarps) {
-        const int page = page_of(a.c, b, j, a.status);
-        if (page < 0) continue;
-        const float x = score(a, q, page, h, j, lane);
-        const float top = fmaxf(m, x);
-        const float ref = top == kNegInf ? 0.0f : top;
-        const float keep = expf(m - ref), p = expf(x - ref);
-        float v[4];
-        load4(a.c.v + row_offset(a.c, a.c.v_page_stride, page, h, j) + 4 * lane, v);
-        l = fmaf(l, keep, p);
+    const int items = c.num_kv_heads * a.q_tiles;
+    // shares go round the SMs, so that few shares spread over them
+    const int share = warp * gridDim.x + blockIdx.x;
+    pdl_launch_dependents();
+
+    // ---- the total, then the row and tile where each warp's share begins
+    auto tiles_of = [&](int b) {
+        return b < c.batch ? (int64_t)((row_length(c, b, p.status, blockIdx.x == 0) + kTokens - 1) / kTokens) * items : 0;
+    };
+    auto block_sum = [&](int64_t x, int64_t &before) {  // inclusive prefix sum's total, and the sum before this thread
+        int64_t sum = x;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) o[e] = fmaf(o[e], keep, p * v[e]);
-        m = top;
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t y = __shfl_up_sync(0xffffffffu, sum, o);
+            if (lane >= o) sum += y;
+        }
+        __syncthreads();
+        if (lane == 31) s_sum[warp] = sum;
+        __syncthreads();
+        int64_t total = 0;
+        before = sum - x;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            if (w < warp) before += s_sum[w];
+            total += s_sum[w];
+        }
+        return total;
+    };
+    int64_t total = 0, mine = 0, before;
+    for (int b = threadIdx.x; b < c.batch; b += kThreads) mine += tiles_of(b);
+    total = block_sum(mine, before);
+    const int64_t used = shares_used(total, a.shares);
+    const int64_t begin = share < used ? share_begin(share, total, used) : total;
+    const int64_t end = share < used ? share_begin(share + 1, total, used) : total;
+    if (lane == 0) s_start[warp] = begin;
+    int64_t first = 0;
+    for (int b0 = 0; b0 < c.batch; b0 += kThreads) {
+        const int64_t x = tiles_of(b0 + threadIdx.x);
+        const int64_t sum = block_sum(x, before);  // (its barriers also order s_start)
+        if (blockIdx.x == 0 && b0 + threadIdx.x < c.batch) a.ws.first[b0 + threadIdx.x] = first + before;
+        for (int w = 0; w < kWarps; ++w) {
+            const int64_t off = s_start[w] - first - before;
+            if (off >= 0 && off < x) s_row[w] = b0 + threadIdx.x, s_off[w] = off;
+        }
+        first += sum;
+        __syncthreads();
     }
-    if (lane == 0) s_m[warp] = m, s_l[warp] = l;
+    if (blockIdx.x == 0 && threadIdx.x == 0) a.ws.first[c.batch] = total;
+    if (begin >= end) return;
+    Place at;
+    at.b = s_row[warp];
+    at.n = row_length(c, at.b, p.status, false);
+    at.tiles = (at.n + kTokens - 1) / kTokens;
+    at.item = (int)(s_off[warp] / at.tiles);
+    at.tile = (int)(s_off[warp] - (int64_t)at.item * at.tiles);
+
+    // ---- the ring
+    uint8_t *const ring = smem + warp * (kStages * kStageBytes);
+    uint32_t *const live = reinterpret_cast<uint32_t *>(smem + kRingBytes) + warp * kStages;  // a bit a token
+    const uint32_t ring_addr = smem_addr(ring);
+    const int half_row = lane >> 4, chunk = lane & 15;
+    Place load = at;
+    int64_t to_load = end - begin;
+    auto pages_of = [&](const Place &x) {  // of the tile's two groups of eight tokens
+        const int j = x.tile * kTokens;
+        int2 pg;
+        pg.x = page_at(c, x.b, j, p.status);
+        pg.y = c.page_shift > 3 ? pg.x : j + 8 < x.n ? page_at(c, x.b, j + 8, p.status) : -1;
+        return pg;
+    };
+    int2 pages = pages_of(load);
+    auto fetch = [&](int stage) {
+        if (to_load > 0) {
+            const int j0 = load.tile * kTokens, h = load.item / a.q_tiles, mask = c.page_size - 1;
+            const int left = load.n - j0;  // tokens
+            uint32_t bits = left >= kTokens ? 0xffffu : (1u << left) - 1;
+            if (pages.x < 0) bits &= 0xff00u;
+            if (pages.y < 0) bits &= 0x00ffu;
+            const uint32_t dst = ring_addr + stage * kStageBytes;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) s_o[warp][4 * lane + e] = o[e];
-    __syncthreads();
-    float top = kNegInf, sum = 0.0f, out = 0.0f;
-    for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_m[w]);
+            for (int i = 0; i < 8; ++i) {
+                const int r = 2 * i + half_row;
+                const int page = i < 4 ? pages.x : pages.y;
+                const bool on = (bits >> r) & 1;
+                const size_t row = ((size_t)h * c.page_size + ((j0 + r) & mask)) * kHeadDim + chunk * 8;
+                const size_t k_off = on ? (size_t)page * c.k_page_stride + row : 0;
+                const size_t v_off = on ? (size_t)page * c.v_page_stride + row : 0;
+                cp_async_16(dst + r * 256 + ((chunk ^ ((r & 1) << 2)) << 4), c.k + k_off, on ? 16u : 0u);
+                cp_async_16(dst + kStageBytes / 2 + r * 256 + ((chunk ^ (((r >> 1) & 3) << 1)) << 4), c.v + v_off, on ? 16u : 0u);
+            }
+            if (lane == 0) live[stage] = bits;
+            if (--to_load > 0) {
+                next_tile(load, a, items);
+                pages = pages_of(load);
+            }
+        }
+        cp_async_commit();
+    };
+#pragma unroll
+    for (int s = 0; s < kStages - 1; ++s) fetch(s);
+
+    // ---- the share
+    const int g = lane >> 2, t = lane & 3;
+    const float scale2 = p.scale * kLog2e;
+    int stage = 0;
+    int64_t left = end - begin;
+    while (left > 0) {
+        // a segment: this share's tiles of one item
+        const int h = at.item / a.q_tiles, q0 = (at.item - h * a.q_tiles) * kRows;
+        const int rows = min(kRows, p.group - q0);  // query heads
+        const size_t head0 = (size_t)at.b * p.num_q_heads + (size_t)h * p.group + q0;
+        const bool from_start = at.tile == 0;
+        uint32_t qa[8][4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            uint4 x = make_uint4(0, 0, 0, 0), y = x;
+            if (g < rows) x = __ldg(reinterpret_cast<const uint4 *>(p.q + (head0 + g) * kHeadDim) + t + 4 * j);
+            if (g + 8 < rows) y = __ldg(reinterpret_cast<const uint4 *>(p.q + (head0 + g + 8) * kHeadDim) + t + 4 * j);
+            qa[2 * j][0] = x.x, qa[2 * j][1] = y.x, qa[2 * j][2] = x.y, qa[2 * j][3] = y.y;
+            qa[2 * j + 1][0] = x.z, qa[2 * j + 1][1] = y.z, qa[2 * j + 1][2] = x.w, qa[2 * j + 1][3] = y.w;
+        }
+        float o[16][4];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.0f;
+        float m[2] = {kNegInf, kNegInf}, l[2] = {0.0f, 0.0f};
+        const int tiles = (int)min((int64_t)(at.tiles - at.tile), left);
+        for (int i = 0; i < tiles; ++i, ++at.tile) {
+            fetch(stage == 0 ? kStages - 1 : stage - 1);
+            cp_async_wait<kStages - 1>();
+            __syncwarp();
+            const uint8_t *const ks = ring + stage * kStageBytes, *const vs = ks + kStageBytes / 2;
+            const uint32_t bits = live[stage];
+            float s[2][4];
+#pragma unroll
+            for (int nt = 0; nt < 2; ++nt) {
+                s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.0f;
+                const int r = 8 * nt + g;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const uint4 k = *reinterpret_cast<const uint4 *>(ks + r * 256 + (((t + 4 * j) ^ ((r & 1) << 2)) << 4));
+                    mma_bf16_16816(s[nt], qa[2 * j], k.x, k.y);
+                    mma_bf16_16816(s[nt], qa[2 * j + 1], k.z, k.w);
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const bool on = (bits >> (8 * nt + 2 * t + (e & 1))) & 1;
+                    s[nt][e] = on ? s[nt][e] * scale2 : kNegInf;
+                }
+            }
+            if (p.weight) {
+                float *const dst = a.ws.scores + (head0 + g) * c.capacity + at.tile * kTokens + 2 * t;
+#pragma unroll
+                for (int nt = 0; nt < 2; ++nt)
+                    if (at.tile * kTokens + 8 * nt < c.capacity) {  // (the capacity is a multiple of eight)
+                        if (g < rows) *reinterpret_cast<float2 *>(dst + 8 * nt) = make_float2(s[nt][0], s[nt][1]);
+                        if (g + 8 < rows)
+                            *reinterpret_cast<float2 *>(dst + 8 * (size_t)c.capacity + 8 * nt) = make_float2(s[nt][2], s[nt][3]);
+                    }
+            }
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {  // rows g and g + 8
+                float top = fmaxf(fmaxf(s[0][2 * r], s[0][2 * r + 1]), fmaxf(s[1][2 * r], s[1][2 * r + 1]));
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                const float now = fmaxf(m[r], top);
+                const float ref = now == kNegInf ? 0.0f : now;
+                if (__any_sync(0xffffffffu, now != m[r])) {
+                    const float keep = ex2(m[r] - ref);
+                    l[r] *= keep;
+#pragma unroll
+                    for (int i2 = 0; i2 < 16; ++i2) o[i2][2 * r] *= keep, o[i2][2 * r + 1] *= keep;
+                    m[r] = now;
+                }
+#pragma unroll
+                for (int nt = 0; nt < 2; ++nt) {
+                    const float p0 = ex2(s[nt][2 * r] - ref), p1 = ex2(s[nt][2 * r + 1] - ref);
+                    l[r] += p0 + p1;
+                    const uint32_t w = pack_bf16(p0, p1);
+                    hi[2 * nt + r] = w;
+                    lo[2 * nt + r] = pack_bf16(p0 - __uint_as_float(w << 16), p1 - __uint_as_float(w & 0xffff0000u));
+                }
+            }
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                uint4 v[4];  // rows 2t, 2t + 1, 2t + 8, 2t + 9
+#pragma unroll
+                for (int i2 = 0; i2 < 4; ++i2) {
+                    const int r = 2 * t + (i2 & 1) + 8 * (i2 >> 1);
+                    v[i2] = *reinterpret_cast<const uint4 *>(vs + r * 256 + (((g + 8 * half) ^ (((r >> 1) & 3) << 1)) << 4));
+                }
+                const uint32_t *const v0 = &v[0].x, *const v1 = &v[1].x, *const v2 = &v[2].x, *const v3 = &v[3].x;
+#pragma unroll
+                for (int w = 0; w < 4; ++w) {
+                    const uint32_t b00 = __byte_perm(v0[w], v1[w], 0x5410), b01 = __byte_perm(v2[w], v3[w], 0x5410);
+                    const uint32_t b10 = __byte_perm(v0[w], v1[w], 0x7632), b11 = __byte_perm(v2[w], v3[w], 0x7632);
+                    mma_bf16_16816(o[8 * half + 2 * w], hi, b00, b01);
+                    mma_bf16_16816(o[8 * half + 2 * w + 1], hi, b10, b11);
+                    mma_bf16_16816(o[8 * half + 2 * w], lo, b00, b01);
+                    mma_bf16_16816(o[8 * half + 2 * w + 1], lo, b10, b11);
+                }
+            }
+            __syncwarp();  // the stage is read before a later fetch overwrites it
+            stage = stage == kStages - 1 ? 0 : stage + 1;
+        }
+        left -= tiles;
+        const bool whole = from_start && at.tile == at.tiles;
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
+            l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
+            const int row = g + 8 * r;
+            if (row >= rows) continue;
+            if (whole) {
+                const float inv = l[r] == 0.0f ? 0.0f : 1.0f / l[r];
+                const float v = l[r] == 0.0f ? kNegInf : m[r] + log2f(l[r]);
+                if (t == 0) {
+                    if (p.lse) p.lse[head0 + row] = v * kLn2;
+                    a.ws.lse2[head0 + row] = v;
+                }
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    uint4 *const dst = reinterpret_cast<uint4 *>(p.out + (head0 + row) * kHeadDim + 64 * half + 16 * t);
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {  // eight channels: one accumulator column of eight tiles
+                        uint32_t w[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            w[i] = pack_bf16(o[8 * half + 2 * i][2 * r + e] * inv, o[8 * half + 2 * i + 1][2 * r + e] * inv);
+                        dst[e] = make_uint4(w[0], w[1], w[2], w[3]);
+                    }
+                }
+            } else {
+                Part *const part = a.ws.parts + 2 * (size_t)share + (from_start ? 1 : 0);
+                if (t == 0) part->m[row] = m[r], part->l[row] = l[r];
+#pragma unroll
+                for (int half = 0; half < 2; ++half)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        float4 *const dst = reinterpret_cast<float4 *>(&part->o[row][64 * half + 16 * t + 8 * e]);
+#pragma unroll
+                        for (int i = 0; i < 2; ++i)
+                            dst[i] = make_float4(o[8 * half + 4 * i][2 * r + e], o[8 * half + 4 * i + 1][2 * r + e],
+                                                 o[8 * half + 4 * i + 2][2 * r + e], o[8 * half + 4 * i + 3][2 * r + e]);
+                    }
+            }
+        }
+        if (left > 0) {  // the next item
+            --at.tile;
+            next_tile(at, a, items);
+        }
+    }
+    cp_async_wait<0>();
+}
+
+// One warp for a (row, query head): rows without a token, and the parts of items cut between shares, in
+// the shares' order.
+constexpr int kJoinWarps = 4;
+
+__global__ void __launch_bounds__(kJoinWarps * 32) kda_attn_join_kernel(const Args a) {
+    const AttnDecodeArgs &p = a.p;
+    const int head = blockIdx.x * kJoinWarps + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    pdl_launch_dependents();
+    pdl_wait();
+    if (head >= p.c.batch * p.num_q_heads) return;
+    const int b = head / p.num_q_heads, hq = head - b * p.num_q_heads, h = hq / p.group, in_group = hq - h * p.group;
+    const int item = h * a.q_tiles + in_group / kRows, row = in_group % kRows;
+    const int items = p.c.num_kv_heads * a.q_tiles;
+    const int64_t total = a.ws.first[p.c.batch], lo = a.ws.first[b], tiles = (a.ws.first[b + 1] - lo) / items;
+    uint2 *const out = reinterpret_cast<uint2 *>(p.out + (size_t)head * kHeadDim) + lane;
+    if (tiles == 0) {
+        *out = make_uint2(0, 0);
+        if (lane == 0) {
+            if (p.lse) p.lse[head] = kNegInf;
+            a.ws.lse2[head] = kNegInf;
+        }
+        return;
+    }
+    const int64_t used = shares_used(total, a.shares);
+    const int64_t x0 = lo + item * tiles;
+    const int64_t s0 = share_of(x0, total, used), s1 = share_of(x0 + tiles - 1, total, used);
+    if (s0 == s1) return;
+    auto part_of = [&](int64_t s) { return a.ws.parts + 2 * s + (s == s0 ? 1 : 0); };
+    float top = kNegInf;
+    for (int64_t s = s0 + lane; s <= s1; s += 32) top = fmaxf(top, part_of(s)->m[row]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
     const float ref = top == kNegInf ? 0.0f : top;
-    for (int w = 0; w < kWarps; ++w) {
-        const float f = expf(s_m[w] - ref);
-        sum = fmaf(s_l[w], f, sum);
-        out = fmaf(s_o[w][threadIdx.x], f, out);
+    float l = 0.0f;
+    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+    for (int64_t s = s0; s <= s1; ++s) {
+        const Part *const part = part_of(s);
+        const float f = ex2(part->m[row] - ref);
+        const float4 x = *reinterpret_cast<const float4 *>(&part->o[row][4 * lane]);
+        l = fmaf(part->l[row], f, l);
+        o = make_float4(fmaf(x.x, f, o.x), fmaf(x.y, f, o.y), fmaf(x.z, f, o.z), fmaf(x.w, f, o.w));
     }
-    a.out[(size_t)blockIdx.x * kHeadDim + threadIdx.x] = __float2bfloat16_rn(sum == 0.0f ? 0.0f : out / sum);
-    if (threadIdx.x == 0) {
-        const float v = sum == 0.0f ? kNegInf : ref + logf(sum);
-        lse[blockIdx.x] = v;
-        if (a.lse) a.lse[blockIdx.x] = v;
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    *out = make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
+    if (lane == 0) {
+        const float v = l == 0.0f ? kNegInf : ref + log2f(l);
+        if (p.lse) p.lse[head] = v * kLn2;
+        a.ws.lse2[head] = v;
     }
 }
 
-// weight[b][h][j] += sum over the group's query heads of exp(x_j - lse): one warp per token.
-__global__ void __launch_bounds__(kWarps * 32) kda_attn_weight_kernel(const AttnDecodeArgs a, const float *lse) {
-    const int b = blockIdx.x / a.c.num_kv_heads, h = blockIdx.x - b * a.c.num_kv_heads;
-    const int lane = threadIdx.x & 31;
-    const int n = row_length(a.c, b, a.status, false);
-    for (int j = blockIdx.y * kWarps + (threadIdx.x >> 5); j < n; j += gridDim.y * kWarps) {
-        const int page = page_of(a.c, b, j, a.status);
-        if (page < 0) continue;
-        float sum = 0.0f;
-        for (int g = 0; g < a.group; ++g) {
-            const size_t row = (size_t)b * a.num_q_heads + h * a.group + g;
-            float q[4];
-            load4(a.q + row * kHeadDim + 4 * lane, q);
-            const float x = score(a, q, page, h, j, lane);
-            sum += lse[row] == kNegInf ? 0.0f : expf(x - lse[row]);
+// weight[b][h][j] += sum over the query heads of key head h of 2^(x_j - lse), four tokens a thread.
+constexpr int kWeightThreads = 256, kWeightTokens = 4 * kWeightThreads;
+
+__global__ void __launch_bounds__(kWeightThreads) kda_attn_weight_kernel(const Args a) {
+    const AttnDecodeArgs &p = a.p;
+    const int bh = blockIdx.x, b = bh / p.c.num_kv_heads;
+    const int n = row_length(p.c, b, p.status, false);
+    pdl_wait();
+    const size_t head0 = (size_t)bh * p.group;
+    for (int64_t j = (int64_t)blockIdx.y * kWeightTokens + 4 * threadIdx.x; j < n; j += (int64_t)gridDim.y * kWeightTokens) {
+        float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+        for (int i = 0; i < p.group; ++i) {
+            float lse = a.ws.lse2[head0 + i];
+            if (lse == kNegInf) lse = INFINITY;  // a row without a token: no weight
+            const float4 x = *reinterpret_cast<const float4 *>(a.ws.scores + (head0 + i) * p.c.capacity + j);
+            sum = make_float4(sum.x + ex2(x.x - lse), sum.y + ex2(x.y - lse), sum.z + ex2(x.z - lse), sum.w + ex2(x.w - lse));
         }
-        if (lane == 0) a.weight[(size_t)blockIdx.x * a.c.capacity + j] += sum;
+        float *const w = p.weight + (size_t)bh * p.c.capacity + j;
+        if (j + 4 <= n) {
+            const float4 x = *reinterpret_cast<const float4 *>(w);
+            *reinterpret_cast<float4 *>(w) = make_float4(x.x + sum.x, x.y + sum.y, x.z + sum.z, x.w + sum.w);
+        } else {
+            const float s[4] = {sum.x, sum.y, sum.z, sum.w};
+            for (int e = 0; j + e < n; ++e) w[e] += s[e];
+        }
     }
+}
+
+template <typename... P, typename... A>
+cudaError_t launch(void (*kernel)(P...), dim3 grid, unsigned block, size_t smem, cudaStream_t stream, bool dependent,
+                   const A &...args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(block);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = dependent ? 1 : 0;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+cudaError_t configure_once() {
+    static bool configured[64] = {};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64 || !configured[dev]) {
+        e = cudaFuncSetAttribute(kda_attn_decode_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+        if (e != cudaSuccess) return e;
+        if (dev >= 0 && dev < 64) configured[dev] = true;
+    }
+    return cudaSuccess;
 }
 
 }  // namespace
 
-int64_t attn_decode_workspace_bytes(int32_t batch, int32_t num_q_heads, int32_t, int64_t, bool, int32_t) {
-    return ((int64_t)batch * num_q_heads * 4 + 15) / 16 * 16;
+int64_t attn_decode_workspace_bytes(int32_t batch, int32_t num_q_heads, int32_t, int64_t capacity, bool with_weight,
+                                    int32_t sms) {
+    return workspace_layout(nullptr, nullptr, batch, num_q_heads, capacity, with_weight, (int64_t)sms * kWarps);
 }
 
-cudaError_t launch_attn_decode(const AttnDecodeArgs &a, cudaStream_t stream) {
-    float *lse = static_cast<float *>(a.ws);
-    kda_attn_decode_kernel<<<(unsigned)a.c.batch * (unsigned)a.num_q_heads, kWarps * 32, 0, stream>>>(a, lse);
-    cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess || !a.weight) return e;
-    const unsigned parts = (unsigned)((a.c.capacity + 255) / 256);
-    const dim3 grid((unsigned)(a.c.batch * a.c.num_kv_heads), parts < 1024u ? parts : 1024u);
-    kda_attn_weight_kernel<<<grid, kWarps * 32, 0, stream>>>(a, lse);
-    return cudaGetLastError();
+cudaError_t launch_attn_decode(const AttnDecodeArgs &p, cudaStream_t stream) {
+    int32_t sms = 0;
+    if (sm_count_of_current_device(&sms) != KDA_OK) return cudaErrorInvalidDevice;
+    cudaError_t e = configure_once();
+    if (e != cudaSuccess) return e;
+    Args a;
+    a.p = p;
+    a.shares = sms * kWarps;
+    a.q_tiles = (p.group + kRows - 1) / kRows;
+    workspace_layout(&a.ws, static_cast<char *>(p.ws), p.c.batch, p.num_q_heads, p.c.capacity, p.weight != nullptr, a.shares);
+    e = launch(kda_attn_decode_kernel, dim3((unsigned)sms), kThreads, kSmem, stream, false, a);
+    if (e != cudaSuccess) return e;
+    const unsigned heads = (unsigned)p.c.batch * (unsigned)p.num_q_heads;
+    e = launch(kda_attn_join_kernel, dim3((heads + kJoinWarps - 1) / kJoinWarps), kJoinWarps * 32, 0, stream, true, a);
+    if (e != cudaSuccess || !p.weight) return e;
+    const dim3 grid((unsigned)(p.c.batch * p.c.num_kv_heads), (unsigned)std::min((p.c.capacity + kWeightTokens - 1) / kWeightTokens, 65535));
+    return launch(kda_attn_weight_kernel, grid, kWeightThreads, 0, stream, true, a);
 }
 
 }  // namespace kda
