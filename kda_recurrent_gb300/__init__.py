@@ -357,21 +357,40 @@ def decode(q, k, v, g_raw, beta, slot_idx, state_pool, *, scale, lower_bound=0.0
     return out
 
 
+# The calls below are short on the GPU (a few microseconds for one token), so their host side is kept
+# short too: plain integers for pointers and streams, one expression for a tensor's checks, and the
+# device switched only when it has to be.
+
+_NO_SWITCH = contextlib.nullcontext()
+
+
 def _on(device):
     """Makes `device` current for the call (nothing to do when it is already)."""
     import torch
-    if torch.cuda.current_device() == (device.index or 0):
-        return contextlib.nullcontext()
-    return torch.cuda.device(device)
+    return _NO_SWITCH if torch.cuda.current_device() == device.index else torch.cuda.device(device)
 
 
-def _per_head_or_token(log_decay, rows, H, device):
-    """0 for a decay per head [H], 1 for one per token and head [rows, H]."""
+def _stream_of(stream, device):
     import torch
+    return (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
+
+
+def _address(t):
+    return None if t is None else t.data_ptr()
+
+
+def _need(t, name, dtype, shape, device):
+    """_check, with its separate tests (and messages) only for a tensor that fails."""
+    if not (t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.device == device):
+        _check(t, name, dtype, shape, device)
+
+
+def _per_head_or_token(log_decay, rows, H, dtype, device):
+    """0 for a decay per head [H], 1 for one per token and head [rows, H]."""
     if log_decay.dim() == 1:
-        _check(log_decay, "log_decay", torch.float32, (H,), device)
+        _need(log_decay, "log_decay", dtype, (H,), device)
         return 0
-    _check(log_decay, "log_decay", torch.float32, (rows, H), device)
+    _need(log_decay, "log_decay", dtype, (rows, H), device)
     return 1
 
 
@@ -380,7 +399,7 @@ def _workspace_arg(workspace, device):
         return None, 0
     if workspace.device != device or not workspace.is_contiguous():
         raise ValueError("workspace: must be a contiguous tensor on the inputs' device")
-    return _ptr(workspace), workspace.numel() * workspace.element_size()
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
 def kda_linear_prefill(q, k, v, log_decay, cu_seqlens, init_state, out, final_state, scale, workspace=None,
@@ -389,22 +408,29 @@ def kda_linear_prefill(q, k, v, log_decay, cu_seqlens, init_state, out, final_st
     o_t = scale S_t^T q_t, into caller-owned ``out`` / ``final_state``. ``log_decay`` is g: FP32
     [H], or [T, H] for one per token. ``workspace``: see linear_prefill_workspace (or None)."""
     import torch
-    T, H, d = q.shape
+    bf16, f32 = torch.bfloat16, torch.float32
+    T, H, d = shape = q.shape
     N = cu_seqlens.shape[0] - 1
     dev = q.device
-    for name, t in (("q", q), ("k", k), ("v", v), ("out", out)):
-        _check(t, name, torch.bfloat16, (T, H, HEAD_DIM), dev)
-    per_token = _per_head_or_token(log_decay, T, H, dev)
-    _check(cu_seqlens, "cu_seqlens", torch.int32, (N + 1,), dev)
-    for name, t in (("init_state", init_state), ("final_state", final_state)):
-        if t is not None:
-            _check(t, name, torch.float32, (N, H, d, d), dev)
+    if d != HEAD_DIM:
+        raise ValueError(f"q: expected shape {(T, H, HEAD_DIM)}, got {tuple(shape)}")
+    _need(q, "q", bf16, shape, dev)
+    _need(k, "k", bf16, shape, dev)
+    _need(v, "v", bf16, shape, dev)
+    _need(out, "out", bf16, shape, dev)
+    per_token = _per_head_or_token(log_decay, T, H, f32, dev)
+    _need(cu_seqlens, "cu_seqlens", torch.int32, (N + 1,), dev)
+    if init_state is not None:
+        _need(init_state, "init_state", f32, (N, H, d, d), dev)
+    if final_state is not None:
+        _need(final_state, "final_state", f32, (N, H, d, d), dev)
     ws, nbytes = _workspace_arg(workspace, dev)
     _require_cuda(dev)
     with _on(dev):
-        st = load().kda_linear_prefill(_ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), per_token, _ptr(cu_seqlens),
-                                       _ptr(init_state), _ptr(out), _ptr(final_state), N, T, H, float(scale), ws,
-                                       nbytes, _stream_handle(stream, dev))
+        st = (_lib or load()).kda_linear_prefill(
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), per_token, cu_seqlens.data_ptr(),
+            _address(init_state), out.data_ptr(), _address(final_state), N, T, H, scale, ws, nbytes,
+            _stream_of(stream, dev))
     if st != KDA_OK:
         raise KdaError(st, "kda_linear_prefill")
 
@@ -430,24 +456,27 @@ def kda_linear_decode(q, k, v, log_decay, slot_idx, state_pool, out, scale, stre
     [slots, H, 128, 128] (FP32 or BF16, updated in place) at slots ``slot_idx`` (a negative one
     is a padding row). ``log_decay``: FP32 [H] or [rows, H]."""
     import torch
-    R, H, d = q.shape
+    bf16 = torch.bfloat16
+    R, H, d = shape = q.shape
     dev = q.device
-    for name, t in (("q", q), ("k", k), ("v", v), ("out", out)):
-        _check(t, name, torch.bfloat16, (R, H, HEAD_DIM), dev)
-    per_row = _per_head_or_token(log_decay, R, H, dev)
-    _check(slot_idx, "slot_idx", torch.int32, (R,), dev)
-    if state_pool.dtype == torch.float32:
-        sdt = STATE_DTYPES["f32"]
-    elif state_pool.dtype == torch.bfloat16:
-        sdt = STATE_DTYPES["bf16"]
-    else:
+    if d != HEAD_DIM:
+        raise ValueError(f"q: expected shape {(R, H, HEAD_DIM)}, got {tuple(shape)}")
+    _need(q, "q", bf16, shape, dev)
+    _need(k, "k", bf16, shape, dev)
+    _need(v, "v", bf16, shape, dev)
+    _need(out, "out", bf16, shape, dev)
+    per_row = _per_head_or_token(log_decay, R, H, torch.float32, dev)
+    _need(slot_idx, "slot_idx", torch.int32, (R,), dev)
+    dtype, slots = state_pool.dtype, state_pool.shape[0]
+    if dtype is not torch.float32 and dtype is not bf16:
         raise TypeError("state_pool must be float32 or bfloat16")
-    _check(state_pool, "state_pool", state_pool.dtype, (state_pool.shape[0], H, d, d), dev)
+    _need(state_pool, "state_pool", dtype, (slots, H, d, d), dev)
     _require_cuda(dev)
     with _on(dev):
-        st = load().kda_linear_decode(_ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), per_row, _ptr(slot_idx),
-                                      _ptr(state_pool), int(state_pool.shape[0]), sdt, _ptr(out), R, H, float(scale),
-                                      _stream_handle(stream, dev))
+        st = (_lib or load()).kda_linear_decode(
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), per_row, slot_idx.data_ptr(),
+            state_pool.data_ptr(), slots, STATE_DTYPES["bf16" if dtype is bf16 else "f32"], out.data_ptr(), R, H, scale,
+            _stream_of(stream, dev))
     if st != KDA_OK:
         raise KdaError(st, "kda_linear_decode")
 
@@ -458,22 +487,23 @@ def _check_cache(k_cache, v_cache, block_table, seq_lens, device):
     import torch
     if k_cache.dim() != 4:
         raise ValueError(f"k_cache: expected [pages, heads, page_size, {HEAD_DIM}], got {tuple(k_cache.shape)}")
-    pages, Hkv, ps, d = k_cache.shape
+    pages, Hkv, ps, _ = k_cache.shape
+    shape, inner = (pages, Hkv, ps, HEAD_DIM), (ps * HEAD_DIM, HEAD_DIM, 1)
     for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
-        if t.dtype != torch.bfloat16:
+        if t.dtype is not torch.bfloat16:
             raise TypeError(f"{name}: expected {torch.bfloat16}, got {t.dtype}")
-        if tuple(t.shape) != (pages, Hkv, ps, HEAD_DIM):
-            raise ValueError(f"{name}: expected shape {(pages, Hkv, ps, HEAD_DIM)}, got {tuple(t.shape)}")
-        if tuple(t.stride()[1:]) != (ps * HEAD_DIM, HEAD_DIM, 1):
+        if t.shape != shape:
+            raise ValueError(f"{name}: expected shape {shape}, got {tuple(t.shape)}")
+        if t.stride()[1:] != inner:
             raise ValueError(f"{name}: a page must be contiguous")
         if t.device != device:
             raise ValueError(f"{name}: expected device {device}, got {t.device}")
     B = seq_lens.shape[0]
-    _check(seq_lens, "seq_lens", torch.int32, (B,), device)
+    _need(seq_lens, "seq_lens", torch.int32, (B,), device)
     if block_table.dim() != 2:
         raise ValueError(f"block_table: expected [batch, max_pages], got {tuple(block_table.shape)}")
     P = block_table.shape[1]
-    _check(block_table, "block_table", torch.int32, (B, P), device)
+    _need(block_table, "block_table", torch.int32, (B, P), device)
     return B, Hkv, ps, pages, P, k_cache.stride(0), v_cache.stride(0)
 
 
@@ -488,18 +518,19 @@ def kda_attn_decode(q, k_cache, v_cache, block_table, seq_lens, out, scale, work
     dev = q.device
     B, Hkv, ps, pages, P, ks, vs = _check_cache(k_cache, v_cache, block_table, seq_lens, dev)
     Hq = q.shape[1]
-    for name, t in (("q", q), ("out", out)):
-        _check(t, name, torch.bfloat16, (B, Hq, HEAD_DIM), dev)
+    _need(q, "q", torch.bfloat16, (B, Hq, HEAD_DIM), dev)
+    _need(out, "out", torch.bfloat16, (B, Hq, HEAD_DIM), dev)
     if lse is not None:
-        _check(lse, "lse", torch.float32, (B, Hq), dev)
+        _need(lse, "lse", torch.float32, (B, Hq), dev)
     if weight is not None:
-        _check(weight, "weight", torch.float32, (B, Hkv, P * ps), dev)
+        _need(weight, "weight", torch.float32, (B, Hkv, P * ps), dev)
     ws, nbytes = _workspace_arg(workspace, dev)
     _require_cuda(dev)
     with _on(dev):
-        st = load().kda_attn_decode(_ptr(q), _ptr(k_cache), _ptr(v_cache), ks, vs, pages, ps, _ptr(block_table), P,
-                                    _ptr(seq_lens), _ptr(out), _ptr(lse), _ptr(weight), B, Hq, Hkv, float(scale), ws,
-                                    nbytes, _stream_handle(stream, dev))
+        st = (_lib or load()).kda_attn_decode(
+            q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), ks, vs, pages, ps, block_table.data_ptr(), P,
+            seq_lens.data_ptr(), out.data_ptr(), _address(lse), _address(weight), B, Hq, Hkv, scale, ws, nbytes,
+            _stream_of(stream, dev))
     if st != KDA_OK:
         raise KdaError(st, "kda_attn_decode")
 
@@ -533,18 +564,18 @@ def kda_cache_evict(k_cache, v_cache, block_table, seq_lens, weight, new_lens, k
     dev = k_cache.device
     B, Hkv, ps, pages, P, ks, vs = _check_cache(k_cache, v_cache, block_table, seq_lens, dev)
     dst_weight = weight if dst_weight is None else dst_weight
-    for name, t in (("weight", weight), ("dst_weight", dst_weight)):
-        _check(t, name, torch.float32, (B, Hkv, P * ps), dev)
+    _need(weight, "weight", torch.float32, (B, Hkv, P * ps), dev)
+    _need(dst_weight, "dst_weight", torch.float32, (B, Hkv, P * ps), dev)
     if dst_table is not None:
-        _check(dst_table, "dst_table", torch.int32, (B, P), dev)
-    _check(new_lens, "new_lens", torch.int32, (B,), dev)
-    _check(kept, "kept", torch.int32, (B, Hkv, int(budget)), dev)
+        _need(dst_table, "dst_table", torch.int32, (B, P), dev)
+    _need(new_lens, "new_lens", torch.int32, (B,), dev)
+    _need(kept, "kept", torch.int32, (B, Hkv, budget), dev)
     _require_cuda(dev)
     with _on(dev):
-        st = load().kda_cache_evict(_ptr(k_cache), _ptr(v_cache), ks, vs, pages, ps, _ptr(block_table),
-                                    _ptr(dst_table), P, _ptr(seq_lens), _ptr(weight), _ptr(dst_weight),
-                                    _ptr(new_lens), _ptr(kept), B, Hkv, int(budget), int(sink), int(recent),
-                                    _stream_handle(stream, dev))
+        st = (_lib or load()).kda_cache_evict(
+            k_cache.data_ptr(), v_cache.data_ptr(), ks, vs, pages, ps, block_table.data_ptr(), _address(dst_table), P,
+            seq_lens.data_ptr(), weight.data_ptr(), dst_weight.data_ptr(), new_lens.data_ptr(), kept.data_ptr(), B, Hkv,
+            budget, sink, recent, _stream_of(stream, dev))
     if st != KDA_OK:
         raise KdaError(st, "kda_cache_evict")
 

@@ -163,17 +163,20 @@ __global__ void __launch_bounds__(kThreads, 1) kda_attn_decode_kernel(const Args
         }
         return total;
     };
-    int64_t total = 0, mine = 0, before;
-    for (int b = threadIdx.x; b < c.batch; b += kThreads) mine += tiles_of(b);
-    total = block_sum(mine, before);
+    const int64_t x0 = tiles_of(threadIdx.x);
+    int64_t mine = x0, before0;
+    for (int b = threadIdx.x + kThreads; b < c.batch; b += kThreads) mine += tiles_of(b);
+    const int64_t total = block_sum(mine, before0);
     const int64_t used = shares_used(total, a.shares);
     const int64_t begin = share < used ? share_begin(share, total, used) : total;
     const int64_t end = share < used ? share_begin(share + 1, total, used) : total;
     if (lane == 0) s_start[warp] = begin;
+    __syncthreads();
     int64_t first = 0;
     for (int b0 = 0; b0 < c.batch; b0 += kThreads) {
-        const int64_t x = tiles_of(b0 + threadIdx.x);
-        const int64_t sum = block_sum(x, before);  // (its barriers also order s_start)
+        // (a batch that fits the block has its sums from above)
+        int64_t x = x0, before = before0, sum = total;
+        if (c.batch > kThreads) x = tiles_of(b0 + threadIdx.x), sum = block_sum(x, before);
         if (blockIdx.x == 0 && b0 + threadIdx.x < c.batch) a.ws.first[b0 + threadIdx.x] = first + before;
         for (int w = 0; w < kWarps; ++w) {
             const int64_t off = s_start[w] - first - before;
@@ -390,51 +393,84 @@ __global__ void __launch_bounds__(kThreads, 1) kda_attn_decode_kernel(const Args
     cp_async_wait<0>();
 }
 
-// One warp for a (row, query head): rows without a token, and the parts of items cut between shares, in
-// the shares' order.
+// Four warps for a (row, query head): rows without a token, and the parts of items cut between shares. A
+// warp takes every fourth part, so that a short cache cut into many parts costs a few loads in a row
+// (one warp for all parts took 13 us for 32 of them); the warps' sums are joined in order.
 constexpr int kJoinWarps = 4;
 
 __global__ void __launch_bounds__(kJoinWarps * 32) kda_attn_join_kernel(const Args a) {
+    __shared__ float s_m[kJoinWarps], s_l[kJoinWarps];
+    __shared__ float4 s_o[kJoinWarps][32];
     const AttnDecodeArgs &p = a.p;
-    const int head = blockIdx.x * kJoinWarps + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-    pdl_launch_dependents();
-    pdl_wait();
-    if (head >= p.c.batch * p.num_q_heads) return;
+    const int head = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int b = head / p.num_q_heads, hq = head - b * p.num_q_heads, h = hq / p.group, in_group = hq - h * p.group;
     const int item = h * a.q_tiles + in_group / kRows, row = in_group % kRows;
-    const int items = p.c.num_kv_heads * a.q_tiles;
-    const int64_t total = a.ws.first[p.c.batch], lo = a.ws.first[b], tiles = (a.ws.first[b + 1] - lo) / items;
-    uint2 *const out = reinterpret_cast<uint2 *>(p.out + (size_t)head * kHeadDim) + lane;
+    const int n = row_length(p.c, b, p.status, false);
+    const int64_t tiles = (n + kTokens - 1) / kTokens;
+    pdl_launch_dependents();
+    pdl_wait();
     if (tiles == 0) {
-        *out = make_uint2(0, 0);
-        if (lane == 0) {
+        if (threadIdx.x == 0) {
             if (p.lse) p.lse[head] = kNegInf;
             a.ws.lse2[head] = kNegInf;
         }
+        if (warp == 0) reinterpret_cast<uint2 *>(p.out + (size_t)head * kHeadDim)[lane] = make_uint2(0, 0);
         return;
     }
+    const int64_t total = a.ws.first[p.c.batch], x0 = a.ws.first[b] + item * tiles;
     const int64_t used = shares_used(total, a.shares);
-    const int64_t x0 = lo + item * tiles;
     const int64_t s0 = share_of(x0, total, used), s1 = share_of(x0 + tiles - 1, total, used);
-    if (s0 == s1) return;
-    auto part_of = [&](int64_t s) { return a.ws.parts + 2 * s + (s == s0 ? 1 : 0); };
-    float top = kNegInf;
-    for (int64_t s = s0 + lane; s <= s1; s += 32) top = fmaxf(top, part_of(s)->m[row]);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    const float ref = top == kNegInf ? 0.0f : top;
-    float l = 0.0f;
+    if (s0 == s1) return;  // finished by its warp
+    float m = kNegInf, l = 0.0f;
     float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
-    for (int64_t s = s0; s <= s1; ++s) {
-        const Part *const part = part_of(s);
-        const float f = ex2(part->m[row] - ref);
-        const float4 x = *reinterpret_cast<const float4 *>(&part->o[row][4 * lane]);
-        l = fmaf(part->l[row], f, l);
+    constexpr int kAhead = 8;
+    for (int64_t s = s0 + warp; s <= s1; s += kAhead * kJoinWarps) {
+        float pm[kAhead], pl[kAhead];
+        float4 po[kAhead];
+        float top = m;
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            const int64_t x = s + i * kJoinWarps;
+            pm[i] = kNegInf, pl[i] = 0.0f, po[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            if (x <= s1) {
+                const Part *const part = a.ws.parts + 2 * x + (x == s0 ? 1 : 0);
+                pm[i] = part->m[row], pl[i] = part->l[row];
+                po[i] = *reinterpret_cast<const float4 *>(&part->o[row][4 * lane]);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) top = fmaxf(top, pm[i]);
+        const float ref = top == kNegInf ? 0.0f : top, keep = ex2(m - ref);
+        l *= keep;
+        o = make_float4(o.x * keep, o.y * keep, o.z * keep, o.w * keep);
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            const float f = ex2(pm[i] - ref);
+            l = fmaf(pl[i], f, l);
+            o = make_float4(fmaf(po[i].x, f, o.x), fmaf(po[i].y, f, o.y), fmaf(po[i].z, f, o.z), fmaf(po[i].w, f, o.w));
+        }
+        m = top;
+    }
+    if (lane == 0) s_m[warp] = m, s_l[warp] = l;
+    s_o[warp][lane] = o;
+    __syncthreads();
+    if (warp > 0) return;
+    float top = kNegInf;
+#pragma unroll
+    for (int w = 0; w < kJoinWarps; ++w) top = fmaxf(top, s_m[w]);
+    const float ref = top == kNegInf ? 0.0f : top;
+    l = 0.0f;
+    o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+    for (int w = 0; w < kJoinWarps; ++w) {
+        const float f = ex2(s_m[w] - ref);
+        const float4 x = s_o[w][lane];
+        l = fmaf(s_l[w], f, l);
         o = make_float4(fmaf(x.x, f, o.x), fmaf(x.y, f, o.y), fmaf(x.z, f, o.z), fmaf(x.w, f, o.w));
     }
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-    *out = make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
+    reinterpret_cast<uint2 *>(p.out + (size_t)head * kHeadDim)[lane] =
+        make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
     if (lane == 0) {
         const float v = l == 0.0f ? kNegInf : ref + log2f(l);
         if (p.lse) p.lse[head] = v * kLn2;
@@ -519,8 +555,7 @@ cudaError_t launch_attn_decode(const AttnDecodeArgs &p, cudaStream_t stream) {
     workspace_layout(&a.ws, static_cast<char *>(p.ws), p.c.batch, p.num_q_heads, p.c.capacity, p.weight != nullptr, a.shares);
     e = launch(kda_attn_decode_kernel, dim3((unsigned)sms), kThreads, kSmem, stream, false, a);
     if (e != cudaSuccess) return e;
-    const unsigned heads = (unsigned)p.c.batch * (unsigned)p.num_q_heads;
-    e = launch(kda_attn_join_kernel, dim3((heads + kJoinWarps - 1) / kJoinWarps), kJoinWarps * 32, 0, stream, true, a);
+    e = launch(kda_attn_join_kernel, dim3((unsigned)p.c.batch * (unsigned)p.num_q_heads), kJoinWarps * 32, 0, stream, true, a);
     if (e != cudaSuccess || !p.weight) return e;
     const dim3 grid((unsigned)(p.c.batch * p.c.num_kv_heads), (unsigned)std::min((p.c.capacity + kWeightTokens - 1) / kWeightTokens, 65535));
     return launch(kda_attn_weight_kernel, grid, kWeightThreads, 0, stream, true, a);

@@ -29,6 +29,9 @@ constexpr int kSelElems = 4;                        // tokens per thread of a ti
 constexpr int kSelTile = kSelThreads * kSelElems;
 constexpr int kBins = 256;
 
+__device__ __forceinline__ void pdl_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // Unsigned key with the weights' order; NaN as -inf, -0 as +0.
 __device__ __forceinline__ uint32_t weight_key(float w) {
     if (w != w) w = -INFINITY;
@@ -39,6 +42,7 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
 __global__ void __launch_bounds__(kSelThreads) kda_evict_select_kernel(const CacheEvictArgs a) {
     __shared__ uint32_t s_hist[kBins], s_pick[2];
     __shared__ uint64_t s_warp[kSelWarps];
+    pdl_launch_dependents();
     const int bh = blockIdx.x, b = bh / a.c.num_kv_heads, h = bh - b * a.c.num_kv_heads;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int n = row_length(a.c, b, a.status, tid == 0 && h == 0);
@@ -140,54 +144,74 @@ __global__ void __launch_bounds__(kSelThreads) kda_evict_select_kernel(const Cac
 constexpr int kCopyThreads = 256;
 constexpr int kCopyUnroll = 8;
 
-// kVecs: 16-byte vectors of a token's row that this CTA's slice holds (16, 8 or 4).
-template <int kVecs>
+// kVecs: 16-byte vectors of a token's row that this CTA's slice holds (16, 8 or 4). kOrdered: in place, a
+// tile is read by all before any of it is written.
+template <int kVecs, bool kOrdered>
 __global__ void __launch_bounds__(kCopyThreads) kda_evict_copy_kernel(const CacheEvictArgs a, int rows_per_cta) {
     constexpr int kSlices = 16 / kVecs;
     constexpr int kStep = kCopyThreads / kVecs;  // tokens of one pass over the threads
+    constexpr int kTile = kStep * kCopyUnroll;
     const PagedCache &c = a.c;
     const int bh = blockIdx.x, b = bh / c.num_kv_heads, h = bh - b * c.num_kv_heads;
     const int slice = blockIdx.y % kSlices;
     const bool values = blockIdx.y >= kSlices;
     const int m = min(row_length(c, b, a.status, false), a.budget);  // (the same from the new lengths)
+    const int64_t begin = (int64_t)blockIdx.z * rows_per_cta;
+    const int end = (int)min((int64_t)m, begin + rows_per_cta);
+    pdl_wait();  // the selection is complete
     if (blockIdx.y == 0 && blockIdx.z == 0 && h == 0 && threadIdx.x == 0) a.new_lens[b] = m;
     __nv_bfloat16 *const cache = values ? c.v : c.k;
     const int64_t stride = values ? c.v_page_stride : c.k_page_stride;
     const int32_t *const kept = a.kept + (size_t)bh * a.budget;
     const int32_t *const from = c.block_table + (size_t)b * c.max_pages, *const to = a.dst_table + (size_t)b * c.max_pages;
-    const int col = (slice * kVecs + threadIdx.x % kVecs) * 8, first = threadIdx.x / kVecs;
-    const int mask = c.page_size - 1;
-    const int end = min((int64_t)m, ((int64_t)blockIdx.z + 1) * rows_per_cta);
-    for (int i0 = blockIdx.z * rows_per_cta; i0 < end; i0 += kStep * kCopyUnroll) {
+    const int first = threadIdx.x / kVecs, mask = c.page_size - 1;
+    const size_t base = (size_t)h * c.page_size * kHeadDim + (slice * kVecs + threadIdx.x % kVecs) * 8;
+    // A token's move: its source and destination in the cache (equal: nothing to do). The moves of the next
+    // tile are looked up while this one's rows are on their way.
+    auto look_up = [&](int i, int64_t &src, int64_t &dst) {
+        src = dst = 0;
+        if (i >= end) return;
+        const int j = kept[i], ps = from[j >> c.page_shift], pd = to[i >> c.page_shift];
+        if (ps < 0 || ps >= c.num_pages || pd < 0 || pd >= c.num_pages) {
+            report_error(a.status, KDA_ERR_DEVICE_INPUT, b);
+            return;
+        }
+        src = (int64_t)ps * stride + (int64_t)(j & mask) * kHeadDim;
+        dst = (int64_t)pd * stride + (int64_t)(i & mask) * kHeadDim;
+    };
+    int64_t src[kCopyUnroll], dst[kCopyUnroll];
+#pragma unroll
+    for (int u = 0; u < kCopyUnroll; ++u) look_up((int)begin + u * kStep + first, src[u], dst[u]);
+    for (int i0 = (int)begin; i0 < end; i0 += kTile) {
         uint4 x[kCopyUnroll];
-        __nv_bfloat16 *at[kCopyUnroll];
+        int64_t at[kCopyUnroll];
 #pragma unroll
         for (int u = 0; u < kCopyUnroll; ++u) {
-            const int i = i0 + u * kStep + first;
-            at[u] = nullptr;
-            if (i >= end) continue;
-            const int j = kept[i], ps = from[j >> c.page_shift], pd = to[i >> c.page_shift];
-            if (ps < 0 || ps >= c.num_pages || pd < 0 || pd >= c.num_pages) {
-                report_error(a.status, KDA_ERR_DEVICE_INPUT, b);
-                continue;
-            }
-            if (ps == pd && ((i ^ j) & mask) == 0) continue;  // stays where it is
-            at[u] = cache + (size_t)pd * stride + ((size_t)h * c.page_size + (i & mask)) * kHeadDim + col;
-            x[u] = *reinterpret_cast<const uint4 *>(cache + (size_t)ps * stride +
-                                                    ((size_t)h * c.page_size + (j & mask)) * kHeadDim + col);
+            at[u] = src[u] == dst[u] ? -1 : dst[u];
+            if (at[u] >= 0) x[u] = *reinterpret_cast<const uint4 *>(cache + base + src[u]);
         }
-        __syncthreads();  // the tile is read before any of it is overwritten
+        if (i0 + kTile < end)
+#pragma unroll
+            for (int u = 0; u < kCopyUnroll; ++u) look_up(i0 + kTile + u * kStep + first, src[u], dst[u]);
+        if (kOrdered) __syncthreads();  // the tile is read before any of it is overwritten
 #pragma unroll
         for (int u = 0; u < kCopyUnroll; ++u)
-            if (at[u]) *reinterpret_cast<uint4 *>(at[u]) = x[u];
+            if (at[u] >= 0) *reinterpret_cast<uint4 *>(cache + base + at[u]) = x[u];
     }
 }
 
-template <int kVecs>
+template <int kVecs, bool kOrdered>
 cudaError_t launch_copy(const CacheEvictArgs &a, int rows_per_cta, unsigned parts, cudaStream_t stream) {
-    const dim3 grid((unsigned)(a.c.batch * a.c.num_kv_heads), 2 * (16 / kVecs), parts);
-    kda_evict_copy_kernel<kVecs><<<grid, kCopyThreads, 0, stream>>>(a, rows_per_cta);
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(a.c.batch * a.c.num_kv_heads), 2 * (16 / kVecs), parts);
+    cfg.blockDim = dim3(kCopyThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kda_evict_copy_kernel<kVecs, kOrdered>, a, rows_per_cta);
 }
 
 }  // namespace
@@ -199,16 +223,18 @@ cudaError_t launch_cache_evict(const CacheEvictArgs &a, cudaStream_t stream) {
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     const int most = std::min(a.budget, a.c.capacity);  // tokens a row can keep
-    if (a.dst_table != a.c.block_table) {
-        const int rows = 512;
-        const unsigned parts = (unsigned)std::min<int64_t>(((int64_t)most + rows - 1) / rows, 4096);
-        const int per = (int)(((int64_t)most + parts - 1) / parts);
-        return launch_copy<16>(a, per, parts, stream);
-    }
     const int64_t ctas = (int64_t)a.c.batch * a.c.num_kv_heads * 2;
-    if (ctas >= 4 * sms) return launch_copy<16>(a, most, 1, stream);
-    if (ctas >= 2 * sms) return launch_copy<8>(a, most, 1, stream);
-    return launch_copy<4>(a, most, 1, stream);
+    if (a.dst_table != a.c.block_table) {
+        // one tile a CTA, or up to four where that still leaves several CTAs for every SM
+        const int tile = 16 * kCopyUnroll;
+        const int64_t tiles = (most + tile - 1) / tile;
+        const int64_t per = std::max<int64_t>((tiles + 65534) / 65535, std::min<int64_t>(4, ctas * tiles / (8 * sms)));
+        const int rows = (int)(std::max<int64_t>(per, 1) * tile);
+        return launch_copy<16, false>(a, rows, (unsigned)(((int64_t)most + rows - 1) / rows), stream);
+    }
+    if (ctas >= 4 * sms) return launch_copy<16, true>(a, most, 1, stream);
+    if (ctas >= 2 * sms) return launch_copy<8, true>(a, most, 1, stream);
+    return launch_copy<4, true>(a, most, 1, stream);
 }
 
 }  // namespace kda
