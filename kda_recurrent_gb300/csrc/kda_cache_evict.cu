@@ -28,7 +28,8 @@ constexpr int kSelThreads = 1024;
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kSelElems = 4;                        // tokens per thread of a tile
 constexpr int kSelTile = kSelThreads * kSelElems;
-constexpr int kHeld = 4;                            // tiles whose keys stay in registers
+constexpr int kHeld = 4;                            // tiles of a block, held in registers together
+constexpr int kBlock = kHeld * kSelTile;
 constexpr int kBins = 2048;
 
 __device__ __forceinline__ void pdl_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
@@ -66,10 +67,14 @@ __global__ void __launch_bounds__(kSelThreads, 1) kda_evict_select_kernel(const 
         }
         return;
     }
-    // the first kHeld tiles stay in registers for all passes; later tiles are read again
+    // a row of one block stays in registers for all passes; a longer one is read again by each, a block's
+    // loads together
     float4 held[kHeld];
+    auto load_block = [&](int j0) {
 #pragma unroll
-    for (int i = 0; i < kHeld; ++i) held[i] = four_weights(w, i * kSelTile + 4 * tid, n);
+        for (int i = 0; i < kHeld; ++i) held[i] = four_weights(w, j0 + i * kSelTile + 4 * tid, n);
+    };
+    load_block(0);
     const int lo = a.sink, hi = n - a.recent;  // candidates: [lo, hi), more than are needed
     uint32_t need = a.budget - a.sink - a.recent, prefix = 0;
     if (need > 0) {
@@ -83,18 +88,15 @@ __global__ void __launch_bounds__(kSelThreads, 1) kda_evict_select_kernel(const 
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const uint32_t key = weight_key(x[e]);
-                    const bool in = j + e >= lo && j + e < hi && (key & above) == prefix;
-                    const uint32_t active = __ballot_sync(0xffffffffu, in);
-                    if (!in) continue;
-                    // lanes that share a digit add up once: equal and nearly equal weights are common
-                    const uint32_t bin = (key >> shift) & (bins - 1), same = __match_any_sync(active, bin);
-                    if (lane == __ffs(same) - 1) atomicAdd(&s_hist[bin], __popc(same));
+                    // (adding up equal digits of a warp first, by a match, took longer than their conflicts)
+                    if (j + e >= lo && j + e < hi && (key & above) == prefix) atomicAdd(&s_hist[(key >> shift) & (bins - 1)], 1u);
                 }
             };
+            for (int j0 = 0; j0 < n; j0 += kBlock) {
+                if (n > kBlock) load_block(j0);
 #pragma unroll
-            for (int i = 0; i < kHeld; ++i)
-                if (i * kSelTile < n) count(held[i], i * kSelTile + 4 * tid);
-            for (int j0 = kHeld * kSelTile; j0 < n; j0 += kSelTile) count(four_weights(w, j0 + 4 * tid, n), j0 + 4 * tid);
+                for (int i = 0; i < kHeld; ++i) count(held[i], j0 + i * kSelTile + 4 * tid);
+            }
             __syncthreads();
             // thread i owns digits 2 i and 2 i + 1; the digit where the count from above reaches `need`
             const uint32_t c0 = s_hist[2 * tid], c1 = s_hist[2 * tid + 1];
@@ -164,10 +166,12 @@ __global__ void __launch_bounds__(kSelThreads, 1) kda_evict_select_kernel(const 
         run += total;
         odd ^= 1;
     };
+    for (int j0 = 0; j0 < n; j0 += kBlock) {
+        if (n > kBlock) load_block(j0);  // (in place: no token of this block has been overwritten yet)
 #pragma unroll
-    for (int i = 0; i < kHeld; ++i)
-        if (i * kSelTile < n) emit(held[i], i * kSelTile + 4 * tid);
-    for (int j0 = kHeld * kSelTile; j0 < n; j0 += kSelTile) emit(four_weights(w, j0 + 4 * tid, n), j0 + 4 * tid);
+        for (int i = 0; i < kHeld; ++i)
+            if (j0 + i * kSelTile < n) emit(held[i], j0 + i * kSelTile + 4 * tid);
+    }
     __syncthreads();  // (in place: every tile is done before its tail is cleared)
     for (int i = m + tid; i < n; i += kSelThreads) dst[i] = 0.0f;
 }
