@@ -2,9 +2,14 @@
 //
 //     S <- exp(g) S + k v^T,   o = scale S^T q      for every (row, head), in place
 //
-// The state is the whole cost: 64 KiB (FP32) or 32 KiB (BF16) read and written per item. One
-// CTA per item; thread (r, c) owns 16 bytes of columns (c) of every kRows-th row of the state
-// and sums its rows' share of the outputs, which are joined through shared memory.
+// The state is the whole cost: 64 KiB (FP32) or 32 KiB (BF16) read and written per item, so this
+// is an HBM stream. A CTA owns a block of kWidth columns of one item's state (columns are
+// independent); a thread owns 16 bytes of columns of every kRows-th row, issues all its loads before any
+// arithmetic, and sums its rows' share of the outputs, which are joined by shuffles and through
+// shared memory in a fixed order. Whole items (128 columns) when there are many, narrower blocks, down
+// to 16 columns, when there are few, so that one user's token still spreads over the GPU.
+#include <type_traits>
+
 #include "kda_internal.cuh"
 
 namespace kda {
@@ -46,63 +51,89 @@ struct Vec<__nv_bfloat16> {
     }
 };
 
-template <typename T>
+template <typename T, int kWidth>
 __global__ void __launch_bounds__(kThreads) kda_linear_decode_kernel(const LinearDecodeArgs a) {
     using V = Vec<T>;
     constexpr int E = V::kElems;
-    constexpr int kCols = kHeadDim / E;       // threads across a row
+    constexpr int kCols = kWidth / E;         // threads across a row
     constexpr int kRows = kThreads / kCols;   // rows in flight
-    __shared__ float s_q[kHeadDim], s_k[kHeadDim], s_o[kRows][kHeadDim];
-    const int item = blockIdx.x, r = item / a.num_heads, h = item - r * a.num_heads;
+    constexpr int kPasses = kHeadDim / kRows > 0 ? kHeadDim / kRows : 1;
+    constexpr int kBlocks = kHeadDim / kWidth;
+    static_assert(kRows <= kHeadDim, "every thread has a row");
+    __shared__ float s_q[kHeadDim], s_k[kHeadDim], s_o[kThreads / 32][kWidth];
+    const int item = blockIdx.x / kBlocks, j0 = (blockIdx.x - item * kBlocks) * kWidth;
+    const int r = item / a.num_heads, h = item - r * a.num_heads;
     const int tid = threadIdx.x;
     const size_t tok = (size_t)item * kHeadDim;
     const int32_t slot = a.slot_idx[r];
     if (slot < 0 || slot >= a.num_slots) {
-        if (slot >= 0 && tid == 0) report_error(a.status, KDA_ERR_DEVICE_INPUT, r);
-        if (tid < kHeadDim) a.out[tok + tid] = __float2bfloat16_rn(0.0f);
+        if (slot >= 0 && tid == 0 && h == 0 && j0 == 0) report_error(a.status, KDA_ERR_DEVICE_INPUT, r);
+        if (tid < kWidth) a.out[tok + j0 + tid] = __float2bfloat16_rn(0.0f);
         return;
     }
+    const int cg = tid % kCols, rg = tid / kCols;
+    uint4 *const S = reinterpret_cast<uint4 *>(static_cast<T *>(a.state_pool) +
+                                               ((size_t)slot * a.num_heads + h) * (kHeadDim * kHeadDim) + rg * kHeadDim + j0) + cg;
+    constexpr int kStride = kRows * kHeadDim / E;  // from a thread's row to its next
+    uint4 w[kPasses];
+#pragma unroll
+    for (int i = 0; i < kPasses; ++i) w[i] = __ldcs(S + i * kStride);
     if (tid < kHeadDim) {
         s_q[tid] = __bfloat162float(a.q[tok + tid]);
         s_k[tid] = __bfloat162float(a.k[tok + tid]);
     }
-    __syncthreads();
-    const float decay = expf(a.log_decay[(size_t)r * a.decay_row_stride + h]);
-    const int cg = tid % kCols, rg = tid / kCols;
-    T *const S = static_cast<T *>(a.state_pool) + ((size_t)slot * a.num_heads + h) * (kHeadDim * kHeadDim);
     float v[E], o[E];
 #pragma unroll
-    for (int e = 0; e < E; ++e) v[e] = __bfloat162float(a.v[tok + cg * E + e]), o[e] = 0.0f;
-    for (int i = rg; i < kHeadDim; i += kRows) {
-        uint4 *const at = reinterpret_cast<uint4 *>(S + i * kHeadDim + cg * E);
+    for (int e = 0; e < E; ++e) v[e] = __bfloat162float(a.v[tok + j0 + cg * E + e]), o[e] = 0.0f;
+    const float decay = expf(a.log_decay[(size_t)r * a.decay_row_stride + h]);
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kPasses; ++i) {
+        const float q = s_q[rg + i * kRows], k = s_k[rg + i * kRows];
         float x[E];
-        V::unpack(*at, x);
+        V::unpack(w[i], x);
 #pragma unroll
         for (int e = 0; e < E; ++e) {
-            x[e] = fmaf(x[e], decay, s_k[i] * v[e]);
-            o[e] = fmaf(s_q[i], x[e], o[e]);
+            x[e] = fmaf(x[e], decay, k * v[e]);
+            o[e] = fmaf(q, x[e], o[e]);
         }
-        *at = V::pack(x);
+        __stcs(S + i * kStride, V::pack(x));
     }
 #pragma unroll
-    for (int e = 0; e < E; ++e) s_o[rg][cg * E + e] = o[e];
-    __syncthreads();
-    if (tid < kHeadDim) {
-        float sum = 0.0f;
-        for (int g = 0; g < kRows; ++g) sum += s_o[g][tid];
-        a.out[tok + tid] = __float2bfloat16_rn(a.scale * sum);
+    for (int e = 0; e < E; ++e) {
+#pragma unroll
+        for (int x = kCols; x < 32; x <<= 1) o[e] += __shfl_xor_sync(0xffffffffu, o[e], x);
+        if ((tid & 31) < kCols) s_o[tid >> 5][cg * E + e] = o[e];
     }
+    __syncthreads();
+    if (tid < kWidth) {
+        float sum = 0.0f;
+#pragma unroll
+        for (int g = 0; g < kThreads / 32; ++g) sum += s_o[g][tid];
+        a.out[tok + j0 + tid] = __float2bfloat16_rn(a.scale * sum);
+    }
+}
+
+template <typename T>
+cudaError_t launch_t(const LinearDecodeArgs &a, cudaStream_t stream) {
+    const int64_t items = (int64_t)a.rows * a.num_heads;
+    auto run = [&](auto width) {
+        constexpr int kWidth = decltype(width)::value;
+        const int64_t ctas = items * (kHeadDim / kWidth);
+        if (ctas > 0x7fffffffLL) return cudaErrorInvalidValue;
+        kda_linear_decode_kernel<T, kWidth><<<(unsigned)ctas, kThreads, 0, stream>>>(a);
+        return cudaGetLastError();
+    };
+    if (items >= 1024) return run(std::integral_constant<int, 128>());
+    if (items >= 256) return run(std::integral_constant<int, 64>());
+    if (items >= 64) return run(std::integral_constant<int, 32>());
+    return run(std::integral_constant<int, 16>());
 }
 
 }  // namespace
 
 cudaError_t launch_linear_decode(const LinearDecodeArgs &a, cudaStream_t stream) {
-    const unsigned items = (unsigned)a.rows * (unsigned)a.num_heads;
-    if (a.state_dtype == KDA_STATE_F32)
-        kda_linear_decode_kernel<float><<<items, kThreads, 0, stream>>>(a);
-    else
-        kda_linear_decode_kernel<__nv_bfloat16><<<items, kThreads, 0, stream>>>(a);
-    return cudaGetLastError();
+    return a.state_dtype == KDA_STATE_F32 ? launch_t<float>(a, stream) : launch_t<__nv_bfloat16>(a, stream);
 }
 
 }  // namespace kda
