@@ -26,7 +26,6 @@ Convenience wrappers ``prefill``, ``decode``, ``linear_prefill``, ``linear_decod
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 import threading
@@ -361,18 +360,26 @@ def decode(q, k, v, g_raw, beta, slot_idx, state_pool, *, scale, lower_bound=0.0
 # short too: plain integers for pointers and streams, one expression for a tensor's checks, and the
 # device switched only when it has to be.
 
-_NO_SWITCH = contextlib.nullcontext()
-
-
-def _on(device):
-    """Makes `device` current for the call (nothing to do when it is already)."""
+def _call(name, device, stream, *args):
+    """Calls C entry point `name` with `args` and a stream handle (None: the device's current stream,
+    by torch's raw query where it has one, which costs a twentieth of making a Stream object)."""
     import torch
-    return _NO_SWITCH if torch.cuda.current_device() == device.index else torch.cuda.device(device)
-
-
-def _stream_of(stream, device):
-    import torch
-    return (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
+    if device.type != "cuda":
+        _require_cuda(device)
+    index = device.index
+    if stream is not None:
+        handle = stream.cuda_stream
+    else:
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        handle = raw(index) if raw else torch.cuda.current_stream(device).cuda_stream
+    fn = getattr(_lib or load(), name)
+    if torch.cuda.current_device() == index:
+        st = fn(*args, handle)
+    else:
+        with torch.cuda.device(device):
+            st = fn(*args, handle)
+    if st != KDA_OK:
+        raise KdaError(st, name)
 
 
 def _address(t):
@@ -425,14 +432,9 @@ def kda_linear_prefill(q, k, v, log_decay, cu_seqlens, init_state, out, final_st
     if final_state is not None:
         _need(final_state, "final_state", f32, (N, H, d, d), dev)
     ws, nbytes = _workspace_arg(workspace, dev)
-    _require_cuda(dev)
-    with _on(dev):
-        st = (_lib or load()).kda_linear_prefill(
-            q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), per_token, cu_seqlens.data_ptr(),
-            _address(init_state), out.data_ptr(), _address(final_state), N, T, H, scale, ws, nbytes,
-            _stream_of(stream, dev))
-    if st != KDA_OK:
-        raise KdaError(st, "kda_linear_prefill")
+    _call("kda_linear_prefill", dev, stream,
+          q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), per_token, cu_seqlens.data_ptr(),
+          _address(init_state), out.data_ptr(), _address(final_state), N, T, H, float(scale), ws, nbytes)
 
 
 def kda_linear_prefill_workspace_size(num_seqs, total_tokens, num_heads, sm_count=0) -> int:
@@ -471,14 +473,10 @@ def kda_linear_decode(q, k, v, log_decay, slot_idx, state_pool, out, scale, stre
     if dtype is not torch.float32 and dtype is not bf16:
         raise TypeError("state_pool must be float32 or bfloat16")
     _need(state_pool, "state_pool", dtype, (slots, H, d, d), dev)
-    _require_cuda(dev)
-    with _on(dev):
-        st = (_lib or load()).kda_linear_decode(
-            q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), per_row, slot_idx.data_ptr(),
-            state_pool.data_ptr(), slots, STATE_DTYPES["bf16" if dtype is bf16 else "f32"], out.data_ptr(), R, H, scale,
-            _stream_of(stream, dev))
-    if st != KDA_OK:
-        raise KdaError(st, "kda_linear_decode")
+    _call("kda_linear_decode", dev, stream,
+          q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), per_row, slot_idx.data_ptr(),
+          state_pool.data_ptr(), slots, STATE_DTYPES["bf16" if dtype is bf16 else "f32"], out.data_ptr(), R, H,
+          float(scale))
 
 
 def _check_cache(k_cache, v_cache, block_table, seq_lens, device):
@@ -525,14 +523,10 @@ def kda_attn_decode(q, k_cache, v_cache, block_table, seq_lens, out, scale, work
     if weight is not None:
         _need(weight, "weight", torch.float32, (B, Hkv, P * ps), dev)
     ws, nbytes = _workspace_arg(workspace, dev)
-    _require_cuda(dev)
-    with _on(dev):
-        st = (_lib or load()).kda_attn_decode(
-            q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), ks, vs, pages, ps, block_table.data_ptr(), P,
-            seq_lens.data_ptr(), out.data_ptr(), _address(lse), _address(weight), B, Hq, Hkv, scale, ws, nbytes,
-            _stream_of(stream, dev))
-    if st != KDA_OK:
-        raise KdaError(st, "kda_attn_decode")
+    _call("kda_attn_decode", dev, stream,
+          q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), ks, vs, pages, ps, block_table.data_ptr(), P,
+          seq_lens.data_ptr(), out.data_ptr(), _address(lse), _address(weight), B, Hq, Hkv,
+          float(scale), ws, nbytes)
 
 
 def kda_attn_decode_workspace_size(batch, num_q_heads, num_kv_heads, max_pages, page_size, with_weight=False,
@@ -570,14 +564,10 @@ def kda_cache_evict(k_cache, v_cache, block_table, seq_lens, weight, new_lens, k
         _need(dst_table, "dst_table", torch.int32, (B, P), dev)
     _need(new_lens, "new_lens", torch.int32, (B,), dev)
     _need(kept, "kept", torch.int32, (B, Hkv, budget), dev)
-    _require_cuda(dev)
-    with _on(dev):
-        st = (_lib or load()).kda_cache_evict(
-            k_cache.data_ptr(), v_cache.data_ptr(), ks, vs, pages, ps, block_table.data_ptr(), _address(dst_table), P,
-            seq_lens.data_ptr(), weight.data_ptr(), dst_weight.data_ptr(), new_lens.data_ptr(), kept.data_ptr(), B, Hkv,
-            budget, sink, recent, _stream_of(stream, dev))
-    if st != KDA_OK:
-        raise KdaError(st, "kda_cache_evict")
+    _call("kda_cache_evict", dev, stream,
+          k_cache.data_ptr(), v_cache.data_ptr(), ks, vs, pages, ps, block_table.data_ptr(), _address(dst_table), P,
+          seq_lens.data_ptr(), weight.data_ptr(), dst_weight.data_ptr(), new_lens.data_ptr(), kept.data_ptr(), B, Hkv,
+          int(budget), int(sink), int(recent))
 
 
 def linear_prefill(q, k, v, log_decay, cu_seqlens, init_state=None, *, scale, want_final=True, workspace=None,

@@ -20,15 +20,14 @@
 //   warp 0        a chunk's prefix and suffix sums of g, and its TMA loads: Q, K, V tiles (128-byte
 //                 swizzle) into a ring of five 32 KiB tiles
 //   warp 1        issues every MMA: A, Q S, D by quarters of 32 tokens (hi then lo), P V
-//   warps 4-11    A -> P in place in tensor memory; the second half of V -> hi, lo; O: both accumulators
-//                 -> BF16 -> the tile that held V -> TMA store
-//   warps 12-19   S in registers (row dk, 64 columns a thread): the update and the operand of Q S; the
-//                 first half of the next chunk's V -> hi, lo
-// hi and lo pass through a ring of two quarters. The values are decayed, not the keys, because V is only
-// read by the last product of the chunk, so that the split needs no scores; it is shared out so that
-// each group does its part where it would wait for the tensor core. (All of it on warps 12-19 made their
-// work the longest chain of a chunk, two extra warps took 1.5k cycles a quarter, and four extra warps
-// left too few registers for the state.) O leaves through shared memory because a
+//   warps 4-11    A -> P in place in tensor memory, then O: both accumulators -> BF16 -> the tile that
+//                 held V -> TMA store
+//   warps 12-19   S in registers (row dk, 64 columns a thread): the update and the operand of Q S; V ->
+//                 hi, lo by quarters into a ring of two
+// The values are decayed, not the keys, because V is only read by the last product of the chunk, so that
+// the split needs no scores. (Half of it on warps 4-11 put it on the chain from the scores to P V: 8%
+// slower; two extra warps took 1.5k cycles a quarter; four extra warps left too few registers for the
+// state. Half of D before Q S: 9% slower, since Q's tile, which the next V replaces, is then freed late.) O leaves through shared memory because a
 // thread's row-wise 32-byte stores (32 rows an instruction) kept the load/store unit busy for 2k
 // cycles a chunk, during which the MMAs' operand reads took four times their time (2.56 ms at
 // 8 x 16384 x 96 heads).
@@ -66,8 +65,7 @@ constexpr float kMinLogDecay = -128.0f;
 
 constexpr int kWarpMma = 1, kWarpAlloc = 2, kWarpO = 4, kWarpS = 12;
 constexpr int kOutWarps = 8, kStateWarps = 8;
-constexpr int kGroup = 256;  // threads of each of the two groups
-static_assert(kOutWarps * 32 == kGroup && kStateWarps * 32 == kGroup, "both groups split quarters");
+constexpr int kStateThreads = kStateWarps * 32;
 constexpr int kThreads = (kWarpS + kStateWarps) * 32;
 
 struct Gates {
@@ -290,9 +288,9 @@ __device__ __forceinline__ Span span_of(const LinearPrefillArgs &a, int n, int w
     return s;
 }
 
-// hi and lo of 32 tokens of V, by the 256 threads of a group: row t of the quarter at `tile` (eight
-// threads a row, a thread the same 16 bytes of both halves) times its factor f, rows past the last
-// token as zeros, into the split stage at `to`.
+// hi and lo of 32 tokens of V by the state warps: a row of the quarter at `tile` (eight threads a row, a
+// thread the same 16 bytes of both halves) times its factor f, rows past the last token as zeros, into
+// the split stage at `to`.
 __device__ __forceinline__ void split_quarter(const uint8_t *tile, uint8_t *to, float f, bool live) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -364,7 +362,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < kRing; ++i) mbar_init(&B->full[i], 1), mbar_init(&B->empty[i], 1);
         mbar_init(&B->scores, 1);
         mbar_init(&B->p, kOutWarps);
-        for (int i = 0; i < 2; ++i) mbar_init(&B->split[i], kGroup / 32), mbar_init(&B->split_free[i], 1);
+        for (int i = 0; i < 2; ++i) mbar_init(&B->split[i], kStateWarps), mbar_init(&B->split_free[i], 1);
         for (int i = 0; i < 2; ++i) mbar_init(&B->stored[i], kOutWarps);
         mbar_init(&B->tail, kStateWarps);
         mbar_init(&B->d, 1);
@@ -373,7 +371,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(&B->qs, 1);
         mbar_init(&B->o, 1);
         mbar_init(&B->o_free, kOutWarps);
-        for (int i = 0; i < 2; ++i) mbar_init(&B->gate[i], 1), mbar_init(&B->gate_free[i], kStateWarps + kOutWarps);
+        for (int i = 0; i < 2; ++i) mbar_init(&B->gate[i], 1), mbar_init(&B->gate_free[i], kStateWarps + (kStates ? 0 : kOutWarps));
         mbar_init(&B->drain, 1);
         // the swizzled tiles are laid out for a 1024-byte-aligned base
         B->abort = (smem_addr(smem) & 1023u) != 0;
@@ -398,24 +396,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr int kPer = kStates ? 2 : 3;  // tiles of a chunk: (Q,) K, V
     const int last_rows = sp.eos - sp.bos - (nchunks - 1) * kC;  // of the last chunk
     int issued = 0;                        // loads issued (warp 0)
-    // Quarters [q0, q0 + 2) of chunk c, those that it has, by the 256 threads of a group (thread tid); the
-    // quarters of all chunks count through the ring of two stages (only the last chunk may have fewer
-    // than four).
-    auto split = [&](int c, int q0, int tid) {
-        if (c >= updates) return true;
-        const int L = c + 1 < nchunks ? kC : last_rows;
-        const Gates *G = reinterpret_cast<const Gates *>(smem + kGates) + (c & 1);
-        const uint8_t *const tile = smem + ((c * kPer + kPer - 1) % kRing) * kTile;
-#pragma unroll 1
-        for (int q = q0; q < q0 + 2 && q * kQuarter < L; ++q) {
-            const int use = 4 * c + q, st = use & 1, t = q * kQuarter + (tid >> 3);
-            if (use >= 2 && !wait_warp(&B->split_free[st], ((use >> 1) - 1) & 1, B, p.status)) return false;
-            split_quarter(tile + q * kQuarter * 128 + tid * 16, smem + kSplit + st * kSplitStage + tid * 16, G->suffix[t], t < L);
-            fence_async_smem();
-            arrive_warp(&B->split[st]);
-        }
-        return true;
-    };
 
     if (B->abort) {
         // nothing has started
@@ -476,7 +456,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (kStates && lane == 0) a.decay[(size_t)lc * W + w] = run;
     } else if (warp == kWarpMma) {
-        int quarter = 0;
         for (int c = 0; c < nchunks; ++c) {
             const int iq = c * kPer, ik = iq + kPer - 2, iv = ik + 1;
             const uint32_t k = base + (ik % kRing) * kTile, q = base + (iq % kRing) * kTile, v = base + (iv % kRing) * kTile;
@@ -506,16 +485,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (c < updates) {
                 if (c > 0 && !wait_warp(&B->d_free, (c - 1) & 1, B, p.status)) break;
                 bool lost = false;
-                for (int t = 0; t < L; t += kQuarter, ++quarter) {
-                    const int st = quarter & 1;
-                    lost = !wait_warp(&B->split[st], (quarter >> 1) & 1, B, p.status);
+#pragma unroll 1
+                for (int q = 0; q * kQuarter < L; ++q) {
+                    const int use = 4 * c + q, st = use & 1;
+                    lost = !wait_warp(&B->split[st], (use >> 1) & 1, B, p.status);
                     if (lost) break;
                     tc_fence_after();
-                    const uint64_t da = at(kDescMn, k + t * 128), db = at(kDescSplit, base + kSplit + st * kSplitStage);
+                    const uint64_t da = at(kDescMn, k + q * kQuarter * 128), db = at(kDescSplit, base + kSplit + st * kSplitStage);
 #pragma unroll
                     for (int s = 0; s < 4; ++s)  // hi, hi, lo, lo
                         mma_ss(tmem + kColD, da + (s & 1) * 128, db + (((s >> 1) * kSplitLo + (s & 1) * 2048) >> 4), kIdescD,
-                               t > 0 || s > 0);
+                               q > 0 || s > 0);
                     commit(&B->split_free[st]);
                 }
                 if (lost) break;
@@ -541,21 +521,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         commit(&B->drain);  // every earlier commit has reached its barrier when this one has
         mbar_wait(&B->drain, 0);
-    } else if (warp < kWarpO) {
+    } else if (warp < kWarpO || (kStates && warp < kWarpS)) {
         // idle
     } else if (warp < kWarpS) {
         const int quad = warp & 3, half = (warp - kWarpO) >> 2, row = 32 * quad + lane;
-        const int tid = threadIdx.x - kWarpO * 32;
         const uint32_t lanes = tmem + ((uint32_t)(32 * quad) << 16);
         for (int c = 0; c < nchunks; ++c) {
             const Gates *G = reinterpret_cast<const Gates *>(smem + kGates) + (c & 1);
             const int iv = c * kPer + kPer - 1;
             if (!wait_warp(&B->gate[c & 1], (c >> 1) & 1, B, p.status)) break;
-            if (kStates) {
-                if (!wait_warp(&B->full[iv % kRing], (iv / kRing) & 1, B, p.status) || !split(c, 2, tid)) break;
-                arrive_warp(&B->gate_free[c & 1]);
-                continue;
-            }
             const float gi = G->prefix[row], lam = p.scale * ex2(gi);
             if (!wait_warp(&B->scores, c & 1, B, p.status)) break;
             tc_fence_after();
@@ -588,13 +562,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_wait_st();
             tc_fence_before();
             arrive_warp(&B->p);
+            if (lane == 0) mbar_arrive(&B->gate_free[c & 1]);
             if (c > 0 && lane == 0) {  // by now the last chunk's store has read its tile
                 asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
                 mbar_arrive(&B->stored[(c - 1) & 1]);
             }
             __syncwarp();
-            if (!wait_warp(&B->full[iv % kRing], (iv / kRing) & 1, B, p.status) || !split(c, 2, tid)) break;
-            arrive_warp(&B->gate_free[c & 1]);
             if (!wait_warp(&B->o, c & 1, B, p.status)) break;
             tc_fence_after();
             // rows of 128 bytes into the V tile, which nobody reads any more; a warp whose rows are all
@@ -659,28 +632,47 @@ __global__ void __launch_bounds__(kThreads, 1)
             fence_async_smem();
             arrive_warp(&B->s);
         };
-        if (!kStates && nchunks > 0) publish();
         const int tid = threadIdx.x - kWarpS * 32;
-        // Opens chunk c: its gate sums and V are there; in a chunk that is not full, the rows past the last
-        // token are cleared (they hold another sequence's keys and values, which a zero in the other
-        // operand does not silence if they are not finite); then the first half of the split.
-        auto open_chunk = [&](int c) {
+        // Splits chunk c's V, once its gate sums and V are there. In a chunk that is not full, first clears the
+        // rows past the last token: they hold another sequence's keys and values, which a zero in the
+        // other operand does not silence if they are not finite. The quarters of all chunks count through
+        // the ring of two stages (only the last chunk may have fewer than four).
+        auto split = [&](int c) {
             const int ik = c * kPer + kPer - 2, iv = ik + 1;
             if (!wait_warp(&B->gate[c & 1], (c >> 1) & 1, B, p.status)) return false;
             if (!wait_warp(&B->full[iv % kRing], (iv / kRing) & 1, B, p.status)) return false;
             if (c + 1 == nchunks && last_rows < kC) {
                 if (!wait_warp(&B->full[ik % kRing], (ik / kRing) & 1, B, p.status)) return false;
                 uint8_t *const keys = smem + (ik % kRing) * kTile, *const values = smem + (iv % kRing) * kTile;
-                for (int x = tid; x < 2048; x += kGroup)
+                for (int x = tid; x < 2048; x += kStateThreads)
                     if (((x & 1023) >> 3) >= last_rows)
                         *reinterpret_cast<uint4 *>(values + x * 16) = *reinterpret_cast<uint4 *>(keys + x * 16) = make_uint4(0, 0, 0, 0);
                 fence_async_smem();
                 arrive_warp(&B->tail);
             }
-            return split(c, 0, tid);
+            if (c >= updates) return true;
+            const int L = c + 1 < nchunks ? kC : last_rows;
+            const Gates *G = reinterpret_cast<const Gates *>(smem + kGates) + (c & 1);
+            const uint8_t *const tile = smem + (iv % kRing) * kTile + tid * 16;
+#pragma unroll 1
+            for (int q = 0; q * kQuarter < L; ++q) {
+                const int use = 4 * c + q, st = use & 1, t = q * kQuarter + (tid >> 3);
+                if (use >= 2 && !wait_warp(&B->split_free[st], ((use >> 1) - 1) & 1, B, p.status)) return false;
+                split_quarter(tile + q * kQuarter * 128, smem + kSplit + st * kSplitStage + tid * 16, G->suffix[t], t < L);
+                fence_async_smem();
+                arrive_warp(&B->split[st]);
+            }
+            return true;
         };
-        bool ok = nchunks == 0 || open_chunk(0);
-        for (int c = 0; c < nchunks && ok; ++c) {
+        bool ok = true;
+        for (int c = 0; c < nchunks; ++c) {
+            if (!kStates) {  // S for the queries
+                ok = c == 0 || wait_warp(&B->qs, (c - 1) & 1, B, p.status);
+                if (!ok) break;
+                publish();
+            }
+            ok = split(c);
+            if (!ok) break;
             const float decay = (reinterpret_cast<const Gates *>(smem + kGates) + (c & 1))->decay;
             arrive_warp(&B->gate_free[c & 1]);
             if (c < updates) {
@@ -698,14 +690,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc_fence_before();
                 arrive_warp(&B->d_free);  // (only with an update: an arrival for a chunk without one could complete
                                           // a second phase before the MMA warp has seen the first)
-            }
-            if (c + 1 < nchunks) {
-                if (!kStates) {
-                    ok = wait_warp(&B->qs, c & 1, B, p.status);
-                    if (!ok) break;
-                    publish();
-                }
-                ok = open_chunk(c + 1);
             }
         }
         pdl_wait();  // an initial state in the same place has been read by the launches before
