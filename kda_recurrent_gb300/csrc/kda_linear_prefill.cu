@@ -20,8 +20,9 @@
 //   warp 0        a chunk's prefix and suffix sums of g, and its TMA loads: Q, K, V tiles (128-byte
 //                 swizzle) into a ring of five 32 KiB tiles
 //   warp 1        issues every MMA: A, Q S, D by quarters of 32 tokens (hi then lo), P V
+//   warp 3        TMA stores of O
 //   warps 4-11    A -> P in place in tensor memory, then O: both accumulators -> BF16 -> the tile that
-//                 held V -> TMA store
+//                 held V
 //   warps 12-19   S in registers (row dk, 64 columns a thread): the update and the operand of Q S; V ->
 //                 hi, lo by quarters into a ring of two
 // The values are decayed, not the keys, because V is only read by the last product of the chunk, so that
@@ -63,7 +64,7 @@ constexpr int kRing = 5;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kMinLogDecay = -128.0f;
 
-constexpr int kWarpMma = 1, kWarpAlloc = 2, kWarpO = 4, kWarpS = 12;
+constexpr int kWarpMma = 1, kWarpAlloc = 2, kWarpStore = 3, kWarpO = 4, kWarpS = 12;
 constexpr int kOutWarps = 8, kStateWarps = 8;
 constexpr int kStateThreads = kStateWarps * 32;
 constexpr int kThreads = (kWarpS + kStateWarps) * 32;
@@ -87,7 +88,8 @@ struct Bars {
     uint64_t qs;       // Q S done: the S operand is free
     uint64_t o;        // P V done (and everything before it)
     uint64_t o_free;   // both output accumulators read (8 warps)
-    uint64_t stored[2];  // the chunk's V tile, reused for O, has been read by the stores (8 warps)
+    uint64_t o_tile[2];  // O written to the chunk's V tile (8 warps)
+    uint64_t stored[2];  // and read by the stores
     uint64_t gate[2], gate_free[2];
     uint64_t drain;
     uint32_t tmem;
@@ -363,7 +365,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(&B->scores, 1);
         mbar_init(&B->p, kOutWarps);
         for (int i = 0; i < 2; ++i) mbar_init(&B->split[i], kStateWarps), mbar_init(&B->split_free[i], 1);
-        for (int i = 0; i < 2; ++i) mbar_init(&B->stored[i], kOutWarps);
+        for (int i = 0; i < 2; ++i) mbar_init(&B->o_tile[i], kOutWarps), mbar_init(&B->stored[i], 1);
         mbar_init(&B->tail, kStateWarps);
         mbar_init(&B->d, 1);
         mbar_init(&B->d_free, kStateWarps);
@@ -521,6 +523,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         commit(&B->drain);  // every earlier commit has reached its barrier when this one has
         mbar_wait(&B->drain, 0);
+    } else if (warp == kWarpStore && !kStates) {
+        // lane 4 h + q stores rows [32 q, 32 q + 32) of half h, unless they are not all tokens of the window
+        // (then their warp has stored what is left)
+        const int quad = lane & 3, half = lane >> 2;
+        for (int c = 0; c < nchunks; ++c) {
+            if (!wait_warp(&B->o_tile[c & 1], (c >> 1) & 1, B, p.status)) break;
+            const int iv = c * kPer + kPer - 1;
+            if (lane < 8 && (c + 1 < nchunks || 32 * quad + 32 <= last_rows)) {
+                tma_store(&map_o, base + (iv % kRing) * kTile + half * kHalf + quad * 4096, 64 * half, h, sp.bos + c * kC + 32 * quad);
+                asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+                asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+            }
+            arrive_warp(&B->stored[c & 1]);
+        }
+        asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+        __syncwarp();
     } else if (warp < kWarpO || (kStates && warp < kWarpS)) {
         // idle
     } else if (warp < kWarpS) {
@@ -528,7 +546,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t lanes = tmem + ((uint32_t)(32 * quad) << 16);
         for (int c = 0; c < nchunks; ++c) {
             const Gates *G = reinterpret_cast<const Gates *>(smem + kGates) + (c & 1);
-            const int iv = c * kPer + kPer - 1;
             if (!wait_warp(&B->gate[c & 1], (c >> 1) & 1, B, p.status)) break;
             const float gi = G->prefix[row], lam = p.scale * ex2(gi);
             if (!wait_warp(&B->scores, c & 1, B, p.status)) break;
@@ -563,16 +580,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_before();
             arrive_warp(&B->p);
             if (lane == 0) mbar_arrive(&B->gate_free[c & 1]);
-            if (c > 0 && lane == 0) {  // by now the last chunk's store has read its tile
-                asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-                mbar_arrive(&B->stored[(c - 1) & 1]);
-            }
-            __syncwarp();
             if (!wait_warp(&B->o, c & 1, B, p.status)) break;
             tc_fence_after();
-            // rows of 128 bytes into the V tile, which nobody reads any more; a warp whose rows are all
-            // tokens of the window sends them by one TMA store, else its lanes store what is left
-            const int t = sp.bos + c * kC + row;
+            // rows of 128 bytes into the V tile, which nobody reads any more, for warp 3 to store; a warp whose
+            // rows are not all tokens of the window stores them itself
+            const int iv = c * kPer + kPer - 1, t = sp.bos + c * kC + row;
             const bool whole = c + 1 < nchunks || 32 * quad + 32 <= last_rows;
             uint8_t *const rows = smem + (iv % kRing) * kTile + half * kHalf + quad * 4096;
             uint4 *const dst = reinterpret_cast<uint4 *>(p.out + ((size_t)t * H + h) * kHeadDim + 64 * half);
@@ -598,14 +610,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_before();
             fence_async_smem();
             arrive_warp(&B->o_free);
-            if (whole && lane == 0) {
-                tma_store(&map_o, smem_addr(rows), 64 * half, h, t);
-                asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-            }
-            __syncwarp();
+            if (lane == 0) mbar_arrive(&B->o_tile[c & 1]);
         }
-        if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
-        __syncwarp();
     } else {
         const int quad = warp & 3, half = (warp - kWarpS) >> 2, row = 32 * quad + lane;  // row: dk
         const uint32_t lanes = tmem + ((uint32_t)(32 * quad) << 16) + kColD + 64 * half;
