@@ -68,6 +68,7 @@ constexpr int kWarpMma = 1, kWarpAlloc = 2, kWarpStore = 3, kWarpO = 4, kWarpS =
 constexpr int kOutWarps = 8, kStateWarps = 8;
 constexpr int kStateThreads = kStateWarps * 32;
 constexpr int kThreads = (kWarpS + kStateWarps) * 32;
+constexpr int32_t kTimedOut = 1, kMisplaced = 2;  // why a CTA gave up
 
 struct Gates {
     float prefix[kC];  // log2 units: inclusive prefix sums, and sums over the later tokens
@@ -76,12 +77,26 @@ struct Gates {
     float pad[3];
 };
 
+// Sequences in order of length, longest first (ties by index): items are handed out in index order,
+// so the longest chains start first. More than kRanked sequences keep index order.
+constexpr int kRanked = 256;
+
+// A chain, or a window of one. nchunks < 0: there are no more items.
+struct Item {
+    const float *start;  // state before it, or NULL for zeros
+    float *end;          // where its end state goes, or NULL
+    float *total;        // where its total decay goes (state pass)
+    int32_t h, bos, eos, nchunks, updates, last_rows;
+    int32_t carried;     // start was written by the launch before
+    int32_t pad;
+};
+
 struct Bars {
     uint64_t full[kRing], empty[kRing];  // TMA -> users, users (tcgen05.commit) -> TMA
     uint64_t scores;   // A done
     uint64_t p;        // P written (8 warps)
     uint64_t split[2], split_free[2];  // hi and lo of a quarter written (8 warps), and read
-    uint64_t tail;     // rows past the window's last token cleared (8 warps)
+    uint64_t tail[2];  // rows past the window's last token cleared (8 warps)
     uint64_t d;        // D done
     uint64_t d_free;   // D read (8 warps)
     uint64_t s;        // S operand written (8 warps)
@@ -91,9 +106,14 @@ struct Bars {
     uint64_t o_tile[2];  // O written to the chunk's V tile (8 warps)
     uint64_t stored[2];  // and read by the stores
     uint64_t gate[2], gate_free[2];
+    uint64_t item[2], item_free[2];  // work items handed to the roles
+    uint64_t next;                   // the answer to the request for another item
     uint64_t drain;
+    uint4 answer;
+    Item items[2];
     uint32_t tmem;
-    int32_t abort;
+    int32_t abort, progress, finished;  // progress: chunks issued; finished: roles' warps
+    uint8_t order[kRanked];  // sequences by length, longest first
 };
 
 // ---- shared memory (bytes); the swizzled tiles need 1024-byte alignment
@@ -186,10 +206,40 @@ __device__ __forceinline__ void expect_tx(uint64_t *bar, uint32_t bytes) {
     asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_addr(bar)), "r"(bytes) : "memory");
 }
 
-// Bounded wait of one thread that also gives up as soon as any thread of the CTA has.
-__device__ __forceinline__ bool wait_one(uint64_t *bar, uint32_t parity, Bars *B, DeviceStatus *st) {
+// Asks for the index of a CTA of this grid that has not been launched (16 bytes to `answer`, completed
+// on `bar`); taken() is the index, or -1 when there was none left.
+__device__ __forceinline__ void try_cancel(uint4 *answer, uint64_t *bar) {
+    asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+                     smem_addr(answer)),
+                 "r"(smem_addr(bar))
+                 : "memory");
+}
+
+__device__ __forceinline__ int taken(const uint4 *answer) {
+    uint32_t x, ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        ".reg .b128 r;\n\t"
+        "ld.shared.b128 r, [%2];\n\t"
+        "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\t"
+        "selp.u32 %1, 1, 0, p;\n\t"
+        "mov.u32 %0, 0;\n\t"
+        "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %0, r;\n\t}"
+        : "=r"(x), "=r"(ok)
+        : "r"(smem_addr(answer))
+        : "memory");
+    return ok ? (int)x : -1;
+}
+
+// Wait of a warp, with one decision for all its lanes. It is bounded by the watchdog warp, which raises the
+// abort flag when the CTA has made no progress for kWaitLimitNs: with a timer in each of the kernel's
+// thirty waits, whose roles share an instruction cache, the kernel was 8 KiB longer. The lanes vote inside
+// the loop, so that the compiler sees one exit for the warp: with the vote behind the loop it took
+// what follows for divergent, and eight MMAs needed 900 cycles to issue instead of 300 (8 x 16384 x 96
+// heads: 2.56 ms).
+__device__ __forceinline__ bool wait_warp(uint64_t *bar, uint32_t parity, Bars *B) {
     const uint32_t addr = smem_addr(bar);
-    uint64_t start = 0;
+    bool ok = true;
     for (;;) {
         uint32_t done;
         asm volatile(
@@ -199,22 +249,27 @@ __device__ __forceinline__ bool wait_one(uint64_t *bar, uint32_t parity, Bars *B
             : "=r"(done)
             : "r"(addr), "r"(parity), "r"(kSuspendHintNs)
             : "memory");
-        if (done) return true;
-        if (*reinterpret_cast<volatile int32_t *>(&B->abort)) return false;
-        const uint64_t now = global_ns();
-        if (start == 0) {
-            start = now;
-        } else if (now - start > kWaitLimitNs) {
-            *reinterpret_cast<volatile int32_t *>(&B->abort) = 1;
-            report_error(st, KDA_ERR_DEVICE_TIMEOUT, (int)blockIdx.x);
-            return false;
-        }
+        if (__all_sync(0xffffffffu, done)) break;
+        if (__any_sync(0xffffffffu, *reinterpret_cast<volatile int32_t *>(&B->abort))) { ok = false; break; }
     }
+    return ok;
 }
 
-// The same for a whole warp, with one decision for all its lanes.
-__device__ __forceinline__ bool wait_warp(uint64_t *bar, uint32_t parity, Bars *B, DeviceStatus *st) {
-    return __all_sync(0xffffffffu, wait_one(bar, parity, B, st));
+// The watchdog: returns when all `roles` warps have finished, or after it has raised the abort flag.
+__device__ __forceinline__ void watch(Bars *B, int roles) {
+    const volatile int32_t *const abort = &B->abort, *const finished = &B->finished, *const progress = &B->progress;
+    uint64_t since = global_ns();
+    int32_t seen = 0;
+    while (*finished < roles && !*abort) {
+        __nanosleep(200);
+        const int32_t now = *progress + *finished;
+        if (now != seen) {
+            seen = now;
+            since = global_ns();
+        } else if (global_ns() - since > kWaitLimitNs) {
+            *const_cast<volatile int32_t *>(abort) = kTimedOut;
+        }
+    }
 }
 
 // One arrival for a warp, after what its lanes did.
@@ -236,33 +291,31 @@ struct ChunkArgs {
     Plan plan;
     float *slots;  // windowed chain lc, window w: the window's own end state, then the start of window w + 1
     float *decay;  // windowed chain lc, window w: its total decay (log2)
+    int32_t take_over;  // whether a CTA takes over items of CTAs not launched yet: in a grid of one wave, it
+                        // would only take those that are about to start on an idle SM
 };
 
 __device__ __forceinline__ float *slot_of(const ChunkArgs &a, int lc, int w) {
     return a.slots + ((size_t)lc * (a.plan.wins - 1) + w) * (kHeadDim * kHeadDim);
 }
 
-// Chains in order of their sequences' lengths, longest first (ties by index; more than kRanked
-// sequences keep index order): CTAs start in index order, so the longest start first.
-constexpr int kRanked = 256;
-
-__device__ __forceinline__ int seq_of_rank(const LinearPrefillArgs &a, int j, int *scratch) {
+// order[r] = the sequence of rank r; holds CTA barriers. `scratch`: kRanked ints.
+__device__ __forceinline__ void rank_sequences(const LinearPrefillArgs &a, int *scratch, uint8_t *order) {
     const int N = a.num_seqs;
-    if (N <= 1 || N > kRanked) return j;
-    int *len = scratch, *pick = scratch + kRanked;
-    for (int i = threadIdx.x; i < N; i += blockDim.x)
-        len[i] = (int)((unsigned)__ldg(a.cu_seqlens + i + 1) - (unsigned)__ldg(a.cu_seqlens + i));
+    if (N > kRanked) return;
+#pragma unroll 1
+    for (int i = threadIdx.x; i < N; i += blockDim.x)  // wrapping difference: any input orders
+        scratch[i] = (int)((unsigned)__ldg(a.cu_seqlens + i + 1) - (unsigned)__ldg(a.cu_seqlens + i));
     __syncthreads();
+#pragma unroll 1
     for (int i = threadIdx.x; i < N; i += blockDim.x) {
-        const int li = len[i];
+        const int li = scratch[i];
         int r = 0;
-        for (int m = 0; m < N; ++m) r += (len[m] > li) | ((len[m] == li) & (m < i));
-        if (r == j) *pick = i;
+#pragma unroll 1
+        for (int m = 0; m < N; ++m) r += (scratch[m] > li) | ((scratch[m] == li) & (m < i));
+        order[r] = (uint8_t)i;
     }
     __syncthreads();
-    const int n = *pick;
-    __syncthreads();
-    return n;
 }
 
 struct Span {
@@ -274,7 +327,7 @@ struct Span {
 __device__ __forceinline__ Span span_of(const LinearPrefillArgs &a, int n, int w, int W, bool report) {
     int sb = a.cu_seqlens[n], se = a.cu_seqlens[n + 1];
     if (sb < 0 || se < sb || se > a.total_tokens) {
-        if (report && threadIdx.x == 0) report_error(a.status, KDA_ERR_DEVICE_INPUT, n);
+        if (report && (threadIdx.x & 31) == 0) report_error(a.status, KDA_ERR_DEVICE_INPUT, n);
         sb = min(max(sb, 0), a.total_tokens);
         se = min(max(se, sb), a.total_tokens);
     }
@@ -319,11 +372,61 @@ __device__ __forceinline__ uint32_t empty_parity(int i, bool with_v) {
     // tile j is a V tile when j % 3 == 2; over three uses of a slot (15 tiles) exactly one is
     const int first = i % kRing;
     int vs = uses / 3;
+#pragma unroll 1
     for (int u = uses / 3 * 3; u < uses; ++u) vs += (first + kRing * u) % 3 == 2;
     return (uses - vs) & 1;
 }
 
+// The work item of index i: a whole chain, or a window of a windowed chain.
+template <bool kStates>
+__device__ __forceinline__ Item item_of(const ChunkArgs &a, int i, const uint8_t *order) {
+    const LinearPrefillArgs &p = a.p;
+    const int W = a.plan.wins, H = p.num_heads;
+    int pos = i, w = 0, lc = -1;
+    if (kStates || i >= a.plan.seq_chains) {
+        const int per = kStates ? W - 1 : W;
+        if (!kStates) i -= a.plan.seq_chains;
+        lc = i / per;
+        w = i - lc * per;
+        pos = a.plan.seq_chains + lc;
+    }
+    const int h = pos % H, rank = pos / H;
+    const int n = p.num_seqs <= kRanked ? order[rank] : rank;
+    const Span sp = span_of(p, n, w, lc >= 0 ? W : 1, !kStates && h == 0 && w == 0);
+    const size_t chain = ((size_t)n * H + h) * (kHeadDim * kHeadDim);
+    Item it;
+    it.h = h;
+    it.bos = sp.bos;
+    it.eos = sp.eos;
+    it.nchunks = (sp.eos - sp.bos + kC - 1) / kC;
+    it.start = nullptr;
+    it.end = nullptr;
+    it.carried = 0;
+    it.total = nullptr;
+    if (kStates) {
+        if (!sp.live || sp.last) {
+            it.nchunks = 0;
+        } else {
+            it.end = slot_of(a, lc, w);
+            it.total = a.decay + (size_t)lc * W + w;
+        }
+    } else if (sp.live) {
+        it.carried = lc >= 0 && !sp.first;
+        it.start = it.carried ? slot_of(a, lc, w - 1) : p.init_state ? p.init_state + chain : nullptr;
+        it.end = sp.last && p.final_state ? p.final_state + chain : nullptr;
+    }
+    // the last chunk's update is needed only where somebody reads the end state
+    it.updates = it.end ? it.nchunks : it.nchunks - 1;
+    it.last_rows = it.eos - it.bos - (it.nchunks - 1) * kC;
+    return it;
+}
+
 // kStates: only the state update, from zero, over the windows of the windowed chains but the last.
+//
+// A CTA runs item after item (its own index first, then those of CTAs of the grid that have not been
+// launched, which it takes over by clusterlaunchcontrol): items are handed out as SMs become free, the
+// longest first, and the roles go from one item's last chunk to the next one's first without emptying
+// the pipeline. All counters that give a barrier's phase run on over the items.
 template <bool kStates>
 __global__ void __launch_bounds__(kThreads, 1)
     kda_linear_chunk_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap map_q,
@@ -334,49 +437,35 @@ __global__ void __launch_bounds__(kThreads, 1)
     Bars *B = reinterpret_cast<Bars *>(smem + kBars);
     // the shuffle tells the compiler that the role is one for the warp
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31, H = p.num_heads;
-    const int W = a.plan.wins;
-    // the item: a whole chain, or window w of windowed chain lc
-    int pos = blockIdx.x, w = 0, lc = -1;
-    if (kStates || pos >= a.plan.seq_chains) {
-        const int per = kStates ? W - 1 : W;
-        const int i = kStates ? pos : pos - a.plan.seq_chains;
-        lc = i / per;
-        w = i - lc * per;
-        pos = a.plan.seq_chains + lc;
-    }
-    const int h = pos % H;
-    const int n = seq_of_rank(p, pos / H, reinterpret_cast<int *>(smem));
-    const Span sp = span_of(p, n, w, lc >= 0 ? W : 1, h == 0 && w == 0 && !kStates);
     if (kStates) pdl_launch_dependents();
-    if (!sp.live || (kStates && sp.last)) {
-        if (!kStates) pdl_wait();  // every CTA ends after the launches before: see the last lines
-        return;
-    }
-    const int nchunks = (sp.eos - sp.bos + kC - 1) / kC;
-    const size_t chain = ((size_t)n * H + h) * (kHeadDim * kHeadDim);
-    const float *const start = kStates ? nullptr : lc >= 0 && !sp.first ? slot_of(a, lc, w - 1)
-                                               : p.init_state ? p.init_state + chain : nullptr;
-    float *const end = kStates ? slot_of(a, lc, w) : sp.last && p.final_state ? p.final_state + chain : nullptr;
-    // the last chunk's update is needed only where somebody reads the end state
-    const int updates = end ? nchunks : nchunks - 1;
+    rank_sequences(p, reinterpret_cast<int *>(smem), B->order);
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < kRing; ++i) mbar_init(&B->full[i], 1), mbar_init(&B->empty[i], 1);
         mbar_init(&B->scores, 1);
         mbar_init(&B->p, kOutWarps);
-        for (int i = 0; i < 2; ++i) mbar_init(&B->split[i], kStateWarps), mbar_init(&B->split_free[i], 1);
-        for (int i = 0; i < 2; ++i) mbar_init(&B->o_tile[i], kOutWarps), mbar_init(&B->stored[i], 1);
-        mbar_init(&B->tail, kStateWarps);
         mbar_init(&B->d, 1);
         mbar_init(&B->d_free, kStateWarps);
         mbar_init(&B->s, kStateWarps);
         mbar_init(&B->qs, 1);
         mbar_init(&B->o, 1);
         mbar_init(&B->o_free, kOutWarps);
-        for (int i = 0; i < 2; ++i) mbar_init(&B->gate[i], 1), mbar_init(&B->gate_free[i], kStateWarps + (kStates ? 0 : kOutWarps));
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&B->split[i], kStateWarps);
+            mbar_init(&B->split_free[i], 1);
+            mbar_init(&B->tail[i], kStateWarps);
+            mbar_init(&B->o_tile[i], kOutWarps);
+            mbar_init(&B->stored[i], 1);
+            mbar_init(&B->gate[i], 1);
+            mbar_init(&B->gate_free[i], kStateWarps + (kStates ? 0 : kOutWarps));
+            mbar_init(&B->item[i], 1);
+            mbar_init(&B->item_free[i], 1 + kStateWarps + (kStates ? 0 : 1 + kOutWarps));
+        }
+        mbar_init(&B->next, 1);
         mbar_init(&B->drain, 1);
         // the swizzled tiles are laid out for a 1024-byte-aligned base
-        B->abort = (smem_addr(smem) & 1023u) != 0;
+        B->abort = (smem_addr(smem) & 1023u) != 0 ? kMisplaced : 0;
+        B->progress = B->finished = 0;
         if (B->abort) report_error(p.status, KDA_ERR_CUDA, 0);
         fence_mbar_init();
     }
@@ -391,135 +480,190 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr uint32_t tmem = 0;
     if (threadIdx.x == 0 && B->tmem != 0) {
         report_error(p.status, KDA_ERR_CUDA, 1);
-        B->abort = 1;
+        B->abort = kMisplaced;
     }
     __syncthreads();
     const uint32_t base = smem_addr(smem);
     constexpr int kPer = kStates ? 2 : 3;  // tiles of a chunk: (Q,) K, V
-    const int last_rows = sp.eos - sp.bos - (nchunks - 1) * kC;  // of the last chunk
     int issued = 0;                        // loads issued (warp 0)
+    int asked = 0, told = 0;               // next items asked for, and answers seen (warp 0)
+
+    // The k-th item, for every role but warp 0; nchunks < 0 after the last (and if the CTA gave up). The
+    // shuffles tell the compiler that the values are one for the warp.
+    auto next_item = [&](int k) {
+        const bool ok = wait_warp(&B->item[k & 1], (k >> 1) & 1, B);
+        const Item &from = B->items[k & 1];
+        Item it;
+        it.start = from.start;
+        it.end = from.end;
+        it.h = __shfl_sync(0xffffffffu, from.h, 0);
+        it.bos = __shfl_sync(0xffffffffu, from.bos, 0);
+        it.eos = __shfl_sync(0xffffffffu, from.eos, 0);
+        it.nchunks = __shfl_sync(0xffffffffu, ok ? from.nchunks : -1, 0);
+        it.updates = __shfl_sync(0xffffffffu, from.updates, 0);
+        it.last_rows = __shfl_sync(0xffffffffu, from.last_rows, 0);
+        it.carried = __shfl_sync(0xffffffffu, from.carried, 0);
+        arrive_warp(&B->item_free[k & 1]);
+        return it;
+    };
 
     if (B->abort) {
         // nothing has started
     } else if (warp == 0) {
-        float run = 0.0f;  // total decay of the window so far
-        for (int c = 0; c < nchunks; ++c) {
-            const int t0 = sp.bos + c * kC, L = min(kC, sp.eos - t0), b = c & 1;
-            float g[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int t = 4 * lane + e;
-                g[e] = t < L ? p.log_decay[(size_t)(t0 + t) * p.decay_token_stride + h] : 0.0f;
+        int g = 0, index = blockIdx.x;  // g: chunks of the items before
+        for (int k = 0;; ++k) {
+            Item it;
+            it.nchunks = -1;
+            if (index >= 0) it = item_of<kStates>(a, index, B->order);
+            if (k >= 2 && !wait_warp(&B->item_free[k & 1], ((k >> 1) - 1) & 1, B)) break;
+            if (lane == 0) B->items[k & 1] = it;
+            arrive_warp(&B->item[k & 1]);
+            if (index < 0) break;
+            if (a.take_over) {
+                if (lane == 0) {
+                    fence_async_smem();
+                    expect_tx(&B->next, 16);
+                    try_cancel(&B->answer, &B->next);
+                }
+                ++asked;
             }
             bool ok = true;
-            for (int which = 0; which < kPer; ++which, ++issued) {
-                const int slot = issued % kRing;
-                if (issued >= kRing) {  // the tile five loads ago has been read
-                    const int before = issued - kRing, cb = before / kPer;
-                    const bool is_v = !kStates && before - cb * kPer == kPer - 1;  // then also as O
-                    ok = is_v ? wait_warp(&B->stored[cb & 1], (cb >> 1) & 1, B, p.status)
-                              : wait_warp(&B->empty[slot], empty_parity(before, kStates), B, p.status);
-                    if (!ok) break;
+            float run = 0.0f;  // total decay of the window so far
+            for (int c = 0; c < it.nchunks; ++c, ++g) {
+                const int t0 = it.bos + c * kC, L = min(kC, it.eos - t0), b = g & 1;
+                float x[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int t = 4 * lane + e;
+                    x[e] = t < L ? p.log_decay[(size_t)(t0 + t) * p.decay_token_stride + it.h] : 0.0f;
                 }
-                const CUtensorMap *map = which == kPer - 1 ? &map_v : which == kPer - 2 ? &map_k : &map_q;
-                if (lane == 0) {
-                    expect_tx(&B->full[slot], kTile);
-                    tma_load(base + slot * kTile, map, 0, h, t0, &B->full[slot]);
-                    tma_load(base + slot * kTile + kHalf, map, 64, h, t0, &B->full[slot]);
+#pragma unroll 1
+                for (int which = 0; which < kPer; ++which, ++issued) {
+                    const int slot = issued % kRing;
+                    if (issued >= kRing) {  // the tile five loads ago has been read
+                        const int before = issued - kRing, cb = before / kPer;
+                        const bool is_v = !kStates && before - cb * kPer == kPer - 1;  // then also as O
+                        ok = is_v ? wait_warp(&B->stored[cb & 1], (cb >> 1) & 1, B)
+                                  : wait_warp(&B->empty[slot], empty_parity(before, kStates), B);
+                        if (!ok) break;
+                    }
+                    const CUtensorMap *map = which == kPer - 1 ? &map_v : which == kPer - 2 ? &map_k : &map_q;
+                    if (lane == 0) {
+                        expect_tx(&B->full[slot], kTile);
+                        tma_load(base + slot * kTile, map, 0, it.h, t0, &B->full[slot]);
+                        tma_load(base + slot * kTile + kHalf, map, 64, it.h, t0, &B->full[slot]);
+                    }
+                    __syncwarp();
                 }
-                __syncwarp();
+                if (!ok) break;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) x[e] = (x[e] < kMinLogDecay ? kMinLogDecay : x[e]) * kLog2e;
+                const float mine = (x[0] + x[1]) + (x[2] + x[3]);
+                float up = mine, down = mine;  // inclusive over the lanes before, and after
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const float y = __shfl_up_sync(0xffffffffu, up, o), z = __shfl_down_sync(0xffffffffu, down, o);
+                    if (lane >= o) up += y;
+                    if (lane + o < 32) down += z;
+                }
+                float before = __shfl_up_sync(0xffffffffu, up, 1), after = __shfl_down_sync(0xffffffffu, down, 1);
+                if (lane == 0) before = 0.0f;
+                if (lane == 31) after = 0.0f;
+                const float total = __shfl_sync(0xffffffffu, down, 0);
+                ok = g < 2 || wait_warp(&B->gate_free[b], ((g >> 1) - 1) & 1, B);
+                if (!ok) break;
+                Gates *G = reinterpret_cast<Gates *>(smem + kGates) + b;
+                const float p0 = before + x[0], p1 = p0 + x[1], p2 = p1 + x[2], p3 = p2 + x[3];
+                *reinterpret_cast<float4 *>(&G->prefix[4 * lane]) = make_float4(p0, p1, p2, p3);
+                const float s2 = after + x[3], s1 = s2 + x[2], s0 = s1 + x[1];
+                *reinterpret_cast<float4 *>(&G->suffix[4 * lane]) = make_float4(ex2(s0), ex2(s1), ex2(s2), ex2(after));
+                // exp2f, not the 2^-22 of the hardware's: this error repeats every chunk and adds up over
+                // the chunks that a slowly decaying state remembers
+                if (lane == 0) G->decay = exp2f(total);
+                arrive_warp(&B->gate[b]);
+                run += total;
             }
             if (!ok) break;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) g[e] = (g[e] < kMinLogDecay ? kMinLogDecay : g[e]) * kLog2e;
-            const float mine = (g[0] + g[1]) + (g[2] + g[3]);
-            float up = mine, down = mine;  // inclusive over the lanes before, and after
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const float x = __shfl_up_sync(0xffffffffu, up, o), y = __shfl_down_sync(0xffffffffu, down, o);
-                if (lane >= o) up += x;
-                if (lane + o < 32) down += y;
-            }
-            float before = __shfl_up_sync(0xffffffffu, up, 1), after = __shfl_down_sync(0xffffffffu, down, 1);
-            if (lane == 0) before = 0.0f;
-            if (lane == 31) after = 0.0f;
-            const float total = __shfl_sync(0xffffffffu, down, 0);
-            if (c >= 2 && !wait_warp(&B->gate_free[b], ((c >> 1) - 1) & 1, B, p.status)) break;
-            Gates *G = reinterpret_cast<Gates *>(smem + kGates) + b;
-            const float p0 = before + g[0], p1 = p0 + g[1], p2 = p1 + g[2], p3 = p2 + g[3];
-            *reinterpret_cast<float4 *>(&G->prefix[4 * lane]) = make_float4(p0, p1, p2, p3);
-            const float s2 = after + g[3], s1 = s2 + g[2], s0 = s1 + g[1];
-            *reinterpret_cast<float4 *>(&G->suffix[4 * lane]) = make_float4(ex2(s0), ex2(s1), ex2(s2), ex2(after));
-            // exp2f, not the 2^-22 of the hardware's: this error repeats every chunk and adds up over
-            // the chunks that a slowly decaying state remembers
-            if (lane == 0) G->decay = exp2f(total);
-            arrive_warp(&B->gate[b]);
-            run += total;
+            if (kStates && lane == 0 && it.total) *it.total = run;
+            index = -1;
+            if (!a.take_over) continue;
+            if (!wait_warp(&B->next, k & 1, B)) break;
+            ++told;
+            index = taken(&B->answer);
+            __syncwarp();
         }
-        if (kStates && lane == 0) a.decay[(size_t)lc * W + w] = run;
     } else if (warp == kWarpMma) {
-        for (int c = 0; c < nchunks; ++c) {
-            const int iq = c * kPer, ik = iq + kPer - 2, iv = ik + 1;
-            const uint32_t k = base + (ik % kRing) * kTile, q = base + (iq % kRing) * kTile, v = base + (iv % kRing) * kTile;
-            const int L = c + 1 < nchunks ? kC : last_rows;
-            if (!wait_warp(&B->full[ik % kRing], (ik / kRing) & 1, B, p.status)) break;
-            if (!kStates) {
-                if (!wait_warp(&B->full[iq % kRing], (iq / kRing) & 1, B, p.status)) break;
-                if (c > 0 && !wait_warp(&B->o, (c - 1) & 1, B, p.status)) break;  // P of the last chunk has been read
-                const uint64_t dq = at(kDescK, q), dk = at(kDescK, k);
+        int g = 0, u = 0, use = 0, tl = 0;  // chunks, updates, quarters and partial chunks so far
+        bool ok = true;
+        for (int k = 0; ok; ++k) {
+            const Item it = next_item(k);
+            if (it.nchunks < 0) break;
+            for (int c = 0; c < it.nchunks; ++c, ++g) {
+                ok = false;
+                if (lane == 0) *reinterpret_cast<volatile int32_t *>(&B->progress) = g + 1;
+                const int iq = g * kPer, ik = iq + kPer - 2, iv = ik + 1;
+                const uint32_t k = base + (ik % kRing) * kTile, q = base + (iq % kRing) * kTile, v = base + (iv % kRing) * kTile;
+                const int L = c + 1 < it.nchunks ? kC : it.last_rows;
+                if (!wait_warp(&B->full[ik % kRing], (ik / kRing) & 1, B)) break;
+                if (!kStates) {
+                    if (!wait_warp(&B->full[iq % kRing], (iq / kRing) & 1, B)) break;
+                    if (g > 0 && !wait_warp(&B->o, (g - 1) & 1, B)) break;  // P of the last chunk has been read
+                    const uint64_t dq = at(kDescK, q), dk = at(kDescK, k);
 #pragma unroll
-                for (int s = 0; s < 8; ++s) {
-                    const uint32_t off = ((s >> 2) * kHalf + (s & 3) * 32) >> 4;
-                    mma_ss(tmem + kColA, dq + off, dk + off, kIdescQK, s > 0);
-                }
-                commit(&B->scores);
-                if (!wait_warp(&B->s, c & 1, B, p.status)) break;
-                if (c > 0 && !wait_warp(&B->o_free, (c - 1) & 1, B, p.status)) break;
-                tc_fence_after();
-                const uint64_t ds = at(kDescMn, base + kS);
-#pragma unroll
-                for (int s = 0; s < 8; ++s)
-                    mma_ss(tmem + kColQS, dq + (((s >> 2) * kHalf + (s & 3) * 32) >> 4), ds + s * 128, kIdescQS, s > 0);
-                commit(&B->qs);
-                commit(&B->empty[iq % kRing]);
-            }
-            if (L < kC && !wait_warp(&B->tail, 0, B, p.status)) break;
-            if (c < updates) {
-                if (c > 0 && !wait_warp(&B->d_free, (c - 1) & 1, B, p.status)) break;
-                bool lost = false;
-#pragma unroll 1
-                for (int q = 0; q * kQuarter < L; ++q) {
-                    const int use = 4 * c + q, st = use & 1;
-                    lost = !wait_warp(&B->split[st], (use >> 1) & 1, B, p.status);
-                    if (lost) break;
+                    for (int s = 0; s < 8; ++s) {
+                        const uint32_t off = ((s >> 2) * kHalf + (s & 3) * 32) >> 4;
+                        mma_ss(tmem + kColA, dq + off, dk + off, kIdescQK, s > 0);
+                    }
+                    commit(&B->scores);
+                    if (!wait_warp(&B->s, g & 1, B)) break;
+                    if (g > 0 && !wait_warp(&B->o_free, (g - 1) & 1, B)) break;
                     tc_fence_after();
-                    const uint64_t da = at(kDescMn, k + q * kQuarter * 128), db = at(kDescSplit, base + kSplit + st * kSplitStage);
-#pragma unroll
-                    for (int s = 0; s < 4; ++s)  // hi, hi, lo, lo
-                        mma_ss(tmem + kColD, da + (s & 1) * 128, db + (((s >> 1) * kSplitLo + (s & 1) * 2048) >> 4), kIdescD,
-                               q > 0 || s > 0);
-                    commit(&B->split_free[st]);
-                }
-                if (lost) break;
-                commit(&B->d);
-            }
-            commit(&B->empty[ik % kRing]);
-            if (!wait_warp(&B->full[iv % kRing], (iv / kRing) & 1, B, p.status)) break;
-            if (!kStates) {
-                if (!wait_warp(&B->p, c & 1, B, p.status)) break;
-                tc_fence_after();
-                const uint64_t dv = at(kDescMn, v);
-                if (L == kC) {
+                    const uint64_t ds = at(kDescMn, base + kS);
 #pragma unroll
                     for (int s = 0; s < 8; ++s)
-                        mma_ts(tmem + kColO, tmem + kColA + 32 * (s >> 1) + 8 * (s & 1), dv + s * 128, kIdescPV, s > 0);
-                } else {
-                    for (int s = 0; s * 16 < L; ++s)
-                        mma_ts(tmem + kColO, tmem + kColA + 32 * (s >> 1) + 8 * (s & 1), dv + s * 128, kIdescPV, s > 0);
+                        mma_ss(tmem + kColQS, dq + (((s >> 2) * kHalf + (s & 3) * 32) >> 4), ds + s * 128, kIdescQS, s > 0);
+                    commit(&B->qs);
+                    commit(&B->empty[iq % kRing]);
                 }
-                commit(&B->o);
+                if (L < kC) {
+                    if (!wait_warp(&B->tail[tl & 1], (tl >> 1) & 1, B)) break;
+                    ++tl;
+                }
+                if (c < it.updates) {
+                    if (u > 0 && !wait_warp(&B->d_free, (u - 1) & 1, B)) break;
+                    bool lost = false;
+#pragma unroll 1
+                    for (int r = 0; r < L; r += kQuarter, ++use) {
+                        const int st = use & 1;
+                        lost = !wait_warp(&B->split[st], (use >> 1) & 1, B);
+                        if (lost) break;
+                        tc_fence_after();
+                        const uint64_t da = at(kDescMn, k + r * 128), db = at(kDescSplit, base + kSplit + st * kSplitStage);
+#pragma unroll
+                        for (int s = 0; s < 4; ++s)  // hi, hi, lo, lo
+                            mma_ss(tmem + kColD, da + (s & 1) * 128, db + (((s >> 1) * kSplitLo + (s & 1) * 2048) >> 4), kIdescD,
+                                   r > 0 || s > 0);
+                        commit(&B->split_free[st]);
+                    }
+                    if (lost) break;
+                    commit(&B->d);
+                    ++u;
+                }
+                commit(&B->empty[ik % kRing]);
+                if (!wait_warp(&B->full[iv % kRing], (iv / kRing) & 1, B)) break;
+                if (!kStates) {
+                    if (!wait_warp(&B->p, g & 1, B)) break;
+                    tc_fence_after();
+                    const uint64_t dv = at(kDescMn, v);
+#pragma unroll
+                    for (int s = 0; s < 8; ++s)  // (16 tokens past the last one would be zeros)
+                        if (s * 16 < L) mma_ts(tmem + kColO, tmem + kColA + 32 * (s >> 1) + 8 * (s & 1), dv + s * 128, kIdescPV, s > 0);
+                    commit(&B->o);
+                }
+                if (kStates) commit(&B->empty[iv % kRing]);
+                ok = true;
             }
-            if (kStates) commit(&B->empty[iv % kRing]);
+            if (it.nchunks == 0) ok = true;
         }
         commit(&B->drain);  // every earlier commit has reached its barrier when this one has
         mbar_wait(&B->drain, 0);
@@ -527,189 +671,214 @@ __global__ void __launch_bounds__(kThreads, 1)
         // lane 4 h + q stores rows [32 q, 32 q + 32) of half h, unless they are not all tokens of the window
         // (then their warp has stored what is left)
         const int quad = lane & 3, half = lane >> 2;
-        for (int c = 0; c < nchunks; ++c) {
-            if (!wait_warp(&B->o_tile[c & 1], (c >> 1) & 1, B, p.status)) break;
-            const int iv = c * kPer + kPer - 1;
-            if (lane < 8 && (c + 1 < nchunks || 32 * quad + 32 <= last_rows)) {
-                tma_store(&map_o, base + (iv % kRing) * kTile + half * kHalf + quad * 4096, 64 * half, h, sp.bos + c * kC + 32 * quad);
-                asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-                asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+        int g = 0;
+        bool ok = true;
+        for (int k = 0; ok; ++k) {
+            const Item it = next_item(k);
+            if (it.nchunks < 0) break;
+            for (int c = 0; c < it.nchunks; ++c, ++g) {
+                ok = wait_warp(&B->o_tile[g & 1], (g >> 1) & 1, B);
+                if (!ok) break;
+                const int iv = g * kPer + kPer - 1;
+                if (lane < 8 && (c + 1 < it.nchunks || 32 * quad + 32 <= it.last_rows)) {
+                    tma_store(&map_o, base + (iv % kRing) * kTile + half * kHalf + quad * 4096, 64 * half, it.h, it.bos + c * kC + 32 * quad);
+                    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+                    asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+                }
+                arrive_warp(&B->stored[g & 1]);
             }
-            arrive_warp(&B->stored[c & 1]);
         }
         asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
         __syncwarp();
+    } else if (warp == kWarpAlloc) {
+        watch(B, kStates ? 2 + kStateWarps : 3 + kOutWarps + kStateWarps);
     } else if (warp < kWarpO || (kStates && warp < kWarpS)) {
         // idle
     } else if (warp < kWarpS) {
         const int quad = warp & 3, half = (warp - kWarpO) >> 2, row = 32 * quad + lane;
         const uint32_t lanes = tmem + ((uint32_t)(32 * quad) << 16);
-        for (int c = 0; c < nchunks; ++c) {
-            const Gates *G = reinterpret_cast<const Gates *>(smem + kGates) + (c & 1);
-            if (!wait_warp(&B->gate[c & 1], (c >> 1) & 1, B, p.status)) break;
-            const float gi = G->prefix[row], lam = p.scale * ex2(gi);
-            if (!wait_warp(&B->scores, c & 1, B, p.status)) break;
-            tc_fence_after();
-            // this warp's blocks of 32 columns: every other one
+        int g = 0;
+        bool ok = true;
+        for (int k = 0; ok; ++k) {
+            const Item it = next_item(k);
+            if (it.nchunks < 0) break;
+            for (int c = 0; c < it.nchunks; ++c, ++g) {
+                ok = false;
+                const Gates *G = reinterpret_cast<const Gates *>(smem + kGates) + (g & 1);
+                if (!wait_warp(&B->gate[g & 1], (g >> 1) & 1, B)) break;
+                const float gi = G->prefix[row], lam = p.scale * ex2(gi);
+                if (!wait_warp(&B->scores, g & 1, B)) break;
+                tc_fence_after();
+                // this warp's blocks of 32 columns: every other one
+#pragma unroll 1
+                for (int i = 0; i < 2; ++i) {
+                    const int b = 2 * i + half;
+                    float f[16];
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int b = 2 * i + half;
-                float f[16];
+                    for (int j = 0; j < 16; ++j) f[j] = 0.0f;
+                    if (b <= quad) {
 #pragma unroll
-                for (int j = 0; j < 16; ++j) f[j] = 0.0f;
-                if (b <= quad) {
+                        for (int u = 0; u < 2; ++u) {
+                            float s[16], e[16];
+                            tmem_ld16(lanes + kColA + 32 * b + 16 * u, s);
 #pragma unroll
-                    for (int u = 0; u < 2; ++u) {
-                        float s[16], e[16];
-                        tmem_ld16(lanes + kColA + 32 * b + 16 * u, s);
+                            for (int j = 0; j < 16; j += 4) {
+                                const float4 gj = *reinterpret_cast<const float4 *>(&G->prefix[32 * b + 16 * u + j]);
+                                e[j] = ex2(gi - gj.x), e[j + 1] = ex2(gi - gj.y), e[j + 2] = ex2(gi - gj.z), e[j + 3] = ex2(gi - gj.w);
+                            }
+                            tmem_wait_ld();
 #pragma unroll
-                        for (int j = 0; j < 16; j += 4) {
-                            const float4 gj = *reinterpret_cast<const float4 *>(&G->prefix[32 * b + 16 * u + j]);
-                            e[j] = ex2(gi - gj.x), e[j + 1] = ex2(gi - gj.y), e[j + 2] = ex2(gi - gj.z), e[j + 3] = ex2(gi - gj.w);
+                            for (int j = 0; j < 16; ++j) s[j] = (b < quad || 16 * u + j <= lane) ? s[j] * e[j] : 0.0f;
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) f[8 * u + j] = __uint_as_float(pack_bf16(s[2 * j], s[2 * j + 1]));
                         }
-                        tmem_wait_ld();
+                    }
+                    tmem_st16(lanes + kColA + 32 * b, f);
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                arrive_warp(&B->p);
+                if (lane == 0) mbar_arrive(&B->gate_free[g & 1]);
+                if (!wait_warp(&B->o, g & 1, B)) break;
+                tc_fence_after();
+                // rows of 128 bytes into the V tile, which nobody reads any more, for warp 3 to store; a warp whose
+                // rows are not all tokens of the window stores them itself
+                const int iv = g * kPer + kPer - 1, t = it.bos + c * kC + row;
+                const bool whole = c + 1 < it.nchunks || 32 * quad + 32 <= it.last_rows;
+                uint8_t *const rows = smem + (iv % kRing) * kTile + half * kHalf + quad * 4096;
+                uint4 *const dst = reinterpret_cast<uint4 *>(p.out + ((size_t)t * H + it.h) * kHeadDim + 64 * half);
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) s[j] = (b < quad || 16 * u + j <= lane) ? s[j] * e[j] : 0.0f;
+                for (int b = 0; b < 4; ++b) {
+                    float o[16], x[16];
+                    tmem_ld16(lanes + kColO + 64 * half + 16 * b, o);
+                    tmem_ld16(lanes + kColQS + 64 * half + 16 * b, x);
+                    tmem_wait_ld();
+                    uint32_t pk[8];
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) f[8 * u + j] = __uint_as_float(pack_bf16(s[2 * j], s[2 * j + 1]));
+                    for (int j = 0; j < 8; ++j)
+                        pk[j] = pack_bf16(fmaf(lam, x[2 * j], p.scale * o[2 * j]), fmaf(lam, x[2 * j + 1], p.scale * o[2 * j + 1]));
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const uint4 y = make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
+                        if (whole)
+                            *reinterpret_cast<uint4 *>(rows + lane * 128 + (((2 * b + i) ^ (lane & 7)) << 4)) = y;
+                        else if (t < it.eos)
+                            dst[2 * b + i] = y;
                     }
                 }
-                tmem_st16(lanes + kColA + 32 * b, f);
+                tc_fence_before();
+                fence_async_smem();
+                arrive_warp(&B->o_free);
+                if (lane == 0) mbar_arrive(&B->o_tile[g & 1]);
+                ok = true;
             }
-            tmem_wait_st();
-            tc_fence_before();
-            arrive_warp(&B->p);
-            if (lane == 0) mbar_arrive(&B->gate_free[c & 1]);
-            if (!wait_warp(&B->o, c & 1, B, p.status)) break;
-            tc_fence_after();
-            // rows of 128 bytes into the V tile, which nobody reads any more, for warp 3 to store; a warp whose
-            // rows are not all tokens of the window stores them itself
-            const int iv = c * kPer + kPer - 1, t = sp.bos + c * kC + row;
-            const bool whole = c + 1 < nchunks || 32 * quad + 32 <= last_rows;
-            uint8_t *const rows = smem + (iv % kRing) * kTile + half * kHalf + quad * 4096;
-            uint4 *const dst = reinterpret_cast<uint4 *>(p.out + ((size_t)t * H + h) * kHeadDim + 64 * half);
-#pragma unroll
-            for (int b = 0; b < 4; ++b) {
-                float o[16], x[16];
-                tmem_ld16(lanes + kColO + 64 * half + 16 * b, o);
-                tmem_ld16(lanes + kColQS + 64 * half + 16 * b, x);
-                tmem_wait_ld();
-                uint32_t pk[8];
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    pk[j] = pack_bf16(fmaf(lam, x[2 * j], p.scale * o[2 * j]), fmaf(lam, x[2 * j + 1], p.scale * o[2 * j + 1]));
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const uint4 y = make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
-                    if (whole)
-                        *reinterpret_cast<uint4 *>(rows + lane * 128 + (((2 * b + i) ^ (lane & 7)) << 4)) = y;
-                    else if (t < sp.eos)
-                        dst[2 * b + i] = y;
-                }
-            }
-            tc_fence_before();
-            fence_async_smem();
-            arrive_warp(&B->o_free);
-            if (lane == 0) mbar_arrive(&B->o_tile[c & 1]);
+            if (it.nchunks == 0) ok = true;
         }
     } else {
         const int quad = warp & 3, half = (warp - kWarpS) >> 2, row = 32 * quad + lane;  // row: dk
+        const int tid = threadIdx.x - kWarpS * 32;
         const uint32_t lanes = tmem + ((uint32_t)(32 * quad) << 16) + kColD + 64 * half;
         uint8_t *const s_row = smem + kS + half * kHalf + row * 128;
+        int g = 0, u = 0, use = 0, tl = 0;  // chunks, updates, quarters and partial chunks so far
         float S[64];
-        if (!kStates && lc >= 0 && !sp.first) pdl_wait();  // the slots are written by the launch before
-        if (start) {
-            const float4 *src = reinterpret_cast<const float4 *>(start + (size_t)row * kHeadDim + 64 * half);
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const float4 x = src[i];
-                S[4 * i] = x.x, S[4 * i + 1] = x.y, S[4 * i + 2] = x.z, S[4 * i + 3] = x.w;
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < 64; ++i) S[i] = 0.0f;
-        }
-        auto publish = [&] {  // S as the BF16 operand of Q S
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                *reinterpret_cast<uint4 *>(s_row + ((i ^ (row & 7)) << 4)) =
-                    make_uint4(pack_bf16(S[8 * i], S[8 * i + 1]), pack_bf16(S[8 * i + 2], S[8 * i + 3]),
-                               pack_bf16(S[8 * i + 4], S[8 * i + 5]), pack_bf16(S[8 * i + 6], S[8 * i + 7]));
-            fence_async_smem();
-            arrive_warp(&B->s);
-        };
-        const int tid = threadIdx.x - kWarpS * 32;
-        // Splits chunk c's V, once its gate sums and V are there. In a chunk that is not full, first clears the
-        // rows past the last token: they hold another sequence's keys and values, which a zero in the
-        // other operand does not silence if they are not finite. The quarters of all chunks count through
-        // the ring of two stages (only the last chunk may have fewer than four).
-        auto split = [&](int c) {
-            const int ik = c * kPer + kPer - 2, iv = ik + 1;
-            if (!wait_warp(&B->gate[c & 1], (c >> 1) & 1, B, p.status)) return false;
-            if (!wait_warp(&B->full[iv % kRing], (iv / kRing) & 1, B, p.status)) return false;
-            if (c + 1 == nchunks && last_rows < kC) {
-                if (!wait_warp(&B->full[ik % kRing], (ik / kRing) & 1, B, p.status)) return false;
-                uint8_t *const keys = smem + (ik % kRing) * kTile, *const values = smem + (iv % kRing) * kTile;
-                for (int x = tid; x < 2048; x += kStateThreads)
-                    if (((x & 1023) >> 3) >= last_rows)
-                        *reinterpret_cast<uint4 *>(values + x * 16) = *reinterpret_cast<uint4 *>(keys + x * 16) = make_uint4(0, 0, 0, 0);
-                fence_async_smem();
-                arrive_warp(&B->tail);
-            }
-            if (c >= updates) return true;
-            const int L = c + 1 < nchunks ? kC : last_rows;
-            const Gates *G = reinterpret_cast<const Gates *>(smem + kGates) + (c & 1);
-            const uint8_t *const tile = smem + (iv % kRing) * kTile + tid * 16;
-#pragma unroll 1
-            for (int q = 0; q * kQuarter < L; ++q) {
-                const int use = 4 * c + q, st = use & 1, t = q * kQuarter + (tid >> 3);
-                if (use >= 2 && !wait_warp(&B->split_free[st], ((use >> 1) - 1) & 1, B, p.status)) return false;
-                split_quarter(tile + q * kQuarter * 128, smem + kSplit + st * kSplitStage + tid * 16, G->suffix[t], t < L);
-                fence_async_smem();
-                arrive_warp(&B->split[st]);
-            }
-            return true;
-        };
         bool ok = true;
-        for (int c = 0; c < nchunks; ++c) {
-            if (!kStates) {  // S for the queries
-                ok = c == 0 || wait_warp(&B->qs, (c - 1) & 1, B, p.status);
-                if (!ok) break;
-                publish();
-            }
-            ok = split(c);
-            if (!ok) break;
-            const float decay = (reinterpret_cast<const Gates *>(smem + kGates) + (c & 1))->decay;
-            arrive_warp(&B->gate_free[c & 1]);
-            if (c < updates) {
-                ok = wait_warp(&B->d, c & 1, B, p.status);
-                if (!ok) break;
-                tc_fence_after();
+        for (int k = 0; ok; ++k) {
+            const Item it = next_item(k);
+            if (it.nchunks < 0) break;
+            const size_t mine = (size_t)row * kHeadDim + 64 * half;
+            if (it.carried) pdl_wait();  // the slots are written by the launch before
+            if (it.start) {
+                const float4 *src = reinterpret_cast<const float4 *>(it.start + mine);
 #pragma unroll
-                for (int b = 0; b < 4; ++b) {
-                    float d[16];
-                    tmem_ld16(lanes + 16 * b, d);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) S[16 * b + j] = fmaf(S[16 * b + j], decay, d[j]);
+                for (int i = 0; i < 16; ++i) {
+                    const float4 x = src[i];
+                    S[4 * i] = x.x, S[4 * i + 1] = x.y, S[4 * i + 2] = x.z, S[4 * i + 3] = x.w;
                 }
-                tc_fence_before();
-                arrive_warp(&B->d_free);  // (only with an update: an arrival for a chunk without one could complete
-                                          // a second phase before the MMA warp has seen the first)
-            }
-        }
-        pdl_wait();  // an initial state in the same place has been read by the launches before
-        if (ok && end) {
-            float4 *dst = reinterpret_cast<float4 *>(end + (size_t)row * kHeadDim + 64 * half);
+            } else {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) dst[i] = make_float4(S[4 * i], S[4 * i + 1], S[4 * i + 2], S[4 * i + 3]);
+                for (int i = 0; i < 64; ++i) S[i] = 0.0f;
+            }
+            for (int c = 0; c < it.nchunks; ++c, ++g) {
+                ok = false;
+                if (!kStates) {  // S as the BF16 operand of Q S
+                    if (g > 0 && !wait_warp(&B->qs, (g - 1) & 1, B)) break;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        *reinterpret_cast<uint4 *>(s_row + ((i ^ (row & 7)) << 4)) =
+                            make_uint4(pack_bf16(S[8 * i], S[8 * i + 1]), pack_bf16(S[8 * i + 2], S[8 * i + 3]),
+                                       pack_bf16(S[8 * i + 4], S[8 * i + 5]), pack_bf16(S[8 * i + 6], S[8 * i + 7]));
+                    fence_async_smem();
+                    arrive_warp(&B->s);
+                }
+                const int ik = g * kPer + kPer - 2, iv = ik + 1;
+                const int L = c + 1 < it.nchunks ? kC : it.last_rows;
+                const Gates *G = reinterpret_cast<const Gates *>(smem + kGates) + (g & 1);
+                if (!wait_warp(&B->gate[g & 1], (g >> 1) & 1, B)) break;
+                if (!wait_warp(&B->full[iv % kRing], (iv / kRing) & 1, B)) break;
+                uint8_t *const values = smem + (iv % kRing) * kTile;
+                if (L < kC) {
+                    // The rows past the last token hold another sequence's keys and values, which a zero in the
+                    // other operand does not silence if they are not finite: clear them.
+                    if (!wait_warp(&B->full[ik % kRing], (ik / kRing) & 1, B)) break;
+                    uint8_t *const keys = smem + (ik % kRing) * kTile;
+#pragma unroll 1
+                    for (int x = tid; x < 2048; x += kStateThreads)
+                        if (((x & 1023) >> 3) >= L)
+                            *reinterpret_cast<uint4 *>(values + x * 16) = *reinterpret_cast<uint4 *>(keys + x * 16) = make_uint4(0, 0, 0, 0);
+                    fence_async_smem();
+                    arrive_warp(&B->tail[tl & 1]);
+                    ++tl;
+                }
+                bool lost = false;
+#pragma unroll 1
+                for (int r = 0; r < L && c < it.updates; r += kQuarter, ++use) {
+                    const int st = use & 1, t = r + (tid >> 3);
+                    lost = use >= 2 && !wait_warp(&B->split_free[st], ((use >> 1) - 1) & 1, B);
+                    if (lost) break;
+                    split_quarter(values + tid * 16 + r * 128, smem + kSplit + st * kSplitStage + tid * 16, G->suffix[t], t < L);
+                    fence_async_smem();
+                    arrive_warp(&B->split[st]);
+                }
+                if (lost) break;
+                const float decay = G->decay;
+                arrive_warp(&B->gate_free[g & 1]);
+                if (c < it.updates) {
+                    if (!wait_warp(&B->d, u & 1, B)) break;
+                    tc_fence_after();
+#pragma unroll
+                    for (int b = 0; b < 4; ++b) {
+                        float d[16];
+                        tmem_ld16(lanes + 16 * b, d);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) S[16 * b + j] = fmaf(S[16 * b + j], decay, d[j]);
+                    }
+                    tc_fence_before();
+                    arrive_warp(&B->d_free);  // (only with an update: an arrival for a chunk without one could
+                                              // complete a second phase before the MMA warp has seen the first)
+                    ++u;
+                }
+                ok = true;
+            }
+            if (it.nchunks == 0) ok = true;
+            if (ok && it.end) {
+                pdl_wait();  // an initial state in the same place has been read by the launches before
+                float4 *dst = reinterpret_cast<float4 *>(it.end + mine);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) dst[i] = make_float4(S[4 * i], S[4 * i + 1], S[4 * i + 2], S[4 * i + 3]);
+            }
         }
     }
     __syncwarp();
+    if (lane == 0 && !(warp == kWarpAlloc || (kStates && (warp == kWarpStore || (warp >= kWarpO && warp < kWarpS))))) atomicAdd(&B->finished, 1);
     __syncthreads();
     if (B->abort) {  // wait (bounded) for what is still in flight before the memory is given back
-        if (threadIdx.x == 0)
+        if (threadIdx.x == 0) {
+            if (B->abort == kTimedOut) report_error(p.status, KDA_ERR_DEVICE_TIMEOUT, (int)blockIdx.x);
+#pragma unroll 1
             for (int i = max(0, issued - kRing); i < issued; ++i) mbar_wait(&B->full[i % kRing], (i / kRing) & 1);
+            if (asked > told) mbar_wait(&B->next, told & 1);
+        }
         __syncthreads();
     }
     tc_fence_after();
@@ -724,10 +893,12 @@ constexpr int kScanThreads = 128;
 constexpr int kScanCtas = kHeadDim * kHeadDim / (4 * kScanThreads);
 
 __global__ void __launch_bounds__(kScanThreads) kda_linear_scan_kernel(const ChunkArgs a) {
-    __shared__ int scratch[kRanked + 1];
+    __shared__ int scratch[kRanked];
+    __shared__ uint8_t order[kRanked];
     const int lc = blockIdx.x / kScanCtas, part = blockIdx.x - lc * kScanCtas;
     const int pos = a.plan.seq_chains + lc, h = pos % a.p.num_heads, W = a.plan.wins;
-    const int n = seq_of_rank(a.p, pos / a.p.num_heads, scratch);
+    rank_sequences(a.p, scratch, order);
+    const int n = a.p.num_seqs <= kRanked ? order[pos / a.p.num_heads] : pos / a.p.num_heads;
     pdl_launch_dependents();
     const size_t off = ((size_t)part * kScanThreads + threadIdx.x) * 4;
     float4 S = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
@@ -854,9 +1025,10 @@ cudaError_t launch_linear_prefill(const LinearPrefillArgs &args, cudaStream_t st
     a.plan = {1, (int32_t)chains};
     a.slots = nullptr;
     a.decay = nullptr;
+    a.take_over = 0;
+    int32_t sms = 0;
+    if (sm_count_of_current_device(&sms) != KDA_OK) return cudaErrorInvalidDevice;
     if (args.ws) {
-        int32_t sms = 0;
-        if (sm_count_of_current_device(&sms) != KDA_OK) return cudaErrorInvalidDevice;
         a.plan = plan_linear(args.num_seqs, args.total_tokens, args.num_heads, sms);
     }
     const int64_t tail = chains - a.plan.seq_chains;
@@ -877,8 +1049,9 @@ cudaError_t launch_linear_prefill(const LinearPrefillArgs &args, cudaStream_t st
         e = launch(kda_linear_scan_kernel, (unsigned)(tail * kScanCtas), kScanThreads, 0, stream, true, a);
         if (e != cudaSuccess) return e;
     }
-    return launch(kda_linear_chunk_kernel<false>, (unsigned)(a.plan.seq_chains + tail * a.plan.wins), kThreads, kSmem, stream,
-                  tail > 0, a, mq, mk, mv, mo);
+    const int64_t items = a.plan.seq_chains + tail * a.plan.wins;
+    a.take_over = items > sms;
+    return launch(kda_linear_chunk_kernel<false>, (unsigned)items, kThreads, kSmem, stream, tail > 0, a, mq, mk, mv, mo);
 }
 
 }  // namespace kda
