@@ -59,7 +59,7 @@ int kda_linear_prefill(const void *q, const void *k, const void *v, const float 
     if (num_seqs < 0 || total_tokens < 0 || num_heads < 1) return KDA_ERR_INVALID_ARG;
     if (!isfinite(scale) || (decay_per_token != 0 && decay_per_token != 1)) return KDA_ERR_INVALID_ARG;
     if ((int64_t)total_tokens * num_heads * kHeadDim > (int64_t)1 << 40) return KDA_ERR_UNSUPPORTED;
-    if ((int64_t)num_seqs * num_heads > 0x7fffffffLL / 64) return KDA_ERR_UNSUPPORTED;
+    if ((int64_t)num_seqs * num_heads > 0x7fffffffLL / kHeadDim) return KDA_ERR_UNSUPPORTED;
     if (num_seqs == 0) return total_tokens == 0 ? KDA_OK : KDA_ERR_INVALID_ARG;
     if (cu_seqlens == nullptr) return KDA_ERR_INVALID_ARG;
     if (total_tokens > 0 && (!q || !k || !v || !log_decay || !out)) return KDA_ERR_INVALID_ARG;

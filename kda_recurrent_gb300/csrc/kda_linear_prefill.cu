@@ -20,18 +20,24 @@
 //   warp 0        a chunk's prefix and suffix sums of g, and its TMA loads: Q, K, V tiles (128-byte
 //                 swizzle) into a ring of five 32 KiB tiles
 //   warp 1        issues every MMA: A, Q S, D by quarters of 32 tokens (hi then lo), P V
+//   warp 2        allocates tensor memory, then the watchdog
 //   warp 3        TMA stores of O
 //   warps 4-11    A -> P in place in tensor memory, then O: both accumulators -> BF16 -> the tile that
 //                 held V
-//   warps 12-19   S in registers (row dk, 64 columns a thread): the update and the operand of Q S; V ->
-//                 hi, lo by quarters into a ring of two
+//   warps 12-19   S in registers (row dk, 64 columns a thread): the operand of Q S; V -> hi, lo by quarters
+//                 into a ring of two; the update
 // The values are decayed, not the keys, because V is only read by the last product of the chunk, so that
-// the split needs no scores. (Half of it on warps 4-11 put it on the chain from the scores to P V: 8%
-// slower; two extra warps took 1.5k cycles a quarter; four extra warps left too few registers for the
-// state. Half of D before Q S: 9% slower, since Q's tile, which the next V replaces, is then freed late.) O leaves through shared memory because a
-// thread's row-wise 32-byte stores (32 rows an instruction) kept the load/store unit busy for 2k
-// cycles a chunk, during which the MMAs' operand reads took four times their time (2.56 ms at
-// 8 x 16384 x 96 heads).
+// the split needs no scores. It is the longest part of a chunk's chain (0.85k cycles a quarter, most of
+// them latency). Measured and dropped: half of it on warps 4-11 behind P (8% slower, it delays D) or
+// between P and O (10%, it waits for the next V); on two extra warps (1.5k cycles a quarter); on four (too
+// few registers for the state); half of D before Q S (9%, Q's tile, which the next V replaces, is then
+// freed late). In the state pass, which has no P and O, warps 4-11 do every other quarter.
+//
+// O leaves through shared memory because a thread's row-wise 32-byte stores (32 rows an instruction) kept
+// the load/store unit busy for 2k cycles a chunk, during which the MMAs' operand reads took four times
+// their time (2.56 ms at 8 x 16384 x 96 heads); the end state likewise (5k cycles by direct stores).
+// These measurements are in cycles of about 1.85 GHz, all SMs busy.
+//
 // The suffix sums G_last - G_j are scanned from the end, not formed as differences, so that a
 // strong decay early in a chunk costs the later tokens' weights no precision. A log decay below
 // -128 counts as -128 (both decay to zero in FP32), which keeps the sums finite.
@@ -84,11 +90,10 @@ constexpr int kRanked = 256;
 // A chain, or a window of one. nchunks < 0: there are no more items.
 struct Item {
     const float *start;  // state before it, or NULL for zeros
-    float *end;          // where its end state goes, or NULL
     float *total;        // where its total decay goes (state pass)
     int32_t h, bos, eos, nchunks, updates, last_rows;
     int32_t carried;     // start was written by the launch before
-    int32_t pad;
+    int32_t end_row;     // where its end state goes: row of the end states' tensor, or -1
 };
 
 struct Bars {
@@ -196,9 +201,19 @@ __device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap *map, i
         : "memory");
 }
 
+__device__ __forceinline__ void prefetch_map(const CUtensorMap *map) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
+}
+
 __device__ __forceinline__ void tma_store(const CUtensorMap *map, uint32_t src, int x, int y, int z) {
     asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(map), "r"(x),
                  "r"(y), "r"(z), "r"(src)
+                 : "memory");
+}
+
+__device__ __forceinline__ void tma_store(const CUtensorMap *map, uint32_t src, int x, int y) {
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(map), "r"(x), "r"(y),
+                 "r"(src)
                  : "memory");
 }
 
@@ -303,6 +318,11 @@ __device__ __forceinline__ float *slot_of(const ChunkArgs &a, int lc, int w) {
 __device__ __forceinline__ void rank_sequences(const LinearPrefillArgs &a, int *scratch, uint8_t *order) {
     const int N = a.num_seqs;
     if (N > kRanked) return;
+    if (N == 1) {
+        if (threadIdx.x == 0) order[0] = 0;
+        __syncthreads();
+        return;
+    }
 #pragma unroll 1
     for (int i = threadIdx.x; i < N; i += blockDim.x)  // wrapping difference: any input orders
         scratch[i] = (int)((unsigned)__ldg(a.cu_seqlens + i + 1) - (unsigned)__ldg(a.cu_seqlens + i));
@@ -400,23 +420,23 @@ __device__ __forceinline__ Item item_of(const ChunkArgs &a, int i, const uint8_t
     it.eos = sp.eos;
     it.nchunks = (sp.eos - sp.bos + kC - 1) / kC;
     it.start = nullptr;
-    it.end = nullptr;
+    it.end_row = -1;
     it.carried = 0;
     it.total = nullptr;
     if (kStates) {
         if (!sp.live || sp.last) {
             it.nchunks = 0;
         } else {
-            it.end = slot_of(a, lc, w);
+            it.end_row = (lc * (W - 1) + w) * kHeadDim;
             it.total = a.decay + (size_t)lc * W + w;
         }
     } else if (sp.live) {
         it.carried = lc >= 0 && !sp.first;
         it.start = it.carried ? slot_of(a, lc, w - 1) : p.init_state ? p.init_state + chain : nullptr;
-        it.end = sp.last && p.final_state ? p.final_state + chain : nullptr;
+        it.end_row = sp.last && p.final_state ? (n * H + h) * kHeadDim : -1;
     }
     // the last chunk's update is needed only where somebody reads the end state
-    it.updates = it.end ? it.nchunks : it.nchunks - 1;
+    it.updates = it.end_row >= 0 ? it.nchunks : it.nchunks - 1;
     it.last_rows = it.eos - it.bos - (it.nchunks - 1) * kC;
     return it;
 }
@@ -431,7 +451,7 @@ template <bool kStates>
 __global__ void __launch_bounds__(kThreads, 1)
     kda_linear_chunk_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap map_q,
                             const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
-                            const __grid_constant__ CUtensorMap map_o) {
+                            const __grid_constant__ CUtensorMap map_o, const __grid_constant__ CUtensorMap map_s) {
     extern __shared__ __align__(1024) uint8_t smem[];
     const LinearPrefillArgs &p = a.p;
     Bars *B = reinterpret_cast<Bars *>(smem + kBars);
@@ -440,6 +460,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (kStates) pdl_launch_dependents();
     rank_sequences(p, reinterpret_cast<int *>(smem), B->order);
 
+    if (threadIdx.x == 32) {
+        prefetch_map(&map_k);
+        prefetch_map(&map_v);
+        prefetch_map(&map_s);
+        if (!kStates) prefetch_map(&map_q), prefetch_map(&map_o);
+    }
     if (threadIdx.x == 0) {
         for (int i = 0; i < kRing; ++i) mbar_init(&B->full[i], 1), mbar_init(&B->empty[i], 1);
         mbar_init(&B->scores, 1);
@@ -457,9 +483,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&B->o_tile[i], kOutWarps);
             mbar_init(&B->stored[i], 1);
             mbar_init(&B->gate[i], 1);
-            mbar_init(&B->gate_free[i], kStateWarps + (kStates ? 0 : kOutWarps));
+            mbar_init(&B->gate_free[i], kStateWarps + kOutWarps);
             mbar_init(&B->item[i], 1);
-            mbar_init(&B->item_free[i], 1 + kStateWarps + (kStates ? 0 : 1 + kOutWarps));
+            mbar_init(&B->item_free[i], 1 + kStateWarps + kOutWarps + (kStates ? 0 : 1));
         }
         mbar_init(&B->next, 1);
         mbar_init(&B->drain, 1);
@@ -469,20 +495,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (B->abort) report_error(p.status, KDA_ERR_CUDA, 0);
         fence_mbar_init();
     }
+    fence_async_smem();  // the ranking's scratch lies where the first tiles go
+    __syncthreads();
+    // Tensor memory is allocated while warp 0 begins to load.
+    constexpr uint32_t tmem = 0;
     if (warp == kWarpAlloc) {
         tmem_alloc(&B->tmem, kTmemCols);
         tmem_relinquish();
+        if (lane == 0 && *reinterpret_cast<volatile uint32_t *>(&B->tmem) != tmem) {
+            report_error(p.status, KDA_ERR_CUDA, 1);
+            *reinterpret_cast<volatile int32_t *>(&B->abort) = kMisplaced;
+        }
     }
-    tc_fence_before();
-    fence_async_smem();  // the ranking's scratch lies where the first tiles go
-    __syncthreads();
-    tc_fence_after();
-    constexpr uint32_t tmem = 0;
-    if (threadIdx.x == 0 && B->tmem != 0) {
-        report_error(p.status, KDA_ERR_CUDA, 1);
-        B->abort = kMisplaced;
+    if (warp != 0) {
+        tc_fence_before();
+        asm volatile("bar.sync 1, %0;" ::"n"(kThreads - 32) : "memory");
+        tc_fence_after();
     }
-    __syncthreads();
     const uint32_t base = smem_addr(smem);
     constexpr int kPer = kStates ? 2 : 3;  // tiles of a chunk: (Q,) K, V
     int issued = 0;                        // loads issued (warp 0)
@@ -495,7 +524,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         const Item &from = B->items[k & 1];
         Item it;
         it.start = from.start;
-        it.end = from.end;
         it.h = __shfl_sync(0xffffffffu, from.h, 0);
         it.bos = __shfl_sync(0xffffffffu, from.bos, 0);
         it.eos = __shfl_sync(0xffffffffu, from.eos, 0);
@@ -503,8 +531,26 @@ __global__ void __launch_bounds__(kThreads, 1)
         it.updates = __shfl_sync(0xffffffffu, from.updates, 0);
         it.last_rows = __shfl_sync(0xffffffffu, from.last_rows, 0);
         it.carried = __shfl_sync(0xffffffffu, from.carried, 0);
+        it.end_row = __shfl_sync(0xffffffffu, from.end_row, 0);
         arrive_warp(&B->item_free[k & 1]);
         return it;
+    };
+
+    // hi and lo of the quarters of chunk g (L tokens, values at `tile`) by the 256 threads of a group; `use`
+    // counts the quarters of all chunks through the ring of two stages. odd < 0: all quarters, else those of
+    // that parity.
+    auto split = [&](const uint8_t *tile, int g, int L, int &use, int odd, int tid) {
+        const Gates *G = reinterpret_cast<const Gates *>(smem + kGates) + (g & 1);
+#pragma unroll 1
+        for (int r = 0; r < L; r += kQuarter, ++use) {
+            const int st = use & 1, t = r + (tid >> 3);
+            if (odd >= 0 && st != odd) continue;
+            if (use >= 2 && !wait_warp(&B->split_free[st], ((use >> 1) - 1) & 1, B)) return false;
+            split_quarter(tile + tid * 16 + r * 128, smem + kSplit + st * kSplitStage + tid * 16, G->suffix[t], t < L);
+            fence_async_smem();
+            arrive_warp(&B->split[st]);
+        }
+        return true;
     };
 
     if (B->abort) {
@@ -688,11 +734,25 @@ __global__ void __launch_bounds__(kThreads, 1)
                 arrive_warp(&B->stored[g & 1]);
             }
         }
-        asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
-        __syncwarp();
     } else if (warp == kWarpAlloc) {
-        watch(B, kStates ? 2 + kStateWarps : 3 + kOutWarps + kStateWarps);
-    } else if (warp < kWarpO || (kStates && warp < kWarpS)) {
+        watch(B, (kStates ? 2 : 3) + kOutWarps + kStateWarps);
+    } else if (kStates && warp >= kWarpO && warp < kWarpS) {
+        // the state pass has no outputs: these warps split the odd quarters
+        const int tid = threadIdx.x - kWarpO * 32;
+        int g = 0, use = 0;
+        bool ok = true;
+        for (int k = 0; ok; ++k) {
+            const Item it = next_item(k);
+            if (it.nchunks < 0) break;
+            for (int c = 0; c < it.nchunks; ++c, ++g) {
+                const int iv = g * kPer + kPer - 1, L = c + 1 < it.nchunks ? kC : it.last_rows;
+                ok = wait_warp(&B->gate[g & 1], (g >> 1) & 1, B) && wait_warp(&B->full[iv % kRing], (iv / kRing) & 1, B) &&
+                     split(smem + (iv % kRing) * kTile, g, L, use, 1, tid);
+                if (!ok) break;
+                arrive_warp(&B->gate_free[g & 1]);
+            }
+        }
+    } else if (warp < kWarpO) {
         // idle
     } else if (warp < kWarpS) {
         const int quad = warp & 3, half = (warp - kWarpO) >> 2, row = 32 * quad + lane;
@@ -829,17 +889,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     arrive_warp(&B->tail[tl & 1]);
                     ++tl;
                 }
-                bool lost = false;
-#pragma unroll 1
-                for (int r = 0; r < L && c < it.updates; r += kQuarter, ++use) {
-                    const int st = use & 1, t = r + (tid >> 3);
-                    lost = use >= 2 && !wait_warp(&B->split_free[st], ((use >> 1) - 1) & 1, B);
-                    if (lost) break;
-                    split_quarter(values + tid * 16 + r * 128, smem + kSplit + st * kSplitStage + tid * 16, G->suffix[t], t < L);
-                    fence_async_smem();
-                    arrive_warp(&B->split[st]);
-                }
-                if (lost) break;
+                if (c < it.updates && !split(values, g, L, use, kStates ? 0 : -1, tid)) break;
                 const float decay = G->decay;
                 arrive_warp(&B->gate_free[g & 1]);
                 if (c < it.updates) {
@@ -861,16 +911,35 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ok = true;
             }
             if (it.nchunks == 0) ok = true;
-            if (ok && it.end) {
+            if (ok && it.end_row >= 0) {
                 pdl_wait();  // an initial state in the same place has been read by the launches before
-                float4 *dst = reinterpret_cast<float4 *>(it.end + mine);
+                // 32 columns at a time through the warp's own 4 KiB of the S operand, once the last chunk's
+                // queries have read it (128-byte rows, swizzled), each by one TMA store
+                if (!kStates && g > 0 && !wait_warp(&B->qs, (g - 1) & 1, B)) {
+                    ok = false;
+                    break;
+                }
+                uint8_t *const stage = smem + kS + (half * 4 + quad) * 4096;
 #pragma unroll
-                for (int i = 0; i < 16; ++i) dst[i] = make_float4(S[4 * i], S[4 * i + 1], S[4 * i + 2], S[4 * i + 3]);
+                for (int r = 0; r < 2; ++r) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        *reinterpret_cast<float4 *>(stage + lane * 128 + ((i ^ (lane & 7)) << 4)) =
+                            make_float4(S[32 * r + 4 * i], S[32 * r + 4 * i + 1], S[32 * r + 4 * i + 2], S[32 * r + 4 * i + 3]);
+                    fence_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        tma_store(&map_s, smem_addr(stage), 64 * half + 32 * r, it.end_row + 32 * quad);
+                        asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+                        asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+                    }
+                    __syncwarp();
+                }
             }
         }
     }
     __syncwarp();
-    if (lane == 0 && !(warp == kWarpAlloc || (kStates && (warp == kWarpStore || (warp >= kWarpO && warp < kWarpS))))) atomicAdd(&B->finished, 1);
+    if (lane == 0 && warp != kWarpAlloc && !(kStates && warp == kWarpStore)) atomicAdd(&B->finished, 1);
     __syncthreads();
     if (B->abort) {  // wait (bounded) for what is still in flight before the memory is given back
         if (threadIdx.x == 0) {
@@ -956,6 +1025,19 @@ cudaError_t token_map(CUtensorMap *map, const __nv_bfloat16 *base, int32_t T, in
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
+// States [states][128][128] FP32 as rows of 128, in boxes of 32 rows x 32 columns.
+cudaError_t state_map(CUtensorMap *map, const void *base, int64_t states) {
+    const EncodeTiled encode = encode_tiled();
+    if (!encode) return cudaErrorNotSupported;
+    const cuuint64_t dims[2] = {kHeadDim, (cuuint64_t)states * kHeadDim};
+    const cuuint64_t strides[1] = {kHeadDim * 4};
+    const cuuint32_t box[2] = {32, 32}, step[2] = {1, 1};
+    const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, const_cast<void *>(base), dims, strides, box, step,
+                              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
 template <bool kStates>
 cudaError_t configure_once() {
     static bool configured[64] = {};
@@ -1032,7 +1114,7 @@ cudaError_t launch_linear_prefill(const LinearPrefillArgs &args, cudaStream_t st
         a.plan = plan_linear(args.num_seqs, args.total_tokens, args.num_heads, sms);
     }
     const int64_t tail = chains - a.plan.seq_chains;
-    CUtensorMap mq, mk, mv, mo;
+    CUtensorMap mq, mk, mv, mo, ms;
     cudaError_t e = token_map(&mq, args.q, args.total_tokens, args.num_heads, kC);
     if (e == cudaSuccess) e = token_map(&mk, args.k, args.total_tokens, args.num_heads, kC);
     if (e == cudaSuccess) e = token_map(&mv, args.v, args.total_tokens, args.num_heads, kC);
@@ -1044,14 +1126,20 @@ cudaError_t launch_linear_prefill(const LinearPrefillArgs &args, cudaStream_t st
         a.decay = a.slots + slot_bytes(tail, a.plan.wins) / 4;
         e = configure_once<true>();
         if (e != cudaSuccess) return e;
-        e = launch(kda_linear_chunk_kernel<true>, (unsigned)(tail * (a.plan.wins - 1)), kThreads, kSmem, stream, false, a, mq, mk, mv, mo);
+        e = state_map(&ms, a.slots, tail * (a.plan.wins - 1));
+        if (e != cudaSuccess) return e;
+        e = launch(kda_linear_chunk_kernel<true>, (unsigned)(tail * (a.plan.wins - 1)), kThreads, kSmem, stream, false, a, mq, mk, mv, mo,
+                   ms);
         if (e != cudaSuccess) return e;
         e = launch(kda_linear_scan_kernel, (unsigned)(tail * kScanCtas), kScanThreads, 0, stream, true, a);
         if (e != cudaSuccess) return e;
     }
     const int64_t items = a.plan.seq_chains + tail * a.plan.wins;
     a.take_over = items > sms;
-    return launch(kda_linear_chunk_kernel<false>, (unsigned)items, kThreads, kSmem, stream, tail > 0, a, mq, mk, mv, mo);
+    // (without a final state the map is not used)
+    e = args.final_state ? state_map(&ms, args.final_state, chains) : state_map(&ms, args.q, 1);
+    if (e != cudaSuccess) return e;
+    return launch(kda_linear_chunk_kernel<false>, (unsigned)items, kThreads, kSmem, stream, tail > 0, a, mq, mk, mv, mo, ms);
 }
 
 }  // namespace kda
