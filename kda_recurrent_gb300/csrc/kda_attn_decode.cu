@@ -5,20 +5,20 @@
 // Every cached token is read once (512 bytes a key head) and used by the query heads that share
 // its key head, so the kernel is an HBM stream. An item is a (row, key head, 16 of its query
 // heads); its tokens come in tiles of 16. All items' tiles, laid end to end, are cut into
-// equal shares, one for each warp of the GPU (eight on an SM), so that any mixture of lengths keeps
-// every warp busy to the end. A warp walks its share alone: its own ring of cp.async stages
-// (three tiles, so about 128 KiB are in flight on an SM), no barrier with other warps. It keeps
-// the running maximum m, sum l = sum 2^(x - m) and o of its 16 query rows in registers; the products
+// equal shares, one for each CTA (one on an SM) and in it one for each of its eight warps, so that any
+// mixture of lengths keeps every warp busy to the end. A warp walks its share alone: its own ring of
+// cp.async stages (three tiles, so about 128 KiB are in flight on an SM), no barrier with other warps. It
+// keeps the running maximum m, sum l = sum 2^(x - m) and o of its 16 query rows in registers; the products
 // are m16n8k16 BF16 tensor-core instructions whose 16 rows are the query heads. (Tensor memory and
 // tcgen05 would need 64 or 128 rows; the rows here are 1 to 16, and the tensor work is a few
 // percent of the time.) The probabilities are split into two BF16 terms for P V, which costs
 // nothing here and leaves the output's own rounding as the only one.
 //
 // An item inside one share is finished by its warp. An item cut between shares leaves (m, l, o) of each
-// part in the workspace, and a second kernel joins the parts in order, which makes the result
-// independent of timing. It also writes the rows that have no token. With `weight`, the first kernel
-// stores the scores (4 bytes a query head beside the token's 512) and a third adds
-// 2^(x - lse) to the weights.
+// part in the workspace; a CTA whose whole share lies in one item joins its warps' parts first, so that
+// a long cache leaves one part an SM. A second kernel joins an item's parts in their order, which makes
+// the result independent of timing. With `weight`, the first kernel stores the scores (4 bytes a query
+// head beside the token's 512) and a third adds 2^(x - lse) to the weights.
 //
 // The order of the 128 channels inside a product is free, so the fragments are laid out for 16-byte
 // shared-memory reads: a lane's 16 bytes of a key row serve two k-steps, and of a value row eight column
@@ -41,7 +41,7 @@ constexpr int kStages = 3;
 constexpr int kStageBytes = 2 * kTokens * kHeadDim * 2;
 constexpr int kRingBytes = kWarps * kStages * kStageBytes;
 constexpr int kSmem = kRingBytes + kWarps * kStages * 4;
-constexpr int kMinTiles = 2;  // a share holds at least this many tiles, as long as there are shares to spare
+constexpr int kMinTiles = 2;  // a warp's share holds at least this many tiles, as long as there are warps to spare
 constexpr float kNegInf = -INFINITY;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
@@ -60,11 +60,26 @@ struct Part {
     float o[kRows][kHeadDim];
 };
 
+// The parts of a cut item, in their order; part i is part_at(i) of the workspace. Kept for the first share that
+// begins inside the item (count = 0: the share's beginning cuts no item, or not for the first time).
+struct Cut {
+    int32_t cta_a, warp_a, n_a;  // its first CTA: parts of n_a warps from warp_a on (or the CTA's one)
+    int32_t mid;                 // CTAs that lie inside it
+    int32_t cta_b, count;        // its last CTA; all parts
+    int32_t head, rows;          // its first row's place among all (row, query head) pairs; its rows
+    __device__ __forceinline__ int64_t part_at(int i) const {
+        const int64_t share = i < n_a         ? (int64_t)cta_a * kWarps + warp_a + i
+                              : i < n_a + mid ? (int64_t)(cta_a + 1 + i - n_a) * kWarps
+                                              : (int64_t)cta_b * kWarps + (i - n_a - mid);
+        return 2 * share + (i == 0 ? 1 : 0);
+    }
+};
+
 struct Workspace {
-    int64_t *first;  // [batch + 1]: tiles of all items of the rows before
-    float *lse2;     // [batch][query heads]: log2(sum 2^x)
-    Part *parts;     // [shares][2]: an item begun in an earlier share, and one begun in this share
-    float *scores;   // [batch][query heads][capacity] (with weights): x in log2 units
+    Cut *cuts;      // [shares]
+    float *lse2;    // [batch][query heads]: log2(sum 2^x)
+    Part *parts;    // [shares][2]: of an item begun in an earlier share, and of one begun in this share
+    float *scores;  // [batch][query heads][capacity] (with weights): x in log2 units
 };
 
 __host__ __device__ __forceinline__ int64_t align16(int64_t n) { return (n + 15) / 16 * 16; }
@@ -72,8 +87,8 @@ __host__ __device__ __forceinline__ int64_t align16(int64_t n) { return (n + 15)
 __host__ __device__ __forceinline__ int64_t workspace_layout(Workspace *w, char *base, int64_t batch, int64_t q_heads,
                                                              int64_t capacity, bool with_weight, int64_t shares) {
     int64_t at = 0;
-    if (w) w->first = reinterpret_cast<int64_t *>(base + at);
-    at += align16((batch + 1) * 8);
+    if (w) w->cuts = reinterpret_cast<Cut *>(base + at);
+    at += align16(shares * (int64_t)sizeof(Cut));
     if (w) w->lse2 = reinterpret_cast<float *>(base + at);
     at += align16(batch * q_heads * 4);
     if (w) w->parts = reinterpret_cast<Part *>(base + at);
@@ -86,20 +101,47 @@ __host__ __device__ __forceinline__ int64_t workspace_layout(Workspace *w, char 
 struct Args {
     AttnDecodeArgs p;
     Workspace ws;
-    int32_t shares;  // warps of the first kernel
+    int32_t ctas;     // of the first kernel
     int32_t q_tiles;  // items of a key head
 };
 
-// Share s covers tiles [s total / used, (s + 1) total / used) of all items, laid end to end.
-__device__ __forceinline__ int64_t shares_used(int64_t total, int shares) {
-    const int64_t most = (total + kMinTiles - 1) / kMinTiles;
-    return most < 1 ? 1 : most < shares ? most : shares;
+// CTA i of `used` has tiles [i total / used, (i + 1) total / used) of all items, laid end to end; warp w of
+// the `warps` that it uses has the same cut of those. U is uint32_t when every product fits (the host knows
+// a bound of the total), else uint64_t, whose divisions take four times the instructions: a call of one
+// short row would spend most of its time on them.
+template <typename U>
+__device__ __forceinline__ U ctas_used(U total, int ctas) {
+    const U most = (total + kMinTiles - 1) / kMinTiles;
+    return most < (U)ctas ? most : (U)ctas;
 }
 
-__device__ __forceinline__ int64_t share_begin(int64_t s, int64_t total, int64_t used) { return s * total / used; }
+template <typename U>
+__device__ __forceinline__ U cta_begin(U i, U total, U used) {
+    return i * total / used;
+}
 
-// The share that holds tile x.
-__device__ __forceinline__ int64_t share_of(int64_t x, int64_t total, int64_t used) { return ((x + 1) * used - 1) / total; }
+// The CTA that holds tile x.
+template <typename U>
+__device__ __forceinline__ U cta_of(U x, U total, U used) {
+    return ((x + 1) * used - 1) / total;
+}
+
+template <typename U>
+__device__ __forceinline__ U warps_used(U tiles) {
+    const U most = (tiles + kMinTiles - 1) / kMinTiles;
+    return most < (U)kWarps ? most : (U)kWarps;
+}
+
+template <typename U>
+__device__ __forceinline__ U warp_begin(U w, U begin, U tiles, U warps) {
+    return begin + w * tiles / warps;
+}
+
+// The warp that holds tile x of a CTA's tiles.
+template <typename U>
+__device__ __forceinline__ U warp_of(U x, U begin, U tiles, U warps) {
+    return ((x - begin + 1) * warps - 1) / tiles;
+}
 
 __device__ __forceinline__ int page_at(const PagedCache &c, int b, int j, DeviceStatus *st) {
     const int page = __ldg(c.block_table + (size_t)b * c.max_pages + (j >> c.page_shift));
@@ -128,33 +170,66 @@ __device__ __forceinline__ void next_tile(Place &at, const Args &a, int items) {
     at.tiles = (at.n + kTokens - 1) / kTokens;
 }
 
+// The cut of the item whose tiles are [x0, x1).
+template <typename U>
+__device__ __forceinline__ Cut cut_of(U x0, U x1, U total, U used) {
+    const U ca = cta_of(x0, total, used), cb = cta_of(x1 - 1, total, used);
+    const U a0 = cta_begin(ca, total, used), a1 = cta_begin(ca + 1, total, used);
+    const U b0 = cta_begin(cb, total, used), b1 = cta_begin(cb + 1, total, used);
+    const U wa = warps_used<U>(a1 - a0), first = warp_of(x0, a0, a1 - a0, wa);
+    const U last_a = x1 < a1 ? warp_of<U>(x1 - 1, a0, a1 - a0, wa) : wa - 1;
+    const U last_b = warp_of<U>(x1 - 1, b0, b1 - b0, warps_used<U>(b1 - b0));
+    const bool inside = a0 == x0 && a1 <= x1;  // the first CTA lies inside the item
+    Cut c;
+    c.cta_a = (int)ca;
+    c.cta_b = (int)cb;
+    c.mid = cb > ca ? (int)(cb - ca - 1) : 0;
+    c.warp_a = inside ? 0 : (int)first;
+    c.n_a = inside ? 1 : (int)(last_a - first + 1);
+    c.count = c.n_a + c.mid + (cb > ca ? (b1 == x1 ? 1 : (int)last_b + 1) : 0);
+    return c;
+}
+
+// A finished row by one warp: lane's four channels of o over the sum l, at maximum m.
+__device__ __forceinline__ void write_row(const Args &a, size_t head, int lane, float m, float l, const float4 &o) {
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    reinterpret_cast<uint2 *>(a.p.out + head * kHeadDim)[lane] =
+        make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
+    if (lane == 0) {
+        const float v = l == 0.0f ? kNegInf : (m == kNegInf ? 0.0f : m) + log2f(l);
+        if (a.p.lse) a.p.lse[head] = v * kLn2;
+        a.ws.lse2[head] = v;
+    }
+}
+
+template <typename U>
 __global__ void __launch_bounds__(kThreads, 1) kda_attn_decode_kernel(const Args a) {
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ int64_t s_sum[kWarps], s_start[kWarps], s_off[kWarps];
-    __shared__ int s_row[kWarps];
+    __shared__ U s_sum[kWarps], s_place[kWarps + 1], s_off[kWarps + 1];
+    __shared__ int s_row[kWarps + 1];
+    __shared__ float s_m[kWarps][kRows], s_l[kWarps][kRows];
     const AttnDecodeArgs &p = a.p;
     const PagedCache &c = p.c;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int items = c.num_kv_heads * a.q_tiles;
-    // shares go round the SMs, so that few shares spread over them
-    const int share = warp * gridDim.x + blockIdx.x;
+    const int share = blockIdx.x * kWarps + warp;
     pdl_launch_dependents();
 
-    // ---- the total, then the row and tile where each warp's share begins
+    // ---- the total, then the row and tile where each warp's share begins, and where the CTA's last tile is
     auto tiles_of = [&](int b) {
-        return b < c.batch ? (int64_t)((row_length(c, b, p.status, blockIdx.x == 0) + kTokens - 1) / kTokens) * items : 0;
+        return b < c.batch ? (U)((row_length(c, b, p.status, blockIdx.x == 0) + kTokens - 1) / kTokens) * (U)items : (U)0;
     };
-    auto block_sum = [&](int64_t x, int64_t &before) {  // inclusive prefix sum's total, and the sum before this thread
-        int64_t sum = x;
+    auto block_sum = [&](U x, U &before) {  // inclusive prefix sum's total, and the sum before this thread
+        U sum = x;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const int64_t y = __shfl_up_sync(0xffffffffu, sum, o);
+            const U y = __shfl_up_sync(0xffffffffu, sum, o);
             if (lane >= o) sum += y;
         }
         __syncthreads();
         if (lane == 31) s_sum[warp] = sum;
         __syncthreads();
-        int64_t total = 0;
+        U total = 0;
         before = sum - x;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
@@ -163,36 +238,63 @@ __global__ void __launch_bounds__(kThreads, 1) kda_attn_decode_kernel(const Args
         }
         return total;
     };
-    const int64_t x0 = tiles_of(threadIdx.x);
-    int64_t mine = x0, before0;
+    const U x0 = tiles_of(threadIdx.x);
+    U mine = x0, before0;
     for (int b = threadIdx.x + kThreads; b < c.batch; b += kThreads) mine += tiles_of(b);
-    const int64_t total = block_sum(mine, before0);
-    const int64_t used = shares_used(total, a.shares);
-    const int64_t begin = share < used ? share_begin(share, total, used) : total;
-    const int64_t end = share < used ? share_begin(share + 1, total, used) : total;
-    if (lane == 0) s_start[warp] = begin;
+    const U total = block_sum(mine, before0);
+    const U used = ctas_used(total, a.ctas);
+    const bool idle = blockIdx.x >= used;
+    const U cta_lo = idle ? total : cta_begin<U>(blockIdx.x, total, used);
+    const U cta_hi = idle ? total : cta_begin<U>(blockIdx.x + 1, total, used);
+    const U warps = idle ? 0 : warps_used<U>(cta_hi - cta_lo);
+    // s_place: where each warp's share begins (a warp without one: the CTA's end), and the CTA's last tile
+    if (threadIdx.x <= kWarps) {
+        const U w = threadIdx.x;
+        s_place[w] = w == kWarps ? cta_hi - 1 : w < warps ? warp_begin<U>(w, cta_lo, cta_hi - cta_lo, warps) : cta_hi;
+    }
     __syncthreads();
-    int64_t first = 0;
-    for (int b0 = 0; b0 < c.batch; b0 += kThreads) {
+    U first = 0;
+    for (int b0 = 0; b0 < c.batch && !idle; b0 += kThreads) {
         // (a batch that fits the block has its sums from above)
-        int64_t x = x0, before = before0, sum = total;
+        U x = x0, before = before0, sum = total;
         if (c.batch > kThreads) x = tiles_of(b0 + threadIdx.x), sum = block_sum(x, before);
-        if (blockIdx.x == 0 && b0 + threadIdx.x < c.batch) a.ws.first[b0 + threadIdx.x] = first + before;
-        for (int w = 0; w < kWarps; ++w) {
-            const int64_t off = s_start[w] - first - before;
-            if (off >= 0 && off < x) s_row[w] = b0 + threadIdx.x, s_off[w] = off;
+        for (int w = 0; w <= kWarps; ++w) {
+            const U off = s_place[w] - first - before;  // (wraps when the place lies before)
+            if (off < x) s_row[w] = b0 + threadIdx.x, s_off[w] = off;
         }
         first += sum;
-        __syncthreads();
     }
-    if (blockIdx.x == 0 && threadIdx.x == 0) a.ws.first[c.batch] = total;
-    if (begin >= end) return;
-    Place at;
-    at.b = s_row[warp];
-    at.n = row_length(c, at.b, p.status, false);
-    at.tiles = (at.n + kTokens - 1) / kTokens;
-    at.item = (int)(s_off[warp] / at.tiles);
-    at.tile = (int)(s_off[warp] - (int64_t)at.item * at.tiles);
+    __syncthreads();
+    const U begin = s_place[warp], end = (U)warp + 1 < warps ? s_place[warp + 1] : cta_hi;
+    Place at = {-1, 0, 0, 0, 0};
+    if (begin < end) {
+        at.b = s_row[warp];
+        at.n = row_length(c, at.b, p.status, false);
+        at.tiles = (at.n + kTokens - 1) / kTokens;
+        at.item = (int)(s_off[warp] / (U)at.tiles);
+        at.tile = (int)(s_off[warp] - (U)at.item * at.tiles);
+    }
+    // rows without a token
+    for (int b = blockIdx.x; b < c.batch; b += gridDim.x) {
+        if (row_length(c, b, p.status, false) > 0) continue;
+        const size_t h0 = (size_t)b * p.num_q_heads;
+        for (int i = threadIdx.x; i < p.num_q_heads * (kHeadDim / 8); i += kThreads)
+            reinterpret_cast<uint4 *>(p.out + h0 * kHeadDim)[i] = make_uint4(0, 0, 0, 0);
+        for (int i = threadIdx.x; i < p.num_q_heads; i += kThreads) {
+            if (p.lse) p.lse[h0 + i] = kNegInf;
+            a.ws.lse2[h0 + i] = kNegInf;
+        }
+    }
+    // whether the CTA's tiles are all of one item, which its warps then join before they leave
+    bool one_item = false;
+    if (warps > 1 && s_row[0] == s_row[kWarps]) {
+        const U tiles = (U)((row_length(c, s_row[0], p.status, false) + kTokens - 1) / kTokens);
+        one_item = s_off[0] / tiles == s_off[kWarps] / tiles;
+    }
+    if (begin >= end) {
+        if (lane == 0) a.ws.cuts[share].count = 0;
+        if (!one_item) return;
+    }
 
     // ---- the ring
     uint8_t *const ring = smem + warp * (kStages * kStageBytes);
@@ -200,7 +302,7 @@ __global__ void __launch_bounds__(kThreads, 1) kda_attn_decode_kernel(const Args
     const uint32_t ring_addr = smem_addr(ring);
     const int half_row = lane >> 4, chunk = lane & 15;
     Place load = at;
-    int64_t to_load = end - begin;
+    U to_load = end - begin;  // (0: a warp that is only there for the join)
     auto pages_of = [&](const Place &x) {  // of the tile's two groups of eight tokens
         const int j = x.tile * kTokens;
         int2 pg;
@@ -208,7 +310,8 @@ __global__ void __launch_bounds__(kThreads, 1) kda_attn_decode_kernel(const Args
         pg.y = c.page_shift > 3 ? pg.x : j + 8 < x.n ? page_at(c, x.b, j + 8, p.status) : -1;
         return pg;
     };
-    int2 pages = pages_of(load);
+    int2 pages = make_int2(-1, -1);
+    if (to_load > 0) pages = pages_of(load);
     auto fetch = [&](int stage) {
         if (to_load > 0) {
             const int j0 = load.tile * kTokens, h = load.item / a.q_tiles, mask = c.page_size - 1;
@@ -238,12 +341,34 @@ __global__ void __launch_bounds__(kThreads, 1) kda_attn_decode_kernel(const Args
     };
 #pragma unroll
     for (int s = 0; s < kStages - 1; ++s) fetch(s);
+    // While the first tiles come: if the share's beginning is the first to cut its item, the second kernel joins
+    // the item for it. (Found here, because there it would delay everything.)
+    if (begin < end) {
+        Cut cut;
+        cut.count = 0;
+        if (at.tile > 0) {
+            const U x0 = begin - at.tile;
+            U before = s_place[warp > 0 ? warp - 1 : 0];  // where the share before this one begins
+            if (warp == 0) {
+                const U lo = cta_begin<U>(blockIdx.x - 1, total, used), ws = warps_used<U>(cta_lo - lo);
+                before = warp_begin<U>(ws - 1, lo, cta_lo - lo, ws);
+            }
+            if (before <= x0) {
+                cut = cut_of<U>(x0, x0 + at.tiles, total, used);
+                if (cut.count == 1) cut.count = 0;  // one CTA's, joined there
+                const int h = at.item / a.q_tiles, q0 = (at.item - h * a.q_tiles) * kRows;
+                cut.head = at.b * p.num_q_heads + h * p.group + q0;
+                cut.rows = min(kRows, p.group - q0);
+            }
+        }
+        if (lane == 0) a.ws.cuts[share] = cut;
+    }
 
     // ---- the share
     const int g = lane >> 2, t = lane & 3;
     const float scale2 = p.scale * kLog2e;
     int stage = 0;
-    int64_t left = end - begin;
+    U left = end - begin;
     while (left > 0) {
         // a segment: this share's tiles of one item
         const int h = at.item / a.q_tiles, q0 = (at.item - h * a.q_tiles) * kRows;
@@ -263,7 +388,7 @@ __global__ void __launch_bounds__(kThreads, 1) kda_attn_decode_kernel(const Args
 #pragma unroll
         for (int i = 0; i < 16; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.0f;
         float m[2] = {kNegInf, kNegInf}, l[2] = {0.0f, 0.0f};
-        const int tiles = (int)min((int64_t)(at.tiles - at.tile), left);
+        const int tiles = (int)min((U)(at.tiles - at.tile), left);
         for (int i = 0; i < tiles; ++i, ++at.tile) {
             fetch(stage == 0 ? kStages - 1 : stage - 1);
             cp_async_wait<kStages - 1>();
@@ -345,6 +470,28 @@ __global__ void __launch_bounds__(kThreads, 1) kda_attn_decode_kernel(const Args
         }
         left -= tiles;
         const bool whole = from_start && at.tile == at.tiles;
+        if (one_item) {  // (the share's only segment) to shared memory, over the warp's ring
+            cp_async_wait<0>();
+            __syncwarp();
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
+                l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
+                const int row = g + 8 * r;
+                if (t == 0) s_m[warp][row] = m[r], s_l[warp][row] = l[r];
+#pragma unroll
+                for (int half = 0; half < 2; ++half)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        float4 *const dst = reinterpret_cast<float4 *>(ring + row * 512 + (64 * half + 16 * t + 8 * e) * 4);
+#pragma unroll
+                        for (int i = 0; i < 2; ++i)
+                            dst[i] = make_float4(o[8 * half + 4 * i][2 * r + e], o[8 * half + 4 * i + 1][2 * r + e],
+                                                 o[8 * half + 4 * i + 2][2 * r + e], o[8 * half + 4 * i + 3][2 * r + e]);
+                    }
+            }
+            break;
+        }
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
             l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
@@ -391,91 +538,115 @@ __global__ void __launch_bounds__(kThreads, 1) kda_attn_decode_kernel(const Args
         }
     }
     cp_async_wait<0>();
+    if (!one_item) return;
+    // ---- the warps' parts of the CTA's one item: a warp joins every eighth row
+    __syncthreads();
+    const int b = s_row[0], tiles = (row_length(c, b, p.status, false) + kTokens - 1) / kTokens;
+    const int item = (int)(s_off[0] / (U)tiles), tile = (int)(s_off[0] - (U)item * tiles);
+    const int h = item / a.q_tiles, q0 = (item - h * a.q_tiles) * kRows, rows = min(kRows, p.group - q0);
+    const bool whole = tile == 0 && cta_hi - cta_lo == (U)tiles;
+    for (int row = warp; row < rows; row += kWarps) {
+        float top = kNegInf, l = 0.0f;
+        for (int w = 0; w < (int)warps; ++w) top = fmaxf(top, s_m[w][row]);
+        const float ref = top == kNegInf ? 0.0f : top;
+        float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        for (int w = 0; w < (int)warps; ++w) {
+            const float f = ex2(s_m[w][row] - ref);
+            const float4 x = *reinterpret_cast<const float4 *>(smem + w * (kStages * kStageBytes) + row * 512 + lane * 16);
+            l = fmaf(s_l[w][row], f, l);
+            o = make_float4(fmaf(x.x, f, o.x), fmaf(x.y, f, o.y), fmaf(x.z, f, o.z), fmaf(x.w, f, o.w));
+        }
+        if (whole) {
+            write_row(a, (size_t)b * p.num_q_heads + (size_t)h * p.group + q0 + row, lane, top, l, o);
+        } else {
+            Part *const part = a.ws.parts + 2 * (size_t)(blockIdx.x * kWarps) + (tile == 0 ? 1 : 0);
+            if (lane == 0) part->m[row] = top, part->l[row] = l;
+            *reinterpret_cast<float4 *>(&part->o[row][4 * lane]) = o;
+        }
+    }
 }
 
-// Four warps for a (row, query head): rows without a token, and the parts of items cut between shares. A
-// warp takes every fourth part, so that a short cache cut into many parts costs a few loads in a row
-// (one warp for all parts took 13 us for 32 of them); the warps' sums are joined in order.
-constexpr int kJoinWarps = 4;
-
-__global__ void __launch_bounds__(kJoinWarps * 32) kda_attn_join_kernel(const Args a) {
-    __shared__ float s_m[kJoinWarps], s_l[kJoinWarps];
-    __shared__ float4 s_o[kJoinWarps][32];
-    const AttnDecodeArgs &p = a.p;
-    const int head = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int b = head / p.num_q_heads, hq = head - b * p.num_q_heads, h = hq / p.group, in_group = hq - h * p.group;
-    const int item = h * a.q_tiles + in_group / kRows, row = in_group % kRows;
-    const int n = row_length(p.c, b, p.status, false);
-    const int64_t tiles = (n + kTokens - 1) / kTokens;
-    pdl_launch_dependents();
-    pdl_wait();
-    if (tiles == 0) {
-        if (threadIdx.x == 0) {
-            if (p.lse) p.lse[head] = kNegInf;
-            a.ws.lse2[head] = kNegInf;
-        }
-        if (warp == 0) reinterpret_cast<uint2 *>(p.out + (size_t)head * kHeadDim)[lane] = make_uint2(0, 0);
-        return;
-    }
-    const int64_t total = a.ws.first[p.c.batch], x0 = a.ws.first[b] + item * tiles;
-    const int64_t used = shares_used(total, a.shares);
-    const int64_t s0 = share_of(x0, total, used), s1 = share_of(x0 + tiles - 1, total, used);
-    if (s0 == s1) return;  // finished by its warp
-    float m = kNegInf, l = 0.0f;
-    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+// Adds parts i, i + step, ... of row `row` to (m, l, o), eight loads in flight.
+__device__ __forceinline__ void add_parts(const Part *parts, const Cut &cut, int row, int lane, int i, int step, float &m, float &l,
+                                          float4 &o) {
+    const int n = cut.count;
     constexpr int kAhead = 8;
-    for (int64_t s = s0 + warp; s <= s1; s += kAhead * kJoinWarps) {
+    for (; i < n; i += kAhead * step) {
         float pm[kAhead], pl[kAhead];
         float4 po[kAhead];
         float top = m;
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i) {
-            const int64_t x = s + i * kJoinWarps;
-            pm[i] = kNegInf, pl[i] = 0.0f, po[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            if (x <= s1) {
-                const Part *const part = a.ws.parts + 2 * x + (x == s0 ? 1 : 0);
-                pm[i] = part->m[row], pl[i] = part->l[row];
-                po[i] = *reinterpret_cast<const float4 *>(&part->o[row][4 * lane]);
+        for (int e = 0; e < kAhead; ++e) {
+            const int x = i + e * step;
+            pm[e] = kNegInf, pl[e] = 0.0f, po[e] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            if (x < n) {
+                const Part *const part = parts + cut.part_at(x);
+                pm[e] = part->m[row], pl[e] = part->l[row];
+                po[e] = *reinterpret_cast<const float4 *>(&part->o[row][4 * lane]);
             }
         }
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i) top = fmaxf(top, pm[i]);
+        for (int e = 0; e < kAhead; ++e) top = fmaxf(top, pm[e]);
         const float ref = top == kNegInf ? 0.0f : top, keep = ex2(m - ref);
         l *= keep;
         o = make_float4(o.x * keep, o.y * keep, o.z * keep, o.w * keep);
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i) {
-            const float f = ex2(pm[i] - ref);
-            l = fmaf(pl[i], f, l);
-            o = make_float4(fmaf(po[i].x, f, o.x), fmaf(po[i].y, f, o.y), fmaf(po[i].z, f, o.z), fmaf(po[i].w, f, o.w));
+        for (int e = 0; e < kAhead; ++e) {
+            const float f = ex2(pm[e] - ref);
+            l = fmaf(pl[e], f, l);
+            o = make_float4(fmaf(po[e].x, f, o.x), fmaf(po[e].y, f, o.y), fmaf(po[e].z, f, o.z), fmaf(po[e].w, f, o.w));
         }
         m = top;
     }
+}
+
+// Joins the cut items: CTA (i, row) those of the eight shares of the first kernel's CTA i, a warp for each. An
+// item of many parts (at most one begins to be cut in a CTA) is joined by all warps.
+constexpr int kManyParts = 16;
+
+__global__ void __launch_bounds__(kThreads, 2) kda_attn_join_kernel(const Args a) {
+    __shared__ float s_m[kWarps], s_l[kWarps];
+    __shared__ float4 s_o[kWarps][32];
+    __shared__ Cut s_cut;
+    __shared__ int s_many;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, row = blockIdx.y;
+    if (threadIdx.x == 0) s_many = 0;
+    pdl_launch_dependents();
+    pdl_wait();
+    const Cut cut = a.ws.cuts[blockIdx.x * kWarps + warp];
+    __syncthreads();
+    if (cut.count > 0 && row < cut.rows) {
+        if (cut.count > kManyParts) {
+            if (lane == 0) s_cut = cut, s_many = 1;
+        } else {
+            float m = kNegInf, l = 0.0f;
+            float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            add_parts(a.ws.parts, cut, row, lane, 0, 1, m, l, o);
+            write_row(a, (size_t)cut.head + row, lane, m, l, o);
+        }
+    }
+    __syncthreads();
+    if (!s_many) return;
+    float m = kNegInf, l = 0.0f;
+    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    add_parts(a.ws.parts, s_cut, row, lane, warp, kWarps, m, l, o);
     if (lane == 0) s_m[warp] = m, s_l[warp] = l;
     s_o[warp][lane] = o;
     __syncthreads();
     if (warp > 0) return;
-    float top = kNegInf;
-#pragma unroll
-    for (int w = 0; w < kJoinWarps; ++w) top = fmaxf(top, s_m[w]);
-    const float ref = top == kNegInf ? 0.0f : top;
-    l = 0.0f;
+    m = kNegInf, l = 0.0f;
     o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
-    for (int w = 0; w < kJoinWarps; ++w) {
+    for (int w = 0; w < kWarps; ++w) m = fmaxf(m, s_m[w]);
+    const float ref = m == kNegInf ? 0.0f : m;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
         const float f = ex2(s_m[w] - ref);
         const float4 x = s_o[w][lane];
         l = fmaf(s_l[w], f, l);
         o = make_float4(fmaf(x.x, f, o.x), fmaf(x.y, f, o.y), fmaf(x.z, f, o.z), fmaf(x.w, f, o.w));
     }
-    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-    reinterpret_cast<uint2 *>(p.out + (size_t)head * kHeadDim)[lane] =
-        make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
-    if (lane == 0) {
-        const float v = l == 0.0f ? kNegInf : ref + log2f(l);
-        if (p.lse) p.lse[head] = v * kLn2;
-        a.ws.lse2[head] = v;
-    }
+    write_row(a, (size_t)s_cut.head + row, lane, m, l, o);
 }
 
 // weight[b][h][j] += sum over the query heads of key head h of 2^(x_j - lse), four tokens a thread.
@@ -523,13 +694,14 @@ cudaError_t launch(void (*kernel)(P...), dim3 grid, unsigned block, size_t smem,
     return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
+template <typename U>
 cudaError_t configure_once() {
     static bool configured[64] = {};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= 64 || !configured[dev]) {
-        e = cudaFuncSetAttribute(kda_attn_decode_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+        e = cudaFuncSetAttribute(kda_attn_decode_kernel<U>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
         if (e != cudaSuccess) return e;
         if (dev >= 0 && dev < 64) configured[dev] = true;
     }
@@ -546,16 +718,21 @@ int64_t attn_decode_workspace_bytes(int32_t batch, int32_t num_q_heads, int32_t,
 cudaError_t launch_attn_decode(const AttnDecodeArgs &p, cudaStream_t stream) {
     int32_t sms = 0;
     if (sm_count_of_current_device(&sms) != KDA_OK) return cudaErrorInvalidDevice;
-    cudaError_t e = configure_once();
-    if (e != cudaSuccess) return e;
     Args a;
     a.p = p;
-    a.shares = sms * kWarps;
+    a.ctas = sms;
     a.q_tiles = (p.group + kRows - 1) / kRows;
-    workspace_layout(&a.ws, static_cast<char *>(p.ws), p.c.batch, p.num_q_heads, p.c.capacity, p.weight != nullptr, a.shares);
-    e = launch(kda_attn_decode_kernel, dim3((unsigned)sms), kThreads, kSmem, stream, false, a);
+    workspace_layout(&a.ws, static_cast<char *>(p.ws), p.c.batch, p.num_q_heads, p.c.capacity, p.weight != nullptr,
+                     (int64_t)sms * kWarps);
+    // tiles there can be, times the CTAs they are cut for, in 32 bits?
+    const int64_t most = (int64_t)p.c.batch * p.c.num_kv_heads * a.q_tiles * ((p.c.capacity + kTokens - 1) / kTokens);
+    const bool small = most < (int64_t)0xffffffffLL / (std::max(sms, kWarps) + 1);
+    cudaError_t e = small ? configure_once<uint32_t>() : configure_once<uint64_t>();
     if (e != cudaSuccess) return e;
-    e = launch(kda_attn_join_kernel, dim3((unsigned)p.c.batch * (unsigned)p.num_q_heads), kJoinWarps * 32, 0, stream, true, a);
+    e = small ? launch(kda_attn_decode_kernel<uint32_t>, dim3((unsigned)sms), kThreads, kSmem, stream, false, a)
+              : launch(kda_attn_decode_kernel<uint64_t>, dim3((unsigned)sms), kThreads, kSmem, stream, false, a);
+    if (e != cudaSuccess) return e;
+    e = launch(kda_attn_join_kernel, dim3((unsigned)sms, (unsigned)std::min(p.group, kRows)), kThreads, 0, stream, true, a);
     if (e != cudaSuccess || !p.weight) return e;
     const dim3 grid((unsigned)(p.c.batch * p.c.num_kv_heads), (unsigned)std::min((p.c.capacity + kWeightTokens - 1) / kWeightTokens, 65535));
     return launch(kda_attn_weight_kernel, grid, kWeightThreads, 0, stream, true, a);

@@ -70,6 +70,28 @@ def test_attn_ragged(lens, Hkv):
     check(queries(len(lens), 2 * Hkv, 6), R.cache_inputs(lens, Hkv, 16, seed=41, max_pages=600, device=DEV))
 
 
+@pytest.mark.parametrize("lens,Hq,Hkv", [([60000], 3, 1), ([20000], 20, 1), ([0, 30000, 7], 16, 2)])
+def test_attn_long_row_of_few_heads(lens, Hq, Hkv):
+    # a row cut between many SMs: each leaves one part, and the parts are more than a warp joins alone
+    check(queries(len(lens), Hq, 54), R.cache_inputs(lens, Hkv, 64, seed=54, device=DEV))
+
+
+def test_attn_table_far_wider_than_the_rows():
+    # so many tiles that a table could hold pass 32-bit products: the work is cut in 64 bits
+    c = R.cache_inputs([300, 5000], 2, 64, seed=55, max_pages=1 << 21, device=DEV)
+    q = queries(2, 8, 55)
+    narrow = dict(c, block_table=c["block_table"][:, :80].contiguous())
+    out, lse, _ = check(q, narrow, weight=False)
+    wide, wide_lse = K.attn_decode(q, c["k_cache"], c["v_cache"], c["block_table"], c["seq_lens"], scale=SCALE,
+                                   want_lse=True)
+    assert torch.equal(wide, out) and torch.equal(wide_lse, lse)
+
+
+def test_attn_many_short_rows():
+    lens = [(7 * i) % 40 for i in range(300)]
+    check(queries(300, 8, 56), R.cache_inputs(lens, 4, 8, seed=56, device=DEV))
+
+
 def test_attn_one_token_is_its_value():
     c = R.cache_inputs([1], 1, 16, seed=42, device=DEV)
     out, lse, _ = check(queries(1, 1, 42), c)

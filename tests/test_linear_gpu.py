@@ -57,6 +57,30 @@ def test_prefill_windows(lens, H, decay):
     check(R.linear_inputs(lens, H, seed=12, decay=decay, device=DEV), workspace=True)
 
 
+def test_prefill_workspace_is_used_for_few_chains():
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    assert K.linear_prefill_workspace(1, 2048, 2, DEV) is not None
+    assert K.linear_prefill_workspace(1, 2048, sms, DEV) is None
+
+
+@pytest.mark.parametrize("final", [True, False])
+def test_prefill_many_short_chains(final):
+    # more items than SMs: every CTA takes over several, full and partial chunks in turn
+    lens = [(37 * i) % 300 for i in range(60)]
+    inp = R.linear_inputs(lens, 6, seed=22, decay="token", device=DEV)
+    out, fin = run(inp, want_final=final)
+    ref_out, ref_fin = R.linear_prefill(inp, SCALE)
+    assert_out_close(out, ref_out)
+    if final:
+        assert_state_close(fin, ref_fin, tol=STATE_TOL)
+    assert K.kda_device_status()[0] == K.KDA_OK
+
+
+def test_prefill_more_sequences_than_are_ranked():
+    lens = [1 + (13 * i) % 40 for i in range(300)]
+    check(R.linear_inputs(lens, 1, seed=23, device=DEV))
+
+
 def test_prefill_windowed_last_wave():
     # more chains than SMs, and a last wave of a few: whole chains and windows in one call
     sms = torch.cuda.get_device_properties(0).multi_processor_count
