@@ -26,6 +26,7 @@ Convenience wrappers ``prefill``, ``decode``, ``linear_prefill``, ``linear_decod
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
@@ -570,14 +571,22 @@ def kda_cache_evict(k_cache, v_cache, block_table, seq_lens, weight, new_lens, k
           int(budget), int(sink), int(recent))
 
 
+def _allocate_on(stream):
+    """Tensors made inside belong to the stream that the call runs on, so that the caching allocator
+    neither hands out memory still in use on another stream nor reuses it too early."""
+    import torch
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
 def linear_prefill(q, k, v, log_decay, cu_seqlens, init_state=None, *, scale, want_final=True, workspace=None,
                    stream=None):
     """Allocates ``out`` (and ``final_state``) and runs ``kda_linear_prefill``; returns (out, final_state)."""
     import torch
     T, H, d = q.shape
     N = cu_seqlens.shape[0] - 1
-    out = torch.empty_like(q)
-    final = torch.empty(N, H, d, d, dtype=torch.float32, device=q.device) if want_final else None
+    with _allocate_on(stream):
+        out = torch.empty_like(q)
+        final = torch.empty(N, H, d, d, dtype=torch.float32, device=q.device) if want_final else None
     kda_linear_prefill(q, k, v, log_decay, cu_seqlens, init_state, out, final, scale, workspace, stream)
     return out, final
 
@@ -585,7 +594,8 @@ def linear_prefill(q, k, v, log_decay, cu_seqlens, init_state=None, *, scale, wa
 def linear_decode(q, k, v, log_decay, slot_idx, state_pool, *, scale, stream=None):
     """Allocates ``out`` and runs ``kda_linear_decode`` (pool updated in place); returns out."""
     import torch
-    out = torch.empty_like(q)
+    with _allocate_on(stream):
+        out = torch.empty_like(q)
     kda_linear_decode(q, k, v, log_decay, slot_idx, state_pool, out, scale, stream)
     return out
 
@@ -596,14 +606,13 @@ def attn_decode(q, k_cache, v_cache, block_table, seq_lens, *, scale, want_lse=F
     ``kda_attn_decode``; returns out, or (out, lse)."""
     import torch
     B, Hq, _ = q.shape
-    out = torch.empty_like(q)
-    lse = torch.empty(B, Hq, dtype=torch.float32, device=q.device) if want_lse else None
     _require_cuda(q.device)
-    if workspace is None:
-        workspace = attn_decode_workspace(B, Hq, k_cache.shape[1], block_table.shape[1], k_cache.shape[2],
-                                          weight is not None, q.device)
-        if stream is not None:  # the caching allocator must not hand it out while `stream` uses it
-            workspace.record_stream(stream)
+    with _allocate_on(stream):
+        out = torch.empty_like(q)
+        lse = torch.empty(B, Hq, dtype=torch.float32, device=q.device) if want_lse else None
+        if workspace is None:
+            workspace = attn_decode_workspace(B, Hq, k_cache.shape[1], block_table.shape[1], k_cache.shape[2],
+                                              weight is not None, q.device)
     kda_attn_decode(q, k_cache, v_cache, block_table, seq_lens, out, scale, workspace, lse, weight, stream)
     return (out, lse) if want_lse else out
 
@@ -612,8 +621,10 @@ def cache_evict(k_cache, v_cache, block_table, seq_lens, weight, *, budget, sink
                 dst_weight=None, stream=None):
     """Allocates ``new_lens`` and ``kept`` and runs ``kda_cache_evict``; returns (new_lens, kept)."""
     import torch
-    new_lens = torch.empty_like(seq_lens)
-    kept = torch.empty(seq_lens.shape[0], k_cache.shape[1], int(budget), dtype=torch.int32, device=seq_lens.device)
+    with _allocate_on(stream):
+        new_lens = torch.empty_like(seq_lens)
+        kept = torch.empty(seq_lens.shape[0], k_cache.shape[1], int(budget), dtype=torch.int32,
+                           device=seq_lens.device)
     kda_cache_evict(k_cache, v_cache, block_table, seq_lens, weight, new_lens, kept, budget, sink, recent, dst_table,
                     dst_weight, stream)
     return new_lens, kept

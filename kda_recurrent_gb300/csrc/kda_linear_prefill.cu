@@ -868,7 +868,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                             make_uint4(pack_bf16(S[8 * i], S[8 * i + 1]), pack_bf16(S[8 * i + 2], S[8 * i + 3]),
                                        pack_bf16(S[8 * i + 4], S[8 * i + 5]), pack_bf16(S[8 * i + 6], S[8 * i + 7]));
                     fence_async_smem();
-                    arrive_warp(&B->s);
+#ifdef KDA_TEST_WITHHOLD_HANDOFF  // failure-detection test: one hand-off never comes
+                    if (g != KDA_TEST_WITHHOLD_HANDOFF)
+#endif
+                        arrive_warp(&B->s);
                 }
                 const int ik = g * kPer + kPer - 2, iv = ik + 1;
                 const int L = c + 1 < it.nchunks ? kC : it.last_rows;
