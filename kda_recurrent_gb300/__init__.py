@@ -357,57 +357,32 @@ def decode(q, k, v, g_raw, beta, slot_idx, state_pool, *, scale, lower_bound=0.0
     return out
 
 
-# The calls below are short on the GPU (a few microseconds for one token), so their host side is kept
-# short too: plain integers for pointers and streams, one expression for a tensor's checks, and the
-# device switched only when it has to be.
+# The calls below are short on the GPU (a few microseconds for one token), so their checks and the C
+# call are in compiled code (csrc/binding.cpp), which raises TypeError and ValueError like the checks
+# above.
 
-def _call(name, device, stream, *args):
-    """Calls C entry point `name` with `args` and a stream handle (None: the device's current stream,
-    by torch's raw query where it has one, which costs a twentieth of making a Stream object)."""
-    import torch
-    if device.type != "cuda":
-        _require_cuda(device)
-    index = device.index
-    if stream is not None:
-        handle = stream.cuda_stream
-    else:
-        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-        handle = raw(index) if raw else torch.cuda.current_stream(device).cuda_stream
-    fn = getattr(_lib or load(), name)
-    if torch.cuda.current_device() == index:
-        st = fn(*args, handle)
-    else:
-        with torch.cuda.device(device):
-            st = fn(*args, handle)
-    if st != KDA_OK:
-        raise KdaError(st, name)
+_native = None
 
 
-def _address(t):
-    return None if t is None else t.data_ptr()
-
-
-def _need(t, name, dtype, shape, device):
-    """_check, with its separate tests (and messages) only for a tensor that fails."""
-    if not (t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.device == device):
-        _check(t, name, dtype, shape, device)
-
-
-def _per_head_or_token(log_decay, rows, H, dtype, device):
-    """0 for a decay per head [H], 1 for one per token and head [rows, H]."""
-    if log_decay.dim() == 1:
-        _need(log_decay, "log_decay", dtype, (H,), device)
-        return 0
-    _need(log_decay, "log_decay", dtype, (rows, H), device)
-    return 1
-
-
-def _workspace_arg(workspace, device):
-    if workspace is None:
-        return None, 0
-    if workspace.device != device or not workspace.is_contiguous():
-        raise ValueError("workspace: must be a contiguous tensor on the inputs' device")
-    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+def _load_native():
+    """The compiled part of the binding (linked against the library, which has to load first)."""
+    global _native
+    load()
+    with _lock:
+        if _native is None:
+            import importlib.machinery
+            import importlib.util
+            import torch  # its libraries
+            del torch
+            path = _build.BINDING_PATH
+            if not os.path.exists(path):
+                raise RuntimeError(f"KDA binding not built: {path} (run kda_recurrent_gb300.build.build())")
+            name = "kda_gb300_binding"
+            loader = importlib.machinery.ExtensionFileLoader(name, path)
+            module = importlib.util.module_from_spec(importlib.util.spec_from_file_location(name, path, loader=loader))
+            loader.exec_module(module)
+            _native = module
+    return _native
 
 
 def kda_linear_prefill(q, k, v, log_decay, cu_seqlens, init_state, out, final_state, scale, workspace=None,
@@ -415,27 +390,10 @@ def kda_linear_prefill(q, k, v, log_decay, cu_seqlens, init_state, out, final_st
     """Varlen linear attention with a decay for each head, S_t = exp(g_t) S_{t-1} + k_t v_t^T and
     o_t = scale S_t^T q_t, into caller-owned ``out`` / ``final_state``. ``log_decay`` is g: FP32
     [H], or [T, H] for one per token. ``workspace``: see linear_prefill_workspace (or None)."""
-    import torch
-    bf16, f32 = torch.bfloat16, torch.float32
-    T, H, d = shape = q.shape
-    N = cu_seqlens.shape[0] - 1
-    dev = q.device
-    if d != HEAD_DIM:
-        raise ValueError(f"q: expected shape {(T, H, HEAD_DIM)}, got {tuple(shape)}")
-    _need(q, "q", bf16, shape, dev)
-    _need(k, "k", bf16, shape, dev)
-    _need(v, "v", bf16, shape, dev)
-    _need(out, "out", bf16, shape, dev)
-    per_token = _per_head_or_token(log_decay, T, H, f32, dev)
-    _need(cu_seqlens, "cu_seqlens", torch.int32, (N + 1,), dev)
-    if init_state is not None:
-        _need(init_state, "init_state", f32, (N, H, d, d), dev)
-    if final_state is not None:
-        _need(final_state, "final_state", f32, (N, H, d, d), dev)
-    ws, nbytes = _workspace_arg(workspace, dev)
-    _call("kda_linear_prefill", dev, stream,
-          q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), per_token, cu_seqlens.data_ptr(),
-          _address(init_state), out.data_ptr(), _address(final_state), N, T, H, float(scale), ws, nbytes)
+    st = (_native or _load_native()).linear_prefill(q, k, v, log_decay, cu_seqlens, init_state, out, final_state, scale,
+                                                    workspace, stream)
+    if st != KDA_OK:
+        raise KdaError(st, "kda_linear_prefill")
 
 
 def kda_linear_prefill_workspace_size(num_seqs, total_tokens, num_heads, sm_count=0) -> int:
@@ -458,52 +416,9 @@ def kda_linear_decode(q, k, v, log_decay, slot_idx, state_pool, out, scale, stre
     """One token per row of linear attention with a decay for each head, on ``state_pool``
     [slots, H, 128, 128] (FP32 or BF16, updated in place) at slots ``slot_idx`` (a negative one
     is a padding row). ``log_decay``: FP32 [H] or [rows, H]."""
-    import torch
-    bf16 = torch.bfloat16
-    R, H, d = shape = q.shape
-    dev = q.device
-    if d != HEAD_DIM:
-        raise ValueError(f"q: expected shape {(R, H, HEAD_DIM)}, got {tuple(shape)}")
-    _need(q, "q", bf16, shape, dev)
-    _need(k, "k", bf16, shape, dev)
-    _need(v, "v", bf16, shape, dev)
-    _need(out, "out", bf16, shape, dev)
-    per_row = _per_head_or_token(log_decay, R, H, torch.float32, dev)
-    _need(slot_idx, "slot_idx", torch.int32, (R,), dev)
-    dtype, slots = state_pool.dtype, state_pool.shape[0]
-    if dtype is not torch.float32 and dtype is not bf16:
-        raise TypeError("state_pool must be float32 or bfloat16")
-    _need(state_pool, "state_pool", dtype, (slots, H, d, d), dev)
-    _call("kda_linear_decode", dev, stream,
-          q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), per_row, slot_idx.data_ptr(),
-          state_pool.data_ptr(), slots, STATE_DTYPES["bf16" if dtype is bf16 else "f32"], out.data_ptr(), R, H,
-          float(scale))
-
-
-def _check_cache(k_cache, v_cache, block_table, seq_lens, device):
-    """(batch, key heads, page size, pages, table width, page strides) of a paged cache: k_cache and
-    v_cache BF16 [pages, Hkv, page_size, 128], contiguous but for the distance between pages."""
-    import torch
-    if k_cache.dim() != 4:
-        raise ValueError(f"k_cache: expected [pages, heads, page_size, {HEAD_DIM}], got {tuple(k_cache.shape)}")
-    pages, Hkv, ps, _ = k_cache.shape
-    shape, inner = (pages, Hkv, ps, HEAD_DIM), (ps * HEAD_DIM, HEAD_DIM, 1)
-    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
-        if t.dtype is not torch.bfloat16:
-            raise TypeError(f"{name}: expected {torch.bfloat16}, got {t.dtype}")
-        if t.shape != shape:
-            raise ValueError(f"{name}: expected shape {shape}, got {tuple(t.shape)}")
-        if t.stride()[1:] != inner:
-            raise ValueError(f"{name}: a page must be contiguous")
-        if t.device != device:
-            raise ValueError(f"{name}: expected device {device}, got {t.device}")
-    B = seq_lens.shape[0]
-    _need(seq_lens, "seq_lens", torch.int32, (B,), device)
-    if block_table.dim() != 2:
-        raise ValueError(f"block_table: expected [batch, max_pages], got {tuple(block_table.shape)}")
-    P = block_table.shape[1]
-    _need(block_table, "block_table", torch.int32, (B, P), device)
-    return B, Hkv, ps, pages, P, k_cache.stride(0), v_cache.stride(0)
+    st = (_native or _load_native()).linear_decode(q, k, v, log_decay, slot_idx, state_pool, out, scale, stream)
+    if st != KDA_OK:
+        raise KdaError(st, "kda_linear_decode")
 
 
 def kda_attn_decode(q, k_cache, v_cache, block_table, seq_lens, out, scale, workspace, lse=None, weight=None,
@@ -513,21 +428,10 @@ def kda_attn_decode(q, k_cache, v_cache, block_table, seq_lens, out, scale, work
     [B, max_pages] (negative: missing page), ``seq_lens`` int32 [B]. Optionally writes ``lse``
     [B, Hq] and adds each token's attention weight, summed over the query heads of its key head,
     to ``weight`` FP32 [B, Hkv, max_pages * page_size]. ``workspace``: attn_decode_workspace."""
-    import torch
-    dev = q.device
-    B, Hkv, ps, pages, P, ks, vs = _check_cache(k_cache, v_cache, block_table, seq_lens, dev)
-    Hq = q.shape[1]
-    _need(q, "q", torch.bfloat16, (B, Hq, HEAD_DIM), dev)
-    _need(out, "out", torch.bfloat16, (B, Hq, HEAD_DIM), dev)
-    if lse is not None:
-        _need(lse, "lse", torch.float32, (B, Hq), dev)
-    if weight is not None:
-        _need(weight, "weight", torch.float32, (B, Hkv, P * ps), dev)
-    ws, nbytes = _workspace_arg(workspace, dev)
-    _call("kda_attn_decode", dev, stream,
-          q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), ks, vs, pages, ps, block_table.data_ptr(), P,
-          seq_lens.data_ptr(), out.data_ptr(), _address(lse), _address(weight), B, Hq, Hkv,
-          float(scale), ws, nbytes)
+    st = (_native or _load_native()).attn_decode(q, k_cache, v_cache, block_table, seq_lens, out, scale, workspace, lse,
+                                                 weight, stream)
+    if st != KDA_OK:
+        raise KdaError(st, "kda_attn_decode")
 
 
 def kda_attn_decode_workspace_size(batch, num_q_heads, num_kv_heads, max_pages, page_size, with_weight=False,
@@ -555,20 +459,10 @@ def kda_cache_evict(k_cache, v_cache, block_table, seq_lens, weight, new_lens, k
     order into the pages of ``dst_table`` (None: in place), their weights into ``dst_weight``
     (None: in place). Writes ``new_lens`` int32 [B] and ``kept`` int32 [B, Hkv, budget] (old
     positions, ascending, then -1)."""
-    import torch
-    dev = k_cache.device
-    B, Hkv, ps, pages, P, ks, vs = _check_cache(k_cache, v_cache, block_table, seq_lens, dev)
-    dst_weight = weight if dst_weight is None else dst_weight
-    _need(weight, "weight", torch.float32, (B, Hkv, P * ps), dev)
-    _need(dst_weight, "dst_weight", torch.float32, (B, Hkv, P * ps), dev)
-    if dst_table is not None:
-        _need(dst_table, "dst_table", torch.int32, (B, P), dev)
-    _need(new_lens, "new_lens", torch.int32, (B,), dev)
-    _need(kept, "kept", torch.int32, (B, Hkv, budget), dev)
-    _call("kda_cache_evict", dev, stream,
-          k_cache.data_ptr(), v_cache.data_ptr(), ks, vs, pages, ps, block_table.data_ptr(), _address(dst_table), P,
-          seq_lens.data_ptr(), weight.data_ptr(), dst_weight.data_ptr(), new_lens.data_ptr(), kept.data_ptr(), B, Hkv,
-          int(budget), int(sink), int(recent))
+    st = (_native or _load_native()).cache_evict(k_cache, v_cache, block_table, seq_lens, weight, new_lens, kept, budget,
+                                                 sink, recent, dst_table, dst_weight, stream)
+    if st != KDA_OK:
+        raise KdaError(st, "kda_cache_evict")
 
 
 def _allocate_on(stream):

@@ -3,6 +3,9 @@
 Each translation unit under ``csrc/`` compiles in its own nvcc process (in
 parallel), then one link step produces the shared library next to this file in
 ``_build/``. Only ``-gencode arch=compute_103a,code=sm_103a`` is emitted.
+
+``csrc/binding.cpp``, the compiled part of the Python binding, becomes
+``_build/kda_gb300_binding.so``, linked against that library and torch's headers.
 """
 from __future__ import annotations
 
@@ -10,11 +13,13 @@ import concurrent.futures as cf
 import os
 import shutil
 import subprocess
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 BUILD_DIR = os.path.join(HERE, "_build")
 LIB_PATH = os.path.join(BUILD_DIR, "libkda_gb300.so")
+BINDING_PATH = os.path.join(BUILD_DIR, "kda_gb300_binding.so")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -34,17 +39,42 @@ def sources():
 
 
 def _deps():
-    files = sources() + [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cuh", ".h"))]
+    files = sources() + [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cuh", ".h", ".cpp"))]
     files.append(os.path.join(INCLUDE, "kda.h"))
     files.append(os.path.abspath(__file__))
     return files
 
 
 def up_to_date(lib_path: str = LIB_PATH) -> bool:
-    if not os.path.exists(lib_path):
+    made = [lib_path, BINDING_PATH] if lib_path == LIB_PATH else [lib_path]
+    if not all(os.path.exists(f) for f in made):
         return False
-    t = os.path.getmtime(lib_path)
+    t = min(os.path.getmtime(f) for f in made)
     return all(os.path.getmtime(f) <= t for f in _deps())
+
+
+def _compile_binding():
+    """Compiles csrc/binding.cpp; returns its object and what links it."""
+    import torch
+    root = os.path.dirname(os.path.abspath(torch.__file__))
+    obj = os.path.join(BUILD_DIR, "binding.o")
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-I", INCLUDE,
+           "-isystem", sysconfig.get_paths()["include"], "-isystem", os.path.join(root, "include"),
+           "-isystem", os.path.join(os.path.dirname(os.path.dirname(_nvcc())), "include"),
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+           "-c", os.path.join(CSRC, "binding.cpp"), "-o", obj]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on binding.cpp:\n{r.stdout}\n{r.stderr}")
+    return obj, ["-L", os.path.join(root, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
+
+
+def _link(cmd, path):
+    tmp = path + f".{os.getpid()}.tmp"
+    r = subprocess.run([*cmd, "-o", tmp], capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, path)
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=(), lib_path: str = LIB_PATH) -> str:
@@ -69,14 +99,14 @@ def build(force: bool = False, verbose: bool = False, extra_flags=(), lib_path: 
         return obj
 
     srcs = sources()
-    with cf.ThreadPoolExecutor(max_workers=min(len(srcs), os.cpu_count() or 1)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=min(len(srcs) + 1, os.cpu_count() or 1)) as ex:
+        binding = ex.submit(_compile_binding) if lib_path == LIB_PATH else None
         objs = list(ex.map(compile_one, srcs))
-    tmp = lib_path + f".{os.getpid()}.tmp"
-    cmd = [nvcc, *ARCH, "-shared", "-o", tmp, *objs, "-cudart", "static"]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, lib_path)
+    _link([nvcc, *ARCH, "-shared", *objs, "-cudart", "static"], lib_path)
+    if binding is not None:
+        obj, libs = binding.result()
+        _link(["g++", "-shared", obj, "-L", build_dir, "-l:" + os.path.basename(lib_path), "-Wl,-rpath,$ORIGIN", *libs],
+              BINDING_PATH)
     return lib_path
 
 
