@@ -27,6 +27,7 @@
 // conflicts.
 #include <algorithm>
 
+#include "kda_dependent.cuh"
 #include "kda_internal.cuh"
 #include "kda_mma.cuh"
 
@@ -50,9 +51,6 @@ __device__ __forceinline__ float ex2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-
-__device__ __forceinline__ void pdl_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // A part of an item: (m, l) of its rows, then o.
 struct Part {
@@ -213,7 +211,8 @@ __global__ void __launch_bounds__(kThreads, 1) kda_attn_decode_kernel(const Args
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int items = c.num_kv_heads * a.q_tiles;
     const int share = blockIdx.x * kWarps + warp;
-    pdl_launch_dependents();
+    wait_for_prior();
+    allow_next();
 
     // ---- the total, then the row and tile where each warp's share begins, and where the CTA's last tile is
     auto tiles_of = [&](int b) {
@@ -611,8 +610,8 @@ __global__ void __launch_bounds__(kThreads, 2) kda_attn_join_kernel(const Args a
     __shared__ int s_many;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, row = blockIdx.y;
     if (threadIdx.x == 0) s_many = 0;
-    pdl_launch_dependents();
-    pdl_wait();
+    allow_next();
+    wait_for_prior();
     const Cut cut = a.ws.cuts[blockIdx.x * kWarps + warp];
     __syncthreads();
     if (cut.count > 0 && row < cut.rows) {
@@ -656,7 +655,8 @@ __global__ void __launch_bounds__(kWeightThreads) kda_attn_weight_kernel(const A
     const AttnDecodeArgs &p = a.p;
     const int bh = blockIdx.x, b = bh / p.c.num_kv_heads;
     const int n = row_length(p.c, b, p.status, false);
-    pdl_wait();
+    allow_next();
+    wait_for_prior();
     const size_t head0 = (size_t)bh * p.group;
     for (int64_t j = (int64_t)blockIdx.y * kWeightTokens + 4 * threadIdx.x; j < n; j += (int64_t)gridDim.y * kWeightTokens) {
         float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
@@ -676,22 +676,6 @@ __global__ void __launch_bounds__(kWeightThreads) kda_attn_weight_kernel(const A
             for (int e = 0; j + e < n; ++e) w[e] += s[e];
         }
     }
-}
-
-template <typename... P, typename... A>
-cudaError_t launch(void (*kernel)(P...), dim3 grid, unsigned block, size_t smem, cudaStream_t stream, bool dependent,
-                   const A &...args) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3(block);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = dependent ? 1 : 0;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
 template <typename U>
@@ -729,13 +713,13 @@ cudaError_t launch_attn_decode(const AttnDecodeArgs &p, cudaStream_t stream) {
     const bool small = most < (int64_t)0xffffffffLL / (std::max(sms, kWarps) + 1);
     cudaError_t e = small ? configure_once<uint32_t>() : configure_once<uint64_t>();
     if (e != cudaSuccess) return e;
-    e = small ? launch(kda_attn_decode_kernel<uint32_t>, dim3((unsigned)sms), kThreads, kSmem, stream, false, a)
-              : launch(kda_attn_decode_kernel<uint64_t>, dim3((unsigned)sms), kThreads, kSmem, stream, false, a);
+    e = small ? launch_dependent(kda_attn_decode_kernel<uint32_t>, dim3((unsigned)sms), kThreads, kSmem, stream, a)
+              : launch_dependent(kda_attn_decode_kernel<uint64_t>, dim3((unsigned)sms), kThreads, kSmem, stream, a);
     if (e != cudaSuccess) return e;
-    e = launch(kda_attn_join_kernel, dim3((unsigned)sms, (unsigned)std::min(p.group, kRows)), kThreads, 0, stream, true, a);
+    e = launch_dependent(kda_attn_join_kernel, dim3((unsigned)sms, (unsigned)std::min(p.group, kRows)), kThreads, 0, stream, a);
     if (e != cudaSuccess || !p.weight) return e;
     const dim3 grid((unsigned)(p.c.batch * p.c.num_kv_heads), (unsigned)std::min((p.c.capacity + kWeightTokens - 1) / kWeightTokens, 65535));
-    return launch(kda_attn_weight_kernel, grid, kWeightThreads, 0, stream, true, a);
+    return launch_dependent(kda_attn_weight_kernel, grid, kWeightThreads, 0, stream, a);
 }
 
 }  // namespace kda

@@ -18,6 +18,7 @@
 //     GPU idle; between disjoint pages the tokens split too.
 #include <algorithm>
 
+#include "kda_dependent.cuh"
 #include "kda_internal.cuh"
 #include "kda_mma.cuh"
 
@@ -31,9 +32,6 @@ constexpr int kSelTile = kSelThreads * kSelElems;
 constexpr int kHeld = 4;                            // tiles of a block, held in registers together
 constexpr int kBlock = kHeld * kSelTile;
 constexpr int kBins = 2048;
-
-__device__ __forceinline__ void pdl_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // Unsigned key with the weights' order; NaN as -inf, -0 as +0.
 __device__ __forceinline__ uint32_t weight_key(float w) {
@@ -51,7 +49,8 @@ __device__ __forceinline__ float4 four_weights(const float *w, int j, int n) {
 __global__ void __launch_bounds__(kSelThreads, 1) kda_evict_select_kernel(const CacheEvictArgs a) {
     __shared__ uint32_t s_hist[kBins], s_pick[2], s_sum[kSelWarps];
     __shared__ uint64_t s_warp[2][kSelWarps];
-    pdl_launch_dependents();
+    wait_for_prior();
+    allow_next();
     const int bh = blockIdx.x, b = bh / a.c.num_kv_heads, h = bh - b * a.c.num_kv_heads;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int n = row_length(a.c, b, a.status, tid == 0 && h == 0);
@@ -205,10 +204,11 @@ __global__ void __launch_bounds__(kCopyThreads) kda_evict_copy_kernel(const Cach
     const int slice = blockIdx.y % kSlices;
     const bool values = blockIdx.y >= kSlices;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    allow_next();
     const int m = min(row_length(c, b, a.status, false), a.budget);  // (the same from the new lengths)
     const int64_t begin = (int64_t)blockIdx.z * rows_per_cta;
     const int end = (int)min((int64_t)m, begin + rows_per_cta);
-    pdl_wait();  // the selection is complete
+    wait_for_prior();  // the selection is complete
     if (blockIdx.y == 0 && blockIdx.z == 0 && h == 0 && threadIdx.x == 0) a.new_lens[b] = m;
     if (begin >= end) return;
     const int64_t stride = values ? c.v_page_stride : c.k_page_stride;
@@ -303,17 +303,9 @@ cudaError_t launch_copy(const CacheEvictArgs &a, int rows_per_cta, unsigned part
         if (e != cudaSuccess) return e;
         if (dev >= 0 && dev < 64) configured[dev] = true;
     }
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(a.c.batch * a.c.num_kv_heads), 2 * (16 / kVecs), parts);
-    cfg.blockDim = dim3(kCopyThreads);
-    cfg.dynamicSmemBytes = kSmem;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kda_evict_copy_kernel<kVecs, kOrdered>, a, rows_per_cta);
+    return launch_dependent(kda_evict_copy_kernel<kVecs, kOrdered>,
+                            dim3((unsigned)(a.c.batch * a.c.num_kv_heads), 2 * (16 / kVecs), parts), kCopyThreads, kSmem, stream, a,
+                            rows_per_cta);
 }
 
 }  // namespace
@@ -321,8 +313,8 @@ cudaError_t launch_copy(const CacheEvictArgs &a, int rows_per_cta, unsigned part
 cudaError_t launch_cache_evict(const CacheEvictArgs &a, cudaStream_t stream) {
     int32_t sms = 0;
     if (sm_count_of_current_device(&sms) != KDA_OK) return cudaErrorInvalidDevice;
-    kda_evict_select_kernel<<<(unsigned)(a.c.batch * a.c.num_kv_heads), kSelThreads, 0, stream>>>(a);
-    const cudaError_t e = cudaGetLastError();
+    const cudaError_t e =
+        launch_dependent(kda_evict_select_kernel, dim3((unsigned)(a.c.batch * a.c.num_kv_heads)), kSelThreads, 0, stream, a);
     if (e != cudaSuccess) return e;
     const int most = std::min(a.budget, a.c.capacity);  // tokens a row can keep
     const int64_t ctas = (int64_t)a.c.batch * a.c.num_kv_heads * 2;

@@ -1,0 +1,33 @@
+// Launches that overlap the end of the launch before them on the stream (programmatic dependent launch).
+//
+// A kernel launched so may start while earlier work on its stream still runs. The first kernel of a call
+// therefore passes wait_for_prior in every thread before it touches global memory, and only then lets the
+// call's next kernel start by allow_next; that one may read the call's inputs at once, but what the call's
+// earlier kernels write only after a wait of its own, which every kernel passes before it ends (so that
+// waiting for the last kernel of a call is waiting for all). A launch's latency and its kernel's set-up so
+// lie behind the kernel before it.
+#pragma once
+
+#include <cuda_runtime.h>
+
+namespace kda {
+
+__device__ __forceinline__ void wait_for_prior() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void allow_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+template <typename... P, typename... A>
+cudaError_t launch_dependent(void (*kernel)(P...), dim3 grid, unsigned block, size_t smem, cudaStream_t stream, const A &...args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(block);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+}  // namespace kda

@@ -10,6 +10,7 @@
 // to 16 columns, when there are few, so that one user's token still spreads over the GPU.
 #include <type_traits>
 
+#include "kda_dependent.cuh"
 #include "kda_internal.cuh"
 
 namespace kda {
@@ -65,6 +66,8 @@ __global__ void __launch_bounds__(kThreads) kda_linear_decode_kernel(const Linea
     const int r = item / a.num_heads, h = item - r * a.num_heads;
     const int tid = threadIdx.x;
     const size_t tok = (size_t)item * kHeadDim;
+    wait_for_prior();
+    allow_next();
     const int32_t slot = a.slot_idx[r];
     if (slot < 0 || slot >= a.num_slots) {
         if (slot >= 0 && tid == 0 && h == 0 && j0 == 0) report_error(a.status, KDA_ERR_DEVICE_INPUT, r);
@@ -121,8 +124,7 @@ cudaError_t launch_t(const LinearDecodeArgs &a, cudaStream_t stream) {
         constexpr int kWidth = decltype(width)::value;
         const int64_t ctas = items * (kHeadDim / kWidth);
         if (ctas > 0x7fffffffLL) return cudaErrorInvalidValue;
-        kda_linear_decode_kernel<T, kWidth><<<(unsigned)ctas, kThreads, 0, stream>>>(a);
-        return cudaGetLastError();
+        return launch_dependent(kda_linear_decode_kernel<T, kWidth>, dim3((unsigned)ctas), kThreads, 0, stream, a);
     };
     if (items >= 1024) return run(std::integral_constant<int, 128>());
     if (items >= 256) return run(std::integral_constant<int, 64>());

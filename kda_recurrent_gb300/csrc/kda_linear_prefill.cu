@@ -56,6 +56,7 @@
 
 #include <algorithm>
 
+#include "kda_dependent.cuh"
 #include "kda_internal.cuh"
 #include "kda_mma.cuh"
 #include "kda_tc.cuh"
@@ -293,9 +294,6 @@ __device__ __forceinline__ void arrive_warp(uint64_t *bar) {
     if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
 }
 
-__device__ __forceinline__ void pdl_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-
 struct Plan {
     int32_t wins;        // windows of each windowed chain (1: none)
     int32_t seq_chains;  // chains before the windowed ones
@@ -308,6 +306,7 @@ struct ChunkArgs {
     float *decay;  // windowed chain lc, window w: its total decay (log2)
     int32_t take_over;  // whether a CTA takes over items of CTAs not launched yet: in a grid of one wave, it
                         // would only take those that are about to start on an idle SM
+    int32_t first;      // the call's first launch
 };
 
 __device__ __forceinline__ float *slot_of(const ChunkArgs &a, int lc, int w) {
@@ -457,9 +456,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     Bars *B = reinterpret_cast<Bars *>(smem + kBars);
     // the shuffle tells the compiler that the role is one for the warp
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31, H = p.num_heads;
-    if (kStates) pdl_launch_dependents();
-    rank_sequences(p, reinterpret_cast<int *>(smem), B->order);
-
     if (threadIdx.x == 32) {
         prefetch_map(&map_k);
         prefetch_map(&map_v);
@@ -495,6 +491,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (B->abort) report_error(p.status, KDA_ERR_CUDA, 0);
         fence_mbar_init();
     }
+    if (kStates || a.first) wait_for_prior();
+    if (kStates) allow_next();
+    rank_sequences(p, reinterpret_cast<int *>(smem), B->order);
     fence_async_smem();  // the ranking's scratch lies where the first tiles go
     __syncthreads();
     // Tensor memory is allocated while warp 0 begins to load.
@@ -846,7 +845,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const Item it = next_item(k);
             if (it.nchunks < 0) break;
             const size_t mine = (size_t)row * kHeadDim + 64 * half;
-            if (it.carried) pdl_wait();  // the slots are written by the launch before
+            if (it.carried) wait_for_prior();  // the slots are written by the launch before
             if (it.start) {
                 const float4 *src = reinterpret_cast<const float4 *>(it.start + mine);
 #pragma unroll
@@ -915,7 +914,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (it.nchunks == 0) ok = true;
             if (ok && it.end_row >= 0) {
-                pdl_wait();  // an initial state in the same place has been read by the launches before
+                wait_for_prior();  // an initial state in the same place has been read by the launches before
                 // 32 columns at a time through the warp's own 4 KiB of the S operand, once the last chunk's
                 // queries have read it (128-byte rows, swizzled), each by one TMA store
                 if (!kStates && g > 0 && !wait_warp(&B->qs, (g - 1) & 1, B)) {
@@ -956,7 +955,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     if (warp == kWarpAlloc) tmem_dealloc(B->tmem, kTmemCols);
     // whatever follows this grid on the stream also follows the launches that it may overlap
-    pdl_wait();
+    wait_for_prior();
 }
 
 // S_{w+1} = exp2(g_w) S_w + D_w over the windows of a windowed chain, in place in its slots; one
@@ -971,12 +970,12 @@ __global__ void __launch_bounds__(kScanThreads) kda_linear_scan_kernel(const Chu
     const int pos = a.plan.seq_chains + lc, h = pos % a.p.num_heads, W = a.plan.wins;
     rank_sequences(a.p, scratch, order);
     const int n = a.p.num_seqs <= kRanked ? order[pos / a.p.num_heads] : pos / a.p.num_heads;
-    pdl_launch_dependents();
+    allow_next();
     const size_t off = ((size_t)part * kScanThreads + threadIdx.x) * 4;
     float4 S = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     if (a.p.init_state)
         S = *reinterpret_cast<const float4 *>(a.p.init_state + ((size_t)n * a.p.num_heads + h) * (kHeadDim * kHeadDim) + off);
-    pdl_wait();
+    wait_for_prior();
     constexpr int kAhead = 16;  // one round of loads for most plans (4: 7.4 us for 16 windows)
     for (int w0 = 0; w0 < W - 1; w0 += kAhead) {
         float4 d[kAhead];
@@ -1055,22 +1054,6 @@ cudaError_t configure_once() {
     return cudaSuccess;
 }
 
-template <typename... P, typename... A>
-cudaError_t launch(void (*kernel)(P...), unsigned grid, unsigned block, size_t smem, cudaStream_t stream, bool dependent,
-                   const A &...args) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid);
-    cfg.blockDim = dim3(block);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = dependent ? 1 : 0;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, args...);
-}
-
 // Chains that fill at most a third of the GPU, alone or as a last wave, are cut into windows.
 Plan plan_linear(int32_t num_seqs, int32_t total_tokens, int32_t num_heads, int32_t sms) {
     const int64_t chains = (int64_t)num_seqs * num_heads;
@@ -1111,6 +1094,7 @@ cudaError_t launch_linear_prefill(const LinearPrefillArgs &args, cudaStream_t st
     a.slots = nullptr;
     a.decay = nullptr;
     a.take_over = 0;
+    a.first = 1;
     int32_t sms = 0;
     if (sm_count_of_current_device(&sms) != KDA_OK) return cudaErrorInvalidDevice;
     if (args.ws) {
@@ -1131,18 +1115,19 @@ cudaError_t launch_linear_prefill(const LinearPrefillArgs &args, cudaStream_t st
         if (e != cudaSuccess) return e;
         e = state_map(&ms, a.slots, tail * (a.plan.wins - 1));
         if (e != cudaSuccess) return e;
-        e = launch(kda_linear_chunk_kernel<true>, (unsigned)(tail * (a.plan.wins - 1)), kThreads, kSmem, stream, false, a, mq, mk, mv, mo,
+        e = launch_dependent(kda_linear_chunk_kernel<true>, (unsigned)(tail * (a.plan.wins - 1)), kThreads, kSmem, stream, a, mq, mk, mv, mo,
                    ms);
         if (e != cudaSuccess) return e;
-        e = launch(kda_linear_scan_kernel, (unsigned)(tail * kScanCtas), kScanThreads, 0, stream, true, a);
+        e = launch_dependent(kda_linear_scan_kernel, (unsigned)(tail * kScanCtas), kScanThreads, 0, stream, a);
         if (e != cudaSuccess) return e;
     }
     const int64_t items = a.plan.seq_chains + tail * a.plan.wins;
     a.take_over = items > sms;
+    a.first = tail == 0;
     // (without a final state the map is not used)
     e = args.final_state ? state_map(&ms, args.final_state, chains) : state_map(&ms, args.q, 1);
     if (e != cudaSuccess) return e;
-    return launch(kda_linear_chunk_kernel<false>, (unsigned)items, kThreads, kSmem, stream, tail > 0, a, mq, mk, mv, mo, ms);
+    return launch_dependent(kda_linear_chunk_kernel<false>, (unsigned)items, kThreads, kSmem, stream, a, mq, mk, mv, mo, ms);
 }
 
 }  // namespace kda
