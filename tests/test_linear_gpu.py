@@ -61,6 +61,7 @@ def test_prefill_workspace_is_used_for_few_chains():
     sms = torch.cuda.get_device_properties(0).multi_processor_count
     assert K.linear_prefill_workspace(1, 2048, 2, DEV) is not None
     assert K.linear_prefill_workspace(1, 2048, sms, DEV) is None
+    assert K.linear_prefill_workspace(1, 256, 2, DEV) is None  # too short to gain
 
 
 @pytest.mark.parametrize("final", [True, False])
@@ -167,6 +168,49 @@ def test_prefill_sequences_do_not_touch(workspace):
     out2, fin2 = run(bad, workspace)
     for lo, hi, n in ((0, 70, 0), (199, 399, 2), (399, 1039, 3)):
         assert torch.equal(out2[lo:hi], out[lo:hi]) and torch.equal(fin2[n], fin[n])
+
+
+def test_prefill_windows_in_place():
+    # the initial state lies where the end state goes, which other windows' launches read before
+    inp = R.linear_inputs([1400, 0, 1700], 2, seed=24, decay="token", device=DEV)
+    ref_out, ref_fin = R.linear_prefill(inp, SCALE)
+    state, out = inp["init_state"].clone(), torch.empty_like(inp["q"])
+    ws = K.linear_prefill_workspace(3, 3100, 2, DEV)
+    assert ws is not None
+    K.kda_linear_prefill(inp["q"], inp["k"], inp["v"], inp["log_decay"], inp["cu_seqlens"], state, out, state, SCALE,
+                         workspace=ws)
+    assert_out_close(out, ref_out)
+    assert_state_close(state, ref_fin, tol=STATE_TOL)
+    assert torch.equal(state[1], inp["init_state"][1])
+
+
+def test_prefill_windows_do_not_touch():
+    # windows end at multiples of a chunk inside a sequence; another sequence's NaN begins right behind it
+    lens = [1300, 129, 1601]
+    inp = R.linear_inputs(lens, 2, seed=25, device=DEV)
+    assert K.linear_prefill_workspace(3, sum(lens), 2, DEV) is not None
+    out, fin = run(inp, True)
+    bad = {n: None if x is None else x.clone() for n, x in inp.items()}
+    bad["q"][1300:1429], bad["k"][1300:1429], bad["v"][1300:1429] = math.nan, math.inf, math.nan
+    out2, fin2 = run(bad, True)
+    for lo, hi, n in ((0, 1300, 0), (1429, 3030, 2)):
+        assert torch.equal(out2[lo:hi], out[lo:hi]) and torch.equal(fin2[n], fin[n])
+
+
+def test_prefill_long_windowed_last_wave():
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    H = sms + 2
+    inp = R.linear_inputs([1450], H, seed=26, decay="token", device=DEV)
+    assert K.linear_prefill_workspace(1, 1450, H, DEV) is not None
+    out, fin = run(inp, workspace=True)
+    heads = [0, sms - 1, sms, sms + 1]
+    sub = {n: x for n, x in inp.items()}
+    for n in ("q", "k", "v", "log_decay"):
+        sub[n] = inp[n][:, heads].contiguous()
+    sub["init_state"] = inp["init_state"][:, heads].contiguous()
+    ref_out, ref_fin = R.linear_prefill(sub, SCALE)
+    assert_out_close(out[:, heads], ref_out)
+    assert_state_close(fin[:, heads], ref_fin, tol=STATE_TOL)
 
 
 def test_prefill_repeats_bit_for_bit():
