@@ -25,12 +25,8 @@
 namespace kda {
 namespace {
 
-constexpr int kSelThreads = 1024;
-constexpr int kSelWarps = kSelThreads / 32;
-constexpr int kSelElems = 4;                        // tokens per thread of a tile
-constexpr int kSelTile = kSelThreads * kSelElems;
-constexpr int kHeld = 4;                            // tiles of a block, held in registers together
-constexpr int kBlock = kHeld * kSelTile;
+constexpr int kElems = 4;  // tokens per thread of a tile
+constexpr int kHeld = 4;   // tiles of a block, held in registers together
 constexpr int kBins = 2048;
 
 // Unsigned key with the weights' order; NaN as -inf, -0 as +0.
@@ -46,41 +42,46 @@ __device__ __forceinline__ float4 four_weights(const float *w, int j, int n) {
     return make_float4(j < n ? w[j] : 0.0f, j + 1 < n ? w[j + 1] : 0.0f, j + 2 < n ? w[j + 2] : 0.0f, 0.0f);
 }
 
-__global__ void __launch_bounds__(kSelThreads, 1) kda_evict_select_kernel(const CacheEvictArgs a) {
-    __shared__ uint32_t s_hist[kBins], s_pick[2], s_sum[kSelWarps];
-    __shared__ uint64_t s_warp[2][kSelWarps];
+template <int kThreads>
+__global__ void __launch_bounds__(kThreads) kda_evict_select_kernel(const CacheEvictArgs a) {
+    constexpr int kWarps = kThreads / 32, kTile = kThreads * kElems, kBlock = kHeld * kTile;
+    constexpr int kOwn = kBins / kThreads;  // digits of a thread
+    __shared__ __align__(16) uint32_t s_hist[kBins];
+    __shared__ uint32_t s_pick[3], s_sum[kWarps], s_warp[2][kWarps];
     wait_for_prior();
     allow_next();
     const int bh = blockIdx.x, b = bh / a.c.num_kv_heads, h = bh - b * a.c.num_kv_heads;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int n = row_length(a.c, b, a.status, tid == 0 && h == 0);
-    const int m = min(n, a.budget);
     const float *const w = a.weight + (size_t)bh * a.c.capacity;  // dst may alias: plain loads
     float *const dst = a.dst_weight + (size_t)bh * a.c.capacity;
     int32_t *const kept = a.kept + (size_t)bh * a.budget;
-    for (int64_t i = (int64_t)m + tid; i < a.budget; i += kSelThreads) kept[i] = -1;
+    // A row of one block stays in registers for all passes; a longer one is read again by each, a block's loads
+    // together. Where every row is of one block, it is loaded beside its length, up to the capacity.
+    const bool short_rows = a.c.capacity <= kBlock;
+    float4 held[kHeld];
+    auto load_block = [&](int j0, int n) {
+#pragma unroll
+        for (int i = 0; i < kHeld; ++i) held[i] = four_weights(w, j0 + i * kTile + 4 * tid, n);
+    };
+    if (short_rows) load_block(0, a.c.capacity);
+    const int n = row_length(a.c, b, a.status, tid == 0 && h == 0);
+    const int m = min(n, a.budget);
+    for (int64_t i = (int64_t)m + tid; i < a.budget; i += kThreads) kept[i] = -1;
     if (n <= a.budget) {
-        for (int i = tid; i < n; i += kSelThreads) {
+        for (int i = tid; i < n; i += kThreads) {
             kept[i] = i;
             dst[i] = w[i];
         }
         return;
     }
-    // a row of one block stays in registers for all passes; a longer one is read again by each, a block's
-    // loads together
-    float4 held[kHeld];
-    auto load_block = [&](int j0) {
-#pragma unroll
-        for (int i = 0; i < kHeld; ++i) held[i] = four_weights(w, j0 + i * kSelTile + 4 * tid, n);
-    };
-    load_block(0);
+    if (!short_rows) load_block(0, n);
     const int lo = a.sink, hi = n - a.recent;  // candidates: [lo, hi), more than are needed
     uint32_t need = a.budget - a.sink - a.recent, prefix = 0;
     if (need > 0) {
         for (int pass = 0; pass < 3; ++pass) {
             const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bins = pass < 2 ? 2048 : 1024;
             const uint32_t above = pass == 0 ? 0u : pass == 1 ? 0xffffffffu << 21 : 0xffffffffu << 10;
-            for (int i = tid; i < kBins; i += kSelThreads) s_hist[i] = 0;
+            for (int i = tid; i < kBins / 4; i += kThreads) reinterpret_cast<uint4 *>(s_hist)[i] = make_uint4(0, 0, 0, 0);
             __syncthreads();
             auto count = [&](const float4 &x4, int j) {
                 const float x[4] = {x4.x, x4.y, x4.z, x4.w};
@@ -92,14 +93,17 @@ __global__ void __launch_bounds__(kSelThreads, 1) kda_evict_select_kernel(const 
                 }
             };
             for (int j0 = 0; j0 < n; j0 += kBlock) {
-                if (n > kBlock) load_block(j0);
+                if (n > kBlock) load_block(j0, n);
 #pragma unroll
-                for (int i = 0; i < kHeld; ++i) count(held[i], j0 + i * kSelTile + 4 * tid);
+                for (int i = 0; i < kHeld; ++i)
+                    if (j0 + i * kTile + 128 * warp < n) count(held[i], j0 + i * kTile + 4 * tid);
             }
             __syncthreads();
-            // thread i owns digits 2 i and 2 i + 1; the digit where the count from above reaches `need`
-            const uint32_t c0 = s_hist[2 * tid], c1 = s_hist[2 * tid + 1];
-            uint32_t from = c0 + c1;  // over this thread's digits and the higher ones of its warp
+            // a thread owns kOwn digits; the one where the count from above reaches `need`
+            uint32_t c[kOwn], own = 0;
+#pragma unroll
+            for (int i = 0; i < kOwn; ++i) own += c[i] = s_hist[kOwn * tid + i];
+            uint32_t from = own;  // over this thread's digits and the higher ones of its warp
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const uint32_t x = __shfl_down_sync(0xffffffffu, from, o);
@@ -107,73 +111,80 @@ __global__ void __launch_bounds__(kSelThreads, 1) kda_evict_select_kernel(const 
             }
             if (lane == 0) s_sum[warp] = from;
             __syncthreads();
-            uint32_t rest = lane > warp ? s_sum[lane] : 0;  // (32 warps: a lane for each)
+            uint32_t higher = from - own + __reduce_add_sync(0xffffffffu, lane > warp && lane < kWarps ? s_sum[lane] : 0u);
+            if (higher < need && need <= higher + own) {
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) rest += __shfl_xor_sync(0xffffffffu, rest, o);
-            const uint32_t higher = from + rest - c0 - c1;  // above digit 2 i + 1
-            if (higher < need && need <= higher + c1) s_pick[0] = 2 * tid + 1, s_pick[1] = need - higher;
-            if (higher + c1 < need && need <= higher + c1 + c0) s_pick[0] = 2 * tid, s_pick[1] = need - higher - c1;
+                for (int i = kOwn - 1; i >= 0; --i) {
+                    if (higher < need && need <= higher + c[i]) s_pick[0] = kOwn * tid + i, s_pick[1] = need - higher, s_pick[2] = c[i];
+                    higher += c[i];
+                }
+            }
             __syncthreads();
             prefix |= s_pick[0] << shift;
             need = s_pick[1];
+            if (need == s_pick[2]) {  // all with this prefix stay: no further digit decides
+                --prefix;             // (not 0, which would be all candidates, and those are more)
+                need = 0;
+                break;
+            }
         }
     } else {
         prefix = 0xffffffffu;  // no weight has this key: none of the candidates stays
     }
     // prefix: the key T of the last candidate kept; need: how many tokens with that key stay
-    uint64_t run = 0;  // tokens before this tile: (key == T) << 32 | kept for certain
+    uint32_t sure0 = 0, ties0 = 0;  // before this tile: tokens kept for certain, tokens with key T
     int odd = 0;
     auto emit = [&](const float4 &x4, int j) {
         const float x[4] = {x4.x, x4.y, x4.z, x4.w};
-        uint64_t mine = 0, flag[kSelElems];
+        uint32_t mine = 0, flag[kElems];  // ties << 16 | kept for certain (a tile has at most 4096 tokens)
 #pragma unroll
-        for (int e = 0; e < kSelElems; ++e) {
+        for (int e = 0; e < kElems; ++e) {
             const uint32_t key = weight_key(x[e]);
             const bool safe = j + e < lo || j + e >= hi;
-            flag[e] = j + e >= n ? 0ull : (safe || key > prefix) ? 1ull : key == prefix ? 1ull << 32 : 0ull;
+            flag[e] = j + e >= n ? 0u : (safe || key > prefix) ? 1u : key == prefix ? 1u << 16 : 0u;
             mine += flag[e];
         }
-        uint64_t sum = mine;  // inclusive over the warp
+        uint32_t sum = mine;  // inclusive over the warp
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const uint64_t y = __shfl_up_sync(0xffffffffu, sum, o);
+            const uint32_t y = __shfl_up_sync(0xffffffffu, sum, o);
             if (lane >= o) sum += y;
         }
         if (lane == 31) s_warp[odd][warp] = sum;
         // one barrier a tile (the sums alternate between two arrays): after it the tile's weights have been
         // read, so that they may be overwritten
         __syncthreads();
-        const uint64_t all = s_warp[odd][lane];
-        uint64_t before = lane < warp ? all : 0, total = all;
+        const uint32_t all = lane < kWarps ? s_warp[odd][lane] : 0u;
+        const uint32_t total = __reduce_add_sync(0xffffffffu, all);
+        const uint32_t before = __reduce_add_sync(0xffffffffu, lane < warp ? all : 0u) + sum - mine;
+        uint32_t sure = sure0 + (before & 0xffffu), ties = ties0 + (before >> 16);
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            before += __shfl_xor_sync(0xffffffffu, before, o);
-            total += __shfl_xor_sync(0xffffffffu, total, o);
-        }
-        before += run + sum - mine;
-#pragma unroll
-        for (int e = 0; e < kSelElems; ++e) {
-            const uint32_t sure = (uint32_t)before, ties = (uint32_t)(before >> 32);
-            const bool stays = flag[e] == 1ull || (flag[e] != 0 && ties < need);
-            if (stays) {
+        for (int e = 0; e < kElems; ++e) {
+            if (flag[e] == 1u || (flag[e] != 0u && ties < need)) {
                 const uint32_t at = sure + min(ties, need);
                 kept[at] = j + e;
                 dst[at] = x[e];
             }
-            before += flag[e];
+            sure += flag[e] & 0xffffu;
+            ties += flag[e] >> 16;
         }
-        run += total;
+        sure0 += total & 0xffffu;
+        ties0 += total >> 16;
         odd ^= 1;
     };
     for (int j0 = 0; j0 < n; j0 += kBlock) {
-        if (n > kBlock) load_block(j0);  // (in place: no token of this block has been overwritten yet)
+        if (n > kBlock) load_block(j0, n);  // (in place: no token of this block has been overwritten yet)
 #pragma unroll
         for (int i = 0; i < kHeld; ++i)
-            if (j0 + i * kSelTile < n) emit(held[i], j0 + i * kSelTile + 4 * tid);
+            if (j0 + i * kTile < n) emit(held[i], j0 + i * kTile + 4 * tid);
     }
     __syncthreads();  // (in place: every tile is done before its tail is cleared)
-    for (int i = m + tid; i < n; i += kSelThreads) dst[i] = 0.0f;
+    for (int i = m + tid; i < n; i += kThreads) dst[i] = 0.0f;
 }
+
+// Threads of a row's CTA: a row of at most 4096 tokens is in the registers of 256, several CTAs on an SM.
+constexpr int kShortThreads = 256, kLongThreads = 1024;
+constexpr int kShortRow = kShortThreads * kElems * kHeld;
 
 constexpr int kCopyWarps = 8;
 constexpr int kCopyThreads = kCopyWarps * 32;
@@ -313,8 +324,10 @@ cudaError_t launch_copy(const CacheEvictArgs &a, int rows_per_cta, unsigned part
 cudaError_t launch_cache_evict(const CacheEvictArgs &a, cudaStream_t stream) {
     int32_t sms = 0;
     if (sm_count_of_current_device(&sms) != KDA_OK) return cudaErrorInvalidDevice;
-    const cudaError_t e =
-        launch_dependent(kda_evict_select_kernel, dim3((unsigned)(a.c.batch * a.c.num_kv_heads)), kSelThreads, 0, stream, a);
+    const dim3 rows_heads((unsigned)(a.c.batch * a.c.num_kv_heads));
+    const cudaError_t e = a.c.capacity <= kShortRow
+                              ? launch_dependent(kda_evict_select_kernel<kShortThreads>, rows_heads, kShortThreads, 0, stream, a)
+                              : launch_dependent(kda_evict_select_kernel<kLongThreads>, rows_heads, kLongThreads, 0, stream, a);
     if (e != cudaSuccess) return e;
     const int most = std::min(a.budget, a.c.capacity);  // tokens a row can keep
     const int64_t ctas = (int64_t)a.c.batch * a.c.num_kv_heads * 2;
