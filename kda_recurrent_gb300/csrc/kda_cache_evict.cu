@@ -335,7 +335,7 @@ cudaError_t launch_cache_evict(const CacheEvictArgs &a, cudaStream_t stream) {
         // one tile a CTA, or up to sixteen where that still leaves several CTAs for every SM
         const int tile = 2 * kCopyUnroll * kCopyWarps;
         const int64_t tiles = (most + tile - 1) / tile;
-        const int64_t per = std::max<int64_t>((tiles + 65534) / 65535, std::min<int64_t>(16, ctas * tiles / (8 * sms)));
+        const int64_t per = std::max<int64_t>((tiles + 65534) / 65535, std::min<int64_t>(16, ctas * tiles / (4 * sms)));
         const int rows = (int)(std::max<int64_t>(per, 1) * tile);
         return launch_copy<16, false>(a, rows, (unsigned)(((int64_t)most + rows - 1) / rows), stream);
     }
