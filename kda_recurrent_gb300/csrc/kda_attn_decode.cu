@@ -42,7 +42,7 @@ constexpr int kStages = 3;
 constexpr int kStageBytes = 2 * kTokens * kHeadDim * 2;
 constexpr int kRingBytes = kWarps * kStages * kStageBytes;
 constexpr int kSmem = kRingBytes + kWarps * kStages * 4;
-constexpr int kMinTiles = 2;  // a warp's share holds at least this many tiles, as long as there are warps to spare
+constexpr int kMinTiles = 4;  // the least share of a CTA (1000 tokens on 8 heads: 7.5 us; two tiles 7.4, eight 9.1)
 constexpr float kNegInf = -INFINITY;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
@@ -103,42 +103,18 @@ struct Args {
     int32_t q_tiles;  // items of a key head
 };
 
-// CTA i of `used` has tiles [i total / used, (i + 1) total / used) of all items, laid end to end; warp w of
-// the `warps` that it uses has the same cut of those. U is uint32_t when every product fits (the host knows
-// a bound of the total), else uint64_t, whose divisions take four times the instructions: a call of one
-// short row would spend most of its time on them.
+// All items' tiles, laid end to end, are cut into CTAs' shares of `per` tiles and those into warps' shares of
+// warp_share tiles (the last of each may be shorter): equal numbers rather than equal fractions, because then
+// one division places a tile. U is uint32_t when every place fits (the host knows a bound of the total).
 template <typename U>
-__device__ __forceinline__ U ctas_used(U total, int ctas) {
-    const U most = (total + kMinTiles - 1) / kMinTiles;
-    return most < (U)ctas ? most : (U)ctas;
+__device__ __forceinline__ U cta_share(U total, int ctas) {
+    const U per = (total + ctas - 1) / (U)ctas;
+    return per < (U)kMinTiles ? (U)kMinTiles : per;
 }
 
 template <typename U>
-__device__ __forceinline__ U cta_begin(U i, U total, U used) {
-    return i * total / used;
-}
-
-// The CTA that holds tile x.
-template <typename U>
-__device__ __forceinline__ U cta_of(U x, U total, U used) {
-    return ((x + 1) * used - 1) / total;
-}
-
-template <typename U>
-__device__ __forceinline__ U warps_used(U tiles) {
-    const U most = (tiles + kMinTiles - 1) / kMinTiles;
-    return most < (U)kWarps ? most : (U)kWarps;
-}
-
-template <typename U>
-__device__ __forceinline__ U warp_begin(U w, U begin, U tiles, U warps) {
-    return begin + w * tiles / warps;
-}
-
-// The warp that holds tile x of a CTA's tiles.
-template <typename U>
-__device__ __forceinline__ U warp_of(U x, U begin, U tiles, U warps) {
-    return ((x - begin + 1) * warps - 1) / tiles;
+__device__ __forceinline__ U warp_share(U tiles) {
+    return tiles == 0 ? 1 : (tiles + kWarps - 1) / kWarps;
 }
 
 __device__ __forceinline__ int page_at(const PagedCache &c, int b, int j, DeviceStatus *st) {
@@ -170,13 +146,11 @@ __device__ __forceinline__ void next_tile(Place &at, const Args &a, int items) {
 
 // The cut of the item whose tiles are [x0, x1).
 template <typename U>
-__device__ __forceinline__ Cut cut_of(U x0, U x1, U total, U used) {
-    const U ca = cta_of(x0, total, used), cb = cta_of(x1 - 1, total, used);
-    const U a0 = cta_begin(ca, total, used), a1 = cta_begin(ca + 1, total, used);
-    const U b0 = cta_begin(cb, total, used), b1 = cta_begin(cb + 1, total, used);
-    const U wa = warps_used<U>(a1 - a0), first = warp_of(x0, a0, a1 - a0, wa);
-    const U last_a = x1 < a1 ? warp_of<U>(x1 - 1, a0, a1 - a0, wa) : wa - 1;
-    const U last_b = warp_of<U>(x1 - 1, b0, b1 - b0, warps_used<U>(b1 - b0));
+__device__ __forceinline__ Cut cut_of(U x0, U x1, U total, U per) {
+    const U ca = x0 / per, cb = (x1 - 1) / per, a0 = ca * per, b0 = cb * per;
+    const U a1 = min(a0 + per, total), b1 = min(b0 + per, total);
+    const U wa = warp_share<U>(a1 - a0), wb = warp_share<U>(b1 - b0);
+    const U first = (x0 - a0) / wa, last_a = (min(x1, a1) - 1 - a0) / wa, last_b = (x1 - 1 - b0) / wb;
     const bool inside = a0 == x0 && a1 <= x1;  // the first CTA lies inside the item
     Cut c;
     c.cta_a = (int)ca;
@@ -203,8 +177,8 @@ __device__ __forceinline__ void write_row(const Args &a, size_t head, int lane, 
 template <typename U>
 __global__ void __launch_bounds__(kThreads, 1) kda_attn_decode_kernel(const Args a) {
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ U s_sum[kWarps], s_place[kWarps + 1], s_off[kWarps + 1];
-    __shared__ int s_row[kWarps + 1];
+    __shared__ U s_sum[kWarps], s_off[kWarps + 1];
+    __shared__ int s_row[kWarps + 1], s_len[kWarps + 1];
     __shared__ float s_m[kWarps][kRows], s_l[kWarps][kRows];
     const AttnDecodeArgs &p = a.p;
     const PagedCache &c = p.c;
@@ -215,9 +189,8 @@ __global__ void __launch_bounds__(kThreads, 1) kda_attn_decode_kernel(const Args
     allow_next();
 
     // ---- the total, then the row and tile where each warp's share begins, and where the CTA's last tile is
-    auto tiles_of = [&](int b) {
-        return b < c.batch ? (U)((row_length(c, b, p.status, blockIdx.x == 0) + kTokens - 1) / kTokens) * (U)items : (U)0;
-    };
+    auto length_of = [&](int b) { return b < c.batch ? row_length(c, b, p.status, blockIdx.x == 0) : 0; };
+    auto tiles_of = [&](int n) { return (U)((n + kTokens - 1) / kTokens) * (U)items; };
     auto block_sum = [&](U x, U &before) {  // inclusive prefix sum's total, and the sum before this thread
         U sum = x;
 #pragma unroll
@@ -237,62 +210,66 @@ __global__ void __launch_bounds__(kThreads, 1) kda_attn_decode_kernel(const Args
         }
         return total;
     };
-    const U x0 = tiles_of(threadIdx.x);
-    U mine = x0, before0;
-    for (int b = threadIdx.x + kThreads; b < c.batch; b += kThreads) mine += tiles_of(b);
+    const int n0 = length_of(threadIdx.x);
+    U mine = tiles_of(n0), before0;
+    for (int b = threadIdx.x + kThreads; b < c.batch; b += kThreads) mine += tiles_of(length_of(b));
     const U total = block_sum(mine, before0);
-    const U used = ctas_used(total, a.ctas);
-    const bool idle = blockIdx.x >= used;
-    const U cta_lo = idle ? total : cta_begin<U>(blockIdx.x, total, used);
-    const U cta_hi = idle ? total : cta_begin<U>(blockIdx.x + 1, total, used);
-    const U warps = idle ? 0 : warps_used<U>(cta_hi - cta_lo);
-    // s_place: where each warp's share begins (a warp without one: the CTA's end), and the CTA's last tile
-    if (threadIdx.x <= kWarps) {
-        const U w = threadIdx.x;
-        s_place[w] = w == kWarps ? cta_hi - 1 : w < warps ? warp_begin<U>(w, cta_lo, cta_hi - cta_lo, warps) : cta_hi;
-    }
-    __syncthreads();
+    const U per = cta_share(total, a.ctas);
+    const U cta_lo = min((U)blockIdx.x * per, total), cta_hi = min(cta_lo + per, total);
+    const U per_warp = warp_share<U>(cta_hi - cta_lo);
     U first = 0;
-    for (int b0 = 0; b0 < c.batch && !idle; b0 += kThreads) {
+    for (int b0 = 0; b0 < c.batch && cta_lo < cta_hi; b0 += kThreads) {
         // (a batch that fits the block has its sums from above)
-        U x = x0, before = before0, sum = total;
-        if (c.batch > kThreads) x = tiles_of(b0 + threadIdx.x), sum = block_sum(x, before);
-        for (int w = 0; w <= kWarps; ++w) {
-            const U off = s_place[w] - first - before;  // (wraps when the place lies before)
-            if (off < x) s_row[w] = b0 + threadIdx.x, s_off[w] = off;
+        int n = n0;
+        U before = before0, sum = total;
+        if (c.batch > kThreads) n = length_of(b0 + threadIdx.x), sum = block_sum(tiles_of(n), before);
+        const U x = tiles_of(n);
+#pragma unroll
+        for (int w = 0; w <= kWarps; ++w) {  // (w = kWarps: the CTA's last tile)
+            const U place = w == kWarps ? cta_hi - 1 : cta_lo + w * per_warp;
+            const U off = place - first - before;  // (wraps when the place lies before)
+            if (off < x) s_row[w] = b0 + threadIdx.x, s_off[w] = off, s_len[w] = n;
         }
         first += sum;
     }
     __syncthreads();
-    const U begin = s_place[warp], end = (U)warp + 1 < warps ? s_place[warp + 1] : cta_hi;
+    const U begin = min(cta_lo + warp * per_warp, cta_hi), end = min(begin + per_warp, cta_hi);
     Place at = {-1, 0, 0, 0, 0};
     if (begin < end) {
         at.b = s_row[warp];
-        at.n = row_length(c, at.b, p.status, false);
+        at.n = s_len[warp];
         at.tiles = (at.n + kTokens - 1) / kTokens;
         at.item = (int)(s_off[warp] / (U)at.tiles);
         at.tile = (int)(s_off[warp] - (U)at.item * at.tiles);
     }
-    // rows without a token
-    for (int b = blockIdx.x; b < c.batch; b += gridDim.x) {
-        if (row_length(c, b, p.status, false) > 0) continue;
-        const size_t h0 = (size_t)b * p.num_q_heads;
-        for (int i = threadIdx.x; i < p.num_q_heads * (kHeadDim / 8); i += kThreads)
-            reinterpret_cast<uint4 *>(p.out + h0 * kHeadDim)[i] = make_uint4(0, 0, 0, 0);
-        for (int i = threadIdx.x; i < p.num_q_heads; i += kThreads) {
-            if (p.lse) p.lse[h0 + i] = kNegInf;
-            a.ws.lse2[h0 + i] = kNegInf;
-        }
-    }
-    // whether the CTA's tiles are all of one item, which its warps then join before they leave
+    // Whether the CTA's tiles are all of one item and of several warps, which then join before they leave: its
+    // first tile's item, and the end of that.
     bool one_item = false;
-    if (warps > 1 && s_row[0] == s_row[kWarps]) {
-        const U tiles = (U)((row_length(c, s_row[0], p.status, false) + kTokens - 1) / kTokens);
-        one_item = s_off[0] / tiles == s_off[kWarps] / tiles;
+    int cta_item = 0, cta_tile = 0, cta_tiles = 0;
+    if (cta_hi - cta_lo > per_warp && s_row[0] == s_row[kWarps]) {
+        cta_tiles = (s_len[0] + kTokens - 1) / kTokens;
+        cta_item = (int)(s_off[0] / (U)cta_tiles);
+        cta_tile = (int)(s_off[0] - (U)cta_item * cta_tiles);
+        one_item = cta_hi - cta_lo <= (U)(cta_tiles - cta_tile);
     }
+    auto empty_rows = [&] {
+        for (int b = blockIdx.x; b < c.batch; b += gridDim.x) {
+            if (row_length(c, b, p.status, false) > 0) continue;
+            const size_t h0 = (size_t)b * p.num_q_heads;
+            for (int i = threadIdx.x; i < p.num_q_heads * (kHeadDim / 8); i += kThreads)
+                reinterpret_cast<uint4 *>(p.out + h0 * kHeadDim)[i] = make_uint4(0, 0, 0, 0);
+            for (int i = threadIdx.x; i < p.num_q_heads; i += kThreads) {
+                if (p.lse) p.lse[h0 + i] = kNegInf;
+                a.ws.lse2[h0 + i] = kNegInf;
+            }
+        }
+    };
     if (begin >= end) {
         if (lane == 0) a.ws.cuts[share].count = 0;
-        if (!one_item) return;
+        if (!one_item) {
+            empty_rows();
+            return;
+        }
     }
 
     // ---- the ring
@@ -347,13 +324,10 @@ __global__ void __launch_bounds__(kThreads, 1) kda_attn_decode_kernel(const Args
         cut.count = 0;
         if (at.tile > 0) {
             const U x0 = begin - at.tile;
-            U before = s_place[warp > 0 ? warp - 1 : 0];  // where the share before this one begins
-            if (warp == 0) {
-                const U lo = cta_begin<U>(blockIdx.x - 1, total, used), ws = warps_used<U>(cta_lo - lo);
-                before = warp_begin<U>(ws - 1, lo, cta_lo - lo, ws);
-            }
+            // where the share before this one begins (the CTA before is a full one)
+            const U before = warp > 0 ? begin - per_warp : begin - ((per - 1) % warp_share(per) + 1);
             if (before <= x0) {
-                cut = cut_of<U>(x0, x0 + at.tiles, total, used);
+                cut = cut_of<U>(x0, x0 + at.tiles, total, per);
                 if (cut.count == 1) cut.count = 0;  // one CTA's, joined there
                 const int h = at.item / a.q_tiles, q0 = (at.item - h * a.q_tiles) * kRows;
                 cut.head = at.b * p.num_q_heads + h * p.group + q0;
@@ -362,6 +336,7 @@ __global__ void __launch_bounds__(kThreads, 1) kda_attn_decode_kernel(const Args
         }
         if (lane == 0) a.ws.cuts[share] = cut;
     }
+    empty_rows();
 
     // ---- the share
     const int g = lane >> 2, t = lane & 3;
@@ -540,16 +515,15 @@ __global__ void __launch_bounds__(kThreads, 1) kda_attn_decode_kernel(const Args
     if (!one_item) return;
     // ---- the warps' parts of the CTA's one item: a warp joins every eighth row
     __syncthreads();
-    const int b = s_row[0], tiles = (row_length(c, b, p.status, false) + kTokens - 1) / kTokens;
-    const int item = (int)(s_off[0] / (U)tiles), tile = (int)(s_off[0] - (U)item * tiles);
-    const int h = item / a.q_tiles, q0 = (item - h * a.q_tiles) * kRows, rows = min(kRows, p.group - q0);
-    const bool whole = tile == 0 && cta_hi - cta_lo == (U)tiles;
+    const int b = s_row[0], warps = (int)((cta_hi - cta_lo + per_warp - 1) / per_warp);
+    const int h = cta_item / a.q_tiles, q0 = (cta_item - h * a.q_tiles) * kRows, rows = min(kRows, p.group - q0);
+    const bool whole = cta_tile == 0 && cta_hi - cta_lo == (U)cta_tiles;
     for (int row = warp; row < rows; row += kWarps) {
         float top = kNegInf, l = 0.0f;
-        for (int w = 0; w < (int)warps; ++w) top = fmaxf(top, s_m[w][row]);
+        for (int w = 0; w < warps; ++w) top = fmaxf(top, s_m[w][row]);
         const float ref = top == kNegInf ? 0.0f : top;
         float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        for (int w = 0; w < (int)warps; ++w) {
+        for (int w = 0; w < warps; ++w) {
             const float f = ex2(s_m[w][row] - ref);
             const float4 x = *reinterpret_cast<const float4 *>(smem + w * (kStages * kStageBytes) + row * 512 + lane * 16);
             l = fmaf(s_l[w][row], f, l);
@@ -558,7 +532,7 @@ __global__ void __launch_bounds__(kThreads, 1) kda_attn_decode_kernel(const Args
         if (whole) {
             write_row(a, (size_t)b * p.num_q_heads + (size_t)h * p.group + q0 + row, lane, top, l, o);
         } else {
-            Part *const part = a.ws.parts + 2 * (size_t)(blockIdx.x * kWarps) + (tile == 0 ? 1 : 0);
+            Part *const part = a.ws.parts + 2 * (size_t)(blockIdx.x * kWarps) + (cta_tile == 0 ? 1 : 0);
             if (lane == 0) part->m[row] = top, part->l[row] = l;
             *reinterpret_cast<float4 *>(&part->o[row][4 * lane]) = o;
         }
@@ -610,8 +584,10 @@ __global__ void __launch_bounds__(kThreads, 2) kda_attn_join_kernel(const Args a
     __shared__ int s_many;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, row = blockIdx.y;
     if (threadIdx.x == 0) s_many = 0;
-    allow_next();
+    // (a launch for the weights starts only when the first kernel's scores are there, which it reads at once)
+    if (!a.p.weight) allow_next();
     wait_for_prior();
+    if (a.p.weight) allow_next();
     const Cut cut = a.ws.cuts[blockIdx.x * kWarps + warp];
     __syncthreads();
     if (cut.count > 0 && row < cut.rows) {
@@ -648,7 +624,8 @@ __global__ void __launch_bounds__(kThreads, 2) kda_attn_join_kernel(const Args a
     write_row(a, (size_t)s_cut.head + row, lane, m, l, o);
 }
 
-// weight[b][h][j] += sum over the query heads of key head h of 2^(x_j - lse), four tokens a thread.
+// weight[b][h][j] += sum over the query heads of key head h of 2^(x_j - lse), four tokens a thread. It starts
+// beside the join, whose sums it waits for with its first loads done.
 constexpr int kWeightThreads = 256, kWeightTokens = 4 * kWeightThreads;
 
 __global__ void __launch_bounds__(kWeightThreads) kda_attn_weight_kernel(const Args a) {
@@ -656,24 +633,39 @@ __global__ void __launch_bounds__(kWeightThreads) kda_attn_weight_kernel(const A
     const int bh = blockIdx.x, b = bh / p.c.num_kv_heads;
     const int n = row_length(p.c, b, p.status, false);
     allow_next();
-    wait_for_prior();
     const size_t head0 = (size_t)bh * p.group;
-    for (int64_t j = (int64_t)blockIdx.y * kWeightTokens + 4 * threadIdx.x; j < n; j += (int64_t)gridDim.y * kWeightTokens) {
+    constexpr int kAhead = 8;
+    float4 x[kAhead], old;
+    auto load = [&](int64_t j) {
+        const float *const scores = a.ws.scores + head0 * p.c.capacity + j;
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i)
+            if (i < p.group) x[i] = *reinterpret_cast<const float4 *>(scores + (size_t)i * p.c.capacity);
+        old = *reinterpret_cast<const float4 *>(p.weight + (size_t)bh * p.c.capacity + j);
+    };
+    int64_t j = (int64_t)blockIdx.y * kWeightTokens + 4 * threadIdx.x;
+    if (j < n) load(j);
+    wait_for_prior();
+    for (; j < n; j += (int64_t)gridDim.y * kWeightTokens) {
+        if (j >= (int64_t)gridDim.y * kWeightTokens) load(j);
         float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
-        for (int i = 0; i < p.group; ++i) {
+        auto add = [&](const float4 &x4, int i) {
             float lse = a.ws.lse2[head0 + i];
             if (lse == kNegInf) lse = INFINITY;  // a row without a token: no weight
-            const float4 x = *reinterpret_cast<const float4 *>(a.ws.scores + (head0 + i) * p.c.capacity + j);
-            sum = make_float4(sum.x + ex2(x.x - lse), sum.y + ex2(x.y - lse), sum.z + ex2(x.z - lse), sum.w + ex2(x.w - lse));
-        }
+            sum = make_float4(sum.x + ex2(x4.x - lse), sum.y + ex2(x4.y - lse), sum.z + ex2(x4.z - lse), sum.w + ex2(x4.w - lse));
+        };
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i)
+            if (i < p.group) add(x[i], i);
+#pragma unroll 4
+        for (int i = kAhead; i < p.group; ++i)
+            add(*reinterpret_cast<const float4 *>(a.ws.scores + (head0 + i) * p.c.capacity + j), i);
         float *const w = p.weight + (size_t)bh * p.c.capacity + j;
         if (j + 4 <= n) {
-            const float4 x = *reinterpret_cast<const float4 *>(w);
-            *reinterpret_cast<float4 *>(w) = make_float4(x.x + sum.x, x.y + sum.y, x.z + sum.z, x.w + sum.w);
+            *reinterpret_cast<float4 *>(w) = make_float4(old.x + sum.x, old.y + sum.y, old.z + sum.z, old.w + sum.w);
         } else {
-            const float s[4] = {sum.x, sum.y, sum.z, sum.w};
-            for (int e = 0; j + e < n; ++e) w[e] += s[e];
+            const float s[4] = {old.x + sum.x, old.y + sum.y, old.z + sum.z, old.w + sum.w};
+            for (int e = 0; j + e < n; ++e) w[e] = s[e];
         }
     }
 }
@@ -708,9 +700,9 @@ cudaError_t launch_attn_decode(const AttnDecodeArgs &p, cudaStream_t stream) {
     a.q_tiles = (p.group + kRows - 1) / kRows;
     workspace_layout(&a.ws, static_cast<char *>(p.ws), p.c.batch, p.num_q_heads, p.c.capacity, p.weight != nullptr,
                      (int64_t)sms * kWarps);
-    // tiles there can be, times the CTAs they are cut for, in 32 bits?
+    // do the tiles there can be, and the end of the last CTA's share, fit 32 bits?
     const int64_t most = (int64_t)p.c.batch * p.c.num_kv_heads * a.q_tiles * ((p.c.capacity + kTokens - 1) / kTokens);
-    const bool small = most < (int64_t)0xffffffffLL / (std::max(sms, kWarps) + 1);
+    const bool small = most < 0x7fffffffLL;
     cudaError_t e = small ? configure_once<uint32_t>() : configure_once<uint64_t>();
     if (e != cudaSuccess) return e;
     e = small ? launch_dependent(kda_attn_decode_kernel<uint32_t>, dim3((unsigned)sms), kThreads, kSmem, stream, a)
