@@ -573,9 +573,10 @@ __device__ __forceinline__ void add_parts(const Part *parts, const Cut &cut, int
     }
 }
 
-// Joins the cut items: CTA (i, row) those of the eight shares of the first kernel's CTA i, a warp for each. An
-// item of many parts (at most one begins to be cut in a CTA) is joined by all warps.
-constexpr int kManyParts = 16;
+// Joins the cut items: CTA (i, row) those of the eight shares of the first kernel's CTA i, a warp for each, or
+// all warps for an item of more parts than a CTA has shares (it reaches beyond the CTA, so there is one at most).
+// 8 x 8000 tokens: 12.0 us, with one warp for up to 64 parts 14.4; 1 x 100000 tokens: 18, with one warp 31.
+constexpr int kManyParts = kWarps;
 
 __global__ void __launch_bounds__(kThreads, 2) kda_attn_join_kernel(const Args a) {
     __shared__ float s_m[kWarps], s_l[kWarps];

@@ -182,9 +182,10 @@ __global__ void __launch_bounds__(kThreads) kda_evict_select_kernel(const CacheE
     for (int i = m + tid; i < n; i += kThreads) dst[i] = 0.0f;
 }
 
-// Threads of a row's CTA: a row of at most 4096 tokens is in the registers of 256, several CTAs on an SM.
-constexpr int kShortThreads = 256, kLongThreads = 1024;
-constexpr int kShortRow = kShortThreads * kElems * kHeld;
+// Threads of a row's CTA: short rows take 256, whose barriers cost less and of which several CTAs share an SM.
+// Whole call with 256 and 1024, in us: 8 row-heads of up to 600 tokens 6.0 and 6.9, of 1500 6.7 and 7.2, of
+// 4096 8.2 and 7.5; 296 of 600 15.0 and 17.5, of 4096 61.3 and 60.5.
+constexpr int kShortThreads = 256, kLongThreads = 1024, kShortRow = 2048;
 
 constexpr int kCopyWarps = 8;
 constexpr int kCopyThreads = kCopyWarps * 32;
@@ -339,9 +340,12 @@ cudaError_t launch_cache_evict(const CacheEvictArgs &a, cudaStream_t stream) {
         const int rows = (int)(std::max<int64_t>(per, 1) * tile);
         return launch_copy<16, false>(a, rows, (unsigned)(((int64_t)most + rows - 1) / rows), stream);
     }
-    if (ctas >= 4 * sms) return launch_copy<16, true>(a, most, 1, stream);
-    if (ctas >= 2 * sms) return launch_copy<8, true>(a, most, 1, stream);
-    return launch_copy<4, true>(a, most, 1, stream);
+    // The narrowest slices whose CTAs still run at once (two on an SM). Whole call for 2000 of 4096 tokens of 8,
+    // 64, 144 and 312 row-heads with slices of 64 / 128 / 256 bytes, in us: 12 / 15 / 22, 39 / 27 / 33,
+    // 80 / 60 / 55, 187 / 121 / 123.
+    if (4 * ctas <= 2 * sms) return launch_copy<4, true>(a, most, 1, stream);
+    if (2 * ctas <= 2 * sms) return launch_copy<8, true>(a, most, 1, stream);
+    return launch_copy<16, true>(a, most, 1, stream);
 }
 
 }  // namespace kda
