@@ -261,13 +261,13 @@ KDA_API int kda_decode_ex(const void *q, const void *k, const void *v, const voi
  *                clamped and recorded as KDA_ERR_DEVICE_INPUT).
  *   workspace    NULL: one thread block walks each (sequence, head) chain; otherwise at
  *                least kda_linear_prefill_workspace_size(..., 0) bytes, 16-byte aligned, or
- *                KDA_ERR_INVALID_ARG: chains too few to fill the GPU (or its last wave) are
- *                then cut into windows that run in parallel. Contents on entry do not
+ *                KDA_ERR_INVALID_ARG: chains too few to fill the GPU (or its last wave), and
+ *                long enough, are then cut into windows that run in parallel. Contents on entry do not
  *                matter; calls sharing one workspace must not overlap on the GPU. Results
  *                agree up to rounding.
  * Outputs are rounded once to BF16 from FP32 sums of products whose inner factors (the
  * decayed scores and the state the queries read) are BF16; the state itself is carried in
- * FP32 and its update keeps the decayed keys to 16 bits of mantissa.
+ * FP32 and its update takes the decayed values to 17 bits of mantissa.
  */
 KDA_API int kda_linear_prefill(const void *q, const void *k, const void *v, const float *log_decay,
                                int32_t decay_per_token, const int32_t *cu_seqlens,

@@ -20,6 +20,10 @@
 // the result independent of timing. With `weight`, the first kernel stores the scores (4 bytes a query
 // head beside the token's 512) and a third adds 2^(x - lse) to the weights.
 //
+// 64 rows of 4096 to 32768 tokens, 8 key heads: 758 us, 6.72 TB/s (0.99 of a copy's rate). 16 rows of 1600
+// tokens, 8 key heads: about 24 us, of which the stream is 16 and the rest start (3: lengths, places, first
+// tiles), join and the gaps between the launches. One row of 1000 tokens on 8 heads: 7.4 us, all latency.
+//
 // The order of the 128 channels inside a product is free, so the fragments are laid out for 16-byte
 // shared-memory reads: a lane's 16 bytes of a key row serve two k-steps, and of a value row eight column
 // tiles, which leaves a lane with 16 consecutive output channels. Two swizzles (keys: bit 2 of the

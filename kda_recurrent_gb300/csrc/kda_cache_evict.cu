@@ -6,16 +6,21 @@
 //  1. Selection, one CTA per (row, key head). Weights map to 32-bit keys whose unsigned order
 //     is the weights' order; a radix select finds the key T of the last candidate kept (digits of
 //     11, 11 and 10 bits from the top: a histogram of the candidates that share the prefix, then
-//     the digit where the count from above reaches what is needed). One ordered pass then
-//     writes the kept positions: a token's new position is the number kept before it,
-//     #(key > T) + min(#(key == T), ties kept) over the tokens before it, which one prefix
-//     sum of the two packed counts gives.
+//     the digit where the count from above reaches what is needed; a digit whose tokens all stay
+//     ends it). One ordered pass then writes the kept positions: a token's new position is the
+//     number kept before it, #(key > T) + min(#(key == T), ties kept) over the tokens before it,
+//     which one prefix sum of the two packed counts gives.
 //  2. The copy of the kept tokens' keys and values. In place a token moves to an equal or
 //     earlier position, so a CTA that owns a slice of columns and walks the tokens in order,
 //     reading a tile before it writes it, never overwrites a token still to be read: later
 //     tiles' sources lie beyond every position written so far. Slices of columns do not
 //     touch each other, which is what the CTAs of one head split by when few heads leave the
 //     GPU idle; between disjoint pages the tokens split too.
+//
+// Bound: the copy's HBM traffic for long rows (32 rows of 8192 to 16384 tokens, 8 heads, cut to 4096: 189 us,
+// 25 of them the selection; 5.8 TB/s over the whole, 0.86 of a copy's rate), latency for short ones (2 rows of
+// 1500 tokens, 8 heads, cut to 512: 7.2 us; the selection's chain is a row's length beside its weights, two or
+// three digits of four barriers each, and the ordered pass).
 #include <algorithm>
 
 #include "kda_dependent.cuh"
@@ -333,7 +338,8 @@ cudaError_t launch_cache_evict(const CacheEvictArgs &a, cudaStream_t stream) {
     const int most = std::min(a.budget, a.c.capacity);  // tokens a row can keep
     const int64_t ctas = (int64_t)a.c.batch * a.c.num_kv_heads * 2;
     if (a.dst_table != a.c.block_table) {
-        // one tile a CTA, or up to sixteen where that still leaves several CTAs for every SM
+        // one tile a CTA, or up to sixteen where that still leaves two waves of CTAs (105 row-heads cut to 1235
+        // tokens: 30 us, with four waves 33, with one 30; 256 cut to 4096: 189, 187, 189)
         const int tile = 2 * kCopyUnroll * kCopyWarps;
         const int64_t tiles = (most + tile - 1) / tile;
         const int64_t per = std::max<int64_t>((tiles + 65534) / 65535, std::min<int64_t>(16, ctas * tiles / (4 * sms)));
