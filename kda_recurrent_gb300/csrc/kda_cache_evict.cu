@@ -17,8 +17,8 @@
 //     touch each other, which is what the CTAs of one head split by when few heads leave the
 //     GPU idle; between disjoint pages the tokens split too.
 //
-// Bound: the copy's HBM traffic for long rows (32 rows of 8192 to 16384 tokens, 8 heads, cut to 4096: 189 us,
-// 25 of them the selection; 5.8 TB/s over the whole, 0.86 of a copy's rate), latency for short ones (2 rows of
+// Bound: the copy's HBM traffic for long rows (32 rows of 8192 to 16384 tokens, 8 heads, cut to 4096: 183 us,
+// 25 of them the selection; 5.98 TB/s over the whole, 0.88 of a copy's rate), latency for short ones (2 rows of
 // 1500 tokens, 8 heads, cut to 512: 7.2 us; the selection's chain is a row's length beside its weights, two or
 // three digits of four barriers each, and the ordered pass).
 #include <algorithm>
@@ -194,22 +194,98 @@ constexpr int kShortThreads = 256, kLongThreads = 1024, kShortRow = 2048;
 
 constexpr int kCopyWarps = 8;
 constexpr int kCopyThreads = kCopyWarps * 32;
-constexpr int kCopyStages = 3;
-constexpr int kCopyUnroll = 8;                             // 16-byte vectors a lane moves of a tile
-constexpr int kTileBytes = 32 * kCopyUnroll * 16;          // of a warp
+constexpr int kCopyUnroll = 8;                     // 16-byte vectors a lane moves of a tile
+constexpr int kTileBytes = 32 * kCopyUnroll * 16;  // of a warp
 
 struct Move {
-    int64_t src, dst;  // elements from the cache's base; dst < 0: nothing to do
+    const __nv_bfloat16 *src;
+    __nv_bfloat16 *dst;  // NULL: nothing to do
 };
 
-// kVecs: 16-byte vectors of a token's row that this CTA's slice holds (16, 8 or 4). A warp moves tiles of
-// kTokens tokens through its own ring: rows arrive by cp.async two tiles ahead, their moves (position ->
-// pages -> offsets, two dependent loads) are looked up one step further ahead, so that only the rows'
-// own latency is left and about 128 KiB are in flight on an SM. (Rows held in registers instead, eight
-// a thread: 4.1 TB/s read and written.) kOrdered: in place, a tile of the whole CTA is read before any
-// of it is written.
-template <int kVecs, bool kOrdered>
-__global__ void __launch_bounds__(kCopyThreads) kda_evict_copy_kernel(const CacheEvictArgs a, int rows_per_cta) {
+// Position j of a row moves to position i; `head`: the key head's place in a page, ps and pd the two pages.
+__device__ __forceinline__ Move move_of(const CacheEvictArgs &a, __nv_bfloat16 *head, int64_t stride, int b, int i, int j, int ps, int pd) {
+    const PagedCache &c = a.c;
+    const int mask = c.page_size - 1;
+    if (j < 0) return {nullptr, nullptr};
+    if (ps < 0 || ps >= c.num_pages || pd < 0 || pd >= c.num_pages) {
+        report_error(a.status, KDA_ERR_DEVICE_INPUT, b);
+        return {nullptr, nullptr};
+    }
+    if (ps == pd && ((i ^ j) & mask) == 0) return {nullptr, nullptr};  // it stays where it is
+    return {head + (int64_t)ps * stride + (int64_t)(j & mask) * kHeadDim, head + (int64_t)pd * stride + (int64_t)(i & mask) * kHeadDim};
+}
+
+// A warp's tile of a stage (its vectors, then its moves, kVecs vectors each): loads begun, and stored.
+template <int kVecs>
+__device__ __forceinline__ void fetch_tile(uint8_t *stage, int lane) {
+    const Move *const moves = reinterpret_cast<const Move *>(stage + kTileBytes);
+    const uint32_t to = smem_addr(stage) + lane * 16;
+#pragma unroll
+    for (int u = 0; u < kCopyUnroll; ++u) {
+        const Move mv = moves[u * (32 / kVecs) + lane / kVecs];
+        if (mv.dst) cp_async_16(to + u * 512, mv.src + lane % kVecs * 8, 16u);
+    }
+}
+
+template <int kVecs>
+__device__ __forceinline__ void store_tile(const uint8_t *stage, int lane) {
+    const Move *const moves = reinterpret_cast<const Move *>(stage + kTileBytes);
+#pragma unroll
+    for (int u = 0; u < kCopyUnroll; ++u) {
+        __nv_bfloat16 *const dst = moves[u * (32 / kVecs) + lane / kVecs].dst;
+        if (dst) *reinterpret_cast<uint4 *>(dst + lane % kVecs * 8) = *reinterpret_cast<const uint4 *>(stage + lane * 16 + u * 512);
+    }
+}
+
+// Between disjoint pages: a warp moves 16 kept tokens' keys or values, all loads (position -> pages -> rows, by
+// cp.async) before the stores; 48 warps an SM hide each other's latency, about 190 KiB in flight. 256 row-heads
+// cut to 4096 tokens of 8192 to 16384: 182 us with the selection; warps that walk up to 16 such tiles through a
+// ring of three: 187; the same by one wave of CTAs: 200.
+constexpr int kCopyTokens = 2 * kCopyUnroll;  // of a warp
+constexpr int kCopyStage = kTileBytes + kCopyTokens * (int)sizeof(Move);
+
+__global__ void __launch_bounds__(kCopyThreads) kda_evict_copy_kernel(const CacheEvictArgs a) {
+    extern __shared__ __align__(16) uint8_t smem[];
+    const PagedCache &c = a.c;
+    const int bh = blockIdx.x, b = bh / c.num_kv_heads, h = bh - b * c.num_kv_heads;
+    const bool values = blockIdx.y == 1;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    uint8_t *const stage = smem + warp * kCopyStage;
+    allow_next();
+    const int m = min(row_length(c, b, a.status, false), a.budget);  // (the same from the new lengths)
+    wait_for_prior();  // the selection is complete
+    if (blockIdx.y == 0 && blockIdx.z == 0 && h == 0 && threadIdx.x == 0) a.new_lens[b] = m;
+    const int64_t stride = values ? c.v_page_stride : c.k_page_stride;
+    __nv_bfloat16 *const head = (values ? c.v : c.k) + (size_t)h * c.page_size * kHeadDim;
+    const int32_t *const from = c.block_table + (size_t)b * c.max_pages, *const to = a.dst_table + (size_t)b * c.max_pages;
+    for (int64_t i0 = ((int64_t)blockIdx.z * kCopyWarps + warp) * kCopyTokens; i0 < m; i0 += (int64_t)gridDim.z * kCopyWarps * kCopyTokens) {
+        if (lane < kCopyTokens) {
+            const int i = (int)i0 + lane, j = i < m ? a.kept[(size_t)bh * a.budget + i] : -1;
+            int ps = 0, pd = 0;
+            if (j >= 0) ps = from[j >> c.page_shift], pd = to[i >> c.page_shift];
+            reinterpret_cast<Move *>(stage + kTileBytes)[lane] = move_of(a, head, stride, b, i, j, ps, pd);
+        }
+        __syncwarp();
+        fetch_tile<16>(stage, lane);
+        cp_async_commit();
+        cp_async_wait<0>();
+        __syncwarp();
+        store_tile<16>(stage, lane);
+        __syncwarp();
+    }
+}
+
+// In place. A CTA has a slice of kVecs 16-byte vectors of a (row, key head)'s keys or values, and walks its
+// tokens in order; a tile of the whole CTA is read before any of it is written. So few CTAs run at once: a warp
+// moves its part of a tile through its own ring, rows arriving two tiles ahead, their moves looked up one step
+// further ahead, so that only the rows' own latency is left and about 128 KiB are in flight on an SM.
+constexpr int kCopyStages = 3;
+
+template <int kVecs>
+constexpr int kPackSmem = kCopyWarps * kCopyStages * (kTileBytes + 32 * kCopyUnroll / kVecs * (int)sizeof(Move));
+
+template <int kVecs>
+__global__ void __launch_bounds__(kCopyThreads) kda_evict_pack_kernel(const CacheEvictArgs a) {
     constexpr int kSlices = 16 / kVecs;
     constexpr int kTokens = 32 * kCopyUnroll / kVecs;  // 16, 32 or 64
     constexpr int kEach = (kTokens + 31) / 32;         // tokens a lane looks up
@@ -223,61 +299,39 @@ __global__ void __launch_bounds__(kCopyThreads) kda_evict_copy_kernel(const Cach
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     allow_next();
     const int m = min(row_length(c, b, a.status, false), a.budget);  // (the same from the new lengths)
-    const int64_t begin = (int64_t)blockIdx.z * rows_per_cta;
-    const int end = (int)min((int64_t)m, begin + rows_per_cta);
     wait_for_prior();  // the selection is complete
-    if (blockIdx.y == 0 && blockIdx.z == 0 && h == 0 && threadIdx.x == 0) a.new_lens[b] = m;
-    if (begin >= end) return;
+    if (blockIdx.y == 0 && h == 0 && threadIdx.x == 0) a.new_lens[b] = m;
     const int64_t stride = values ? c.v_page_stride : c.k_page_stride;
-    const int mask = c.page_size - 1;
-    __nv_bfloat16 *const cache = (values ? c.v : c.k) + (size_t)h * c.page_size * kHeadDim + (slice * kVecs + lane % kVecs) * 8;
+    __nv_bfloat16 *const head = (values ? c.v : c.k) + (size_t)h * c.page_size * kHeadDim + slice * kVecs * 8;
     const int32_t *const kept = a.kept + (size_t)bh * a.budget;
-    const int32_t *const from = c.block_table + (size_t)b * c.max_pages, *const to = a.dst_table + (size_t)b * c.max_pages;
+    const int32_t *const table = c.block_table + (size_t)b * c.max_pages;
     uint8_t *const ring = smem + warp * (kCopyStages * kStageBytes);
-    const int tiles = (end - (int)begin + kStep - 1) / kStep;
-    const int mine = (int)begin + warp * kTokens;  // this warp's first token; + kStep a tile
+    const int tiles = (m + kStep - 1) / kStep;
 
     int j[kEach], jp[kEach], ps[kEach], pd[kEach];  // positions of one tile; of the tile before it, with pages
+    auto token = [&](int tile, int e) { return warp * kTokens + tile * kStep + lane + 32 * e; };
     auto positions = [&](int tile) {
 #pragma unroll
-        for (int e = 0; e < kEach; ++e) {
-            const int i = mine + tile * kStep + lane + 32 * e;
-            j[e] = tile < tiles && lane + 32 * e < kTokens && i < end ? kept[i] : -1;
-        }
+        for (int e = 0; e < kEach; ++e)
+            j[e] = tile < tiles && lane + 32 * e < kTokens && token(tile, e) < m ? kept[token(tile, e)] : -1;
     };
     auto pages = [&](int tile) {
 #pragma unroll
         for (int e = 0; e < kEach; ++e) {
-            const int i = mine + tile * kStep + lane + 32 * e;
             jp[e] = j[e];
-            if (j[e] >= 0) ps[e] = from[j[e] >> c.page_shift], pd[e] = to[i >> c.page_shift];
+            if (j[e] >= 0) ps[e] = table[j[e] >> c.page_shift], pd[e] = table[token(tile, e) >> c.page_shift];
         }
     };
     auto fetch = [&](int tile) {
         uint8_t *const stage = ring + (tile % kCopyStages) * kStageBytes;
-        Move *const moves = reinterpret_cast<Move *>(stage + kTileBytes);
         if (tile < tiles) {
 #pragma unroll
-            for (int e = 0; e < kEach; ++e) {
-                if (lane + 32 * e >= kTokens) continue;
-                const int i = mine + tile * kStep + lane + 32 * e;
-                Move mv = {0, -1};
-                if (jp[e] >= 0) {
-                    if (ps[e] < 0 || ps[e] >= c.num_pages || pd[e] < 0 || pd[e] >= c.num_pages)
-                        report_error(a.status, KDA_ERR_DEVICE_INPUT, b);
-                    else if (ps[e] != pd[e] || ((i ^ jp[e]) & mask) != 0)  // else it stays where it is
-                        mv = {(int64_t)ps[e] * stride + (int64_t)(jp[e] & mask) * kHeadDim,
-                              (int64_t)pd[e] * stride + (int64_t)(i & mask) * kHeadDim};
-                }
-                moves[lane + 32 * e] = mv;
-            }
+            for (int e = 0; e < kEach; ++e)
+                if (lane + 32 * e < kTokens)
+                    reinterpret_cast<Move *>(stage + kTileBytes)[lane + 32 * e] =
+                        move_of(a, head, stride, b, token(tile, e), jp[e], ps[e], pd[e]);
             __syncwarp();
-            const uint32_t dst = smem_addr(stage) + lane * 16;
-#pragma unroll
-            for (int u = 0; u < kCopyUnroll; ++u) {
-                const Move mv = moves[u * (32 / kVecs) + lane / kVecs];
-                if (mv.dst >= 0) cp_async_16(dst + u * 512, cache + mv.src, 16u);
-            }
+            fetch_tile<kVecs>(stage, lane);
         }
         cp_async_commit();
     };
@@ -295,34 +349,26 @@ __global__ void __launch_bounds__(kCopyThreads) kda_evict_copy_kernel(const Cach
         pages(tile + 3);
         positions(tile + 4);
         cp_async_wait<2>();
-        if (kOrdered) __syncthreads(); else __syncwarp();
-        const uint8_t *const stage = ring + (tile % kCopyStages) * kStageBytes;
-        const Move *const moves = reinterpret_cast<const Move *>(stage + kTileBytes);
-#pragma unroll
-        for (int u = 0; u < kCopyUnroll; ++u) {
-            const int64_t dst = moves[u * (32 / kVecs) + lane / kVecs].dst;
-            if (dst >= 0) *reinterpret_cast<uint4 *>(cache + dst) = *reinterpret_cast<const uint4 *>(stage + lane * 16 + u * 512);
-        }
-        __syncwarp();  // the stage is read before it is filled again
+        __syncthreads();
+        store_tile<kVecs>(ring + (tile % kCopyStages) * kStageBytes, lane);
+        __syncwarp();
     }
     cp_async_wait<0>();
 }
 
-template <int kVecs, bool kOrdered>
-cudaError_t launch_copy(const CacheEvictArgs &a, int rows_per_cta, unsigned parts, cudaStream_t stream) {
-    constexpr int kSmem = kCopyWarps * kCopyStages * (kTileBytes + 32 * kCopyUnroll / kVecs * (int)sizeof(Move));
+template <int kVecs>
+cudaError_t launch_pack(const CacheEvictArgs &a, cudaStream_t stream) {
     static bool configured[64] = {};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= 64 || !configured[dev]) {
-        e = cudaFuncSetAttribute(kda_evict_copy_kernel<kVecs, kOrdered>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+        e = cudaFuncSetAttribute(kda_evict_pack_kernel<kVecs>, cudaFuncAttributeMaxDynamicSharedMemorySize, kPackSmem<kVecs>);
         if (e != cudaSuccess) return e;
         if (dev >= 0 && dev < 64) configured[dev] = true;
     }
-    return launch_dependent(kda_evict_copy_kernel<kVecs, kOrdered>,
-                            dim3((unsigned)(a.c.batch * a.c.num_kv_heads), 2 * (16 / kVecs), parts), kCopyThreads, kSmem, stream, a,
-                            rows_per_cta);
+    const dim3 grid((unsigned)(a.c.batch * a.c.num_kv_heads), 2 * (16 / kVecs));
+    return launch_dependent(kda_evict_pack_kernel<kVecs>, grid, kCopyThreads, kPackSmem<kVecs>, stream, a);
 }
 
 }  // namespace
@@ -335,23 +381,20 @@ cudaError_t launch_cache_evict(const CacheEvictArgs &a, cudaStream_t stream) {
                               ? launch_dependent(kda_evict_select_kernel<kShortThreads>, rows_heads, kShortThreads, 0, stream, a)
                               : launch_dependent(kda_evict_select_kernel<kLongThreads>, rows_heads, kLongThreads, 0, stream, a);
     if (e != cudaSuccess) return e;
-    const int most = std::min(a.budget, a.c.capacity);  // tokens a row can keep
-    const int64_t ctas = (int64_t)a.c.batch * a.c.num_kv_heads * 2;
+    const int rows = a.c.batch * a.c.num_kv_heads;
     if (a.dst_table != a.c.block_table) {
-        // one tile a CTA, or up to sixteen where that still leaves two waves of CTAs (105 row-heads cut to 1235
-        // tokens: 30 us, with four waves 33, with one 30; 256 cut to 4096: 189, 187, 189)
-        const int tile = 2 * kCopyUnroll * kCopyWarps;
-        const int64_t tiles = (most + tile - 1) / tile;
-        const int64_t per = std::max<int64_t>((tiles + 65534) / 65535, std::min<int64_t>(16, ctas * tiles / (4 * sms)));
-        const int rows = (int)(std::max<int64_t>(per, 1) * tile);
-        return launch_copy<16, false>(a, rows, (unsigned)(((int64_t)most + rows - 1) / rows), stream);
+        const int parts = (std::min(a.budget, a.c.capacity) + kCopyWarps * kCopyTokens - 1) / (kCopyWarps * kCopyTokens);
+        constexpr int kSmem = kCopyWarps * kCopyStage;
+        static_assert(kSmem <= 48 * 1024, "no opt-in");
+        return launch_dependent(kda_evict_copy_kernel, dim3((unsigned)rows, 2, (unsigned)std::min(parts, 65535)), kCopyThreads, kSmem,
+                                stream, a);
     }
     // The narrowest slices whose CTAs still run at once (two on an SM). Whole call for 2000 of 4096 tokens of 8,
     // 64, 144 and 312 row-heads with slices of 64 / 128 / 256 bytes, in us: 12 / 15 / 22, 39 / 27 / 33,
     // 80 / 60 / 55, 187 / 121 / 123.
-    if (4 * ctas <= 2 * sms) return launch_copy<4, true>(a, most, 1, stream);
-    if (2 * ctas <= 2 * sms) return launch_copy<8, true>(a, most, 1, stream);
-    return launch_copy<16, true>(a, most, 1, stream);
+    if (4 * 2 * (int64_t)rows <= 2 * sms) return launch_pack<4>(a, stream);
+    if (2 * 2 * (int64_t)rows <= 2 * sms) return launch_pack<8>(a, stream);
+    return launch_pack<16>(a, stream);
 }
 
 }  // namespace kda
