@@ -3,7 +3,7 @@
 // For each (row, key head) longer than the budget, keep the first `sink` and last `recent`
 // tokens and the heaviest others (ties: the earlier), packed in order. Two kernels:
 //
-//  1. Selection, one CTA per (row, key head). Weights map to 32-bit keys whose unsigned order
+//  1. Selection, one CTA (or, for few long rows, a cluster) per (row, key head). Weights map to 32-bit keys whose unsigned order
 //     is the weights' order; a radix select finds the key T of the last candidate kept (digits of
 //     11, 11 and 10 bits from the top: a histogram of the candidates that share the prefix, then
 //     the digit where the count from above reaches what is needed; a digit whose tokens all stay
@@ -47,22 +47,39 @@ __device__ __forceinline__ float4 four_weights(const float *w, int j, int n) {
     return make_float4(j < n ? w[j] : 0.0f, j + 1 < n ? w[j + 1] : 0.0f, j + 2 < n ? w[j + 2] : 0.0f, 0.0f);
 }
 
-template <int kThreads>
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// The two words at `p` of this CTA's shared memory, in that of CTA `rank` of the cluster.
+__device__ __forceinline__ uint2 load_cluster(const uint32_t *p, int rank) {
+    uint32_t at;
+    uint2 x;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_addr(p)), "r"(rank));
+    asm volatile("ld.shared::cluster.v2.u32 {%0, %1}, [%2];" : "=r"(x.x), "=r"(x.y) : "r"(at));
+    return x;
+}
+
+// A row by a cluster of kParts CTAs, each with at most a block of its tokens, or by one.
+template <int kThreads, int kParts>
 __global__ void __launch_bounds__(kThreads) kda_evict_select_kernel(const CacheEvictArgs a) {
+    constexpr bool kSplit = kParts > 1;
     constexpr int kWarps = kThreads / 32, kTile = kThreads * kElems, kBlock = kHeld * kTile;
     constexpr int kOwn = kBins / kThreads;  // digits of a thread
     __shared__ __align__(16) uint32_t s_hist[kBins];
     __shared__ uint32_t s_pick[3], s_sum[kWarps], s_warp[2][kWarps];
+    __shared__ __align__(8) uint32_t s_total[2];
     wait_for_prior();
     allow_next();
-    const int bh = blockIdx.x, b = bh / a.c.num_kv_heads, h = bh - b * a.c.num_kv_heads;
+    const int bh = blockIdx.x / kParts, part = blockIdx.x % kParts;
+    const int b = bh / a.c.num_kv_heads, h = bh - b * a.c.num_kv_heads;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const float *const w = a.weight + (size_t)bh * a.c.capacity;  // dst may alias: plain loads
     float *const dst = a.dst_weight + (size_t)bh * a.c.capacity;
     int32_t *const kept = a.kept + (size_t)bh * a.budget;
     // A row of one block stays in registers for all passes; a longer one is read again by each, a block's loads
     // together. Where every row is of one block, it is loaded beside its length, up to the capacity.
-    const bool short_rows = a.c.capacity <= kBlock;
+    const bool short_rows = !kSplit && a.c.capacity <= kBlock;
     float4 held[kHeld];
     auto load_block = [&](int j0, int n) {
 #pragma unroll
@@ -71,15 +88,18 @@ __global__ void __launch_bounds__(kThreads) kda_evict_select_kernel(const CacheE
     if (short_rows) load_block(0, a.c.capacity);
     const int n = row_length(a.c, b, a.status, tid == 0 && h == 0);
     const int m = min(n, a.budget);
-    for (int64_t i = (int64_t)m + tid; i < a.budget; i += kThreads) kept[i] = -1;
+    const int every = kParts * kThreads, mine0 = part * kThreads + tid;
+    for (int64_t i = (int64_t)m + mine0; i < a.budget; i += every) kept[i] = -1;
     if (n <= a.budget) {
-        for (int i = tid; i < n; i += kThreads) {
+        for (int i = mine0; i < n; i += every) {
             kept[i] = i;
             dst[i] = w[i];
         }
         return;
     }
-    if (!short_rows) load_block(0, n);
+    const int per = kSplit ? ((n + kParts - 1) / kParts + 3) / 4 * 4 : n;
+    const int begin = kSplit ? min(part * per, n) : 0, end = kSplit ? min(begin + per, n) : n;  // this CTA's tokens
+    if (!short_rows) load_block(begin, end);
     const int lo = a.sink, hi = n - a.recent;  // candidates: [lo, hi), more than are needed
     uint32_t need = a.budget - a.sink - a.recent, prefix = 0;
     if (need > 0) {
@@ -94,20 +114,29 @@ __global__ void __launch_bounds__(kThreads) kda_evict_select_kernel(const CacheE
                 for (int e = 0; e < 4; ++e) {
                     const uint32_t key = weight_key(x[e]);
                     // (adding up equal digits of a warp first, by a match, took longer than their conflicts)
-                    if (j + e >= lo && j + e < hi && (key & above) == prefix) atomicAdd(&s_hist[(key >> shift) & (bins - 1)], 1u);
+                    if (j + e >= lo && j + e < min(hi, end) && (key & above) == prefix) atomicAdd(&s_hist[(key >> shift) & (bins - 1)], 1u);
                 }
             };
-            for (int j0 = 0; j0 < n; j0 += kBlock) {
-                if (n > kBlock) load_block(j0, n);
+            for (int j0 = begin; j0 < end; j0 += kBlock) {
+                if (!kSplit && n > kBlock) load_block(j0, n);
 #pragma unroll
                 for (int i = 0; i < kHeld; ++i)
-                    if (j0 + i * kTile + 128 * warp < n) count(held[i], j0 + i * kTile + 4 * tid);
+                    if (j0 + i * kTile + 128 * warp < end) count(held[i], j0 + i * kTile + 4 * tid);
             }
-            __syncthreads();
+            if (kSplit) cluster_sync(); else __syncthreads();
             // a thread owns kOwn digits; the one where the count from above reaches `need`
             uint32_t c[kOwn], own = 0;
 #pragma unroll
-            for (int i = 0; i < kOwn; ++i) own += c[i] = s_hist[kOwn * tid + i];
+            for (int i = 0; i < kOwn; i += 2) {
+                uint2 x[kParts];
+#pragma unroll
+                for (int r = 0; r < kParts; ++r)
+                    x[r] = kSplit ? load_cluster(&s_hist[kOwn * tid + i], r) : *reinterpret_cast<const uint2 *>(&s_hist[kOwn * tid + i]);
+                c[i] = c[i + 1] = 0;
+#pragma unroll
+                for (int r = 0; r < kParts; ++r) c[i] += x[r].x, c[i + 1] += x[r].y;
+                own += c[i] + c[i + 1];
+            }
             uint32_t from = own;  // over this thread's digits and the higher ones of its warp
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -124,7 +153,7 @@ __global__ void __launch_bounds__(kThreads) kda_evict_select_kernel(const CacheE
                     higher += c[i];
                 }
             }
-            __syncthreads();
+            if (kSplit) cluster_sync(); else __syncthreads();  // (the counts have been read)
             prefix |= s_pick[0] << shift;
             need = s_pick[1];
             if (need == s_pick[2]) {  // all with this prefix stay: no further digit decides
@@ -139,16 +168,42 @@ __global__ void __launch_bounds__(kThreads) kda_evict_select_kernel(const CacheE
     // prefix: the key T of the last candidate kept; need: how many tokens with that key stay
     uint32_t sure0 = 0, ties0 = 0;  // before this tile: tokens kept for certain, tokens with key T
     int odd = 0;
-    auto emit = [&](const float4 &x4, int j) {
+    auto flags = [&](const float4 &x4, int j, uint32_t (&flag)[kElems]) {
+        // ties << 16 | kept for certain (the sums stay below 2^16: a block has at most 2^14 tokens)
         const float x[4] = {x4.x, x4.y, x4.z, x4.w};
-        uint32_t mine = 0, flag[kElems];  // ties << 16 | kept for certain (a tile has at most 4096 tokens)
+        uint32_t sum = 0;
 #pragma unroll
         for (int e = 0; e < kElems; ++e) {
             const uint32_t key = weight_key(x[e]);
             const bool safe = j + e < lo || j + e >= hi;
-            flag[e] = j + e >= n ? 0u : (safe || key > prefix) ? 1u : key == prefix ? 1u << 16 : 0u;
-            mine += flag[e];
+            flag[e] = j + e >= end ? 0u : (safe || key > prefix) ? 1u : key == prefix ? 1u << 16 : 0u;
+            sum += flag[e];
         }
+        return sum;
+    };
+    if (kSplit) {  // those of the CTAs before (whose weights have been read by now, too)
+        uint32_t flag[kElems], sum = 0;
+#pragma unroll
+        for (int i = 0; i < kHeld; ++i) sum += flags(held[i], begin + i * kTile + 4 * tid, flag);
+        sum = __reduce_add_sync(0xffffffffu, sum);
+        if (lane == 0) s_sum[warp] = sum;
+        __syncthreads();
+        if (warp == 0) {
+            sum = __reduce_add_sync(0xffffffffu, lane < kWarps ? s_sum[lane] : 0u);
+            if (lane == 0) s_total[0] = sum;
+        }
+        cluster_sync();
+#pragma unroll
+        for (int r = 0; r < kParts; ++r) {
+            const uint32_t x = load_cluster(s_total, r).x;
+            sure0 += r < part ? x & 0xffffu : 0u;
+            ties0 += r < part ? x >> 16 : 0u;
+        }
+    }
+    auto emit = [&](const float4 &x4, int j) {
+        const float x[4] = {x4.x, x4.y, x4.z, x4.w};
+        uint32_t flag[kElems];
+        const uint32_t mine = flags(x4, j, flag);
         uint32_t sum = mine;  // inclusive over the warp
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -177,20 +232,26 @@ __global__ void __launch_bounds__(kThreads) kda_evict_select_kernel(const CacheE
         ties0 += total >> 16;
         odd ^= 1;
     };
-    for (int j0 = 0; j0 < n; j0 += kBlock) {
-        if (n > kBlock) load_block(j0, n);  // (in place: no token of this block has been overwritten yet)
+    for (int j0 = begin; j0 < end; j0 += kBlock) {
+        if (!kSplit && n > kBlock) load_block(j0, n);  // (in place: no token of this block has been overwritten yet)
 #pragma unroll
         for (int i = 0; i < kHeld; ++i)
-            if (j0 + i * kTile < n) emit(held[i], j0 + i * kTile + 4 * tid);
+            if (j0 + i * kTile < end) emit(held[i], j0 + i * kTile + 4 * tid);
     }
-    __syncthreads();  // (in place: every tile is done before its tail is cleared)
-    for (int i = m + tid; i < n; i += kThreads) dst[i] = 0.0f;
+    // (in place: every tile is done before its tail is cleared; a cluster's CTAs leave when the others have read
+    // their shared memory)
+    if (kSplit) cluster_sync(); else __syncthreads();
+    for (int i = m + mine0; i < n; i += every) dst[i] = 0.0f;
 }
 
 // Threads of a row's CTA: short rows take 256, whose barriers cost less and of which several CTAs share an SM.
 // Whole call with 256 and 1024, in us: 8 row-heads of up to 600 tokens 6.0 and 6.9, of 1500 6.7 and 7.2, of
 // 4096 8.2 and 7.5; 296 of 600 15.0 and 17.5, of 4096 61.3 and 60.5.
 constexpr int kShortThreads = 256, kLongThreads = 1024, kShortRow = 2048;
+// Few long rows are each split over a cluster, as long as its CTAs can hold the row. Whole call, cut to an eighth,
+// by one CTA and by eight, in us: 8 row-heads of 16384 tokens 15.6 and 20.3, of 32768 27.7 and 23.2, 2 of 131072
+// 88 and 30 (the eight exchange 64 KiB a digit and wait for one another eight times).
+constexpr int kSplitParts = 8, kSplitRow = 32768;
 
 constexpr int kCopyWarps = 8;
 constexpr int kCopyThreads = kCopyWarps * 32;
@@ -377,9 +438,13 @@ cudaError_t launch_cache_evict(const CacheEvictArgs &a, cudaStream_t stream) {
     int32_t sms = 0;
     if (sm_count_of_current_device(&sms) != KDA_OK) return cudaErrorInvalidDevice;
     const dim3 rows_heads((unsigned)(a.c.batch * a.c.num_kv_heads));
-    const cudaError_t e = a.c.capacity <= kShortRow
-                              ? launch_dependent(kda_evict_select_kernel<kShortThreads>, rows_heads, kShortThreads, 0, stream, a)
-                              : launch_dependent(kda_evict_select_kernel<kLongThreads>, rows_heads, kLongThreads, 0, stream, a);
+    const bool split = a.c.capacity >= kSplitRow && a.c.capacity <= kSplitParts * kLongThreads * kElems * kHeld &&
+                       (int64_t)rows_heads.x * kSplitParts <= sms;
+    const cudaError_t e =
+        split ? launch_clusters(kSplitParts, kda_evict_select_kernel<kLongThreads, kSplitParts>, dim3(rows_heads.x * kSplitParts),
+                                kLongThreads, 0, stream, a)
+        : a.c.capacity <= kShortRow ? launch_dependent(kda_evict_select_kernel<kShortThreads, 1>, rows_heads, kShortThreads, 0, stream, a)
+                                    : launch_dependent(kda_evict_select_kernel<kLongThreads, 1>, rows_heads, kLongThreads, 0, stream, a);
     if (e != cudaSuccess) return e;
     const int rows = a.c.batch * a.c.num_kv_heads;
     if (a.dst_table != a.c.block_table) {

@@ -279,6 +279,21 @@ def test_evict(lens, Hkv, page, budget, sink, recent, in_place):
 
 
 @pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("lens,Hkv,page,budget,sink,recent", [
+    ([40000], 2, 64, 9000, 16, 500), ([33000, 9, 70001], 1, 128, 20000, 3, 0), ([131072], 1, 256, 131071, 0, 1),
+    ([131100], 1, 32, 700, 4, 100), ([36000] * 20, 1, 256, 300, 0, 10)])
+def test_evict_long_rows(lens, Hkv, page, budget, sink, recent, in_place):
+    check_evict(lens, Hkv, page, budget, sink, recent, seed=67, in_place=in_place)
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+def test_evict_long_row_of_ties(in_place):
+    def weights(B, H, cap, gen):
+        return (torch.rand(B, H, cap, generator=gen) * 3).floor()
+    check_evict([50001], 2, 64, 30000, 5, 77, seed=68, in_place=in_place, weights=weights)
+
+
+@pytest.mark.parametrize("in_place", [False, True])
 def test_evict_many_heads(in_place):
     check_evict([200 + 10 * i for i in range(40)], 8, 16, 128, 4, 32, seed=62, in_place=in_place)
 
