@@ -31,7 +31,8 @@
 // them latency). Measured and dropped: half of it on warps 4-11 behind P (8% slower, it delays D) or
 // between P and O (10%, it waits for the next V); on two extra warps (1.5k cycles a quarter); on four (too
 // few registers for the state); half of D before Q S (9%, Q's tile, which the next V replaces, is then
-// freed late). In the state pass, which has no P and O, warps 4-11 do every other quarter.
+// freed late); the next chunk's first quarter split before this chunk's update, or its first two (6 and 13%,
+// the same V comes too late for that). In the state pass, which has no P and O, warps 4-11 do every other quarter.
 //
 // O leaves through shared memory because a thread's row-wise 32-byte stores (32 rows an instruction) kept
 // the load/store unit busy for 2k cycles a chunk, during which the MMAs' operand reads took four times
