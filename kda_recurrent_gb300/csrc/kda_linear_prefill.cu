@@ -118,6 +118,7 @@ struct Bars {
     uint64_t stored[2];  // and read by the stores
     uint64_t gate[2], gate_free[2];
     uint64_t item[2], item_free[2];  // work items handed to the roles
+    uint64_t state_read;             // an end state has left shared memory (8 warps)
     uint64_t next;                   // the answer to the request for another item
     uint64_t drain;
     uint4 answer;
@@ -488,6 +489,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&B->item[i], 1);
             mbar_init(&B->item_free[i], 1 + kStateWarps + kOutWarps + (kStates ? 0 : 1));
         }
+        mbar_init(&B->state_read, kStateWarps);
         mbar_init(&B->next, 1);
         mbar_init(&B->drain, 1);
         // the swizzled tiles are laid out for a 1024-byte-aligned base
@@ -845,7 +847,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint8_t *const s_row = smem + kS + half * kHalf + row * 128;
         int g = 0, u = 0, use = 0, tl = 0;  // chunks, updates, quarters and partial chunks so far
         float S[64];
-        bool ok = true;
+        int stored = 0;  // end states that have left shared memory
+        bool ok = true, storing = false;
         for (int k = 0; ok; ++k) {
             const Item it = next_item(k);
             if (it.nchunks < 0) break;
@@ -861,6 +864,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             } else {
 #pragma unroll
                 for (int i = 0; i < 64; ++i) S[i] = 0.0f;
+            }
+            if (storing) {  // the last item's end state, by all state warps
+                if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+                arrive_warp(&B->state_read);
+                ok = wait_warp(&B->state_read, stored & 1, B);
+                if (!ok) break;
+                ++stored;
+                storing = false;
             }
             for (int c = 0; c < it.nchunks; ++c, ++g) {
                 ok = false;
@@ -919,16 +930,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (it.nchunks == 0) ok = true;
             if (ok && it.end_row >= 0) {
-                wait_for_prior();  // an initial state in the same place has been read by the launches before
-                // 32 columns at a time through the warp's own 4 KiB of the S operand, once the last chunk's
-                // queries have read it (128-byte rows, swizzled), each by one TMA store
+                if (!kStates && !a.first) wait_for_prior();  // an initial state in the same place has been read by the launches before
+                // 32 columns at a time (128-byte rows, swizzled), each by one TMA store, through the warp's own 4 KiB
+                // of the S operand, once the last chunk's queries have read it, then of the split stages, which the
+                // last D has read; they are waited for when the next item writes there (1.6% at 16 ragged sequences
+                // of 32 heads). The state pass, which shares the split stages with warps 4-11, has one item.
                 if (!kStates && g > 0 && !wait_warp(&B->qs, (g - 1) & 1, B)) {
                     ok = false;
                     break;
                 }
-                uint8_t *const stage = smem + kS + (half * 4 + quad) * 4096;
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
+                    uint8_t *const stage = smem + (kStates || r == 0 ? kS : kSplit) + (half * 4 + quad) * 4096;
 #pragma unroll
                     for (int i = 0; i < 8; ++i)
                         *reinterpret_cast<float4 *>(stage + lane * 128 + ((i ^ (lane & 7)) << 4)) =
@@ -938,12 +951,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (lane == 0) {
                         tma_store(&map_s, smem_addr(stage), 64 * half + 32 * r, it.end_row + 32 * quad);
                         asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-                        asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+                        if (kStates) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
                     }
                     __syncwarp();
                 }
+                storing = !kStates;
             }
         }
+        if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
     }
     __syncwarp();
     if (lane == 0 && warp != kWarpAlloc && !(kStates && warp == kWarpStore)) atomicAdd(&B->finished, 1);
