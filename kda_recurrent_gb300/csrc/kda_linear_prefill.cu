@@ -121,10 +121,11 @@ struct Bars {
     uint64_t state_read;             // an end state has left shared memory (8 warps)
     uint64_t next;                   // the answer to the request for another item
     uint64_t drain;
+    uint64_t finished;  // all roles' warps are done
     uint4 answer;
     Item items[2];
     uint32_t tmem;
-    int32_t abort, progress, finished;  // progress: chunks issued; finished: roles' warps
+    int32_t abort, progress;  // progress: chunks issued
     uint8_t order[kRanked];  // sequences by length, longest first
 };
 
@@ -277,19 +278,29 @@ __device__ __forceinline__ bool wait_warp(uint64_t *bar, uint32_t parity, Bars *
     return ok;
 }
 
-// The watchdog: returns when all `roles` warps have finished, or after it has raised the abort flag.
-__device__ __forceinline__ void watch(Bars *B, int roles) {
-    const volatile int32_t *const abort = &B->abort, *const finished = &B->finished, *const progress = &B->progress;
+// The watchdog: returns when all roles' warps have finished, after raising the abort flag if the CTA made no
+// progress for kWaitLimitNs. (It sleeps on the barrier, not on a timer, because its return ends the CTA.)
+__device__ __forceinline__ void watch(Bars *B) {
+    volatile int32_t *const abort = &B->abort, *const progress = &B->progress;
+    const uint32_t addr = smem_addr(&B->finished);
     uint64_t since = global_ns();
     int32_t seen = 0;
-    while (*finished < roles && !*abort) {
-        __nanosleep(200);
-        const int32_t now = *progress + *finished;
+    for (;;) {
+        uint32_t done;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], 0, %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(done)
+            : "r"(addr), "r"(kSuspendHintNs)
+            : "memory");
+        if (done) return;
+        const int32_t now = *progress;
         if (now != seen) {
             seen = now;
             since = global_ns();
-        } else if (global_ns() - since > kWaitLimitNs) {
-            *const_cast<volatile int32_t *>(abort) = kTimedOut;
+        } else if (global_ns() - since > kWaitLimitNs && !*abort) {
+            *abort = kTimedOut;
         }
     }
 }
@@ -492,9 +503,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(&B->state_read, kStateWarps);
         mbar_init(&B->next, 1);
         mbar_init(&B->drain, 1);
+        mbar_init(&B->finished, (kStates ? 2 : 3) + kOutWarps + kStateWarps);
         // the swizzled tiles are laid out for a 1024-byte-aligned base
         B->abort = (smem_addr(smem) & 1023u) != 0 ? kMisplaced : 0;
-        B->progress = B->finished = 0;
+        B->progress = 0;
         if (B->abort) report_error(p.status, KDA_ERR_CUDA, 0);
         fence_mbar_init();
     }
@@ -741,7 +753,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
     } else if (warp == kWarpAlloc) {
-        watch(B, (kStates ? 2 : 3) + kOutWarps + kStateWarps);
+        watch(B);
     } else if (kStates && warp >= kWarpO && warp < kWarpS) {
         // the state pass has no outputs: these warps split the odd quarters
         const int tid = threadIdx.x - kWarpO * 32;
@@ -961,7 +973,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
     }
     __syncwarp();
-    if (lane == 0 && warp != kWarpAlloc && !(kStates && warp == kWarpStore)) atomicAdd(&B->finished, 1);
+    if (lane == 0 && warp != kWarpAlloc && !(kStates && warp == kWarpStore)) mbar_arrive(&B->finished);
     __syncthreads();
     if (B->abort) {  // wait (bounded) for what is still in flight before the memory is given back
         if (threadIdx.x == 0) {
@@ -975,7 +987,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     if (warp == kWarpAlloc) tmem_dealloc(B->tmem, kTmemCols);
     // whatever follows this grid on the stream also follows the launches that it may overlap
-    wait_for_prior();
+    if (!kStates && !a.first) wait_for_prior();
 }
 
 // S_{w+1} = exp2(g_w) S_w + D_w over the windows of a windowed chain, in place in its slots; one
