@@ -32,7 +32,8 @@
 // between P and O (10%, it waits for the next V); on two extra warps (1.5k cycles a quarter); on four (too
 // few registers for the state); half of D before Q S (9%, Q's tile, which the next V replaces, is then
 // freed late); the next chunk's first quarter split before this chunk's update, or its first two (6 and 13%,
-// the same V comes too late for that). In the state pass, which has no P and O, warps 4-11 do every other quarter.
+// the same V comes too late for that). In the state pass, which has no P and O, warps 4-11 do every other
+// quarter.
 //
 // O leaves through shared memory because a thread's row-wise 32-byte stores (32 rows an instruction) kept
 // the load/store unit busy for 2k cycles a chunk, during which the MMAs' operand reads took four times
@@ -44,8 +45,8 @@
 // -128 counts as -128 (both decay to zero in FP32), which keeps the sums finite.
 //
 // Bound: 1 KiB of HBM traffic a token and head against 164 KFLOP of BF16 products, so bandwidth where there
-// are chains for every SM: 8 x 16384 tokens x 96 heads take 2.17 ms, 5.99 TB/s (0.88 of a copy's rate), 16
-// sequences of 256 to 4096 tokens x 32 heads 167 us, 5.27 TB/s. A chain alone takes 2.9 us a chunk (its own
+// are chains for every SM: 8 x 16384 tokens x 96 heads take 2.16 ms, 6.0 TB/s (0.89 of a copy's rate), 16
+// sequences of 256 to 4096 tokens x 32 heads 165 us, 5.33 TB/s. A chain alone takes 2.9 us a chunk (its own
 // latency: split, D, the update, the operand of the next Q S), about what its share of the bandwidth allows
 // when all SMs run one.
 //
