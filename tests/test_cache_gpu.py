@@ -318,6 +318,63 @@ def test_evict_ties_and_special_weights(kind, in_place):
     check_evict([400, 90, 5000], 2, 16, 100, 3, 20, seed=63, weights=weights, in_place=in_place)
 
 
+def test_evict_in_place_by_slices():
+    # as many heads as the middle width of column slices takes
+    check_evict([260 + 7 * i for i in range(10)], 5, 16, 200, 4, 50, seed=69, in_place=True)
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+def test_evict_offsets_pass_32_bits(in_place):
+    pages, ps = 140000, 16  # 2.3e9 elements each
+    k = torch.empty(pages, 8, ps, 128, dtype=torch.bfloat16, device=DEV)
+    v = torch.empty_like(k)
+    at = torch.tensor([139999, 5, 133000], device=DEV)
+    to = at if in_place else torch.tensor([139000, 6, 132000], device=DEV)
+    gen = torch.Generator(device=DEV).manual_seed(70)
+    for x in (k, v):
+        x[at] = torch.randn(3, 8, ps, 128, generator=gen, device=DEV).to(torch.bfloat16)
+    before = [x[at].transpose(0, 1).reshape(8, 3 * ps, 128).clone() for x in (k, v)]
+    w = torch.rand(1, 8, 3 * ps, generator=gen, device=DEV)
+    lens = torch.tensor([45], dtype=torch.int32, device=DEV)
+    new_lens, kept = K.cache_evict(k, v, at[None].to(torch.int32), lens, w, budget=33, sink=1, recent=3,
+                                   dst_table=None if in_place else to[None].to(torch.int32))
+    assert new_lens.item() == 33
+    for x, old in zip((k, v), before):
+        got = x[to].transpose(0, 1).reshape(8, 3 * ps, 128)[:, :33]
+        assert torch.equal(got, old.gather(1, kept[0].long()[..., None].expand(8, 33, 128)))
+
+
+def test_calls_without_waits_equal_calls_with_waits():
+    """Launches overlap the work before them: every call here reads what the one before it writes."""
+    def run(wait):
+        c = R.cache_inputs([700, 300], 2, 16, seed=71, device=DEV)
+        cap = c["block_table"].shape[1] * 16
+        w, lens = torch.zeros(2, 2, cap, device=DEV), c["seq_lens"].clone()
+        pool = torch.zeros(2, 8, 128, 128, device=DEV)
+        slots, g = torch.arange(2, dtype=torch.int32, device=DEV), torch.full((8,), -0.1, device=DEV)
+        cu = torch.tensor([0, 1, 2], dtype=torch.int32, device=DEV)
+        x, seen = queries(2, 8, 71), []
+        ws = K.attn_decode_workspace(2, 8, 2, c["block_table"].shape[1], 16, True, DEV)
+        pause = torch.cuda.synchronize if wait else lambda: None
+        for step in range(12):
+            x = K.linear_decode(x, x, x, g, slots, pool, scale=0.3)
+            pause()
+            x = K.attn_decode(x, c["k_cache"], c["v_cache"], c["block_table"], lens, scale=SCALE, weight=w, workspace=ws)
+            pause()
+            x, state = K.linear_prefill(x, x, x, g, cu, pool, scale=0.3)
+            pause()
+            pool.copy_(state)
+            if step % 4 == 3:
+                lens, kept = K.cache_evict(c["k_cache"], c["v_cache"], c["block_table"], lens, w, budget=250 - 40 * (step // 4),
+                                           sink=2, recent=30)
+                pause()
+                seen.append(kept)
+            x = (x.float() / x.float().norm(dim=-1, keepdim=True)).to(torch.bfloat16)
+        return [x, pool, w, lens, c["k_cache"], c["v_cache"], *seen]
+    for a, b in zip(run(True), run(False)):
+        assert torch.equal(a.nan_to_num(), b.nan_to_num())
+
+
 def test_evict_new_lens_may_be_seq_lens():
     c = R.cache_inputs([100, 20], 2, 16, seed=64, device=DEV)
     w = torch.rand(2, 2, c["block_table"].shape[1] * 16, device=DEV)
