@@ -54,7 +54,9 @@
 // window's end state from zero (the update half of the kernel) and its total decay, an
 // elementwise pass chains the windows' start states, S_{w+1} = exp(g_w) S_w + D_w, and the chunk
 // kernel runs every window from its start state. The same is done for the chains of a short last
-// wave, whose windows are launched behind the whole chains.
+// wave, whose windows are launched behind the whole chains. Every window starts from a slot of the
+// workspace, the first one too (from a copy of the initial state): the chain's last window, on another CTA,
+// may store the end state over the initial one before the first window has begun.
 //
 // All waits are bounded; on expiry the CTA records KDA_ERR_DEVICE_TIMEOUT, waits for its own
 // copies and MMAs in flight, frees its tensor memory and returns.
@@ -99,7 +101,7 @@ struct Item {
     const float *start;  // state before it, or NULL for zeros
     float *total;        // where its total decay goes (state pass)
     int32_t h, bos, eos, nchunks, updates, last_rows;
-    int32_t carried;     // start was written by the launch before
+    int32_t carried;     // start is a slot, written by the launch before
     int32_t end_row;     // where its end state goes: row of the end states' tensor, or -1
 };
 
@@ -320,7 +322,7 @@ struct Plan {
 struct ChunkArgs {
     LinearPrefillArgs p;
     Plan plan;
-    float *slots;  // windowed chain lc, window w: the window's own end state, then the start of window w + 1
+    float *slots;  // windowed chain lc, window w: the end state of window w - 1 alone, then the start of window w
     float *decay;  // windowed chain lc, window w: its total decay (log2)
     int32_t take_over;  // whether a CTA takes over items of CTAs not launched yet: in a grid of one wave, it
                         // would only take those that are about to start on an idle SM
@@ -328,7 +330,7 @@ struct ChunkArgs {
 };
 
 __device__ __forceinline__ float *slot_of(const ChunkArgs &a, int lc, int w) {
-    return a.slots + ((size_t)lc * (a.plan.wins - 1) + w) * (kHeadDim * kHeadDim);
+    return a.slots + ((size_t)lc * a.plan.wins + w) * (kHeadDim * kHeadDim);
 }
 
 // order[r] = the sequence of rank r; holds CTA barriers. `scratch`: kRanked ints.
@@ -444,12 +446,12 @@ __device__ __forceinline__ Item item_of(const ChunkArgs &a, int i, const uint8_t
         if (!sp.live || sp.last) {
             it.nchunks = 0;
         } else {
-            it.end_row = (lc * (W - 1) + w) * kHeadDim;
+            it.end_row = (lc * W + w + 1) * kHeadDim;
             it.total = a.decay + (size_t)lc * W + w;
         }
     } else if (sp.live) {
-        it.carried = lc >= 0 && !sp.first;
-        it.start = it.carried ? slot_of(a, lc, w - 1) : p.init_state ? p.init_state + chain : nullptr;
+        it.carried = lc >= 0 && (!sp.first || p.init_state);
+        it.start = it.carried ? slot_of(a, lc, w) : p.init_state ? p.init_state + chain : nullptr;
         it.end_row = sp.last && p.final_state ? (n * H + h) * kHeadDim : -1;
     }
     // the last chunk's update is needed only where somebody reads the end state
@@ -943,7 +945,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (it.nchunks == 0) ok = true;
             if (ok && it.end_row >= 0) {
-                if (!kStates && !a.first) wait_for_prior();  // an initial state in the same place has been read by the launches before
+                if (!kStates && !a.first) wait_for_prior();  // an initial state in the same place has been copied by the launch before
                 // 32 columns at a time (128-byte rows, swizzled), each by one TMA store, through the warp's own 4 KiB
                 // of the S operand, once the last chunk's queries have read it, then of the split stages, which the
                 // last D has read; they are waited for when the next item writes there (1.6% at 16 ragged sequences
@@ -991,8 +993,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (!kStates && !a.first) wait_for_prior();
 }
 
-// S_{w+1} = exp2(g_w) S_w + D_w over the windows of a windowed chain, in place in its slots; one
-// float4 of the state a thread, the windows' own states loaded ahead.
+// S_{w+1} = exp2(g_w) S_w + D_w over the windows of a windowed chain, in place in its slots, from a copy of the
+// initial state in the first; one float4 of the state a thread, the windows' own states loaded ahead.
 constexpr int kScanThreads = 128;
 constexpr int kScanCtas = kHeadDim * kHeadDim / (4 * kScanThreads);
 
@@ -1009,6 +1011,7 @@ __global__ void __launch_bounds__(kScanThreads) kda_linear_scan_kernel(const Chu
     if (a.p.init_state)
         S = *reinterpret_cast<const float4 *>(a.p.init_state + ((size_t)n * a.p.num_heads + h) * (kHeadDim * kHeadDim) + off);
     wait_for_prior();
+    if (a.p.init_state) *reinterpret_cast<float4 *>(slot_of(a, lc, 0) + off) = S;
     constexpr int kAhead = 16;  // one round of loads for most plans (4: 7.4 us for 16 windows)
     for (int w0 = 0; w0 < W - 1; w0 += kAhead) {
         float4 d[kAhead];
@@ -1020,7 +1023,7 @@ __global__ void __launch_bounds__(kScanThreads) kda_linear_scan_kernel(const Chu
             const Span sp = span_of(a.p, n, w, W, false);
             on[i] = w < W - 1 && sp.live && !sp.last;
             if (on[i]) {
-                d[i] = *reinterpret_cast<const float4 *>(slot_of(a, lc, w) + off);
+                d[i] = *reinterpret_cast<const float4 *>(slot_of(a, lc, w + 1) + off);
                 g[i] = exp2f(a.decay[(size_t)lc * W + w]);
             }
         }
@@ -1028,7 +1031,7 @@ __global__ void __launch_bounds__(kScanThreads) kda_linear_scan_kernel(const Chu
         for (int i = 0; i < kAhead; ++i) {
             if (!on[i]) continue;
             S = make_float4(fmaf(S.x, g[i], d[i].x), fmaf(S.y, g[i], d[i].y), fmaf(S.z, g[i], d[i].z), fmaf(S.w, g[i], d[i].w));
-            *reinterpret_cast<float4 *>(slot_of(a, lc, w0 + i) + off) = S;
+            *reinterpret_cast<float4 *>(slot_of(a, lc, w0 + i + 1) + off) = S;
         }
     }
 }
@@ -1110,7 +1113,7 @@ Plan plan_linear(int32_t num_seqs, int32_t total_tokens, int32_t num_heads, int3
     return p;
 }
 
-int64_t slot_bytes(int64_t tail, int64_t wins) { return tail * (wins - 1) * (kHeadDim * kHeadDim * 4LL); }
+int64_t slot_bytes(int64_t tail, int64_t wins) { return tail * wins * (kHeadDim * kHeadDim * 4LL); }
 
 }  // namespace
 
@@ -1154,7 +1157,7 @@ cudaError_t launch_linear_prefill(const LinearPrefillArgs &args, cudaStream_t st
         a.decay = a.slots + slot_bytes(tail, a.plan.wins) / 4;
         e = configure_once<true>();
         if (e != cudaSuccess) return e;
-        e = state_map(&ms, a.slots, tail * (a.plan.wins - 1));
+        e = state_map(&ms, a.slots, tail * a.plan.wins);
         if (e != cudaSuccess) return e;
         e = launch_dependent(kda_linear_chunk_kernel<true>, (unsigned)(tail * (a.plan.wins - 1)), kThreads, kSmem, stream, a, mq, mk, mv, mo,
                    ms);

@@ -213,6 +213,22 @@ def test_prefill_long_windowed_last_wave():
     assert_state_close(fin[:, heads], ref_fin, tol=STATE_TOL)
 
 
+@pytest.mark.parametrize("lens,H", [([8192] * 5 + [300] * 15, 8), ([16384] + [2048] * 4, 32), ([1450], 154)])
+def test_prefill_windowed_last_wave_in_place(lens, H):
+    # A CTA takes its next item when it begins one: behind long chains a window's beginning may come long after
+    # the end of its chain's last window, which stores the end state where the initial one lay.
+    assert len(lens) * H - torch.cuda.get_device_properties(0).multi_processor_count in range(1, 51)
+    inp = R.linear_inputs(lens, H, seed=27, decay="head", device=DEV)
+    out, fin = run(inp, workspace=True)
+    ws = K.linear_prefill_workspace(len(lens), sum(lens), H, DEV)
+    assert ws is not None
+    for _ in range(4):
+        state, again = inp["init_state"].clone(), torch.empty_like(out)
+        K.kda_linear_prefill(inp["q"], inp["k"], inp["v"], inp["log_decay"], inp["cu_seqlens"], state, again, state,
+                             SCALE, workspace=ws)
+        assert torch.equal(again, out) and torch.equal(state, fin)
+
+
 def test_prefill_repeats_bit_for_bit():
     inp = R.linear_inputs([1500, 77], 3, seed=19, device=DEV)
     for ws in (False, True):
