@@ -590,10 +590,8 @@ __global__ void __launch_bounds__(kThreads, 4) kda_attn_join_kernel(const Args a
     __shared__ int s_many;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, row = blockIdx.y;
     if (threadIdx.x == 0) s_many = 0;
-    // (a launch for the weights starts only when the first kernel's scores are there, which it reads at once)
-    if (!a.p.weight) allow_next();
+    allow_next();
     wait_for_prior();
-    if (a.p.weight) allow_next();
     const Cut cut = a.ws.cuts[blockIdx.x * kWarps + warp];
     __syncthreads();
     if (cut.count > 0 && row < cut.rows) {
@@ -630,15 +628,15 @@ __global__ void __launch_bounds__(kThreads, 4) kda_attn_join_kernel(const Args a
     write_row(a, (size_t)s_cut.head + row, lane, m, l, o);
 }
 
-// weight[b][h][j] += sum over the query heads of key head h of 2^(x_j - lse), four tokens a thread. It starts
-// beside the join, whose sums it waits for with its first loads done.
+// weight[b][h][j] += sum over the query heads of key head h of 2^(x_j - lse), four tokens a thread.
 constexpr int kWeightThreads = 256, kWeightTokens = 4 * kWeightThreads;
 
 __global__ void __launch_bounds__(kWeightThreads) kda_attn_weight_kernel(const Args a) {
     const AttnDecodeArgs &p = a.p;
     const int bh = blockIdx.x, b = bh / p.c.num_kv_heads;
-    const int n = row_length(p.c, b, p.status, false);
     allow_next();
+    wait_for_prior();
+    const int n = row_length(p.c, b, p.status, false);
     const size_t head0 = (size_t)bh * p.group;
     constexpr int kAhead = 8;
     float4 x[kAhead], old;
@@ -649,11 +647,8 @@ __global__ void __launch_bounds__(kWeightThreads) kda_attn_weight_kernel(const A
             if (i < p.group) x[i] = *reinterpret_cast<const float4 *>(scores + (size_t)i * p.c.capacity);
         old = *reinterpret_cast<const float4 *>(p.weight + (size_t)bh * p.c.capacity + j);
     };
-    int64_t j = (int64_t)blockIdx.y * kWeightTokens + 4 * threadIdx.x;
-    if (j < n) load(j);
-    wait_for_prior();
-    for (; j < n; j += (int64_t)gridDim.y * kWeightTokens) {
-        if (j >= (int64_t)gridDim.y * kWeightTokens) load(j);
+    for (int64_t j = (int64_t)blockIdx.y * kWeightTokens + 4 * threadIdx.x; j < n; j += (int64_t)gridDim.y * kWeightTokens) {
+        load(j);
         float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         auto add = [&](const float4 &x4, int i) {
             float lse = a.ws.lse2[head0 + i];

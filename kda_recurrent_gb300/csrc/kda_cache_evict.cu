@@ -313,8 +313,8 @@ __global__ void __launch_bounds__(kCopyThreads) kda_evict_copy_kernel(const Cach
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     uint8_t *const stage = smem + warp * kCopyStage;
     allow_next();
-    const int m = min(row_length(c, b, a.status, false), a.budget);  // (the same from the new lengths)
     wait_for_prior();  // the selection is complete
+    const int m = min(row_length(c, b, a.status, false), a.budget);  // (the same from the new lengths)
     if (blockIdx.y == 0 && blockIdx.z == 0 && h == 0 && threadIdx.x == 0) a.new_lens[b] = m;
     const int64_t stride = values ? c.v_page_stride : c.k_page_stride;
     __nv_bfloat16 *const head = (values ? c.v : c.k) + (size_t)h * c.page_size * kHeadDim;
@@ -359,8 +359,8 @@ __global__ void __launch_bounds__(kCopyThreads) kda_evict_pack_kernel(const Cach
     const bool values = blockIdx.y >= kSlices;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     allow_next();
-    const int m = min(row_length(c, b, a.status, false), a.budget);  // (the same from the new lengths)
     wait_for_prior();  // the selection is complete
+    const int m = min(row_length(c, b, a.status, false), a.budget);  // (the same from the new lengths)
     if (blockIdx.y == 0 && h == 0 && threadIdx.x == 0) a.new_lens[b] = m;
     const int64_t stride = values ? c.v_page_stride : c.k_page_stride;
     __nv_bfloat16 *const head = (values ? c.v : c.k) + (size_t)h * c.page_size * kHeadDim + slice * kVecs * 8;

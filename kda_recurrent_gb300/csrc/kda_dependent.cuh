@@ -1,11 +1,10 @@
 // Launches that overlap the end of the launch before them on the stream (programmatic dependent launch).
 //
-// A kernel launched so may start while earlier work on its stream still runs. The first kernel of a call
-// therefore passes wait_for_prior in every thread before it touches global memory, and only then lets the
-// call's next kernel start by allow_next; that one may read the call's inputs at once, but what the call's
-// earlier kernels write only after a wait of its own, which every kernel passes before it ends (so that
-// waiting for the last kernel of a call is waiting for all). A launch's latency and its kernel's set-up so
-// lie behind the kernel before it.
+// A kernel launched so may start while earlier work on its stream still runs. Every thread therefore passes
+// wait_for_prior before it touches global memory, the call's inputs included: only that wait makes visible
+// what was written before, by the launch before directly and, since that one waited too, by all earlier
+// ones. allow_next lets the next launch start at any time, which then waits in the same way. A launch's
+// latency and its kernel's set-up so lie behind the kernel before it.
 #pragma once
 
 #include <cuda_runtime.h>

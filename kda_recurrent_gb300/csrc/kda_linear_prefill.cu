@@ -101,7 +101,6 @@ struct Item {
     const float *start;  // state before it, or NULL for zeros
     float *total;        // where its total decay goes (state pass)
     int32_t h, bos, eos, nchunks, updates, last_rows;
-    int32_t carried;     // start is a slot, written by the launch before
     int32_t end_row;     // where its end state goes: row of the end states' tensor, or -1
 };
 
@@ -326,7 +325,6 @@ struct ChunkArgs {
     float *decay;  // windowed chain lc, window w: its total decay (log2)
     int32_t take_over;  // whether a CTA takes over items of CTAs not launched yet: in a grid of one wave, it
                         // would only take those that are about to start on an idle SM
-    int32_t first;      // the call's first launch
 };
 
 __device__ __forceinline__ float *slot_of(const ChunkArgs &a, int lc, int w) {
@@ -440,7 +438,6 @@ __device__ __forceinline__ Item item_of(const ChunkArgs &a, int i, const uint8_t
     it.nchunks = (sp.eos - sp.bos + kC - 1) / kC;
     it.start = nullptr;
     it.end_row = -1;
-    it.carried = 0;
     it.total = nullptr;
     if (kStates) {
         if (!sp.live || sp.last) {
@@ -450,8 +447,8 @@ __device__ __forceinline__ Item item_of(const ChunkArgs &a, int i, const uint8_t
             it.total = a.decay + (size_t)lc * W + w;
         }
     } else if (sp.live) {
-        it.carried = lc >= 0 && (!sp.first || p.init_state);
-        it.start = it.carried ? slot_of(a, lc, w) : p.init_state ? p.init_state + chain : nullptr;
+        if (lc >= 0 && (!sp.first || p.init_state)) it.start = slot_of(a, lc, w);
+        else if (p.init_state) it.start = p.init_state + chain;
         it.end_row = sp.last && p.final_state ? (n * H + h) * kHeadDim : -1;
     }
     // the last chunk's update is needed only where somebody reads the end state
@@ -513,7 +510,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (B->abort) report_error(p.status, KDA_ERR_CUDA, 0);
         fence_mbar_init();
     }
-    if (kStates || a.first) wait_for_prior();
+    wait_for_prior();
     if (kStates) allow_next();
     rank_sequences(p, reinterpret_cast<int *>(smem), B->order);
     fence_async_smem();  // the ranking's scratch lies where the first tiles go
@@ -551,7 +548,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         it.nchunks = __shfl_sync(0xffffffffu, ok ? from.nchunks : -1, 0);
         it.updates = __shfl_sync(0xffffffffu, from.updates, 0);
         it.last_rows = __shfl_sync(0xffffffffu, from.last_rows, 0);
-        it.carried = __shfl_sync(0xffffffffu, from.carried, 0);
         it.end_row = __shfl_sync(0xffffffffu, from.end_row, 0);
         arrive_warp(&B->item_free[k & 1]);
         return it;
@@ -868,7 +864,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             const Item it = next_item(k);
             if (it.nchunks < 0) break;
             const size_t mine = (size_t)row * kHeadDim + 64 * half;
-            if (it.carried) wait_for_prior();  // the slots are written by the launch before
             if (it.start) {
                 const float4 *src = reinterpret_cast<const float4 *>(it.start + mine);
 #pragma unroll
@@ -945,7 +940,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (it.nchunks == 0) ok = true;
             if (ok && it.end_row >= 0) {
-                if (!kStates && !a.first) wait_for_prior();  // an initial state in the same place has been copied by the launch before
                 // 32 columns at a time (128-byte rows, swizzled), each by one TMA store, through the warp's own 4 KiB
                 // of the S operand, once the last chunk's queries have read it, then of the split stages, which the
                 // last D has read; they are waited for when the next item writes there (1.6% at 16 ragged sequences
@@ -989,8 +983,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     tc_fence_after();
     if (warp == kWarpAlloc) tmem_dealloc(B->tmem, kTmemCols);
-    // whatever follows this grid on the stream also follows the launches that it may overlap
-    if (!kStates && !a.first) wait_for_prior();
 }
 
 // S_{w+1} = exp2(g_w) S_w + D_w over the windows of a windowed chain, in place in its slots, from a copy of the
@@ -1003,14 +995,14 @@ __global__ void __launch_bounds__(kScanThreads) kda_linear_scan_kernel(const Chu
     __shared__ uint8_t order[kRanked];
     const int lc = blockIdx.x / kScanCtas, part = blockIdx.x - lc * kScanCtas;
     const int pos = a.plan.seq_chains + lc, h = pos % a.p.num_heads, W = a.plan.wins;
+    allow_next();
+    wait_for_prior();
     rank_sequences(a.p, scratch, order);
     const int n = a.p.num_seqs <= kRanked ? order[pos / a.p.num_heads] : pos / a.p.num_heads;
-    allow_next();
     const size_t off = ((size_t)part * kScanThreads + threadIdx.x) * 4;
     float4 S = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     if (a.p.init_state)
         S = *reinterpret_cast<const float4 *>(a.p.init_state + ((size_t)n * a.p.num_heads + h) * (kHeadDim * kHeadDim) + off);
-    wait_for_prior();
     if (a.p.init_state) *reinterpret_cast<float4 *>(slot_of(a, lc, 0) + off) = S;
     constexpr int kAhead = 16;  // one round of loads for most plans (4: 7.4 us for 16 windows)
     for (int w0 = 0; w0 < W - 1; w0 += kAhead) {
@@ -1138,7 +1130,6 @@ cudaError_t launch_linear_prefill(const LinearPrefillArgs &args, cudaStream_t st
     a.slots = nullptr;
     a.decay = nullptr;
     a.take_over = 0;
-    a.first = 1;
     int32_t sms = 0;
     if (sm_count_of_current_device(&sms) != KDA_OK) return cudaErrorInvalidDevice;
     if (args.ws) {
@@ -1167,7 +1158,6 @@ cudaError_t launch_linear_prefill(const LinearPrefillArgs &args, cudaStream_t st
     }
     const int64_t items = a.plan.seq_chains + tail * a.plan.wins;
     a.take_over = items > sms;
-    a.first = tail == 0;
     // (without a final state the map is not used)
     e = args.final_state ? state_map(&ms, args.final_state, chains) : state_map(&ms, args.q, 1);
     if (e != cudaSuccess) return e;

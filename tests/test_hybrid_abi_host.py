@@ -2,6 +2,8 @@
 library touches the device (the pointers are plain integers that are never dereferenced), or in the
 Python binding before the library is called."""
 import math
+import os
+import re
 
 import pytest
 import torch
@@ -119,6 +121,21 @@ def evict(lib, **over):
     (dict(nl=A + 2), MISALIGNED), (dict(kept=A + 2), MISALIGNED), (dict(dt=A + 2), MISALIGNED)])
 def test_cache_evict_arguments(lib, over, want):
     assert evict(lib, **over) == want
+
+
+@pytest.mark.parametrize("name", ["kda_linear_prefill", "kda_linear_decode", "kda_attn_decode", "kda_cache_evict"])
+def test_kernels_wait_for_the_launch_before_they_touch_memory(name):
+    """These kernels may start while the launch before them still runs. In each one's source the wait comes first:
+    unconditionally, and before anything that reads or writes global memory."""
+    text = open(os.path.join(kbuild.CSRC, name + ".cu")).read()
+    bodies = re.findall(r"__global__ void.*?\n(.*?)\n}\n", text, re.S)
+    assert len(bodies) == text.count("__global__ void") >= 1
+    for body in bodies:
+        before, wait, _ = body.partition("\n    wait_for_prior();")
+        assert wait and body.count("wait_for_prior") == 1
+        touches = [m for m in re.findall(r"\b(\w+)\(", before) if m in ("row_length", "load_block", "load", "__ldg", "__ldcs",
+                                                                       "rank_sequences", "item_of", "tma_load", "next_item")]
+        assert not touches, touches
 
 
 # ---------------------------------------------------------------- the binding's own checks

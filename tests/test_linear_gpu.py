@@ -229,6 +229,26 @@ def test_prefill_windowed_last_wave_in_place(lens, H):
         assert torch.equal(again, out) and torch.equal(state, fin)
 
 
+def test_prefill_windowed_calls_without_waits_equal_calls_with_waits():
+    """Launches overlap the work before them: each call here reads what the one before it writes."""
+    lens, H = [1400, 0, 1700], 2
+    inp = R.linear_inputs(lens, H, seed=28, decay="head", device=DEV)
+    ws = K.linear_prefill_workspace(len(lens), sum(lens), H, DEV)
+    assert ws is not None
+
+    def chain(wait):
+        a, b, state = inp["v"].clone(), torch.empty_like(inp["v"]), inp["init_state"].clone()
+        for step in range(20):
+            K.kda_linear_prefill(inp["q"], inp["k"], a, inp["log_decay"], inp["cu_seqlens"], state, b, state, 1.0,
+                                 workspace=ws)
+            if wait:
+                torch.cuda.synchronize()
+            a, b = b, a
+        return a, state
+    for x, y in zip(chain(True), chain(False)):
+        assert torch.isfinite(x).all() and torch.equal(x, y)
+
+
 def test_prefill_repeats_bit_for_bit():
     inp = R.linear_inputs([1500, 77], 3, seed=19, device=DEV)
     for ws in (False, True):
