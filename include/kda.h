@@ -317,7 +317,8 @@ KDA_API int kda_linear_decode(const void *q, const void *k, const void *v, const
  *   lse          FP32 [batch, num_q_heads] log(sum_j exp(x_j)), or NULL
  *   weight       FP32 [batch, num_kv_heads, max_pages * page_size], or NULL. weight[b][h][j]
  *                grows by p_j summed over the query heads that read key head h, for every
- *                unmasked token j; other entries are not written.
+ *                unmasked token j; other entries are not written. (x_j = -inf: p_j = 0,
+ *                also where another token makes the row NaN.)
  *   workspace    at least kda_attn_decode_workspace_size(...) bytes, 16-byte aligned.
  *                Contents on entry do not matter; calls sharing one must not overlap.
  * A row with no unmasked token (or whose every x_j is -inf) gives zeros, and -inf in lse. The

@@ -628,7 +628,9 @@ __global__ void __launch_bounds__(kThreads, 4) kda_attn_join_kernel(const Args a
     write_row(a, (size_t)s_cut.head + row, lane, m, l, o);
 }
 
-// weight[b][h][j] += sum over the query heads of key head h of 2^(x_j - lse), four tokens a thread.
+// weight[b][h][j] += sum over the query heads of key head h of 2^(x_j - lse), four tokens a thread. A score of
+// -inf has no weight whatever the lse (which a NaN key elsewhere in the row makes NaN). Tokens of a missing page
+// are not written: a page holds whole groups of four, so those are the groups that have no other score.
 constexpr int kWeightThreads = 256, kWeightTokens = 4 * kWeightThreads;
 
 __global__ void __launch_bounds__(kWeightThreads) kda_attn_weight_kernel(const Args a) {
@@ -650,10 +652,12 @@ __global__ void __launch_bounds__(kWeightThreads) kda_attn_weight_kernel(const A
     for (int64_t j = (int64_t)blockIdx.y * kWeightTokens + 4 * threadIdx.x; j < n; j += (int64_t)gridDim.y * kWeightTokens) {
         load(j);
         float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        bool any = false;
         auto add = [&](const float4 &x4, int i) {
-            float lse = a.ws.lse2[head0 + i];
-            if (lse == kNegInf) lse = INFINITY;  // a row without a token: no weight
-            sum = make_float4(sum.x + ex2(x4.x - lse), sum.y + ex2(x4.y - lse), sum.z + ex2(x4.z - lse), sum.w + ex2(x4.w - lse));
+            const float lse = a.ws.lse2[head0 + i];
+            auto weight = [&](float x) { return x == kNegInf ? 0.0f : ex2(x - lse); };
+            any |= x4.x != kNegInf || x4.y != kNegInf || x4.z != kNegInf || x4.w != kNegInf;
+            sum = make_float4(sum.x + weight(x4.x), sum.y + weight(x4.y), sum.z + weight(x4.z), sum.w + weight(x4.w));
         };
 #pragma unroll
         for (int i = 0; i < kAhead; ++i)
@@ -661,6 +665,7 @@ __global__ void __launch_bounds__(kWeightThreads) kda_attn_weight_kernel(const A
 #pragma unroll 4
         for (int i = kAhead; i < p.group; ++i)
             add(*reinterpret_cast<const float4 *>(a.ws.scores + (head0 + i) * p.c.capacity + j), i);
+        if (!any) continue;
         float *const w = p.weight + (size_t)bh * p.c.capacity + j;
         if (j + 4 <= n) {
             *reinterpret_cast<float4 *>(w) = make_float4(old.x + sum.x, old.y + sum.y, old.z + sum.z, old.w + sum.w);

@@ -152,6 +152,25 @@ def test_attn_nan_stays_in_its_row():
     assert torch.isnan(lse2[1, :2]).all() and torch.isnan(out2[1, :2]).all()
 
 
+@pytest.mark.parametrize("page", [8, 16])
+def test_attn_weights_of_missing_pages_are_not_written(page):
+    # ... whatever lies there, also in a row that a NaN key makes NaN
+    c = R.cache_inputs([100, 90, 40], 2, page, seed=57, device=DEV)
+    q, p = queries(3, 4, 57), c["block_table"]
+    p[0, 1], p[1, 0], p[2, :] = -1, -1, -1
+    c["k_cache"][p[1, 3].long(), 0, 3] = math.nan
+    for fill in (-0.0, math.nan, 0.5):
+        w = torch.full((3, 2, p.shape[1] * page), fill, device=DEV)
+        K.attn_decode(q, c["k_cache"], c["v_cache"], p, c["seq_lens"], scale=SCALE, weight=w)
+        masked = (p < 0).repeat_interleave(page, 1)
+        masked |= torch.arange(p.shape[1] * page, device=DEV) >= c["seq_lens"][:, None]
+        got = w.transpose(0, 1)[:, masked]
+        assert torch.equal(got.view(torch.int32), torch.full_like(got, fill).view(torch.int32))
+        if fill == 0.5:
+            assert torch.isnan(w[1, 0][~masked[1]]).all() and torch.isfinite(w[1, 1]).all()
+            assert (w[0][:, ~masked[0]] > 0.5).all()
+
+
 def test_attn_infinite_scores():
     # a key of -inf scores takes no weight; a row of them gives zeros
     c = R.cache_inputs([40, 20], 1, 16, seed=49, device=DEV)
