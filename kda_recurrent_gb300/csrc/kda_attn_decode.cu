@@ -12,7 +12,8 @@
 // are m16n8k16 BF16 tensor-core instructions whose 16 rows are the query heads. (Tensor memory and
 // tcgen05 would need 64 or 128 rows; the rows here are 1 to 16, and the tensor work is a few
 // percent of the time.) The probabilities are split into two BF16 terms for P V, which costs
-// nothing here and leaves the output's own rounding as the only one.
+// nothing here and leaves the output's own rounding as the only one. A value that is not finite meets only
+// the first term (the second may be zero or negative, and would make an infinite channel NaN).
 //
 // An item inside one share is finished by its warp. An item cut between shares leaves (m, l, o) of each
 // part in the workspace; a CTA whose whole share lies in one item joins its warps' parts first, so that
@@ -166,11 +167,21 @@ __device__ __forceinline__ Cut cut_of(U x0, U x1, U total, U per) {
     return c;
 }
 
+// Whether one of two BF16 numbers is an infinity or NaN; those numbers as zeros; the larger magnitude (NaN if any
+// is), number by number.
+__device__ __forceinline__ uint32_t not_finite(uint32_t x) { return ((x & 0x7fff7fffu) + 0x00800080u) & 0x80008000u; }
+__device__ __forceinline__ uint32_t only_finite(uint32_t x) { return x & ~((not_finite(x) >> 15) * 0xffffu); }
+__device__ __forceinline__ uint32_t max_abs(uint32_t x, uint32_t y) {
+    uint32_t z;
+    asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(z) : "r"(x), "r"(y));
+    return z;
+}
+
 // A finished row by one warp: lane's four channels of o over the sum l, at maximum m.
 __device__ __forceinline__ void write_row(const Args &a, size_t head, int lane, float m, float l, const float4 &o) {
-    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    const float inv = 1.0f / l;  // (l = 0: zeros, whatever the values)
     reinterpret_cast<uint2 *>(a.p.out + head * kHeadDim)[lane] =
-        make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
+        l == 0.0f ? make_uint2(0, 0) : make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
     if (lane == 0) {
         const float v = l == 0.0f ? kNegInf : (m == kNegInf ? 0.0f : m) + log2f(l);
         if (a.p.lse) a.p.lse[head] = v * kLn2;
@@ -432,15 +443,24 @@ __global__ void __launch_bounds__(kThreads, 1) kda_attn_decode_kernel(const Args
                     const int r = 2 * t + (i2 & 1) + 8 * (i2 >> 1);
                     v[i2] = *reinterpret_cast<const uint4 *>(vs + r * 256 + (((g + 8 * half) ^ (((r >> 1) & 3) << 1)) << 4));
                 }
-                const uint32_t *const v0 = &v[0].x, *const v1 = &v[1].x, *const v2 = &v[2].x, *const v3 = &v[3].x;
+                uint32_t *const v0 = &v[0].x, *const v1 = &v[1].x, *const v2 = &v[2].x, *const v3 = &v[3].x;
+                auto add = [&](const uint32_t (&p)[4], int w) {
+                    mma_bf16_16816(o[8 * half + 2 * w], p, __byte_perm(v0[w], v1[w], 0x5410), __byte_perm(v2[w], v3[w], 0x5410));
+                    mma_bf16_16816(o[8 * half + 2 * w + 1], p, __byte_perm(v0[w], v1[w], 0x7632), __byte_perm(v2[w], v3[w], 0x7632));
+                };
+                uint32_t top = 0;
 #pragma unroll
-                for (int w = 0; w < 4; ++w) {
-                    const uint32_t b00 = __byte_perm(v0[w], v1[w], 0x5410), b01 = __byte_perm(v2[w], v3[w], 0x5410);
-                    const uint32_t b10 = __byte_perm(v0[w], v1[w], 0x7632), b11 = __byte_perm(v2[w], v3[w], 0x7632);
-                    mma_bf16_16816(o[8 * half + 2 * w], hi, b00, b01);
-                    mma_bf16_16816(o[8 * half + 2 * w + 1], hi, b10, b11);
-                    mma_bf16_16816(o[8 * half + 2 * w], lo, b00, b01);
-                    mma_bf16_16816(o[8 * half + 2 * w + 1], lo, b10, b11);
+                for (int w = 0; w < 4; ++w) top = max_abs(max_abs(max_abs(v0[w], v1[w]), max_abs(v2[w], v3[w])), top);
+                if (!__any_sync(0xffffffffu, not_finite(top) != 0)) {
+#pragma unroll
+                    for (int w = 0; w < 4; ++w) add(hi, w), add(lo, w);
+                } else {
+#pragma unroll
+                    for (int w = 0; w < 4; ++w) {
+                        add(hi, w);
+                        v0[w] = only_finite(v0[w]), v1[w] = only_finite(v1[w]), v2[w] = only_finite(v2[w]), v3[w] = only_finite(v3[w]);
+                        add(lo, w);
+                    }
                 }
             }
             __syncwarp();  // the stage is read before a later fetch overwrites it
@@ -477,7 +497,7 @@ __global__ void __launch_bounds__(kThreads, 1) kda_attn_decode_kernel(const Args
             const int row = g + 8 * r;
             if (row >= rows) continue;
             if (whole) {
-                const float inv = l[r] == 0.0f ? 0.0f : 1.0f / l[r];
+                const float inv = 1.0f / l[r];
                 const float v = l[r] == 0.0f ? kNegInf : m[r] + log2f(l[r]);
                 if (t == 0) {
                     if (p.lse) p.lse[head0 + row] = v * kLn2;
@@ -491,7 +511,7 @@ __global__ void __launch_bounds__(kThreads, 1) kda_attn_decode_kernel(const Args
                         uint32_t w[4];
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
-                            w[i] = pack_bf16(o[8 * half + 2 * i][2 * r + e] * inv, o[8 * half + 2 * i + 1][2 * r + e] * inv);
+                            w[i] = l[r] == 0.0f ? 0 : pack_bf16(o[8 * half + 2 * i][2 * r + e] * inv, o[8 * half + 2 * i + 1][2 * r + e] * inv);
                         dst[e] = make_uint4(w[0], w[1], w[2], w[3]);
                     }
                 }

@@ -187,6 +187,38 @@ def test_attn_infinite_scores():
     assert (out[1] == 0).all() and lse[1, 0].item() == -math.inf
 
 
+@pytest.mark.parametrize("lens,Hq,Hkv", [([1, 40, 100], 4, 2), ([5000, 17], 2, 1), ([700] * 40, 8, 4), ([60000], 20, 1)])
+def test_attn_infinite_values(lens, Hq, Hkv):
+    # an infinite value makes its channel infinite, opposite ones or a NaN make it NaN; the others keep their bits
+    c = R.cache_inputs(lens, Hkv, 16, seed=58, device=DEV)
+    q, p = queries(len(lens), Hq, 58), c["block_table"].cpu()
+    clean, lse, _ = check(q, c, weight=False)
+    rows = torch.arange(len(lens))
+    first, last = p[:, 0].long(), p[rows, torch.tensor([(n - 1) // 16 for n in lens])].long()
+    at = torch.tensor([(n - 1) % 16 for n in lens])
+    v = c["v_cache"]
+    v[first, :, 0, 3] = math.inf
+    v[last, :, at, 126] = -math.inf
+    v[last, :, at, 64] = math.nan
+    v[first, :, 0, 9], v[last, :, at, 9] = math.inf, -math.inf
+    out, lse2 = K.attn_decode(q, c["k_cache"], v, c["block_table"], c["seq_lens"], scale=SCALE, want_lse=True)
+    ref, _, _ = R.attn_decode(q, c, SCALE)
+    odd = [3, 9, 64, 126]
+    assert torch.equal(out[..., odd].cpu().double().nan_to_num(nan=7.0), ref[..., odd].nan_to_num(nan=7.0))
+    assert not torch.isfinite(ref[..., odd]).any()
+    keep = [i for i in range(128) if i not in odd]
+    assert torch.equal(out[..., keep], clean[..., keep]) and torch.equal(lse2, lse)
+
+
+def test_attn_no_score_above_minus_infinity_gives_zeros():
+    c = R.cache_inputs([20, 5000], 1, 16, seed=59, device=DEV)
+    q = queries(2, 1, 59).abs() + 0.5
+    c["k_cache"][...] = -math.inf
+    c["v_cache"][:, :, 3] = math.inf
+    out, lse = K.attn_decode(q, c["k_cache"], c["v_cache"], c["block_table"], c["seq_lens"], scale=SCALE, want_lse=True)
+    assert (out == 0).all() and (lse == -math.inf).all()
+
+
 def test_attn_repeats_bit_for_bit():
     c = R.cache_inputs([3000, 17, 900], 2, 16, seed=50, device=DEV)
     q = queries(3, 8, 50)
