@@ -268,6 +268,10 @@ KDA_API int kda_decode_ex(const void *q, const void *k, const void *v, const voi
  * Outputs are rounded once to BF16 from FP32 sums of products whose inner factors (the
  * decayed scores and the state the queries read) are BF16; the state itself is carried in
  * FP32 and its update takes the decayed values to 17 bits of mantissa.
+ * A NaN or infinity in v reaches its channel's outputs from its token on and its column of the
+ * state, one in q, k or log_decay the outputs from its token on that the recurrence takes it to;
+ * nothing earlier and no other sequence or head. Where the recurrence gives an infinity these may
+ * be NaN; in the state they are for an infinity in k, or one that a decay of zero meets.
  */
 KDA_API int kda_linear_prefill(const void *q, const void *k, const void *v, const float *log_decay,
                                int32_t decay_per_token, const int32_t *cu_seqlens,

@@ -167,9 +167,7 @@ __device__ __forceinline__ Cut cut_of(U x0, U x1, U total, U per) {
     return c;
 }
 
-// Whether one of two BF16 numbers is an infinity or NaN; those numbers as zeros; the larger magnitude (NaN if any
-// is), number by number.
-__device__ __forceinline__ uint32_t not_finite(uint32_t x) { return ((x & 0x7fff7fffu) + 0x00800080u) & 0x80008000u; }
+// Two BF16 numbers: those that are not finite as zeros; the larger magnitude of each (NaN if either is one).
 __device__ __forceinline__ uint32_t only_finite(uint32_t x) { return x & ~((not_finite(x) >> 15) * 0xffffu); }
 __device__ __forceinline__ uint32_t max_abs(uint32_t x, uint32_t y) {
     uint32_t z;

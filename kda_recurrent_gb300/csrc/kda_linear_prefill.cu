@@ -58,6 +58,13 @@
 // workspace, the first one too (from a copy of the initial state): the chain's last window, on another CTA,
 // may store the end state over the initial one before the first window has begun.
 //
+// A value that is not finite belongs to its channel's outputs from its token on, but P V carries it to the chunk's
+// earlier tokens too (0 inf = NaN). The output warps add 0 times each element of P V to a sum, which is NaN then;
+// in that rare case they form the outputs of those tokens again, by single products. At 8 x 16384 x 96 heads this
+// takes 1.2%, the saturating conversion in the split 0.6% (looking through the values instead: 6% from the split,
+// which is the chunk's critical path, 7% from the output warps, as the chunks are short of shared-memory
+// bandwidth).
+//
 // All waits are bounded; on expiry the CTA records KDA_ERR_DEVICE_TIMEOUT, waits for its own
 // copies and MMAs in flight, frees its tensor memory and returns.
 #include <cuda.h>
@@ -382,7 +389,8 @@ __device__ __forceinline__ Span span_of(const LinearPrefillArgs &a, int n, int w
 
 // hi and lo of 32 tokens of V by the state warps: a row of the quarter at `tile` (eight threads a row, a
 // thread the same 16 bytes of both halves) times its factor f, rows past the last token as zeros, into
-// the split stage at `to`.
+// the split stage at `to`. hi saturates: an infinity becomes the largest number and an infinity, whose products
+// with a key have one sign.
 __device__ __forceinline__ void split_quarter(const uint8_t *tile, uint8_t *to, float f, bool live) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -393,11 +401,69 @@ __device__ __forceinline__ void split_quarter(const uint8_t *tile, uint8_t *to, 
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             const float y0 = __uint_as_float(u[e] << 16) * f, y1 = __uint_as_float(u[e] & 0xffff0000u) * f;
-            hi[e] = pack_bf16(y0, y1);
+            hi[e] = pack_bf16_finite(y0, y1);
             rest[e] = pack_bf16(y0 - __uint_as_float(hi[e] << 16), y1 - __uint_as_float(hi[e] & 0xffff0000u));
         }
         *reinterpret_cast<uint4 *>(to + i * kSplitHalf) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
         *reinterpret_cast<uint4 *>(to + kSplitLo + i * kSplitHalf) = make_uint4(rest[0], rest[1], rest[2], rest[3]);
+    }
+}
+
+__device__ __forceinline__ float dot2(uint32_t x, uint32_t y, float sum) {  // of two BF16 pairs
+    sum = fmaf(__uint_as_float(x & 0xffff0000u), __uint_as_float(y & 0xffff0000u), sum);
+    return fmaf(__uint_as_float(x << 16), __uint_as_float(y << 16), sum);
+}
+
+// lam * (Q S) + scale * sum_{j <= row} P_ij v_j again, token by token in FP32, for the channels of a row's 64 that a
+// value which is not finite reached from a later token of its chunk only (0.06 to 3.3 ms a chunk). `out` holds the row's outputs, its 16-byte
+// groups swizzled by `swizzle`; Q S is at `qs` in tensor memory. Called by whole warps; `live`: the row is a token.
+__device__ __noinline__ void repair_row(const LinearPrefillArgs &p, int h, int t0, int row, int rows, int half, bool live, float lam,
+                                        uint32_t qs, uint4 *out, int swizzle) {
+    const size_t stride = (size_t)p.num_heads * kHeadDim, first = (size_t)t0 * stride + (size_t)h * kHeadDim;
+    const __nv_bfloat16 *const v = p.v + first + 64 * half, *const k = p.k + first, *const q = p.q + first + row * stride;
+#pragma unroll 1
+    for (int i = 0; i < 8; ++i) {
+        __syncwarp();
+        float x[16];
+        tmem_ld16(qs + 16 * (i >> 1), x);
+        tmem_wait_ld();
+        uint32_t own[4] = {}, later[4] = {};  // two channels each
+#pragma unroll 8
+        for (int j = 0; j < rows; ++j) {
+            const uint4 w = *reinterpret_cast<const uint4 *>(v + j * stride + 8 * i);
+            const uint32_t u[4] = {not_finite(w.x), not_finite(w.y), not_finite(w.z), not_finite(w.w)};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) (j <= row ? own[e] : later[e]) |= u[e];
+        }
+        uint32_t any = 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) any |= later[e] &= ~own[e];
+        if (!live || any == 0) continue;
+        float sum[8] = {}, decay = 0.0f;
+#pragma unroll 1
+        for (int j = row; j >= 0; --j) {
+            float s = 0.0f;
+#pragma unroll 4
+            for (int d = 0; d < kHeadDim; d += 8) {
+                const uint4 a = *reinterpret_cast<const uint4 *>(q + d), b = *reinterpret_cast<const uint4 *>(k + j * stride + d);
+                s = dot2(a.x, b.x, dot2(a.y, b.y, dot2(a.z, b.z, dot2(a.w, b.w, s))));
+            }
+            s *= ex2(decay);
+#pragma unroll
+            for (int c = 0; c < 8; ++c) sum[c] = fmaf(s, __bfloat162float(v[j * stride + 8 * i + c]), sum[c]);
+            const float g = p.log_decay[(size_t)(t0 + j) * p.decay_token_stride + h];
+            decay += (g < kMinLogDecay ? kMinLogDecay : g) * kLog2e;
+        }
+        uint4 *const at = out + (i ^ swizzle);
+        const uint4 w = *at;
+        uint32_t y[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float x0 = i & 1 ? x[8 + 2 * e] : x[2 * e], x1 = i & 1 ? x[9 + 2 * e] : x[2 * e + 1];
+            const uint32_t mask = (later[e] >> 15) * 0xffffu;
+            y[e] = (y[e] & ~mask) | (pack_bf16(fmaf(lam, x0, p.scale * sum[2 * e]), fmaf(lam, x1, p.scale * sum[2 * e + 1])) & mask);
+        }
+        *at = make_uint4(y[0], y[1], y[2], y[3]);
     }
 }
 
@@ -824,12 +890,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const bool whole = c + 1 < it.nchunks || 32 * quad + 32 <= it.last_rows;
                 uint8_t *const rows = smem + (iv % kRing) * kTile + half * kHalf + quad * 4096;
                 uint4 *const dst = reinterpret_cast<uint4 *>(p.out + ((size_t)t * H + it.h) * kHeadDim + 64 * half);
+                float finite[4] = {};
 #pragma unroll
                 for (int b = 0; b < 4; ++b) {
                     float o[16], x[16];
                     tmem_ld16(lanes + kColO + 64 * half + 16 * b, o);
                     tmem_ld16(lanes + kColQS + 64 * half + 16 * b, x);
                     tmem_wait_ld();
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) finite[j & 3] = fmaf(o[j], 0.0f, finite[j & 3]);
                     uint32_t pk[8];
 #pragma unroll
                     for (int j = 0; j < 8; ++j)
@@ -843,6 +912,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                             dst[2 * b + i] = y;
                     }
                 }
+                if (__any_sync(0xffffffffu, (finite[0] + finite[1]) + (finite[2] + finite[3]) != 0.0f && t < it.eos))
+                    repair_row(p, it.h, it.bos + c * kC, row, c + 1 < it.nchunks ? kC : it.last_rows, half, t < it.eos, lam,
+                               lanes + kColQS + 64 * half, whole ? reinterpret_cast<uint4 *>(rows + lane * 128) : dst, whole ? lane & 7 : 0);
                 tc_fence_before();
                 fence_async_smem();
                 arrive_warp(&B->o_free);

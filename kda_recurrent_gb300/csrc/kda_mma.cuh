@@ -16,6 +16,16 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     return *reinterpret_cast<uint32_t *>(&v);
 }
 
+// The same, except that magnitudes above the largest finite number become that (NaN stays NaN).
+__device__ __forceinline__ uint32_t pack_bf16_finite(float lo, float hi) {
+    uint32_t v;
+    asm("cvt.rn.satfinite.bf16x2.f32 %0, %1, %2;" : "=r"(v) : "f"(hi), "f"(lo));
+    return v;
+}
+
+// Bits 15 and 31: whether the low and the high one of two BF16 numbers is an infinity or NaN.
+__device__ __forceinline__ uint32_t not_finite(uint32_t x) { return ((x & 0x7fff7fffu) + 0x00800080u) & 0x80008000u; }
+
 // FP32 -> TF32 (round to nearest, ties away from zero), returned as the 32-bit pattern the
 // tensor cores read. Done on the integer pipe: half a TF32 ulp (bit 12) is added to the
 // magnitude bits and the 13 bits below the TF32 mantissa are cleared; a carry into the

@@ -170,6 +170,75 @@ def test_prefill_sequences_do_not_touch(workspace):
         assert torch.equal(out2[lo:hi], out[lo:hi]) and torch.equal(fin2[n], fin[n])
 
 
+@pytest.mark.parametrize("lens,H,at,final", [([300], 2, 200, True), ([300], 2, 290, False), ([128], 1, 5, False),
+                                             ([70, 129, 60], 3, 100, True), ([40] * 200, 2, 50, False),
+                                             ([1500], 2, 700, True), ([2000], 1, 1990, False)])
+@pytest.mark.parametrize("workspace", [False, True])
+def test_prefill_values_that_are_not_finite_stay_in_their_channel(lens, H, at, final, workspace):
+    # ... and begin at their token: earlier outputs, other channels, sequences and heads do not see them
+    inp = R.linear_inputs(lens, H, seed=29, decay="head", device=DEV)
+    inp["log_decay"].fill_(-0.01)
+    out, fin = run(inp, workspace, want_final=final)
+    cu = inp["cu_seqlens"].tolist()
+    n = max(i for i, a in enumerate(cu[:-1]) if a <= at)
+    last = min(at + 20, cu[n + 1] - 1)
+    bad = {m: None if x is None else x.clone() for m, x in inp.items()}
+    places = ((at, 3, math.inf), (at, 70, -math.inf), (last, 127, math.nan), (at, 9, math.inf), (last, 9, -math.inf),
+              (last, 71, math.inf))
+    for t, c, x in places:
+        bad["v"][t, H - 1, c] = x
+    out2, fin2 = run(bad, workspace, want_final=final)
+    odd = sorted({c for _, c, _ in places})
+    one = {m: None if x is None else x[:, H - 1:].contiguous() if m in "qkv" else x[H - 1:] if m == "log_decay" else
+           x[:, H - 1:] if m == "init_state" else x for m, x in bad.items()}
+    ref_out, ref_fin = R.linear_prefill(one, SCALE)
+    a, b = cu[n], cu[n + 1]
+    got, ref = out2[a:b, H - 1][:, odd].cpu().double(), ref_out[a:b, 0][:, odd]
+    assert torch.equal(torch.isfinite(got), torch.isfinite(ref)) and not torch.isfinite(ref[-1]).any()
+    assert_out_close(got[torch.isfinite(ref)], ref[torch.isfinite(ref)])
+    same = torch.ones(out.shape, dtype=torch.bool, device=DEV)
+    same[a:b, H - 1, odd] = False
+    assert torch.equal(out2[same], out[same])
+    if final:
+        assert torch.equal(fin2[n, H - 1][:, odd].cpu().double().nan_to_num(nan=7.0), ref_fin[n, 0][:, odd].nan_to_num(nan=7.0))
+        fin2[n, H - 1][:, odd] = fin[n, H - 1][:, odd]
+        assert torch.equal(fin2, fin)
+
+
+@pytest.mark.parametrize("name,x", [("q", math.nan), ("q", math.inf), ("k", math.nan), ("k", -math.inf), ("log_decay", math.nan)])
+@pytest.mark.parametrize("lens,at", [([300], 200), ([1500, 40], 700)])
+@pytest.mark.parametrize("workspace", [False, True])
+def test_prefill_nothing_that_is_not_finite_reaches_an_earlier_token(name, x, lens, at, workspace):
+    inp = R.linear_inputs(lens, 2, seed=36, decay="token", device=DEV)
+    out, fin = run(inp, workspace)
+    inp[name] = inp[name].clone()
+    inp[name][at, 1] = x
+    out2, fin2 = run(inp, workspace)
+    assert not torch.isfinite(out2[at, 1]).any()
+    same = torch.ones(out.shape, dtype=torch.bool, device=DEV)
+    same[at:lens[0] if name != "q" else at + 1, 1] = False
+    assert torch.equal(out2[same], out[same])
+    assert torch.equal(fin2[1:], fin[1:]) and torch.equal(fin2[0, 0], fin[0, 0])
+    assert torch.equal(fin2[0, 1], fin[0, 1]) if name == "q" else not torch.isfinite(fin2[0, 1]).any()
+
+
+def test_prefill_every_chunk_ends_in_nan():
+    # every output but each chunk's last is formed again
+    inp = R.linear_inputs([1280], 2, seed=37, device=DEV)
+    clean, _ = run(inp)
+    inp["v"][127::128] = math.nan
+    out, fin = run(inp)
+    assert_out_close(out[:127], clean[:127])
+    assert torch.isnan(out[127:]).all() and torch.isnan(fin).all()
+
+
+def test_prefill_all_values_nan():
+    inp = R.linear_inputs([20, 400], 2, seed=30, device=DEV)
+    inp["v"].fill_(math.nan)
+    out, fin = run(inp)
+    assert torch.isnan(out).all() and torch.isnan(fin).all()
+
+
 def test_prefill_windows_in_place():
     # the initial state lies where the end state goes, which other windows' launches read before
     inp = R.linear_inputs([1400, 0, 1700], 2, seed=24, decay="token", device=DEV)
