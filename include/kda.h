@@ -280,7 +280,8 @@ KDA_API int kda_linear_prefill(const void *q, const void *k, const void *v, cons
                                void *workspace, int64_t workspace_bytes, kda_stream_t stream);
 
 /* kda_linear_prefill_workspace_size -- bytes of workspace kda_linear_prefill uses for this
- * shape (0: none). sm_count as for kda_prefill_workspace_size. */
+ * shape (0: none). sm_count as for kda_prefill_workspace_size. Sizes that the call refuses are
+ * refused here with the same status (negative). */
 KDA_API int64_t kda_linear_prefill_workspace_size(int32_t num_seqs, int32_t total_tokens,
                                                   int32_t num_heads, int32_t sm_count);
 
@@ -336,7 +337,8 @@ KDA_API int kda_attn_decode(const void *q, const void *k_cache, const void *v_ca
                             void *workspace, int64_t workspace_bytes, kda_stream_t stream);
 
 /* kda_attn_decode_workspace_size -- bytes of workspace for a call of this shape, with or
- * without `weight`. sm_count 0 asks the current device; > 0 is pure host arithmetic. */
+ * without `weight`. sm_count 0 asks the current device; > 0 is pure host arithmetic. Sizes that
+ * the call refuses are refused here with the same status (negative). */
 KDA_API int64_t kda_attn_decode_workspace_size(int32_t batch, int32_t num_q_heads, int32_t num_kv_heads,
                                                int32_t max_pages, int32_t page_size,
                                                int32_t with_weight, int32_t sm_count);

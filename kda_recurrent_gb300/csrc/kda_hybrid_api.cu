@@ -12,19 +12,40 @@ bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p
 
 int from_cuda(cudaError_t e) { return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA; }
 
+// What a cache's shape may be: 32-bit token positions and item counts, 64-bit cache offsets.
+int cache_shape(int32_t batch, int32_t num_kv_heads, int32_t max_pages, int32_t page_size) {
+    if (batch < 0 || num_kv_heads < 1 || max_pages < 1 || page_size < 1) return KDA_ERR_INVALID_ARG;
+    if (page_size < 8 || page_size > 1024 || (page_size & (page_size - 1)) != 0) return KDA_ERR_UNSUPPORTED;
+    if ((int64_t)max_pages * page_size > 0x3fffffffLL || (int64_t)batch * num_kv_heads > 0xffffffLL ||
+        (int64_t)num_kv_heads * page_size * kHeadDim > 0x3fffffffLL)
+        return KDA_ERR_UNSUPPORTED;
+    return KDA_OK;
+}
+
+int attn_shape(int32_t batch, int32_t num_q_heads, int32_t num_kv_heads, int32_t max_pages, int32_t page_size) {
+    if (num_q_heads < 1 || num_kv_heads < 1 || num_q_heads % num_kv_heads != 0) return KDA_ERR_INVALID_ARG;
+    const int bad = cache_shape(batch, num_kv_heads, max_pages, page_size);
+    if (bad != KDA_OK) return bad;
+    return (int64_t)batch * num_q_heads > 0xffffffLL ? KDA_ERR_UNSUPPORTED : KDA_OK;
+}
+
+int linear_prefill_shape(int32_t num_seqs, int32_t total_tokens, int32_t num_heads) {
+    if (num_seqs < 0 || total_tokens < 0 || num_heads < 1) return KDA_ERR_INVALID_ARG;
+    if ((int64_t)total_tokens * num_heads > ((int64_t)1 << 40) / kHeadDim) return KDA_ERR_UNSUPPORTED;
+    return (int64_t)num_seqs * num_heads > 0x7fffffffLL / kHeadDim ? KDA_ERR_UNSUPPORTED : KDA_OK;
+}
+
 // Checks the cache's sizes and pointers and fills `c`.
 int paged_cache(PagedCache *c, void *k_cache, void *v_cache, int64_t k_page_stride, int64_t v_page_stride,
                 int64_t num_pages, int32_t page_size, const int32_t *block_table, int32_t max_pages,
                 const int32_t *seq_lens, int32_t batch, int32_t num_kv_heads) {
-    if (batch < 0 || num_kv_heads < 1 || num_pages < 1 || max_pages < 1 || page_size < 1) return KDA_ERR_INVALID_ARG;
-    if (page_size < 8 || page_size > 1024 || (page_size & (page_size - 1)) != 0) return KDA_ERR_UNSUPPORTED;
+    if (num_pages < 1) return KDA_ERR_INVALID_ARG;
+    const int bad = cache_shape(batch, num_kv_heads, max_pages, page_size);
+    if (bad != KDA_OK) return bad;
     const int64_t page = (int64_t)num_kv_heads * page_size * kHeadDim;
     if (k_page_stride < page || v_page_stride < page) return KDA_ERR_INVALID_ARG;
     if (k_page_stride % 8 != 0 || v_page_stride % 8 != 0) return KDA_ERR_MISALIGNED;
-    // 32-bit token positions and item counts; 64-bit cache offsets
-    if ((int64_t)max_pages * page_size > 0x3fffffffLL || (int64_t)batch * num_kv_heads > 0xffffffLL ||
-        page > 0x3fffffffLL || num_pages > 0x7fffffffLL)
-        return KDA_ERR_UNSUPPORTED;
+    if (num_pages > 0x7fffffffLL) return KDA_ERR_UNSUPPORTED;
     const int64_t stride = k_page_stride > v_page_stride ? k_page_stride : v_page_stride;
     if (stride > ((int64_t)1 << 60) / num_pages) return KDA_ERR_UNSUPPORTED;
     if (batch == 0) return KDA_OK;
@@ -56,10 +77,9 @@ int kda_linear_prefill(const void *q, const void *k, const void *v, const float 
                        const int32_t *cu_seqlens, const float *init_state, void *out, float *final_state,
                        int32_t num_seqs, int32_t total_tokens, int32_t num_heads, float scale, void *workspace,
                        int64_t workspace_bytes, kda_stream_t stream) {
-    if (num_seqs < 0 || total_tokens < 0 || num_heads < 1) return KDA_ERR_INVALID_ARG;
     if (!isfinite(scale) || (decay_per_token != 0 && decay_per_token != 1)) return KDA_ERR_INVALID_ARG;
-    if ((int64_t)total_tokens * num_heads * kHeadDim > (int64_t)1 << 40) return KDA_ERR_UNSUPPORTED;
-    if ((int64_t)num_seqs * num_heads > 0x7fffffffLL / kHeadDim) return KDA_ERR_UNSUPPORTED;
+    const int bad = linear_prefill_shape(num_seqs, total_tokens, num_heads);
+    if (bad != KDA_OK) return bad;
     if (num_seqs == 0) return total_tokens == 0 ? KDA_OK : KDA_ERR_INVALID_ARG;
     if (cu_seqlens == nullptr) return KDA_ERR_INVALID_ARG;
     if (total_tokens > 0 && (!q || !k || !v || !log_decay || !out)) return KDA_ERR_INVALID_ARG;
@@ -96,7 +116,9 @@ int kda_linear_prefill(const void *q, const void *k, const void *v, const float 
 
 int64_t kda_linear_prefill_workspace_size(int32_t num_seqs, int32_t total_tokens, int32_t num_heads,
                                           int32_t sm_count) {
-    if (num_seqs < 0 || total_tokens < 0 || num_heads < 1 || sm_count < 0) return KDA_ERR_INVALID_ARG;
+    if (sm_count < 0) return KDA_ERR_INVALID_ARG;
+    const int bad = linear_prefill_shape(num_seqs, total_tokens, num_heads);
+    if (bad != KDA_OK) return bad;
     if (sm_count == 0) {
         const int st = sm_count_of_current_device(&sm_count);
         if (st != KDA_OK) return st;
@@ -138,9 +160,9 @@ int kda_linear_decode(const void *q, const void *k, const void *v, const float *
 
 int64_t kda_attn_decode_workspace_size(int32_t batch, int32_t num_q_heads, int32_t num_kv_heads, int32_t max_pages,
                                        int32_t page_size, int32_t with_weight, int32_t sm_count) {
-    if (batch < 0 || num_kv_heads < 1 || num_q_heads < 1 || num_q_heads % num_kv_heads != 0 || max_pages < 1 ||
-        page_size < 1 || sm_count < 0)
-        return KDA_ERR_INVALID_ARG;
+    if (sm_count < 0) return KDA_ERR_INVALID_ARG;
+    const int bad = attn_shape(batch, num_q_heads, num_kv_heads, max_pages, page_size);
+    if (bad != KDA_OK) return bad;
     if (sm_count == 0) {
         const int st = sm_count_of_current_device(&sm_count);
         if (st != KDA_OK) return st;
@@ -154,14 +176,14 @@ int kda_attn_decode(const void *q, const void *k_cache, const void *v_cache, int
                     int32_t max_pages, const int32_t *seq_lens, void *out, float *lse, float *weight, int32_t batch,
                     int32_t num_q_heads, int32_t num_kv_heads, float scale, void *workspace, int64_t workspace_bytes,
                     kda_stream_t stream) {
-    if (num_q_heads < 1 || num_kv_heads < 1 || num_q_heads % num_kv_heads != 0 || !isfinite(scale))
-        return KDA_ERR_INVALID_ARG;
+    if (!isfinite(scale)) return KDA_ERR_INVALID_ARG;
+    int bad = attn_shape(batch, num_q_heads, num_kv_heads, max_pages, page_size);
+    if (bad != KDA_OK) return bad;
     AttnDecodeArgs a;
-    const int bad = paged_cache(&a.c, const_cast<void *>(k_cache), const_cast<void *>(v_cache), k_page_stride,
+    bad = paged_cache(&a.c, const_cast<void *>(k_cache), const_cast<void *>(v_cache), k_page_stride,
                                 v_page_stride, num_pages, page_size, block_table, max_pages, seq_lens, batch,
                                 num_kv_heads);
     if (bad != KDA_OK) return bad;
-    if ((int64_t)batch * num_q_heads > 0xffffffLL) return KDA_ERR_UNSUPPORTED;
     if (batch == 0) return KDA_OK;
     if (!q || !out || !workspace) return KDA_ERR_INVALID_ARG;
     if (!aligned(q, 16) || !aligned(out, 16) || !aligned(workspace, 16) || !aligned(lse, 4) || !aligned(weight, 16))

@@ -50,6 +50,11 @@ def test_linear_prefill_workspace_size(lib):
         assert e.value.status == INVALID
 
 
+@pytest.mark.parametrize("N,T,H", [(2**30, 0, 100), (2**31 - 1, 2**31 - 1, 2**31 - 1), (1, 2**31 - 1, 100), (2**24, 5, 2)])
+def test_linear_prefill_workspace_size_has_the_calls_limits(lib, N, T, H):
+    assert lib.kda_linear_prefill_workspace_size(N, T, H, 152) == UNSUPPORTED == prefill(lib, N=N, T=T, H=H)
+
+
 def decode(lib, **over):
     a = dict(q=A, k=A, v=A, g=A, per=0, slot=A, pool=A, slots=4, dt=0, out=A, R=3, H=2, scale=0.1)
     a.update(over)
@@ -103,6 +108,20 @@ def test_attn_decode_workspace_size(lib):
         with pytest.raises(K.KdaError) as e:
             K.kda_attn_decode_workspace_size(*bad, sm_count=152)
         assert e.value.status == INVALID
+
+
+@pytest.mark.parametrize("B,Hq,Hkv,P,ps", [(2**31 - 1, 64, 64, 1 << 20, 1024), (1 << 23, 64, 1, 4, 16), (2, 4, 2, 1 << 27, 16),
+                                           (2, 4, 2, 10, 4), (2, 4, 2, 10, 24), (2, 4, 2, 10, 2048), (1, 1 << 20, 1 << 20, 4, 1024)])
+@pytest.mark.parametrize("weight", [0, 1])
+def test_attn_decode_workspace_size_has_the_calls_limits(lib, B, Hq, Hkv, P, ps, weight):
+    assert lib.kda_attn_decode_workspace_size(B, Hq, Hkv, P, ps, weight, 152) == UNSUPPORTED
+    assert attn(lib, B=B, Hq=Hq, Hkv=Hkv, P=P, ps=ps, ks=1 << 40, vs=1 << 40) == UNSUPPORTED
+
+
+def test_attn_decode_workspace_size_of_the_largest_calls(lib):
+    # every size that the call takes has its bytes in 64 bits
+    n = lib.kda_attn_decode_workspace_size((1 << 24) - 1, 1, 1, (1 << 20) - 1, 1024, 1, 152)
+    assert n >= ((1 << 24) - 1) * ((1 << 20) - 1) * 1024 * 4
 
 
 def evict(lib, **over):
