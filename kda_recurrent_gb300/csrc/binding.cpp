@@ -167,6 +167,7 @@ int32_t decay_rows(PyObject *o, int64_t rows, int64_t heads, at::Device device) 
 struct Cache {
     const at::Tensor &k, &v, &lens, &table;
     int64_t batch, heads, page_size, pages, width;
+    int64_t stride(const at::Tensor &t) const { return pages == 1 ? heads * page_size * kHeadDim : t.stride(0); }  // (any, for one page)
 };
 
 Cache cache_of(PyObject *const *a, at::Device device) {
@@ -242,7 +243,7 @@ PyObject *attn_decode(PyObject *const *a) {
     const int32_t size = int_of(c.page_size, "k_cache"), width = int_of(c.width, "block_table"), batch = int_of(c.batch, "seq_lens"),
                   hq = int_of(Hq, "q"), heads = int_of(c.heads, "k_cache");
     return run(device, a[10], [&](kda_stream_t stream) {
-        return kda_attn_decode(address(q), address(c.k), address(c.v), c.k.stride(0), c.v.stride(0), c.pages, size,
+        return kda_attn_decode(address(q), address(c.k), address(c.v), c.stride(c.k), c.stride(c.v), c.pages, size,
                                address<int32_t>(c.table), width, address<int32_t>(c.lens), address(out), lse, weight, batch, hq,
                                heads, scale, ws.base, ws.bytes, stream);
     });
@@ -264,7 +265,7 @@ PyObject *cache_evict(PyObject *const *a) {
     const int32_t size = int_of(c.page_size, "k_cache"), width = int_of(c.width, "block_table"), batch = int_of(c.batch, "seq_lens"),
                   heads = int_of(c.heads, "k_cache");
     return run(device, a[12], [&](kda_stream_t stream) {
-        return kda_cache_evict(address(c.k), address(c.v), c.k.stride(0), c.v.stride(0), c.pages, size, address<int32_t>(c.table),
+        return kda_cache_evict(address(c.k), address(c.v), c.stride(c.k), c.stride(c.v), c.pages, size, address<int32_t>(c.table),
                                dst_table, width, address<int32_t>(c.lens), address<float>(weight), dst_weight,
                                address<int32_t>(new_lens), address<int32_t>(kept), batch, heads, budget, sink, recent, stream);
     });

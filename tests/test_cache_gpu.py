@@ -104,6 +104,19 @@ def test_attn_combined_cache():
     check(queries(2, 6, 43), c)
 
 
+def test_cache_of_one_page_has_any_page_stride():
+    c = R.cache_inputs([13], 2, 16, seed=60, extra_pages=0, device=DEV)
+    k, v = (torch.empty(2, 1, 16, 128, dtype=torch.bfloat16, device=DEV).transpose(0, 1).copy_(c[n]) for n in ("k_cache", "v_cache"))
+    assert k.shape[0] == 1 and k.stride(0) < k[0].numel()
+    q = queries(1, 4, 60)
+    args = (c["block_table"], c["seq_lens"])
+    assert torch.equal(K.attn_decode(q, k, v, *args, scale=SCALE), K.attn_decode(q, c["k_cache"], c["v_cache"], *args, scale=SCALE))
+    w = torch.rand(1, 2, 16, device=DEV)
+    for cache in ((k, v), (c["k_cache"], c["v_cache"])):
+        K.cache_evict(*cache, *args, w.clone(), budget=5)
+    assert torch.equal(k[:, :, :5], c["k_cache"][:, :, :5]) and torch.equal(v[:, :, :5], c["v_cache"][:, :, :5])
+
+
 def test_attn_missing_pages_are_masked():
     c = R.cache_inputs([200, 64, 500], 2, 16, seed=44, device=DEV)
     c["block_table"][0, 3] = -1
