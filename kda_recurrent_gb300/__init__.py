@@ -376,7 +376,8 @@ def _load_native():
             del torch
             path = _build.BINDING_PATH
             if not os.path.exists(path):
-                raise RuntimeError(f"KDA binding not built: {path} (run kda_recurrent_gb300.build.build())")
+                raise RuntimeError(f"KDA binding not built: {path} (run kda_recurrent_gb300.build.build(), which says why "
+                                   "where it cannot build it)")
             name = "kda_gb300_binding"
             loader = importlib.machinery.ExtensionFileLoader(name, path)
             module = importlib.util.module_from_spec(importlib.util.spec_from_file_location(name, path, loader=loader))

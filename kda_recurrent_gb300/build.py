@@ -5,7 +5,8 @@ parallel), then one link step produces the shared library next to this file in
 ``_build/``. Only ``-gencode arch=compute_103a,code=sm_103a`` is emitted.
 
 ``csrc/binding.cpp``, the compiled part of the Python binding, becomes
-``_build/kda_gb300_binding.so``, linked against that library and torch's headers.
+``_build/kda_gb300_binding.so``, linked against that library and torch's headers. Where g++ or the Python
+or torch headers are missing, the library is built without it: the calls that need it raise then.
 """
 from __future__ import annotations
 
@@ -14,6 +15,7 @@ import os
 import shutil
 import subprocess
 import sysconfig
+import warnings
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
@@ -39,18 +41,22 @@ def sources():
 
 
 def _deps():
-    files = sources() + [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cuh", ".h", ".cpp"))]
+    files = sources() + [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cuh", ".h"))]
     files.append(os.path.join(INCLUDE, "kda.h"))
     files.append(os.path.abspath(__file__))
     return files
 
 
+def _newer(made: str, files) -> bool:
+    return os.path.exists(made) and all(os.path.getmtime(f) <= os.path.getmtime(made) for f in files)
+
+
 def up_to_date(lib_path: str = LIB_PATH) -> bool:
-    made = [lib_path, BINDING_PATH] if lib_path == LIB_PATH else [lib_path]
-    if not all(os.path.exists(f) for f in made):
-        return False
-    t = min(os.path.getmtime(f) for f in made)
-    return all(os.path.getmtime(f) <= t for f in _deps())
+    return _newer(lib_path, _deps())
+
+
+def binding_up_to_date() -> bool:
+    return _newer(BINDING_PATH, [os.path.join(CSRC, "binding.cpp"), os.path.join(INCLUDE, "kda.h"), os.path.abspath(__file__)])
 
 
 def _compile_binding():
@@ -82,7 +88,9 @@ def build(force: bool = False, verbose: bool = False, extra_flags=(), lib_path: 
 
     ``extra_flags`` and another ``lib_path`` build a variant of the library in its own folder
     beside it (the failure-detection test builds one with a short wait limit that way)."""
-    if not force and up_to_date(lib_path):
+    with_binding = lib_path == LIB_PATH and (force or not binding_up_to_date())
+    with_library = force or not up_to_date(lib_path)
+    if not with_binding and not with_library:
         return lib_path
     build_dir = os.path.dirname(lib_path)
     os.makedirs(build_dir, exist_ok=True)
@@ -98,15 +106,21 @@ def build(force: bool = False, verbose: bool = False, extra_flags=(), lib_path: 
             print(r.stdout + r.stderr)
         return obj
 
-    srcs = sources()
+    srcs = sources() if with_library else []
     with cf.ThreadPoolExecutor(max_workers=min(len(srcs) + 1, os.cpu_count() or 1)) as ex:
-        binding = ex.submit(_compile_binding) if lib_path == LIB_PATH else None
+        binding = ex.submit(_compile_binding) if with_binding else None
         objs = list(ex.map(compile_one, srcs))
-    _link([nvcc, *ARCH, "-shared", *objs, "-cudart", "static"], lib_path)
-    if binding is not None:
-        obj, libs = binding.result()
-        _link(["g++", "-shared", obj, "-L", build_dir, "-l:" + os.path.basename(lib_path), "-Wl,-rpath,$ORIGIN", *libs],
-              BINDING_PATH)
+    if with_library:
+        _link([nvcc, *ARCH, "-shared", *objs, "-cudart", "static"], lib_path)
+    if with_binding:
+        try:
+            obj, libs = binding.result()
+            _link(["g++", "-shared", obj, "-L", build_dir, "-l:" + os.path.basename(lib_path), "-Wl,-rpath,$ORIGIN", *libs],
+                  BINDING_PATH)
+        except (ImportError, OSError, RuntimeError) as e:
+            if os.path.exists(BINDING_PATH):  # of other sources
+                os.remove(BINDING_PATH)
+            warnings.warn(f"the compiled part of the Python binding is missing, and the calls that need it will raise: {e}")
     return lib_path
 
 

@@ -157,6 +157,30 @@ def test_kernels_wait_for_the_launch_before_they_touch_memory(name):
         assert not touches, touches
 
 
+# ---------------------------------------------------------------- the build
+
+
+@pytest.mark.parametrize("fails", ["compile", "headers"])
+def test_the_library_builds_without_the_compiled_binding(lib, monkeypatch, tmp_path, fails):
+    """Who calls the C functions only, or the KDA calls, needs no Python or torch headers."""
+    path = tmp_path / "binding.so"
+    path.write_bytes(b"")
+    os.utime(path, (0, 0))  # of older sources
+    monkeypatch.setattr(kbuild, "BINDING_PATH", str(path))
+    if fails == "compile":
+        def refuse():
+            raise RuntimeError("g++ failed on binding.cpp")
+        monkeypatch.setattr(kbuild, "_compile_binding", refuse)
+    else:
+        monkeypatch.setattr(kbuild.sysconfig, "get_paths", lambda: {"include": str(tmp_path / "none")})
+    with pytest.warns(UserWarning, match="binding"):
+        assert kbuild.build() == kbuild.LIB_PATH
+    assert kbuild.up_to_date() and not path.exists()
+    monkeypatch.setattr(K, "_native", None)
+    with pytest.raises(RuntimeError, match="binding not built"):
+        K.linear_decode(*[torch.zeros(1, 1, 128, dtype=torch.bfloat16)] * 3, None, None, None, scale=1.0)
+
+
 # ---------------------------------------------------------------- the binding's own checks
 
 
