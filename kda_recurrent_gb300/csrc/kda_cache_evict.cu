@@ -344,6 +344,9 @@ constexpr int kCopyStages = 3;
 
 template <int kVecs>
 constexpr int kPackSmem = kCopyWarps * kCopyStages * (kTileBytes + 32 * kCopyUnroll / kVecs * (int)sizeof(Move));
+template <int kVecs>  // CTAs on an SM: of its 228 KiB each takes 1 KiB more
+constexpr int kPackCtas = 228 * 1024 / (kPackSmem<kVecs> + 1024);
+static_assert(kPackCtas<4> == 1 && kPackCtas<8> == 2 && kPackCtas<16> == 2, "the moves of narrow slices take a third of their memory");
 
 template <int kVecs>
 __global__ void __launch_bounds__(kCopyThreads) kda_evict_pack_kernel(const CacheEvictArgs a) {
@@ -454,11 +457,11 @@ cudaError_t launch_cache_evict(const CacheEvictArgs &a, cudaStream_t stream) {
         return launch_dependent(kda_evict_copy_kernel, dim3((unsigned)rows, 2, (unsigned)std::min(parts, 65535)), kCopyThreads, kSmem,
                                 stream, a);
     }
-    // The narrowest slices whose CTAs still run at once (two on an SM). Whole call for 2000 of 4096 tokens of 8,
-    // 64, 144 and 312 row-heads with slices of 64 / 128 / 256 bytes, in us: 12 / 15 / 22, 39 / 27 / 33,
-    // 80 / 60 / 55, 187 / 121 / 123.
-    if (4 * 2 * (int64_t)rows <= 2 * sms) return launch_pack<4>(a, stream);
-    if (2 * 2 * (int64_t)rows <= 2 * sms) return launch_pack<8>(a, stream);
+    // The narrowest slices whose CTAs still run at once. Whole call for 2000 of 4096 tokens of 8, 19, 20, 30, 64, 76,
+    // 144 and 312 row-heads with slices of 64 / 128 / 256 bytes, in us: 12 / 15 / 23, 13 / 16 / 24, 18 / 16 / 24,
+    // 19 / 16 / 24, 35 / 25 / 34, 40 / 29 / 36, 73 / 55 / 53, 191 / 124 / 127.
+    if (4 * 2 * (int64_t)rows <= kPackCtas<4> * sms) return launch_pack<4>(a, stream);
+    if (2 * 2 * (int64_t)rows <= kPackCtas<8> * sms) return launch_pack<8>(a, stream);
     return launch_pack<16>(a, stream);
 }
 

@@ -387,6 +387,11 @@ def test_evict_in_place_by_slices():
     check_evict([260 + 7 * i for i in range(10)], 5, 16, 200, 4, 50, seed=69, in_place=True)
 
 
+@pytest.mark.parametrize("rows,Hkv", [(19, 1), (10, 2), (38, 1), (13, 3), (19, 4), (11, 7)])
+def test_evict_in_place_beside_the_slices_limits(rows, Hkv):
+    check_evict([230 + 11 * i for i in range(rows)], Hkv, 16, 200, 4, 50, seed=72, in_place=True)
+
+
 @pytest.mark.parametrize("in_place", [False, True])
 def test_evict_offsets_pass_32_bits(in_place):
     pages, ps = 140000, 16  # 2.3e9 elements each
