@@ -318,6 +318,93 @@ def test_prefill_windowed_calls_without_waits_equal_calls_with_waits():
         assert torch.isfinite(x).all() and torch.equal(x, y)
 
 
+def windowed(N, T, H):
+    ws = K.linear_prefill_workspace(N, T, H, DEV)
+    assert ws is not None
+    return ws
+
+
+@pytest.mark.parametrize("decay", ["head", "token"])
+@pytest.mark.parametrize("lens,H", [([1024, 1, 2400], 2), ([2500, 0, 130, 128, 7], 3), ([40, 3000], 5), ([16 * 128, 16 * 128 + 1], 4)])
+def test_prefill_windows_varlen(lens, H, decay):
+    windowed(len(lens), sum(lens), H)
+    inp = R.linear_inputs(lens, H, seed=38, decay=decay, init=decay == "token", device=DEV)
+    out, fin = check(inp, workspace=True)
+    alone, none = run(inp, workspace=True, want_final=False)
+    assert none is None and torch.equal(alone, out)
+
+
+def test_prefill_windows_split_and_carry():
+    # the state goes from one windowed call to the next in place
+    inp = R.linear_inputs([4300], 2, seed=39, decay="token", device=DEV)
+    ref_out, ref_fin = R.linear_prefill(inp, SCALE)
+    state, outs = inp["init_state"].clone(), []
+    for a, b in ((0, 1300), (1300, 2900), (2900, 4300)):
+        part = [inp[n][a:b].contiguous() for n in ("q", "k", "v", "log_decay")]
+        outs.append(torch.empty_like(part[0]))
+        K.kda_linear_prefill(*part, torch.tensor([0, b - a], dtype=torch.int32, device=DEV), state, outs[-1], state, SCALE,
+                             workspace=windowed(1, b - a, 2))
+    assert_out_close(torch.cat(outs), ref_out)
+    assert_state_close(state, ref_fin, tol=3 * STATE_TOL)
+
+
+def test_prefill_windows_on_another_stream_and_graph():
+    inp = R.linear_inputs([2700, 50], 2, seed=40, device=DEV)
+    ref, fref = run(inp, True)
+    ws = windowed(2, 2750, 2)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        q, k, v = (inp[n].clone() for n in "qkv")  # on that stream, behind which the call has to wait
+    out, fin = K.linear_prefill(q, k, v, inp["log_decay"], inp["cu_seqlens"], inp["init_state"], scale=SCALE, workspace=ws,
+                                stream=s)
+    s.synchronize()
+    assert torch.equal(out, ref) and torch.equal(fin, fref)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=s):
+        K.kda_linear_prefill(q, k, v, inp["log_decay"], inp["cu_seqlens"], inp["init_state"], out, fin, SCALE, workspace=ws)
+    for _ in range(3):
+        out.zero_(), fin.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, ref) and torch.equal(fin, fref)
+
+
+def test_prefill_token_offsets_pass_32_bits():
+    T, H = 69800, 256  # 2.3e9 elements each
+    gen = torch.Generator(device=DEV).manual_seed(41)
+    q, k, v = (torch.empty(T, H, 128, dtype=torch.bfloat16, device=DEV).normal_(0.0, s, generator=gen) for s in (0.1, 0.1, 1.0))
+    g = -torch.rand(T, H, generator=gen, device=DEV)
+    cu = torch.tensor([0, 68000, 69500, T], dtype=torch.int32, device=DEV)
+    out, fin = K.linear_prefill(q, k, v, g, cu, scale=SCALE)
+    a = 68000
+    assert (a * H + 200) * 128 > 2 ** 31
+    heads = [0, 200, 255]
+    part = [x[a:, heads].contiguous() for x in (q, k, v, g)]
+    small, fsmall = K.linear_prefill(*part, cu[1:] - a, scale=SCALE)
+    assert torch.equal(out[a:, heads], small) and torch.equal(fin[1:, heads], fsmall)
+    inp = dict(zip(("q", "k", "v", "log_decay"), part), cu_seqlens=cu[1:] - a, init_state=None)
+    ref_out, ref_fin = R.linear_prefill(inp, SCALE)
+    assert_out_close(small, ref_out)
+    assert_state_close(fsmall, ref_fin, tol=STATE_TOL)
+
+
+def test_prefill_state_offsets_pass_32_bits():
+    N = 140000  # sequences of one token: 2.3e9 state elements, in place
+    gen = torch.Generator(device=DEV).manual_seed(42)
+    q, k, v = (torch.randn(N, 1, 128, generator=gen, device=DEV).to(torch.bfloat16) for _ in range(3))
+    g = torch.full((1,), -0.5, device=DEV)
+    state = torch.full((N, 1, 128, 128), 0.25, device=DEV)
+    cu = torch.arange(N + 1, dtype=torch.int32, device=DEV)
+    out = torch.empty_like(q)
+    K.kda_linear_prefill(q, k, v, g, cu, state, out, state, 0.01)
+    for n in (0, 131071, 131072, N - 1):
+        want = 0.25 * math.exp(-0.5) + k[n, 0].double()[:, None] * v[n, 0].double()
+        assert_state_close(state[n, 0], want, tol=STATE_TOL)
+        assert_out_close(out[n, 0], 0.01 * q[n, 0].double() @ want)
+    assert K.kda_device_status()[0] == K.KDA_OK
+
+
 def test_prefill_repeats_bit_for_bit():
     inp = R.linear_inputs([1500, 77], 3, seed=19, device=DEV)
     for ws in (False, True):
