@@ -326,6 +326,10 @@ KDA_API int kda_linear_decode(const void *q, const void *k, const void *v, const
  *                also where another token makes the row NaN.)
  *   workspace    at least kda_attn_decode_workspace_size(...) bytes, 16-byte aligned.
  *                Contents on entry do not matter; calls sharing one must not overlap.
+ * With `weight`, the workspace holds 4 bytes for every query head and token of the table's width, and
+ * the launch grows with that width: max_pages is best kept near the longest row. More than 16
+ * query heads a key head read the cache once for every 16. A value that is not finite reaches its
+ * own channel only.
  * A row with no unmasked token (or whose every x_j is -inf) gives zeros, and -inf in lse. The
  * sums run in a fixed order: equal inputs give equal bits.
  */

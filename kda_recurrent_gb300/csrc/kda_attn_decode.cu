@@ -4,7 +4,7 @@
 //
 // Every cached token is read once (512 bytes a key head) and used by the query heads that share
 // its key head, so the kernel is an HBM stream. An item is a (row, key head, 16 of its query
-// heads); its tokens come in tiles of 16. All items' tiles, laid end to end, are cut into
+// heads); a key head with more of them is read once for every 16. Its tokens come in tiles of 16. All items' tiles, laid end to end, are cut into
 // equal shares, one for each CTA (one on an SM) and in it one for each of its eight warps, so that any
 // mixture of lengths keeps every warp busy to the end. A warp walks its share alone: its own ring of
 // cp.async stages (three tiles, so about 128 KiB are in flight on an SM), no barrier with other warps. It
@@ -21,9 +21,10 @@
 // the result independent of timing. With `weight`, the first kernel stores the scores (4 bytes a query
 // head beside the token's 512) and a third adds 2^(x - lse) to the weights.
 //
-// 64 rows of 4096 to 32768 tokens, 8 key heads: 758 us, 6.72 TB/s (0.99 of a copy's rate). 16 rows of 1600
-// tokens, 8 key heads: about 24 us, of which the stream is 16 and the rest start (3: lengths, places, first
-// tiles), join and the gaps between the launches. One row of 1000 tokens on 8 heads: 7.4 us, all latency.
+// 64 rows of 4096 to 32768 tokens, 8 key heads: 727-746 us, 6.8-7.0 TB/s (1.00-1.03 of a copy's rate). 16 rows of
+// 1600 tokens, 8 key heads: about 24 us, with weights 30, of which the stream is 16 and the rest start (3: lengths,
+// places, first tiles), join, weights and the gaps between the launches. One row of 1000 tokens on 8 heads: 7.7
+// us, all latency.
 //
 // The order of the 128 channels inside a product is free, so the fragments are laid out for 16-byte
 // shared-memory reads: a lane's 16 bytes of a key row serve two k-steps, and of a value row eight column
@@ -648,7 +649,8 @@ __global__ void __launch_bounds__(kThreads, 4) kda_attn_join_kernel(const Args a
 
 // weight[b][h][j] += sum over the query heads of key head h of 2^(x_j - lse), four tokens a thread. A score of
 // -inf has no weight whatever the lse (which a NaN key elsewhere in the row makes NaN). Tokens of a missing page
-// are not written: a page holds whole groups of four, so those are the groups that have no other score.
+// are not written: a page holds whole groups of four, so those are the groups that have no other score. The grid
+// covers the table's width, which is what the host knows; CTAs past their row's length leave at once.
 constexpr int kWeightThreads = 256, kWeightTokens = 4 * kWeightThreads;
 
 __global__ void __launch_bounds__(kWeightThreads) kda_attn_weight_kernel(const Args a) {

@@ -17,9 +17,9 @@
 //     touch each other, which is what the CTAs of one head split by when few heads leave the
 //     GPU idle; between disjoint pages the tokens split too.
 //
-// Bound: the copy's HBM traffic for long rows (32 rows of 8192 to 16384 tokens, 8 heads, cut to 4096: 183 us,
-// 25 of them the selection; 5.98 TB/s over the whole, 0.88 of a copy's rate), latency for short ones (2 rows of
-// 1500 tokens, 8 heads, cut to 512: 7.2 us; the selection's chain is a row's length beside its weights, two or
+// Bound: the copy's HBM traffic for long rows (32 rows of 8192 to 16384 tokens, 8 heads, cut to 4096: 184 us,
+// 25 of them the selection; 5.96 TB/s over the whole, 0.88 of a copy's rate), latency for short ones (2 rows of
+// 1500 tokens, 8 heads, cut to 512: 7.4 us; the selection's chain is a row's length beside its weights, two or
 // three digits of four barriers each, and the ordered pass).
 #include <algorithm>
 

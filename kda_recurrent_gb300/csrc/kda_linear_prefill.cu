@@ -41,12 +41,14 @@
 // These measurements are in cycles of about 1.85 GHz, all SMs busy.
 //
 // The suffix sums G_last - G_j are scanned from the end, not formed as differences, so that a
-// strong decay early in a chunk costs the later tokens' weights no precision. A log decay below
-// -128 counts as -128 (both decay to zero in FP32), which keeps the sums finite.
+// strong decay early in a chunk costs the later tokens' weights in the state no precision. The scores' exponents
+// G_i - G_j are differences of prefix sums: behind many decays near the least one they lose up to 5e-4 of a
+// score, a quarter of what its rounding to BF16 may take. A log decay below -128 counts as -128 (both decay to
+// zero in FP32), which keeps the sums finite.
 //
 // Bound: 1 KiB of HBM traffic a token and head against 164 KFLOP of BF16 products, so bandwidth where there
-// are chains for every SM: 8 x 16384 tokens x 96 heads take 2.16 ms, 6.0 TB/s (0.89 of a copy's rate), 16
-// sequences of 256 to 4096 tokens x 32 heads 165 us, 5.33 TB/s. A chain alone takes 2.9 us a chunk (its own
+// are chains for every SM: 8 x 16384 tokens x 96 heads take 2.18 to 2.26 ms by machine, 5.7 to 5.9 TB/s (0.85-0.88 of
+// a copy's rate), 16 sequences of 256 to 4096 tokens x 32 heads 166-170 us, 5.2 TB/s. A chain alone takes 3.0 us a chunk (its own
 // latency: split, D, the update, the operand of the next Q S), about what its share of the bandwidth allows
 // when all SMs run one.
 //
@@ -99,8 +101,8 @@ struct Gates {
     float pad[3];
 };
 
-// Sequences in order of length, longest first (ties by index): items are handed out in index order,
-// so the longest chains start first. More than kRanked sequences keep index order.
+// Sequences in order of length, longest first (ties by index): items are handed out in index order, so that the
+// longest chains are the first ones. More than kRanked sequences keep index order.
 constexpr int kRanked = 256;
 
 // A chain, or a window of one. nchunks < 0: there are no more items.
@@ -526,9 +528,11 @@ __device__ __forceinline__ Item item_of(const ChunkArgs &a, int i, const uint8_t
 // kStates: only the state update, from zero, over the windows of the windowed chains but the last.
 //
 // A CTA runs item after item (its own index first, then those of CTAs of the grid that have not been
-// launched, which it takes over by clusterlaunchcontrol): items are handed out as SMs become free, the
-// longest first, and the roles go from one item's last chunk to the next one's first without emptying
-// the pipeline. All counters that give a barrier's phase run on over the items.
+// launched, which it takes over by clusterlaunchcontrol), and the roles go from one item's last chunk to
+// the next one's first without emptying the pipeline. It asks for the next item when it begins one, which
+// hides the answer's latency, also in items of one chunk, but holds that item back from SMs that run out of
+// work earlier: items are handed out in index order, one ahead of when they are begun. All counters that give a
+// barrier's phase run on over the items.
 template <bool kStates>
 __global__ void __launch_bounds__(kThreads, 1)
     kda_linear_chunk_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap map_q,
@@ -1156,11 +1160,11 @@ cudaError_t configure_once() {
 
 // Chains that fill at most a third of the GPU, alone or as a last wave, are cut into windows, if the longest
 // of them can be expected to gain: the lengths are on the device, so it is taken to be what it is on average
-// for lengths uniform over [0, L], 2 / (num_seqs + 1) of all chunks. A chunk takes 2.9 us of a chain's time,
-// windows cost about 11 us and run through a window's chunks twice (the first time faster). Whole chains
-// against windows, in us: 8 chains (19 windows) of 4 chunks 17 and 21, of 8 28 and 21, of 64 189 and 40; 24
-// chains (6 windows) of 6 chunks 23 and 25, of 12 40 and 30; 48 chains (3 windows) of 16 chunks 53 and 55, of
-// 24 76 and 67.
+// for lengths uniform over [0, L], 2 / (num_seqs + 1) of all chunks. A chunk takes 3.0 us of a chain's time,
+// windows cost about 12 us and run through a window's chunks twice (the first time faster). Whole chains
+// against windows, in us: 8 chains (19 windows) of 4 chunks 17 and 21, of 8 29 and 22, of 64 194 and 41; 24
+// chains (6 windows) of 6 chunks 23 and 25, of 12 41 and 30; 48 chains (3 windows) of 16 chunks 54 and 55, of
+// 24 77 and 67.
 constexpr int64_t kLeastGain = 5;  // chunks
 
 Plan plan_linear(int32_t num_seqs, int32_t total_tokens, int32_t num_heads, int32_t sms) {
