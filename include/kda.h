@@ -245,7 +245,9 @@ KDA_API int kda_decode_ex(const void *q, const void *k, const void *v, const voi
 /*
  * The operators a hybrid model needs beside KDA layers: linear attention with one decay a
  * head (kda_linear_prefill, kda_linear_decode), attention of one new token over a paged
- * key-value cache (kda_attn_decode) and eviction from that cache (kda_cache_evict).
+ * key-value cache (kda_attn_decode) and eviction from that cache (kda_cache_evict). Around that
+ * attention: pages for growing and shrinking rows (kda_page_resize), norm and rotation of queries and
+ * keys on their way into the cache (kda_qk_norm_rope).
  */
 
 /*
@@ -372,6 +374,73 @@ KDA_API int kda_cache_evict(void *k_cache, void *v_cache, int64_t k_page_stride,
                             const float *weight, float *dst_weight, int32_t *new_lens, int32_t *kept,
                             int32_t batch, int32_t num_kv_heads, int32_t budget, int32_t sink,
                             int32_t recent, kda_stream_t stream);
+
+/*
+ * kda_page_resize -- pages of a paged key-value cache handed out as rows grow and shrink, and the
+ * slots of the new tokens. Row b goes from seq_lens[b] to new_lens[b] tokens; a row of n tokens
+ * holds the first ceil(n / page_size) entries of its table.
+ *   block_table  int32 [batch, max_pages]: entries of pages taken are written, no others (those
+ *                of pages given back keep their old values, behind the row's new end)
+ *   free_pages   int32 [num_pages], a ring, and free_state int32 [2] {first, count}: the free
+ *                pages are the count entries from index first on, modulo num_pages. Rows take from
+ *                its front and give back behind its end, both in row order and in the order of
+ *                the table. What a call gives back, a later call can take.
+ *   out_lens     int32 [batch]: the rows' lengths after the call. May equal seq_lens or new_lens.
+ *   out_state    int32 [2]: {first, count} after the call. May equal free_state.
+ *   cu_tokens    int32 [batch + 1], or NULL: sums of the new tokens, max(0, new - old) a row
+ *   slots        int64 [max_tokens], or NULL: for each new token, packed row after row, page *
+ *                page_size + offset (what kda_qk_norm_rope takes); -1 where its row got no pages
+ *                or its page is missing
+ *   positions    int32 [max_tokens], or NULL: its position in its row
+ *   rows         int32 [max_tokens], or NULL: its row
+ * Entries of the three maps past the last new token become -1, 0 and -1, so that a captured call
+ * may serve fewer tokens than it was made for.
+ * Rows are served in order: the first row whose pages are not all free, and every later row that
+ * needs pages, gets none and keeps its length (its tokens keep their places in the packed order,
+ * with slot -1), and is recorded as KDA_ERR_DEVICE_INPUT. Also recorded: a length outside
+ * [0, max_pages * page_size] (clamped), a state or a page outside its range (taken as an empty
+ * ring, and as missing), new tokens past max_tokens (left out of the maps), a page given back
+ * when the ring is full. Missing pages (negative entries) are not given back. A page that
+ * several rows share is given back by each row that shrinks below it: shrink all but one of them
+ * no further than what they share. 1 <= num_pages < 2^30.
+ */
+KDA_API int kda_page_resize(int32_t *block_table, const int32_t *seq_lens, const int32_t *new_lens,
+                            int32_t *out_lens, int32_t *free_pages, const int32_t *free_state,
+                            int32_t *out_state, int32_t num_pages, int32_t page_size, int32_t batch,
+                            int32_t max_pages, int32_t *cu_tokens, int64_t *slots,
+                            int32_t *positions, int32_t *rows, int32_t max_tokens,
+                            kda_stream_t stream);
+
+/*
+ * kda_qk_norm_rope -- queries and keys normed and rotated, keys and values written to the cache:
+ *     y = x * (mean x^2 + eps)^-1/2 * w                  over the 128 channels of each head
+ *     (a, b) -> magnitude * (a cos - b sin, b cos + a sin), angle = position * inv_freq[i]
+ * for the pairs i of the first rot_dim channels: (i, i + rot_dim / 2), or (2i, 2i + 1) if interleaved.
+ *   q            BF16 [tokens, num_q_heads, 128]; k, v BF16 [tokens, num_kv_heads, 128]. A token's
+ *                heads are contiguous and tokens q_stride, k_stride, v_stride elements apart
+ *                (multiples of 8), so that the three may be views of one projection's output.
+ *   positions    int32 [tokens]; inv_freq FP32 [rot_dim / 2] (radians a position, finite; any
+ *                scaling for long contexts is in its values, and in magnitude, the factor on
+ *                the rotated channels). The angle is exact to 2^-30 of a turn for positions up
+ *                to 2^20. rot_dim is a multiple of 16 in [0, 128]; 0: no rotation (both may be NULL).
+ *   q_weight, k_weight  [128], FP32 (weight_bf16 = 0) or BF16 (1); NULL: no norm. eps >= 0.
+ *   q_out        BF16 like q, with its own stride; may be q itself (with q's stride)
+ *   k_out        BF16 like k, or NULL (only with a cache); may be k itself
+ *   slots        int64 [tokens]: token t's key and value go to slot slots[t] % page_size of page
+ *                slots[t] / page_size. Negative: not written. One past the cache: not written,
+ *                and recorded as KDA_ERR_DEVICE_INPUT. Slots must be unique. slots, k_cache and
+ *                v_cache are NULL together (v is then not read); the cache as for kda_attn_decode.
+ * Computed in FP32 and rounded once. The outputs must not overlap the inputs otherwise.
+ */
+KDA_API int kda_qk_norm_rope(const void *q, const void *k, const void *v, int64_t q_stride, int64_t k_stride,
+                             int64_t v_stride, const int32_t *positions, const float *inv_freq,
+                             int32_t rot_dim, int32_t interleaved, float magnitude, const void *q_weight,
+                             const void *k_weight, int32_t weight_bf16, float eps, void *q_out,
+                             int64_t q_out_stride, void *k_out, int64_t k_out_stride, void *k_cache,
+                             void *v_cache, int64_t k_page_stride, int64_t v_page_stride,
+                             int64_t num_pages, int32_t page_size, const int64_t *slots,
+                             int32_t tokens, int32_t num_q_heads, int32_t num_kv_heads,
+                             kda_stream_t stream);
 
 /* A static, human-readable name for a kda_status value. Never NULL. */
 KDA_API const char *kda_status_string(int status);

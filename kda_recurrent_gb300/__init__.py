@@ -21,8 +21,14 @@ attention over a paged key-value cache):
                     weight=None, stream=None)
     kda_cache_evict(k_cache, v_cache, block_table, seq_lens, weight, new_lens, kept, budget,
                     sink=0, recent=0, dst_table=None, dst_weight=None, stream=None)
+    kda_page_resize(block_table, seq_lens, new_lens, free_pages, free_state, page_size, out_lens,
+                    out_state, cu_tokens=None, slots=None, positions=None, rows=None, stream=None)
+    kda_qk_norm_rope(q, k, positions, inv_freq, q_out, k_out, eps=1e-6, q_weight=None,
+                     k_weight=None, magnitude=1.0, interleaved=False, v=None, k_cache=None,
+                     v_cache=None, slots=None, stream=None)
 Convenience wrappers ``prefill``, ``decode``, ``linear_prefill``, ``linear_decode``,
-``attn_decode`` and ``cache_evict`` allocate the outputs.
+``attn_decode``, ``cache_evict``, ``page_resize`` and ``qk_norm_rope`` allocate the outputs;
+``rope_frequencies`` makes rotation tables.
 """
 from __future__ import annotations
 
@@ -48,7 +54,7 @@ CHUNK = 32
 
 EXPORTED_SYMBOLS = ("kda_prefill", "kda_prefill_ex", "kda_prefill_workspace_size", "kda_prefill_noalloc", "kda_decode",
                     "kda_decode_ex", "kda_linear_prefill", "kda_linear_prefill_workspace_size", "kda_linear_decode",
-                    "kda_attn_decode", "kda_attn_decode_workspace_size", "kda_cache_evict", "kda_status_string",
+                    "kda_attn_decode", "kda_attn_decode_workspace_size", "kda_cache_evict", "kda_page_resize", "kda_qk_norm_rope", "kda_status_string",
                     "kda_device_status", "kda_abi_version")
 KDA_NOALLOC_SCRATCH_BYTES = 32 << 20  # fixed scratch array of kda_prefill_noalloc
 KDA_DECODE_L2NORM_QK = 1
@@ -115,6 +121,11 @@ def bind(lib):
     lib.kda_cache_evict.restype = ctypes.c_int
     lib.kda_cache_evict.argtypes = [vp, vp, i64, i64, i64, i32, vp, vp, i32, vp, vp, vp, vp, vp, i32, i32, i32, i32,
                                     i32, vp]
+    lib.kda_page_resize.restype = ctypes.c_int
+    lib.kda_page_resize.argtypes = [vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, vp, vp, vp, vp, i32, vp]
+    lib.kda_qk_norm_rope.restype = ctypes.c_int
+    lib.kda_qk_norm_rope.argtypes = [vp, vp, vp, i64, i64, i64, vp, vp, i32, i32, f32, vp, vp, i32, f32, vp, i64, vp, i64,
+                                     vp, vp, i64, i64, i64, i32, vp, i32, i32, i32, vp]
     lib.kda_status_string.restype = ctypes.c_char_p
     lib.kda_status_string.argtypes = [ctypes.c_int]
     lib.kda_device_status.restype = ctypes.c_int
@@ -466,6 +477,35 @@ def kda_cache_evict(k_cache, v_cache, block_table, seq_lens, weight, new_lens, k
         raise KdaError(st, "kda_cache_evict")
 
 
+def kda_page_resize(block_table, seq_lens, new_lens, free_pages, free_state, page_size, out_lens, out_state,
+                    cu_tokens=None, slots=None, positions=None, rows=None, stream=None):
+    """Takes pages for rows of a paged cache that grow from ``seq_lens`` to ``new_lens`` tokens, gives
+    back those of rows that shrink, and maps the new tokens, packed row after row, to cache slots.
+    ``block_table`` int32 [B, max_pages] is written where pages are taken; ``free_pages`` int32
+    [pages] is a ring whose free entries ``free_state`` int32 [2] {first, count} names; ``out_lens``
+    and ``out_state`` are the lengths and the state after the call (may be the tensors before it).
+    Optional: ``cu_tokens`` int32 [B + 1], and for each token ``slots`` int64, ``positions`` and
+    ``rows`` int32, all of one length, -1 / 0 / -1 past the last token. A row for which too few
+    pages are free keeps its length (see include/kda.h)."""
+    st = (_native or _load_native()).page_resize(block_table, seq_lens, new_lens, free_pages, free_state, page_size,
+                                                 out_lens, out_state, cu_tokens, slots, positions, rows, stream)
+    if st != KDA_OK:
+        raise KdaError(st, "kda_page_resize")
+
+
+def kda_qk_norm_rope(q, k, positions, inv_freq, q_out, k_out, eps=1e-6, q_weight=None, k_weight=None, magnitude=1.0,
+                     interleaved=False, v=None, k_cache=None, v_cache=None, slots=None, stream=None):
+    """Norms each head of ``q`` BF16 [T, Hq, 128] and ``k`` BF16 [T, Hkv, 128] (RMS, weights [128] FP32
+    or BF16; None: no norm), rotates the first 2 len(inv_freq) channels by ``positions`` int32 [T]
+    times ``inv_freq`` FP32 (None: no rotation), pairs (i, i + half) or ``interleaved``, and writes
+    ``q_out``, ``k_out`` (or None) and, given ``v``, ``slots`` int64 [T] and the caches [pages, Hkv,
+    page_size, 128], keys and values into the cache. Tokens may be strided (views of one projection)."""
+    st = (_native or _load_native()).qk_norm_rope(q, k, positions, inv_freq, q_out, k_out, eps, q_weight, k_weight,
+                                                  magnitude, interleaved, v, k_cache, v_cache, slots, stream)
+    if st != KDA_OK:
+        raise KdaError(st, "kda_qk_norm_rope")
+
+
 def _allocate_on(stream):
     """Tensors made inside belong to the stream that the call runs on, so that the caching allocator
     neither hands out memory still in use on another stream nor reuses it too early."""
@@ -523,3 +563,53 @@ def cache_evict(k_cache, v_cache, block_table, seq_lens, weight, *, budget, sink
     kda_cache_evict(k_cache, v_cache, block_table, seq_lens, weight, new_lens, kept, budget, sink, recent, dst_table,
                     dst_weight, stream)
     return new_lens, kept
+
+
+def page_resize(block_table, seq_lens, new_lens, free_pages, free_state, page_size, *, max_tokens, stream=None):
+    """Runs ``kda_page_resize`` in place (``seq_lens`` and ``free_state`` become those after the call) and
+    allocates its maps for ``max_tokens`` new tokens; returns (cu_tokens, slots, positions, rows)."""
+    import torch
+    dev = block_table.device
+    with _allocate_on(stream):
+        cu = torch.empty(block_table.shape[0] + 1, dtype=torch.int32, device=dev)
+        slots = torch.empty(max_tokens, dtype=torch.int64, device=dev)
+        positions, rows = (torch.empty(max_tokens, dtype=torch.int32, device=dev) for _ in range(2))
+    kda_page_resize(block_table, seq_lens, new_lens, free_pages, free_state, page_size, seq_lens, free_state, cu, slots,
+                    positions, rows, stream)
+    return cu, slots, positions, rows
+
+
+def qk_norm_rope(q, k, positions, inv_freq, *, eps=1e-6, q_weight=None, k_weight=None, magnitude=1.0, interleaved=False,
+                 v=None, k_cache=None, v_cache=None, slots=None, stream=None):
+    """Allocates ``q_out`` and, without a cache, ``k_out``, and runs ``kda_qk_norm_rope``; returns q_out, or
+    (q_out, k_out)."""
+    import torch
+    with _allocate_on(stream):
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        k_out = None if slots is not None else torch.empty(k.shape, dtype=k.dtype, device=k.device)
+    kda_qk_norm_rope(q, k, positions, inv_freq, q_out, k_out, eps, q_weight, k_weight, magnitude, interleaved, v, k_cache,
+                     v_cache, slots, stream)
+    return q_out if k_out is None else (q_out, k_out)
+
+
+def rope_frequencies(rot_dim, base=10000.0, factor=1.0, original_length=0, slow_turns=1.0, fast_turns=32.0, device="cuda"):
+    """(inv_freq FP32 [rot_dim / 2], magnitude) for ``kda_qk_norm_rope``: base^(-2 i / rot_dim), for contexts ``factor``
+    times as long as a model was trained for. With ``original_length`` (of the training) only the slow waves stretch:
+    those with fewer than ``slow_turns`` turns over it by the whole factor, those with more than ``fast_turns`` not at
+    all, linearly in the turns between, and the magnitude becomes 1 + ln(factor) / 10; without it all of them stretch
+    by the factor."""
+    import math
+    import torch
+    if rot_dim < 0 or rot_dim > HEAD_DIM or rot_dim % 16 != 0:
+        raise ValueError(f"rot_dim: expected a multiple of 16 in [0, {HEAD_DIM}], got {rot_dim}")
+    if not (factor >= 1.0 and base > 0.0 and slow_turns < fast_turns):
+        raise ValueError("expected factor >= 1, base > 0 and slow_turns < fast_turns")
+    f = base ** (-torch.arange(0, rot_dim, 2, dtype=torch.float64) / max(rot_dim, 1))
+    magnitude = 1.0
+    if original_length:
+        keep = ((original_length * f / (2 * math.pi) - slow_turns) / (fast_turns - slow_turns)).clamp(0, 1)
+        f = f * keep + f / factor * (1 - keep)
+        magnitude += 0.1 * math.log(factor)
+    else:
+        f = f / factor
+    return f.to(torch.float32).to(device), magnitude

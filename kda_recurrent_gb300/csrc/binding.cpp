@@ -41,12 +41,16 @@ const at::Tensor &tensor(PyObject *o, const char *name, int64_t dims) {
 }
 
 const char *dtype_name(at::ScalarType type) {
-    return type == at::kBFloat16 ? "torch.bfloat16" : type == at::kFloat ? "torch.float32" : "torch.int32";
+    return type == at::kBFloat16 ? "torch.bfloat16" : type == at::kFloat ? "torch.float32" : type == at::kLong ? "torch.int64" : "torch.int32";
 }
+
+// What a tensor's strides may be: contiguous; [pages, heads, page size, 128], contiguous but for the distance between
+// pages; [tokens, heads, 128], contiguous but for the distance between tokens.
+enum Order { kDense, kPages, kTokens };
 
 // Type, shape, order and device of a tensor; -1 in `shape` takes any extent.
 const at::Tensor &need(PyObject *o, const char *name, at::ScalarType type, std::initializer_list<int64_t> shape, at::Device device,
-                       bool pages = false) {
+                       Order order = kDense) {
     const at::Tensor &t = tensor(o, name);
     if (t.scalar_type() != type) {
         PyObject *const got = PyObject_GetAttrString(o, "dtype");
@@ -68,7 +72,13 @@ const at::Tensor &need(PyObject *o, const char *name, at::ScalarType type, std::
         Py_XDECREF(got);
         throw Raised();
     }
-    if (pages) {  // [pages, heads, page size, 128]: contiguous but for the distance between pages
+    if (order == kTokens) {
+        const at::IntArrayRef s = t.strides();
+        if ((sizes[1] != 1 && s[1] != kHeadDim) || s[2] != 1) {
+            PyErr_Format(PyExc_ValueError, "%s: a token's heads must be contiguous", name);
+            throw Raised();
+        }
+    } else if (order == kPages) {
         const at::IntArrayRef s = t.strides();
         if ((sizes[1] != 1 && s[1] != sizes[2] * kHeadDim) || s[2] != kHeadDim || s[3] != 1) {
             PyErr_Format(PyExc_ValueError, "%s: a page must be contiguous", name);
@@ -171,9 +181,9 @@ struct Cache {
 };
 
 Cache cache_of(PyObject *const *a, at::Device device) {
-    const at::Tensor &k = need(a[0], "k_cache", at::kBFloat16, {-1, -1, -1, kHeadDim}, device, true);
+    const at::Tensor &k = need(a[0], "k_cache", at::kBFloat16, {-1, -1, -1, kHeadDim}, device, kPages);
     const int64_t pages = k.size(0), heads = k.size(1), size = k.size(2);
-    const at::Tensor &v = need(a[1], "v_cache", at::kBFloat16, {pages, heads, size, kHeadDim}, device, true);
+    const at::Tensor &v = need(a[1], "v_cache", at::kBFloat16, {pages, heads, size, kHeadDim}, device, kPages);
     const at::Tensor &lens = need(a[3], "seq_lens", at::kInt, {-1}, device);
     const at::Tensor &table = need(a[2], "block_table", at::kInt, {lens.size(0), -1}, device);
     return {k, v, lens, table, lens.size(0), heads, size, pages, table.size(1)};
@@ -271,6 +281,102 @@ PyObject *cache_evict(PyObject *const *a) {
     });
 }
 
+// (block_table, seq_lens, new_lens, free_pages, free_state, page_size, out_lens, out_state, cu_tokens, slots, positions, rows,
+//  stream)
+PyObject *page_resize(PyObject *const *a) {
+    const at::Device device = tensor(a[0], "block_table", 2).device();
+    const at::Tensor &table = need(a[0], "block_table", at::kInt, {-1, -1}, device);
+    const int64_t B = table.size(0);
+    const at::Tensor &lens = need(a[1], "seq_lens", at::kInt, {B}, device);
+    const at::Tensor &new_lens = need(a[2], "new_lens", at::kInt, {B}, device);
+    const at::Tensor &ring = need(a[3], "free_pages", at::kInt, {-1}, device);
+    const at::Tensor &state = need(a[4], "free_state", at::kInt, {2}, device);
+    const at::Tensor &out_lens = need(a[6], "out_lens", at::kInt, {B}, device);
+    const at::Tensor &out_state = need(a[7], "out_state", at::kInt, {2}, device);
+    int32_t *const cu = optional<int32_t>(a[8], "cu_tokens", at::kInt, {B + 1}, device);
+    int64_t tokens = -1;  // of the maps that are given
+    const char *const names[] = {"slots", "positions", "rows"};
+    void *maps[3];
+    for (int i = 0; i < 3; ++i) {
+        maps[i] = optional(a[9 + i], names[i], i == 0 ? at::kLong : at::kInt, {tokens}, device);
+        if (a[9 + i] != Py_None) tokens = THPVariable_Unpack(a[9 + i]).size(0);
+    }
+    const int32_t size = int_of(a[5], "page_size"), b = int_of(B, "block_table"), width = int_of(table.size(1), "block_table"),
+                  pages = int_of(ring.size(0), "free_pages"), t = tokens < 0 ? 0 : int_of(tokens, "slots");
+    return run(device, a[12], [&](kda_stream_t stream) {
+        return kda_page_resize(address<int32_t>(table), address<int32_t>(lens), address<int32_t>(new_lens), address<int32_t>(out_lens),
+                               address<int32_t>(ring), address<int32_t>(state), address<int32_t>(out_state), pages, size, b, width, cu,
+                               static_cast<int64_t *>(maps[0]), static_cast<int32_t *>(maps[1]), static_cast<int32_t *>(maps[2]), t,
+                               stream);
+    });
+}
+
+// (q, k, positions, inv_freq, q_out, k_out, eps, q_weight, k_weight, magnitude, interleaved, v, k_cache, v_cache, slots, stream)
+PyObject *qk_norm_rope(PyObject *const *a) {
+    const at::Tensor &q = tensor(a[0], "q", 3), &k = tensor(a[1], "k", 3);
+    const at::Device device = q.device();
+    const int64_t T = q.size(0), Hq = q.size(1), Hkv = k.size(1);
+    auto tokens = [&](PyObject *o, const char *name, int64_t heads, void *&base, int64_t &stride) {
+        if (o == Py_None) return;
+        const at::Tensor &t = need(o, name, at::kBFloat16, {T, heads, kHeadDim}, device, kTokens);
+        base = t.data_ptr();
+        stride = T > 1 ? t.stride(0) : heads * kHeadDim;  // (any, for one token)
+    };
+    void *at_q = nullptr, *at_k = nullptr, *at_v = nullptr, *q_out = nullptr, *k_out = nullptr;
+    int64_t qs = 0, ks = 0, vs = 0, qos = 0, kos = 0;
+    tokens(a[0], "q", Hq, at_q, qs);
+    tokens(a[1], "k", Hkv, at_k, ks);
+    if (a[4] == Py_None) tensor(a[4], "q_out");  // (raises)
+    tokens(a[4], "q_out", Hq, q_out, qos);
+    tokens(a[5], "k_out", Hkv, k_out, kos);
+    const int32_t *positions = nullptr;
+    const float *freq = nullptr;
+    int64_t rot = 0;
+    if (a[3] != Py_None) {
+        const at::Tensor &f = need(a[3], "inv_freq", at::kFloat, {-1}, device);
+        freq = address<float>(f);
+        rot = 2 * f.size(0);
+    }
+    if (a[2] != Py_None || rot > 0) positions = address<int32_t>(need(a[2], "positions", at::kInt, {T}, device));
+    int32_t bf16 = -1;
+    const void *weights[2];
+    for (int i = 0; i < 2; ++i) {
+        const char *const name = i == 0 ? "q_weight" : "k_weight";
+        weights[i] = nullptr;
+        if (a[7 + i] == Py_None) continue;
+        const at::ScalarType type = tensor(a[7 + i], name).scalar_type();
+        if ((type != at::kFloat && type != at::kBFloat16) || (bf16 >= 0 && bf16 != (type == at::kBFloat16))) {
+            PyErr_SetString(PyExc_TypeError, "q_weight and k_weight must be both float32 or both bfloat16");
+            throw Raised();
+        }
+        bf16 = type == at::kBFloat16;
+        weights[i] = address(need(a[7 + i], name, type, {kHeadDim}, device));
+    }
+    void *k_cache = nullptr, *v_cache = nullptr;
+    const int64_t *slots = nullptr;
+    int64_t kps = 0, vps = 0, pages = 0, size = 0;
+    if (a[11] != Py_None || a[12] != Py_None || a[13] != Py_None || a[14] != Py_None) {
+        if (a[11] == Py_None) tensor(a[11], "v");  // (raises: all four or none)
+        tokens(a[11], "v", Hkv, at_v, vs);
+        const at::Tensor &kc = need(a[12], "k_cache", at::kBFloat16, {-1, Hkv, -1, kHeadDim}, device, kPages);
+        pages = kc.size(0), size = kc.size(2);
+        const at::Tensor &vc = need(a[13], "v_cache", at::kBFloat16, {pages, Hkv, size, kHeadDim}, device, kPages);
+        slots = address<int64_t>(need(a[14], "slots", at::kLong, {T}, device));
+        k_cache = address(kc), v_cache = address(vc);
+        kps = pages > 1 ? kc.stride(0) : Hkv * size * kHeadDim, vps = pages > 1 ? vc.stride(0) : Hkv * size * kHeadDim;  // (any, for one page)
+    }
+    const float eps = float_of(a[6]), magnitude = float_of(a[9]);
+    const int interleaved = PyObject_IsTrue(a[10]);
+    if (interleaved < 0) throw Raised();
+    const int32_t t = int_of(T, "q"), hq = int_of(Hq, "q"), hkv = int_of(Hkv, "k"), r = int_of(rot, "inv_freq"),
+                  ps = int_of(size, "k_cache");
+    return run(device, a[15], [&](kda_stream_t stream) {
+        return kda_qk_norm_rope(at_q, at_k, at_v, qs, ks, vs, positions, freq, r, interleaved, magnitude, weights[0], weights[1],
+                                bf16 == 1, eps, q_out, qos, k_out, kos, k_cache, v_cache, kps, vps, pages, ps, slots, t, hq, hkv,
+                                stream);
+    });
+}
+
 template <PyObject *(*kCall)(PyObject *const *), int kArgs>
 PyObject *entry(PyObject *, PyObject *const *args, Py_ssize_t n) {
     if (n != kArgs) return PyErr_Format(PyExc_TypeError, "expected %d arguments, got %zd", kArgs, n);
@@ -290,6 +396,7 @@ PyMethodDef method(const char *name) {
 
 PyMethodDef methods[] = {method<linear_prefill, 11>("linear_prefill"), method<linear_decode, 9>("linear_decode"),
                          method<attn_decode, 11>("attn_decode"), method<cache_evict, 13>("cache_evict"),
+                         method<page_resize, 13>("page_resize"), method<qk_norm_rope, 16>("qk_norm_rope"),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "kda_gb300_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

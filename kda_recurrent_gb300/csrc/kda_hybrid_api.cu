@@ -1,5 +1,6 @@
 // C ABI of the operators beside KDA layers (linear attention with a decay for each head,
-// paged attention of one token, cache eviction): argument checks on the host, then dispatch.
+// paged attention of one token, also behind a shared prefix, cache eviction, pages from lengths, norm and
+// rotation of queries and keys): argument checks on the host, then dispatch.
 #include <math.h>
 
 #include "kda_internal.cuh"
@@ -11,6 +12,12 @@ namespace {
 bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 int from_cuda(cudaError_t e) { return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA; }
+
+int32_t shift_of(int32_t page_size) {
+    int32_t shift = 0;
+    while ((1 << shift) < page_size) ++shift;
+    return shift;
+}
 
 // What a cache's shape may be: 32-bit token positions and item counts, 64-bit cache offsets.
 int cache_shape(int32_t batch, int32_t num_kv_heads, int32_t max_pages, int32_t page_size) {
@@ -63,8 +70,7 @@ int paged_cache(PagedCache *c, void *k_cache, void *v_cache, int64_t k_page_stri
     c->num_kv_heads = num_kv_heads;
     c->max_pages = max_pages;
     c->page_size = page_size;
-    c->page_shift = 0;
-    while ((1 << c->page_shift) < page_size) ++c->page_shift;
+    c->page_shift = shift_of(page_size);
     c->capacity = max_pages * page_size;
     return KDA_OK;
 }
@@ -231,6 +237,118 @@ int kda_cache_evict(void *k_cache, void *v_cache, int64_t k_page_stride, int64_t
     a.recent = recent;
     if (device_status_ptr(&a.status) != cudaSuccess) return KDA_ERR_CUDA;
     return from_cuda(launch_cache_evict(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int kda_page_resize(int32_t *block_table, const int32_t *seq_lens, const int32_t *new_lens, int32_t *out_lens,
+                    int32_t *free_pages, const int32_t *free_state, int32_t *out_state, int32_t num_pages,
+                    int32_t page_size, int32_t batch, int32_t max_pages, int32_t *cu_tokens, int64_t *slots,
+                    int32_t *positions, int32_t *rows, int32_t max_tokens, kda_stream_t stream) {
+    if (num_pages < 1 || max_tokens < 0) return KDA_ERR_INVALID_ARG;
+    const int bad = cache_shape(batch, 1, max_pages, page_size);
+    if (bad != KDA_OK) return bad;
+    if (num_pages > 0x3fffffff) return KDA_ERR_UNSUPPORTED;
+    if (!free_pages || !free_state || !out_state) return KDA_ERR_INVALID_ARG;
+    if (batch > 0 && (!block_table || !seq_lens || !new_lens || !out_lens)) return KDA_ERR_INVALID_ARG;
+    const void *p4[] = {block_table, seq_lens, new_lens, out_lens, free_pages, free_state, out_state, cu_tokens, positions, rows};
+    for (const void *p : p4)
+        if (!aligned(p, 4)) return KDA_ERR_MISALIGNED;
+    if (!aligned(slots, 8)) return KDA_ERR_MISALIGNED;
+    PageResizeArgs a;
+    a.block_table = block_table;
+    a.seq_lens = seq_lens;
+    a.new_lens = new_lens;
+    a.out_lens = out_lens;
+    a.free_pages = free_pages;
+    a.free_state = free_state;
+    a.out_state = out_state;
+    a.cu_tokens = cu_tokens;
+    a.slots = slots;
+    a.positions = positions;
+    a.rows = rows;
+    a.num_pages = num_pages;
+    a.page_size = page_size;
+    a.page_shift = shift_of(page_size);
+    a.batch = batch;
+    a.max_pages = max_pages;
+    a.capacity = max_pages * page_size;
+    a.has_maps = slots || positions || rows;
+    a.max_tokens = a.has_maps ? max_tokens : 0;
+    if (device_status_ptr(&a.status) != cudaSuccess) return KDA_ERR_CUDA;
+    return from_cuda(launch_page_resize(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int kda_qk_norm_rope(const void *q, const void *k, const void *v, int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                     const int32_t *positions, const float *inv_freq, int32_t rot_dim, int32_t interleaved,
+                     float magnitude, const void *q_weight, const void *k_weight, int32_t weight_bf16, float eps,
+                     void *q_out, int64_t q_out_stride, void *k_out, int64_t k_out_stride, void *k_cache, void *v_cache,
+                     int64_t k_page_stride, int64_t v_page_stride, int64_t num_pages, int32_t page_size,
+                     const int64_t *slots, int32_t tokens, int32_t num_q_heads, int32_t num_kv_heads,
+                     kda_stream_t stream) {
+    if (tokens < 0 || num_q_heads < 1 || num_kv_heads < 1 || rot_dim < 0 || rot_dim > kHeadDim) return KDA_ERR_INVALID_ARG;
+    if ((interleaved != 0 && interleaved != 1) || (weight_bf16 != 0 && weight_bf16 != 1)) return KDA_ERR_INVALID_ARG;
+    if (!isfinite(magnitude) || !isfinite(eps) || eps < 0.0f) return KDA_ERR_INVALID_ARG;
+    if (rot_dim % 16 != 0 || num_q_heads > 0xffff || num_kv_heads > 0xffff) return KDA_ERR_UNSUPPORTED;
+    const bool cached = slots != nullptr || k_cache != nullptr || v_cache != nullptr;
+    const int64_t strides[] = {q_stride, k_stride, v_stride, q_out_stride, k_out_stride};
+    const int32_t heads[] = {num_q_heads, num_kv_heads, num_kv_heads, num_q_heads, num_kv_heads};
+    const bool there[] = {true, true, cached, true, k_out != nullptr};
+    for (int i = 0; i < 5; ++i) {
+        if (!there[i]) continue;
+        if (strides[i] < (int64_t)heads[i] * kHeadDim) return KDA_ERR_INVALID_ARG;
+        if (strides[i] % 8 != 0) return KDA_ERR_MISALIGNED;
+        if (strides[i] > ((int64_t)1 << 60) / (tokens > 0 ? tokens : 1)) return KDA_ERR_UNSUPPORTED;
+    }
+    if (cached) {
+        const int bad = cache_shape(0, num_kv_heads, 1, page_size);
+        if (bad != KDA_OK) return bad;
+        if (num_pages < 1) return KDA_ERR_INVALID_ARG;
+        const int64_t page = (int64_t)num_kv_heads * page_size * kHeadDim;
+        if (k_page_stride < page || v_page_stride < page) return KDA_ERR_INVALID_ARG;
+        if (k_page_stride % 8 != 0 || v_page_stride % 8 != 0) return KDA_ERR_MISALIGNED;
+        const int64_t stride = k_page_stride > v_page_stride ? k_page_stride : v_page_stride;
+        if (num_pages > 0x7fffffffLL || stride > ((int64_t)1 << 60) / num_pages) return KDA_ERR_UNSUPPORTED;
+    } else if (k_out == nullptr) {
+        return KDA_ERR_INVALID_ARG;  // the keys would go nowhere
+    }
+    if (tokens == 0) return KDA_OK;
+    if (!q || !k || !q_out || (cached && (!v || !slots || !k_cache || !v_cache))) return KDA_ERR_INVALID_ARG;
+    if (rot_dim > 0 && (!positions || !inv_freq)) return KDA_ERR_INVALID_ARG;
+    const void *p16[] = {q, k, v, q_out, k_out, k_cache, v_cache, q_weight, k_weight};
+    for (const void *p : p16)
+        if (!aligned(p, 16)) return KDA_ERR_MISALIGNED;
+    if (!aligned(positions, 4) || !aligned(inv_freq, 4) || !aligned(slots, 8)) return KDA_ERR_MISALIGNED;
+    QkRopeArgs a;
+    a.q = static_cast<const __nv_bfloat16 *>(q);
+    a.k = static_cast<const __nv_bfloat16 *>(k);
+    a.v = static_cast<const __nv_bfloat16 *>(v);
+    a.q_stride = q_stride;
+    a.k_stride = k_stride;
+    a.v_stride = v_stride;
+    a.q_out_stride = q_out_stride;
+    a.k_out_stride = k_out_stride;
+    a.positions = positions;
+    a.inv_freq = inv_freq;
+    a.q_weight = q_weight;
+    a.k_weight = k_weight;
+    a.q_out = static_cast<__nv_bfloat16 *>(q_out);
+    a.k_out = static_cast<__nv_bfloat16 *>(k_out);
+    a.k_cache = static_cast<__nv_bfloat16 *>(k_cache);
+    a.v_cache = static_cast<__nv_bfloat16 *>(v_cache);
+    a.k_page_stride = k_page_stride;
+    a.v_page_stride = v_page_stride;
+    a.num_pages = num_pages;
+    a.slots = slots;
+    a.page_shift = cached ? shift_of(page_size) : 0;
+    a.tokens = tokens;
+    a.num_q_heads = num_q_heads;
+    a.num_kv_heads = num_kv_heads;
+    a.rot = rot_dim;
+    a.interleaved = interleaved;
+    a.weight_bf16 = weight_bf16;
+    a.eps = eps;
+    a.magnitude = magnitude;
+    if (device_status_ptr(&a.status) != cudaSuccess) return KDA_ERR_CUDA;
+    return from_cuda(launch_qk_rope(a, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -155,6 +155,36 @@ struct CacheEvictArgs {
     DeviceStatus *status;
 };
 
+// Norm and rotation of queries and keys, keys and values into the cache's slots.
+struct QkRopeArgs {
+    const __nv_bfloat16 *q, *k, *v;
+    int64_t q_stride, k_stride, v_stride, q_out_stride, k_out_stride;  // elements between tokens
+    const int32_t *positions;
+    const float *inv_freq;
+    const void *q_weight, *k_weight;  // [128] FP32 or BF16, or NULL
+    __nv_bfloat16 *q_out, *k_out;
+    __nv_bfloat16 *k_cache, *v_cache;
+    int64_t k_page_stride, v_page_stride, num_pages;
+    const int64_t *slots;  // NULL: no cache
+    int32_t page_shift;
+    int32_t tokens, num_q_heads, num_kv_heads, rot, interleaved, weight_bf16;
+    float eps, magnitude;
+    DeviceStatus *status;
+};
+
+struct PageResizeArgs {
+    int32_t *block_table;
+    const int32_t *seq_lens, *new_lens;
+    int32_t *out_lens, *free_pages;
+    const int32_t *free_state;
+    int32_t *out_state;
+    int32_t *cu_tokens;
+    int64_t *slots;
+    int32_t *positions, *rows;
+    int32_t num_pages, page_size, page_shift, batch, max_pages, capacity, max_tokens, has_maps;
+    DeviceStatus *status;
+};
+
 // Token count of a row, clamped into range; `report` (one caller per row) records a bad value.
 __device__ __forceinline__ int row_length(const PagedCache &c, int b, DeviceStatus *st, bool report) {
     const int n = c.seq_lens[b];
@@ -167,6 +197,8 @@ cudaError_t launch_linear_prefill(const LinearPrefillArgs &a, cudaStream_t strea
 cudaError_t launch_linear_decode(const LinearDecodeArgs &a, cudaStream_t stream);
 cudaError_t launch_attn_decode(const AttnDecodeArgs &a, cudaStream_t stream);
 cudaError_t launch_cache_evict(const CacheEvictArgs &a, cudaStream_t stream);
+cudaError_t launch_qk_rope(const QkRopeArgs &a, cudaStream_t stream);
+cudaError_t launch_page_resize(const PageResizeArgs &a, cudaStream_t stream);
 int64_t linear_prefill_workspace_bytes(int32_t num_seqs, int32_t total_tokens, int32_t num_heads, int32_t sms);
 int64_t attn_decode_workspace_bytes(int32_t batch, int32_t num_q_heads, int32_t num_kv_heads, int64_t capacity,
                                     bool with_weight, int32_t sms);

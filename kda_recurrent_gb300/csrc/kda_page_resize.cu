@@ -1,0 +1,264 @@
+// Pages of a key-value cache handed out on the GPU as rows grow and shrink, and the slots of the new tokens
+// (sm_103a).
+//
+// A row of n tokens holds ceil(n / page_size) pages. Free pages lie in a ring [first, first + count); rows that
+// grow take from its front, in row order, rows that shrink give back to its end, so that what a call takes and
+// what it gives never meet. Where each row's pages and tokens begin follows from prefix sums over the rows. One
+// launch does all of it: every CTA of one cluster forms the sums of 1024 rows at a time by itself (8 bytes a row)
+// and handles its part of the tokens and pages, which it finds in the sums by bisection; the cluster's barrier
+// lies between the last read of a length and its update in place. Nothing here is wide: it is a chain of
+// dependent reads (lengths, sums, table or ring, map), and the launch is most of a small call.
+//
+// Pages given back are compacted (a missing page of the table is not given back) in table order: each thread
+// counts four entries, and the CTAs exchange their counts through distributed shared memory.
+#include <algorithm>
+
+#include "kda_dependent.cuh"
+#include "kda_internal.cuh"
+#include "kda_mma.cuh"
+
+namespace kda {
+namespace {
+
+constexpr int kMaxThreads = 1024;  // rows at a time, too
+constexpr int kMaxCluster = 8;
+constexpr int kGive = 4;  // entries of a thread at a time
+constexpr uint32_t kMost = 0x7fffffffu;
+
+// Sums of counts that stop at 2^31 - 1 (adding so is associative, too).
+__device__ __forceinline__ uint32_t add(uint32_t x, uint32_t y) { return min(x + y, kMost); }
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+    return r;
+}
+// All threads of the cluster; what they wrote before is visible to all of them behind it.
+__device__ __forceinline__ void cluster_barrier() {
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void store_remote(const void *local, uint32_t rank, uint32_t x) {
+    uint32_t addr;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(addr) : "r"(smem_addr(local)), "r"(rank));
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(x) : "memory");
+}
+
+// The first of n inclusive sums above x (there is one).
+__device__ __forceinline__ int row_of(const uint32_t *sums, int n, uint32_t x) {
+    int lo = 0, hi = n - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (sums[mid] > x) hi = mid;
+        else lo = mid + 1;
+    }
+    return lo;
+}
+
+__global__ void __launch_bounds__(kMaxThreads) kda_page_resize_kernel(const PageResizeArgs p) {
+    __shared__ uint32_t s_tok[kMaxThreads], s_take[kMaxThreads], s_give[kMaxThreads];  // inclusive sums of a chunk's rows
+    __shared__ int32_t s_old[kMaxThreads], s_new[kMaxThreads];
+    __shared__ uint32_t s_warp[3][32];
+    __shared__ uint32_t s_given[2][kMaxCluster];
+    const int threads = blockDim.x, warps = threads >> 5, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = (int)cluster_rank(), ctas = (int)cluster_size();
+    const int me = rank * threads + threadIdx.x, all = ctas * threads;
+    const int F = p.num_pages, ps = p.page_size;
+    wait_for_prior();
+    allow_next();
+    int first = p.free_state[0], count = p.free_state[1];
+    if (first < 0 || first >= F || count < 0 || count > F) {
+        if (me == 0) report_error(p.status, KDA_ERR_DEVICE_INPUT, -1);
+        first = 0, count = 0;
+    }
+    auto pages = [&](int n) { return (uint32_t)((n + ps - 1) >> p.page_shift); };
+    auto valid = [&](int page, int row) {  // a page of the table or the ring; -1 for one that does not exist
+        if (page >= F) report_error(p.status, KDA_ERR_DEVICE_INPUT, row);
+        return page >= 0 && page < F ? page : -1;
+    };
+    auto free_page = [&](uint32_t i, int row) {
+        uint32_t at = (uint32_t)first + i;  // (both below F)
+        if (at >= (uint32_t)F) at -= F;
+        const int page = p.free_pages[at];
+        if (page < 0) report_error(p.status, KDA_ERR_DEVICE_INPUT, row);
+        return valid(page, row);
+    };
+    if (me == 0 && p.cu_tokens) p.cu_tokens[0] = 0;
+    if (ctas > 1) cluster_barrier();  // every CTA has begun: its shared memory may be written
+
+    uint32_t tokens = 0, taken = 0, used = 0, given = 0;  // of the rows before the chunk; used: pages really taken
+    int round = 0;
+    for (int r0 = 0; r0 < p.batch; r0 += threads) {
+        const int rows = min(threads, p.batch - r0), r = r0 + threadIdx.x;
+        int n = 0, m = 0;
+        if ((int)threadIdx.x < rows) {
+            n = p.seq_lens[r], m = p.new_lens[r];
+            if (n < 0 || n > p.capacity || m < 0 || m > p.capacity) {
+                if (rank == 0) report_error(p.status, KDA_ERR_DEVICE_INPUT, r);
+                n = min(max(n, 0), p.capacity), m = min(max(m, 0), p.capacity);
+            }
+        }
+        const uint32_t held = pages(n), want = pages(m);
+        uint32_t x[3] = {m > n ? (uint32_t)(m - n) : 0u, want > held ? want - held : 0u, held > want ? held - want : 0u};
+        const uint32_t my_tokens = x[0], my_take = x[1];
+#pragma unroll
+        for (int i = 0; i < 3; ++i) {
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const uint32_t y = __shfl_up_sync(0xffffffffu, x[i], o);
+                if (lane >= o) x[i] = add(x[i], y);
+            }
+            if (lane == 31) s_warp[i][warp] = x[i];
+        }
+        __syncthreads();
+        uint32_t total[3];
+#pragma unroll
+        for (int i = 0; i < 3; ++i) {  // (the warps' sums, by every warp)
+            uint32_t y = lane < warps ? s_warp[i][lane] : 0;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const uint32_t z = __shfl_up_sync(0xffffffffu, y, o);
+                if (lane >= o) y = add(y, z);
+            }
+            total[i] = __shfl_sync(0xffffffffu, y, 31);
+            const uint32_t before = __shfl_sync(0xffffffffu, y, max(warp - 1, 0));
+            if (warp > 0) x[i] = add(x[i], before);
+        }
+        s_tok[threadIdx.x] = x[0], s_take[threadIdx.x] = x[1], s_give[threadIdx.x] = x[2];
+        s_old[threadIdx.x] = n, s_new[threadIdx.x] = m;
+        // in order: the first row whose pages are not there, and all later ones that need pages, get none
+        const bool served = my_take == 0 || add(taken, x[1]) <= (uint32_t)count;
+        const uint32_t left = (uint32_t)count - min(taken, (uint32_t)count);
+        if (!served && rank == 0) report_error(p.status, KDA_ERR_DEVICE_INPUT, r);
+        if (rank == 0 && (int)threadIdx.x < rows && p.cu_tokens) p.cu_tokens[r + 1] = (int)add(tokens, x[0]);
+        if (rank == 0 && my_tokens > 0 && p.has_maps && add(tokens, x[0]) > (uint32_t)p.max_tokens)
+            report_error(p.status, KDA_ERR_DEVICE_INPUT, r);
+        __syncthreads();
+
+        // ---- pages taken
+        const uint32_t takes = min(total[1], left);
+        for (uint32_t i = me; i < takes; i += all) {
+            const int row = row_of(s_take, rows, i);
+            if (s_take[row] > left) continue;  // the row that does not fit
+            const uint32_t have = pages(s_old[row]), before = row > 0 ? s_take[row - 1] : 0;
+            p.block_table[(size_t)(r0 + row) * p.max_pages + have + (i - before)] = free_page(taken + i, r0 + row);
+        }
+        // ---- slots of the new tokens
+        if (p.has_maps) {
+            const uint32_t room = (uint32_t)p.max_tokens - min(tokens, (uint32_t)p.max_tokens), here = min(total[0], room);
+            for (uint32_t i = me; i < here; i += all) {
+                const int row = row_of(s_tok, rows, i);
+                const uint32_t before = row > 0 ? s_tok[row - 1] : 0, have = pages(s_old[row]);
+                const int j = s_old[row] + (int)(i - before);
+                const uint32_t pg = (uint32_t)j >> p.page_shift, take0 = row > 0 ? s_take[row - 1] : 0;
+                const bool fits = pages(s_new[row]) <= have || s_take[row] <= left;
+                if (p.slots) {
+                    int page = -1;
+                    if (fits) page = pg < have ? valid(p.block_table[(size_t)(r0 + row) * p.max_pages + pg], r0 + row)
+                                               : free_page(taken + take0 + (pg - have), r0 + row);
+                    p.slots[tokens + i] = page < 0 ? -1 : ((int64_t)page << p.page_shift) + (j & (ps - 1));
+                }
+                if (p.positions) p.positions[tokens + i] = j;
+                if (p.rows) p.rows[tokens + i] = r0 + row;
+            }
+        }
+        // ---- pages given back, behind the ring's end
+        for (uint32_t base = 0; base < total[2]; base += (uint32_t)all * kGive, ++round) {
+            int page[kGive], mine = 0, row[kGive];
+#pragma unroll
+            for (int e = 0; e < kGive; ++e) {
+                const uint32_t i = base + (uint32_t)me * kGive + e;
+                page[e] = -1, row[e] = 0;
+                if (i < total[2]) {
+                    row[e] = row_of(s_give, rows, i);
+                    const uint32_t before = row[e] > 0 ? s_give[row[e] - 1] : 0;
+                    page[e] = valid(p.block_table[(size_t)(r0 + row[e]) * p.max_pages + pages(s_new[row[e]]) + (i - before)], r0 + row[e]);
+                }
+                mine += page[e] >= 0;
+            }
+            uint32_t sum = mine;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const uint32_t y = __shfl_up_sync(0xffffffffu, sum, o);
+                if (lane >= o) sum += y;
+            }
+            __syncthreads();  // (s_warp has been read)
+            if (lane == 31) s_warp[0][warp] = sum;
+            __syncthreads();
+            uint32_t block = 0, at = given + sum - mine;
+            for (int w = 0; w < warps; ++w) {
+                if (w < warp) at += s_warp[0][w];
+                block += s_warp[0][w];
+            }
+            if (ctas > 1) {
+                if ((int)threadIdx.x < ctas) store_remote(&s_given[round & 1][rank], threadIdx.x, block);
+                cluster_barrier();
+                block = 0;
+                for (int c = 0; c < ctas; ++c) {
+                    if (c < rank) at += s_given[round & 1][c];
+                    block += s_given[round & 1][c];
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < kGive; ++e) {
+                if (page[e] < 0) continue;
+                if (at < (uint32_t)(F - count)) {
+                    uint32_t to = (uint32_t)first + count + at;
+                    while (to >= (uint32_t)F) to -= F;  // (at most twice)
+                    p.free_pages[to] = page[e];
+                } else {  // more pages than there are: one was given back twice
+                    report_error(p.status, KDA_ERR_DEVICE_INPUT, r0 + row[e]);
+                }
+                ++at;
+            }
+            given = min(given + block, (uint32_t)(F - count));
+        }
+        // ---- the rows' new lengths, when no CTA reads the old ones any more
+        const uint32_t end = add(taken, x[1]);
+        const int best = served && my_take > 0 ? (int)end : 0;
+        if (ctas > 1) cluster_barrier();
+        if (rank == 0 && (int)threadIdx.x < rows) p.out_lens[r] = served ? m : n;
+        // pages really taken: the sum at the last row that was served
+        int top = best;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+        __syncthreads();  // (s_warp and the chunk's sums have been read)
+        if (lane == 0) s_warp[0][warp] = (uint32_t)top;
+        __syncthreads();
+        for (int w = 0; w < warps; ++w) used = max(used, s_warp[0][w]);
+        tokens = add(tokens, total[0]);
+        taken = add(taken, total[1]);
+        __syncthreads();
+    }
+    if (p.has_maps) {
+        for (uint32_t i = tokens + me; i < (uint32_t)p.max_tokens; i += all) {
+            if (p.slots) p.slots[i] = -1;
+            if (p.positions) p.positions[i] = 0;
+            if (p.rows) p.rows[i] = -1;
+        }
+    }
+    if (ctas > 1) cluster_barrier();  // the state has been read
+    else __syncthreads();
+    if (me == 0) {
+        uint32_t at = (uint32_t)first + used;
+        if (at >= (uint32_t)F) at -= F;
+        p.out_state[0] = (int)at;
+        p.out_state[1] = (int)((uint32_t)count - used + given);
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_page_resize(const PageResizeArgs &p, cudaStream_t stream) {
+    const int threads = p.batch <= 256 && p.max_tokens <= 1024 ? 256 : kMaxThreads;
+    int ctas = 1;
+    while (ctas < kMaxCluster && (int64_t)ctas * 4 * kMaxThreads < p.max_tokens) ctas *= 2;
+    return launch_clusters((unsigned)ctas, kda_page_resize_kernel, dim3((unsigned)ctas), (unsigned)threads, 0, stream, p);
+}
+
+}  // namespace kda
