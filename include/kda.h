@@ -247,7 +247,8 @@ KDA_API int kda_decode_ex(const void *q, const void *k, const void *v, const voi
  * head (kda_linear_prefill, kda_linear_decode), attention of one new token over a paged
  * key-value cache (kda_attn_decode) and eviction from that cache (kda_cache_evict). Around that
  * attention: pages for growing and shrinking rows (kda_page_resize), norm and rotation of queries and
- * keys on their way into the cache (kda_qk_norm_rope).
+ * keys on their way into the cache (kda_qk_norm_rope), and the attention of rows that share a long
+ * prefix (kda_attn_prefix_decode).
  */
 
 /*
@@ -374,6 +375,41 @@ KDA_API int kda_cache_evict(void *k_cache, void *v_cache, int64_t k_page_stride,
                             const float *weight, float *dst_weight, int32_t *new_lens, int32_t *kept,
                             int32_t batch, int32_t num_kv_heads, int32_t budget, int32_t sink,
                             int32_t recent, kda_stream_t stream);
+
+/*
+ * kda_attn_prefix_decode -- kda_attn_decode for rows that share the first tokens of their caches:
+ * what a group of rows shares is read once for all of them. Rows cu_groups[g] .. cu_groups[g + 1]
+ * - 1 hold the same first prefix_lens[g] tokens, as every row's own table says by pointing to the
+ * same pages, or to pages of the same contents. The result is that of kda_attn_decode on the same
+ * tables, up to rounding: any tokens of the prefix may be read through the table of one of its
+ * rows (of at least prefix_lens[g] tokens), or through each row's own.
+ *   cu_groups    int32 [num_groups + 1], device, non-decreasing, within [0, batch]; rows outside
+ *                of them share nothing. Other values are recorded as KDA_ERR_DEVICE_INPUT, and
+ *                then nothing is taken as shared.
+ *   prefix_lens  int32 [num_groups], device; a value outside [0, max_pages * page_size] is
+ *                clamped and recorded. A row shorter than its group's prefix (a padding row of no
+ *                tokens, say) stands for itself.
+ *   workspace    at least kda_attn_prefix_decode_workspace_size(...) bytes, 16-byte aligned.
+ *                Contents on entry do not matter; calls sharing one must not overlap.
+ *   All other arguments as for kda_attn_decode.
+ * Whole tiles of 128 shared tokens of a group of two rows or more are computed together, with
+ * probabilities rounded to BF16 (and their sum formed before). A value that is not finite in such
+ * a tile reaches its own channel of the group's rows. Equal inputs give equal bits.
+ */
+KDA_API int kda_attn_prefix_decode(const void *q, const void *k_cache, const void *v_cache,
+                                   int64_t k_page_stride, int64_t v_page_stride, int64_t num_pages,
+                                   int32_t page_size, const int32_t *block_table, int32_t max_pages,
+                                   const int32_t *seq_lens, const int32_t *cu_groups,
+                                   const int32_t *prefix_lens, int32_t num_groups, void *out, float *lse,
+                                   int32_t batch, int32_t num_q_heads, int32_t num_kv_heads, float scale,
+                                   void *workspace, int64_t workspace_bytes, kda_stream_t stream);
+
+/* kda_attn_prefix_decode_workspace_size -- bytes of workspace for a call of this shape. sm_count 0
+ * asks the current device; > 0 is pure host arithmetic. Sizes that the call refuses are refused
+ * here with the same status (negative). */
+KDA_API int64_t kda_attn_prefix_decode_workspace_size(int32_t batch, int32_t num_q_heads, int32_t num_kv_heads,
+                                                      int32_t max_pages, int32_t page_size,
+                                                      int32_t num_groups, int32_t sm_count);
 
 /*
  * kda_page_resize -- pages of a paged key-value cache handed out as rows grow and shrink, and the

@@ -21,13 +21,16 @@ attention over a paged key-value cache):
                     weight=None, stream=None)
     kda_cache_evict(k_cache, v_cache, block_table, seq_lens, weight, new_lens, kept, budget,
                     sink=0, recent=0, dst_table=None, dst_weight=None, stream=None)
+    kda_attn_prefix_decode(q, k_cache, v_cache, block_table, seq_lens, cu_groups, prefix_lens, out,
+                           scale, workspace, lse=None, stream=None)
     kda_page_resize(block_table, seq_lens, new_lens, free_pages, free_state, page_size, out_lens,
                     out_state, cu_tokens=None, slots=None, positions=None, rows=None, stream=None)
     kda_qk_norm_rope(q, k, positions, inv_freq, q_out, k_out, eps=1e-6, q_weight=None,
                      k_weight=None, magnitude=1.0, interleaved=False, v=None, k_cache=None,
                      v_cache=None, slots=None, stream=None)
 Convenience wrappers ``prefill``, ``decode``, ``linear_prefill``, ``linear_decode``,
-``attn_decode``, ``cache_evict``, ``page_resize`` and ``qk_norm_rope`` allocate the outputs;
+``attn_decode``, ``cache_evict``, ``attn_prefix_decode``, ``page_resize`` and ``qk_norm_rope``
+allocate the outputs;
 ``rope_frequencies`` makes rotation tables.
 """
 from __future__ import annotations
@@ -54,7 +57,8 @@ CHUNK = 32
 
 EXPORTED_SYMBOLS = ("kda_prefill", "kda_prefill_ex", "kda_prefill_workspace_size", "kda_prefill_noalloc", "kda_decode",
                     "kda_decode_ex", "kda_linear_prefill", "kda_linear_prefill_workspace_size", "kda_linear_decode",
-                    "kda_attn_decode", "kda_attn_decode_workspace_size", "kda_cache_evict", "kda_page_resize", "kda_qk_norm_rope", "kda_status_string",
+                    "kda_attn_decode", "kda_attn_decode_workspace_size", "kda_cache_evict", "kda_attn_prefix_decode", "kda_attn_prefix_decode_workspace_size",
+                    "kda_page_resize", "kda_qk_norm_rope", "kda_status_string",
                     "kda_device_status", "kda_abi_version")
 KDA_NOALLOC_SCRATCH_BYTES = 32 << 20  # fixed scratch array of kda_prefill_noalloc
 KDA_DECODE_L2NORM_QK = 1
@@ -121,6 +125,11 @@ def bind(lib):
     lib.kda_cache_evict.restype = ctypes.c_int
     lib.kda_cache_evict.argtypes = [vp, vp, i64, i64, i64, i32, vp, vp, i32, vp, vp, vp, vp, vp, i32, i32, i32, i32,
                                     i32, vp]
+    lib.kda_attn_prefix_decode.restype = ctypes.c_int
+    lib.kda_attn_prefix_decode.argtypes = [vp, vp, vp, i64, i64, i64, i32, vp, i32, vp, vp, vp, i32, vp, vp, i32, i32, i32,
+                                           f32, vp, i64, vp]
+    lib.kda_attn_prefix_decode_workspace_size.restype = ctypes.c_int64
+    lib.kda_attn_prefix_decode_workspace_size.argtypes = [i32, i32, i32, i32, i32, i32, i32]
     lib.kda_page_resize.restype = ctypes.c_int
     lib.kda_page_resize.argtypes = [vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, vp, vp, vp, vp, i32, vp]
     lib.kda_qk_norm_rope.restype = ctypes.c_int
@@ -477,6 +486,36 @@ def kda_cache_evict(k_cache, v_cache, block_table, seq_lens, weight, new_lens, k
         raise KdaError(st, "kda_cache_evict")
 
 
+def kda_attn_prefix_decode(q, k_cache, v_cache, block_table, seq_lens, cu_groups, prefix_lens, out, scale, workspace,
+                           lse=None, stream=None):
+    """``kda_attn_decode`` for rows that share the first tokens of their caches: rows ``cu_groups[g]`` ..
+    ``cu_groups[g + 1] - 1`` (int32 [G + 1]) hold the same first ``prefix_lens[g]`` (int32 [G]) tokens,
+    which their own tables point to; they are read once for all of them. Same result, up to rounding.
+    ``workspace``: attn_prefix_decode_workspace."""
+    st = (_native or _load_native()).attn_prefix_decode(q, k_cache, v_cache, block_table, seq_lens, cu_groups, prefix_lens,
+                                                        out, scale, workspace, lse, stream)
+    if st != KDA_OK:
+        raise KdaError(st, "kda_attn_prefix_decode")
+
+
+def kda_attn_prefix_decode_workspace_size(batch, num_q_heads, num_kv_heads, max_pages, page_size, num_groups,
+                                          sm_count=0) -> int:
+    """Workspace bytes of kda_attn_prefix_decode for this shape; sm_count 0 asks the current device."""
+    n = load().kda_attn_prefix_decode_workspace_size(int(batch), int(num_q_heads), int(num_kv_heads), int(max_pages),
+                                                     int(page_size), int(num_groups), int(sm_count))
+    if n < 0:
+        raise KdaError(int(n), "kda_attn_prefix_decode_workspace_size")
+    return int(n)
+
+
+def attn_prefix_decode_workspace(batch, num_q_heads, num_kv_heads, max_pages, page_size, num_groups, device):
+    """A uint8 device tensor sized for kda_attn_prefix_decode on `device`."""
+    import torch
+    with torch.cuda.device(device):
+        n = kda_attn_prefix_decode_workspace_size(batch, num_q_heads, num_kv_heads, max_pages, page_size, num_groups)
+    return torch.empty(max(n, 16), dtype=torch.uint8, device=device)
+
+
 def kda_page_resize(block_table, seq_lens, new_lens, free_pages, free_state, page_size, out_lens, out_state,
                     cu_tokens=None, slots=None, positions=None, rows=None, stream=None):
     """Takes pages for rows of a paged cache that grow from ``seq_lens`` to ``new_lens`` tokens, gives
@@ -563,6 +602,24 @@ def cache_evict(k_cache, v_cache, block_table, seq_lens, weight, *, budget, sink
     kda_cache_evict(k_cache, v_cache, block_table, seq_lens, weight, new_lens, kept, budget, sink, recent, dst_table,
                     dst_weight, stream)
     return new_lens, kept
+
+
+def attn_prefix_decode(q, k_cache, v_cache, block_table, seq_lens, cu_groups, prefix_lens, *, scale, want_lse=False,
+                       workspace=None, stream=None):
+    """Allocates ``out`` (and ``lse``, and a workspace when none is given) and runs
+    ``kda_attn_prefix_decode``; returns out, or (out, lse)."""
+    import torch
+    B, Hq, _ = q.shape
+    _require_cuda(q.device)
+    with _allocate_on(stream):
+        out = torch.empty_like(q)
+        lse = torch.empty(B, Hq, dtype=torch.float32, device=q.device) if want_lse else None
+        if workspace is None:
+            workspace = attn_prefix_decode_workspace(B, Hq, k_cache.shape[1], block_table.shape[1], k_cache.shape[2],
+                                                     prefix_lens.shape[0], q.device)
+    kda_attn_prefix_decode(q, k_cache, v_cache, block_table, seq_lens, cu_groups, prefix_lens, out, scale, workspace, lse,
+                           stream)
+    return (out, lse) if want_lse else out
 
 
 def page_resize(block_table, seq_lens, new_lens, free_pages, free_state, page_size, *, max_tokens, stream=None):

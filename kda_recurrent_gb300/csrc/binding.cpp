@@ -281,6 +281,29 @@ PyObject *cache_evict(PyObject *const *a) {
     });
 }
 
+// (q, k_cache, v_cache, block_table, seq_lens, cu_groups, prefix_lens, out, scale, workspace, lse, stream)
+PyObject *attn_prefix_decode(PyObject *const *a) {
+    const at::Tensor &q = tensor(a[0], "q", 3);
+    const at::Device device = q.device();
+    const Cache c = cache_of(a + 1, device);
+    const int64_t Hq = q.size(1);
+    need(a[0], "q", at::kBFloat16, {c.batch, Hq, kHeadDim}, device);
+    const at::Tensor &prefix = need(a[6], "prefix_lens", at::kInt, {-1}, device);
+    const at::Tensor &groups = need(a[5], "cu_groups", at::kInt, {prefix.size(0) + 1}, device);
+    const at::Tensor &out = need(a[7], "out", at::kBFloat16, {c.batch, Hq, kHeadDim}, device);
+    float *const lse = optional<float>(a[10], "lse", at::kFloat, {c.batch, Hq}, device);
+    const Workspace ws = workspace_of(a[9], device);
+    const float scale = float_of(a[8]);
+    const int32_t size = int_of(c.page_size, "k_cache"), width = int_of(c.width, "block_table"), batch = int_of(c.batch, "seq_lens"),
+                  hq = int_of(Hq, "q"), heads = int_of(c.heads, "k_cache"), n = int_of(prefix.size(0), "prefix_lens");
+    return run(device, a[11], [&](kda_stream_t stream) {
+        return kda_attn_prefix_decode(address(q), address(c.k), address(c.v), c.stride(c.k), c.stride(c.v), c.pages, size,
+                                      address<int32_t>(c.table), width, address<int32_t>(c.lens), address<int32_t>(groups),
+                                      address<int32_t>(prefix), n, address(out), lse, batch, hq, heads, scale, ws.base, ws.bytes,
+                                      stream);
+    });
+}
+
 // (block_table, seq_lens, new_lens, free_pages, free_state, page_size, out_lens, out_state, cu_tokens, slots, positions, rows,
 //  stream)
 PyObject *page_resize(PyObject *const *a) {
@@ -396,7 +419,7 @@ PyMethodDef method(const char *name) {
 
 PyMethodDef methods[] = {method<linear_prefill, 11>("linear_prefill"), method<linear_decode, 9>("linear_decode"),
                          method<attn_decode, 11>("attn_decode"), method<cache_evict, 13>("cache_evict"),
-                         method<page_resize, 13>("page_resize"), method<qk_norm_rope, 16>("qk_norm_rope"),
+                         method<attn_prefix_decode, 12>("attn_prefix_decode"), method<page_resize, 13>("page_resize"), method<qk_norm_rope, 16>("qk_norm_rope"),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "kda_gb300_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

@@ -36,6 +36,7 @@
 #include "kda_dependent.cuh"
 #include "kda_internal.cuh"
 #include "kda_mma.cuh"
+#include "kda_prefix.cuh"
 
 namespace kda {
 namespace {
@@ -107,7 +108,17 @@ struct Args {
     Workspace ws;
     int32_t ctas;     // of the first kernel
     int32_t q_tiles;  // items of a key head
+    PrefixParts x;    // (tails only)
 };
+
+// kTail: only a row's tokens from x.start on are its tiles, and what comes before is in parts that each finished
+// query row is joined with. The start is a multiple of 128 tokens, so that tiles lie in pages as without it.
+template <bool kTail>
+__device__ __forceinline__ int start_of(const Args &a, int b) { return kTail ? a.x.start[b] : 0; }
+template <bool kTail>
+__device__ __forceinline__ int tokens_of(const Args &a, int b, bool report) {
+    return row_length(a.p.c, b, a.p.status, report) - start_of<kTail>(a, b);
+}
 
 // All items' tiles, laid end to end, are cut into CTAs' shares of `per` tiles and those into warps' shares of
 // warp_share tiles (the last of each may be shorter): equal numbers rather than equal fractions, because then
@@ -133,11 +144,12 @@ __device__ __forceinline__ int page_at(const PagedCache &c, int b, int j, Device
 }
 
 // A place in the sequence of tiles: tile `tile` of the `tiles` of item `item` of row b, which has n
-// tokens.
+// tokens (from token `start` on).
 struct Place {
-    int b, item, tile, tiles, n;
+    int b, item, tile, tiles, n, start;
 };
 
+template <bool kTail>
 __device__ __forceinline__ void next_tile(Place &at, const Args &a, int items) {
     if (++at.tile < at.tiles) return;
     at.tile = 0;
@@ -145,8 +157,9 @@ __device__ __forceinline__ void next_tile(Place &at, const Args &a, int items) {
     at.item = 0;
     do {  // the next row with a token (there is one: the share holds another tile)
         ++at.b;
-        at.n = row_length(a.p.c, at.b, a.p.status, false);
+        at.n = tokens_of<kTail>(a, at.b, false);
     } while (at.n == 0 && at.b + 1 < a.p.c.batch);
+    at.start = start_of<kTail>(a, at.b);
     at.tiles = (at.n + kTokens - 1) / kTokens;
 }
 
@@ -176,8 +189,33 @@ __device__ __forceinline__ uint32_t max_abs(uint32_t x, uint32_t y) {
     return z;
 }
 
+// The parts of a query row's prefix: how many, and the factors that join one with (m, l).
+__device__ __forceinline__ int prefix_parts(const Args &a, size_t head, PrefixCut &c) {
+    if (a.x.start[head / a.p.num_q_heads] == 0) return 0;
+    c = a.x.cuts[head];
+    return c.per * (1 + c.ctas);
+}
+__device__ __forceinline__ void join(float2 part, float &m, float &l, float &keep, float &add) {
+    const float top = fmaxf(m, part.x), ref = top == kNegInf ? 0.0f : top;
+    keep = ex2(m - ref), add = ex2(part.x - ref);
+    l = fmaf(l, keep, part.y * add);
+    m = top;
+}
+
 // A finished row by one warp: lane's four channels of o over the sum l, at maximum m.
-__device__ __forceinline__ void write_row(const Args &a, size_t head, int lane, float m, float l, const float4 &o) {
+template <bool kTail>
+__device__ __forceinline__ void write_row(const Args &a, size_t head, int lane, float m, float l, float4 o) {
+    if constexpr (kTail) {
+        PrefixCut c;
+        const int n = prefix_parts(a, head, c);
+        for (int i = 0; i < n; ++i) {
+            const int64_t part = a.x.part_at(c, (int64_t)head, i);
+            const float4 x = *reinterpret_cast<const float4 *>(a.x.o + part * kHeadDim + 4 * lane);
+            float keep, add;
+            join(a.x.ml[part], m, l, keep, add);
+            o = make_float4(fmaf(o.x, keep, x.x * add), fmaf(o.y, keep, x.y * add), fmaf(o.z, keep, x.z * add), fmaf(o.w, keep, x.w * add));
+        }
+    }
     const float inv = 1.0f / l;  // (l = 0: zeros, whatever the values)
     reinterpret_cast<uint2 *>(a.p.out + head * kHeadDim)[lane] =
         l == 0.0f ? make_uint2(0, 0) : make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
@@ -188,7 +226,7 @@ __device__ __forceinline__ void write_row(const Args &a, size_t head, int lane, 
     }
 }
 
-template <typename U>
+template <typename U, bool kTail>
 __global__ void __launch_bounds__(kThreads, 1) kda_attn_decode_kernel(const Args a) {
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ U s_sum[kWarps], s_off[kWarps + 1];
@@ -203,7 +241,7 @@ __global__ void __launch_bounds__(kThreads, 1) kda_attn_decode_kernel(const Args
     allow_next();
 
     // ---- the total, then the row and tile where each warp's share begins, and where the CTA's last tile is
-    auto length_of = [&](int b) { return b < c.batch ? row_length(c, b, p.status, blockIdx.x == 0) : 0; };
+    auto length_of = [&](int b) { return b < c.batch ? tokens_of<kTail>(a, b, blockIdx.x == 0) : 0; };
     auto tiles_of = [&](int n) { return (U)((n + kTokens - 1) / kTokens) * (U)items; };
     auto block_sum = [&](U x, U &before) {  // inclusive prefix sum's total, and the sum before this thread
         U sum = x;
@@ -248,10 +286,11 @@ __global__ void __launch_bounds__(kThreads, 1) kda_attn_decode_kernel(const Args
     }
     __syncthreads();
     const U begin = min(cta_lo + warp * per_warp, cta_hi), end = min(begin + per_warp, cta_hi);
-    Place at = {-1, 0, 0, 0, 0};
+    Place at = {-1, 0, 0, 0, 0, 0};
     if (begin < end) {
         at.b = s_row[warp];
         at.n = s_len[warp];
+        at.start = start_of<kTail>(a, at.b);
         at.tiles = (at.n + kTokens - 1) / kTokens;
         at.item = (int)(s_off[warp] / (U)at.tiles);
         at.tile = (int)(s_off[warp] - (U)at.item * at.tiles);
@@ -268,8 +307,13 @@ __global__ void __launch_bounds__(kThreads, 1) kda_attn_decode_kernel(const Args
     }
     auto empty_rows = [&] {
         for (int b = blockIdx.x; b < c.batch; b += gridDim.x) {
-            if (row_length(c, b, p.status, false) > 0) continue;
+            if (tokens_of<kTail>(a, b, false) > 0) continue;
             const size_t h0 = (size_t)b * p.num_q_heads;
+            if constexpr (kTail) {
+                for (int i = warp; i < p.num_q_heads; i += kWarps)
+                    write_row<kTail>(a, h0 + i, lane, kNegInf, 0.0f, make_float4(0.0f, 0.0f, 0.0f, 0.0f));
+                continue;
+            }
             for (int i = threadIdx.x; i < p.num_q_heads * (kHeadDim / 8); i += kThreads)
                 reinterpret_cast<uint4 *>(p.out + h0 * kHeadDim)[i] = make_uint4(0, 0, 0, 0);
             for (int i = threadIdx.x; i < p.num_q_heads; i += kThreads) {
@@ -294,10 +338,10 @@ __global__ void __launch_bounds__(kThreads, 1) kda_attn_decode_kernel(const Args
     Place load = at;
     U to_load = end - begin;  // (0: a warp that is only there for the join)
     auto pages_of = [&](const Place &x) {  // of the tile's two groups of eight tokens
-        const int j = x.tile * kTokens;
+        const int j = x.start + x.tile * kTokens;
         int2 pg;
         pg.x = page_at(c, x.b, j, p.status);
-        pg.y = c.page_shift > 3 ? pg.x : j + 8 < x.n ? page_at(c, x.b, j + 8, p.status) : -1;
+        pg.y = c.page_shift > 3 ? pg.x : j + 8 < x.start + x.n ? page_at(c, x.b, j + 8, p.status) : -1;
         return pg;
     };
     int2 pages = make_int2(-1, -1);
@@ -305,7 +349,7 @@ __global__ void __launch_bounds__(kThreads, 1) kda_attn_decode_kernel(const Args
     auto fetch = [&](int stage) {
         if (to_load > 0) {
             const int j0 = load.tile * kTokens, h = load.item / a.q_tiles, mask = c.page_size - 1;
-            const int left = load.n - j0;  // tokens
+            const int left = load.n - j0, first = load.start + j0;  // tokens
             uint32_t bits = left >= kTokens ? 0xffffu : (1u << left) - 1;
             if (pages.x < 0) bits &= 0xff00u;
             if (pages.y < 0) bits &= 0x00ffu;
@@ -315,7 +359,7 @@ __global__ void __launch_bounds__(kThreads, 1) kda_attn_decode_kernel(const Args
                 const int r = 2 * i + half_row;
                 const int page = i < 4 ? pages.x : pages.y;
                 const bool on = (bits >> r) & 1;
-                const size_t row = ((size_t)h * c.page_size + ((j0 + r) & mask)) * kHeadDim + chunk * 8;
+                const size_t row = ((size_t)h * c.page_size + ((first + r) & mask)) * kHeadDim + chunk * 8;
                 const size_t k_off = on ? (size_t)page * c.k_page_stride + row : 0;
                 const size_t v_off = on ? (size_t)page * c.v_page_stride + row : 0;
                 cp_async_16(dst + r * 256 + ((chunk ^ ((r & 1) << 2)) << 4), c.k + k_off, on ? 16u : 0u);
@@ -323,7 +367,7 @@ __global__ void __launch_bounds__(kThreads, 1) kda_attn_decode_kernel(const Args
             }
             if (lane == 0) live[stage] = bits;
             if (--to_load > 0) {
-                next_tile(load, a, items);
+                next_tile<kTail>(load, a, items);
                 pages = pages_of(load);
             }
         }
@@ -495,6 +539,29 @@ __global__ void __launch_bounds__(kThreads, 1) kda_attn_decode_kernel(const Args
             l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
             const int row = g + 8 * r;
             if (row >= rows) continue;
+            if constexpr (kTail) {
+                PrefixCut c;
+                const int n = whole ? prefix_parts(a, head0 + row, c) : 0;
+                for (int i = 0; i < n; ++i) {
+                    const int64_t part = a.x.part_at(c, (int64_t)(head0 + row), i);
+                    float keep, add;
+                    join(a.x.ml[part], m[r], l[r], keep, add);
+#pragma unroll
+                    for (int half = 0; half < 2; ++half)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e)
+#pragma unroll
+                            for (int i2 = 0; i2 < 2; ++i2) {
+                                const float4 y = *reinterpret_cast<const float4 *>(a.x.o + part * kHeadDim + 64 * half + 16 * t + 8 * e + 4 * i2);
+                                const float x[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+                                for (int k = 0; k < 4; ++k) {
+                                    float &dst = o[8 * half + 4 * i2 + k][2 * r + e];
+                                    dst = fmaf(dst, keep, x[k] * add);
+                                }
+                            }
+                }
+            }
             if (whole) {
                 const float inv = 1.0f / l[r];
                 const float v = l[r] == 0.0f ? kNegInf : m[r] + log2f(l[r]);
@@ -531,7 +598,7 @@ __global__ void __launch_bounds__(kThreads, 1) kda_attn_decode_kernel(const Args
         }
         if (left > 0) {  // the next item
             --at.tile;
-            next_tile(at, a, items);
+            next_tile<kTail>(at, a, items);
         }
     }
     cp_async_wait<0>();
@@ -553,7 +620,7 @@ __global__ void __launch_bounds__(kThreads, 1) kda_attn_decode_kernel(const Args
             o = make_float4(fmaf(x.x, f, o.x), fmaf(x.y, f, o.y), fmaf(x.z, f, o.z), fmaf(x.w, f, o.w));
         }
         if (whole) {
-            write_row(a, (size_t)b * p.num_q_heads + (size_t)h * p.group + q0 + row, lane, top, l, o);
+            write_row<kTail>(a, (size_t)b * p.num_q_heads + (size_t)h * p.group + q0 + row, lane, top, l, o);
         } else {
             Part *const part = a.ws.parts + 2 * (size_t)(blockIdx.x * kWarps) + (cta_tile == 0 ? 1 : 0);
             if (lane == 0) part->m[row] = top, part->l[row] = l;
@@ -602,6 +669,7 @@ __device__ __forceinline__ void add_parts(const Part *parts, const Cut &cut, int
 // 8 x 8000 tokens: 12.0 us, with one warp for up to 64 parts 14.4; 1 x 100000 tokens: 18, with one warp 31.
 constexpr int kManyParts = kWarps;
 
+template <bool kTail>
 __global__ void __launch_bounds__(kThreads, 4) kda_attn_join_kernel(const Args a) {
     __shared__ float s_m[kWarps], s_l[kWarps];
     __shared__ float4 s_o[kWarps][32];
@@ -620,7 +688,7 @@ __global__ void __launch_bounds__(kThreads, 4) kda_attn_join_kernel(const Args a
             float m = kNegInf, l = 0.0f;
             float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
             add_parts(a.ws.parts, cut, row, lane, 0, 1, m, l, o);
-            write_row(a, (size_t)cut.head + row, lane, m, l, o);
+            write_row<kTail>(a, (size_t)cut.head + row, lane, m, l, o);
         }
     }
     __syncthreads();
@@ -644,7 +712,7 @@ __global__ void __launch_bounds__(kThreads, 4) kda_attn_join_kernel(const Args a
         l = fmaf(s_l[w], f, l);
         o = make_float4(fmaf(x.x, f, o.x), fmaf(x.y, f, o.y), fmaf(x.z, f, o.z), fmaf(x.w, f, o.w));
     }
-    write_row(a, (size_t)s_cut.head + row, lane, m, l, o);
+    write_row<kTail>(a, (size_t)s_cut.head + row, lane, m, l, o);
 }
 
 // weight[b][h][j] += sum over the query heads of key head h of 2^(x_j - lse), four tokens a thread. A score of
@@ -696,14 +764,14 @@ __global__ void __launch_bounds__(kWeightThreads) kda_attn_weight_kernel(const A
     }
 }
 
-template <typename U>
+template <typename U, bool kTail>
 cudaError_t configure_once() {
     static bool configured[64] = {};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= 64 || !configured[dev]) {
-        e = cudaFuncSetAttribute(kda_attn_decode_kernel<U>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+        e = cudaFuncSetAttribute(kda_attn_decode_kernel<U, kTail>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
         if (e != cudaSuccess) return e;
         if (dev >= 0 && dev < 64) configured[dev] = true;
     }
@@ -717,11 +785,15 @@ int64_t attn_decode_workspace_bytes(int32_t batch, int32_t num_q_heads, int32_t,
     return workspace_layout(nullptr, nullptr, batch, num_q_heads, capacity, with_weight, (int64_t)sms * kWarps);
 }
 
-cudaError_t launch_attn_decode(const AttnDecodeArgs &p, cudaStream_t stream) {
+namespace {
+
+template <bool kTail>
+cudaError_t launch(const AttnDecodeArgs &p, const PrefixParts &x, cudaStream_t stream) {
     int32_t sms = 0;
     if (sm_count_of_current_device(&sms) != KDA_OK) return cudaErrorInvalidDevice;
     Args a;
     a.p = p;
+    a.x = x;
     a.ctas = sms;
     a.q_tiles = (p.group + kRows - 1) / kRows;
     workspace_layout(&a.ws, static_cast<char *>(p.ws), p.c.batch, p.num_q_heads, p.c.capacity, p.weight != nullptr,
@@ -729,15 +801,21 @@ cudaError_t launch_attn_decode(const AttnDecodeArgs &p, cudaStream_t stream) {
     // do the tiles there can be, and the end of the last CTA's share, fit 32 bits?
     const int64_t most = (int64_t)p.c.batch * p.c.num_kv_heads * a.q_tiles * ((p.c.capacity + kTokens - 1) / kTokens);
     const bool small = most < 0x7fffffffLL;
-    cudaError_t e = small ? configure_once<uint32_t>() : configure_once<uint64_t>();
+    cudaError_t e = small ? configure_once<uint32_t, kTail>() : configure_once<uint64_t, kTail>();
     if (e != cudaSuccess) return e;
-    e = small ? launch_dependent(kda_attn_decode_kernel<uint32_t>, dim3((unsigned)sms), kThreads, kSmem, stream, a)
-              : launch_dependent(kda_attn_decode_kernel<uint64_t>, dim3((unsigned)sms), kThreads, kSmem, stream, a);
+    e = small ? launch_dependent(kda_attn_decode_kernel<uint32_t, kTail>, dim3((unsigned)sms), kThreads, kSmem, stream, a)
+              : launch_dependent(kda_attn_decode_kernel<uint64_t, kTail>, dim3((unsigned)sms), kThreads, kSmem, stream, a);
     if (e != cudaSuccess) return e;
-    e = launch_dependent(kda_attn_join_kernel, dim3((unsigned)sms, (unsigned)std::min(p.group, kRows)), kThreads, 0, stream, a);
+    e = launch_dependent(kda_attn_join_kernel<kTail>, dim3((unsigned)sms, (unsigned)std::min(p.group, kRows)), kThreads, 0, stream, a);
     if (e != cudaSuccess || !p.weight) return e;
     const dim3 grid((unsigned)(p.c.batch * p.c.num_kv_heads), (unsigned)std::min((p.c.capacity + kWeightTokens - 1) / kWeightTokens, 65535));
     return launch_dependent(kda_attn_weight_kernel, grid, kWeightThreads, 0, stream, a);
 }
+
+}  // namespace
+
+cudaError_t launch_attn_decode(const AttnDecodeArgs &p, cudaStream_t stream) { return launch<false>(p, PrefixParts(), stream); }
+
+cudaError_t launch_attn_tails(const AttnDecodeArgs &p, const PrefixParts &x, cudaStream_t stream) { return launch<true>(p, x, stream); }
 
 }  // namespace kda

@@ -4,6 +4,7 @@
 #include <math.h>
 
 #include "kda_internal.cuh"
+#include "kda_prefix.cuh"
 
 using namespace kda;
 
@@ -237,6 +238,59 @@ int kda_cache_evict(void *k_cache, void *v_cache, int64_t k_page_stride, int64_t
     a.recent = recent;
     if (device_status_ptr(&a.status) != cudaSuccess) return KDA_ERR_CUDA;
     return from_cuda(launch_cache_evict(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int64_t kda_attn_prefix_decode_workspace_size(int32_t batch, int32_t num_q_heads, int32_t num_kv_heads,
+                                              int32_t max_pages, int32_t page_size, int32_t num_groups,
+                                              int32_t sm_count) {
+    if (sm_count < 0 || num_groups < 0) return KDA_ERR_INVALID_ARG;
+    const int bad = attn_shape(batch, num_q_heads, num_kv_heads, max_pages, page_size);
+    if (bad != KDA_OK) return bad;
+    if (sm_count == 0) {
+        const int st = sm_count_of_current_device(&sm_count);
+        if (st != KDA_OK) return st;
+    }
+    return attn_prefix_workspace_bytes(batch, num_q_heads, num_kv_heads, (int64_t)max_pages * page_size, sm_count);
+}
+
+int kda_attn_prefix_decode(const void *q, const void *k_cache, const void *v_cache, int64_t k_page_stride,
+                           int64_t v_page_stride, int64_t num_pages, int32_t page_size, const int32_t *block_table,
+                           int32_t max_pages, const int32_t *seq_lens, const int32_t *cu_groups,
+                           const int32_t *prefix_lens, int32_t num_groups, void *out, float *lse, int32_t batch,
+                           int32_t num_q_heads, int32_t num_kv_heads, float scale, void *workspace,
+                           int64_t workspace_bytes, kda_stream_t stream) {
+    if (!isfinite(scale) || num_groups < 0) return KDA_ERR_INVALID_ARG;
+    int bad = attn_shape(batch, num_q_heads, num_kv_heads, max_pages, page_size);
+    if (bad != KDA_OK) return bad;
+    AttnPrefixArgs a;
+    bad = paged_cache(&a.d.c, const_cast<void *>(k_cache), const_cast<void *>(v_cache), k_page_stride, v_page_stride,
+                      num_pages, page_size, block_table, max_pages, seq_lens, batch, num_kv_heads);
+    if (bad != KDA_OK) return bad;
+    // (a tensor map's strides are below 2^40 bytes)
+    if (k_page_stride >= (int64_t)1 << 39 || v_page_stride >= (int64_t)1 << 39) return KDA_ERR_UNSUPPORTED;
+    if (batch == 0) return KDA_OK;
+    if (!q || !out || !workspace || (num_groups > 0 && (!cu_groups || !prefix_lens))) return KDA_ERR_INVALID_ARG;
+    if (!aligned(q, 16) || !aligned(out, 16) || !aligned(workspace, 16) || !aligned(lse, 4) || !aligned(cu_groups, 4) ||
+        !aligned(prefix_lens, 4))
+        return KDA_ERR_MISALIGNED;
+    int32_t sms = 0;
+    const int st = sm_count_of_current_device(&sms);
+    if (st != KDA_OK) return st;
+    if (workspace_bytes < attn_prefix_workspace_bytes(batch, num_q_heads, num_kv_heads, a.d.c.capacity, sms))
+        return KDA_ERR_INVALID_ARG;
+    a.d.q = static_cast<const __nv_bfloat16 *>(q);
+    a.d.out = static_cast<__nv_bfloat16 *>(out);
+    a.d.lse = lse;
+    a.d.weight = nullptr;
+    a.d.num_q_heads = num_q_heads;
+    a.d.group = num_q_heads / num_kv_heads;
+    a.d.scale = scale;
+    a.d.ws = workspace;
+    a.cu_groups = cu_groups;
+    a.prefix_lens = prefix_lens;
+    a.groups = num_groups;
+    if (device_status_ptr(&a.d.status) != cudaSuccess) return KDA_ERR_CUDA;
+    return from_cuda(launch_attn_prefix(a, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 int kda_page_resize(int32_t *block_table, const int32_t *seq_lens, const int32_t *new_lens, int32_t *out_lens,

@@ -77,6 +77,7 @@
 #include "kda_internal.cuh"
 #include "kda_mma.cuh"
 #include "kda_tc.cuh"
+#include "kda_tc_bf16.cuh"
 
 namespace kda {
 namespace {
@@ -157,7 +158,6 @@ constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColA = 0;  // A (128); each 32 columns then hold their part of P in the first 16
 constexpr uint32_t kColO = 128, kColQS = 256, kColD = 384;
 
-constexpr uint32_t kTransA = 1u << 15, kTransB = 1u << 16;  // MN-major operands
 constexpr uint32_t kIdescQK = instr_desc(1, 128, 128);
 constexpr uint32_t kIdescQS = instr_desc(1, 128, 128) | kTransB;
 constexpr uint32_t kIdescD = instr_desc(1, 128, 128) | kTransA | kTransB;
@@ -169,48 +169,7 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
-// Operand descriptors: the constant part plus the address in 16-byte units (under 2^14 for any
-// address in shared memory, so an offset adds without carry).
-//   K-major, 128-byte swizzle: smem_desc_sw128.
-//   MN-major, 128-byte swizzle: 128-byte rows hold 64 elements along M or N, eight rows (along K)
-//   make a 1024-byte group; `lbo` = distance between blocks of 64 along M or N.
-__device__ __forceinline__ constexpr uint64_t desc_mn(uint32_t lbo) {
-    return (uint64_t)(lbo >> 4) << 16 | (uint64_t)(1024 >> 4) << 32 | (uint64_t)1 << 46 | (uint64_t)2 << 61;
-}
-constexpr uint64_t kDescK = (uint64_t)1 << 16 | (uint64_t)(1024 >> 4) << 32 | (uint64_t)1 << 46 | (uint64_t)2 << 61;
 constexpr uint64_t kDescMn = desc_mn(kHalf), kDescSplit = desc_mn(kSplitHalf);
-
-__device__ __forceinline__ uint64_t at(uint64_t desc, uint32_t saddr) { return desc | (saddr >> 4); }
-
-// Every lane of the warp calls these with the same operands (which keeps them in uniform
-// registers); one elected lane issues, always the same one, so that its commits follow its MMAs.
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
-    asm volatile(
-        "{\n\t.reg .pred p, e;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "elect.sync _|e, 0xffffffff;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc)
-        : "memory");
-}
-
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool acc) {
-    asm volatile(
-        "{\n\t.reg .pred p, e;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "elect.sync _|e, 0xffffffff;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc)
-        : "memory");
-}
-
-__device__ __forceinline__ void commit(uint64_t *bar) {
-    asm volatile(
-        "{\n\t.reg .pred e;\n\t"
-        "elect.sync _|e, 0xffffffff;\n\t"
-        "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_addr(bar))
-        : "memory");
-}
 
 __device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap *map, int x, int y, int z, uint64_t *bar) {
     asm volatile(
@@ -218,10 +177,6 @@ __device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap *map, i
             dst),
         "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_addr(bar))
         : "memory");
-}
-
-__device__ __forceinline__ void prefetch_map(const CUtensorMap *map) {
-    asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
 }
 
 __device__ __forceinline__ void tma_store(const CUtensorMap *map, uint32_t src, int x, int y, int z) {
@@ -234,10 +189,6 @@ __device__ __forceinline__ void tma_store(const CUtensorMap *map, uint32_t src, 
     asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(map), "r"(x), "r"(y),
                  "r"(src)
                  : "memory");
-}
-
-__device__ __forceinline__ void expect_tx(uint64_t *bar, uint32_t bytes) {
-    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_addr(bar)), "r"(bytes) : "memory");
 }
 
 // Asks for the index of a CTA of this grid that has not been launched (16 bytes to `answer`, completed
@@ -314,12 +265,6 @@ __device__ __forceinline__ void watch(Bars *B) {
             *abort = kTimedOut;
         }
     }
-}
-
-// One arrival for a warp, after what its lanes did.
-__device__ __forceinline__ void arrive_warp(uint64_t *bar) {
-    __syncwarp();
-    if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
 }
 
 struct Plan {
@@ -1102,20 +1047,6 @@ __global__ void __launch_bounds__(kScanThreads) kda_linear_scan_kernel(const Chu
             *reinterpret_cast<float4 *>(slot_of(a, lc, w0 + i + 1) + off) = S;
         }
     }
-}
-
-using EncodeTiled = decltype(&cuTensorMapEncodeTiled);
-
-EncodeTiled encode_tiled() {
-    static const EncodeTiled fn = [] {
-        void *p = nullptr;
-        cudaDriverEntryPointQueryResult found = cudaDriverEntryPointSymbolNotFound;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &found) != cudaSuccess ||
-            found != cudaDriverEntryPointSuccess)
-            p = nullptr;
-        return reinterpret_cast<EncodeTiled>(p);
-    }();
-    return fn;
 }
 
 // [T][H][128] BF16, in boxes of `rows` tokens x one head x 64 columns; tokens past T read as zeros.
