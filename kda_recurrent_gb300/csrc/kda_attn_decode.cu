@@ -189,32 +189,14 @@ __device__ __forceinline__ uint32_t max_abs(uint32_t x, uint32_t y) {
     return z;
 }
 
-// The parts of a query row's prefix: how many, and the factors that join one with (m, l).
-__device__ __forceinline__ int prefix_parts(const Args &a, size_t head, PrefixCut &c) {
-    if (a.x.start[head / a.p.num_q_heads] == 0) return 0;
-    c = a.x.cuts[head];
-    return c.per * (1 + c.ctas);
-}
-__device__ __forceinline__ void join(float2 part, float &m, float &l, float &keep, float &add) {
-    const float top = fmaxf(m, part.x), ref = top == kNegInf ? 0.0f : top;
-    keep = ex2(m - ref), add = ex2(part.x - ref);
-    l = fmaf(l, keep, part.y * add);
-    m = top;
-}
-
 // A finished row by one warp: lane's four channels of o over the sum l, at maximum m.
 template <bool kTail>
 __device__ __forceinline__ void write_row(const Args &a, size_t head, int lane, float m, float l, float4 o) {
-    if constexpr (kTail) {
-        PrefixCut c;
-        const int n = prefix_parts(a, head, c);
-        for (int i = 0; i < n; ++i) {
-            const int64_t part = a.x.part_at(c, (int64_t)head, i);
-            const float4 x = *reinterpret_cast<const float4 *>(a.x.o + part * kHeadDim + 4 * lane);
-            float keep, add;
-            join(a.x.ml[part], m, l, keep, add);
-            o = make_float4(fmaf(o.x, keep, x.x * add), fmaf(o.y, keep, x.y * add), fmaf(o.z, keep, x.z * add), fmaf(o.w, keep, x.w * add));
-        }
+    if constexpr (kTail) {  // to be joined with what comes before
+        const int64_t part = 2 * (int64_t)a.x.heads + (int64_t)head;
+        if (lane == 0) a.x.ml[part] = make_float2(m, l), a.x.tails[head] = kTailHome;
+        *reinterpret_cast<float4 *>(a.x.o + part * kHeadDim + 4 * lane) = o;
+        return;
     }
     const float inv = 1.0f / l;  // (l = 0: zeros, whatever the values)
     reinterpret_cast<uint2 *>(a.p.out + head * kHeadDim)[lane] =
@@ -310,8 +292,7 @@ __global__ void __launch_bounds__(kThreads, 1) kda_attn_decode_kernel(const Args
             if (tokens_of<kTail>(a, b, false) > 0) continue;
             const size_t h0 = (size_t)b * p.num_q_heads;
             if constexpr (kTail) {
-                for (int i = warp; i < p.num_q_heads; i += kWarps)
-                    write_row<kTail>(a, h0 + i, lane, kNegInf, 0.0f, make_float4(0.0f, 0.0f, 0.0f, 0.0f));
+                for (int i = threadIdx.x; i < p.num_q_heads; i += kThreads) a.x.tails[h0 + i] = kTailNone;
                 continue;
             }
             for (int i = threadIdx.x; i < p.num_q_heads * (kHeadDim / 8); i += kThreads)
@@ -390,6 +371,7 @@ __global__ void __launch_bounds__(kThreads, 1) kda_attn_decode_kernel(const Args
                 const int h = at.item / a.q_tiles, q0 = (at.item - h * a.q_tiles) * kRows;
                 cut.head = at.b * p.num_q_heads + h * p.group + q0;
                 cut.rows = min(kRows, p.group - q0);
+                if (kTail && cut.count > 1 && lane < cut.rows) a.x.tails[cut.head + lane] = share;
             }
         }
         if (lane == 0) a.ws.cuts[share] = cut;
@@ -539,30 +521,7 @@ __global__ void __launch_bounds__(kThreads, 1) kda_attn_decode_kernel(const Args
             l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
             const int row = g + 8 * r;
             if (row >= rows) continue;
-            if constexpr (kTail) {
-                PrefixCut c;
-                const int n = whole ? prefix_parts(a, head0 + row, c) : 0;
-                for (int i = 0; i < n; ++i) {
-                    const int64_t part = a.x.part_at(c, (int64_t)(head0 + row), i);
-                    float keep, add;
-                    join(a.x.ml[part], m[r], l[r], keep, add);
-#pragma unroll
-                    for (int half = 0; half < 2; ++half)
-#pragma unroll
-                        for (int e = 0; e < 2; ++e)
-#pragma unroll
-                            for (int i2 = 0; i2 < 2; ++i2) {
-                                const float4 y = *reinterpret_cast<const float4 *>(a.x.o + part * kHeadDim + 64 * half + 16 * t + 8 * e + 4 * i2);
-                                const float x[4] = {y.x, y.y, y.z, y.w};
-#pragma unroll
-                                for (int k = 0; k < 4; ++k) {
-                                    float &dst = o[8 * half + 4 * i2 + k][2 * r + e];
-                                    dst = fmaf(dst, keep, x[k] * add);
-                                }
-                            }
-                }
-            }
-            if (whole) {
+            if (!kTail && whole) {
                 const float inv = 1.0f / l[r];
                 const float v = l[r] == 0.0f ? kNegInf : m[r] + log2f(l[r]);
                 if (t == 0) {
@@ -583,12 +542,19 @@ __global__ void __launch_bounds__(kThreads, 1) kda_attn_decode_kernel(const Args
                 }
             } else {
                 Part *const part = a.ws.parts + 2 * (size_t)share + (from_start ? 1 : 0);
-                if (t == 0) part->m[row] = m[r], part->l[row] = l[r];
+                float *o_row = part->o[row];
+                if (kTail && whole) {
+                    const int64_t home = 2 * (int64_t)a.x.heads + (int64_t)(head0 + row);
+                    o_row = a.x.o + home * kHeadDim;
+                    if (t == 0) a.x.ml[home] = make_float2(m[r], l[r]), a.x.tails[head0 + row] = kTailHome;
+                } else if (t == 0) {
+                    part->m[row] = m[r], part->l[row] = l[r];
+                }
 #pragma unroll
                 for (int half = 0; half < 2; ++half)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        float4 *const dst = reinterpret_cast<float4 *>(&part->o[row][64 * half + 16 * t + 8 * e]);
+                        float4 *const dst = reinterpret_cast<float4 *>(o_row + 64 * half + 16 * t + 8 * e);
 #pragma unroll
                         for (int i = 0; i < 2; ++i)
                             dst[i] = make_float4(o[8 * half + 4 * i][2 * r + e], o[8 * half + 4 * i + 1][2 * r + e],
@@ -669,7 +635,6 @@ __device__ __forceinline__ void add_parts(const Part *parts, const Cut &cut, int
 // 8 x 8000 tokens: 12.0 us, with one warp for up to 64 parts 14.4; 1 x 100000 tokens: 18, with one warp 31.
 constexpr int kManyParts = kWarps;
 
-template <bool kTail>
 __global__ void __launch_bounds__(kThreads, 4) kda_attn_join_kernel(const Args a) {
     __shared__ float s_m[kWarps], s_l[kWarps];
     __shared__ float4 s_o[kWarps][32];
@@ -688,7 +653,7 @@ __global__ void __launch_bounds__(kThreads, 4) kda_attn_join_kernel(const Args a
             float m = kNegInf, l = 0.0f;
             float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
             add_parts(a.ws.parts, cut, row, lane, 0, 1, m, l, o);
-            write_row<kTail>(a, (size_t)cut.head + row, lane, m, l, o);
+            write_row<false>(a, (size_t)cut.head + row, lane, m, l, o);
         }
     }
     __syncthreads();
@@ -712,7 +677,81 @@ __global__ void __launch_bounds__(kThreads, 4) kda_attn_join_kernel(const Args a
         l = fmaf(s_l[w], f, l);
         o = make_float4(fmaf(x.x, f, o.x), fmaf(x.y, f, o.y), fmaf(x.z, f, o.z), fmaf(x.w, f, o.w));
     }
-    write_row<kTail>(a, (size_t)s_cut.head + row, lane, m, l, o);
+    write_row<false>(a, (size_t)s_cut.head + row, lane, m, l, o);
+}
+
+// Joins all parts of a query row: those of its prefix and those of the rest, in this order, by `per_row` warps of a
+// CTA, which take every per_row-th part. (8192 query rows of 6 to 8 parts: about 7 us, which the parts' 30 MB take.)
+__global__ void __launch_bounds__(kThreads, 4) kda_attn_prefix_join_kernel(const Args a, int per_row) {
+    __shared__ float s_m[kWarps], s_l[kWarps];
+    __shared__ float4 s_o[kWarps][32];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t head = (int64_t)blockIdx.x * (kWarps / per_row) + warp / per_row;
+    const int first = warp % per_row;
+    allow_next();
+    wait_for_prior();
+    float m = kNegInf, l = 0.0f;
+    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (head < a.x.heads) {
+        const int tail = a.x.tails[head];
+        PrefixCut pre = a.x.cuts[head];
+        const int before = a.x.start[head / a.p.num_q_heads] == 0 ? 0 : pre.per * (1 + pre.ctas);
+        Cut cut;
+        cut.count = tail == kTailHome ? 1 : 0;
+        if (tail >= 0) cut = a.ws.cuts[tail];
+        const int row = tail >= 0 ? (int)(head - cut.head) : 0, n = before + cut.count;
+        constexpr int kAhead = 4;
+        for (int i = first; i < n; i += kAhead * per_row) {
+            float pm[kAhead], pl[kAhead];
+            float4 po[kAhead];
+            float top = m;
+#pragma unroll
+            for (int e = 0; e < kAhead; ++e) {
+                const int x = i + e * per_row;
+                pm[e] = kNegInf, pl[e] = 0.0f, po[e] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                if (x < before || (x < n && tail < 0)) {
+                    const int64_t part = x < before ? a.x.part_at(pre, head, x) : 2 * (int64_t)a.x.heads + head;
+                    const float2 ml = a.x.ml[part];
+                    pm[e] = ml.x, pl[e] = ml.y;
+                    po[e] = *reinterpret_cast<const float4 *>(a.x.o + part * kHeadDim + 4 * lane);
+                } else if (x < n) {
+                    const Part *const part = a.ws.parts + cut.part_at(x - before);
+                    pm[e] = part->m[row], pl[e] = part->l[row];
+                    po[e] = *reinterpret_cast<const float4 *>(&part->o[row][4 * lane]);
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < kAhead; ++e) top = fmaxf(top, pm[e]);
+            const float ref = top == kNegInf ? 0.0f : top, keep = ex2(m - ref);
+            l *= keep;
+            o = make_float4(o.x * keep, o.y * keep, o.z * keep, o.w * keep);
+#pragma unroll
+            for (int e = 0; e < kAhead; ++e) {
+                const float f = ex2(pm[e] - ref);
+                l = fmaf(pl[e], f, l);
+                o = make_float4(fmaf(po[e].x, f, o.x), fmaf(po[e].y, f, o.y), fmaf(po[e].z, f, o.z), fmaf(po[e].w, f, o.w));
+            }
+            m = top;
+        }
+    }
+    if (per_row > 1) {
+        if (lane == 0) s_m[warp] = m, s_l[warp] = l;
+        s_o[warp][lane] = o;
+        __syncthreads();
+        if (first > 0) return;
+        float top = kNegInf;
+        for (int w = 0; w < per_row; ++w) top = fmaxf(top, s_m[warp + w]);
+        const float ref = top == kNegInf ? 0.0f : top;
+        m = top, l = 0.0f;
+        o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        for (int w = 0; w < per_row; ++w) {
+            const float f = ex2(s_m[warp + w] - ref);
+            const float4 x = s_o[warp + w][lane];
+            l = fmaf(s_l[warp + w], f, l);
+            o = make_float4(fmaf(x.x, f, o.x), fmaf(x.y, f, o.y), fmaf(x.z, f, o.z), fmaf(x.w, f, o.w));
+        }
+    }
+    if (head < a.x.heads) write_row<false>(a, (size_t)head, lane, m, l, o);
 }
 
 // weight[b][h][j] += sum over the query heads of key head h of 2^(x_j - lse), four tokens a thread. A score of
@@ -806,7 +845,14 @@ cudaError_t launch(const AttnDecodeArgs &p, const PrefixParts &x, cudaStream_t s
     e = small ? launch_dependent(kda_attn_decode_kernel<uint32_t, kTail>, dim3((unsigned)sms), kThreads, kSmem, stream, a)
               : launch_dependent(kda_attn_decode_kernel<uint64_t, kTail>, dim3((unsigned)sms), kThreads, kSmem, stream, a);
     if (e != cudaSuccess) return e;
-    e = launch_dependent(kda_attn_join_kernel<kTail>, dim3((unsigned)sms, (unsigned)std::min(p.group, kRows)), kThreads, 0, stream, a);
+    if (kTail) {
+        // warps of a query row: all of a CTA's for few rows, which can have long rests in many parts
+        int per_row = kWarps;
+        while (per_row > 1 && (int64_t)x.heads * per_row > (int64_t)sms * 4 * kWarps) per_row /= 2;
+        const int rows = kWarps / per_row;
+        return launch_dependent(kda_attn_prefix_join_kernel, dim3((unsigned)((x.heads + rows - 1) / rows)), kThreads, 0, stream, a, per_row);
+    }
+    e = launch_dependent(kda_attn_join_kernel, dim3((unsigned)sms, (unsigned)std::min(p.group, kRows)), kThreads, 0, stream, a);
     if (e != cudaSuccess || !p.weight) return e;
     const dim3 grid((unsigned)(p.c.batch * p.c.num_kv_heads), (unsigned)std::min((p.c.capacity + kWeightTokens - 1) / kWeightTokens, 65535));
     return launch_dependent(kda_attn_weight_kernel, grid, kWeightThreads, 0, stream, a);

@@ -512,7 +512,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc_fence_after();
             }
             const int64_t part = w.step == 0 ? (shared ? 0 : (int64_t)g * a.x.heads) + head
-                                             : 2 * (int64_t)a.x.heads + (int64_t)cta * kPrefixSlots + g * kT + r;
+                                             : 3 * (int64_t)a.x.heads + (int64_t)cta * kPrefixSlots + g * kT + r;
             if (valid) a.x.ml[part] = make_float2(m, l);
             float4 *const dst = reinterpret_cast<float4 *>(a.x.o + part * kHeadDim);
 #pragma unroll
