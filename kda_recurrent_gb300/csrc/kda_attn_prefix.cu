@@ -37,10 +37,11 @@ namespace {
 
 constexpr int kT = kPrefixTile;
 constexpr int kTile = kT * kHeadDim * 2, kHalf = kTile / 2;  // two halves of 64 channels: 128 rows of 128 bytes
-constexpr int kRing = 5;
-constexpr int kWarpLoad = 8, kWarpMma = 9;  // the eight before them: softmax
-constexpr int kThreads = 10 * 32;
-constexpr int kLive = 16;  // masks kept (more tiles than the loads can be ahead of the softmax)
+constexpr int kKeyRing = 2, kValueRing = 3, kRing = kKeyRing + kValueRing;
+constexpr int kWarpKeys = 8, kWarpMma = 10;  // (9: values; 11: the second group's products); the eight before them: softmax
+constexpr int kThreads = 12 * 32;
+constexpr int kLive = 8;  // masks kept (more tiles than the loads can be ahead of the softmax)
+constexpr int kTmaPage = 64;  // the least page that is loaded by TMA
 constexpr float kNegInf = -INFINITY;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kSlack = 8.0f;  // log2: how far a maximum may grow before O is scaled
@@ -48,17 +49,18 @@ constexpr int32_t kLeastRows = 2;  // of a group, for its prefix to be shared
 
 constexpr uint32_t kTmemCols = 512;  // all: the base is column 0
 constexpr uint32_t kColS = 0, kColO = 256;  // of the first group of warps; the second's are 128 columns further
-constexpr uint32_t kIdescS = instr_desc(1, 128, 128), kIdescO = instr_desc(1, 128, 128) | kTransB;
+constexpr uint32_t kIdescS = instr_desc(1, 128, 64), kIdescO = instr_desc(1, 128, 128) | kTransB;
 constexpr uint64_t kDescV = desc_mn(kHalf);
 
 struct Bars {
-    uint64_t full[kRing], empty[kRing];
-    // of each group of warps: queries written (4 warps), scores done, probabilities written (4 warps), P V done
-    uint64_t q[2], s[2], p[2], o[2];
-    uint64_t drain;
+    uint64_t full[kRing], empty[kRing];  // of the keys' places, then the values'
+    // of each group of warps: queries written (4 warps); for half a tile's tokens: scores done, probabilities written
+    // (4 warps); P V done
+    uint64_t q[2], s[2][2], p[2][2], o[2][2];
+    uint64_t drain[2];
     uint32_t live[kLive];  // of a tile of keys: a bit for eight tokens
-    int64_t sums[kThreads / 32], offset;  // where the CTA's share begins: the place in its first group
-    int32_t group;
+    int64_t sums[kThreads / 32];
+    int32_t group, offset;  // where the CTA's share begins: its first group, and the place in that
     uint32_t tmem;
     int32_t abort;
 };
@@ -73,9 +75,40 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float y;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+    return y;
+}
+
+// Two numbers at a time.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 y;
+    asm("{\n\t.reg .b64 a, b, c, d;\n\t"
+        "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+        "fma.rn.f32x2 d, a, b, c;\n\t"
+        "mov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(y.x), "=f"(y.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return y;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 y;
+    asm("{\n\t.reg .b64 a, b, d;\n\t"
+        "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+        "add.rn.f32x2 d, a, b;\n\t"
+        "mov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(y.x), "=f"(y.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return y;
+}
+
+// (one lane's, by a whole warp with the same operands: a lane for each box took 70 cycles a box)
 __device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap *map, int x, int y, int z, int w, uint64_t *bar) {
     asm volatile(
-        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(
+        "{\n\t.reg .pred e;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "@e cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];\n\t}" ::"r"(
             dst),
         "l"(map), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_addr(bar))
         : "memory");
@@ -121,13 +154,16 @@ __device__ __forceinline__ int64_t head_steps(const AttnPrefixArgs &a, const Gro
 }
 
 // (of ordered cu_groups)
-__device__ __forceinline__ Group group_at(const AttnPrefixArgs &a, int g) {
+__device__ __forceinline__ Group group_of(const AttnPrefixArgs &a, int lo, int hi, int tokens) {
     Group x;
-    x.row0 = a.cu_groups[g];
-    x.rows = a.cu_groups[g + 1] - x.row0;
-    x.tokens = min(max(a.prefix_lens[g], 0), a.d.c.capacity);
+    x.row0 = lo;
+    x.rows = hi - lo;
+    x.tokens = min(max(tokens, 0), a.d.c.capacity);
     x.tiles = x.rows >= kLeastRows ? x.tokens / kT : 0;
     return x;
+}
+__device__ __forceinline__ Group group_at(const AttnPrefixArgs &a, int g) {
+    return group_of(a, a.cu_groups[g], a.cu_groups[g + 1], a.prefix_lens[g]);
 }
 
 // A CTA's walk over its share: the segments of items in it.
@@ -137,14 +173,14 @@ struct Walk {
     int32_t step, steps;        // the segment's first step; the item's steps
     int32_t n;                  // the segment's steps
     int32_t rows;               // the item's query rows (1 .. 256), from row pair * 256 of the group's
-    int64_t first, left;        // place of the item's first step; steps of the share from the segment on
+    int32_t first, left;        // place of the item's first step; steps of the share from the segment on
 };
 
 __device__ __forceinline__ void set_item(const AttnPrefixArgs &a, Walk &w) {
     const int rows = query_rows(a, w.g);
     w.rows = min(rows - w.pair * kPrefixSlots, kPrefixSlots);
     w.steps = pair_steps(rows, w.pair, w.g.tiles);
-    w.n = (int)min((int64_t)(w.steps - w.step), w.left);
+    w.n = min(w.steps - w.step, w.left);
 }
 
 __device__ __forceinline__ void next_segment(const AttnPrefixArgs &a, Walk &w) {
@@ -163,6 +199,194 @@ __device__ __forceinline__ void next_segment(const AttnPrefixArgs &a, Walk &w) {
     set_item(a, w);
 }
 
+// The segment's tiles of keys (and of values), and the steps of it that group g of warps has a tile in: all, but for
+// the second group's at the end of an item with an odd number of tiles.
+__device__ __forceinline__ int tiles_in(const Walk &w) {
+    return w.rows > kT ? w.n : 2 * w.n - (2 * (w.step + w.n) - 1 < w.g.tiles ? 0 : 1);
+}
+__device__ __forceinline__ int steps_in(const Walk &w, int g) { return w.rows > kT || g == 0 ? w.n : tiles_in(w) - w.n; }
+
+// The loads of the keys' or the values' tiles, by one warp: tile s for step s, or 2 s and 2 s + 1. Large pages come by
+// TMA, a box for each page (or 128 tokens of it) and half of the channels; a box takes about 100 cycles to ask for,
+// so that small pages come faster by 16-byte copies of all lanes.
+__device__ __forceinline__ void load_tiles(const AttnPrefixArgs &a, Walk w, const CUtensorMap *map, bool keys, uint8_t *smem, Bars *B) {
+    const PagedCache &c = a.d.c;
+    const int lane = threadIdx.x & 31, rows_a_box = min(c.page_size, kT), boxes = kT / rows_a_box;
+    const uint32_t ring = keys ? kKeyRing : kValueRing, place0 = keys ? 0 : kKeyRing, base = smem_addr(smem) + place0 * kTile;
+    uint64_t *const full = B->full + place0, *const empty = B->empty + place0;
+    const __nv_bfloat16 *const cache = keys ? c.k : c.v;
+    const int64_t page_stride = keys ? c.k_page_stride : c.v_page_stride;
+    const bool tma = c.page_size >= kTmaPage;
+    int leader = -1, leader_of = -1;
+    uint32_t count = 0, slot = 0, turn = 0;  // tiles so far; the next one's place, and the times that was used
+    bool ok = true;
+    for (; ok && w.left > 0; next_segment(a, w)) {
+        if (leader_of != w.index) {  // the first row that holds the whole prefix: the others' pages are the same
+            leader = w.g.row0;
+            for (int b0 = 0; b0 < w.g.rows; b0 += 32) {
+                const int b = w.g.row0 + b0 + lane;
+                const bool has = b0 + lane < w.g.rows && row_length(c, b, a.d.status, false) >= w.g.tokens;
+                const uint32_t who = __ballot_sync(0xffffffffu, has);
+                if (who) { leader = w.g.row0 + b0 + __ffs(who) - 1; break; }
+            }
+            leader_of = w.index;
+        }
+        const int32_t *const table = c.block_table + (size_t)leader * c.max_pages;
+        auto page_of = [&](int tile) {  // lane i: of box i
+            int page = -1;
+            if (lane < boxes) page = table[(tile * kT + lane * rows_a_box) >> c.page_shift];
+            if (page >= c.num_pages) {
+                report_error(a.d.status, KDA_ERR_DEVICE_INPUT, leader);
+                page = -1;
+            }
+            return page;
+        };
+        int tile = w.rows > kT ? w.step : 2 * w.step;
+        const int end = tile + tiles_in(w);
+        int next = page_of(tile);
+        for (; tile < end; ++tile) {
+            const int page = next;
+            if (tile + 1 < end) next = page_of(tile + 1);
+            ok = turn == 0 || wait_warp(&empty[slot], (turn - 1) & 1, B);
+            if (!ok) break;
+            const uint32_t missing = __ballot_sync(0xffffffffu, lane < boxes && page < 0);
+            uint32_t live = 0xffffu;
+            for (uint32_t left = missing; left; left &= left - 1)
+                live &= ~(((1u << (rows_a_box / 8)) - 1) << ((__ffs(left) - 1) * rows_a_box / 8));
+            if (keys && lane == 0) B->live[count % kLive] = live;
+            const uint32_t dst = base + slot * kTile;
+            const int row = (tile * kT) & (c.page_size - 1);
+            if (tma) {
+                if (missing) {  // clear their rows
+                    for (int i = 0; i < boxes; ++i) {
+                        if (!((missing >> i) & 1)) continue;
+                        for (int half = 0; half < 2; ++half)
+                            for (int e = lane; e < rows_a_box * 8; e += 32)
+                                *reinterpret_cast<uint4 *>(smem + (place0 + slot) * kTile + half * kHalf + i * rows_a_box * 128 + e * 16) =
+                                    make_uint4(0, 0, 0, 0);
+                    }
+                    fence_async_smem();
+                    __syncwarp();
+                }
+                if (lane == 0) expect_tx(&full[slot], 2 * (boxes - __popc(missing)) * rows_a_box * 128);
+                __syncwarp();
+                for (int i = 0; i < boxes; ++i) {
+                    const int pg = __shfl_sync(0xffffffffu, page, i);
+                    if (pg < 0) continue;
+                    tma_load(dst + i * rows_a_box * 128, map, 0, row, w.head, pg, &full[slot]);
+                    tma_load(dst + kHalf + i * rows_a_box * 128, map, 64, row, w.head, pg, &full[slot]);
+                }
+            } else {
+                // two tokens at a time, a half-warp for each
+                const int sub = lane >> 4, chunk = lane & 15;
+                const uint32_t to = dst + (chunk >> 3) * kHalf + sub * 128;
+                for (int i = 0; i < boxes; ++i) {
+                    const int pg = __shfl_sync(0xffffffffu, page, i);
+                    const __nv_bfloat16 *src = cache + (pg < 0 ? 0 : pg * page_stride + ((int64_t)w.head * c.page_size + row) * kHeadDim) +
+                                               sub * kHeadDim + chunk * 8;
+                    const uint32_t bytes = pg < 0 ? 0 : 16;  // (0: zeros)
+                    for (int r = 0; r < rows_a_box; r += 8, src += 8 * kHeadDim)
+#pragma unroll
+                        for (int u = 0; u < 4; ++u)
+                            cp_async_16(to + (i * rows_a_box + r + 2 * u) * 128 + (((chunk & 7) ^ (2 * u + sub)) << 4), src + 2 * u * kHeadDim, bytes);
+                }
+                asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(&full[slot])) : "memory");
+                if (lane == 0) mbar_arrive(&full[slot]);
+            }
+            ++count;
+            if (++slot == ring) slot = 0, ++turn;
+        }
+    }
+    if (!tma) {
+        cp_async_wait<0>();
+    } else if (!ok) {  // what was asked for has to arrive before the CTA leaves
+        for (uint32_t i = count > ring ? count - ring : 0; i < count; ++i) mbar_wait(&full[i % ring], (i / ring) & 1);
+    }
+}
+
+// The products of group g of warps, issued by one warp: S = Q K^T of a step behind O += P V of the one before. Both
+// groups' warps pass every place of the rings, in order, and free it, so that neither is ever two turns of a ring
+// ahead of the other (the barriers' parity could not tell).
+__device__ __forceinline__ void issue_products(const AttnPrefixArgs &a, Walk w, int g, uint8_t *smem, Bars *B) {
+    const uint32_t base = smem_addr(smem), tmem = B->tmem, col_s = tmem + kColS + 128 * g, col_o = tmem + kColO + 128 * g;
+    const bool copies = a.d.c.page_size < kTmaPage;  // (their writes are not yet the tensor core's to see)
+    const uint64_t dq = at(kDescK, base + kQ + g * kTile);
+    uint32_t k_slot = 0, k_turn = 0, v_slot = 0, v_turn = 0;  // the next places
+    uint32_t used = 0, queries = 0;                           // tiles, and segments, of this group
+    bool ok = true;
+    for (; ok && w.left > 0; next_segment(a, w)) {
+        const bool shared = w.rows > kT;
+        const int tiles = tiles_in(w), steps = steps_in(w, g);
+        // the tiles of step i that are the other group's alone: before (or after) this one's
+        auto skip = [&](int i, int other, uint32_t ring, uint32_t place0, uint32_t &slot, uint32_t &turn) {
+            if (shared || other == g || 2 * i + other >= tiles) return true;
+            if (!wait_warp(&B->full[place0 + slot], turn & 1, B)) return false;
+            arrive_warp(&B->empty[place0 + slot]);
+            if (++slot == ring) slot = 0, ++turn;
+            return true;
+        };
+        // the scores of half the tokens of step i's tile
+        auto scores = [&](int i, int half) {
+            if (half == 0 && !skip(i, 0, kKeyRing, 0, k_slot, k_turn)) return false;
+            if (i < steps) {
+                if (half == 0) {
+                    if (!wait_warp(&B->full[k_slot], k_turn & 1, B)) return false;
+                    if (copies) fence_async_smem();
+                }
+                const uint64_t dk = at(kDescK, base + k_slot * kTile + half * (kHalf / 2));
+#pragma unroll
+                for (int s = 0; s < 8; ++s) {
+                    const uint32_t off = ((s >> 2) * kHalf + (s & 3) * 32) >> 4;
+                    mma_ss(col_s + 64 * half, dq + off, dk + off, kIdescS, s > 0);
+                }
+                commit(&B->s[g][half]);
+                if (half == 1) {
+                    commit(&B->empty[k_slot]);
+                    if (++k_slot == kKeyRing) k_slot = 0, ++k_turn;
+                }
+            }
+            return half == 0 || skip(i, 1, kKeyRing, 0, k_slot, k_turn);
+        };
+        if (steps > 0) {
+            ok = wait_warp(&B->q[g], queries & 1, B);
+            ++queries;
+            tc_fence_after();
+        }
+        ok = ok && scores(0, 0) && scores(0, 1);
+        for (int i = 0; ok && i < w.n; ++i) {
+            ok = skip(i, 0, kValueRing, kKeyRing, v_slot, v_turn);
+            const bool own = i < steps;
+            if (ok && own) {
+                ok = wait_warp(&B->full[kKeyRing + v_slot], v_turn & 1, B);
+                if (copies) fence_async_smem();
+            }
+            const uint64_t dv = at(kDescV, base + (kKeyRing + v_slot) * kTile);
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                if (ok && own) {
+                    ok = wait_warp(&B->p[g][half], used & 1, B);
+                    if (!ok) break;
+                    tc_fence_after();
+#pragma unroll
+                    for (int s = 0; s < 4; ++s)
+                        mma_ts(col_o, col_s + 64 * half + 8 * s, dv + (4 * half + s) * 128, kIdescO, i > 0 || half > 0 || s > 0);
+                    commit(&B->o[g][half]);
+                    if (half == 1) commit(&B->empty[kKeyRing + v_slot]);
+                }
+                ok = ok && (i + 1 >= w.n || scores(i + 1, half));
+            }
+            if (!ok) break;
+            if (own) {
+                ++used;
+                if (++v_slot == kValueRing) v_slot = 0, ++v_turn;
+            }
+            ok = skip(i, 1, kValueRing, kKeyRing, v_slot, v_turn);
+        }
+    }
+    commit(&B->drain[g]);  // every earlier product is done when this arrives
+    mbar_wait(&B->drain[g], 0);
+}
+
 __global__ void __launch_bounds__(kThreads, 1)
     kda_attn_prefix_kernel(const AttnPrefixArgs a, const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v) {
     extern __shared__ __align__(1024) uint8_t smem[];
@@ -176,26 +400,36 @@ __global__ void __launch_bounds__(kThreads, 1)
         return;
     }
     if (threadIdx.x == 0) {
-        for (int i = 0; i < kRing; ++i) mbar_init(&B->full[i], 1), mbar_init(&B->empty[i], 1);
-        for (int w = 0; w < 2; ++w) mbar_init(&B->q[w], 4), mbar_init(&B->s[w], 1), mbar_init(&B->p[w], 4), mbar_init(&B->o[w], 1);
-        mbar_init(&B->drain, 1);
+        // (a place is freed by both groups' warps)
+        for (int i = 0; i < kRing; ++i) mbar_init(&B->full[i], c.page_size >= kTmaPage ? 1 : 33), mbar_init(&B->empty[i], 2);
+        for (int w = 0; w < 2; ++w) {
+            mbar_init(&B->q[w], 4);
+            for (int h = 0; h < 2; ++h) mbar_init(&B->s[w][h], 1), mbar_init(&B->p[w][h], 4), mbar_init(&B->o[w][h], 1);
+        }
+        mbar_init(&B->drain[0], 1), mbar_init(&B->drain[1], 1);
         B->abort = 0;
         fence_mbar_init();
         prefetch_map(&map_k);
         prefetch_map(&map_v);
     }
+    if (warp == kWarpMma) {
+        tmem_alloc(&B->tmem, kTmemCols);
+        tmem_relinquish();
+        tc_fence_before();
+    }
     wait_for_prior();
     allow_next();
 
     // ---- the steps of all groups, and where this CTA's share begins
-    auto steps_of = [&](int g) { return g < a.groups ? (int64_t)c.num_kv_heads * head_steps(a, group_at(a, g)) : 0; };
     bool bad = false;
-    for (int g = threadIdx.x; g < a.groups; g += kThreads) {
+    auto steps_of = [&](int g) {
+        if (g >= a.groups) return (int64_t)0;
         const int lo = a.cu_groups[g], hi = a.cu_groups[g + 1], n = a.prefix_lens[g];
-        bad |= lo < 0 || hi < lo || hi > c.batch;
-        if (cta == 0 && (lo < 0 || hi < lo || hi > c.batch || n < 0 || n > c.capacity)) report_error(p.status, KDA_ERR_DEVICE_INPUT, g);
-    }
-    bad = __syncthreads_or(bad);  // then nothing is taken as shared: the rows' own tables hold all of their tokens
+        const bool wrong = lo < 0 || hi < lo || hi > c.batch;
+        if (cta == 0 && (wrong || n < 0 || n > c.capacity)) report_error(p.status, KDA_ERR_DEVICE_INPUT, g);
+        bad |= wrong;
+        return wrong ? 0 : (int64_t)c.num_kv_heads * head_steps(a, group_of(a, lo, hi, n));
+    };
     auto block_sum = [&](int64_t x, int64_t &before) {
         int64_t sum = x;
 #pragma unroll
@@ -203,330 +437,209 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int64_t y = __shfl_up_sync(0xffffffffu, sum, o);
             if (lane >= o) sum += y;
         }
-        __syncthreads();
         if (lane == 31) B->sums[warp] = sum;
         __syncthreads();
-        int64_t total = 0;
+        int64_t total = lane < kThreads / 32 ? B->sums[lane] : 0;
         before = sum - x;
+        int64_t low = lane < warp ? total : 0;
 #pragma unroll
-        for (int w = 0; w < kThreads / 32; ++w) {
-            if (w < warp) before += B->sums[w];
-            total += B->sums[w];
+        for (int o = 16; o > 0; o >>= 1) {
+            total += __shfl_xor_sync(0xffffffffu, total, o);
+            low += __shfl_xor_sync(0xffffffffu, low, o);
         }
+        before += low;
         return total;
     };
     int64_t mine = 0, before0 = 0;
-    if (!bad)
-        for (int g = threadIdx.x; g < a.groups; g += kThreads) mine += steps_of(g);
-    const int64_t total = block_sum(mine, before0), per = max((total + ctas - 1) / ctas, (int64_t)1);
-    const int64_t lo = min(cta * per, total), hi = min(lo + per, total);
+    for (int g = threadIdx.x; g < a.groups; g += kThreads) mine += steps_of(g);
+    bad = __syncthreads_or(bad);  // then nothing is taken as shared: the rows' own tables hold all of their tokens
+    const int64_t all = block_sum(mine, before0);
+    bad |= all > 0x3fffffff;  // (tables that repeat their pages very often: places are 32-bit numbers below)
+    const int total = bad ? 0 : (int)all, per = max((total + ctas - 1) / ctas, 1);
+    const int lo = min(cta * per, total), hi = min(lo + per, total);
     if (lo < hi) {
         int64_t first = 0;
         for (int g0 = 0; g0 < a.groups; g0 += kThreads) {
-            int64_t x = mine, before = before0, sum = total;
-            if (a.groups > kThreads) x = steps_of(g0 + threadIdx.x), sum = block_sum(x, before);
+            int64_t x = mine, before = before0, sum = all;
+            if (a.groups > kThreads) {
+                x = steps_of(g0 + threadIdx.x);
+                __syncthreads();  // (the sums have been read)
+                sum = block_sum(x, before);
+            }
             const int64_t off = lo - first - before;
-            if (off >= 0 && off < x) B->group = g0 + threadIdx.x, B->offset = off;
+            if (off >= 0 && off < x) B->group = g0 + threadIdx.x, B->offset = (int)off;
             first += sum;
         }
     }
-    // ---- each row's start: this CTA's of every group's rows
-    if (!bad) {
-        for (int g = threadIdx.x; g < a.groups; g += kThreads) {
-            const Group x = group_at(a, g);
-            for (int b = x.row0 + cta; b < x.row0 + x.rows; b += ctas)
-                a.x.start[b] = row_length(c, b, p.status, true) >= x.tokens ? x.tiles * kT : 0;
-        }
-    }
-    // rows of no group
-    {
-        const int from = bad ? c.batch : a.cu_groups[0], to = bad ? c.batch : a.cu_groups[a.groups];
-        for (int b = cta * kThreads + threadIdx.x; b < c.batch; b += ctas * kThreads)
-            if (b < from || b >= to) a.x.start[b] = 0;
-    }
-    __syncthreads();
-    if (lo >= hi) return;
-
-    if (warp == kWarpMma) {
-        tmem_alloc(&B->tmem, kTmemCols);
-        tmem_relinquish();
-        tc_fence_before();
-    }
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = B->tmem, base = smem_addr(smem);
+    const uint32_t tmem = B->tmem;
     Walk w;
-    w.index = B->group;
-    w.g = group_at(a, w.index);
     w.left = hi - lo;
-    {
-        const int64_t per_head = head_steps(a, w.g), off = B->offset;
-        w.head = (int)(off / per_head);
-        const int64_t in_head = off - w.head * per_head;
-        const int pairs = (query_rows(a, w.g) + kPrefixSlots - 1) / kPrefixSlots;
-        w.pair = (int)min(in_head / w.g.tiles, (int64_t)(pairs - 1));
-        w.step = (int)(in_head - (int64_t)w.pair * w.g.tiles);
+    if (w.left > 0) {
+        w.index = B->group;
+        w.g = group_at(a, w.index);
+        const int per_head = (int)head_steps(a, w.g), pairs = (query_rows(a, w.g) + kPrefixSlots - 1) / kPrefixSlots;
+        w.head = B->offset / per_head;
+        const int in_head = B->offset - w.head * per_head;
+        w.pair = min(in_head / w.g.tiles, pairs - 1);
+        w.step = in_head - w.pair * w.g.tiles;
         w.first = lo - w.step;
         set_item(a, w);
     }
-    // Tiles of tokens: a step's are tile s for both groups of warps, or 2 s + i for group i (if there is one).
-    // In the ring a step has its keys, then its values.
-
-    if (warp == kWarpLoad) {
-        const int rows_a_box = min(c.page_size, kT), boxes = kT / rows_a_box;
-        const int sub = lane >> 1, half = lane & 1;  // this lane's box
-        const bool on = sub < boxes;
-        int leader = -1, leader_of = -1;
-        uint32_t count = 0;  // tiles so far
-        bool ok = true;
-        for (; ok && w.left > 0; next_segment(a, w)) {
-            if (leader_of != w.index) {  // the first row that holds the whole prefix: the others' pages are the same
-                leader = w.g.row0;
-                for (int b0 = 0; b0 < w.g.rows; b0 += 32) {
-                    const int b = w.g.row0 + b0 + lane;
-                    const bool has = b0 + lane < w.g.rows && row_length(c, b, p.status, false) >= w.g.tokens;
-                    const uint32_t who = __ballot_sync(0xffffffffu, has);
-                    if (who) { leader = w.g.row0 + b0 + __ffs(who) - 1; break; }
+    if (warp >= kWarpKeys) {
+        if (warp < kWarpMma) {
+            load_tiles(a, w, warp == kWarpKeys ? &map_k : &map_v, warp == kWarpKeys, smem, B);
+        } else {
+            if (warp != kWarpMma) {
+                // each row's start: this CTA's of every group's rows, and of the rows of no group
+                if (!bad) {
+                    for (int g = lane; g < a.groups; g += 32) {
+                        const Group x = group_at(a, g);
+                        for (int b = x.row0 + cta; b < x.row0 + x.rows; b += ctas)
+                            a.x.start[b] = row_length(c, b, p.status, true) >= x.tokens ? x.tiles * kT : 0;
+                    }
                 }
-                leader_of = w.index;
+                const int from = bad ? c.batch : a.cu_groups[0], to = bad ? c.batch : a.cu_groups[a.groups];
+                for (int b = cta * 32 + lane; b < c.batch; b += ctas * 32)
+                    if (b < from || b >= to) a.x.start[b] = 0;
             }
-            const int32_t *const table = c.block_table + (size_t)leader * c.max_pages;
-            const bool shared = w.rows > kT;
-            auto page_of = [&](int tile) {
-                int page = -1;
-                if (on) page = table[(tile * kT + sub * rows_a_box) >> c.page_shift];
-                if (page >= c.num_pages) {
-                    report_error(p.status, KDA_ERR_DEVICE_INPUT, leader);
-                    page = -1;
-                }
-                return page;
-            };
-            auto load = [&](const CUtensorMap *map, int tile, int page, bool keys) {
-                const int slot = count % kRing;
-                if (count >= kRing && !wait_warp(&B->empty[slot], (count / kRing - 1) & 1, B)) return false;
-                const uint32_t dst = base + slot * kTile + half * kHalf + sub * rows_a_box * 128;
-                const uint32_t missing = __ballot_sync(0xffffffffu, on && page < 0);
-                uint32_t live = 0xffffu;
-                if (missing) {
-                    for (int i = 0; i < boxes; ++i)
-                        if ((missing >> (2 * i)) & 1) live &= ~(((1u << (rows_a_box / 8)) - 1) << (i * rows_a_box / 8));
-                    if (on && page < 0)
-                        for (int i = 0; i < rows_a_box * 8; ++i)
-                            *reinterpret_cast<uint4 *>(smem + (dst - base) + i * 16) = make_uint4(0, 0, 0, 0);
-                    fence_async_smem();
-                    __syncwarp();
-                }
-                if (lane == 0) {
-                    if (keys) B->live[count % kLive] = live;
-                    expect_tx(&B->full[slot], (2 * boxes - __popc(missing)) * rows_a_box * 128);
-                }
-                __syncwarp();
-                if (on && page >= 0) tma_load(dst, map, 64 * half, (tile * kT) & (c.page_size - 1), w.head, page, &B->full[slot]);
-                ++count;
-                return true;
-            };
-            int t = shared ? w.step : 2 * w.step;
-            int page0 = page_of(t), page1 = shared || t + 1 >= w.g.tiles ? -1 : page_of(t + 1);
-            for (int i = 0; ok && i < w.n; ++i) {
-                const int now0 = page0, now1 = page1, now = t;
-                const bool two = !shared && now + 1 < w.g.tiles;
-                t += shared ? 1 : 2;
-                if (i + 1 < w.n) {
-                    page0 = page_of(t);
-                    if (!shared && t + 1 < w.g.tiles) page1 = page_of(t + 1);
-                }
-                ok = load(&map_k, now, now0, true) && (!two || load(&map_k, now + 1, now1, true)) && load(&map_v, now, now0, false) &&
-                     (!two || load(&map_v, now + 1, now1, false));
-            }
+            issue_products(a, w, warp - kWarpMma, smem, B);
         }
-        if (!ok)  // what was asked for has to arrive before the CTA leaves
-            for (uint32_t i = count > kRing ? count - kRing : 0; i < count; ++i) mbar_wait(&B->full[i % kRing], (i / kRing) & 1);
-    } else if (warp == kWarpMma) {
-        uint32_t count = 0, used[2] = {0, 0}, queries[2] = {0, 0};
-        bool ok = true;
-        for (; ok && w.left > 0; next_segment(a, w)) {
-            const bool shared = w.rows > kT;
-            // step i of the segment: its tiles in the ring, and whether group g has one
-            auto has = [&](int i, int g) { return shared || g == 0 || 2 * (w.step + i) + 1 < w.g.tiles; };
-            auto keys_at = [&](int i, int g) { return count + (shared ? 2 * i : 4 * i + g); };
-            auto values_at = [&](int i, int g) { return count + (shared ? 2 * i + 1 : 4 * i + (has(i, 1) ? 2 : 1) + g); };
-            auto scores = [&](int i, int g) {
-                if (!has(i, g)) return true;
-                const uint32_t k = keys_at(i, g), slot = k % kRing;
-                if (!wait_warp(&B->full[slot], (k / kRing) & 1, B)) return false;
-                const uint64_t dq = at(kDescK, base + kQ + g * kTile), dk = at(kDescK, base + slot * kTile);
-#pragma unroll
-                for (int s = 0; s < 8; ++s) {
-                    const uint32_t off = ((s >> 2) * kHalf + (s & 3) * 32) >> 4;
-                    mma_ss(tmem + kColS + 128 * g, dq + off, dk + off, kIdescS, s > 0);
-                }
-                commit(&B->s[g]);
-                if (!shared || g == 1) commit(&B->empty[slot]);
-                return true;
-            };
-            auto products = [&](int i, int g) {
-                if (!has(i, g)) return true;
-                const uint32_t v = values_at(i, g), slot = v % kRing;
-                if (!wait_warp(&B->full[slot], (v / kRing) & 1, B) || !wait_warp(&B->p[g], used[g] & 1, B)) return false;
-                ++used[g];
-                tc_fence_after();
-                const uint64_t dv = at(kDescV, base + slot * kTile);
-#pragma unroll
-                for (int s = 0; s < 8; ++s)
-                    mma_ts(tmem + kColO + 128 * g, tmem + kColS + 128 * g + 8 * s, dv + s * 128, kIdescO, i > 0 || s > 0);
-                commit(&B->o[g]);
-                if (!shared || g == 1) commit(&B->empty[slot]);
-                return true;
-            };
-            for (int g = 0; ok && g < 2; ++g) {
-                if (!has(0, g)) continue;
-                ok = wait_warp(&B->q[g], queries[g] & 1, B);
-                ++queries[g];
-            }
-            if (!ok) break;
-            tc_fence_after();
-            ok = scores(0, 0) && scores(0, 1);
-            for (int i = 0; ok && i < w.n; ++i) {
-                ok = products(i, 0) && (i + 1 >= w.n || scores(i + 1, 0));
-                ok = ok && products(i, 1) && (i + 1 >= w.n || scores(i + 1, 1));
-            }
-            const int last = w.step + w.n - 1;
-            count += shared ? 2 * w.n : 4 * w.n - (2 * last + 1 < w.g.tiles ? 0 : 2);
-        }
-        commit(&B->drain);  // every earlier product is done when this arrives
-        mbar_wait(&B->drain, 0);
     } else {
         const int g = warp >> 2, quad = warp & 3, r = 32 * quad + lane;  // the group of warps; the row of its tile
-        const uint32_t lanes = tmem + ((uint32_t)(32 * quad) << 16), col_s = lanes + kColS + 128 * g, col_o = lanes + kColO + 128 * g;
+        const uint32_t lanes = tmem + ((uint32_t)(32 * quad) << 16) + 128 * g, col_s = lanes + kColS, col_o = lanes + kColO;
         const float scale2 = fabsf(p.scale) * kLog2e;
-        const uint32_t flip = p.scale < 0.0f ? 0x80008000u : 0u;  // (the scale's sign goes to the queries)
-        uint32_t count = 0, used = 0;  // tiles in the ring; tiles of this group
+        uint32_t count = 0, used = 0;  // tiles before the segment; tiles of this group
         bool ok = true;
         for (; ok && w.left > 0; next_segment(a, w)) {
             const bool shared = w.rows > kT;
             const int mine = shared ? g * kT + r : r;  // the query row of the item
             const bool valid = mine < w.rows;
             const int in_group = w.pair * kPrefixSlots + mine, row = in_group / p.group;
-            const int64_t head = (int64_t)(w.g.row0 + row) * p.num_q_heads + w.head * p.group + (in_group - row * p.group);
-            // (a group of warps without a tile writes no queries: it could come by here again before the other)
-            if (shared || g == 0 || 2 * w.step + 1 < w.g.tiles) {
-                const uint4 *const src = reinterpret_cast<const uint4 *>(p.q + head * kHeadDim);
+            const int head = (w.g.row0 + row) * p.num_q_heads + w.head * p.group + (in_group - row * p.group);
+            const int steps = steps_in(w, g);
+            if (steps > 0) {  // (a group without a tile writes no queries: it could come by here again before the other)
+                const uint32_t flip = p.scale < 0.0f ? 0x80008000u : 0u;  // (the scale's sign goes to the queries)
+                const uint4 *const src = reinterpret_cast<const uint4 *>(p.q + (int64_t)head * kHeadDim);
                 uint8_t *const dst = smem + kQ + g * kTile + r * 128;
+                uint4 x[16];
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    uint4 x = make_uint4(0, 0, 0, 0);
-                    if (valid) x = __ldg(src + i);
-                    x.x ^= flip, x.y ^= flip, x.z ^= flip, x.w ^= flip;
-                    *reinterpret_cast<uint4 *>(dst + (i >> 3) * kHalf + (((i & 7) ^ (r & 7)) << 4)) = x;
-                }
+                for (int i = 0; i < 16; ++i) x[i] = valid ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    *reinterpret_cast<uint4 *>(dst + (i >> 3) * kHalf + (((i & 7) ^ (r & 7)) << 4)) =
+                        make_uint4(x[i].x ^ flip, x[i].y ^ flip, x[i].z ^ flip, x[i].w ^ flip);
                 fence_async_smem();
                 arrive_warp(&B->q[g]);
             }
             if (valid && w.step == 0 && (shared || g == 0)) {
                 // this segment begins the item: where its other parts will be
-                const int64_t last = (w.first + w.steps - 1) / per;
                 PrefixCut cut;
                 cut.per = shared ? 1 : 2;
-                cut.slot = shared ? g * kT + r : r;
+                cut.slot = mine;
                 cut.cta = cta + 1;
-                cut.ctas = (int)(last - cta);
+                cut.ctas = (w.first + w.steps - 1) / per - cta;
                 a.x.cuts[head] = cut;
             }
             float m = kNegInf, l = 0.0f;
-            bool any = false;
-            for (int i = 0; ok && i < w.n; ++i) {
-                if (!(shared || g == 0 || 2 * (w.step + i) + 1 < w.g.tiles)) break;  // (the item's last step)
-                ok = wait_warp(&B->s[g], used & 1, B);
-                if (!ok) break;
-                tc_fence_after();
-                const uint32_t live = *reinterpret_cast<volatile uint32_t *>(&B->live[(count + (shared ? 2 * i : 4 * i + g)) % kLive]);
-                float s[4][32];
-#pragma unroll
-                for (int b = 0; b < 4; ++b) tmem_ld32(col_s + 32 * b, s[b]);
-                tmem_wait_ld();
-                if (live != 0xffffu) {
-#pragma unroll
-                    for (int b = 0; b < 4; ++b)
-#pragma unroll
-                        for (int j = 0; j < 32; ++j)
-                            if (!((live >> (4 * b + (j >> 3))) & 1)) s[b][j] = kNegInf;
-                }
-                float top[4];
-#pragma unroll
-                for (int b = 0; b < 4; ++b) {
-                    top[b] = s[b][0];
-#pragma unroll
-                    for (int j = 1; j < 32; ++j) top[b] = fmaxf(top[b], s[b][j]);
-                }
-                // (NaN scores are passed over, and make their row's sum NaN)
-                const float now = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * scale2;
-                const bool grow = !any ? true : now > m + kSlack;
-                if (!any) {
-                    m = now == now ? now : kNegInf;  // (-inf * 0)
-                    any = true;
-                } else if (__any_sync(0xffffffffu, grow)) {
-                    const float to = fmaxf(m, now), f = to == kNegInf ? 1.0f : ex2(m - to);
-                    ok = wait_warp(&B->o[g], (used - 1) & 1, B);
+            for (int i = 0; ok && i < steps; ++i, ++used) {
+                const uint32_t mask = count + (shared ? i : 2 * i + g);
+#pragma unroll 1
+                for (int half = 0; half < 2; ++half) {
+                    const uint32_t col = col_s + 64 * half;
+                    ok = wait_warp(&B->s[g][half], used & 1, B);
                     if (!ok) break;
                     tc_fence_after();
+                    float s[2][32], sc = scale2;
+                    tmem_ld32(col, s[0]);
+                    tmem_ld32(col + 32, s[1]);
+                    const uint32_t live = (*reinterpret_cast<volatile uint32_t *>(&B->live[mask % kLive]) >> (8 * half)) & 0xffu;
+                    tmem_wait_ld();
+                    if (live != 0xffu) {
+                        const bool zero = scale2 == 0.0f;  // (then -inf would not stay what it is)
+                        if (zero) sc = 1.0f;
 #pragma unroll
-                    for (int b = 0; b < 8; ++b) {
-                        float o[16];
-                        tmem_ld16(col_o + 16 * b, o);
-                        tmem_wait_ld();
+                        for (int b = 0; b < 2; ++b)
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) o[j] *= f;
-                        tmem_st16(col_o + 16 * b, o);
+                            for (int j = 0; j < 32; ++j)
+                                s[b][j] = (live >> (4 * b + (j >> 3))) & 1 ? (zero ? s[b][j] * 0.0f : s[b][j]) : kNegInf;
                     }
-                    l *= f;
-                    m = to;
-                }
-                const float ref = m == kNegInf ? 0.0f : m;
-                float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                    float top[4];
 #pragma unroll
-                for (int b = 0; b < 4; ++b) {
-                    float pk[16];
+                    for (int b = 0; b < 4; ++b) {
+                        const float *const x = &s[b >> 1][16 * (b & 1)];
+                        top[b] = fmaxf(x[0], x[15]);
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        float x0 = ex2(fmaf(s[b][2 * j], scale2, -ref)), x1 = ex2(fmaf(s[b][2 * j + 1], scale2, -ref));
-                        if (live != 0xffffu && !((live >> (4 * b + (j >> 2))) & 1)) x0 = x1 = 0.0f;
-                        sum[j & 1] += x0;
-                        sum[2 + (j & 1)] += x1;
-                        pk[j] = __uint_as_float(pack_bf16(x0, x1));
+                        for (int j = 1; j < 15; j += 2) top[b] = max3(top[b], x[j], x[j + 1]);
                     }
-                    tmem_st16(col_s + 16 * b, pk);
+                    // (NaN scores are passed over, and make their row's sum NaN)
+                    const float now = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * sc;
+                    if (i == 0 && half == 0) {
+                        m = fmaxf(m, now);
+                    } else if (__any_sync(0xffffffffu, now > m + kSlack)) {
+                        const float to = fmaxf(m, now), f = to == kNegInf ? 1.0f : ex2(m - to);
+                        ok = wait_warp(&B->o[g][half ^ 1], (used - 1 + half) & 1, B);  // of the half tile before this one
+                        if (!ok) break;
+                        tc_fence_after();
+#pragma unroll 1
+                        for (int b = 0; b < 8; ++b) {
+                            float o[16];
+                            tmem_ld16(col_o + 16 * b, o);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) o[j] *= f;
+                            tmem_st16(col_o + 16 * b, o);
+                        }
+                        l *= f;
+                        m = to;
+                    }
+                    const float ref = m == kNegInf ? 0.0f : -m;
+                    const float2 by = make_float2(sc, sc), less = make_float2(ref, ref);
+                    float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+#pragma unroll
+                    for (int b = 0; b < 2; ++b) {
+                        float pk[16];
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) {
+                            float2 x = fma2(make_float2(s[b][2 * j], s[b][2 * j + 1]), by, less);
+                            x = make_float2(ex2(x.x), ex2(x.y));
+                            sum[j & 1] = add2(sum[j & 1], x);
+                            pk[j] = __uint_as_float(pack_bf16(x.x, x.y));
+                        }
+                        tmem_st16(col + 16 * b, pk);
+                    }
+                    sum[0] = add2(sum[0], sum[1]);
+                    l += sum[0].x + sum[0].y;
+                    tmem_wait_st();
+                    tc_fence_before();
+                    arrive_warp(&B->p[g][half]);
                 }
-                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-                tmem_wait_st();
-                tc_fence_before();
-                arrive_warp(&B->p[g]);
-                ++used;
             }
             if (!ok) break;
-            const int last = w.step + w.n - 1;
-            count += shared ? 2 * w.n : 4 * w.n - (2 * last + 1 < w.g.tiles ? 0 : 2);
+            count += tiles_in(w);
             // ---- the segment's part
-            if (any) {
-                ok = wait_warp(&B->o[g], (used - 1) & 1, B);
+            const int64_t part = w.step == 0 ? (shared ? 0 : (int64_t)g * a.x.heads) + head
+                                             : 3 * (int64_t)a.x.heads + (int64_t)cta * kPrefixSlots + g * kT + r;
+            if (steps > 0) {
+                ok = wait_warp(&B->o[g][1], (used - 1) & 1, B);
                 if (!ok) break;
                 tc_fence_after();
             }
-            const int64_t part = w.step == 0 ? (shared ? 0 : (int64_t)g * a.x.heads) + head
-                                             : 3 * (int64_t)a.x.heads + (int64_t)cta * kPrefixSlots + g * kT + r;
             if (valid) a.x.ml[part] = make_float2(m, l);
             float4 *const dst = reinterpret_cast<float4 *>(a.x.o + part * kHeadDim);
 #pragma unroll
-            for (int b = 0; b < 8; ++b) {
-                float o[16];
+            for (int b = 0; b < 4; ++b) {
+                float o[32];
 #pragma unroll
-                for (int j = 0; j < 16; ++j) o[j] = 0.0f;
-                if (any) {
-                    tmem_ld16(col_o + 16 * b, o);
+                for (int j = 0; j < 32; ++j) o[j] = 0.0f;
+                if (steps > 0) {
+                    tmem_ld32(col_o + 32 * b, o);
                     tmem_wait_ld();
                 }
                 if (valid)
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) dst[4 * b + j] = make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+                    for (int j = 0; j < 8; ++j) dst[8 * b + j] = make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
             }
             tc_fence_before();
         }
