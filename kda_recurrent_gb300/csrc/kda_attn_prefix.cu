@@ -56,6 +56,7 @@ struct Bars {
     uint64_t full[kRing], empty[kRing];  // of the keys' places, then the values'
     // of each group of warps: queries written (4 warps); for half a tile's tokens: scores done, probabilities written
     // (4 warps); P V done
+    // (for the last tile of a segment)
     uint64_t q[2], s[2][2], p[2][2], o[2][2];
     uint64_t drain[2];
     uint32_t live[kLive];  // of a tile of keys: a bit for eight tokens
@@ -114,21 +115,29 @@ __device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap *map, i
         : "memory");
 }
 
-// Wait of a warp, bounded, with one decision for all its lanes.
-__device__ __forceinline__ bool wait_warp(uint64_t *bar, uint32_t parity, Bars *B) {
-    const uint32_t addr = smem_addr(bar);
+__device__ __forceinline__ uint32_t try_wait(const uint64_t *bar, uint32_t parity) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(smem_addr(bar)), "r"(parity), "r"(kSuspendHintNs)
+        : "memory");
+    return done;
+}
+
+// Wait of a warp for up to three phases, bounded, with one decision for all its lanes. (One after the other, waits for
+// phases that are long complete take some 150 cycles each.)
+template <int kCount>
+__device__ __forceinline__ bool wait_all(uint64_t *const (&bar)[kCount], const uint32_t (&parity)[kCount], Bars *B) {
     volatile int32_t *const abort = &B->abort;
     uint64_t since = 0;
     bool ok = true;
     for (;;) {
-        uint32_t done;
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t"
-            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-            "selp.u32 %0, 1, 0, p;\n\t}"
-            : "=r"(done)
-            : "r"(addr), "r"(parity), "r"(kSuspendHintNs)
-            : "memory");
+        uint32_t done = 1;
+#pragma unroll
+        for (int i = 0; i < kCount; ++i) done &= try_wait(bar[i], parity[i]);
         if (__all_sync(0xffffffffu, done)) break;
         const uint64_t now = global_ns();
         if (since == 0) since = now;
@@ -136,6 +145,12 @@ __device__ __forceinline__ bool wait_warp(uint64_t *bar, uint32_t parity, Bars *
         if (__any_sync(0xffffffffu, *abort)) { ok = false; break; }
     }
     return ok;
+}
+
+__device__ __forceinline__ bool wait_warp(uint64_t *bar, uint32_t parity, Bars *B) {
+    uint64_t *const bars[1] = {bar};
+    const uint32_t parities[1] = {parity};
+    return wait_all(bars, parities, B);
 }
 
 // A group's query rows and tiles of shared tokens (0: nothing is shared), and the steps of one key head.
@@ -209,7 +224,7 @@ __device__ __forceinline__ int steps_in(const Walk &w, int g) { return w.rows > 
 // The loads of the keys' or the values' tiles, by one warp: tile s for step s, or 2 s and 2 s + 1. Large pages come by
 // TMA, a box for each page (or 128 tokens of it) and half of the channels; a box takes about 100 cycles to ask for,
 // so that small pages come faster by 16-byte copies of all lanes.
-__device__ __forceinline__ void load_tiles(const AttnPrefixArgs &a, Walk w, const CUtensorMap *map, bool keys, uint8_t *smem, Bars *B) {
+__device__ __forceinline__ void load_tiles(const AttnPrefixArgs &a, Walk w, int per, const CUtensorMap *map, bool keys, uint8_t *smem, Bars *B) {
     const PagedCache &c = a.d.c;
     const int lane = threadIdx.x & 31, rows_a_box = min(c.page_size, kT), boxes = kT / rows_a_box;
     const uint32_t ring = keys ? kKeyRing : kValueRing, place0 = keys ? 0 : kKeyRing, base = smem_addr(smem) + place0 * kTile;
@@ -217,7 +232,7 @@ __device__ __forceinline__ void load_tiles(const AttnPrefixArgs &a, Walk w, cons
     const __nv_bfloat16 *const cache = keys ? c.k : c.v;
     const int64_t page_stride = keys ? c.k_page_stride : c.v_page_stride;
     const bool tma = c.page_size >= kTmaPage;
-    int leader = -1, leader_of = -1;
+    int leader = -1, leader_of = -1, done = 0;
     uint32_t count = 0, slot = 0, turn = 0;  // tiles so far; the next one's place, and the times that was used
     bool ok = true;
     for (; ok && w.left > 0; next_segment(a, w)) {
@@ -241,12 +256,22 @@ __device__ __forceinline__ void load_tiles(const AttnPrefixArgs &a, Walk w, cons
             }
             return page;
         };
-        int tile = w.rows > kT ? w.step : 2 * w.step;
-        const int end = tile + tiles_in(w);
+        // The order of the tiles is free. CTAs that work on other query rows of the same tokens read them at the same
+        // time, once from HBM, when each begins where its tile's number modulo the length of a share is the number of
+        // steps that it has done.
+        const int begin = w.rows > kT ? w.step : 2 * w.step, tiles = tiles_in(w);
+        int tile = begin;
+        if (w.rows > kT) {
+            int ahead = (done - w.step) % per;
+            if (ahead < 0) ahead += per;
+            if (ahead < tiles) tile += ahead;
+        }
+        done += w.n;
         int next = page_of(tile);
-        for (; tile < end; ++tile) {
-            const int page = next;
-            if (tile + 1 < end) next = page_of(tile + 1);
+        for (int i = 0; i < tiles; ++i) {
+            const int page = next, now = tile;
+            if (++tile == begin + tiles) tile = begin;
+            if (i + 1 < tiles) next = page_of(tile);
             ok = turn == 0 || wait_warp(&empty[slot], (turn - 1) & 1, B);
             if (!ok) break;
             const uint32_t missing = __ballot_sync(0xffffffffu, lane < boxes && page < 0);
@@ -255,7 +280,7 @@ __device__ __forceinline__ void load_tiles(const AttnPrefixArgs &a, Walk w, cons
                 live &= ~(((1u << (rows_a_box / 8)) - 1) << ((__ffs(left) - 1) * rows_a_box / 8));
             if (keys && lane == 0) B->live[count % kLive] = live;
             const uint32_t dst = base + slot * kTile;
-            const int row = (tile * kT) & (c.page_size - 1);
+            const int row = (now * kT) & (c.page_size - 1);
             if (tma) {
                 if (missing) {  // clear their rows
                     for (int i = 0; i < boxes; ++i) {
@@ -325,62 +350,60 @@ __device__ __forceinline__ void issue_products(const AttnPrefixArgs &a, Walk w, 
             if (++slot == ring) slot = 0, ++turn;
             return true;
         };
-        // the scores of half the tokens of step i's tile
-        auto scores = [&](int i, int half) {
-            if (half == 0 && !skip(i, 0, kKeyRing, 0, k_slot, k_turn)) return false;
-            if (i < steps) {
-                if (half == 0) {
-                    if (!wait_warp(&B->full[k_slot], k_turn & 1, B)) return false;
-                    if (copies) fence_async_smem();
-                }
-                const uint64_t dk = at(kDescK, base + k_slot * kTile + half * (kHalf / 2));
+        auto scores = [&](int half) {  // of half the tokens of the next place's tile
+            const uint64_t dk = at(kDescK, base + k_slot * kTile + half * (kHalf / 2));
 #pragma unroll
-                for (int s = 0; s < 8; ++s) {
-                    const uint32_t off = ((s >> 2) * kHalf + (s & 3) * 32) >> 4;
-                    mma_ss(col_s + 64 * half, dq + off, dk + off, kIdescS, s > 0);
-                }
-                commit(&B->s[g][half]);
-                if (half == 1) {
-                    commit(&B->empty[k_slot]);
-                    if (++k_slot == kKeyRing) k_slot = 0, ++k_turn;
-                }
+            for (int s = 0; s < 8; ++s) {
+                const uint32_t off = ((s >> 2) * kHalf + (s & 3) * 32) >> 4;
+                mma_ss(col_s + 64 * half, dq + off, dk + off, kIdescS, s > 0);
             }
-            return half == 0 || skip(i, 1, kKeyRing, 0, k_slot, k_turn);
+            commit(&B->s[g][half]);
+            if (half == 0) return;
+            commit(&B->empty[k_slot]);
+            if (++k_slot == kKeyRing) k_slot = 0, ++k_turn;
         };
-        if (steps > 0) {
-            ok = wait_warp(&B->q[g], queries & 1, B);
+        ok = skip(0, 0, kKeyRing, 0, k_slot, k_turn);
+        if (ok && steps > 0) {
+            uint64_t *const bars[2] = {&B->q[g], &B->full[k_slot]};
+            const uint32_t parities[2] = {queries & 1, k_turn & 1};
+            ok = wait_all(bars, parities, B);
+            if (!ok) break;
             ++queries;
             tc_fence_after();
+            if (copies) fence_async_smem();
+            scores(0);
+            scores(1);
         }
-        ok = ok && scores(0, 0) && scores(0, 1);
+        ok = ok && skip(0, 1, kKeyRing, 0, k_slot, k_turn);
         for (int i = 0; ok && i < w.n; ++i) {
-            ok = skip(i, 0, kValueRing, kKeyRing, v_slot, v_turn);
-            const bool own = i < steps;
-            if (ok && own) {
-                ok = wait_warp(&B->full[kKeyRing + v_slot], v_turn & 1, B);
-                if (copies) fence_async_smem();
-            }
-            const uint64_t dv = at(kDescV, base + (kKeyRing + v_slot) * kTile);
+            ok = skip(i, 0, kValueRing, kKeyRing, v_slot, v_turn) && (i + 1 == w.n || skip(i + 1, 0, kKeyRing, 0, k_slot, k_turn));
+            if (!ok) break;
+            if (i < steps) {
+                const bool more = i + 1 < steps;
+                // (without a next tile its wait is the values' again)
+                uint64_t *const values = &B->full[kKeyRing + v_slot];
+                uint64_t *const bars[3] = {values, more ? &B->full[k_slot] : values, &B->p[g][0]};
+                const uint32_t parities[3] = {v_turn & 1, more ? k_turn & 1 : v_turn & 1, used & 1};
+                ok = wait_all(bars, parities, B);
+                const uint64_t dv = at(kDescV, base + (kKeyRing + v_slot) * kTile);
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                if (ok && own) {
-                    ok = wait_warp(&B->p[g][half], used & 1, B);
+                for (int half = 0; half < 2; ++half) {
+                    if (half == 1) ok = wait_warp(&B->p[g][1], used & 1, B);
                     if (!ok) break;
                     tc_fence_after();
+                    if (copies && half == 0) fence_async_smem();
 #pragma unroll
                     for (int s = 0; s < 4; ++s)
                         mma_ts(col_o, col_s + 64 * half + 8 * s, dv + (4 * half + s) * 128, kIdescO, i > 0 || half > 0 || s > 0);
-                    commit(&B->o[g][half]);
+                    if (!more) commit(&B->o[g][half]);
                     if (half == 1) commit(&B->empty[kKeyRing + v_slot]);
+                    if (more) scores(half);
                 }
-                ok = ok && (i + 1 >= w.n || scores(i + 1, half));
-            }
-            if (!ok) break;
-            if (own) {
+                if (!ok) break;
                 ++used;
                 if (++v_slot == kValueRing) v_slot = 0, ++v_turn;
             }
-            ok = skip(i, 1, kValueRing, kKeyRing, v_slot, v_turn);
+            ok = skip(i, 1, kValueRing, kKeyRing, v_slot, v_turn) && (i + 1 == w.n || skip(i + 1, 1, kKeyRing, 0, k_slot, k_turn));
         }
     }
     commit(&B->drain[g]);  // every earlier product is done when this arrives
@@ -489,7 +512,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (warp >= kWarpKeys) {
         if (warp < kWarpMma) {
-            load_tiles(a, w, warp == kWarpKeys ? &map_k : &map_v, warp == kWarpKeys, smem, B);
+            load_tiles(a, w, per, warp == kWarpKeys ? &map_k : &map_v, warp == kWarpKeys, smem, B);
         } else {
             if (warp != kWarpMma) {
                 // each row's start: this CTA's of every group's rows, and of the rows of no group
@@ -510,7 +533,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int g = warp >> 2, quad = warp & 3, r = 32 * quad + lane;  // the group of warps; the row of its tile
         const uint32_t lanes = tmem + ((uint32_t)(32 * quad) << 16) + 128 * g, col_s = lanes + kColS, col_o = lanes + kColO;
         const float scale2 = fabsf(p.scale) * kLog2e;
-        uint32_t count = 0, used = 0;  // tiles before the segment; tiles of this group
+        uint32_t count = 0, used = 0, segments = 0;  // tiles before the segment; tiles, and segments, of this group
         bool ok = true;
         for (; ok && w.left > 0; next_segment(a, w)) {
             const bool shared = w.rows > kT;
@@ -520,15 +543,20 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int head = (w.g.row0 + row) * p.num_q_heads + w.head * p.group + (in_group - row * p.group);
             const int steps = steps_in(w, g);
             if (steps > 0) {  // (a group without a tile writes no queries: it could come by here again before the other)
+                // a half-warp reads a row, into the rows of the two swizzled halves
                 const uint32_t flip = p.scale < 0.0f ? 0x80008000u : 0u;  // (the scale's sign goes to the queries)
-                const uint4 *const src = reinterpret_cast<const uint4 *>(p.q + (int64_t)head * kHeadDim);
-                uint8_t *const dst = smem + kQ + g * kTile + r * 128;
+                const int sub = lane >> 4, chunk = lane & 15;
+                uint8_t *const dst = smem + kQ + g * kTile + (chunk >> 3) * kHalf + 32 * quad * 128;
                 uint4 x[16];
 #pragma unroll
-                for (int i = 0; i < 16; ++i) x[i] = valid ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
+                for (int i = 0; i < 16; ++i) {
+                    const int from = __shfl_sync(0xffffffffu, valid ? head : -1, 2 * i + sub);
+                    x[i] = make_uint4(0, 0, 0, 0);
+                    if (from >= 0) x[i] = __ldg(reinterpret_cast<const uint4 *>(p.q + (int64_t)from * kHeadDim) + chunk);
+                }
 #pragma unroll
                 for (int i = 0; i < 16; ++i)
-                    *reinterpret_cast<uint4 *>(dst + (i >> 3) * kHalf + (((i & 7) ^ (r & 7)) << 4)) =
+                    *reinterpret_cast<uint4 *>(dst + (2 * i + sub) * 128 + (((chunk & 7) ^ ((2 * i + sub) & 7)) << 4)) =
                         make_uint4(x[i].x ^ flip, x[i].y ^ flip, x[i].z ^ flip, x[i].w ^ flip);
                 fence_async_smem();
                 arrive_warp(&B->q[g]);
@@ -579,7 +607,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                         m = fmaxf(m, now);
                     } else if (__any_sync(0xffffffffu, now > m + kSlack)) {
                         const float to = fmaxf(m, now), f = to == kNegInf ? 1.0f : ex2(m - to);
-                        ok = wait_warp(&B->o[g][half ^ 1], (used - 1 + half) & 1, B);  // of the half tile before this one
+                        // P V of the half tile before this one: what was issued behind it are this tile's second scores,
+                        // or the next one's first; in the segment's last tile nothing was
+                        if (half == 0) ok = wait_warp(&B->s[g][1], used & 1, B);
+                        else if (i + 1 < steps) ok = wait_warp(&B->s[g][0], (used + 1) & 1, B);
+                        else ok = wait_warp(&B->o[g][0], segments & 1, B);
                         if (!ok) break;
                         tc_fence_after();
 #pragma unroll 1
@@ -619,27 +651,43 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!ok) break;
             count += tiles_in(w);
             // ---- the segment's part
-            const int64_t part = w.step == 0 ? (shared ? 0 : (int64_t)g * a.x.heads) + head
-                                             : 3 * (int64_t)a.x.heads + (int64_t)cta * kPrefixSlots + g * kT + r;
+            const int part = w.step == 0 ? (shared ? 0 : g * a.x.heads) + head : 3 * a.x.heads + cta * kPrefixSlots + g * kT + r;  // (below 2^26)
             if (steps > 0) {
-                ok = wait_warp(&B->o[g][1], (used - 1) & 1, B);
+                ok = wait_warp(&B->o[g][1], segments & 1, B);
+                ++segments;
                 if (!ok) break;
                 tc_fence_after();
             }
             if (valid) a.x.ml[part] = make_float2(m, l);
-            float4 *const dst = reinterpret_cast<float4 *>(a.x.o + part * kHeadDim);
+            // 64 channels at a time through the warp's own rows of the query tile, which have been read, so that a half-warp
+            // writes a row
+            const int sub = lane >> 4, chunk = lane & 15;
+            uint8_t *const rows = smem + kQ + g * kTile + 32 * quad * 128;
 #pragma unroll
-            for (int b = 0; b < 4; ++b) {
-                float o[32];
+            for (int half = 0; half < 2; ++half) {
 #pragma unroll
-                for (int j = 0; j < 32; ++j) o[j] = 0.0f;
-                if (steps > 0) {
-                    tmem_ld32(col_o + 32 * b, o);
-                    tmem_wait_ld();
+                for (int b = 0; b < 2; ++b) {
+                    float o[32];
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) o[j] = 0.0f;
+                    if (steps > 0) {
+                        tmem_ld32(col_o + 64 * half + 32 * b, o);
+                        tmem_wait_ld();
+                    }
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        *reinterpret_cast<float4 *>(rows + b * kHalf + lane * 128 + ((j ^ (lane & 7)) << 4)) =
+                            make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
                 }
-                if (valid)
+                __syncwarp();
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) dst[8 * b + j] = make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+                for (int i = 0; i < 16; ++i) {
+                    const int from = 2 * i + sub;
+                    const int to = __shfl_sync(0xffffffffu, valid ? part : -1, from);
+                    const float4 x = *reinterpret_cast<const float4 *>(rows + (chunk >> 3) * kHalf + from * 128 + (((chunk & 7) ^ (from & 7)) << 4));
+                    if (to >= 0) reinterpret_cast<float4 *>(a.x.o + (int64_t)to * kHeadDim + 64 * half)[chunk] = x;
+                }
+                __syncwarp();
             }
             tc_fence_before();
         }
