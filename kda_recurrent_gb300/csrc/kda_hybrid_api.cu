@@ -327,6 +327,7 @@ int kda_page_resize(int32_t *block_table, const int32_t *seq_lens, const int32_t
     a.capacity = max_pages * page_size;
     a.has_maps = slots || positions || rows;
     a.max_tokens = a.has_maps ? max_tokens : 0;
+    a.wide_maps = aligned(slots, 16) && aligned(positions, 16) && aligned(rows, 16);
     if (device_status_ptr(&a.status) != cudaSuccess) return KDA_ERR_CUDA;
     return from_cuda(launch_page_resize(a, reinterpret_cast<cudaStream_t>(stream)));
 }

@@ -182,6 +182,7 @@ struct PageResizeArgs {
     int64_t *slots;
     int32_t *positions, *rows;
     int32_t num_pages, page_size, page_shift, batch, max_pages, capacity, max_tokens, has_maps;
+    int32_t wide_maps;  // the maps may be written by 16 bytes
     DeviceStatus *status;
 };
 

@@ -3,14 +3,18 @@
 //
 // A row of n tokens holds ceil(n / page_size) pages. Free pages lie in a ring [first, first + count); rows that
 // grow take from its front, in row order, rows that shrink give back to its end, so that what a call takes and
-// what it gives never meet. Where each row's pages and tokens begin follows from prefix sums over the rows. One
-// launch does all of it: every CTA of one cluster forms the sums of 1024 rows at a time by itself (8 bytes a row)
-// and handles its part of the tokens and pages, which it finds in the sums by bisection; the cluster's barrier
-// lies between the last read of a length and its update in place. Nothing here is wide: it is a chain of
-// dependent reads (lengths, sums, table or ring, map), and the launch is most of a small call.
+// what it gives never meet. Where each row's pages and tokens begin follows from prefix sums over the rows, which
+// every CTA forms by itself, 1024 rows at a time (8 bytes a row); tokens and pages find their row in the sums by
+// bisection. Nothing here is wide: it is a chain of dependent reads (lengths, sums, table or ring, map), and the
+// launch is most of a small call.
+//
+// Up to kFewTokens new tokens one launch does everything, of one CTA, or of a cluster where the tables could give many
+// pages back. More tokens are mapped by CTAs all over the GPU, four tokens a
+// thread, which also take the pages; a second launch of one cluster then gives pages back and sets the lengths and
+// the state, which the first one reads.
 //
 // Pages given back are compacted (a missing page of the table is not given back) in table order: each thread
-// counts four entries, and the CTAs exchange their counts through distributed shared memory.
+// counts four entries, and the CTAs of the cluster exchange their counts through distributed shared memory.
 #include <algorithm>
 
 #include "kda_dependent.cuh"
@@ -24,20 +28,11 @@ constexpr int kMaxThreads = 1024;  // rows at a time, too
 constexpr int kMaxCluster = 8;
 constexpr int kGive = 4;  // entries of a thread at a time
 constexpr uint32_t kMost = 0x7fffffffu;
+constexpr int kFewTokens = 4096, kFewPages = 32768;  // (of all tables)
 
 // Sums of counts that stop at 2^31 - 1 (adding so is associative, too).
 __device__ __forceinline__ uint32_t add(uint32_t x, uint32_t y) { return min(x + y, kMost); }
 
-__device__ __forceinline__ uint32_t cluster_rank() {
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-__device__ __forceinline__ uint32_t cluster_size() {
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
-    return r;
-}
 // All threads of the cluster; what they wrote before is visible to all of them behind it.
 __device__ __forceinline__ void cluster_barrier() {
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
@@ -60,20 +55,25 @@ __device__ __forceinline__ int row_of(const uint32_t *sums, int n, uint32_t x) {
     return lo;
 }
 
+// kMaps: pages taken, slots, positions and rows of the new tokens. kState: pages given back, lengths and state.
+// kQuad: tokens of a thread at a time (1, or 4 that are written together).
+template <bool kMaps, bool kState, int kQuad>
 __global__ void __launch_bounds__(kMaxThreads) kda_page_resize_kernel(const PageResizeArgs p) {
     __shared__ uint32_t s_tok[kMaxThreads], s_take[kMaxThreads], s_give[kMaxThreads];  // inclusive sums of a chunk's rows
     __shared__ int32_t s_old[kMaxThreads], s_new[kMaxThreads];
     __shared__ uint32_t s_warp[3][32];
     __shared__ uint32_t s_given[2][kMaxCluster];
+    __shared__ uint32_t s_used;  // pages really taken
     const int threads = blockDim.x, warps = threads >> 5, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int rank = (int)cluster_rank(), ctas = (int)cluster_size();
+    const int rank = (int)blockIdx.x, ctas = (int)gridDim.x;  // (with kState the grid is one cluster)
     const int me = rank * threads + threadIdx.x, all = ctas * threads;
     const int F = p.num_pages, ps = p.page_size;
+    if (threadIdx.x == 0) s_used = 0;  // (first read behind the chunk's barriers)
     wait_for_prior();
     allow_next();
     int first = p.free_state[0], count = p.free_state[1];
     if (first < 0 || first >= F || count < 0 || count > F) {
-        if (me == 0) report_error(p.status, KDA_ERR_DEVICE_INPUT, -1);
+        if (kMaps && me == 0) report_error(p.status, KDA_ERR_DEVICE_INPUT, -1);
         first = 0, count = 0;
     }
     auto pages = [&](int n) { return (uint32_t)((n + ps - 1) >> p.page_shift); };
@@ -88,18 +88,19 @@ __global__ void __launch_bounds__(kMaxThreads) kda_page_resize_kernel(const Page
         if (page < 0) report_error(p.status, KDA_ERR_DEVICE_INPUT, row);
         return valid(page, row);
     };
-    if (me == 0 && p.cu_tokens) p.cu_tokens[0] = 0;
-    if (ctas > 1) cluster_barrier();  // every CTA has begun: its shared memory may be written
+    if (kMaps && me == 0 && p.cu_tokens) p.cu_tokens[0] = 0;
+    if (kState && ctas > 1) cluster_barrier();  // every CTA has begun: its shared memory may be written
 
-    uint32_t tokens = 0, taken = 0, used = 0, given = 0;  // of the rows before the chunk; used: pages really taken
+    uint32_t tokens = 0, taken = 0, given = 0;  // of the rows before the chunk
     int round = 0;
+    uint32_t quad = me;  // this thread's next tokens
     for (int r0 = 0; r0 < p.batch; r0 += threads) {
         const int rows = min(threads, p.batch - r0), r = r0 + threadIdx.x;
         int n = 0, m = 0;
         if ((int)threadIdx.x < rows) {
             n = p.seq_lens[r], m = p.new_lens[r];
             if (n < 0 || n > p.capacity || m < 0 || m > p.capacity) {
-                if (rank == 0) report_error(p.status, KDA_ERR_DEVICE_INPUT, r);
+                if (kMaps && rank == 0) report_error(p.status, KDA_ERR_DEVICE_INPUT, r);
                 n = min(max(n, 0), p.capacity), m = min(max(m, 0), p.capacity);
             }
         }
@@ -134,41 +135,70 @@ __global__ void __launch_bounds__(kMaxThreads) kda_page_resize_kernel(const Page
         // in order: the first row whose pages are not there, and all later ones that need pages, get none
         const bool served = my_take == 0 || add(taken, x[1]) <= (uint32_t)count;
         const uint32_t left = (uint32_t)count - min(taken, (uint32_t)count);
-        if (!served && rank == 0) report_error(p.status, KDA_ERR_DEVICE_INPUT, r);
-        if (rank == 0 && (int)threadIdx.x < rows && p.cu_tokens) p.cu_tokens[r + 1] = (int)add(tokens, x[0]);
-        if (rank == 0 && my_tokens > 0 && p.has_maps && add(tokens, x[0]) > (uint32_t)p.max_tokens)
+        if (kMaps && !served && rank == 0) report_error(p.status, KDA_ERR_DEVICE_INPUT, r);
+        if (kMaps && rank == 0 && (int)threadIdx.x < rows && p.cu_tokens) p.cu_tokens[r + 1] = (int)add(tokens, x[0]);
+        if (kMaps && rank == 0 && my_tokens > 0 && p.has_maps && add(tokens, x[0]) > (uint32_t)p.max_tokens)
             report_error(p.status, KDA_ERR_DEVICE_INPUT, r);
         __syncthreads();
 
         // ---- pages taken
         const uint32_t takes = min(total[1], left);
-        for (uint32_t i = me; i < takes; i += all) {
+        for (uint32_t i = me; kMaps && i < takes; i += all) {
             const int row = row_of(s_take, rows, i);
             if (s_take[row] > left) continue;  // the row that does not fit
             const uint32_t have = pages(s_old[row]), before = row > 0 ? s_take[row - 1] : 0;
             p.block_table[(size_t)(r0 + row) * p.max_pages + have + (i - before)] = free_page(taken + i, r0 + row);
         }
         // ---- slots of the new tokens
-        if (p.has_maps) {
-            const uint32_t room = (uint32_t)p.max_tokens - min(tokens, (uint32_t)p.max_tokens), here = min(total[0], room);
-            for (uint32_t i = me; i < here; i += all) {
-                const int row = row_of(s_tok, rows, i);
-                const uint32_t before = row > 0 ? s_tok[row - 1] : 0, have = pages(s_old[row]);
-                const int j = s_old[row] + (int)(i - before);
-                const uint32_t pg = (uint32_t)j >> p.page_shift, take0 = row > 0 ? s_take[row - 1] : 0;
-                const bool fits = pages(s_new[row]) <= have || s_take[row] <= left;
-                if (p.slots) {
-                    int page = -1;
-                    if (fits) page = pg < have ? valid(p.block_table[(size_t)(r0 + row) * p.max_pages + pg], r0 + row)
-                                               : free_page(taken + take0 + (pg - have), r0 + row);
-                    p.slots[tokens + i] = page < 0 ? -1 : ((int64_t)page << p.page_shift) + (j & (ps - 1));
+        if (kMaps && p.has_maps) {
+            const uint32_t end = min(add(tokens, total[0]), (uint32_t)p.max_tokens);  // (of this chunk's rows)
+            for (; quad * kQuad < end; quad += all) {
+                const uint32_t t0 = max(quad * kQuad, tokens), t1 = min((quad + 1) * kQuad, end);
+                int64_t slot[kQuad];
+                int position[kQuad], of_row[kQuad];
+                int row = t0 < t1 ? row_of(s_tok, rows, t0 - tokens) : 0, page = -1;
+                uint32_t page_at = ~0u;
+#pragma unroll
+                for (int e = 0; e < kQuad; ++e) {
+                    const uint32_t t = quad * kQuad + e;
+                    if (t < t0 || t >= t1) continue;
+                    while (s_tok[row] <= t - tokens) ++row, page_at = ~0u;
+                    const int j = s_old[row] + (int)(t - tokens - (row > 0 ? s_tok[row - 1] : 0));
+                    const uint32_t pg = (uint32_t)j >> p.page_shift;
+                    if (p.slots && pg != page_at) {
+                        const uint32_t have = pages(s_old[row]), take0 = row > 0 ? s_take[row - 1] : 0;
+                        page = -1;
+                        if (pages(s_new[row]) <= have || s_take[row] <= left)
+                            page = pg < have ? valid(p.block_table[(size_t)(r0 + row) * p.max_pages + pg], r0 + row)
+                                             : free_page(taken + take0 + (pg - have), r0 + row);
+                        page_at = pg;
+                    }
+                    slot[e] = page < 0 ? -1 : ((int64_t)page << p.page_shift) + (j & (ps - 1));
+                    position[e] = j;
+                    of_row[e] = r0 + row;
                 }
-                if (p.positions) p.positions[tokens + i] = j;
-                if (p.rows) p.rows[tokens + i] = r0 + row;
+                const uint32_t t = quad * kQuad;
+                if (kQuad == 4 && p.wide_maps && t1 - t0 == kQuad) {
+                    if (p.slots) {
+                        *reinterpret_cast<longlong2 *>(p.slots + t) = make_longlong2(slot[0], slot[1 % kQuad]);
+                        *reinterpret_cast<longlong2 *>(p.slots + t + 2) = make_longlong2(slot[2 % kQuad], slot[3 % kQuad]);
+                    }
+                    if (p.positions) *reinterpret_cast<int4 *>(p.positions + t) = make_int4(position[0], position[1 % kQuad], position[2 % kQuad], position[3 % kQuad]);
+                    if (p.rows) *reinterpret_cast<int4 *>(p.rows + t) = make_int4(of_row[0], of_row[1 % kQuad], of_row[2 % kQuad], of_row[3 % kQuad]);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < kQuad; ++e) {
+                        if (t + e < t0 || t + e >= t1) continue;
+                        if (p.slots) p.slots[t + e] = slot[e];
+                        if (p.positions) p.positions[t + e] = position[e];
+                        if (p.rows) p.rows[t + e] = of_row[e];
+                    }
+                }
+                if ((quad + 1) * kQuad > end) break;  // (the rest is of later rows)
             }
         }
         // ---- pages given back, behind the ring's end
-        for (uint32_t base = 0; base < total[2]; base += (uint32_t)all * kGive, ++round) {
+        for (uint32_t base = 0; kState && base < total[2]; base += (uint32_t)all * kGive, ++round) {
             int page[kGive], mine = 0, row[kGive];
 #pragma unroll
             for (int e = 0; e < kGive; ++e) {
@@ -190,11 +220,15 @@ __global__ void __launch_bounds__(kMaxThreads) kda_page_resize_kernel(const Page
             __syncthreads();  // (s_warp has been read)
             if (lane == 31) s_warp[0][warp] = sum;
             __syncthreads();
-            uint32_t block = 0, at = given + sum - mine;
-            for (int w = 0; w < warps; ++w) {
-                if (w < warp) at += s_warp[0][w];
-                block += s_warp[0][w];
+            uint32_t block = lane < warps ? s_warp[0][lane] : 0, at = given + sum - mine;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const uint32_t y = __shfl_up_sync(0xffffffffu, block, o);
+                if (lane >= o) block += y;
             }
+            const uint32_t below = __shfl_sync(0xffffffffu, block, max(warp - 1, 0));
+            if (warp > 0) at += below;
+            block = __shfl_sync(0xffffffffu, block, 31);
             if (ctas > 1) {
                 if ((int)threadIdx.x < ctas) store_remote(&s_given[round & 1][rank], threadIdx.x, block);
                 cluster_barrier();
@@ -221,30 +255,29 @@ __global__ void __launch_bounds__(kMaxThreads) kda_page_resize_kernel(const Page
         // ---- the rows' new lengths, when no CTA reads the old ones any more
         const uint32_t end = add(taken, x[1]);
         const int best = served && my_take > 0 ? (int)end : 0;
-        if (ctas > 1) cluster_barrier();
-        if (rank == 0 && (int)threadIdx.x < rows) p.out_lens[r] = served ? m : n;
+        if (kState && ctas > 1) cluster_barrier();
+        if (kState && rank == 0 && (int)threadIdx.x < rows) p.out_lens[r] = served ? m : n;
         // pages really taken: the sum at the last row that was served
-        int top = best;
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-        __syncthreads();  // (s_warp and the chunk's sums have been read)
-        if (lane == 0) s_warp[0][warp] = (uint32_t)top;
-        __syncthreads();
-        for (int w = 0; w < warps; ++w) used = max(used, s_warp[0][w]);
+        if (kState) {
+            const uint32_t top = __reduce_max_sync(0xffffffffu, (uint32_t)best);
+            if (lane == 0 && top > 0) atomicMax(&s_used, top);
+        }
         tokens = add(tokens, total[0]);
         taken = add(taken, total[1]);
         __syncthreads();
     }
-    if (p.has_maps) {
+    if (kMaps && p.has_maps) {
         for (uint32_t i = tokens + me; i < (uint32_t)p.max_tokens; i += all) {
             if (p.slots) p.slots[i] = -1;
             if (p.positions) p.positions[i] = 0;
             if (p.rows) p.rows[i] = -1;
         }
     }
+    if (!kState) return;
     if (ctas > 1) cluster_barrier();  // the state has been read
     else __syncthreads();
     if (me == 0) {
+        const uint32_t used = s_used;
         uint32_t at = (uint32_t)first + used;
         if (at >= (uint32_t)F) at -= F;
         p.out_state[0] = (int)at;
@@ -255,10 +288,18 @@ __global__ void __launch_bounds__(kMaxThreads) kda_page_resize_kernel(const Page
 }  // namespace
 
 cudaError_t launch_page_resize(const PageResizeArgs &p, cudaStream_t stream) {
-    const int threads = p.batch <= 256 && p.max_tokens <= 1024 ? 256 : kMaxThreads;
-    int ctas = 1;
-    while (ctas < kMaxCluster && (int64_t)ctas * 4 * kMaxThreads < p.max_tokens) ctas *= 2;
-    return launch_clusters((unsigned)ctas, kda_page_resize_kernel, dim3((unsigned)ctas), (unsigned)threads, 0, stream, p);
+    if (p.max_tokens <= kFewTokens) {
+        const bool one = (int64_t)p.batch * p.max_pages <= kFewPages;
+        const int threads = one && p.batch <= 256 && p.max_tokens <= 1024 ? 256 : kMaxThreads;
+        const unsigned ctas = one ? 1 : kMaxCluster;
+        return launch_clusters(ctas, kda_page_resize_kernel<true, true, 1>, dim3(ctas), (unsigned)threads, 0, stream, p);
+    }
+    int32_t sms = 0;
+    if (sm_count_of_current_device(&sms) != KDA_OK) return cudaErrorInvalidDevice;
+    const int quads = (p.max_tokens + 3) / 4, ctas = std::min((quads + kMaxThreads - 1) / kMaxThreads, sms);
+    const cudaError_t e = launch_dependent(kda_page_resize_kernel<true, false, 4>, dim3((unsigned)ctas), kMaxThreads, 0, stream, p);
+    if (e != cudaSuccess) return e;
+    return launch_clusters(kMaxCluster, kda_page_resize_kernel<false, true, 1>, dim3(kMaxCluster), kMaxThreads, 0, stream, p);
 }
 
 }  // namespace kda

@@ -25,7 +25,7 @@ namespace {
 
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
-constexpr int kCtas = 3;            // on an SM
+constexpr int kCtas = 2;            // on an SM
 constexpr int kLoads = 4;           // of a lane at a time
 constexpr int kHeads = 2 * kLoads;  // of a warp at a time
 enum Layout { kNone, kHalves, kInterleaved };
@@ -80,88 +80,103 @@ __global__ void __launch_bounds__(kThreads, kCtas) kda_qk_rope_kernel(const Args
     const int angle0 = kLayout == kInterleaved ? 4 * chunk : chunk < reach ? 8 * chunk : 8 * (chunk - reach);
     const float side = kLayout == kHalves && chunk < reach ? -p.magnitude : p.magnitude;
 
-    for (int64_t t = first; t < p.tokens; t += workers) {
-        float cs[kAngles], sn[kAngles];
-        int64_t slot = -1;
-        if (p.slots) {
-            slot = __ldg(p.slots + t);
+    auto load = [&](uint4 (&raw)[kLoads], int64_t t, int h0) {
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+            const int h = h0 + 2 * i + sub, hk = h - p.num_q_heads, hv = hk - p.num_kv_heads;
+            const __nv_bfloat16 *src = p.q + t * p.q_stride + (int64_t)h * kHeadDim;
+            if (hk >= 0) src = p.k + t * p.k_stride + (int64_t)hk * kHeadDim;
+            if (hv >= 0) src = p.v + t * p.v_stride + (int64_t)hv * kHeadDim;
+            raw[i] = make_uint4(0, 0, 0, 0);
+            if (h < a.heads) raw[i] = *(reinterpret_cast<const uint4 *>(src) + chunk);
+        }
+    };
+    // the next eight heads (and the next token's place) are on their way while these are computed
+    uint4 raw[kLoads], ahead[kLoads];
+    int64_t t = first, slot_ahead = -1;
+    int h0 = part * kHeads, pos_ahead = 0;
+    auto place = [&](int64_t t) {
+        if (p.slots) slot_ahead = __ldg(p.slots + t);
+        if (kLayout != kNone) pos_ahead = __ldg(p.positions + t);
+    };
+    if (h0 >= a.heads || t >= p.tokens) return;
+    load(ahead, t, h0);
+    place(t);
+    float cs[kAngles], sn[kAngles];
+    int64_t slot = -1;
+    while (t < p.tokens) {
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) raw[i] = ahead[i];
+        if (h0 == part * kHeads) {  // a new token
+            slot = slot_ahead;
             if (slot >= p.num_pages << p.page_shift) {
-                if (lane == 0) report_error(p.status, KDA_ERR_DEVICE_INPUT, (int32_t)t);
+                if (p.slots && lane == 0) report_error(p.status, KDA_ERR_DEVICE_INPUT, (int32_t)t);
                 slot = -1;
             }
-        }
-        const int pos = kLayout == kNone ? 0 : __ldg(p.positions + t);
-        if (kLayout != kNone) {
 #pragma unroll
-            for (int i = 0; i < kAngles; ++i) {
-                cs[i] = 1.0f, sn[i] = 0.0f;
+            for (int i = 0; kLayout != kNone && i < kAngles; ++i) {
+                const uint64_t turn = (uint64_t)(int64_t)pos_ahead * s_turn[(angle0 + i) & (kHeadDim / 2 - 1)];
+                __sincosf((float)(int32_t)(turn >> 32) * 1.4629180792671596e-9f, &sn[i], &cs[i]);  // 2 pi / 2^32
+                sn[i] *= side;
+                cs[i] *= p.magnitude;
+            }
+        }
+        int next_h = h0 + a.split * kHeads;
+        int64_t next_t = t;
+        if (next_h >= a.heads) next_h = part * kHeads, next_t += workers;
+        if (next_t < p.tokens) {
+            load(ahead, next_t, next_h);
+            if (next_t != t) place(next_t);
+        }
+        const int64_t page = slot >> p.page_shift, in_page = slot & ((1 << p.page_shift) - 1);
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+            const int h = h0 + 2 * i + sub, hk = h - p.num_q_heads, hv = hk - p.num_kv_heads;
+            uint4 y = raw[i];
+            float x[8];
+            unpack(y, x);
+            const bool is_q = hk < 0;
+            if (p.q_weight || p.k_weight) {
+                float sum = 0.0f;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) sum = fmaf(x[e], x[e], sum);
+#pragma unroll
+                for (int o = 8; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+                const float r = rsqrtf(fmaf(sum, 1.0f / kHeadDim, p.eps));
+                if (is_q ? p.q_weight != nullptr : p.k_weight != nullptr) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) x[e] *= r * (is_q ? wq[e] : wk[e]);
+                }
+            }
+            if (kLayout == kHalves) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const float other = __shfl_sync(0xffffffffu, x[e], partner);
+                    if (turned) x[e] = fmaf(x[e], cs[e], other * sn[e]);
+                }
+            } else if (kLayout == kInterleaved) {
                 if (turned) {
-                    const uint64_t turn = (uint64_t)(int64_t)pos * s_turn[angle0 + i];
-                    __sincosf((float)(int32_t)(turn >> 32) * 1.4629180792671596e-9f, &sn[i], &cs[i]);  // 2 pi / 2^32
-                    sn[i] *= side;
-                    cs[i] *= p.magnitude;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float b = x[2 * e + 1];
+                        x[2 * e + 1] = fmaf(b, cs[e], x[2 * e] * sn[e]);
+                        x[2 * e] = fmaf(x[2 * e], cs[e], -b * sn[e]);
+                    }
                 }
+            }
+            if (hv < 0) y = make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
+            if (is_q) {
+                reinterpret_cast<uint4 *>(p.q_out + t * p.q_out_stride + (int64_t)h * kHeadDim)[chunk] = y;
+            } else if (hv < 0) {
+                if (p.k_out) reinterpret_cast<uint4 *>(p.k_out + t * p.k_out_stride + (int64_t)hk * kHeadDim)[chunk] = y;
+                if (slot >= 0)
+                    reinterpret_cast<uint4 *>(p.k_cache + page * p.k_page_stride + (((int64_t)hk << p.page_shift) + in_page) * kHeadDim)[chunk] = y;
+            } else if (h < a.heads && slot >= 0) {
+                reinterpret_cast<uint4 *>(p.v_cache + page * p.v_page_stride + (((int64_t)hv << p.page_shift) + in_page) * kHeadDim)[chunk] = y;
             }
         }
-        const int64_t page = slot >> p.page_shift, at = slot & ((1 << p.page_shift) - 1);
-        for (int h0 = part * kHeads; h0 < a.heads; h0 += a.split * kHeads) {
-            uint4 raw[kLoads];
-#pragma unroll
-            for (int i = 0; i < kLoads; ++i) {
-                const int h = h0 + 2 * i + sub, hk = h - p.num_q_heads, hv = hk - p.num_kv_heads;
-                const __nv_bfloat16 *src = nullptr;
-                if (hk < 0) src = p.q + t * p.q_stride + (int64_t)h * kHeadDim;
-                else if (hv < 0) src = p.k + t * p.k_stride + (int64_t)hk * kHeadDim;
-                else if (h < a.heads && slot >= 0) src = p.v + t * p.v_stride + (int64_t)hv * kHeadDim;
-                raw[i] = src ? *(reinterpret_cast<const uint4 *>(src) + chunk) : make_uint4(0, 0, 0, 0);
-            }
-#pragma unroll
-            for (int i = 0; i < kLoads; ++i) {
-                const int h = h0 + 2 * i + sub, hk = h - p.num_q_heads, hv = hk - p.num_kv_heads;
-                uint4 y = raw[i];
-                float x[8];
-                unpack(y, x);
-                const bool is_q = hk < 0;
-                if (p.q_weight || p.k_weight) {
-                    float sum = 0.0f;
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) sum = fmaf(x[e], x[e], sum);
-#pragma unroll
-                    for (int o = 8; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-                    const float r = rsqrtf(fmaf(sum, 1.0f / kHeadDim, p.eps));
-                    if (is_q ? p.q_weight != nullptr : p.k_weight != nullptr) {
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) x[e] *= r * (is_q ? wq[e] : wk[e]);
-                    }
-                }
-                if (kLayout == kHalves) {
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const float other = __shfl_sync(0xffffffffu, x[e], partner);
-                        if (turned) x[e] = fmaf(x[e], cs[e], other * sn[e]);
-                    }
-                } else if (kLayout == kInterleaved) {
-                    if (turned) {
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const float b = x[2 * e + 1];
-                            x[2 * e + 1] = fmaf(b, cs[e], x[2 * e] * sn[e]);
-                            x[2 * e] = fmaf(x[2 * e], cs[e], -b * sn[e]);
-                        }
-                    }
-                }
-                if (hv < 0) y = make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
-                if (is_q) {
-                    reinterpret_cast<uint4 *>(p.q_out + t * p.q_out_stride + (int64_t)h * kHeadDim)[chunk] = y;
-                } else if (hv < 0) {
-                    if (p.k_out) reinterpret_cast<uint4 *>(p.k_out + t * p.k_out_stride + (int64_t)hk * kHeadDim)[chunk] = y;
-                    if (slot >= 0)
-                        reinterpret_cast<uint4 *>(p.k_cache + page * p.k_page_stride + (((int64_t)hk << p.page_shift) + at) * kHeadDim)[chunk] = y;
-                } else if (h < a.heads && slot >= 0) {
-                    reinterpret_cast<uint4 *>(p.v_cache + page * p.v_page_stride + (((int64_t)hv << p.page_shift) + at) * kHeadDim)[chunk] = y;
-                }
-            }
-        }
+        t = next_t;
+        h0 = next_h;
     }
 }
 
