@@ -200,12 +200,15 @@ __global__ void __launch_bounds__(kMaxThreads) kda_page_resize_kernel(const Page
         // ---- pages given back, behind the ring's end
         for (uint32_t base = 0; kState && base < total[2]; base += (uint32_t)all * kGive, ++round) {
             int page[kGive], mine = 0, row[kGive];
+            const uint32_t i0 = base + (uint32_t)me * kGive;
+            int at_row = i0 < total[2] ? row_of(s_give, rows, i0) : 0;
 #pragma unroll
             for (int e = 0; e < kGive; ++e) {
-                const uint32_t i = base + (uint32_t)me * kGive + e;
+                const uint32_t i = i0 + e;
                 page[e] = -1, row[e] = 0;
                 if (i < total[2]) {
-                    row[e] = row_of(s_give, rows, i);
+                    while (s_give[at_row] <= i) ++at_row;
+                    row[e] = at_row;
                     const uint32_t before = row[e] > 0 ? s_give[row[e] - 1] : 0;
                     page[e] = valid(p.block_table[(size_t)(r0 + row[e]) * p.max_pages + pages(s_new[row[e]]) + (i - before)], r0 + row[e]);
                 }
@@ -296,8 +299,9 @@ cudaError_t launch_page_resize(const PageResizeArgs &p, cudaStream_t stream) {
     }
     int32_t sms = 0;
     if (sm_count_of_current_device(&sms) != KDA_OK) return cudaErrorInvalidDevice;
-    const int quads = (p.max_tokens + 3) / 4, ctas = std::min((quads + kMaxThreads - 1) / kMaxThreads, sms);
-    const cudaError_t e = launch_dependent(kda_page_resize_kernel<true, false, 4>, dim3((unsigned)ctas), kMaxThreads, 0, stream, p);
+    const int threads = p.batch <= 256 ? 256 : kMaxThreads, quads = (p.max_tokens + 3) / 4;
+    const int ctas = std::min((quads + threads - 1) / threads, sms * (kMaxThreads / threads));
+    const cudaError_t e = launch_dependent(kda_page_resize_kernel<true, false, 4>, dim3((unsigned)ctas), (unsigned)threads, 0, stream, p);
     if (e != cudaSuccess) return e;
     return launch_clusters(kMaxCluster, kda_page_resize_kernel<false, true, 1>, dim3(kMaxCluster), kMaxThreads, 0, stream, p);
 }
