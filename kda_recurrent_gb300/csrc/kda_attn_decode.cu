@@ -680,21 +680,32 @@ __global__ void __launch_bounds__(kThreads, 4) kda_attn_join_kernel(const Args a
     write_row<false>(a, (size_t)s_cut.head + row, lane, m, l, o);
 }
 
-// Joins all parts of a query row: those of its prefix and those of the rest, in this order, by `per_row` warps of a
-// CTA, which take every per_row-th part. (8192 query rows of 6 to 8 parts: about 7 us, which the parts' 30 MB take.)
-__global__ void __launch_bounds__(kThreads, 4) kda_attn_prefix_join_kernel(const Args a, int per_row) {
-    __shared__ float s_m[kWarps], s_l[kWarps];
-    __shared__ float4 s_o[kWarps][32];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int64_t head = (int64_t)blockIdx.x * (kWarps / per_row) + warp / per_row;
-    const int first = warp % per_row;
+// Joins all parts of a query row: those of its prefix and those of the rest, in this order, by `per_row` half-warps of
+// a CTA, which take every per_row-th part. A lane has eight channels, and four parts' loads in flight. (With a warp a
+// row, 32768 rows of two or three parts: 21.7 instead of XXX us from a cold cache.)
+constexpr int kHalves = 2 * kWarps;
+
+__global__ void __launch_bounds__(kThreads, 3) kda_attn_prefix_join_kernel(const Args a, int per_row) {
+    __shared__ float s_m[kHalves], s_l[kHalves];
+    __shared__ float4 s_o[kHalves][32];
+    const int half = threadIdx.x >> 4, lane = threadIdx.x & 15;
+    const int64_t head = (int64_t)blockIdx.x * (kHalves / per_row) + half / per_row;
+    const int first = half % per_row;
     allow_next();
     wait_for_prior();
-    float m = kNegInf, l = 0.0f;
-    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    float m = kNegInf, l = 0.0f, o[8] = {};
+    auto add = [&](float pm, float pl, float ref, const float4 (&x)[2]) {
+        const float f = ex2(pm - ref);
+        l = fmaf(pl, f, l);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            o[4 * i] = fmaf(x[i].x, f, o[4 * i]), o[4 * i + 1] = fmaf(x[i].y, f, o[4 * i + 1]);
+            o[4 * i + 2] = fmaf(x[i].z, f, o[4 * i + 2]), o[4 * i + 3] = fmaf(x[i].w, f, o[4 * i + 3]);
+        }
+    };
     if (head < a.x.heads) {
         const int tail = a.x.tails[head];
-        PrefixCut pre = a.x.cuts[head];
+        const PrefixCut pre = a.x.cuts[head];
         const int before = a.x.start[head / a.p.num_q_heads] == 0 ? 0 : pre.per * (1 + pre.ctas);
         Cut cut;
         cut.count = tail == kTailHome ? 1 : 0;
@@ -703,55 +714,59 @@ __global__ void __launch_bounds__(kThreads, 4) kda_attn_prefix_join_kernel(const
         constexpr int kAhead = 4;
         for (int i = first; i < n; i += kAhead * per_row) {
             float pm[kAhead], pl[kAhead];
-            float4 po[kAhead];
+            float4 po[kAhead][2];
             float top = m;
 #pragma unroll
             for (int e = 0; e < kAhead; ++e) {
                 const int x = i + e * per_row;
-                pm[e] = kNegInf, pl[e] = 0.0f, po[e] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                if (x < before || (x < n && tail < 0)) {
+                pm[e] = kNegInf, pl[e] = 0.0f, po[e][0] = po[e][1] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                if (x >= n) continue;
+                const float *src;
+                if (x < before || tail < 0) {
                     const int64_t part = x < before ? a.x.part_at(pre, head, x) : 2 * (int64_t)a.x.heads + head;
                     const float2 ml = a.x.ml[part];
                     pm[e] = ml.x, pl[e] = ml.y;
-                    po[e] = *reinterpret_cast<const float4 *>(a.x.o + part * kHeadDim + 4 * lane);
-                } else if (x < n) {
+                    src = a.x.o + part * kHeadDim;
+                } else {
                     const Part *const part = a.ws.parts + cut.part_at(x - before);
                     pm[e] = part->m[row], pl[e] = part->l[row];
-                    po[e] = *reinterpret_cast<const float4 *>(&part->o[row][4 * lane]);
+                    src = part->o[row];
                 }
+                po[e][0] = reinterpret_cast<const float4 *>(src)[2 * lane], po[e][1] = reinterpret_cast<const float4 *>(src)[2 * lane + 1];
             }
 #pragma unroll
             for (int e = 0; e < kAhead; ++e) top = fmaxf(top, pm[e]);
             const float ref = top == kNegInf ? 0.0f : top, keep = ex2(m - ref);
             l *= keep;
-            o = make_float4(o.x * keep, o.y * keep, o.z * keep, o.w * keep);
 #pragma unroll
-            for (int e = 0; e < kAhead; ++e) {
-                const float f = ex2(pm[e] - ref);
-                l = fmaf(pl[e], f, l);
-                o = make_float4(fmaf(po[e].x, f, o.x), fmaf(po[e].y, f, o.y), fmaf(po[e].z, f, o.z), fmaf(po[e].w, f, o.w));
-            }
+            for (int e = 0; e < 8; ++e) o[e] *= keep;
+#pragma unroll
+            for (int e = 0; e < kAhead; ++e) add(pm[e], pl[e], ref, po[e]);
             m = top;
         }
     }
     if (per_row > 1) {
-        if (lane == 0) s_m[warp] = m, s_l[warp] = l;
-        s_o[warp][lane] = o;
+        if (lane == 0) s_m[half] = m, s_l[half] = l;
+        s_o[half][2 * lane] = make_float4(o[0], o[1], o[2], o[3]), s_o[half][2 * lane + 1] = make_float4(o[4], o[5], o[6], o[7]);
         __syncthreads();
         if (first > 0) return;
-        float top = kNegInf;
-        for (int w = 0; w < per_row; ++w) top = fmaxf(top, s_m[warp + w]);
-        const float ref = top == kNegInf ? 0.0f : top;
-        m = top, l = 0.0f;
-        o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        m = kNegInf, l = 0.0f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) o[e] = 0.0f;
+        for (int w = 0; w < per_row; ++w) m = fmaxf(m, s_m[half + w]);
+        const float ref = m == kNegInf ? 0.0f : m;
         for (int w = 0; w < per_row; ++w) {
-            const float f = ex2(s_m[warp + w] - ref);
-            const float4 x = s_o[warp + w][lane];
-            l = fmaf(s_l[warp + w], f, l);
-            o = make_float4(fmaf(x.x, f, o.x), fmaf(x.y, f, o.y), fmaf(x.z, f, o.z), fmaf(x.w, f, o.w));
+            const float4 x[2] = {s_o[half + w][2 * lane], s_o[half + w][2 * lane + 1]};
+            add(s_m[half + w], s_l[half + w], ref, x);
         }
     }
-    if (head < a.x.heads) write_row<false>(a, (size_t)head, lane, m, l, o);
+    if (head >= a.x.heads) return;
+    const float inv = 1.0f / l;  // (l = 0: zeros, whatever the values)
+    uint4 y = make_uint4(0, 0, 0, 0);
+    if (l != 0.0f) y = make_uint4(pack_bf16(o[0] * inv, o[1] * inv), pack_bf16(o[2] * inv, o[3] * inv), pack_bf16(o[4] * inv, o[5] * inv),
+                                  pack_bf16(o[6] * inv, o[7] * inv));
+    reinterpret_cast<uint4 *>(a.p.out + head * kHeadDim)[lane] = y;
+    if (lane == 0 && a.p.lse) a.p.lse[head] = l == 0.0f ? kNegInf : ((m == kNegInf ? 0.0f : m) + log2f(l)) * kLn2;
 }
 
 // weight[b][h][j] += sum over the query heads of key head h of 2^(x_j - lse), four tokens a thread. A score of
@@ -846,10 +861,10 @@ cudaError_t launch(const AttnDecodeArgs &p, const PrefixParts &x, cudaStream_t s
               : launch_dependent(kda_attn_decode_kernel<uint64_t, kTail>, dim3((unsigned)sms), kThreads, kSmem, stream, a);
     if (e != cudaSuccess) return e;
     if (kTail) {
-        // warps of a query row: all of a CTA's for few rows, which can have long rests in many parts
-        int per_row = kWarps;
-        while (per_row > 1 && (int64_t)x.heads * per_row > (int64_t)sms * 4 * kWarps) per_row /= 2;
-        const int rows = kWarps / per_row;
+        // half-warps of a query row: all of a CTA's for few rows, which can have long rests in many parts
+        int per_row = kHalves;
+        while (per_row > 1 && (int64_t)x.heads * per_row > (int64_t)sms * 3 * kHalves) per_row /= 2;
+        const int rows = kHalves / per_row;
         return launch_dependent(kda_attn_prefix_join_kernel, dim3((unsigned)((x.heads + rows - 1) / rows)), kThreads, 0, stream, a, per_row);
     }
     e = launch_dependent(kda_attn_join_kernel, dim3((unsigned)sms, (unsigned)std::min(p.group, kRows)), kThreads, 0, stream, a);

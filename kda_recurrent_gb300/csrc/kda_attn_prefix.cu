@@ -41,7 +41,6 @@ constexpr int kKeyRing = 2, kValueRing = 3, kRing = kKeyRing + kValueRing;
 constexpr int kWarpKeys = 8, kWarpMma = 10;  // (9: values; 11: the second group's products); the eight before them: softmax
 constexpr int kThreads = 12 * 32;
 constexpr int kLive = 8;  // masks kept (more tiles than the loads can be ahead of the softmax)
-constexpr int kTmaPage = 64;  // the least page that is loaded by TMA
 constexpr float kNegInf = -INFINITY;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kSlack = 8.0f;  // log2: how far a maximum may grow before O is scaled
@@ -104,12 +103,9 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
     return y;
 }
 
-// (one lane's, by a whole warp with the same operands: a lane for each box took 70 cycles a box)
 __device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap *map, int x, int y, int z, int w, uint64_t *bar) {
     asm volatile(
-        "{\n\t.reg .pred e;\n\t"
-        "elect.sync _|e, 0xffffffff;\n\t"
-        "@e cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];\n\t}" ::"r"(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(
             dst),
         "l"(map), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_addr(bar))
         : "memory");
@@ -128,23 +124,26 @@ __device__ __forceinline__ uint32_t try_wait(const uint64_t *bar, uint32_t parit
 }
 
 // Wait of a warp for up to three phases, bounded, with one decision for all its lanes. (One after the other, waits for
-// phases that are long complete take some 150 cycles each.)
+// phases that are long complete take some 150 cycles each.) What follows a first try is not inlined: the kernel's
+// many waits would be a sixth of its instructions, which every launch has to fetch anew.
+__device__ __noinline__ bool wait_on(const uint64_t *b0, uint32_t p0, const uint64_t *b1, uint32_t p1, const uint64_t *b2, uint32_t p2, Bars *B) {
+    volatile int32_t *const abort = &B->abort;
+    const uint64_t since = global_ns();
+    for (;;) {
+        const uint32_t done = try_wait(b0, p0) & try_wait(b1, p1) & try_wait(b2, p2);
+        if (__all_sync(0xffffffffu, done)) return true;
+        if (global_ns() - since > kWaitLimitNs) *abort = 1;
+        if (__any_sync(0xffffffffu, *abort)) return false;
+    }
+}
+
 template <int kCount>
 __device__ __forceinline__ bool wait_all(uint64_t *const (&bar)[kCount], const uint32_t (&parity)[kCount], Bars *B) {
-    volatile int32_t *const abort = &B->abort;
-    uint64_t since = 0;
-    bool ok = true;
-    for (;;) {
-        uint32_t done = 1;
+    uint32_t done = 1;
 #pragma unroll
-        for (int i = 0; i < kCount; ++i) done &= try_wait(bar[i], parity[i]);
-        if (__all_sync(0xffffffffu, done)) break;
-        const uint64_t now = global_ns();
-        if (since == 0) since = now;
-        if (now - since > kWaitLimitNs) *abort = 1;
-        if (__any_sync(0xffffffffu, *abort)) { ok = false; break; }
-    }
-    return ok;
+    for (int i = 0; i < kCount; ++i) done &= try_wait(bar[i], parity[i]);
+    if (__all_sync(0xffffffffu, done)) return true;
+    return wait_on(bar[0], parity[0], bar[1 % kCount], parity[1 % kCount], bar[2 % kCount], parity[2 % kCount], B);
 }
 
 __device__ __forceinline__ bool wait_warp(uint64_t *bar, uint32_t parity, Bars *B) {
@@ -221,35 +220,25 @@ __device__ __forceinline__ int tiles_in(const Walk &w) {
 }
 __device__ __forceinline__ int steps_in(const Walk &w, int g) { return w.rows > kT || g == 0 ? w.n : tiles_in(w) - w.n; }
 
-// The loads of the keys' or the values' tiles, by one warp: tile s for step s, or 2 s and 2 s + 1. Large pages come by
-// TMA, a box for each page (or 128 tokens of it) and half of the channels; a box takes about 100 cycles to ask for,
-// so that small pages come faster by 16-byte copies of all lanes.
+// The loads of the keys' or the values' tiles, by one warp: tile s for step s, or 2 s and 2 s + 1. A lane asks for a box
+// of a page (or 128 tokens of it) and half of the channels. (Asked for by one elected lane after another the 16 boxes
+// of a tile of small pages take 55.9 instead of 55.0 us with 32 rows in 4 groups; by 16-byte copies of all lanes 58.6.)
 __device__ __forceinline__ void load_tiles(const AttnPrefixArgs &a, Walk w, int per, const CUtensorMap *map, bool keys, uint8_t *smem, Bars *B) {
     const PagedCache &c = a.d.c;
     const int lane = threadIdx.x & 31, rows_a_box = min(c.page_size, kT), boxes = kT / rows_a_box;
-    const uint32_t ring = keys ? kKeyRing : kValueRing, place0 = keys ? 0 : kKeyRing, base = smem_addr(smem) + place0 * kTile;
+    const uint32_t ring = keys ? kKeyRing : kValueRing, place0 = keys ? 0 : kKeyRing;
     uint64_t *const full = B->full + place0, *const empty = B->empty + place0;
-    const __nv_bfloat16 *const cache = keys ? c.k : c.v;
-    const int64_t page_stride = keys ? c.k_page_stride : c.v_page_stride;
-    const bool tma = c.page_size >= kTmaPage;
+    const int sub = lane >> 1, half = lane & 1;  // this lane's box
     int leader = -1, leader_of = -1, done = 0;
     uint32_t count = 0, slot = 0, turn = 0;  // tiles so far; the next one's place, and the times that was used
     bool ok = true;
     for (; ok && w.left > 0; next_segment(a, w)) {
-        if (leader_of != w.index) {  // the first row that holds the whole prefix: the others' pages are the same
-            leader = w.g.row0;
-            for (int b0 = 0; b0 < w.g.rows; b0 += 32) {
-                const int b = w.g.row0 + b0 + lane;
-                const bool has = b0 + lane < w.g.rows && row_length(c, b, a.d.status, false) >= w.g.tokens;
-                const uint32_t who = __ballot_sync(0xffffffffu, has);
-                if (who) { leader = w.g.row0 + b0 + __ffs(who) - 1; break; }
-            }
-            leader_of = w.index;
-        }
-        const int32_t *const table = c.block_table + (size_t)leader * c.max_pages;
-        auto page_of = [&](int tile) {  // lane i: of box i
-            int page = -1;
-            if (lane < boxes) page = table[(tile * kT + lane * rows_a_box) >> c.page_shift];
+        const bool changed = leader_of != w.index;
+        if (changed) leader = w.g.row0, leader_of = w.index;
+        auto page_at = [&](int tile) {
+            return sub < boxes ? c.block_table[(size_t)leader * c.max_pages + ((tile * kT + sub * rows_a_box) >> c.page_shift)] : -1;
+        };
+        auto page_of = [&](int page) {
             if (page >= c.num_pages) {
                 report_error(a.d.status, KDA_ERR_DEVICE_INPUT, leader);
                 page = -1;
@@ -267,64 +256,47 @@ __device__ __forceinline__ void load_tiles(const AttnPrefixArgs &a, Walk w, int 
             if (ahead < tiles) tile += ahead;
         }
         done += w.n;
-        int next = page_of(tile);
+        int next = page_at(tile);
+        // The pages are those of the first row that holds the whole prefix: most often the first one, whose table is
+        // read beside the rows' lengths.
+        for (int b0 = 0; changed && b0 < w.g.rows; b0 += 32) {
+            const int b = w.g.row0 + b0 + lane;
+            const bool has = b0 + lane < w.g.rows && row_length(c, b, a.d.status, false) >= w.g.tokens;
+            const uint32_t who = __ballot_sync(0xffffffffu, has);
+            if (!who) continue;
+            leader = w.g.row0 + b0 + __ffs(who) - 1;
+            if (leader != w.g.row0) next = page_at(tile);
+            break;
+        }
+        next = page_of(next);
         for (int i = 0; i < tiles; ++i) {
             const int page = next, now = tile;
             if (++tile == begin + tiles) tile = begin;
-            if (i + 1 < tiles) next = page_of(tile);
+            if (i + 1 < tiles) next = page_of(page_at(tile));
             ok = turn == 0 || wait_warp(&empty[slot], (turn - 1) & 1, B);
             if (!ok) break;
-            const uint32_t missing = __ballot_sync(0xffffffffu, lane < boxes && page < 0);
+            const bool on = sub < boxes, gone = on && page < 0;
+            const uint32_t missing = __ballot_sync(0xffffffffu, gone);
             uint32_t live = 0xffffu;
-            for (uint32_t left = missing; left; left &= left - 1)
-                live &= ~(((1u << (rows_a_box / 8)) - 1) << ((__ffs(left) - 1) * rows_a_box / 8));
-            if (keys && lane == 0) B->live[count % kLive] = live;
-            const uint32_t dst = base + slot * kTile;
-            const int row = (now * kT) & (c.page_size - 1);
-            if (tma) {
-                if (missing) {  // clear their rows
-                    for (int i = 0; i < boxes; ++i) {
-                        if (!((missing >> i) & 1)) continue;
-                        for (int half = 0; half < 2; ++half)
-                            for (int e = lane; e < rows_a_box * 8; e += 32)
-                                *reinterpret_cast<uint4 *>(smem + (place0 + slot) * kTile + half * kHalf + i * rows_a_box * 128 + e * 16) =
-                                    make_uint4(0, 0, 0, 0);
-                    }
-                    fence_async_smem();
-                    __syncwarp();
-                }
-                if (lane == 0) expect_tx(&full[slot], 2 * (boxes - __popc(missing)) * rows_a_box * 128);
+            uint8_t *const box = smem + (place0 + slot) * kTile + half * kHalf + sub * rows_a_box * 128;
+            if (missing) {  // clear their rows
+                for (int i = 0; i < boxes; ++i)
+                    if ((missing >> (2 * i)) & 1) live &= ~(((1u << (rows_a_box / 8)) - 1) << (i * rows_a_box / 8));
+                for (int e = 0; gone && e < rows_a_box * 8; ++e) reinterpret_cast<uint4 *>(box)[e] = make_uint4(0, 0, 0, 0);
+                fence_async_smem();
                 __syncwarp();
-                for (int i = 0; i < boxes; ++i) {
-                    const int pg = __shfl_sync(0xffffffffu, page, i);
-                    if (pg < 0) continue;
-                    tma_load(dst + i * rows_a_box * 128, map, 0, row, w.head, pg, &full[slot]);
-                    tma_load(dst + kHalf + i * rows_a_box * 128, map, 64, row, w.head, pg, &full[slot]);
-                }
-            } else {
-                // two tokens at a time, a half-warp for each
-                const int sub = lane >> 4, chunk = lane & 15;
-                const uint32_t to = dst + (chunk >> 3) * kHalf + sub * 128;
-                for (int i = 0; i < boxes; ++i) {
-                    const int pg = __shfl_sync(0xffffffffu, page, i);
-                    const __nv_bfloat16 *src = cache + (pg < 0 ? 0 : pg * page_stride + ((int64_t)w.head * c.page_size + row) * kHeadDim) +
-                                               sub * kHeadDim + chunk * 8;
-                    const uint32_t bytes = pg < 0 ? 0 : 16;  // (0: zeros)
-                    for (int r = 0; r < rows_a_box; r += 8, src += 8 * kHeadDim)
-#pragma unroll
-                        for (int u = 0; u < 4; ++u)
-                            cp_async_16(to + (i * rows_a_box + r + 2 * u) * 128 + (((chunk & 7) ^ (2 * u + sub)) << 4), src + 2 * u * kHeadDim, bytes);
-                }
-                asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(&full[slot])) : "memory");
-                if (lane == 0) mbar_arrive(&full[slot]);
             }
+            if (lane == 0) {
+                if (keys) B->live[count % kLive] = live;
+                expect_tx(&full[slot], (2 * boxes - __popc(missing)) * rows_a_box * 128);
+            }
+            __syncwarp();
+            if (on && !gone) tma_load(smem_addr(box), map, 64 * half, (now * kT) & (c.page_size - 1), w.head, page, &full[slot]);
             ++count;
             if (++slot == ring) slot = 0, ++turn;
         }
     }
-    if (!tma) {
-        cp_async_wait<0>();
-    } else if (!ok) {  // what was asked for has to arrive before the CTA leaves
+    if (!ok) {  // what was asked for has to arrive before the CTA leaves
         for (uint32_t i = count > ring ? count - ring : 0; i < count; ++i) mbar_wait(&full[i % ring], (i / ring) & 1);
     }
 }
@@ -334,7 +306,6 @@ __device__ __forceinline__ void load_tiles(const AttnPrefixArgs &a, Walk w, int 
 // ahead of the other (the barriers' parity could not tell).
 __device__ __forceinline__ void issue_products(const AttnPrefixArgs &a, Walk w, int g, uint8_t *smem, Bars *B) {
     const uint32_t base = smem_addr(smem), tmem = B->tmem, col_s = tmem + kColS + 128 * g, col_o = tmem + kColO + 128 * g;
-    const bool copies = a.d.c.page_size < kTmaPage;  // (their writes are not yet the tensor core's to see)
     const uint64_t dq = at(kDescK, base + kQ + g * kTile);
     uint32_t k_slot = 0, k_turn = 0, v_slot = 0, v_turn = 0;  // the next places
     uint32_t used = 0, queries = 0;                           // tiles, and segments, of this group
@@ -370,7 +341,6 @@ __device__ __forceinline__ void issue_products(const AttnPrefixArgs &a, Walk w, 
             if (!ok) break;
             ++queries;
             tc_fence_after();
-            if (copies) fence_async_smem();
             scores(0);
             scores(1);
         }
@@ -386,12 +356,11 @@ __device__ __forceinline__ void issue_products(const AttnPrefixArgs &a, Walk w, 
                 const uint32_t parities[3] = {v_turn & 1, more ? k_turn & 1 : v_turn & 1, used & 1};
                 ok = wait_all(bars, parities, B);
                 const uint64_t dv = at(kDescV, base + (kKeyRing + v_slot) * kTile);
-#pragma unroll
+#pragma unroll  // (as a loop, with an eighth fewer instructions in the kernel: 192 instead of 178 us, 128 rows of 32768)
                 for (int half = 0; half < 2; ++half) {
                     if (half == 1) ok = wait_warp(&B->p[g][1], used & 1, B);
                     if (!ok) break;
                     tc_fence_after();
-                    if (copies && half == 0) fence_async_smem();
 #pragma unroll
                     for (int s = 0; s < 4; ++s)
                         mma_ts(col_o, col_s + 64 * half + 8 * s, dv + (4 * half + s) * 128, kIdescO, i > 0 || half > 0 || s > 0);
@@ -424,7 +393,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (threadIdx.x == 0) {
         // (a place is freed by both groups' warps)
-        for (int i = 0; i < kRing; ++i) mbar_init(&B->full[i], c.page_size >= kTmaPage ? 1 : 33), mbar_init(&B->empty[i], 2);
+        for (int i = 0; i < kRing; ++i) mbar_init(&B->full[i], 1), mbar_init(&B->empty[i], 2);
         for (int w = 0; w < 2; ++w) {
             mbar_init(&B->q[w], 4);
             for (int h = 0; h < 2; ++h) mbar_init(&B->s[w][h], 1), mbar_init(&B->p[w][h], 4), mbar_init(&B->o[w][h], 1);
@@ -445,69 +414,88 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     // ---- the steps of all groups, and where this CTA's share begins
     bool bad = false;
-    auto steps_of = [&](int g) {
+    Walk w;
+    w.g.row0 = w.g.rows = w.g.tiles = w.g.tokens = 0;
+    auto group_steps = [&](int g, Group &x) {
+        x.row0 = x.rows = x.tiles = x.tokens = 0;
         if (g >= a.groups) return (int64_t)0;
         const int lo = a.cu_groups[g], hi = a.cu_groups[g + 1], n = a.prefix_lens[g];
         const bool wrong = lo < 0 || hi < lo || hi > c.batch;
         if (cta == 0 && (wrong || n < 0 || n > c.capacity)) report_error(p.status, KDA_ERR_DEVICE_INPUT, g);
         bad |= wrong;
-        return wrong ? 0 : (int64_t)c.num_kv_heads * head_steps(a, group_of(a, lo, hi, n));
+        if (!wrong) x = group_of(a, lo, hi, n);
+        return (int64_t)c.num_kv_heads * head_steps(a, x);
     };
-    auto block_sum = [&](int64_t x, int64_t &before) {
-        int64_t sum = x;
+    auto scan = [&](int64_t x) {  // inclusive, over the warp
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const int64_t y = __shfl_up_sync(0xffffffffu, sum, o);
-            if (lane >= o) sum += y;
+            const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+            if (lane >= o) x += y;
         }
-        if (lane == 31) B->sums[warp] = sum;
-        __syncthreads();
-        int64_t total = lane < kThreads / 32 ? B->sums[lane] : 0;
-        before = sum - x;
-        int64_t low = lane < warp ? total : 0;
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            total += __shfl_xor_sync(0xffffffffu, total, o);
-            low += __shfl_xor_sync(0xffffffffu, low, o);
-        }
-        before += low;
-        return total;
+        return x;
     };
-    int64_t mine = 0, before0 = 0;
-    for (int g = threadIdx.x; g < a.groups; g += kThreads) mine += steps_of(g);
-    bad = __syncthreads_or(bad);  // then nothing is taken as shared: the rows' own tables hold all of their tokens
-    const int64_t all = block_sum(mine, before0);
-    bad |= all > 0x3fffffff;  // (tables that repeat their pages very often: places are 32-bit numbers below)
-    const int total = bad ? 0 : (int)all, per = max((total + ctas - 1) / ctas, 1);
-    const int lo = min(cta * per, total), hi = min(lo + per, total);
-    if (lo < hi) {
-        int64_t first = 0;
-        for (int g0 = 0; g0 < a.groups; g0 += kThreads) {
-            int64_t x = mine, before = before0, sum = all;
-            if (a.groups > kThreads) {
-                x = steps_of(g0 + threadIdx.x);
-                __syncthreads();  // (the sums have been read)
-                sum = block_sum(x, before);
-            }
-            const int64_t off = lo - first - before;
-            if (off >= 0 && off < x) B->group = g0 + threadIdx.x, B->offset = (int)off;
-            first += sum;
+    int64_t all;
+    int per = 1, offset = 0;  // the length of a share; this one's place in its first group
+    auto share = [&] {
+        bad |= all > 0x3fffffff;  // (tables that repeat their pages very often: places are 32-bit numbers below)
+        const int total = bad ? 0 : (int)all;
+        per = max((total + ctas - 1) / ctas, 1);
+        w.first = min(cta * per, total);
+        w.left = min(per, total - w.first);
+    };
+    if (a.groups <= 32) {  // each warp by itself
+        Group x;
+        const int64_t mine = group_steps(lane, x), sum = scan(mine);
+        all = __shfl_sync(0xffffffffu, sum, 31);
+        bad = __any_sync(0xffffffffu, bad);
+        share();
+        const int64_t off = w.first - (sum - mine);
+        const uint32_t here = __ballot_sync(0xffffffffu, w.left > 0 && off >= 0 && off < mine);
+        w.index = here ? __ffs(here) - 1 : 0;
+        offset = __shfl_sync(0xffffffffu, (int)off, w.index);
+        w.g.row0 = __shfl_sync(0xffffffffu, x.row0, w.index), w.g.rows = __shfl_sync(0xffffffffu, x.rows, w.index);
+        w.g.tiles = __shfl_sync(0xffffffffu, x.tiles, w.index), w.g.tokens = __shfl_sync(0xffffffffu, x.tokens, w.index);
+        __syncthreads();
+    } else {
+        Group x;
+        auto block_scan = [&](int64_t v, int64_t &total) {
+            const int64_t sum = scan(v);
+            __syncthreads();  // (the sums before have been read)
+            if (lane == 31) B->sums[warp] = sum;
+            __syncthreads();
+            int64_t before = 0;
+            total = 0;
+            for (int i = 0; i < kThreads / 32; ++i) before += i < warp ? B->sums[i] : 0, total += B->sums[i];
+            return sum + before;
+        };
+        int64_t mine = 0;
+        for (int g = threadIdx.x; g < a.groups; g += kThreads) mine += group_steps(g, x);
+        bad = __syncthreads_or(bad);  // then nothing is taken as shared: the rows' own tables hold all of their tokens
+        block_scan(mine, all);
+        share();
+        int64_t before = 0;
+        for (int g0 = 0; w.left > 0 && g0 < a.groups; g0 += kThreads) {
+            int64_t total;
+            mine = group_steps(g0 + threadIdx.x, x);
+            const int64_t sum = block_scan(mine, total), off = w.first - before - (sum - mine);
+            if (off >= 0 && off < mine) B->group = g0 + threadIdx.x, B->offset = (int)off;
+            before += total;
+        }
+        __syncthreads();
+        if (w.left > 0) {
+            w.index = B->group, offset = B->offset;
+            w.g = group_at(a, w.index);
         }
     }
-    __syncthreads();
     tc_fence_after();
     const uint32_t tmem = B->tmem;
-    Walk w;
-    w.left = hi - lo;
     if (w.left > 0) {
-        w.index = B->group;
-        w.g = group_at(a, w.index);
         const int per_head = (int)head_steps(a, w.g), pairs = (query_rows(a, w.g) + kPrefixSlots - 1) / kPrefixSlots;
-        w.head = B->offset / per_head;
-        const int in_head = B->offset - w.head * per_head;
+        w.head = offset / per_head;
+        const int in_head = offset - w.head * per_head;
         w.pair = min(in_head / w.g.tiles, pairs - 1);
         w.step = in_head - w.pair * w.g.tiles;
-        w.first = lo - w.step;
+        w.first -= w.step;
         set_item(a, w);
     }
     if (warp >= kWarpKeys) {
@@ -547,17 +535,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint32_t flip = p.scale < 0.0f ? 0x80008000u : 0u;  // (the scale's sign goes to the queries)
                 const int sub = lane >> 4, chunk = lane & 15;
                 uint8_t *const dst = smem + kQ + g * kTile + (chunk >> 3) * kHalf + 32 * quad * 128;
-                uint4 x[16];
+#pragma unroll 1
+                for (int r0 = 0; r0 < 32; r0 += 16) {
+                    uint4 x[8];
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const int from = __shfl_sync(0xffffffffu, valid ? head : -1, 2 * i + sub);
-                    x[i] = make_uint4(0, 0, 0, 0);
-                    if (from >= 0) x[i] = __ldg(reinterpret_cast<const uint4 *>(p.q + (int64_t)from * kHeadDim) + chunk);
+                    for (int i = 0; i < 8; ++i) {
+                        const int from = __shfl_sync(0xffffffffu, valid ? head : -1, r0 + 2 * i + sub);
+                        x[i] = make_uint4(0, 0, 0, 0);
+                        if (from >= 0) x[i] = __ldg(reinterpret_cast<const uint4 *>(p.q + (int64_t)from * kHeadDim) + chunk);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        *reinterpret_cast<uint4 *>(dst + (r0 + 2 * i + sub) * 128 + (((chunk & 7) ^ ((2 * i + sub) & 7)) << 4)) =
+                            make_uint4(x[i].x ^ flip, x[i].y ^ flip, x[i].z ^ flip, x[i].w ^ flip);
                 }
-#pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    *reinterpret_cast<uint4 *>(dst + (2 * i + sub) * 128 + (((chunk & 7) ^ ((2 * i + sub) & 7)) << 4)) =
-                        make_uint4(x[i].x ^ flip, x[i].y ^ flip, x[i].z ^ flip, x[i].w ^ flip);
                 fence_async_smem();
                 arrive_warp(&B->q[g]);
             }
@@ -661,29 +652,28 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (valid) a.x.ml[part] = make_float2(m, l);
             // 64 channels at a time through the warp's own rows of the query tile, which have been read, so that a half-warp
             // writes a row
-            const int sub = lane >> 4, chunk = lane & 15;
+            const int rows_here = min(max(w.rows - (mine - lane), 0), 32), sub = lane >> 4, chunk = lane & 15;
             uint8_t *const rows = smem + kQ + g * kTile + 32 * quad * 128;
+#pragma unroll 1
+            for (int half = 0; half < 2 && rows_here > 0; ++half) {
+                float o[2][32];
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
+                for (int j = 0; j < 32; ++j) o[0][j] = o[1][j] = 0.0f;
+                if (steps > 0) {
+                    tmem_ld32(col_o + 64 * half, o[0]);
+                    tmem_ld32(col_o + 64 * half + 32, o[1]);
+                    tmem_wait_ld();
+                }
 #pragma unroll
-                for (int b = 0; b < 2; ++b) {
-                    float o[32];
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) o[j] = 0.0f;
-                    if (steps > 0) {
-                        tmem_ld32(col_o + 64 * half + 32 * b, o);
-                        tmem_wait_ld();
-                    }
+                for (int b = 0; b < 2; ++b)
 #pragma unroll
                     for (int j = 0; j < 8; ++j)
                         *reinterpret_cast<float4 *>(rows + b * kHalf + lane * 128 + ((j ^ (lane & 7)) << 4)) =
-                            make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
-                }
+                            make_float4(o[b][4 * j], o[b][4 * j + 1], o[b][4 * j + 2], o[b][4 * j + 3]);
                 __syncwarp();
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const int from = 2 * i + sub;
-                    const int to = __shfl_sync(0xffffffffu, valid ? part : -1, from);
+#pragma unroll 4
+                for (int r0 = 0; r0 < rows_here; r0 += 2) {
+                    const int from = r0 + sub, to = __shfl_sync(0xffffffffu, valid ? part : -1, from);
                     const float4 x = *reinterpret_cast<const float4 *>(rows + (chunk >> 3) * kHalf + from * 128 + (((chunk & 7) ^ (from & 7)) << 4));
                     if (to >= 0) reinterpret_cast<float4 *>(a.x.o + (int64_t)to * kHeadDim + 64 * half)[chunk] = x;
                 }
