@@ -305,6 +305,7 @@ __device__ __forceinline__ void load_tiles(const AttnPrefixArgs &a, Walk w, int 
 // groups' warps pass every place of the rings, in order, and free it, so that neither is ever two turns of a ring
 // ahead of the other (the barriers' parity could not tell).
 __device__ __forceinline__ void issue_products(const AttnPrefixArgs &a, Walk w, int g, uint8_t *smem, Bars *B) {
+    const uint32_t lead = elect_lead();
     const uint32_t base = smem_addr(smem), tmem = B->tmem, col_s = tmem + kColS + 128 * g, col_o = tmem + kColO + 128 * g;
     const uint64_t dq = at(kDescK, base + kQ + g * kTile);
     uint32_t k_slot = 0, k_turn = 0, v_slot = 0, v_turn = 0;  // the next places
@@ -326,11 +327,12 @@ __device__ __forceinline__ void issue_products(const AttnPrefixArgs &a, Walk w, 
 #pragma unroll
             for (int s = 0; s < 8; ++s) {
                 const uint32_t off = ((s >> 2) * kHalf + (s & 3) * 32) >> 4;
-                mma_ss(col_s + 64 * half, dq + off, dk + off, kIdescS, s > 0);
+                mma_ss(lead, col_s + 64 * half, dq + off, dk + off, kIdescS, s > 0);
             }
-            commit(&B->s[g][half]);
-            if (half == 0) return;
-            commit(&B->empty[k_slot]);
+            commit(lead, &B->s[g][half]);
+            if (half == 1) commit(lead, &B->empty[k_slot]);
+        };
+        auto next_keys = [&] {
             if (++k_slot == kKeyRing) k_slot = 0, ++k_turn;
         };
         ok = skip(0, 0, kKeyRing, 0, k_slot, k_turn);
@@ -343,6 +345,7 @@ __device__ __forceinline__ void issue_products(const AttnPrefixArgs &a, Walk w, 
             tc_fence_after();
             scores(0);
             scores(1);
+            next_keys();
         }
         ok = ok && skip(0, 1, kKeyRing, 0, k_slot, k_turn);
         for (int i = 0; ok && i < w.n; ++i) {
@@ -356,17 +359,18 @@ __device__ __forceinline__ void issue_products(const AttnPrefixArgs &a, Walk w, 
                 const uint32_t parities[3] = {v_turn & 1, more ? k_turn & 1 : v_turn & 1, used & 1};
                 ok = wait_all(bars, parities, B);
                 const uint64_t dv = at(kDescV, base + (kKeyRing + v_slot) * kTile);
-#pragma unroll  // (as a loop, with an eighth fewer instructions in the kernel: 192 instead of 178 us, 128 rows of 32768)
+#pragma unroll
                 for (int half = 0; half < 2; ++half) {
                     if (half == 1) ok = wait_warp(&B->p[g][1], used & 1, B);
                     if (!ok) break;
                     tc_fence_after();
 #pragma unroll
                     for (int s = 0; s < 4; ++s)
-                        mma_ts(col_o, col_s + 64 * half + 8 * s, dv + (4 * half + s) * 128, kIdescO, i > 0 || half > 0 || s > 0);
-                    if (!more) commit(&B->o[g][half]);
-                    if (half == 1) commit(&B->empty[kKeyRing + v_slot]);
+                        mma_ts(lead, col_o, col_s + 64 * half + 8 * s, dv + (4 * half + s) * 128, kIdescO, i > 0 || half > 0 || s > 0);
+                    if (!more) commit(lead, &B->o[g][half]);
+                    if (half == 1) commit(lead, &B->empty[kKeyRing + v_slot]);
                     if (more) scores(half);
+                    if (more && half == 1) next_keys();
                 }
                 if (!ok) break;
                 ++used;
@@ -375,7 +379,7 @@ __device__ __forceinline__ void issue_products(const AttnPrefixArgs &a, Walk w, 
             ok = skip(i, 1, kValueRing, kKeyRing, v_slot, v_turn) && (i + 1 == w.n || skip(i + 1, 1, kKeyRing, 0, k_slot, k_turn));
         }
     }
-    commit(&B->drain[g]);  // every earlier product is done when this arrives
+    commit(lead, &B->drain[g]);  // every earlier product is done when this arrives
     mbar_wait(&B->drain[g], 0);
 }
 
@@ -535,20 +539,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint32_t flip = p.scale < 0.0f ? 0x80008000u : 0u;  // (the scale's sign goes to the queries)
                 const int sub = lane >> 4, chunk = lane & 15;
                 uint8_t *const dst = smem + kQ + g * kTile + (chunk >> 3) * kHalf + 32 * quad * 128;
-#pragma unroll 1
-                for (int r0 = 0; r0 < 32; r0 += 16) {
-                    uint4 x[8];
+                uint4 x[16];
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const int from = __shfl_sync(0xffffffffu, valid ? head : -1, r0 + 2 * i + sub);
-                        x[i] = make_uint4(0, 0, 0, 0);
-                        if (from >= 0) x[i] = __ldg(reinterpret_cast<const uint4 *>(p.q + (int64_t)from * kHeadDim) + chunk);
-                    }
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        *reinterpret_cast<uint4 *>(dst + (r0 + 2 * i + sub) * 128 + (((chunk & 7) ^ ((2 * i + sub) & 7)) << 4)) =
-                            make_uint4(x[i].x ^ flip, x[i].y ^ flip, x[i].z ^ flip, x[i].w ^ flip);
+                for (int i = 0; i < 16; ++i) {
+                    const int from = __shfl_sync(0xffffffffu, valid ? head : -1, 2 * i + sub);
+                    x[i] = make_uint4(0, 0, 0, 0);
+                    if (from >= 0) x[i] = __ldg(reinterpret_cast<const uint4 *>(p.q + (int64_t)from * kHeadDim) + chunk);
                 }
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    *reinterpret_cast<uint4 *>(dst + (2 * i + sub) * 128 + (((chunk & 7) ^ ((2 * i + sub) & 7)) << 4)) =
+                        make_uint4(x[i].x ^ flip, x[i].y ^ flip, x[i].z ^ flip, x[i].w ^ flip);
                 fence_async_smem();
                 arrive_warp(&B->q[g]);
             }
