@@ -37,7 +37,7 @@ namespace {
 
 constexpr int kT = kPrefixTile;
 constexpr int kTile = kT * kHeadDim * 2, kHalf = kTile / 2;  // two halves of 64 channels: 128 rows of 128 bytes
-constexpr int kKeyRing = 2, kValueRing = 3, kRing = kKeyRing + kValueRing;
+constexpr int kKeyRing = 3, kValueRing = 2, kRing = kKeyRing + kValueRing;
 constexpr int kWarpKeys = 8, kWarpMma = 10;  // (9: values; 11: the second group's products); the eight before them: softmax
 constexpr int kThreads = 12 * 32;
 constexpr int kLive = 8;  // masks kept (more tiles than the loads can be ahead of the softmax)
