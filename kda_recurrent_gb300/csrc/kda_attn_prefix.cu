@@ -726,8 +726,15 @@ int64_t attn_prefix_workspace_bytes(int32_t batch, int32_t num_q_heads, int32_t 
            prefix_layout(nullptr, nullptr, batch, num_q_heads, sms);
 }
 
+// Where each row reads its own tokens alone anyway: no groups, or so few tokens in all rows' tables that reading them
+// row by row takes less than a launch more. Row by row and shared, in us: 2 rows of 512 tokens on 8/8 heads (5 MB) 8.0
+// and 16.0; 8 of 2048 on 8/8 (69 MB) 17.7 and 18.1; 16 of 1024 on 8/8 (71 MB) 19.1 and 19.0; 8 of 4096 on 32/8 (136 MB) 27.5
+// and 21.7; 64 of 2048 on 64/8 in two groups (554 MB) 87 and 28.
+constexpr int64_t kFewBytes = 72LL << 20;
+
 cudaError_t launch_attn_prefix(const AttnPrefixArgs &args, cudaStream_t stream) {
-    if (args.groups == 0) return launch_attn_decode(args.d, stream);
+    const int64_t reads = (int64_t)args.d.c.batch * args.d.c.num_kv_heads * ((args.d.group + 15) / 16) * args.d.c.capacity;
+    if (args.groups == 0 || reads <= kFewBytes / (2 * kHeadDim * 2)) return launch_attn_decode(args.d, stream);
     int32_t sms = 0;
     if (sm_count_of_current_device(&sms) != KDA_OK) return cudaErrorInvalidDevice;
     AttnPrefixArgs a = args;

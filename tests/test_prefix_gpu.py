@@ -25,16 +25,26 @@ def queries(B, Hq, seed):
     return torch.randn(B, Hq, 128, generator=gen).to(torch.bfloat16).to(DEV)
 
 
+def widened(c, Hq):
+    """With a table so wide that the call shares the prefix (it reads rows of narrow tables one by one)."""
+    rows, width = c["block_table"].shape
+    _, Hkv, page, _ = c["k_cache"].shape
+    tokens = (73 << 20) // (512 * rows * Hkv * -(-Hq // Hkv // 16)) + page
+    table = torch.full((rows, max(width, -(-tokens // page))), -1, dtype=torch.int32, device=DEV)
+    table[:, :width] = c["block_table"]
+    return dict(c, block_table=table)
+
+
 def call(q, c, scale=SCALE, **kw):
     return K.attn_prefix_decode(q, c["k_cache"], c["v_cache"], c["block_table"], c["seq_lens"], c["cu_groups"], c["prefix_lens"],
                                 scale=scale, want_lse=True, **kw)
 
 
-def check(q, c, scale=SCALE, lse_tol=LSE_TOL, status=K.KDA_OK):
+def check(q, c, scale=SCALE, lse_tol=LSE_TOL, status=K.KDA_OK, ref=None):
     K.kda_device_status()
-    out, lse = call(q, c, scale)
+    out, lse = call(q, widened(c, q.shape[1]), scale)
     assert K.kda_device_status()[0] == status
-    ref_out, ref_lse, _ = H.attn_decode(q, c, scale)
+    ref_out, ref_lse, _ = ref or H.attn_decode(q, c, scale)
     empty = torch.isinf(ref_lse)
     assert torch.equal(torch.isinf(lse).cpu(), empty) and (out.cpu()[empty] == 0).all()
     assert_out_close(out, ref_out)
@@ -91,7 +101,7 @@ def test_prefix_first_row_of_a_group_is_padding():
     c = R.prefix_inputs([0, 5], [512], [0, 100, 600, 512, 700], 2, 16, seed=4, device=DEV)
     c["block_table"][0] = 2**30  # a padding row's table may hold anything
     q = queries(5, 8, 4)
-    out, lse = call(q, c)
+    out, lse = call(q, widened(c, 8))
     clean = dict(c, block_table=c["block_table"].clone())
     clean["block_table"][0] = -1
     ref_out, ref_lse, _ = H.attn_decode(q, clean, SCALE)
@@ -139,7 +149,7 @@ def test_prefix_bad_groups_share_nothing(cu):
     check(queries(6, 4, 10), c, status=K.KDA_ERR_DEVICE_INPUT)
 
 
-@pytest.mark.parametrize("n", [-5, 10**6])
+@pytest.mark.parametrize("n", [-5, 2**30])
 def test_prefix_bad_prefix_lengths_are_clamped(n):
     c = inputs([0, 3], [300], [5] * 3, 2, 16, 11)
     c["prefix_lens"][0] = n
@@ -148,12 +158,13 @@ def test_prefix_bad_prefix_lengths_are_clamped(n):
 
 def test_prefix_bad_sequence_lengths_are_clamped():
     c = inputs([0, 3], [256], [0, 16, 0], 2, 16, 12)
-    c["seq_lens"][1] = 10**6  # clamped to the table's 272
+    c = widened(c, 4)
+    c["seq_lens"][1] = 2**30  # clamped to the table's tokens, of which only 272 are there
     K.kda_device_status()
     out, _ = call(queries(3, 4, 12), c)
     assert K.kda_device_status() == (K.KDA_ERR_DEVICE_INPUT, 1)
     c["seq_lens"][1] = 272
-    assert torch.equal(call(queries(3, 4, 12), c)[0], out)
+    assert_out_close(call(queries(3, 4, 12), c)[0], out.double().cpu())
 
 
 @pytest.mark.parametrize("scale", [-0.09, 0.0, 1e-3])
@@ -179,7 +190,7 @@ def test_prefix_infinite_and_nan_values_reach_their_channel_only():
     page = c["block_table"][0, 5].long()
     c["v_cache"][page, 0, 3, 17] = math.inf
     c["v_cache"][page, 0, 9, 40] = math.nan
-    out, lse = call(queries(4, 4, 15), c)
+    out, lse = call(queries(4, 4, 15), widened(c, 4))
     assert (out[:, :, 17] == math.inf).all() and torch.isnan(out[:, :, 40]).all()
     rest = [i for i in range(128) if i not in (17, 40)]
     assert torch.isfinite(out[:, :, rest]).all() and torch.isfinite(lse).all()
@@ -188,24 +199,27 @@ def test_prefix_infinite_and_nan_values_reach_their_channel_only():
 def test_prefix_nan_keys_and_infinite_scores():
     c = inputs([0, 4, 8], [512, 384], [20] * 8, 1, 16, 16)
     c["k_cache"][c["block_table"][0, 5].long(), 0, 3, 17] = math.nan
-    out, _ = call(queries(8, 4, 16), c)
+    out, _ = call(queries(8, 4, 16), widened(c, 4))
     assert torch.isnan(out[:4]).all() and torch.isfinite(out[4:]).all()
     # keys whose score is -inf have no weight
     c = inputs([0, 4], [512], [20] * 4, 1, 16, 17)
     q = queries(4, 4, 17)
     q[..., 0] = 1.0
     c["k_cache"][c["block_table"][0, 5].long(), 0, :, 0] = -math.inf
-    out, lse = call(q, c)
+    out, lse = call(q, widened(c, 4))
     c["block_table"][:, 5] = -1
     ref_out, ref_lse, _ = H.attn_decode(q, c, SCALE)
     assert_out_close(out, ref_out)
     assert (lse.cpu().double() - ref_lse).abs().max() <= LSE_TOL
 
 
-def test_prefix_without_groups_is_the_plain_call():
+@pytest.mark.parametrize("groups", [0, 1])
+def test_prefix_without_groups_or_of_few_tokens_is_the_plain_call(groups):
     c = inputs([0, 3], [300], [5, 6, 7], 2, 16, 18)
-    c["cu_groups"], c["prefix_lens"] = c["cu_groups"][:1], c["prefix_lens"][:0]
     q = queries(3, 4, 18)
+    if groups == 0:
+        c["cu_groups"], c["prefix_lens"] = c["cu_groups"][:1], c["prefix_lens"][:0]
+        c = widened(c, 4)
     out, lse = call(q, c)
     plain, plain_lse = K.attn_decode(q, c["k_cache"], c["v_cache"], c["block_table"], c["seq_lens"], scale=SCALE, want_lse=True)
     assert torch.equal(out, plain) and torch.equal(lse, plain_lse)
@@ -222,6 +236,17 @@ def test_prefix_wide_table():
     assert torch.equal(out, got) and torch.equal(lse, got_lse)
 
 
+@pytest.mark.parametrize("rows,Hq,Hkv,tokens", [(3, 2, 2, 24570), (3, 2, 2, 24584), (5, 40, 2, 4912), (5, 40, 2, 4920)])
+def test_prefix_beside_the_limit_of_few_tokens(rows, Hq, Hkv, tokens):
+    # 72 MiB are 147456 tokens of a row's key head and 16 query heads: rows x Hkv x ceil(group / 16) x table's tokens
+    c = inputs([0, rows], [700], [3] * rows, Hkv, 8, rows, max_pages=-(-tokens // 8))
+    q = queries(rows, Hq, 40)
+    out, lse = call(q, c)
+    ref_out, ref_lse, _ = H.attn_decode(q, dict(c, block_table=c["block_table"][:, :100].contiguous()), SCALE)
+    assert_out_close(out, ref_out)
+    assert (lse.cpu().double() - ref_lse).abs().max() <= LSE_TOL
+
+
 def test_prefix_cache_offsets_pass_32_bits():
     Hkv, page = 4, 128
     pages = 2**31 // (2 * Hkv * page * 128) + 9
@@ -235,12 +260,13 @@ def test_prefix_cache_offsets_pass_32_bits():
                  k_cache=cache[-8:, 0], v_cache=cache[-8:, 1], cu_groups=torch.tensor([0, 2], **i32), prefix_lens=torch.tensor([512], **i32))
     q = queries(2, 8, 20)
     want = check(q, small)
-    got = call(q, dict(small, block_table=table, k_cache=cache[:, 0], v_cache=cache[:, 1]))
+    got = call(q, widened(dict(small, block_table=table, k_cache=cache[:, 0], v_cache=cache[:, 1]), 8))
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
 
 
 def test_prefix_same_bits_again_on_another_stream_and_in_a_graph():
-    c = inputs([0, 20, 30], [1500, 700], [7 * i % 90 for i in range(30)], 2, 16, 21)
+    narrow = inputs([0, 20, 30], [1500, 700], [7 * i % 90 for i in range(30)], 2, 16, 21)
+    c = widened(narrow, 16)
     q = queries(30, 16, 21)
     want = call(q, c)
     ws = K.attn_prefix_decode_workspace(30, 16, 2, c["block_table"].shape[1], 16, 2, DEV)
@@ -261,14 +287,14 @@ def test_prefix_same_bits_again_on_another_stream_and_in_a_graph():
     for lens in ([7, 700], [1500, 0]):  # the captured call follows what its tensors hold
         c["prefix_lens"].copy_(torch.tensor(lens, dtype=torch.int32))
         graph.replay()
-        ref_out, ref_lse, _ = H.attn_decode(q, c, SCALE)
+        ref_out, ref_lse, _ = H.attn_decode(q, narrow, SCALE)
         assert_out_close(out, ref_out)
         assert (lse.cpu().double() - ref_lse).abs().max() <= LSE_TOL
 
 
 def test_prefix_between_other_launches():
     # overlapping launches: lengths, groups and queries come from the launch just before, the output goes to the next
-    c = inputs([0, 8], [900], [30] * 8, 2, 16, 22)
+    c = widened(inputs([0, 8], [900], [30] * 8, 2, 16, 22), 8)
     q = queries(8, 8, 22)
     want = call(q, c)[0]
     ws = K.attn_prefix_decode_workspace(8, 8, 2, c["block_table"].shape[1], 16, 1, DEV)

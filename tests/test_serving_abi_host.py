@@ -59,6 +59,37 @@ def test_qk_norm_rope_arguments(lib, over, want):
     assert rope(lib, **over) == want
 
 
+def prefix(lib, **over):
+    a = dict(q=A, k=A, v=A, ks=2 * 16 * 128, vs=2 * 16 * 128, pages=10, ps=16, bt=A, P=4, sl=A, cu=A, pl=A, G=2, out=A, lse=None,
+             B=2, Hq=4, Hkv=2, scale=0.1, ws=A, nb=1 << 40)
+    a.update(over)
+    return lib.kda_attn_prefix_decode(a["q"], a["k"], a["v"], a["ks"], a["vs"], a["pages"], a["ps"], a["bt"], a["P"], a["sl"],
+                                      a["cu"], a["pl"], a["G"], a["out"], a["lse"], a["B"], a["Hq"], a["Hkv"], a["scale"], a["ws"],
+                                      a["nb"], None)
+
+
+@pytest.mark.parametrize("over,want", [
+    (dict(B=-1), INVALID), (dict(Hq=0), INVALID), (dict(Hkv=0), INVALID), (dict(Hq=5), INVALID), (dict(G=-1), INVALID),
+    (dict(P=0), INVALID), (dict(pages=0), INVALID), (dict(ps=0), INVALID), (dict(scale=math.nan), INVALID), (dict(q=None), INVALID),
+    (dict(k=None), INVALID), (dict(v=None), INVALID), (dict(bt=None), INVALID), (dict(sl=None), INVALID), (dict(cu=None), INVALID),
+    (dict(pl=None), INVALID), (dict(out=None), INVALID), (dict(ws=None), INVALID), (dict(ks=100), INVALID), (dict(ps=12), UNSUPPORTED),
+    (dict(ps=2048), UNSUPPORTED), (dict(ks=1 << 39, pages=1), UNSUPPORTED), (dict(B=2**23, Hq=4), UNSUPPORTED),
+    (dict(vs=2 * 16 * 128 + 4), MISALIGNED), (dict(q=A + 8), MISALIGNED), (dict(k=A + 8), MISALIGNED), (dict(out=A + 2), MISALIGNED),
+    (dict(ws=A + 8), MISALIGNED), (dict(cu=A + 2), MISALIGNED), (dict(pl=A + 1), MISALIGNED), (dict(lse=A + 2), MISALIGNED), (dict(B=0), OK)])
+def test_attn_prefix_decode_arguments(lib, over, want):
+    assert prefix(lib, **over) == want
+
+
+def test_attn_prefix_decode_workspace_size(lib):
+    n = [K.kda_attn_prefix_decode_workspace_size(B, 64, 8, 10, 64, 4, sm_count=152) for B in (1, 8, 512)]
+    assert 0 < n[0] < n[1] < n[2] and all(x % 16 == 0 for x in n)
+    assert n[0] > K.kda_attn_decode_workspace_size(1, 64, 8, 10, 64, sm_count=152)
+    for bad, status in (((1, 4, 3, 4, 16, 1), INVALID), ((1, 4, 2, 4, 16, -1), INVALID), ((1, 4, 2, 4, 24, 1), UNSUPPORTED),
+                        ((2**23, 4, 2, 4, 16, 1), UNSUPPORTED)):
+        assert lib.kda_attn_prefix_decode_workspace_size(*bad, 152) == status
+    assert lib.kda_attn_prefix_decode_workspace_size(1, 4, 2, 4, 16, 1, -1) == INVALID
+
+
 def test_binding_refuses_tensors_that_do_not_fit():
     i32 = dict(dtype=torch.int32)
     t, l, r, s = torch.zeros(2, 3, **i32), torch.zeros(2, **i32), torch.zeros(5, **i32), torch.zeros(2, **i32)
@@ -93,3 +124,16 @@ def test_binding_refuses_tensors_that_do_not_fit():
                         (dict(v=k, k_cache=cache, v_cache=cache, slots=slots.int()), TypeError), (dict(), ValueError)):
         with pytest.raises(error):
             rope(**over)
+
+    q1, table, lens = torch.zeros(2, 4, 128, **bf), torch.zeros(2, 3, **i32), torch.zeros(2, **i32)
+
+    def attend(**over):
+        a = dict(q=q1, k_cache=cache, v_cache=cache, block_table=table, seq_lens=lens, cu_groups=lens, prefix_lens=lens[:1], out=q1,
+                 scale=1.0, workspace=None)
+        K.kda_attn_prefix_decode(**{**a, **over})
+
+    for over, error in ((dict(q=q), ValueError), (dict(cu_groups=lens[:1]), ValueError), (dict(prefix_lens=lens), ValueError),
+                        (dict(prefix_lens=None), TypeError), (dict(cu_groups=lens.float()), TypeError), (dict(lse=torch.zeros(2)), ValueError),
+                        (dict(out=None), TypeError), (dict(seq_lens=pos), ValueError), (dict(v_cache=cache[:1]), ValueError), (dict(), ValueError)):
+        with pytest.raises(error):
+            attend(**over)
