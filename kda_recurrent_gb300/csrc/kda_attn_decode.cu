@@ -706,7 +706,7 @@ __global__ void __launch_bounds__(kThreads, 3) kda_attn_prefix_join_kernel(const
     if (head < a.x.heads) {
         const int tail = a.x.tails[head];
         const PrefixCut pre = a.x.cuts[head];
-        const int before = a.x.start[head / a.p.num_q_heads] == 0 ? 0 : pre.per * (1 + pre.ctas);
+        const int before = a.x.start[head / a.p.num_q_heads] == 0 ? 0 : a.x.parts_of(pre);
         Cut cut;
         cut.count = tail == kTailHome ? 1 : 0;
         if (tail >= 0) cut = a.ws.cuts[tail];

@@ -637,6 +637,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     l += sum[0].x + sum[0].y;
                     tmem_wait_st();
                     tc_fence_before();
+#ifdef KDA_TEST_WITHHOLD_HANDOFF  // failure-detection test: one hand-off never comes
+                    if (used != KDA_TEST_WITHHOLD_HANDOFF || half == 0)
+#endif
                     arrive_warp(&B->p[g][half]);
                 }
             }

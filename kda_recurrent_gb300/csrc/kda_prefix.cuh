@@ -29,6 +29,12 @@ struct PrefixParts {
                       // for each CTA
     int32_t ctas;
 
+    // Parts of a row's prefix; none where the record makes no sense (a CTA that gave up wrote none).
+    __device__ __forceinline__ int parts_of(const PrefixCut &c) const {
+        const bool sane = (c.per == 1 || c.per == 2) && c.slot >= 0 && c.slot < kPrefixSlots / c.per && c.cta >= 0 && c.ctas >= 0 &&
+                          c.cta <= ctas && c.ctas <= ctas - c.cta;
+        return sane ? c.per * (1 + c.ctas) : 0;
+    }
     __device__ __forceinline__ int64_t part_at(const PrefixCut &c, int64_t head, int i) const {
         if (i < c.per) return (int64_t)i * heads + head;
         const int j = i - c.per, behind = c.per == 2 ? j >> 1 : j, w = c.per == 2 ? j & 1 : 0;
