@@ -79,6 +79,45 @@ def test_pages_given_back_in_many_rounds_by_a_cluster():
     check_resize(old, new, 8, seed=9, in_place=True)
 
 
+@pytest.mark.parametrize("in_place", [False, True])
+def test_pages_of_wide_tables_on_a_cluster(in_place):
+    # few new tokens, but tables that could give many pages back: one launch of a cluster does everything
+    B = 200
+    old = lengths(B, 0, 3000, 31)
+    new = [n + 1 if i % 3 else n // 2 for i, n in enumerate(old)]
+    check_resize(old, new, 8, seed=31, max_pages=400, in_place=in_place)
+    check_resize([300000, 0, 300000, 9], [0, 50, 8, 10], 8, seed=32, in_place=in_place)  # three rounds of pages given back
+    check_resize([100] * 4200, [101] * 4100 + [99] * 100, 8, seed=33, max_pages=16, in_place=in_place)  # two launches
+
+
+@pytest.mark.parametrize("T", [30, 5000])
+def test_pages_maps_at_odd_addresses(T):
+    # maps that begin inside a 16-byte word, and are not written together
+    i32 = dict(dtype=torch.int32, device=DEV)
+    pages = -(-T // 16)
+    table, lens, state = torch.full((2, pages), -1, **i32), torch.zeros(2, **i32), torch.tensor([0, pages + 1], **i32)
+    ring = torch.arange(pages + 1, **i32).flip(0).contiguous()
+    slots = torch.full((T + 9,), -9, dtype=torch.int64, device=DEV)
+    positions, rows = (torch.full((T + 9,), -9, **i32) for _ in range(2))
+    K.kda_page_resize(table, lens, torch.tensor([T - 3, 3], **i32), ring, state, 16, lens, state, None, slots[1:T + 5],
+                      positions[3:T + 7], rows[2:T + 6])
+    page = [pages - i for i in range(pages + 1)]
+    first = -(-(T - 3) // 16)  # the second row's page
+    want = [page[t // 16] * 16 + t % 16 for t in range(T - 3)] + [page[first] * 16 + t for t in range(3)] + [-1] * 4
+    assert slots.tolist() == [-9] + want + [-9] * 4
+    assert positions.tolist() == [-9] * 3 + list(range(T - 3)) + [0, 1, 2] + [0] * 4 + [-9] * 2
+    assert rows.tolist() == [-9] * 2 + [0] * (T - 3) + [1] * 3 + [-1] * 4 + [-9] * 3
+
+
+def test_pages_new_lens_become_the_lengths():
+    i32 = dict(dtype=torch.int32, device=DEV)
+    for n in (7, 6000):  # one launch, and two
+        table, state = torch.full((1, 400), -1, **i32), torch.tensor([0, 400], **i32)
+        lens, new = torch.zeros(1, **i32), torch.tensor([n], **i32)
+        K.kda_page_resize(table, lens, new, torch.arange(400, **i32), state, 16, new, state, slots=torch.empty(n, dtype=torch.int64, device=DEV))
+        assert new.tolist() == [n] and lens.tolist() == [0] and state.tolist() == [-(-n // 16), 400 - -(-n // 16)]
+
+
 def test_pages_ring_wraps():
     for start in (0, 1, 10, 21, 22):
         check_resize([40, 0, 80], [0, 60, 85], 8, seed=3, start=start % 23, spare=0)
