@@ -203,17 +203,18 @@ __global__ void __launch_bounds__(kMaxThreads) kda_page_resize_kernel(const Page
             const uint32_t i0 = base + (uint32_t)me * kGive;
             int at_row = i0 < total[2] ? row_of(s_give, rows, i0) : 0;
 #pragma unroll
-            for (int e = 0; e < kGive; ++e) {
+            for (int e = 0; e < kGive; ++e) {  // (all loads before any check, whose report would keep them in order)
                 const uint32_t i = i0 + e;
                 page[e] = -1, row[e] = 0;
                 if (i < total[2]) {
                     while (s_give[at_row] <= i) ++at_row;
                     row[e] = at_row;
-                    const uint32_t before = row[e] > 0 ? s_give[row[e] - 1] : 0;
-                    page[e] = valid(p.block_table[(size_t)(r0 + row[e]) * p.max_pages + pages(s_new[row[e]]) + (i - before)], r0 + row[e]);
+                    const uint32_t before = at_row > 0 ? s_give[at_row - 1] : 0;
+                    page[e] = p.block_table[(size_t)(r0 + at_row) * p.max_pages + pages(s_new[at_row]) + (i - before)];
                 }
-                mine += page[e] >= 0;
             }
+#pragma unroll
+            for (int e = 0; e < kGive; ++e) page[e] = valid(page[e], r0 + row[e]), mine += page[e] >= 0;
             uint32_t sum = mine;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
