@@ -395,7 +395,7 @@ KDA_API int kda_cache_evict(void *k_cache, void *v_cache, int64_t k_page_stride,
  * Whole tiles of 128 shared tokens of a group of two rows or more are computed together, with
  * probabilities rounded to BF16 (and their sum formed before). A value that is not finite in such
  * a tile reaches its own channel of the group's rows. Equal inputs give equal bits. Where the
- * tables hold less than 72 MiB of keys and values in all (counted for each row and 16 query heads
+ * tables hold less than 48 MiB of keys and values in all (counted for each row and 16 query heads
  * of a key head), the call is kda_attn_decode's, and the groups are not looked at.
  */
 KDA_API int kda_attn_prefix_decode(const void *q, const void *k_cache, const void *v_cache,

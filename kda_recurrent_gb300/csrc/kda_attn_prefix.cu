@@ -5,8 +5,8 @@
 // The rows of a group hold the same first tokens in the same pages. Their query heads of one key head, laid end to
 // end, are the rows of a matrix, so that the prefix is a product of tiles of 128 query rows and 128 tokens: S = Q
 // K^T and O += P V with tcgen05, accumulators in tensor memory. Each key and value is read once for up to 256 query
-// rows instead of once a row. This kernel takes whole tiles of tokens; what is left of the prefix and each row's own
-// tokens are the token stream of kda_attn_decode.cu, which joins both sides' (m, l, o).
+// rows instead of once a row. Whole tiles of tokens are taken so; what is left of the prefix and each row's own tokens
+// are the token stream of kda_attn_stream.cuh. A second kernel joins both sides' (m, l, o).
 //
 // Schedule. An item is (group, key head, pair of tiles of query rows). A step of it takes one tile of tokens for two
 // tiles of query rows, or, when it has at most 128 query rows, two tiles of tokens for the one: either way two
@@ -14,17 +14,30 @@
 // steps, laid end to end, are cut into equal shares for the CTAs, one on an SM; a share's part of an item is left
 // in the workspace as (m, l, o). The sums run in a fixed order.
 //
-// Roles: eight warps in two groups for the softmax (a thread a query row, the 128 scores in its registers), one that
-// loads keys and values by TMA into a ring of five tiles, a box for each page (or 128 tokens of it) and half of the
-// channels, and one that issues the products. The probabilities replace their scores in tensor memory as BF16 (2^-8
+// One launch does both kinds of work: each CTA counts the steps and the rest's tiles, and the CTAs are dealt to the two so
+// that both end together. As two launches, one after the other, 25 shapes of 2 to 512 rows took 1.15 times as long (32
+// rows in 4 groups of 2048 to 8192 shared tokens 53.0 and now 45.1 us, 128 rows behind 32768 169.5 and 167.8; the other
+// way 512 rows in 16 groups: 290 and 302, since a step takes longer while the rest is streamed).
+//
+// Roles: eight warps in two groups for the softmax (a thread a query row, 64 scores at a time in its registers), one that
+// loads keys by TMA into a ring of three tiles and one that loads values into a ring of two, a box for each page (or 128
+// tokens of it) and half of the channels, and one for each group that issues its products. Half a tile's scores are
+// formed while the other half's softmax runs. The probabilities replace their scores in tensor memory as BF16 (2^-8
 // of each, which averages out over a prefix; their sum is formed from the unrounded ones) and are the A operand
 // of P V from there. O is scaled down only when a row's maximum has grown by more than 2^8 since it was last fixed.
+//
+// What bounds it. 128 rows of 64 heads behind 32768 tokens: 1.4e11 operations and 408 MB in 168 us, 830 TFLOP/s. A step has
+// 16.8 MFLOP (0.67 us of an SM's products) and 32768 exponentials (1.07 us), and takes 1.6 us where its tokens come from L2
+// and 2.1 and more where they come from HBM: the hand-offs between loads, products and softmax, 64 KB in flight.
+// 512 rows in 16 groups, 1.22 GB: 302 us, 4.0 TB/s; the rest's stream is 230 ns of an SM for a tile of 16 tokens with the
+// beginnings of its short rows, and the prefixes' steps 2.9 us.
 //
 // Tokens of missing pages: their scores are masked, and their rows of the tiles cleared, since a probability of zero
 // does not mask a NaN. All waits are bounded; on expiry the CTA records KDA_ERR_DEVICE_TIMEOUT, waits for its own
 // copies and products in flight, frees its tensor memory and returns.
 #include <algorithm>
 
+#include "kda_attn_stream.cuh"
 #include "kda_dependent.cuh"
 #include "kda_internal.cuh"
 #include "kda_mma.cuh"
@@ -44,6 +57,12 @@ constexpr int kLive = 8;  // masks kept (more tiles than the loads can be ahead 
 constexpr float kNegInf = -INFINITY;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kSlack = 8.0f;  // log2: how far a maximum may grow before O is scaled
+// What the work takes of an SM, in ns, by which the CTAs are dealt to its two kinds: a step of a prefix (the second: when
+// there are more items than CTAs for them, so that pairs of the same tokens are not read at the same time), the
+// beginning and end of an item, a tile of 16 tokens of the rest. Only their ratios count. Over 25 shapes: geometric mean
+// 0.869 of two launches' time, without the second kind of step 0.865 but 336 instead of 302 us for 512 rows in 16
+// groups (of 34, 38, 42 and 46 CTAs for its prefixes: 328, 303, 304 and 313); with 0, 4000 and 3000 ns an item 0.898, 0.889 and 0.865.
+constexpr float kStepNs = 1600.0f, kColdStepNs = 2100.0f, kItemNs = 3000.0f, kTileNs = 180.0f;
 constexpr int32_t kLeastRows = 2;  // of a group, for its prefix to be shared
 
 constexpr uint32_t kTmemCols = 512;  // all: the base is column 0
@@ -60,6 +79,8 @@ struct Bars {
     uint64_t drain[2];
     uint32_t live[kLive];  // of a tile of keys: a bit for eight tokens
     int64_t sums[kThreads / 32];
+    uint32_t tiles[kThreads / 32];
+    float items[kThreads / 32];
     int32_t group, offset;  // where the CTA's share begins: its first group, and the place in that
     uint32_t tmem;
     int32_t abort;
@@ -67,7 +88,7 @@ struct Bars {
 constexpr int kQ = kRing * kTile;
 constexpr int kBars = kQ + 2 * kTile;
 constexpr int kSmem = kBars + (int)sizeof(Bars);
-static_assert(kSmem <= 227 * 1024, "one CTA on an SM");
+static_assert(kSmem <= 227 * 1024 && kBars >= stream::kSmem<uint32_t>, "one CTA on an SM, of either kind");
 
 __device__ __forceinline__ float ex2(float x) {
     float y;
@@ -179,6 +200,24 @@ __device__ __forceinline__ Group group_of(const AttnPrefixArgs &a, int lo, int h
 __device__ __forceinline__ Group group_at(const AttnPrefixArgs &a, int g) {
     return group_of(a, a.cu_groups[g], a.cu_groups[g + 1], a.prefix_lens[g]);
 }
+
+// How many of a row's n tokens are taken with its group's: whole tiles of the group's prefix, if the row holds that.
+struct GroupStarts {
+    static constexpr bool kTail = true;
+    const AttnPrefixArgs &a;
+    bool none;  // nothing is shared
+    __device__ __forceinline__ int operator()(int b, int n) const {
+        if (none || b < a.cu_groups[0] || b >= a.cu_groups[a.groups]) return 0;
+        int lo = 0, hi = a.groups - 1;  // the last group that begins at the row or before it
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (a.cu_groups[mid] <= b) lo = mid;
+            else hi = mid - 1;
+        }
+        const Group g = group_at(a, lo);
+        return n >= g.tokens ? g.tiles * kT : 0;
+    }
+};
 
 // A CTA's walk over its share: the segments of items in it.
 struct Walk {
@@ -384,12 +423,13 @@ __device__ __forceinline__ void issue_products(const AttnPrefixArgs &a, Walk w, 
 }
 
 __global__ void __launch_bounds__(kThreads, 1)
-    kda_attn_prefix_kernel(const AttnPrefixArgs a, const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v) {
+    kda_attn_prefix_kernel(const AttnPrefixArgs a, const stream::Args rest, const __grid_constant__ CUtensorMap map_k,
+                           const __grid_constant__ CUtensorMap map_v) {
     extern __shared__ __align__(1024) uint8_t smem[];
     Bars *const B = reinterpret_cast<Bars *>(smem + kBars);
     const AttnDecodeArgs &p = a.d;
     const PagedCache &c = p.c;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, cta = blockIdx.x, ctas = gridDim.x;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, cta = blockIdx.x;
 
     if ((smem_addr(smem) & 1023) != 0) {  // (never: there is no other shared memory)
         if (threadIdx.x == 0) report_error(p.status, KDA_ERR_DEVICE_TIMEOUT, cta);
@@ -420,7 +460,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool bad = false;
     Walk w;
     w.g.row0 = w.g.rows = w.g.tiles = w.g.tokens = 0;
-    auto group_steps = [&](int g, Group &x) {
+    auto group_steps = [&](int g, Group &x, float &items) {
         x.row0 = x.rows = x.tiles = x.tokens = 0;
         if (g >= a.groups) return (int64_t)0;
         const int lo = a.cu_groups[g], hi = a.cu_groups[g + 1], n = a.prefix_lens[g];
@@ -428,7 +468,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (cta == 0 && (wrong || n < 0 || n > c.capacity)) report_error(p.status, KDA_ERR_DEVICE_INPUT, g);
         bad |= wrong;
         if (!wrong) x = group_of(a, lo, hi, n);
-        return (int64_t)c.num_kv_heads * head_steps(a, x);
+        const int64_t steps = (int64_t)c.num_kv_heads * head_steps(a, x);
+        if (x.tiles > 0) items += (float)(c.num_kv_heads * ((query_rows(a, x) + kPrefixSlots - 1) / kPrefixSlots));
+        return steps;
     };
     auto scan = [&](int64_t x) {  // inclusive, over the warp
 #pragma unroll
@@ -438,28 +480,53 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         return x;
     };
+    auto warp_sum = [](float x) {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+        return x;
+    };
     int64_t all;
     int per = 1, offset = 0;  // the length of a share; this one's place in its first group
-    auto share = [&] {
+    int ctas = 0;             // of the prefixes; the others stream what is left of the rows
+    auto share = [&](float items) {
         bad |= all > 0x3fffffff;  // (tables that repeat their pages very often: places are 32-bit numbers below)
         const int total = bad ? 0 : (int)all;
-        per = max((total + ctas - 1) / ctas, 1);
+        const GroupStarts starts = {a, bad};
+        uint32_t tiles = 0;
+        for (int b = threadIdx.x; b < c.batch; b += kThreads) {
+            const int n = row_length(c, b, p.status, cta == 0);
+            tiles += (uint32_t)(n - starts(b, n) + stream::kTokens - 1) / stream::kTokens;
+        }
+        tiles = __reduce_add_sync(0xffffffffu, tiles);
+        if (lane == 0) B->tiles[warp] = tiles;
+        __syncthreads();
+        tiles = __reduce_add_sync(0xffffffffu, lane < kThreads / 32 ? B->tiles[lane] : 0);
+        // both kinds of work end together, by what a step and a tile take of an SM
+        const float rest_ns = (float)tiles * (float)(c.num_kv_heads * rest.q_tiles) * kTileNs;
+        auto deal = [&](float step_ns) {
+            const float ns = (float)total * step_ns + items * kItemNs;
+            return total == 0 ? 0 : min(max((int)((float)gridDim.x * (ns / (ns + rest_ns)) + 0.5f), 1), (int)gridDim.x - 1);
+        };
+        ctas = deal(kStepNs);
+        if (items > (float)ctas) ctas = deal(kColdStepNs);
+        per = max((total + ctas - 1) / max(ctas, 1), 1);
+        ctas = (total + per - 1) / per;  // (the last ones' shares would be empty)
         w.first = min(cta * per, total);
-        w.left = min(per, total - w.first);
+        w.left = cta < ctas ? min(per, total - w.first) : 0;
     };
     if (a.groups <= 32) {  // each warp by itself
         Group x;
-        const int64_t mine = group_steps(lane, x), sum = scan(mine);
+        float items = 0.0f;
+        const int64_t mine = group_steps(lane, x, items), sum = scan(mine);
         all = __shfl_sync(0xffffffffu, sum, 31);
         bad = __any_sync(0xffffffffu, bad);
-        share();
+        share(warp_sum(items));
         const int64_t off = w.first - (sum - mine);
         const uint32_t here = __ballot_sync(0xffffffffu, w.left > 0 && off >= 0 && off < mine);
         w.index = here ? __ffs(here) - 1 : 0;
         offset = __shfl_sync(0xffffffffu, (int)off, w.index);
         w.g.row0 = __shfl_sync(0xffffffffu, x.row0, w.index), w.g.rows = __shfl_sync(0xffffffffu, x.rows, w.index);
         w.g.tiles = __shfl_sync(0xffffffffu, x.tiles, w.index), w.g.tokens = __shfl_sync(0xffffffffu, x.tokens, w.index);
-        __syncthreads();
     } else {
         Group x;
         auto block_scan = [&](int64_t v, int64_t &total) {
@@ -473,14 +540,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             return sum + before;
         };
         int64_t mine = 0;
-        for (int g = threadIdx.x; g < a.groups; g += kThreads) mine += group_steps(g, x);
+        float items = 0.0f, unused = 0.0f;
+        for (int g = threadIdx.x; g < a.groups; g += kThreads) mine += group_steps(g, x, items);
+        items = warp_sum(items);
+        if (lane == 0) B->items[warp] = items;
         bad = __syncthreads_or(bad);  // then nothing is taken as shared: the rows' own tables hold all of their tokens
         block_scan(mine, all);
-        share();
+        share(warp_sum(lane < kThreads / 32 ? B->items[lane] : 0.0f));
         int64_t before = 0;
         for (int g0 = 0; w.left > 0 && g0 < a.groups; g0 += kThreads) {
             int64_t total;
-            mine = group_steps(g0 + threadIdx.x, x);
+            mine = group_steps(g0 + threadIdx.x, x, unused);
             const int64_t sum = block_scan(mine, total), off = w.first - before - (sum - mine);
             if (off >= 0 && off < mine) B->group = g0 + threadIdx.x, B->offset = (int)off;
             before += total;
@@ -493,6 +563,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     tc_fence_after();
     const uint32_t tmem = B->tmem;
+    if (cta >= ctas) {
+        if (warp == kWarpMma) tmem_dealloc(tmem, kTmemCols);
+        // 12 warps of 168 registers (64512): eight of 232 and four of 40
+        if (warp >= stream::kWarps) {
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+            return;
+        }
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
+        stream::walk_share<uint32_t>(rest, cta - ctas, gridDim.x - ctas, smem, GroupStarts{a, bad},
+                                     [] { asm volatile("bar.sync 1, %0;" ::"n"(stream::kThreads) : "memory"); });
+        return;
+    }
     if (w.left > 0) {
         const int per_head = (int)head_steps(a, w.g), pairs = (query_rows(a, w.g) + kPrefixSlots - 1) / kPrefixSlots;
         w.head = offset / per_head;
@@ -506,19 +588,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (warp < kWarpMma) {
             load_tiles(a, w, per, warp == kWarpKeys ? &map_k : &map_v, warp == kWarpKeys, smem, B);
         } else {
-            if (warp != kWarpMma) {
-                // each row's start: this CTA's of every group's rows, and of the rows of no group
-                if (!bad) {
-                    for (int g = lane; g < a.groups; g += 32) {
-                        const Group x = group_at(a, g);
-                        for (int b = x.row0 + cta; b < x.row0 + x.rows; b += ctas)
-                            a.x.start[b] = row_length(c, b, p.status, true) >= x.tokens ? x.tiles * kT : 0;
-                    }
-                }
-                const int from = bad ? c.batch : a.cu_groups[0], to = bad ? c.batch : a.cu_groups[a.groups];
-                for (int b = cta * 32 + lane; b < c.batch; b += ctas * 32)
-                    if (b < from || b >= to) a.x.start[b] = 0;
-            }
             issue_products(a, w, warp - kWarpMma, smem, B);
         }
     } else {
@@ -646,7 +715,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!ok) break;
             count += tiles_in(w);
             // ---- the segment's part
-            const int part = w.step == 0 ? (shared ? 0 : g * a.x.heads) + head : 3 * a.x.heads + cta * kPrefixSlots + g * kT + r;  // (below 2^26)
+            const int part = w.step == 0 ? (shared ? 0 : g * a.x.heads) + head : 3 * a.x.heads + cta * kPrefixSlots + g * kT + r;
             if (steps > 0) {
                 ok = wait_warp(&B->o[g][1], segments & 1, B);
                 ++segments;
@@ -696,6 +765,95 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
+// Joins all parts of a query row: those of its prefix and those of the rest, in this order, by `per_row` half-warps of
+// a CTA, which take every per_row-th part. A lane has eight channels, and four parts' loads in flight. (With a warp a
+// row, 32768 rows of two or three parts: 21.7 instead of 18.2 us from a cold cache.)
+constexpr int kJoinThreads = 256, kHalves = kJoinThreads / 16;
+
+__global__ void __launch_bounds__(kJoinThreads, 3) kda_attn_prefix_join_kernel(const stream::Args a, int per_row) {
+    __shared__ float s_m[kHalves], s_l[kHalves];
+    __shared__ float4 s_o[kHalves][32];
+    const int half = threadIdx.x >> 4, lane = threadIdx.x & 15;
+    const int64_t head = (int64_t)blockIdx.x * (kHalves / per_row) + half / per_row;
+    const int first = half % per_row;
+    allow_next();
+    wait_for_prior();
+    float m = kNegInf, l = 0.0f, o[8] = {};
+    auto add = [&](float pm, float pl, float ref, const float4 (&x)[2]) {
+        const float f = ex2(pm - ref);
+        l = fmaf(pl, f, l);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            o[4 * i] = fmaf(x[i].x, f, o[4 * i]), o[4 * i + 1] = fmaf(x[i].y, f, o[4 * i + 1]);
+            o[4 * i + 2] = fmaf(x[i].z, f, o[4 * i + 2]), o[4 * i + 3] = fmaf(x[i].w, f, o[4 * i + 3]);
+        }
+    };
+    if (head < a.x.heads) {
+        const int tail = a.x.tails[head];
+        const PrefixCut pre = a.x.cuts[head];
+        const int before = a.x.start[head / a.p.num_q_heads] == 0 ? 0 : a.x.parts_of(pre);
+        stream::Cut cut;
+        cut.count = tail == kTailHome ? 1 : 0;
+        if (tail >= 0) cut = a.ws.cuts[tail];
+        const int row = tail >= 0 ? (int)(head - cut.head) : 0, n = before + cut.count;
+        constexpr int kAhead = 4;
+        for (int i = first; i < n; i += kAhead * per_row) {
+            float pm[kAhead], pl[kAhead];
+            float4 po[kAhead][2];
+            float top = m;
+#pragma unroll
+            for (int e = 0; e < kAhead; ++e) {
+                const int x = i + e * per_row;
+                pm[e] = kNegInf, pl[e] = 0.0f, po[e][0] = po[e][1] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                if (x >= n) continue;
+                const float *src;
+                if (x < before || tail < 0) {
+                    const int64_t part = x < before ? a.x.part_at(pre, head, x) : 2 * (int64_t)a.x.heads + head;
+                    const float2 ml = a.x.ml[part];
+                    pm[e] = ml.x, pl[e] = ml.y;
+                    src = a.x.o + part * kHeadDim;
+                } else {
+                    const stream::Part *const part = a.ws.parts + cut.part_at(x - before);
+                    pm[e] = part->m[row], pl[e] = part->l[row];
+                    src = part->o[row];
+                }
+                po[e][0] = reinterpret_cast<const float4 *>(src)[2 * lane], po[e][1] = reinterpret_cast<const float4 *>(src)[2 * lane + 1];
+            }
+#pragma unroll
+            for (int e = 0; e < kAhead; ++e) top = fmaxf(top, pm[e]);
+            const float ref = top == kNegInf ? 0.0f : top, keep = ex2(m - ref);
+            l *= keep;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) o[e] *= keep;
+#pragma unroll
+            for (int e = 0; e < kAhead; ++e) add(pm[e], pl[e], ref, po[e]);
+            m = top;
+        }
+    }
+    if (per_row > 1) {
+        if (lane == 0) s_m[half] = m, s_l[half] = l;
+        s_o[half][2 * lane] = make_float4(o[0], o[1], o[2], o[3]), s_o[half][2 * lane + 1] = make_float4(o[4], o[5], o[6], o[7]);
+        __syncthreads();
+        if (first > 0) return;
+        m = kNegInf, l = 0.0f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) o[e] = 0.0f;
+        for (int w = 0; w < per_row; ++w) m = fmaxf(m, s_m[half + w]);
+        const float ref = m == kNegInf ? 0.0f : m;
+        for (int w = 0; w < per_row; ++w) {
+            const float4 x[2] = {s_o[half + w][2 * lane], s_o[half + w][2 * lane + 1]};
+            add(s_m[half + w], s_l[half + w], ref, x);
+        }
+    }
+    if (head >= a.x.heads) return;
+    const float inv = 1.0f / l;  // (l = 0: zeros, whatever the values)
+    uint4 y = make_uint4(0, 0, 0, 0);
+    if (l != 0.0f) y = make_uint4(pack_bf16(o[0] * inv, o[1] * inv), pack_bf16(o[2] * inv, o[3] * inv), pack_bf16(o[4] * inv, o[5] * inv),
+                                  pack_bf16(o[6] * inv, o[7] * inv));
+    reinterpret_cast<uint4 *>(a.p.out + head * kHeadDim)[lane] = y;
+    if (lane == 0 && a.p.lse) a.p.lse[head] = l == 0.0f ? kNegInf : ((m == kNegInf ? 0.0f : m) + log2f(l)) * stream::kLn2;
+}
+
 // A cache's tokens as [pages][heads][page size][128], in boxes of a page's (or 128) tokens of one head x 64 channels.
 cudaError_t page_map(CUtensorMap *map, const __nv_bfloat16 *base, const PagedCache &c, int64_t page_stride) {
     const EncodeTiled encode = encode_tiled();
@@ -730,10 +888,11 @@ int64_t attn_prefix_workspace_bytes(int32_t batch, int32_t num_q_heads, int32_t 
 }
 
 // Where each row reads its own tokens alone anyway: no groups, or so few tokens in all rows' tables that reading them
-// row by row takes less than a launch more. Row by row and shared, in us: 2 rows of 512 tokens on 8/8 heads (5 MB) 8.0
-// and 16.0; 8 of 2048 on 8/8 (69 MB) 17.7 and 18.1; 16 of 1024 on 8/8 (71 MB) 19.1 and 19.0; 8 of 4096 on 32/8 (136 MB) 27.5
-// and 21.7; 64 of 2048 on 64/8 in two groups (554 MB) 87 and 28.
-constexpr int64_t kFewBytes = 72LL << 20;
+// row by row takes less than a launch more. Row by row and shared, in us: 4 rows of 2048 tokens on 8/8 heads (35 MB) 13.0
+// and 13.7; 16 of 512 on 64/8 (38 MB) 15.2 and 15.8; 6 of 2048 on 8/8 (52 MB) 15.8 and 13.9; 16 of 768 on 64/8 (55 MB)
+// 18.1 and 16.1; 8 of 2048 on 8/8 (69 MB) 17.5 and 14.4; 8 of 4096 on 32/8 (136 MB) 27.5 and 17.2; 64 of 2048 on 64/8 in two
+// groups (554 MB) 87 and 23. (With one key head, two rows and 32768 tokens it is 20.2 and 23.7.)
+constexpr int64_t kFewBytes = 48LL << 20;
 
 cudaError_t launch_attn_prefix(const AttnPrefixArgs &args, cudaStream_t stream) {
     const int64_t reads = (int64_t)args.d.c.batch * args.d.c.num_kv_heads * ((args.d.group + 15) / 16) * args.d.c.capacity;
@@ -745,13 +904,21 @@ cudaError_t launch_attn_prefix(const AttnPrefixArgs &args, cudaStream_t stream) 
     prefix_layout(&a.x,
                   static_cast<char *>(a.d.ws) + attn_decode_workspace_bytes(c.batch, a.d.num_q_heads, c.num_kv_heads, c.capacity, false, sms),
                   c.batch, a.d.num_q_heads, sms);
+    stream::Args rest;
+    if (!stream::stream_args(&rest, a.d, sms)) return launch_attn_decode(args.d, stream);  // (more than 2^35 tokens of all tables)
+    rest.x = a.x;
     CUtensorMap map_k, map_v;
     cudaError_t e = page_map(&map_k, c.k, c, c.k_page_stride);
     if (e == cudaSuccess) e = page_map(&map_v, c.v, c, c.v_page_stride);
     if (e == cudaSuccess) e = configure_once();
-    if (e == cudaSuccess) e = launch_dependent(kda_attn_prefix_kernel, dim3((unsigned)sms), kThreads, kSmem, stream, a, map_k, map_v);
-    if (e == cudaSuccess) e = launch_attn_tails(a.d, a.x, stream);
-    return e;
+    if (e == cudaSuccess) e = launch_dependent(kda_attn_prefix_kernel, dim3((unsigned)sms), kThreads, kSmem, stream, a, rest, map_k, map_v);
+    if (e != cudaSuccess) return e;
+    // half-warps of a query row: all of a CTA's for few rows, which can have long rests in many parts
+    int per_row = kHalves;
+    while (per_row > 1 && (int64_t)a.x.heads * per_row > (int64_t)sms * 3 * kHalves) per_row /= 2;
+    const int rows = kHalves / per_row;
+    return launch_dependent(kda_attn_prefix_join_kernel, dim3((unsigned)((a.x.heads + rows - 1) / rows)), kJoinThreads, 0, stream, rest,
+                            per_row);
 }
 
 }  // namespace kda

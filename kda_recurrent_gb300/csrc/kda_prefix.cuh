@@ -1,5 +1,5 @@
-// What the kernel that attends to shared prefixes (kda_attn_prefix.cu) leaves for the one that attends to the rest
-// of each row (kda_attn_decode.cu), which joins both.
+// What attention to shared prefixes (kda_attn_prefix.cu) leaves beside the parts of the rest of each row
+// (kda_attn_stream.cuh), for the join of both.
 #pragma once
 
 #include <stdint.h>
@@ -67,9 +67,6 @@ struct AttnPrefixArgs {
 };
 
 int64_t attn_prefix_workspace_bytes(int32_t batch, int32_t num_q_heads, int32_t num_kv_heads, int64_t capacity, int32_t sms);
-// Attention to the rows' tokens from x.start on, joined with the parts of those before (kda_attn_decode.cu); `ws` as
-// for kda_attn_decode without weights.
-cudaError_t launch_attn_tails(const AttnDecodeArgs &p, const PrefixParts &x, cudaStream_t stream);
 cudaError_t launch_attn_prefix(const AttnPrefixArgs &a, cudaStream_t stream);
 
 }  // namespace kda

@@ -236,9 +236,9 @@ def test_prefix_wide_table():
     assert torch.equal(out, got) and torch.equal(lse, got_lse)
 
 
-@pytest.mark.parametrize("rows,Hq,Hkv,tokens", [(3, 2, 2, 24570), (3, 2, 2, 24584), (5, 40, 2, 4912), (5, 40, 2, 4920)])
+@pytest.mark.parametrize("rows,Hq,Hkv,tokens", [(3, 2, 2, 16384), (3, 2, 2, 16392), (5, 40, 2, 4912), (5, 40, 2, 4920)])
 def test_prefix_beside_the_limit_of_few_tokens(rows, Hq, Hkv, tokens):
-    # 72 MiB are 147456 tokens of a row's key head and 16 query heads: rows x Hkv x ceil(group / 16) x table's tokens
+    # 48 MiB are 98304 tokens of a row's key head and 16 query heads: rows x Hkv x ceil(group / 16) x table's tokens
     c = inputs([0, rows], [700], [3] * rows, Hkv, 8, rows, max_pages=-(-tokens // 8))
     q = queries(rows, Hq, 40)
     out, lse = call(q, c)
