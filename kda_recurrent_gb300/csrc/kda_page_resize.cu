@@ -8,10 +8,16 @@
 // bisection. Nothing here is wide: it is a chain of dependent reads (lengths, sums, table or ring, map), and the
 // launch is most of a small call.
 //
-// Up to kFewTokens new tokens one launch does everything, of one CTA, or of a cluster where the tables could give many
-// pages back. More tokens are mapped by CTAs all over the GPU, four tokens a
+// Up to kFewTokens new tokens one launch does everything, of one CTA, or of a cluster where there are more than kOneCta or
+// the tables could give many pages back. More tokens are mapped by CTAs all over the GPU, four tokens a
 // thread, which also take the pages; a second launch of one cluster then gives pages back and sets the lengths and
-// the state, which the first one reads.
+// the state, which the first one reads. In us, calls back to back:
+//     tokens, one CTA and a cluster: 1024 3.5 and 4.4, 2048 4.1 and 4.7, 4096 5.1 and 4.4
+//     tokens, a cluster and two launches: 8192 5.1 and 7.0, 16384 5.8 and 7.1, 32768 7.2 and 7.0
+//     entries of the tables, one CTA and a cluster: 16384 4.0 and 6.8, 64000 (1000 rows) 7.0 and 9.3, 65536 (64 rows) 8.2
+//     and 7.7, 131072 14.2 and 7.8
+// 64 rows that grow by a token from a cold cache: 3.5 us; 1000 rows of a serving step's changes 16.3; 8 prompts of
+// 16384 tokens, 2.1 MB, 7.7.
 //
 // Pages given back are compacted (a missing page of the table is not given back) in table order: each thread
 // counts four entries, and the CTAs of the cluster exchange their counts through distributed shared memory.
@@ -28,7 +34,7 @@ constexpr int kMaxThreads = 1024;  // rows at a time, too
 constexpr int kMaxCluster = 8;
 constexpr int kGive = 4;  // entries of a thread at a time
 constexpr uint32_t kMost = 0x7fffffffu;
-constexpr int kFewTokens = 4096, kFewPages = 32768;  // (of all tables)
+constexpr int kOneCta = 2048, kFewTokens = 16384, kFewPages = 65536;  // (of all tables)
 
 // Sums of counts that stop at 2^31 - 1 (adding so is associative, too).
 __device__ __forceinline__ uint32_t add(uint32_t x, uint32_t y) { return min(x + y, kMost); }
@@ -293,7 +299,7 @@ __global__ void __launch_bounds__(kMaxThreads) kda_page_resize_kernel(const Page
 
 cudaError_t launch_page_resize(const PageResizeArgs &p, cudaStream_t stream) {
     if (p.max_tokens <= kFewTokens) {
-        const bool one = (int64_t)p.batch * p.max_pages <= kFewPages;
+        const bool one = (int64_t)p.batch * p.max_pages <= kFewPages && p.max_tokens <= kOneCta;
         const int threads = one && p.batch <= 256 && p.max_tokens <= 1024 ? 256 : kMaxThreads;
         const unsigned ctas = one ? 1 : kMaxCluster;
         return launch_clusters(ctas, kda_page_resize_kernel<true, true, 1>, dim3(ctas), (unsigned)threads, 0, stream, p);

@@ -87,10 +87,21 @@ def test_pages_of_wide_tables_on_a_cluster(in_place):
     new = [n + 1 if i % 3 else n // 2 for i, n in enumerate(old)]
     check_resize(old, new, 8, seed=31, max_pages=400, in_place=in_place)
     check_resize([300000, 0, 300000, 9], [0, 50, 8, 10], 8, seed=32, in_place=in_place)  # three rounds of pages given back
-    check_resize([100] * 4200, [101] * 4100 + [99] * 100, 8, seed=33, max_pages=16, in_place=in_place)  # two launches
+    check_resize([100] * 4200, [101] * 4100 + [99] * 100, 8, seed=33, max_pages=16, in_place=in_place)
 
 
-@pytest.mark.parametrize("T", [30, 5000])
+@pytest.mark.parametrize("tokens", [1024, 1025, 2048, 2049, 16384, 16385])  # of the maps: one CTA, a cluster, two launches
+@pytest.mark.parametrize("rows", [3, 300])
+@pytest.mark.parametrize("max_pages", [None, 700])
+def test_pages_beside_the_limits_of_few_tokens(tokens, rows, max_pages):
+    old = lengths(rows, 0, 900, tokens)
+    grow = tokens - 7  # (some of the maps stay empty)
+    new = [n + grow // rows + (i < grow % rows) if i % 50 != 2 else n // 2 for i, n in enumerate(old)]
+    T = sum(max(0, b - a) for a, b in zip(old, new))
+    check_resize(old, new, 16, seed=tokens, extra=tokens - T, max_pages=max_pages, in_place=rows == 300)
+
+
+@pytest.mark.parametrize("T", [30, 5000, 20000])
 def test_pages_maps_at_odd_addresses(T):
     # maps that begin inside a 16-byte word, and are not written together
     i32 = dict(dtype=torch.int32, device=DEV)
