@@ -27,8 +27,9 @@
 // of P V from there. O is scaled down only when a row's maximum has grown by more than 2^8 since it was last fixed.
 //
 // What bounds it. 128 rows of 64 heads behind 32768 tokens: 1.4e11 operations and 408 MB in 168 us, 830 TFLOP/s. A step has
-// 16.8 MFLOP (0.67 us of an SM's products) and 32768 exponentials (0.54 us), and takes 1.6 us where its tokens come from L2
-// and 2.1 and more where they come from HBM: the hand-offs between loads, products and softmax, 64 KB in flight.
+// 16.8 MFLOP (0.67 us of an SM's products) and 32768 exponentials (0.54 us), and takes 2.0 us, from L2 or HBM: the hand-offs
+// between products and softmax. With two tiles of tokens for at most 128 query rows it takes 1.7 us from L2 and 2.9 from HBM, 6.7
+// TB/s.
 // 512 rows in 16 groups, 1.22 GB: 302 us, 4.0 TB/s; the rest's stream is 230 ns of an SM for a tile of 16 tokens with the
 // beginnings of its short rows, and the prefixes' steps 2.9 us.
 //
