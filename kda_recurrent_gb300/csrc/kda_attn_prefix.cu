@@ -276,7 +276,7 @@ __device__ __forceinline__ void load_tiles(const AttnPrefixArgs &a, Walk w, int 
         const bool changed = leader_of != w.index;
         if (changed) leader = w.g.row0, leader_of = w.index;
         auto page_at = [&](int tile) {
-            return sub < boxes ? c.block_table[(size_t)leader * c.max_pages + ((tile * kT + sub * rows_a_box) >> c.page_shift)] : -1;
+            return sub < boxes && leader >= 0 ? c.block_table[(size_t)leader * c.max_pages + ((tile * kT + sub * rows_a_box) >> c.page_shift)] : -1;
         };
         auto page_of = [&](int page) {
             if (page >= c.num_pages) {
@@ -298,16 +298,18 @@ __device__ __forceinline__ void load_tiles(const AttnPrefixArgs &a, Walk w, int 
         done += w.n;
         int next = page_at(tile);
         // The pages are those of the first row that holds the whole prefix: most often the first one, whose table is
-        // read beside the rows' lengths.
-        for (int b0 = 0; changed && b0 < w.g.rows; b0 += 32) {
+        // read beside the rows' lengths. (If none does, nobody takes what is formed here, and no table is looked at.)
+        bool found = !changed;
+        for (int b0 = 0; !found && b0 < w.g.rows; b0 += 32) {
             const int b = w.g.row0 + b0 + lane;
             const bool has = b0 + lane < w.g.rows && row_length(c, b, a.d.status, false) >= w.g.tokens;
             const uint32_t who = __ballot_sync(0xffffffffu, has);
             if (!who) continue;
             leader = w.g.row0 + b0 + __ffs(who) - 1;
             if (leader != w.g.row0) next = page_at(tile);
-            break;
+            found = true;
         }
+        if (!found) leader = next = -1;
         next = page_of(next);
         for (int i = 0; i < tiles; ++i) {
             const int page = next, now = tile;

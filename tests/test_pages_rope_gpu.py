@@ -351,6 +351,44 @@ def test_rope_slots_past_the_cache_are_recorded():
     assert cache.sum().item() == 2 * 128 and (cache[0, :, 0, 3] == 1).all()
 
 
+@pytest.mark.parametrize("T", [5, 700])
+def test_rope_on_another_stream_and_in_a_graph(T):
+    gen = torch.Generator().manual_seed(T)
+    q, k, v = (torch.randn(T, h, 128, generator=gen).to(torch.bfloat16).to(DEV) for h in (6, 2, 2))
+    positions = torch.randint(0, 9000, (T,), generator=gen).to(torch.int32).to(DEV)
+    slots = torch.randperm(T + 40, generator=gen)[:T].to(DEV)
+    inv_freq, magnitude = K.rope_frequencies(96, factor=4.0, original_length=2048, device=DEV)
+    weight = torch.randn(128, generator=gen).to(DEV)
+
+    def caches():
+        return [torch.zeros(-(-(T + 40) // 16), 2, 16, 128, dtype=torch.bfloat16, device=DEV) for _ in range(2)]
+
+    def run(kc, vc, **kw):
+        return K.qk_norm_rope(q, k, positions, inv_freq, magnitude=magnitude, q_weight=weight, k_weight=weight, v=v, k_cache=kc,
+                              v_cache=vc, slots=slots, **kw)
+
+    want = caches()
+    want.append(run(*want))
+    got = caches()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got.append(run(*got, stream=side))
+    side.synchronize()
+    assert all(torch.equal(g, w) for g, w in zip(got, want))
+    got = caches()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got.append(run(*got))
+    positions2, slots2 = positions.flip(0).contiguous(), slots.flip(0).contiguous()
+    q2, k2, v2 = (x.flip(0).contiguous() for x in (q, k, v))
+    for x, y in ((positions, positions2), (slots, slots2), (q, q2), (k, k2), (v, v2)):  # other tokens in the same tensors
+        x.copy_(y)
+    for _ in range(2):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]) and torch.equal(got[2], want[2].flip(0))
+
+
 def test_rope_cache_offsets_pass_32_bits():
     ps, H = 1024, 8
     pages = 2**31 // (ps * H * 128) + 2

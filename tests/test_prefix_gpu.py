@@ -110,6 +110,21 @@ def test_prefix_first_row_of_a_group_is_padding():
     assert K.kda_device_status()[0] == K.KDA_OK
 
 
+@pytest.mark.parametrize("lens", [[0, 0], [0, 100], [511, 16]])
+def test_prefix_that_no_row_of_a_group_holds(lens):
+    # behind a row's tokens its table may hold anything, and nobody's prefix is read there
+    c = R.prefix_inputs([0, 2, 5], [512, 512], lens + [600, 512, 700], 2, 16, seed=5, device=DEV)
+    clean = dict(c, block_table=c["block_table"].clone())
+    for b, n in enumerate(lens):
+        c["block_table"][b, -(-n // 16):] = 2**30
+        clean["block_table"][b, -(-n // 16):] = -1
+    q = queries(5, 8, 5)
+    want = check(q, clean)
+    got = call(q, widened(c, 8))
+    assert K.kda_device_status()[0] == K.KDA_OK
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
 def test_prefix_copies_instead_of_shared_pages():
     check(queries(4, 4, 6), inputs([0, 4], [400], [5, 0, 100, 30], 2, 64, 6, copies=True))
 
