@@ -27,9 +27,12 @@
 // of P V from there. O is scaled down only when a row's maximum has grown by more than 2^8 since it was last fixed.
 //
 // What bounds it. 128 rows of 64 heads behind 32768 tokens: 1.4e11 operations and 408 MB in 168 us, 830 TFLOP/s. A step has
-// 16.8 MFLOP (0.67 us of an SM's products) and 32768 exponentials (0.54 us), and takes 2.0 us, from L2 or HBM: the hand-offs
-// between products and softmax. With two tiles of tokens for at most 128 query rows it takes 1.7 us from L2 and 2.9 from HBM, 6.7
-// TB/s.
+// 16.8 MFLOP (1.33 us of an SM's products at the library's rate) and 32768 exponentials (0.54 us), and takes 1.8 to 2.0 us,
+// from L2 or HBM: the warps that issue products wait for the tensor core most of the time, which reads 320 KB of shared
+// memory a step (1.3 us at 128 bytes a clock), since scores in half tiles read the queries twice. Scores by whole tiles
+// read 256 KB, but then a group's softmax waits for them: 32 rows in 4 groups 44.8 and so 44.2 us, 512 rows 301 and 294, 128 rows 168 and
+// 179, the geometric mean of 25 shapes the same. With two tiles of tokens for at most 128 query rows a step takes 1.7 us
+// from L2 and 2.9 from HBM, 6.7 TB/s.
 // 512 rows in 16 groups, 1.22 GB: 302 us, 4.0 TB/s; the rest's stream is 230 ns of an SM for a tile of 16 tokens with the
 // beginnings of its short rows, and the prefixes' steps 2.9 us.
 //
