@@ -424,7 +424,8 @@ KDA_API int64_t kda_attn_prefix_decode_workspace_size(int32_t batch, int32_t num
  *                its front and give back behind its end, both in row order and in the order of
  *                the table. What a call gives back, a later call can take.
  *   out_lens     int32 [batch]: the rows' lengths after the call. May equal seq_lens or new_lens.
- *   out_state    int32 [2]: {first, count} after the call. May equal free_state.
+ *   out_state    int32 [2]: {first, count} after the call. May equal free_state. (With many rows or new
+ *                tokens a call is faster whose out_lens and out_state are apart from its inputs.)
  *   cu_tokens    int32 [batch + 1], or NULL: sums of the new tokens, max(0, new - old) a row
  *   slots        int64 [max_tokens], or NULL: for each new token, packed row after row, page *
  *                page_size + offset (what kda_qk_norm_rope takes); -1 where its row got no pages

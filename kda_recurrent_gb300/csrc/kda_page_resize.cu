@@ -8,16 +8,17 @@
 // bisection. Nothing here is wide: it is a chain of dependent reads (lengths, sums, table or ring, map), and the
 // launch is most of a small call.
 //
-// Up to kFewTokens new tokens one launch does everything, of one CTA, or of a cluster where there are more than kOneCta or
-// the tables could give many pages back. More tokens are mapped by CTAs all over the GPU, four tokens a
-// thread, which also take the pages; a second launch of one cluster then gives pages back and sets the lengths and
-// the state, which the first one reads. In us, calls back to back:
-//     tokens, one CTA and a cluster: 1024 3.5 and 4.4, 2048 4.1 and 4.7, 4096 5.1 and 4.4
-//     tokens, a cluster and two launches: 8192 5.1 and 7.0, 16384 5.8 and 7.1, 32768 7.2 and 7.0
-//     entries of the tables, one CTA and a cluster: 16384 4.0 and 6.8, 64000 (1000 rows) 7.0 and 9.3, 65536 (64 rows) 8.2
-//     and 7.7, 131072 14.2 and 7.8
-// 64 rows that grow by a token from a cold cache: 3.5 us; 1000 rows of a serving step's changes 16.3; 8 prompts of
-// 16384 tokens, 2.1 MB, 7.7.
+// Few new tokens and small tables are one CTA's. Otherwise one launch of CTAs all over the GPU does everything: a cluster
+// gives pages back and sets the lengths and the state, the others map tokens, four a thread, and take the pages. Where the
+// lengths or the state are written over those before the call, which all CTAs read, that is not possible: then one
+// cluster does everything, or, with many tokens, a second launch of one cluster what the first kind does here. In us, calls back to back:
+//     outputs apart, one CTA and the whole GPU: 64 tokens 2.5 and 3.3, 1024 3.5 and 2.9, 2048 4.1 and 3.0, 4096 5.1 and 3.1;
+//     with 65536 entries of tables, 64 rows, 8.2 and 4.8; 1000 rows of 64000 entries 6.9 and 7.5
+//     in place, one CTA and a cluster: 1024 tokens 3.5 and 4.4, 2048 4.1 and 4.7, 4096 5.1 and 4.4; 16384 entries 4.0
+//     and 6.8, 64000 (1000 rows) 7.0 and 9.3, 65536 (64 rows) 8.2 and 7.7, 131072 14.2 and 7.8
+//     in place, a cluster and two launches: 8192 tokens 5.1 and 7.0, 16384 5.8 and 7.1, 32768 7.2 and 7.0
+// 64 rows that grow by a token from a cold cache: 3.5 us; 1000 rows of a serving step's changes 9.0 (in place 16.3); 8
+// prompts of 16384 tokens, 2.1 MB, 4.0 (in place 7.7).
 //
 // Pages given back are compacted (a missing page of the table is not given back) in table order: each thread
 // counts four entries, and the CTAs of the cluster exchange their counts through distributed shared memory.
@@ -34,7 +35,8 @@ constexpr int kMaxThreads = 1024;  // rows at a time, too
 constexpr int kMaxCluster = 8;
 constexpr int kGive = 4;  // entries of a thread at a time
 constexpr uint32_t kMost = 0x7fffffffu;
-constexpr int kOneCta = 2048, kFewTokens = 16384, kFewPages = 65536;  // (of all tables)
+// (tokens, entries of all tables) of one CTA, where the outputs are apart from the inputs and where not; of one cluster
+constexpr int kOneTokens = 512, kOnePages = 32768, kOneTokensInPlace = 2048, kOnePagesInPlace = 65536, kFewTokens = 16384;
 
 // Sums of counts that stop at 2^31 - 1 (adding so is associative, too).
 __device__ __forceinline__ uint32_t add(uint32_t x, uint32_t y) { return min(x + y, kMost); }
@@ -62,24 +64,27 @@ __device__ __forceinline__ int row_of(const uint32_t *sums, int n, uint32_t x) {
 }
 
 // kMaps: pages taken, slots, positions and rows of the new tokens. kState: pages given back, lengths and state.
-// kQuad: tokens of a thread at a time (1, or 4 that are written together).
-template <bool kMaps, bool kState, int kQuad>
-__global__ void __launch_bounds__(kMaxThreads) kda_page_resize_kernel(const PageResizeArgs p) {
+// kQuad: tokens of a thread at a time (1, or 4 that are written together). With both and kWide the first cluster has the
+// state and the CTAs behind it the maps; otherwise all CTAs do all.
+template <bool kMaps, bool kState, int kQuad, bool kWide>
+__global__ void __launch_bounds__(kMaxThreads, 1) kda_page_resize_kernel(const PageResizeArgs p) {
     __shared__ uint32_t s_tok[kMaxThreads], s_take[kMaxThreads], s_give[kMaxThreads];  // inclusive sums of a chunk's rows
     __shared__ int32_t s_old[kMaxThreads], s_new[kMaxThreads];
     __shared__ uint32_t s_warp[3][32];
     __shared__ uint32_t s_given[2][kMaxCluster];
     __shared__ uint32_t s_used;  // pages really taken
     const int threads = blockDim.x, warps = threads >> 5, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int rank = (int)blockIdx.x, ctas = (int)gridDim.x;  // (with kState the grid is one cluster)
-    const int me = rank * threads + threadIdx.x, all = ctas * threads;
+    const int rank = (int)blockIdx.x;
+    const bool state = kState && (!kWide || rank < kMaxCluster), maps = kMaps && (!kWide || rank >= kMaxCluster);
+    const int ctas = !kWide ? (int)gridDim.x : state ? kMaxCluster : (int)gridDim.x - kMaxCluster;  // (the state's are one cluster)
+    const int me = (kWide && maps ? rank - kMaxCluster : rank) * threads + threadIdx.x, all = ctas * threads;
     const int F = p.num_pages, ps = p.page_size;
     if (threadIdx.x == 0) s_used = 0;  // (first read behind the chunk's barriers)
     wait_for_prior();
     allow_next();
     int first = p.free_state[0], count = p.free_state[1];
     if (first < 0 || first >= F || count < 0 || count > F) {
-        if (kMaps && me == 0) report_error(p.status, KDA_ERR_DEVICE_INPUT, -1);
+        if (maps && me == 0) report_error(p.status, KDA_ERR_DEVICE_INPUT, -1);
         first = 0, count = 0;
     }
     auto pages = [&](int n) { return (uint32_t)((n + ps - 1) >> p.page_shift); };
@@ -94,8 +99,8 @@ __global__ void __launch_bounds__(kMaxThreads) kda_page_resize_kernel(const Page
         if (page < 0) report_error(p.status, KDA_ERR_DEVICE_INPUT, row);
         return valid(page, row);
     };
-    if (kMaps && me == 0 && p.cu_tokens) p.cu_tokens[0] = 0;
-    if (kState && ctas > 1) cluster_barrier();  // every CTA has begun: its shared memory may be written
+    if (maps && me == 0 && p.cu_tokens) p.cu_tokens[0] = 0;
+    if (state && ctas > 1) cluster_barrier();  // every CTA has begun: its shared memory may be written
 
     uint32_t tokens = 0, taken = 0, given = 0;  // of the rows before the chunk
     int round = 0;
@@ -149,14 +154,14 @@ __global__ void __launch_bounds__(kMaxThreads) kda_page_resize_kernel(const Page
 
         // ---- pages taken
         const uint32_t takes = min(total[1], left);
-        for (uint32_t i = me; kMaps && i < takes; i += all) {
+        for (uint32_t i = me; maps && i < takes; i += all) {
             const int row = row_of(s_take, rows, i);
             if (s_take[row] > left) continue;  // the row that does not fit
             const uint32_t have = pages(s_old[row]), before = row > 0 ? s_take[row - 1] : 0;
             p.block_table[(size_t)(r0 + row) * p.max_pages + have + (i - before)] = free_page(taken + i, r0 + row);
         }
         // ---- slots of the new tokens
-        if (kMaps && p.has_maps) {
+        if (maps && p.has_maps) {
             const uint32_t end = min(add(tokens, total[0]), (uint32_t)p.max_tokens);  // (of this chunk's rows)
             for (; quad * kQuad < end; quad += all) {
                 const uint32_t t0 = max(quad * kQuad, tokens), t1 = min((quad + 1) * kQuad, end);
@@ -204,7 +209,7 @@ __global__ void __launch_bounds__(kMaxThreads) kda_page_resize_kernel(const Page
             }
         }
         // ---- pages given back, behind the ring's end
-        for (uint32_t base = 0; kState && base < total[2]; base += (uint32_t)all * kGive, ++round) {
+        for (uint32_t base = 0; state && base < total[2]; base += (uint32_t)all * kGive, ++round) {
             int page[kGive], mine = 0, row[kGive];
             const uint32_t i0 = base + (uint32_t)me * kGive;
             int at_row = i0 < total[2] ? row_of(s_give, rows, i0) : 0;
@@ -265,10 +270,10 @@ __global__ void __launch_bounds__(kMaxThreads) kda_page_resize_kernel(const Page
         // ---- the rows' new lengths, when no CTA reads the old ones any more
         const uint32_t end = add(taken, x[1]);
         const int best = served && my_take > 0 ? (int)end : 0;
-        if (kState && ctas > 1) cluster_barrier();
-        if (kState && rank == 0 && (int)threadIdx.x < rows) p.out_lens[r] = served ? m : n;
+        if (state && ctas > 1) cluster_barrier();
+        if (state && rank == 0 && (int)threadIdx.x < rows) p.out_lens[r] = served ? m : n;
         // pages really taken: the sum at the last row that was served
-        if (kState) {
+        if (state) {
             const uint32_t top = __reduce_max_sync(0xffffffffu, (uint32_t)best);
             if (lane == 0 && top > 0) atomicMax(&s_used, top);
         }
@@ -276,14 +281,14 @@ __global__ void __launch_bounds__(kMaxThreads) kda_page_resize_kernel(const Page
         taken = add(taken, total[1]);
         __syncthreads();
     }
-    if (kMaps && p.has_maps) {
+    if (maps && p.has_maps) {
         for (uint32_t i = tokens + me; i < (uint32_t)p.max_tokens; i += all) {
             if (p.slots) p.slots[i] = -1;
             if (p.positions) p.positions[i] = 0;
             if (p.rows) p.rows[i] = -1;
         }
     }
-    if (!kState) return;
+    if (!state) return;
     if (ctas > 1) cluster_barrier();  // the state has been read
     else __syncthreads();
     if (me == 0) {
@@ -295,22 +300,33 @@ __global__ void __launch_bounds__(kMaxThreads) kda_page_resize_kernel(const Page
     }
 }
 
+// Whether `out` and `in`, both of n numbers, have none in common.
+bool apart(const int32_t *out, const int32_t *in, int64_t n) {
+    const intptr_t x = reinterpret_cast<intptr_t>(out), y = reinterpret_cast<intptr_t>(in);
+    return (x < y ? y - x : x - y) >= n * 4;
+}
+
 }  // namespace
 
 cudaError_t launch_page_resize(const PageResizeArgs &p, cudaStream_t stream) {
-    if (p.max_tokens <= kFewTokens) {
-        const bool one = (int64_t)p.batch * p.max_pages <= kFewPages && p.max_tokens <= kOneCta;
-        const int threads = one && p.batch <= 256 && p.max_tokens <= 1024 ? 256 : kMaxThreads;
-        const unsigned ctas = one ? 1 : kMaxCluster;
-        return launch_clusters(ctas, kda_page_resize_kernel<true, true, 1>, dim3(ctas), (unsigned)threads, 0, stream, p);
+    const bool others = apart(p.out_lens, p.seq_lens, p.batch) && apart(p.out_lens, p.new_lens, p.batch) && apart(p.out_state, p.free_state, 2);
+    if ((int64_t)p.batch * p.max_pages <= (others ? kOnePages : kOnePagesInPlace) && p.max_tokens <= (others ? kOneTokens : kOneTokensInPlace)) {
+        const unsigned threads = p.batch <= 256 && p.max_tokens <= 1024 ? 256 : kMaxThreads;
+        return launch_dependent(kda_page_resize_kernel<true, true, 1, false>, dim3(1), threads, 0, stream, p);
     }
     int32_t sms = 0;
     if (sm_count_of_current_device(&sms) != KDA_OK) return cudaErrorInvalidDevice;
     const int threads = p.batch <= 256 ? 256 : kMaxThreads, quads = (p.max_tokens + 3) / 4;
-    const int ctas = std::min((quads + threads - 1) / threads, sms * (kMaxThreads / threads));
-    const cudaError_t e = launch_dependent(kda_page_resize_kernel<true, false, 4>, dim3((unsigned)ctas), (unsigned)threads, 0, stream, p);
+    const int ctas = std::max(std::min((quads + threads - 1) / threads, sms * (kMaxThreads / threads)), 1);
+    if (others) {
+        const int grid = (kMaxCluster + ctas + kMaxCluster - 1) / kMaxCluster * kMaxCluster;
+        return launch_clusters(kMaxCluster, kda_page_resize_kernel<true, true, 4, true>, dim3((unsigned)grid), (unsigned)threads, 0, stream, p);
+    }
+    if (p.max_tokens <= kFewTokens)
+        return launch_clusters(kMaxCluster, kda_page_resize_kernel<true, true, 1, false>, dim3(kMaxCluster), kMaxThreads, 0, stream, p);
+    const cudaError_t e = launch_dependent(kda_page_resize_kernel<true, false, 4, false>, dim3((unsigned)ctas), (unsigned)threads, 0, stream, p);
     if (e != cudaSuccess) return e;
-    return launch_clusters(kMaxCluster, kda_page_resize_kernel<false, true, 1>, dim3(kMaxCluster), kMaxThreads, 0, stream, p);
+    return launch_clusters(kMaxCluster, kda_page_resize_kernel<false, true, 1, false>, dim3(kMaxCluster), kMaxThreads, 0, stream, p);
 }
 
 }  // namespace kda

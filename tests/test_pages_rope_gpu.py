@@ -73,10 +73,14 @@ def test_pages_prompts_on_a_cluster(lens, ps):
     check_resize(lens, [0] * len(lens), ps, seed=8, in_place=True)
 
 
-def test_pages_given_back_in_many_rounds_by_a_cluster():
-    # rows of both kinds, tokens enough for a cluster, more pages given back than one round holds
+@pytest.mark.parametrize("in_place", [False, True])
+def test_pages_given_back_in_many_rounds_by_a_cluster(in_place):
+    # rows of both kinds, tokens enough for all of the GPU, more pages given back than one round holds
     old, new = [0, 60000, 33, 300000, 0, 5], [40000, 7, 33, 0, 900, 6]
-    check_resize(old, new, 8, seed=9, in_place=True)
+    check_resize(old, new, 8, seed=9, in_place=in_place)
+    old = lengths(1100, 0, 300, 34)  # rows of two rounds, too
+    check_resize(old, [n + 100 if i % 2 else n // 3 for i, n in enumerate(old)], 16, seed=34, in_place=in_place)
+    check_resize(old, [n + 100 if i % 2 else n // 3 for i, n in enumerate(old)], 16, seed=35, in_place=in_place, drop=700)
 
 
 @pytest.mark.parametrize("in_place", [False, True])
@@ -90,15 +94,16 @@ def test_pages_of_wide_tables_on_a_cluster(in_place):
     check_resize([100] * 4200, [101] * 4100 + [99] * 100, 8, seed=33, max_pages=16, in_place=in_place)
 
 
-@pytest.mark.parametrize("tokens", [1024, 1025, 2048, 2049, 16384, 16385])  # of the maps: one CTA, a cluster, two launches
-@pytest.mark.parametrize("rows", [3, 300])
-@pytest.mark.parametrize("max_pages", [None, 700])
-def test_pages_beside_the_limits_of_few_tokens(tokens, rows, max_pages):
+@pytest.mark.parametrize("tokens", [512, 513, 1024, 1025, 2048, 2049, 16384, 16385])  # of the maps: one CTA, a cluster, the whole GPU
+@pytest.mark.parametrize("rows,max_pages", [(3, None), (3, 700), (300, None), (300, 109), (300, 110), (300, 218), (300, 219)])
+@pytest.mark.parametrize("in_place", [False, True])
+def test_pages_beside_the_limits_of_few_tokens(tokens, rows, max_pages, in_place):
+    # (300 rows: up to 32768 entries of the tables, up to 65536, more)
     old = lengths(rows, 0, 900, tokens)
     grow = tokens - 7  # (some of the maps stay empty)
     new = [n + grow // rows + (i < grow % rows) if i % 50 != 2 else n // 2 for i, n in enumerate(old)]
     T = sum(max(0, b - a) for a, b in zip(old, new))
-    check_resize(old, new, 16, seed=tokens, extra=tokens - T, max_pages=max_pages, in_place=rows == 300)
+    check_resize(old, new, 16, seed=tokens, extra=tokens - T, max_pages=max_pages, in_place=in_place)
 
 
 @pytest.mark.parametrize("T", [30, 5000, 20000])
@@ -122,11 +127,14 @@ def test_pages_maps_at_odd_addresses(T):
 
 def test_pages_new_lens_become_the_lengths():
     i32 = dict(dtype=torch.int32, device=DEV)
-    for n in (7, 6000):  # one launch, and two
-        table, state = torch.full((1, 400), -1, **i32), torch.tensor([0, 400], **i32)
-        lens, new = torch.zeros(1, **i32), torch.tensor([n], **i32)
-        K.kda_page_resize(table, lens, new, torch.arange(400, **i32), state, 16, new, state, slots=torch.empty(n, dtype=torch.int64, device=DEV))
-        assert new.tolist() == [n] and lens.tolist() == [0] and state.tolist() == [-(-n // 16), 400 - -(-n // 16)]
+    for n in (7, 6000, 30000):  # one CTA, a cluster, two launches
+        table, state = torch.full((1, 1900), -1, **i32), torch.tensor([0, 1900], **i32)
+        lens, new, after = torch.zeros(1, **i32), torch.tensor([n], **i32), torch.empty(2, **i32)
+        slots = torch.empty(n, dtype=torch.int64, device=DEV)
+        K.kda_page_resize(table, lens, new, torch.arange(1900, **i32), state, 16, new, after, slots=slots)
+        assert new.tolist() == [n] and lens.tolist() == [0] and after.tolist() == [-(-n // 16), 1900 - -(-n // 16)]
+        K.kda_page_resize(table, lens, new, torch.arange(1900, **i32), state, 16, torch.empty_like(new), state, slots=slots)
+        assert state.tolist() == after.tolist()
 
 
 def test_pages_ring_wraps():
