@@ -15,9 +15,9 @@
 // in the workspace as (m, l, o). The sums run in a fixed order.
 //
 // One launch does both kinds of work: each CTA counts the steps and the rest's tiles, and the CTAs are dealt to the two so
-// that both end together. As two launches, one after the other, 25 shapes of 2 to 512 rows took 1.15 times as long (32
-// rows in 4 groups of 2048 to 8192 shared tokens 53.0 and now 45.1 us, 128 rows behind 32768 169.5 and 167.8; the other
-// way 512 rows in 16 groups: 290 and 302, since a step takes longer while the rest is streamed).
+// that both end together. As two launches, one after the other, 25 shapes of 2 to 512 rows took 1.22 times as long (32
+// rows in 4 groups of 2048 to 8192 shared tokens 53.0 and now 43.6 us, 512 rows in 16 groups 290 and 284, 128 rows behind
+// 32768 169.5 and 158).
 //
 // Roles: eight warps in two groups for the softmax (a thread a query row, 64 scores at a time in its registers), one that
 // loads keys by TMA into a ring of three tiles and one that loads values into a ring of two, a box for each page (or 128
@@ -26,14 +26,14 @@
 // of each, which averages out over a prefix; their sum is formed from the unrounded ones) and are the A operand
 // of P V from there. O is scaled down only when a row's maximum has grown by more than 2^8 since it was last fixed.
 //
-// What bounds it. 128 rows of 64 heads behind 32768 tokens: 1.4e11 operations and 408 MB in 168 us, 830 TFLOP/s. A step has
+// What bounds it. 128 rows of 64 heads behind 32768 tokens: 1.4e11 operations and 408 MB in 158 us, 885 TFLOP/s. A step has
 // 16.8 MFLOP (1.33 us of an SM's products at the library's rate) and 32768 exponentials (0.54 us), and takes 1.8 to 2.0 us,
 // from L2 or HBM: the warps that issue products wait for the tensor core most of the time, which reads 320 KB of shared
 // memory a step (1.3 us at 128 bytes a clock), since scores in half tiles read the queries twice. Scores by whole tiles
-// read 256 KB, but then a group's softmax waits for them: 32 rows in 4 groups 44.8 and so 44.2 us, 512 rows 301 and 294, 128 rows 168 and
-// 179, the geometric mean of 25 shapes the same. With two tiles of tokens for at most 128 query rows a step takes 1.7 us
+// read 256 KB, but then a group's softmax waits for them: 128 rows 168 and so 179 us, 512 rows 301 and 294, 32 rows in 4 groups
+// 44.8 and 44.2, the geometric mean of 25 shapes the same. With two tiles of tokens for at most 128 query rows a step takes 1.7 us
 // from L2 and 2.9 from HBM, 6.7 TB/s.
-// 512 rows in 16 groups, 1.22 GB: 302 us, 4.0 TB/s; the rest's stream is 230 ns of an SM for a tile of 16 tokens with the
+// 512 rows in 16 groups, 1.22 GB: 284 us, 4.3 TB/s; the rest's stream is about 200 ns of an SM for a tile of 16 tokens with the
 // beginnings of its short rows, and the prefixes' steps 2.9 us.
 //
 // Tokens of missing pages: their scores are masked, and their rows of the tiles cleared, since a probability of zero
@@ -61,12 +61,12 @@ constexpr int kLive = 8;  // masks kept (more tiles than the loads can be ahead 
 constexpr float kNegInf = -INFINITY;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kSlack = 8.0f;  // log2: how far a maximum may grow before O is scaled
-// What the work takes of an SM, in ns, by which the CTAs are dealt to its two kinds: a step of a prefix (the second: when
-// there are more items than CTAs for them, so that pairs of the same tokens are not read at the same time), the
-// beginning and end of an item, a tile of 16 tokens of the rest. Only their ratios count. Over 25 shapes: geometric mean
-// 0.869 of two launches' time, without the second kind of step 0.865 but 336 instead of 302 us for 512 rows in 16
-// groups (of 34, 38, 42 and 46 CTAs for its prefixes: 328, 303, 304 and 313); with 0, 4000 and 3000 ns an item 0.898, 0.889 and 0.865.
-constexpr float kStepNs = 1600.0f, kColdStepNs = 2100.0f, kItemNs = 3000.0f, kTileNs = 180.0f;
+// What the work takes of an SM, in ns, by which the CTAs are dealt to its two kinds: a step of a prefix whose tokens several
+// pairs of tiles of query rows read at the same time, or one alone (that of one pair, or any when there are more items than
+// CTAs for them), the beginning and end of an item, a tile of 16 tokens of the rest. Only their ratios count. Over 25 shapes
+// the geometric mean is 0.821 of two launches' time; with one kind of step 0.831 (512 rows in 16 groups 296 instead of 284 us);
+// with 2000 or 2600 for the dearer one 0.822 (298, 290), with 4000 an item 0.821, with 180 a tile 0.846.
+constexpr float kStepNs = 1600.0f, kColdStepNs = 2300.0f, kItemNs = 3000.0f, kTileNs = 160.0f;
 constexpr int32_t kLeastRows = 2;  // of a group, for its prefix to be shared
 
 constexpr uint32_t kTmemCols = 512;  // all: the base is column 0
@@ -84,7 +84,7 @@ struct Bars {
     uint32_t live[kLive];  // of a tile of keys: a bit for eight tokens
     int64_t sums[kThreads / 32];
     uint32_t tiles[kThreads / 32];
-    float items[kThreads / 32];
+    float2 cost[kThreads / 32];
     int32_t group, offset;  // where the CTA's share begins: its first group, and the place in that
     uint32_t tmem;
     int32_t abort;
@@ -466,7 +466,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool bad = false;
     Walk w;
     w.g.row0 = w.g.rows = w.g.tiles = w.g.tokens = 0;
-    auto group_steps = [&](int g, Group &x, float &items) {
+    auto group_steps = [&](int g, Group &x, float2 &cost) {
         x.row0 = x.rows = x.tiles = x.tokens = 0;
         if (g >= a.groups) return (int64_t)0;
         const int lo = a.cu_groups[g], hi = a.cu_groups[g + 1], n = a.prefix_lens[g];
@@ -475,7 +475,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         bad |= wrong;
         if (!wrong) x = group_of(a, lo, hi, n);
         const int64_t steps = (int64_t)c.num_kv_heads * head_steps(a, x);
-        if (x.tiles > 0) items += (float)(c.num_kv_heads * ((query_rows(a, x) + kPrefixSlots - 1) / kPrefixSlots));
+        if (x.tiles > 0) {
+            const int pairs = (query_rows(a, x) + kPrefixSlots - 1) / kPrefixSlots;
+            const float items = (float)(c.num_kv_heads * pairs);
+            cost.x += (float)steps * (pairs > 1 ? kStepNs : kColdStepNs) + items * kItemNs, cost.y += items;
+        }
         return steps;
     };
     auto scan = [&](int64_t x) {  // inclusive, over the warp
@@ -486,15 +490,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         return x;
     };
-    auto warp_sum = [](float x) {
+    auto warp_sum = [](float2 x) {
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+        for (int o = 16; o > 0; o >>= 1) x.x += __shfl_xor_sync(0xffffffffu, x.x, o), x.y += __shfl_xor_sync(0xffffffffu, x.y, o);
         return x;
     };
     int64_t all;
     int per = 1, offset = 0;  // the length of a share; this one's place in its first group
     int ctas = 0;             // of the prefixes; the others stream what is left of the rows
-    auto share = [&](float items) {
+    auto share = [&](float2 cost) {
         bad |= all > 0x3fffffff;  // (tables that repeat their pages very often: places are 32-bit numbers below)
         const int total = bad ? 0 : (int)all;
         const GroupStarts starts = {a, bad};
@@ -509,12 +513,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         tiles = __reduce_add_sync(0xffffffffu, lane < kThreads / 32 ? B->tiles[lane] : 0);
         // both kinds of work end together, by what a step and a tile take of an SM
         const float rest_ns = (float)tiles * (float)(c.num_kv_heads * rest.q_tiles) * kTileNs;
-        auto deal = [&](float step_ns) {
-            const float ns = (float)total * step_ns + items * kItemNs;
+        auto deal = [&](float ns) {
             return total == 0 ? 0 : min(max((int)((float)gridDim.x * (ns / (ns + rest_ns)) + 0.5f), 1), (int)gridDim.x - 1);
         };
-        ctas = deal(kStepNs);
-        if (items > (float)ctas) ctas = deal(kColdStepNs);
+        ctas = deal(cost.x);
+        if (cost.y > (float)ctas) ctas = deal((float)total * kColdStepNs + cost.y * kItemNs);
         per = max((total + ctas - 1) / max(ctas, 1), 1);
         ctas = (total + per - 1) / per;  // (the last ones' shares would be empty)
         w.first = min(cta * per, total);
@@ -522,11 +525,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     if (a.groups <= 32) {  // each warp by itself
         Group x;
-        float items = 0.0f;
-        const int64_t mine = group_steps(lane, x, items), sum = scan(mine);
+        float2 cost = make_float2(0.0f, 0.0f);
+        const int64_t mine = group_steps(lane, x, cost), sum = scan(mine);
         all = __shfl_sync(0xffffffffu, sum, 31);
         bad = __any_sync(0xffffffffu, bad);
-        share(warp_sum(items));
+        share(warp_sum(cost));
         const int64_t off = w.first - (sum - mine);
         const uint32_t here = __ballot_sync(0xffffffffu, w.left > 0 && off >= 0 && off < mine);
         w.index = here ? __ffs(here) - 1 : 0;
@@ -546,13 +549,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             return sum + before;
         };
         int64_t mine = 0;
-        float items = 0.0f, unused = 0.0f;
-        for (int g = threadIdx.x; g < a.groups; g += kThreads) mine += group_steps(g, x, items);
-        items = warp_sum(items);
-        if (lane == 0) B->items[warp] = items;
+        float2 cost = make_float2(0.0f, 0.0f), unused = cost;
+        for (int g = threadIdx.x; g < a.groups; g += kThreads) mine += group_steps(g, x, cost);
+        cost = warp_sum(cost);
+        if (lane == 0) B->cost[warp] = cost;
         bad = __syncthreads_or(bad);  // then nothing is taken as shared: the rows' own tables hold all of their tokens
         block_scan(mine, all);
-        share(warp_sum(lane < kThreads / 32 ? B->items[lane] : 0.0f));
+        share(warp_sum(lane < kThreads / 32 ? B->cost[lane] : make_float2(0.0f, 0.0f)));
         int64_t before = 0;
         for (int g0 = 0; w.left > 0 && g0 < a.groups; g0 += kThreads) {
             int64_t total;

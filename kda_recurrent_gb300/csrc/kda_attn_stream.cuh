@@ -351,17 +351,21 @@ __device__ __forceinline__ void walk_share(const Args &a, int cta, int ctas, uin
             uint32_t bits = left >= kTokens ? 0xffffu : (1u << left) - 1;
             if (pages.x < 0) bits &= 0xff00u;
             if (pages.y < 0) bits &= 0x00ffu;
-            const uint32_t dst = ring_addr + stage * kStageBytes;
+            const uint32_t dst = ring_addr + stage * kStageBytes + half_row * 256;
+            // two pages' places of the tile's tokens (of this lane's first row and piece), eight tokens from each
+            size_t at_k[2], at_v[2];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int r = 2 * i + half_row;
-                const int page = i < 4 ? pages.x : pages.y;
-                const bool on = (bits >> r) & 1;
-                const size_t row = ((size_t)h * c.page_size + ((first + r) & mask)) * kHeadDim + chunk * 8;
-                const size_t k_off = on ? (size_t)page * c.k_page_stride + row : 0;
-                const size_t v_off = on ? (size_t)page * c.v_page_stride + row : 0;
-                cp_async_16(dst + r * 256 + ((chunk ^ ((r & 1) << 2)) << 4), c.k + k_off, on ? 16u : 0u);
-                cp_async_16(dst + kStageBytes / 2 + r * 256 + ((chunk ^ (((r >> 1) & 3) << 1)) << 4), c.v + v_off, on ? 16u : 0u);
+            for (int e = 0; e < 2; ++e) {
+                const int page = e == 0 ? pages.x : pages.y;
+                const size_t row = ((size_t)h * c.page_size + ((first + 8 * e) & mask) + half_row) * kHeadDim + chunk * 8;
+                at_k[e] = page < 0 ? 0 : (size_t)page * c.k_page_stride + row, at_v[e] = page < 0 ? 0 : (size_t)page * c.v_page_stride + row;
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {  // (a row that is off lies in the cache, too, but is not read)
+                const uint32_t bytes = (bits >> (2 * i + half_row)) & 1 ? 16u : 0u;
+                const size_t off = 2 * (i & 3) * kHeadDim;
+                cp_async_16(dst + i * 512 + ((chunk ^ (half_row << 2)) << 4), c.k + at_k[i >> 2] + off, bytes);
+                cp_async_16(dst + kStageBytes / 2 + i * 512 + ((chunk ^ ((i & 3) << 1)) << 4), c.v + at_v[i >> 2] + off, bytes);
             }
             if (lane == 0) live[stage] = bits;
             if (--to_load > 0) {
@@ -421,8 +425,7 @@ __device__ __forceinline__ void walk_share(const Args &a, int cta, int ctas, uin
         float m[2] = {kNegInf, kNegInf}, l[2] = {0.0f, 0.0f};
         const int tiles = (int)min((U)(at.tiles - at.tile), left);
         for (int i = 0; i < tiles; ++i, ++at.tile) {
-            fetch(stage == 0 ? kStages - 1 : stage - 1);
-            cp_async_wait<kStages - 1>();
+            cp_async_wait<kStages - 2>();
             __syncwarp();
             const uint8_t *const ks = ring + stage * kStageBytes, *const vs = ks + kStageBytes / 2;
             const uint32_t bits = live[stage];
@@ -479,6 +482,10 @@ __device__ __forceinline__ void walk_share(const Args &a, int cta, int ctas, uin
             }
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
+                // the next tile is asked for here, between the products: with every other place, and with copies whose
+                // addresses are formed one by one, the rest of 128 rows takes longer (512 rows of 4096 tokens on 152 SMs 1227
+                // us, at the loop's beginning 1302, addresses one by one 1310; without a prefix 1217, 1294 and 1217)
+                if (half == 1) fetch(stage == 0 ? kStages - 1 : stage - 1);
                 uint4 v[4];  // rows 2t, 2t + 1, 2t + 8, 2t + 9
 #pragma unroll
                 for (int i2 = 0; i2 < 4; ++i2) {
