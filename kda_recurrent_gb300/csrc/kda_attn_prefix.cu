@@ -897,10 +897,11 @@ int64_t attn_prefix_workspace_bytes(int32_t batch, int32_t num_q_heads, int32_t 
 }
 
 // Where each row reads its own tokens alone anyway: no groups, or so few tokens in all rows' tables that reading them
-// row by row takes less than a launch more. Row by row and shared, in us: 4 rows of 2048 tokens on 8/8 heads (35 MB) 13.0
-// and 13.7; 16 of 512 on 64/8 (38 MB) 15.2 and 15.8; 6 of 2048 on 8/8 (52 MB) 15.8 and 13.9; 16 of 768 on 64/8 (55 MB)
-// 18.1 and 16.1; 8 of 2048 on 8/8 (69 MB) 17.5 and 14.4; 8 of 4096 on 32/8 (136 MB) 27.5 and 17.2; 64 of 2048 on 64/8 in two
-// groups (554 MB) 87 and 23. (With one key head, two rows and 32768 tokens it is 20.2 and 23.7.)
+// row by row takes less than a second launch with its parts. Row by row and shared, in us: 4 rows of 2048 tokens on 8/8
+// heads (35 MB) 12.4 and 13.5; 16 of 512 on 64/8 (38 MB) 14.7 and 14.8; 5 of 2048 on 8/8 (43 MB) 13.7 and 13.7; 6 (52 MB) 14.5
+// and 13.5; 16 of 768 on 64/8 (55 MB) 16.8 and 15.5; 8 of 2048 on 8/8 (69 MB) 16.3 and 13.8; 8 of 4096 on 32/8 (136 MB)
+// 24.6 and 15.8; 64 of 2048 on 64/8 in two groups (554 MB) 74 and 25.5. (With one key head, two rows and 32768 tokens it is
+// 19.3 and 22.3.)
 constexpr int64_t kFewBytes = 48LL << 20;
 
 cudaError_t launch_attn_prefix(const AttnPrefixArgs &args, cudaStream_t stream) {
