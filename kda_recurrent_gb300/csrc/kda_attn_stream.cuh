@@ -310,13 +310,13 @@ __device__ __forceinline__ void walk_share(const Args &a, int cta, int ctas, uin
             const size_t h0 = (size_t)b * p.num_q_heads;
             if constexpr (kTail) {
                 for (int i = threadIdx.x; i < p.num_q_heads; i += kThreads) a.x.tails[h0 + i] = kTailNone;
-                continue;
-            }
-            for (int i = threadIdx.x; i < p.num_q_heads * (kHeadDim / 8); i += kThreads)
-                reinterpret_cast<uint4 *>(p.out + h0 * kHeadDim)[i] = make_uint4(0, 0, 0, 0);
-            for (int i = threadIdx.x; i < p.num_q_heads; i += kThreads) {
-                if (p.lse) p.lse[h0 + i] = kNegInf;
-                a.ws.lse2[h0 + i] = kNegInf;
+            } else {
+                for (int i = threadIdx.x; i < p.num_q_heads * (kHeadDim / 8); i += kThreads)
+                    reinterpret_cast<uint4 *>(p.out + h0 * kHeadDim)[i] = make_uint4(0, 0, 0, 0);
+                for (int i = threadIdx.x; i < p.num_q_heads; i += kThreads) {
+                    if (p.lse) p.lse[h0 + i] = kNegInf;
+                    a.ws.lse2[h0 + i] = kNegInf;
+                }
             }
         }
     };
