@@ -322,3 +322,30 @@ def test_prefix_between_other_launches():
         K.kda_attn_prefix_decode(q2, c["k_cache"], c["v_cache"], c["block_table"], lens, groups, prefix, out, SCALE, ws)
         got = out + 0
         assert torch.equal(got, want)
+
+
+def test_prefix_on_two_streams_beside_prompts_on_a_third():
+    # kernels that all hold tensor memory, in flight together
+    a = widened(inputs([0, 20, 30], [1500, 700], [7 * i % 90 for i in range(30)], 2, 16, 23), 16)
+    b = widened(inputs([0, 8], [900], [30] * 8, 2, 64, 24), 8)
+    qa, qb = queries(30, 16, 23), queries(8, 8, 24)
+    want_a, want_b = call(qa, a), call(qb, b)
+    gen = torch.Generator().manual_seed(25)
+    q, k, v = (torch.randn(700, 4, 128, generator=gen).to(torch.bfloat16).to(DEV) for _ in range(3))
+    decay = -torch.rand(700, 4, generator=gen).to(DEV)
+    cu = torch.tensor([0, 300, 700], dtype=torch.int32, device=DEV)
+
+    def prompt(**kw):
+        return K.linear_prefill(q, k, v, decay, cu, scale=SCALE, **kw)
+
+    want_c = prompt()
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    got = []
+    for _ in range(6):
+        got.append((call(qa, a, stream=streams[0]), call(qb, b, stream=streams[1]), prompt(stream=streams[2])))
+    torch.cuda.synchronize()
+    assert K.kda_device_status()[0] == K.KDA_OK
+    for x, y, z in got:
+        assert all(torch.equal(g, w) for g, w in zip((*x, *y, *z), (*want_a, *want_b, *want_c)))
