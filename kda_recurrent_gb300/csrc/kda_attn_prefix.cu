@@ -341,9 +341,9 @@ __device__ __forceinline__ void load_tiles(const AttnPrefixArgs &a, Walk w, int 
             if (++slot == ring) slot = 0, ++turn;
         }
     }
-    if (!ok) {  // what was asked for has to arrive before the CTA leaves
-        for (uint32_t i = count > ring ? count - ring : 0; i < count; ++i) mbar_wait(&full[i % ring], (i / ring) & 1);
-    }
+    // What was asked for has to arrive before the CTA leaves, also where this warp has done all of its work and another
+    // one gives up. (Without that the products' warps wait for the same tiles anyway.)
+    for (uint32_t i = count > ring ? count - ring : 0; i < count; ++i) mbar_wait(&full[i % ring], (i / ring) & 1);
 }
 
 // The products of group g of warps, issued by one warp: S = Q K^T of a step behind O += P V of the one before. Both
