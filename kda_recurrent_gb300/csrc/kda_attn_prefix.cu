@@ -622,7 +622,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int i = 0; i < 16; ++i) {
                     const int from = __shfl_sync(0xffffffffu, valid ? head : -1, 2 * i + sub);
                     x[i] = make_uint4(0, 0, 0, 0);
-                    if (from >= 0) x[i] = __ldg(reinterpret_cast<const uint4 *>(p.q + (int64_t)from * kHeadDim) + chunk);
+                    if (from >= 0) x[i] = reinterpret_cast<const uint4 *>(p.q + (int64_t)from * kHeadDim)[chunk];
                 }
 #pragma unroll
                 for (int i = 0; i < 16; ++i)

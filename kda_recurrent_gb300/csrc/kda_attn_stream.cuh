@@ -142,7 +142,7 @@ __device__ __forceinline__ U warp_share(U tiles) {
 }
 
 __device__ __forceinline__ int page_at(const PagedCache &c, int b, int j, DeviceStatus *st) {
-    const int page = __ldg(c.block_table + (size_t)b * c.max_pages + (j >> c.page_shift));
+    const int page = c.block_table[(size_t)b * c.max_pages + (j >> c.page_shift)];
     if (page >= c.num_pages) {
         report_error(st, KDA_ERR_DEVICE_INPUT, b);
         return -1;
@@ -414,8 +414,8 @@ __device__ __forceinline__ void walk_share(const Args &a, int cta, int ctas, uin
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             uint4 x = make_uint4(0, 0, 0, 0), y = x;
-            if (g < rows) x = __ldg(reinterpret_cast<const uint4 *>(p.q + (head0 + g) * kHeadDim) + t + 4 * j);
-            if (g + 8 < rows) y = __ldg(reinterpret_cast<const uint4 *>(p.q + (head0 + g + 8) * kHeadDim) + t + 4 * j);
+            if (g < rows) x = reinterpret_cast<const uint4 *>(p.q + (head0 + g) * kHeadDim)[t + 4 * j];
+            if (g + 8 < rows) y = reinterpret_cast<const uint4 *>(p.q + (head0 + g + 8) * kHeadDim)[t + 4 * j];
             qa[2 * j][0] = x.x, qa[2 * j][1] = y.x, qa[2 * j][2] = x.y, qa[2 * j][3] = y.y;
             qa[2 * j + 1][0] = x.z, qa[2 * j + 1][1] = y.z, qa[2 * j + 1][2] = x.w, qa[2 * j + 1][3] = y.w;
         }

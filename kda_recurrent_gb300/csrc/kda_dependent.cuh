@@ -3,8 +3,10 @@
 // A kernel launched so may start while earlier work on its stream still runs. Every thread therefore passes
 // wait_for_prior before it touches global memory, the call's inputs included: only that wait makes visible
 // what was written before, by the launch before directly and, since that one waited too, by all earlier
-// ones. allow_next lets the next launch start at any time, which then waits in the same way. A launch's
-// latency and its kernel's set-up so lie behind the kernel before it.
+// ones. Such data is read by ordinary loads: a read-only load (__ldg) takes for granted that nothing wrote the data
+// since the kernel began, so that it may be moved before the wait. allow_next lets the next launch start at any
+// time, which then waits in the same way. A launch's latency and its kernel's set-up so lie behind the kernel
+// before it.
 #pragma once
 
 #include <cuda_runtime.h>

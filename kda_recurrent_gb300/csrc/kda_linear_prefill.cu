@@ -296,7 +296,7 @@ __device__ __forceinline__ void rank_sequences(const LinearPrefillArgs &a, int *
     }
 #pragma unroll 1
     for (int i = threadIdx.x; i < N; i += blockDim.x)  // wrapping difference: any input orders
-        scratch[i] = (int)((unsigned)__ldg(a.cu_seqlens + i + 1) - (unsigned)__ldg(a.cu_seqlens + i));
+        scratch[i] = (int)((unsigned)a.cu_seqlens[i + 1] - (unsigned)a.cu_seqlens[i]);
     __syncthreads();
 #pragma unroll 1
     for (int i = threadIdx.x; i < N; i += blockDim.x) {

@@ -64,7 +64,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) kda_qk_rope_kernel(const Args
         if (w) s_weight[which][c] = p.weight_bf16 ? __bfloat162float(static_cast<const __nv_bfloat16 *>(w)[c]) : static_cast<const float *>(w)[c];
     }
     if (kLayout != kNone && threadIdx.x < pairs) {
-        double turns = (double)__ldg(p.inv_freq + threadIdx.x) * 0.15915494309189533577;  // 1 / (2 pi)
+        double turns = (double)p.inv_freq[threadIdx.x] * 0.15915494309189533577;  // 1 / (2 pi)
         turns -= floor(turns);
         s_turn[threadIdx.x] = turns < 1.0 ? (uint64_t)(turns * 18446744073709551616.0) : 0;
     }
@@ -94,8 +94,8 @@ __global__ void __launch_bounds__(kThreads, kCtas) kda_qk_rope_kernel(const Args
     int64_t t = first, slot_ahead = -1;
     int h0 = part * kHeads, pos_ahead = 0;
     auto place = [&](int64_t t) {
-        if (p.slots) slot_ahead = __ldg(p.slots + t);
-        if (kLayout != kNone) pos_ahead = __ldg(p.positions + t);
+        if (p.slots) slot_ahead = p.slots[t];
+        if (kLayout != kNone) pos_ahead = p.positions[t];
     };
     const bool idle = h0 >= a.heads || t >= p.tokens;
     if (!idle) {
