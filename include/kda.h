@@ -439,9 +439,10 @@ KDA_API int64_t kda_attn_prefix_decode_workspace_size(int32_t batch, int32_t num
  * with slot -1), and is recorded as KDA_ERR_DEVICE_INPUT. Also recorded: a length outside
  * [0, max_pages * page_size] (clamped), a state or a page outside its range (taken as an empty
  * ring, and as missing), new tokens past max_tokens (left out of the maps), a page given back
- * when the ring is full. Missing pages (negative entries) are not given back. A page that
- * several rows share is given back by each row that shrinks below it: shrink all but one of them
- * no further than what they share. 1 <= num_pages < 2^30.
+ * when the ring is full. Missing pages (negative entries) are not given back. Every page of a row
+ * counts as its own here: one that several rows share would be given back by each row that shrinks
+ * below it, and handed out again while others read it. Rows that share pages are resized by
+ * kda_page_resize_ex. 1 <= num_pages < 2^30.
  */
 KDA_API int kda_page_resize(int32_t *block_table, const int32_t *seq_lens, const int32_t *new_lens,
                             int32_t *out_lens, int32_t *free_pages, const int32_t *free_state,
@@ -449,6 +450,25 @@ KDA_API int kda_page_resize(int32_t *block_table, const int32_t *seq_lens, const
                             int32_t max_pages, int32_t *cu_tokens, int64_t *slots,
                             int32_t *positions, int32_t *rows, int32_t max_tokens,
                             kda_stream_t stream);
+
+/*
+ * kda_page_resize_ex -- kda_page_resize for rows of which some share pages (those of a common
+ * prefix, say).
+ *   shared_pages int32 [batch], device, or NULL: the first shared_pages[b] entries of row b's table
+ *                are pages that the row reads and does not own. It never gives them back, to whatever
+ *                length it shrinks: a request that ends goes to length 0 like any other. Whoever owns
+ *                them (a row of the batch with 0 here, or the server) gives them back when the last
+ *                reader has ended. A value outside [0, max_pages] is clamped and recorded as
+ *                KDA_ERR_DEVICE_INPUT. out_lens may equal this, too.
+ * A row that shrank below its shared pages takes pages of its own when it grows again, in their
+ * place in its table: its number here has to go down with it.
+ */
+KDA_API int kda_page_resize_ex(int32_t *block_table, const int32_t *seq_lens, const int32_t *new_lens,
+                               const int32_t *shared_pages, int32_t *out_lens, int32_t *free_pages,
+                               const int32_t *free_state, int32_t *out_state, int32_t num_pages,
+                               int32_t page_size, int32_t batch, int32_t max_pages, int32_t *cu_tokens,
+                               int64_t *slots, int32_t *positions, int32_t *rows, int32_t max_tokens,
+                               kda_stream_t stream);
 
 /*
  * kda_qk_norm_rope -- queries and keys normed and rotated, keys and values written to the cache:

@@ -24,7 +24,8 @@ attention over a paged key-value cache):
     kda_attn_prefix_decode(q, k_cache, v_cache, block_table, seq_lens, cu_groups, prefix_lens, out,
                            scale, workspace, lse=None, stream=None)
     kda_page_resize(block_table, seq_lens, new_lens, free_pages, free_state, page_size, out_lens,
-                    out_state, cu_tokens=None, slots=None, positions=None, rows=None, stream=None)
+                    out_state, cu_tokens=None, slots=None, positions=None, rows=None, stream=None,
+                    *, shared_pages=None)
     kda_qk_norm_rope(q, k, positions, inv_freq, q_out, k_out, eps=1e-6, q_weight=None,
                      k_weight=None, magnitude=1.0, interleaved=False, v=None, k_cache=None,
                      v_cache=None, slots=None, stream=None)
@@ -58,7 +59,7 @@ CHUNK = 32
 EXPORTED_SYMBOLS = ("kda_prefill", "kda_prefill_ex", "kda_prefill_workspace_size", "kda_prefill_noalloc", "kda_decode",
                     "kda_decode_ex", "kda_linear_prefill", "kda_linear_prefill_workspace_size", "kda_linear_decode",
                     "kda_attn_decode", "kda_attn_decode_workspace_size", "kda_cache_evict", "kda_attn_prefix_decode", "kda_attn_prefix_decode_workspace_size",
-                    "kda_page_resize", "kda_qk_norm_rope", "kda_status_string",
+                    "kda_page_resize", "kda_page_resize_ex", "kda_qk_norm_rope", "kda_status_string",
                     "kda_device_status", "kda_abi_version")
 KDA_NOALLOC_SCRATCH_BYTES = 32 << 20  # fixed scratch array of kda_prefill_noalloc
 KDA_DECODE_L2NORM_QK = 1
@@ -132,6 +133,8 @@ def bind(lib):
     lib.kda_attn_prefix_decode_workspace_size.argtypes = [i32, i32, i32, i32, i32, i32, i32]
     lib.kda_page_resize.restype = ctypes.c_int
     lib.kda_page_resize.argtypes = [vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, vp, vp, vp, vp, i32, vp]
+    lib.kda_page_resize_ex.restype = ctypes.c_int
+    lib.kda_page_resize_ex.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, vp, vp, vp, vp, i32, vp]
     lib.kda_qk_norm_rope.restype = ctypes.c_int
     lib.kda_qk_norm_rope.argtypes = [vp, vp, vp, i64, i64, i64, vp, vp, i32, i32, f32, vp, vp, i32, f32, vp, i64, vp, i64,
                                      vp, vp, i64, i64, i64, i32, vp, i32, i32, i32, vp]
@@ -517,7 +520,7 @@ def attn_prefix_decode_workspace(batch, num_q_heads, num_kv_heads, max_pages, pa
 
 
 def kda_page_resize(block_table, seq_lens, new_lens, free_pages, free_state, page_size, out_lens, out_state,
-                    cu_tokens=None, slots=None, positions=None, rows=None, stream=None):
+                    cu_tokens=None, slots=None, positions=None, rows=None, stream=None, *, shared_pages=None):
     """Takes pages for rows of a paged cache that grow from ``seq_lens`` to ``new_lens`` tokens, gives
     back those of rows that shrink, and maps the new tokens, packed row after row, to cache slots.
     ``block_table`` int32 [B, max_pages] is written where pages are taken; ``free_pages`` int32
@@ -525,9 +528,11 @@ def kda_page_resize(block_table, seq_lens, new_lens, free_pages, free_state, pag
     and ``out_state`` are the lengths and the state after the call (may be the tensors before it).
     Optional: ``cu_tokens`` int32 [B + 1], and for each token ``slots`` int64, ``positions`` and
     ``rows`` int32, all of one length, -1 / 0 / -1 past the last token. A row for which too few
-    pages are free keeps its length (see include/kda.h)."""
+    pages are free keeps its length (see include/kda.h). ``shared_pages`` int32 [B]: the first
+    entries of each row's table that are not its own, and are never given back by it; without it
+    every page is given back by each row that shrinks below it, also one that other rows still read."""
     st = (_native or _load_native()).page_resize(block_table, seq_lens, new_lens, free_pages, free_state, page_size,
-                                                 out_lens, out_state, cu_tokens, slots, positions, rows, stream)
+                                                 out_lens, out_state, cu_tokens, slots, positions, rows, stream, shared_pages)
     if st != KDA_OK:
         raise KdaError(st, "kda_page_resize")
 
@@ -622,7 +627,7 @@ def attn_prefix_decode(q, k_cache, v_cache, block_table, seq_lens, cu_groups, pr
     return (out, lse) if want_lse else out
 
 
-def page_resize(block_table, seq_lens, new_lens, free_pages, free_state, page_size, *, max_tokens, stream=None):
+def page_resize(block_table, seq_lens, new_lens, free_pages, free_state, page_size, *, max_tokens, shared_pages=None, stream=None):
     """Runs ``kda_page_resize`` in place (``seq_lens`` and ``free_state`` become those after the call) and
     allocates its maps for ``max_tokens`` new tokens; returns (cu_tokens, slots, positions, rows)."""
     import torch
@@ -632,7 +637,7 @@ def page_resize(block_table, seq_lens, new_lens, free_pages, free_state, page_si
         slots = torch.empty(max_tokens, dtype=torch.int64, device=dev)
         positions, rows = (torch.empty(max_tokens, dtype=torch.int32, device=dev) for _ in range(2))
     kda_page_resize(block_table, seq_lens, new_lens, free_pages, free_state, page_size, seq_lens, free_state, cu, slots,
-                    positions, rows, stream)
+                    positions, rows, stream, shared_pages=shared_pages)
     return cu, slots, positions, rows
 
 

@@ -305,7 +305,7 @@ PyObject *attn_prefix_decode(PyObject *const *a) {
 }
 
 // (block_table, seq_lens, new_lens, free_pages, free_state, page_size, out_lens, out_state, cu_tokens, slots, positions, rows,
-//  stream)
+//  stream, shared_pages)
 PyObject *page_resize(PyObject *const *a) {
     const at::Device device = tensor(a[0], "block_table", 2).device();
     const at::Tensor &table = need(a[0], "block_table", at::kInt, {-1, -1}, device);
@@ -317,6 +317,7 @@ PyObject *page_resize(PyObject *const *a) {
     const at::Tensor &out_lens = need(a[6], "out_lens", at::kInt, {B}, device);
     const at::Tensor &out_state = need(a[7], "out_state", at::kInt, {2}, device);
     int32_t *const cu = optional<int32_t>(a[8], "cu_tokens", at::kInt, {B + 1}, device);
+    const int32_t *const shared = optional<int32_t>(a[13], "shared_pages", at::kInt, {B}, device);
     int64_t tokens = -1;  // of the maps that are given
     const char *const names[] = {"slots", "positions", "rows"};
     void *maps[3];
@@ -327,10 +328,10 @@ PyObject *page_resize(PyObject *const *a) {
     const int32_t size = int_of(a[5], "page_size"), b = int_of(B, "block_table"), width = int_of(table.size(1), "block_table"),
                   pages = int_of(ring.size(0), "free_pages"), t = tokens < 0 ? 0 : int_of(tokens, "slots");
     return run(device, a[12], [&](kda_stream_t stream) {
-        return kda_page_resize(address<int32_t>(table), address<int32_t>(lens), address<int32_t>(new_lens), address<int32_t>(out_lens),
-                               address<int32_t>(ring), address<int32_t>(state), address<int32_t>(out_state), pages, size, b, width, cu,
-                               static_cast<int64_t *>(maps[0]), static_cast<int32_t *>(maps[1]), static_cast<int32_t *>(maps[2]), t,
-                               stream);
+        return kda_page_resize_ex(address<int32_t>(table), address<int32_t>(lens), address<int32_t>(new_lens), shared,
+                                  address<int32_t>(out_lens), address<int32_t>(ring), address<int32_t>(state),
+                                  address<int32_t>(out_state), pages, size, b, width, cu, static_cast<int64_t *>(maps[0]),
+                                  static_cast<int32_t *>(maps[1]), static_cast<int32_t *>(maps[2]), t, stream);
     });
 }
 
@@ -419,7 +420,7 @@ PyMethodDef method(const char *name) {
 
 PyMethodDef methods[] = {method<linear_prefill, 11>("linear_prefill"), method<linear_decode, 9>("linear_decode"),
                          method<attn_decode, 11>("attn_decode"), method<cache_evict, 13>("cache_evict"),
-                         method<attn_prefix_decode, 12>("attn_prefix_decode"), method<page_resize, 13>("page_resize"), method<qk_norm_rope, 16>("qk_norm_rope"),
+                         method<attn_prefix_decode, 12>("attn_prefix_decode"), method<page_resize, 14>("page_resize"), method<qk_norm_rope, 16>("qk_norm_rope"),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "kda_gb300_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

@@ -297,13 +297,21 @@ int kda_page_resize(int32_t *block_table, const int32_t *seq_lens, const int32_t
                     int32_t *free_pages, const int32_t *free_state, int32_t *out_state, int32_t num_pages,
                     int32_t page_size, int32_t batch, int32_t max_pages, int32_t *cu_tokens, int64_t *slots,
                     int32_t *positions, int32_t *rows, int32_t max_tokens, kda_stream_t stream) {
+    return kda_page_resize_ex(block_table, seq_lens, new_lens, nullptr, out_lens, free_pages, free_state, out_state, num_pages,
+                              page_size, batch, max_pages, cu_tokens, slots, positions, rows, max_tokens, stream);
+}
+
+int kda_page_resize_ex(int32_t *block_table, const int32_t *seq_lens, const int32_t *new_lens, const int32_t *shared_pages,
+                       int32_t *out_lens, int32_t *free_pages, const int32_t *free_state, int32_t *out_state,
+                       int32_t num_pages, int32_t page_size, int32_t batch, int32_t max_pages, int32_t *cu_tokens,
+                       int64_t *slots, int32_t *positions, int32_t *rows, int32_t max_tokens, kda_stream_t stream) {
     if (num_pages < 1 || max_tokens < 0) return KDA_ERR_INVALID_ARG;
     const int bad = cache_shape(batch, 1, max_pages, page_size);
     if (bad != KDA_OK) return bad;
     if (num_pages > 0x3fffffff) return KDA_ERR_UNSUPPORTED;
     if (!free_pages || !free_state || !out_state) return KDA_ERR_INVALID_ARG;
     if (batch > 0 && (!block_table || !seq_lens || !new_lens || !out_lens)) return KDA_ERR_INVALID_ARG;
-    const void *p4[] = {block_table, seq_lens, new_lens, out_lens, free_pages, free_state, out_state, cu_tokens, positions, rows};
+    const void *p4[] = {block_table, seq_lens, new_lens, shared_pages, out_lens, free_pages, free_state, out_state, cu_tokens, positions, rows};
     for (const void *p : p4)
         if (!aligned(p, 4)) return KDA_ERR_MISALIGNED;
     if (!aligned(slots, 8)) return KDA_ERR_MISALIGNED;
@@ -311,6 +319,7 @@ int kda_page_resize(int32_t *block_table, const int32_t *seq_lens, const int32_t
     a.block_table = block_table;
     a.seq_lens = seq_lens;
     a.new_lens = new_lens;
+    a.shared_pages = shared_pages;
     a.out_lens = out_lens;
     a.free_pages = free_pages;
     a.free_state = free_state;

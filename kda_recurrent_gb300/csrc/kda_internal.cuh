@@ -175,6 +175,7 @@ struct QkRopeArgs {
 struct PageResizeArgs {
     int32_t *block_table;
     const int32_t *seq_lens, *new_lens;
+    const int32_t *shared_pages;  // NULL: every page of a row is its own
     int32_t *out_lens, *free_pages;
     const int32_t *free_state;
     int32_t *out_state;

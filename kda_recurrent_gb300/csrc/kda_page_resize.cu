@@ -3,7 +3,7 @@
 //
 // A row of n tokens holds ceil(n / page_size) pages. Free pages lie in a ring [first, first + count); rows that
 // grow take from its front, in row order, rows that shrink give back to its end, so that what a call takes and
-// what it gives never meet. Where each row's pages and tokens begin follows from prefix sums over the rows, which
+// what it gives never meet. The pages that a row shares with others, the first ones of its table, it does not give back. Where each row's pages and tokens begin follows from prefix sums over the rows, which
 // every CTA forms by itself, 1024 rows at a time (8 bytes a row); tokens and pages find their row in the sums by
 // bisection. Nothing here is wide: it is a chain of dependent reads (lengths, sums, table or ring, map), and the
 // launch is most of a small call.
@@ -70,6 +70,7 @@ template <bool kMaps, bool kState, int kQuad, bool kWide>
 __global__ void __launch_bounds__(kMaxThreads, 1) kda_page_resize_kernel(const PageResizeArgs p) {
     __shared__ uint32_t s_tok[kMaxThreads], s_take[kMaxThreads], s_give[kMaxThreads];  // inclusive sums of a chunk's rows
     __shared__ int32_t s_old[kMaxThreads], s_new[kMaxThreads];
+    __shared__ uint32_t s_keep[kMaxThreads];  // pages from the table's beginning on that the row does not give back
     __shared__ uint32_t s_warp[3][32];
     __shared__ uint32_t s_given[2][kMaxCluster];
     __shared__ uint32_t s_used;  // pages really taken
@@ -116,7 +117,16 @@ __global__ void __launch_bounds__(kMaxThreads, 1) kda_page_resize_kernel(const P
             }
         }
         const uint32_t held = pages(n), want = pages(m);
-        uint32_t x[3] = {m > n ? (uint32_t)(m - n) : 0u, want > held ? want - held : 0u, held > want ? held - want : 0u};
+        uint32_t keep = want;
+        if (p.shared_pages && (int)threadIdx.x < rows) {
+            int shared = p.shared_pages[r];
+            if (shared < 0 || shared > p.max_pages) {
+                if (kMaps && rank == 0) report_error(p.status, KDA_ERR_DEVICE_INPUT, r);
+                shared = min(max(shared, 0), p.max_pages);
+            }
+            keep = max(want, (uint32_t)shared);
+        }
+        uint32_t x[3] = {m > n ? (uint32_t)(m - n) : 0u, want > held ? want - held : 0u, held > keep ? held - keep : 0u};
         const uint32_t my_tokens = x[0], my_take = x[1];
 #pragma unroll
         for (int i = 0; i < 3; ++i) {
@@ -142,7 +152,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1) kda_page_resize_kernel(const P
             if (warp > 0) x[i] = add(x[i], before);
         }
         s_tok[threadIdx.x] = x[0], s_take[threadIdx.x] = x[1], s_give[threadIdx.x] = x[2];
-        s_old[threadIdx.x] = n, s_new[threadIdx.x] = m;
+        s_old[threadIdx.x] = n, s_new[threadIdx.x] = m, s_keep[threadIdx.x] = keep;
         // in order: the first row whose pages are not there, and all later ones that need pages, get none
         const bool served = my_take == 0 || add(taken, x[1]) <= (uint32_t)count;
         const uint32_t left = (uint32_t)count - min(taken, (uint32_t)count);
@@ -221,7 +231,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1) kda_page_resize_kernel(const P
                     while (s_give[at_row] <= i) ++at_row;
                     row[e] = at_row;
                     const uint32_t before = at_row > 0 ? s_give[at_row - 1] : 0;
-                    page[e] = p.block_table[(size_t)(r0 + at_row) * p.max_pages + pages(s_new[at_row]) + (i - before)];
+                    page[e] = p.block_table[(size_t)(r0 + at_row) * p.max_pages + s_keep[at_row] + (i - before)];
                 }
             }
 #pragma unroll
@@ -309,7 +319,8 @@ bool apart(const int32_t *out, const int32_t *in, int64_t n) {
 }  // namespace
 
 cudaError_t launch_page_resize(const PageResizeArgs &p, cudaStream_t stream) {
-    const bool others = apart(p.out_lens, p.seq_lens, p.batch) && apart(p.out_lens, p.new_lens, p.batch) && apart(p.out_state, p.free_state, 2);
+    const bool others = apart(p.out_lens, p.seq_lens, p.batch) && apart(p.out_lens, p.new_lens, p.batch) &&
+                        (!p.shared_pages || apart(p.out_lens, p.shared_pages, p.batch)) && apart(p.out_state, p.free_state, 2);
     if ((int64_t)p.batch * p.max_pages <= (others ? kOnePages : kOnePagesInPlace) && p.max_tokens <= (others ? kOneTokens : kOneTokensInPlace)) {
         const unsigned threads = p.batch <= 256 && p.max_tokens <= 1024 ? 256 : kMaxThreads;
         return launch_dependent(kda_page_resize_kernel<true, true, 1, false>, dim3(1), threads, 0, stream, p);
