@@ -664,8 +664,9 @@ def rope_frequencies(rot_dim, base=10000.0, factor=1.0, original_length=0, slow_
     import torch
     if rot_dim < 0 or rot_dim > HEAD_DIM or rot_dim % 16 != 0:
         raise ValueError(f"rot_dim: expected a multiple of 16 in [0, {HEAD_DIM}], got {rot_dim}")
-    if not (factor >= 1.0 and base > 0.0 and slow_turns < fast_turns):
-        raise ValueError("expected factor >= 1, base > 0 and slow_turns < fast_turns")
+    if not (factor >= 1.0 and base > 0.0 and original_length >= 0 and slow_turns < fast_turns
+            and all(map(math.isfinite, (factor, base, original_length, slow_turns, fast_turns)))):
+        raise ValueError("expected finite factor >= 1, base > 0, original_length >= 0 and slow_turns < fast_turns")
     f = base ** (-torch.arange(0, rot_dim, 2, dtype=torch.float64) / max(rot_dim, 1))
     magnitude = 1.0
     if original_length:
@@ -674,4 +675,7 @@ def rope_frequencies(rot_dim, base=10000.0, factor=1.0, original_length=0, slow_
         magnitude += 0.1 * math.log(factor)
     else:
         f = f / factor
-    return f.to(torch.float32).to(device), magnitude
+    f = f.to(torch.float32)
+    if not torch.isfinite(f).all():
+        raise ValueError(f"base: {base} gives frequencies that are not finite")
+    return f.to(device), magnitude
