@@ -391,12 +391,16 @@ KDA_API int kda_cache_evict(void *k_cache, void *v_cache, int64_t k_page_stride,
  *                tokens, say) stands for itself.
  *   workspace    at least kda_attn_prefix_decode_workspace_size(...) bytes, 16-byte aligned.
  *                Contents on entry do not matter; calls sharing one must not overlap.
- *   All other arguments as for kda_attn_decode.
+ *   All other arguments as for kda_attn_decode. There is no `weight`: rows that are to be cut by
+ *   kda_cache_evict attend by kda_attn_decode, which accumulates it.
  * Whole tiles of 128 shared tokens of a group of two rows or more are computed together, with
- * probabilities rounded to BF16 (and their sum formed before). A value that is not finite in such
+ * probabilities rounded to BF16 (an output is then off by up to 2^-8 sum_j p_j |v_j| beside its
+ * own rounding; their sum is formed before). A value that is not finite in such
  * a tile reaches its own channel of the group's rows. Equal inputs give equal bits. Where the
- * tables hold less than 48 MiB of keys and values in all (counted for each row and 16 query heads
- * of a key head), the call is kda_attn_decode's, and the groups are not looked at.
+ * tables hold at most 48 MiB of keys and values in all (512 bytes a token, for each row and 16
+ * query heads of a key head, by the tables' width max_pages, whatever the rows' lengths), the
+ * call is kda_attn_decode's, and the groups are not looked at. That is faster for few short rows,
+ * which are best given tables no wider than they need.
  */
 KDA_API int kda_attn_prefix_decode(const void *q, const void *k_cache, const void *v_cache,
                                    int64_t k_page_stride, int64_t v_page_stride, int64_t num_pages,
@@ -480,8 +484,8 @@ KDA_API int kda_page_resize_ex(int32_t *block_table, const int32_t *seq_lens, co
  *                (multiples of 8), so that the three may be views of one projection's output.
  *   positions    int32 [tokens]; inv_freq FP32 [rot_dim / 2] (radians a position, finite; any
  *                scaling for long contexts is in its values, and in magnitude, the factor on
- *                the rotated channels). The angle is exact to 2^-30 of a turn for positions up
- *                to 2^20. rot_dim is a multiple of 16 in [0, 128]; 0: no rotation (both may be NULL).
+ *                the rotated channels). The angle is off by less than 2^-24 of a turn for positions up
+ *                to 2^20, by 2^-21 at 2^31. rot_dim is a multiple of 16 in [0, 128]; 0: no rotation (both may be NULL).
  *   q_weight, k_weight  [128], FP32 (weight_bf16 = 0) or BF16 (1); NULL: no norm. eps >= 0.
  *   q_out        BF16 like q, with its own stride; may be q itself (with q's stride)
  *   k_out        BF16 like k, or NULL (only with a cache); may be k itself

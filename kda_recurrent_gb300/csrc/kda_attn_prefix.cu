@@ -22,9 +22,16 @@
 // Roles: eight warps in two groups for the softmax (a thread a query row, 64 scores at a time in its registers), one that
 // loads keys by TMA into a ring of three tiles and one that loads values into a ring of two, a box for each page (or 128
 // tokens of it) and half of the channels, and one for each group that issues its products. Half a tile's scores are
-// formed while the other half's softmax runs. The probabilities replace their scores in tensor memory as BF16 (2^-8
-// of each, which averages out over a prefix; their sum is formed from the unrounded ones) and are the A operand
-// of P V from there. O is scaled down only when a row's maximum has grown by more than 2^8 since it was last fixed.
+// formed while the other half's softmax runs. The probabilities replace their scores in tensor memory as BF16 and are the
+// A operand of P V from there. O is scaled down only when a row's maximum has grown by more than 2^8 since it was last fixed.
+//
+// Rounding. One BF16 term a probability: each is off by at most 2^-8 of itself, an output so by at most 2^-8 sum_j p_j |v_j|
+// (the sum of the probabilities is formed from the unrounded ones, in 32 bits). For independent values that is the same share
+// of an output at any length, since the output shrinks like the error: 0.0016 of its rms beside 0.0017 of the output's own
+// rounding, together 0.0023 measured, where the token stream with its two terms has the 0.0017. Two terms here (the upper 16
+// bits and the rest) measured 0.0017, too, but are half as many products more: 32 rows in 4 groups 46.3 instead of 43.2 us,
+// 512 rows 304 and 284, 128 rows behind 32768 tokens 192 and 157. One term, because its error stays within a step of the
+// output's type; so the last bits of an output can change where a call passes from the one form to the other (kFewBytes).
 //
 // What bounds it. 128 rows of 64 heads behind 32768 tokens: 1.4e11 operations and 408 MB in 158 us, 885 TFLOP/s. A step has
 // 16.8 MFLOP (1.33 us of an SM's products at the library's rate) and 32768 exponentials (0.54 us), and takes 1.8 to 2.0 us,
@@ -34,7 +41,11 @@
 // 44.8 and 44.2, the geometric mean of 25 shapes the same. With two tiles of tokens for at most 128 query rows a step takes 1.7 us
 // from L2 and 2.9 from HBM, 6.7 TB/s.
 // 512 rows in 16 groups, 1.22 GB: 284 us, 4.3 TB/s; the rest's stream is about 200 ns of an SM for a tile of 16 tokens with the
-// beginnings of its short rows, and the prefixes' steps 2.9 us.
+// beginnings of its short rows, and the prefixes' steps 2.9 us. Both kinds of CTAs end unevenly: the stream's at 228 to 262 us
+// (their mean 241), the prefixes' at 167 to 279 (215).
+// 32 rows in 4 groups, by stamps in a copy that takes 45 us: lengths and dealing 1.8 us, first scores at 10 (queries and keys from memory,
+// the code's first pass), eight steps 16, last products and the part 3.4; the CTAs whose share crosses an item begin and
+// end twice, and are the last at 40 (mean 33); the join 41 to 45.
 //
 // Tokens of missing pages: their scores are masked, and their rows of the tiles cleared, since a probability of zero
 // does not mask a NaN. All waits are bounded; on expiry the CTA records KDA_ERR_DEVICE_TIMEOUT, waits for its own
@@ -63,9 +74,12 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kSlack = 8.0f;  // log2: how far a maximum may grow before O is scaled
 // What the work takes of an SM, in ns, by which the CTAs are dealt to its two kinds: a step of a prefix whose tokens several
 // pairs of tiles of query rows read at the same time, or one alone (that of one pair, or any when there are more items than
-// CTAs for them), the beginning and end of an item, a tile of 16 tokens of the rest. Only their ratios count. Over 25 shapes
-// the geometric mean is 0.821 of two launches' time; with one kind of step 0.831 (512 rows in 16 groups 296 instead of 284 us);
-// with 2000 or 2600 for the dearer one 0.822 (298, 290), with 4000 an item 0.821, with 180 a tile 0.846.
+// CTAs for them), the beginning and end of an item, a tile of 16 tokens of the rest. Only their ratios count, and they are
+// fitted, not measured each by itself (a tile takes 190 to 200 ns, a step 1.8 to 2.9 us). Over 25 shapes (2 to 512 rows of 8 to
+// 64 query heads on 1 or 8 key heads, in 1 to 16 groups, 128 to 32768 shared tokens, 64 to 1024 of the rest), geometric mean of the
+// time over that of two launches: 0.821; with 2000 or 2600 for the dearer step 0.822 (512 rows in 16 groups 298 and 290 instead of
+// 284 us), with 4000 an item 0.821. With the dearer one decided by the pairs alone 0.831 (296), and then with 130, 145 or 180 a tile 0.824, 0.828
+// and 0.846 (128 rows behind 32768 tokens 175, 165 and 158 instead of 157).
 constexpr float kStepNs = 1600.0f, kColdStepNs = 2300.0f, kItemNs = 3000.0f, kTileNs = 160.0f;
 constexpr int32_t kLeastRows = 2;  // of a group, for its prefix to be shared
 
@@ -901,7 +915,9 @@ int64_t attn_prefix_workspace_bytes(int32_t batch, int32_t num_q_heads, int32_t 
 // heads (35 MB) 12.4 and 13.5; 16 of 512 on 64/8 (38 MB) 14.7 and 14.8; 5 of 2048 on 8/8 (43 MB) 13.7 and 13.7; 6 (52 MB) 14.5
 // and 13.5; 16 of 768 on 64/8 (55 MB) 16.8 and 15.5; 8 of 2048 on 8/8 (69 MB) 16.3 and 13.8; 8 of 4096 on 32/8 (136 MB)
 // 24.6 and 15.8; 64 of 2048 on 64/8 in two groups (554 MB) 74 and 25.5. (With one key head, two rows and 32768 tokens it is
-// 19.3 and 22.3.)
+// 19.3 and 22.3.) The host knows the tables' width and not the rows' lengths: short rows in wide tables are shared, too, which
+// costs few of them something (512 shared tokens, tables of 576 and of 32768: 4 rows on 8/8 heads 8.5 and 11.8, 8 rows on 32/8
+// 9.8 and 12.8, 16 rows 12.2 and 12.9).
 constexpr int64_t kFewBytes = 48LL << 20;
 
 cudaError_t launch_attn_prefix(const AttnPrefixArgs &args, cudaStream_t stream) {
