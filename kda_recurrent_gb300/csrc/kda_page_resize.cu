@@ -3,8 +3,9 @@
 //
 // A row of n tokens holds ceil(n / page_size) pages. Free pages lie in a ring [first, first + count); rows that
 // grow take from its front, in row order, rows that shrink give back to its end, so that what a call takes and
-// what it gives never meet. The pages that a row shares with others, the first ones of its table, it does not give back. Where each row's pages and tokens begin follows from prefix sums over the rows, which
-// every CTA forms by itself, 1024 rows at a time (8 bytes a row); tokens and pages find their row in the sums by
+// what it gives never meet. The pages that a row shares with others, the first ones of its table, it does not
+// give back. Where each row's pages and tokens begin follows from prefix sums over the rows, which every CTA
+// forms by itself, 1024 rows at a time (8 bytes a row); tokens and pages find their row in the sums by
 // bisection. Nothing here is wide: it is a chain of dependent reads (lengths, sums, table or ring, map), and the
 // launch is most of a small call.
 //
